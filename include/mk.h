@@ -48,7 +48,10 @@ extern "C" {
 #define MK_ERR_NUMERIC     (-6)  /* a logit was NaN or infinite */
 #define MK_ERR_CUDA        (-7)  /* a CUDA runtime call failed */
 #define MK_ERR_NO_MEMORY   (-8)  /* a device allocation failed */
-#define MK_ERR_BAD_POSITION (-9) /* an MRoPE position-stream value outside the rotary table */
+#define MK_ERR_BAD_POSITION (-9) /* a rotary position (an MRoPE position-stream value) outside the
+                                     rotary table */
+#define MK_ERR_BAD_PAGE   (-10)  /* a sequence index, slot, length or page id outside the page table
+                                    or the cache (found on the device by the paged operators) */
 
 typedef struct mk_handle mk_handle;
 typedef void *mk_stream; /* cudaStream_t */
@@ -324,6 +327,151 @@ int mk_embed_sum(const void *books, int32_t n_books, int32_t book_rows, const vo
 int mk_embed_sum_noalloc(const void *books, int32_t n_books, int32_t book_rows, const void *text,
                          int32_t text_rows, int32_t hidden, const int32_t *codes,
                          const int32_t *text_ids, int32_t n, float *out, mk_stream stream);
+
+/* ---- paged KV cache: several sequences ------------------------------------
+ * A decode step of many sequences at once, for callers that hold the layer loop
+ * themselves: the three operators below are one layer's attention block
+ * (mk_matvec_q4 for the projections, mk_paged_append, mk_paged_attention), and
+ * mk_export_kv hands them a context that mk_prefill or mk_decode has built.  The
+ * pages cover one sequence per kernel only; these entry points have no
+ * counterpart there.
+ *
+ * They differ from the handle's calls in one way: they enqueue on `stream` and
+ * return, allocate nothing, keep nothing between calls and can be captured into
+ * a CUDA graph.  Argument errors are returned before anything is enqueued.
+ * What only the device sees (a page id outside the cache, a position outside
+ * the table) is written to *status if it is not NULL -- the first error's code;
+ * the caller zeroes it -- and no address outside the caller's buffers is formed.
+ * All pointers are on the device that is current at the call; the stream is that
+ * device's.  Tensors named in elements below have a contiguous last dimension,
+ * and their base pointers and all other strides are multiples of 16 bytes.   */
+
+#define MK_F32  0  /* element types of the operators below */
+#define MK_BF16 1
+#define MK_E4M3 2  /* 8-bit float, 4 exponent and 3 mantissa bits, largest value 448 */
+
+/* One layer's cache: n_pages pages of page_size slots each for n_kv_heads heads
+ * of head_dim (64 or 128) elements, in any order of pages, heads and slots given
+ * by the strides (elements; the same for keys and values; not negative).  Token p
+ * of sequence s is slot p % page_size of page table[s][p / page_size]; pages
+ * may be shared by sequences that read them. */
+typedef struct {
+  void *k, *v;                 /* device, dtype MK_BF16 or MK_E4M3 */
+  int32_t dtype;
+  int32_t n_pages, n_kv_heads, page_size, head_dim;
+  int64_t page_stride, head_stride, slot_stride;
+  const float *k_scale, *v_scale; /* MK_E4M3: device [n_kv_heads], what a stored value is multiplied
+                                     by; both or neither (NULL = 1).  MK_BF16: NULL */
+  const int32_t *table;        /* device [table_rows][table_cols] page ids */
+  int32_t table_rows, table_cols;
+  int64_t table_stride;        /* elements from row to row; 0 = every row the same pages */
+} mk_paged_kv;
+
+typedef struct {
+  int32_t n;                   /* token rows; 0 is a no-op */
+  int32_t dtype;               /* of q, k, v and q_out: MK_F32 or MK_BF16 */
+  int32_t n_q_heads;           /* heads of q; 0 = no q */
+  const void *q, *k, *v;       /* device [n][heads][head_dim] */
+  void *q_out;                 /* device [n][n_q_heads][head_dim]; may be q itself (same strides) */
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head, out_row, out_head; /* strides, elements */
+  const int32_t *seqs;         /* device [n] table row of each token row; NULL = row i is sequence i */
+  const int32_t *slots;        /* device [n] token index p in its sequence; negative = a padding row,
+                                  nothing of which is read or written */
+  const float *rope;           /* device [rope_rows][head_dim / 2][2] cos, sin; NULL = no rotation */
+  int32_t rope_rows;
+  int32_t rope_mode;           /* as mk_config.rope_mode; 1 and 2 need positions and sections */
+  int32_t mrope_sections[3];
+  const int32_t *positions;    /* device [n] (rope_mode 0; NULL = the slots) or [3][n] */
+  const void *q_norm, *k_norm; /* device bf16 [head_dim] RMSNorm gains before the rotation; NULL = none */
+  float rms_eps;
+  int32_t *status;             /* device, or NULL */
+} mk_append_args;
+
+/* Append n tokens' keys and values to their slots, QK-norm and rotation on the
+ * way, and write the normalised and rotated queries: for every row
+ *   q_out = rope(norm(q)), cache_k = round(rope(norm(k)) / k_scale), cache_v = round(v / v_scale)
+ * with norm(x) = x / sqrt(mean(x^2) + eps) * gain per head, rope turning the
+ * pairs (i, i + head_dim / 2), all in fp32 and rounded once (to nearest even,
+ * MK_E4M3 saturating at +-448).  One row (a decode step's token) or many
+ * (prompts: seqs and slots say where each row goes).  A slot may be written by
+ * at most one row of a call; with two, each element is one of theirs.  A row
+ * whose sequence, slot or page is outside the table or the cache
+ * (MK_ERR_BAD_PAGE) or whose position is outside the rotary table
+ * (MK_ERR_BAD_POSITION) is skipped: nothing of it is written.  Errors:
+ * MK_ERR_INVALID_ARG, MK_ERR_UNSUPPORTED (head_dim), MK_ERR_CUDA. */
+int mk_paged_append(const mk_paged_kv *kv, const mk_append_args *a, mk_stream stream);
+
+typedef struct {
+  int32_t n;                   /* query rows, one per table row: 0 <= n <= table_rows */
+  int32_t dtype;               /* of q and out: MK_F32 or MK_BF16 */
+  int32_t n_q_heads;           /* a multiple of n_kv_heads; head j reads kv head j / (n_q_heads / n_kv_heads) */
+  const void *q;               /* device [n][n_q_heads][head_dim] */
+  void *out;                   /* device, the same shape; may be q itself (same strides) */
+  int64_t q_row, q_head, out_row, out_head; /* strides, elements */
+  float *lse;                  /* device [n][n_q_heads] log of the softmax's sum, or NULL */
+  const int32_t *lengths;      /* device [n] tokens a row reads, its own included; 0 = none, negative =
+                                  a padding row, whose outputs are left as they were */
+  int32_t window;              /* > 0: only the last `window` of them; 0 = all */
+  float scale;                 /* of q.k; usually 1 / sqrt(head_dim) */
+  void *workspace;             /* device, 16-byte aligned; the call's own until the stream has passed it */
+  int64_t workspace_bytes;     /* at least mk_paged_attention_workspace */
+  int32_t *status;             /* device, or NULL */
+} mk_attention_args;
+
+/* Attention of one new token per row over the paged cache:
+ *   out = sum_p softmax_p(scale * q.k[p]) v[p],  lse = log sum_p exp(scale * q.k[p])
+ * over p in [max(0, length - window), length).  The work of all rows is cut
+ * into equal shares over the SMs whatever the lengths (read on the device, so
+ * that a captured call follows them), and the shares of a row are joined in a
+ * fixed order: the same inputs give the same bits.  A row with no tokens gives
+ * zeros and lse -inf.  Slots at and past a row's length are never read into a
+ * result, whatever they hold.  A row with a page id outside the cache, or a
+ * length past table_cols * page_size, gives NaN and MK_ERR_BAD_PAGE.  Several
+ * new tokens of one sequence (drafted tokens) are rows with the same pages and
+ * growing lengths.  Errors: MK_ERR_INVALID_ARG (a workspace too small among
+ * them), MK_ERR_UNSUPPORTED (head_dim, more than 2^31 tiles of work), MK_ERR_CUDA. */
+int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args *a, mk_stream stream);
+
+/* Bytes of workspace any mk_paged_attention call with these heads needs on the
+ * current device (it does not depend on rows or lengths).  MK_ERR_INVALID_ARG,
+ * MK_ERR_UNSUPPORTED or MK_ERR_CUDA as a negative result. */
+int64_t mk_paged_attention_workspace(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim);
+
+/* Copy cached tokens [first, first + count) of layer `layer` from the handle's
+ * own cache to slots [slot, slot + count) of sequence `seq` of a paged cache of
+ * the same heads (rotated keys as they are; rounded to MK_E4M3 with the cache's
+ * scales if it is one): a prompt prefilled by mk_prefill continues in a batch.
+ * Blocks until `stream` completes.  Errors: MK_ERR_INVALID_ARG (a range the
+ * handle has not filled, a decode not yet waited for), MK_ERR_UNSUPPORTED (other
+ * heads than the handle's), MK_ERR_BAD_PAGE (tokens whose page is bad are
+ * skipped, the others copied), MK_ERR_NO_MEMORY, MK_ERR_CUDA. */
+int mk_export_kv(mk_handle *h, int32_t layer, int32_t first, int32_t count, const mk_paged_kv *kv,
+                 int32_t seq, int32_t slot, mk_stream stream);
+
+/* ---- 4-bit weights ---------------------------------------------------------
+ * w[n][k] = scales[n][k / group] * (code[n][k] - zero[n][k / group]), codes and
+ * zeros 0 .. 15; byte k / 2 of a row holds code k in its low four bits when k is
+ * even, in its high four when k is odd. */
+typedef struct {
+  int32_t m, n, k;             /* y [m][n] = x [m][k] w[n][k]^T; m or n 0 is a no-op; k <= 32768 */
+  int32_t group;               /* 32, 64 or a multiple of 128 that divides k */
+  int32_t dtype;               /* of x, residual and y: MK_F32 or MK_BF16 */
+  const void *x;               /* device [m][k] */
+  int64_t x_row;               /* row strides, elements */
+  const void *codes;           /* device uint8 [n][k / 2], contiguous */
+  const void *scales;          /* device bf16 [n][k / group], contiguous */
+  const uint8_t *zeros;        /* device [n][k / group], contiguous; NULL = 8 everywhere */
+  const void *residual;        /* device [m][n] added to the products, or NULL; may be y itself */
+  int64_t residual_row;
+  void *y;                     /* device [m][n] */
+  int64_t y_row;               /* residual_row and y_row need no alignment */
+} mk_matvec_q4_args;
+
+/* y = x w^T (+ residual) for a few rows x, accumulated in fp32 and rounded once.
+ * Made for decode (m of 1 to some tens); further rows read the weights again.  A
+ * zero above 15 counts modulo 16.  Errors: MK_ERR_INVALID_ARG,
+ * MK_ERR_UNSUPPORTED (group, k), MK_ERR_CUDA. */
+int mk_matvec_q4(const mk_matvec_q4_args *a, mk_stream stream);
 
 /* Free everything the handle owns (not the borrowed weights): the end of the
  * handle lifecycle that mk_create starts.  NULL is a no-op; always MK_OK. */

@@ -16,3 +16,11 @@ from ._binding import (  # noqa: F401
     load_library,
     plan_for,
 )
+from .serving import (  # noqa: F401
+    check_status,
+    matvec_q4,
+    paged_append,
+    paged_attention,
+    quantize_q4,
+    rope_table,
+)

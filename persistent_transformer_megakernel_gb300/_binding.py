@@ -23,7 +23,8 @@ MK_DECODE_STREAM = 4
 _ERRORS = {0: "ok", -1: "invalid argument", -2: "unsupported shape or launch geometry",
            -3: "KV cache full", -4: "token id or sentinel row out of range",
            -5: "device wait timed out", -6: "non-finite logit", -7: "CUDA runtime error",
-           -8: "device out of memory", -9: "position stream outside the rotary table"}
+           -8: "device out of memory", -9: "position stream outside the rotary table",
+           -10: "page, slot or sequence outside the cache or its page table"}
 
 
 class MKError(RuntimeError):
@@ -68,10 +69,44 @@ class mk_info(C.Structure):
                 ("plan", C.c_int32)]
 
 
+class mk_paged_kv(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("dtype", C.c_int32), ("n_pages", C.c_int32),
+                ("n_kv_heads", C.c_int32), ("page_size", C.c_int32), ("head_dim", C.c_int32),
+                ("page_stride", C.c_int64), ("head_stride", C.c_int64), ("slot_stride", C.c_int64),
+                ("k_scale", C.c_void_p), ("v_scale", C.c_void_p), ("table", C.c_void_p),
+                ("table_rows", C.c_int32), ("table_cols", C.c_int32), ("table_stride", C.c_int64)]
+
+
+class mk_append_args(C.Structure):
+    _fields_ = [("n", C.c_int32), ("dtype", C.c_int32), ("n_q_heads", C.c_int32),
+                ("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("q_out", C.c_void_p),
+                ("q_row", C.c_int64), ("q_head", C.c_int64), ("k_row", C.c_int64), ("k_head", C.c_int64),
+                ("v_row", C.c_int64), ("v_head", C.c_int64), ("out_row", C.c_int64), ("out_head", C.c_int64),
+                ("seqs", C.c_void_p), ("slots", C.c_void_p), ("rope", C.c_void_p), ("rope_rows", C.c_int32),
+                ("rope_mode", C.c_int32), ("mrope_sections", C.c_int32 * 3), ("positions", C.c_void_p),
+                ("q_norm", C.c_void_p), ("k_norm", C.c_void_p), ("rms_eps", C.c_float), ("status", C.c_void_p)]
+
+
+class mk_attention_args(C.Structure):
+    _fields_ = [("n", C.c_int32), ("dtype", C.c_int32), ("n_q_heads", C.c_int32), ("q", C.c_void_p),
+                ("out", C.c_void_p), ("q_row", C.c_int64), ("q_head", C.c_int64), ("out_row", C.c_int64),
+                ("out_head", C.c_int64), ("lse", C.c_void_p), ("lengths", C.c_void_p), ("window", C.c_int32),
+                ("scale", C.c_float), ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64),
+                ("status", C.c_void_p)]
+
+
+class mk_matvec_q4_args(C.Structure):
+    _fields_ = [("m", C.c_int32), ("n", C.c_int32), ("k", C.c_int32), ("group", C.c_int32), ("dtype", C.c_int32),
+                ("x", C.c_void_p), ("x_row", C.c_int64), ("codes", C.c_void_p), ("scales", C.c_void_p),
+                ("zeros", C.c_void_p), ("residual", C.c_void_p), ("residual_row", C.c_int64), ("y", C.c_void_p),
+                ("y_row", C.c_int64)]
+
+
 #: every symbol include/mk.h declares
 EXPORTS = ("mk_create", "mk_reset_kv", "mk_decode", "mk_prefill", "mk_decode_start", "mk_decode_wait",
            "mk_mailbox_read", "mk_decode_host", "mk_get_info", "mk_embed_sum",
-           "mk_embed_sum_noalloc", "mk_destroy", "mk_error_string", "mk_plan_for")
+           "mk_embed_sum_noalloc", "mk_destroy", "mk_error_string", "mk_plan_for", "mk_paged_append",
+           "mk_paged_attention", "mk_paged_attention_workspace", "mk_export_kv", "mk_matvec_q4")
 
 _lib = None
 
@@ -102,13 +137,18 @@ def load_library(path: Optional[str] = None):
     lib.mk_plan_for.argtypes = [C.POINTER(mk_config), i32, C.POINTER(i32)]
     lib.mk_embed_sum.argtypes = [vp, i32, i32, vp, i32, i32, vp, vp, i32, vp, vp]
     lib.mk_embed_sum_noalloc.argtypes = [vp, i32, i32, vp, i32, i32, vp, vp, i32, vp, vp]
+    lib.mk_paged_append.argtypes = [C.POINTER(mk_paged_kv), C.POINTER(mk_append_args), vp]
+    lib.mk_paged_attention.argtypes = [C.POINTER(mk_paged_kv), C.POINTER(mk_attention_args), vp]
+    lib.mk_paged_attention_workspace.argtypes = [i32, i32, i32]
+    lib.mk_export_kv.argtypes = [vp, i32, i32, i32, C.POINTER(mk_paged_kv), i32, i32, vp]
+    lib.mk_matvec_q4.argtypes = [C.POINTER(mk_matvec_q4_args), vp]
     lib.mk_destroy.argtypes = [vp]
     lib.mk_error_string.argtypes = [C.c_int]
     lib.mk_error_string.restype = C.c_char_p
     for name in EXPORTS:
         if name != "mk_error_string":
             getattr(lib, name).restype = C.c_int
-    del i64
+    lib.mk_paged_attention_workspace.restype = i64
     if path is None:
         _lib = lib
     return lib
@@ -413,6 +453,22 @@ class Decoder:
         _check(self.lib.mk_prefill(self.h, _ptr(d_in), n, _ptr(out) if all_ids else None, C.byref(o),
                                    _stream_ptr(stream)), "mk_prefill")
         return out[:n] if all_ids else None
+
+    def export_kv(self, layer: int, k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor, *,
+                  seq: int = 0, first: int = 0, count: Optional[int] = None, slot: int = 0,
+                  k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+        """``mk_export_kv``: copy cached tokens ``first .. first + count - 1`` (all by
+        default) of ``layer`` to slots ``slot ..`` of row ``seq`` of a paged cache's
+        ``table`` (tensors as for ``paged_attention``)."""
+        from .serving import paged_struct
+        kv = paged_struct(k_cache, v_cache, table, k_scale, v_scale)
+        if k_cache.device != self.device:
+            raise ValueError("the paged cache must be on %s" % self.device)
+        count = self.position - first if count is None else count
+        with torch.cuda.device(self.device):
+            _check(self.lib.mk_export_kv(self.h, layer, first, count, C.byref(kv), seq, slot, _stream_ptr(stream)),
+                   "mk_export_kv")
 
     def decode_start(self, in_ids=None, n_steps: int = 0, *, out: Optional[torch.Tensor] = None,
                      stream_ids: bool = True, per_op=False, embeds: Optional[torch.Tensor] = None,

@@ -21,6 +21,7 @@
 
 #include "../../include/mk.h"
 #include "mk_launch.h"
+#include "mk_paged.h"
 #include "mk_prefill.h"
 #include "mk_params.h"
 #include "mk_plans.h"
@@ -361,6 +362,7 @@ const char *mk_error_string(int code) {
     case MK_ERR_CUDA: return "CUDA runtime error";
     case MK_ERR_NO_MEMORY: return "device out of memory";
     case MK_ERR_BAD_POSITION: return "position stream outside the rotary table";
+    case MK_ERR_BAD_PAGE: return "page, slot or sequence outside the cache or its page table";
     default: return "unknown error";
   }
 }
@@ -817,6 +819,40 @@ int mk_get_info(const mk_handle *h, mk_info *info) {
   info->kv_bytes = h->kv_bytes;
   info->plan = h->kernel == mk::kernel_hidden1024() ? 1 : h->kernel == mk::kernel_hidden2048() ? 2 : 0;
   return MK_OK;
+}
+
+int mk_export_kv(mk_handle *h, int32_t layer, int32_t first, int32_t count, const mk_paged_kv *kv, int32_t seq,
+                 int32_t slot, mk_stream stream) {
+  if (!h || h->pending || layer < 0 || layer >= h->cfg.n_layers || first < 0 || count < 0 || slot < 0 ||
+      static_cast<int64_t>(first) + count > h->pos || static_cast<int64_t>(slot) + count > INT32_MAX)
+    return MK_ERR_INVALID_ARG;
+  const int rc = mkv::check_cache(kv);
+  if (rc != MK_OK) return rc;
+  if (seq < 0 || seq >= kv->table_rows) return MK_ERR_INVALID_ARG;
+  if (kv->n_kv_heads != h->cfg.n_kv_heads || kv->head_dim != h->cfg.head_dim) return MK_ERR_UNSUPPORTED;
+  if (count == 0) return MK_OK;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int *d_status = nullptr;
+  if (cudaMallocAsync(&d_status, sizeof(int), s) != cudaSuccess) {
+    cudaGetLastError();
+    return MK_ERR_NO_MEMORY;
+  }
+  // the handle's cache is [layer][head][max_seq][d]
+  const int64_t d = h->cfg.head_dim, head = static_cast<int64_t>(h->cfg.max_seq) * d;
+  const int64_t at = layer * h->cfg.n_kv_heads * head + first * d;
+  int status = 0;
+  cudaError_t e = cudaMemsetAsync(d_status, 0, sizeof(int), s);
+  int launched = MK_OK;
+  if (e == cudaSuccess)
+    launched = mkv::append_range(kv, h->base.kcache + at, h->base.vcache + at, d, head, count, seq, slot, d_status, s);
+  if (e == cudaSuccess && launched == MK_OK)
+    e = cudaMemcpyAsync(&status, d_status, sizeof(int), cudaMemcpyDeviceToHost, s);
+  cudaFreeAsync(d_status, s);
+  if (cudaStreamSynchronize(s) != cudaSuccess || e != cudaSuccess) {
+    cudaGetLastError();
+    return MK_ERR_CUDA;
+  }
+  return launched != MK_OK ? launched : status;
 }
 
 int mk_destroy(mk_handle *h) {

@@ -1,0 +1,95 @@
+// Warp-level building blocks of the batched serving kernels: 16x8x16 matrix
+// products of bf16 or fp16 operands with fp32 accumulators, matrix loads from
+// shared memory, 16-byte asynchronous copies and the splitting of fp32 values
+// into sums of 16-bit terms.
+//
+// Fragment layout of a 16x8x16 product (lane = 4 g + t): A holds rows g and
+// g + 8 at k = 2t, 2t+1 (a0, a1) and 2t+8, 2t+9 (a2, a3); B column g at the same
+// k (b0, b1); C rows g (c0, c1) and g + 8 (c2, c3) at columns 2t, 2t+1.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <cstdint>
+
+namespace mkw {
+
+struct BF16Op {};
+struct FP16Op {};
+
+__device__ __forceinline__ void mma(BF16Op, float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma(FP16Op, float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// four 8x8 matrices of 16-bit elements; lane l passes the address of row l % 8 of matrix l / 8
+__device__ __forceinline__ void ldmatrix4(uint32_t *r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t *r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// 16 bytes global -> shared; with valid false nothing is read and zeros are written
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// round a pair to 16 bits, the first in the low half, and leave what it lost
+__device__ __forceinline__ uint32_t take_term(BF16Op, float &x, float &y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  x -= __low2float(h);
+  y -= __high2float(h);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t take_term(FP16Op, float &x, float &y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  x -= __low2float(h);
+  y -= __high2float(h);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// the same for values from outside, bf16 terms by truncation: the largest finite values stay finite, three terms hold
+// all 24 bits of an fp32 value, and an infinity is its first term alone
+__device__ __forceinline__ uint32_t take_input_term(BF16Op, float &x, float &y) {
+  const uint32_t a = __float_as_uint(x) & 0xffff0000u, b = __float_as_uint(y) & 0xffff0000u;
+  x = isinf(x) ? 0.f : x - __uint_as_float(a);
+  y = isinf(y) ? 0.f : y - __uint_as_float(b);
+  return __byte_perm(a, b, 0x7632);
+}
+__device__ __forceinline__ uint32_t take_input_term(FP16Op, float &x, float &y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  x = isinf(x) ? 0.f : x - __low2float(h);
+  y = isinf(y) ? 0.f : y - __high2float(h);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// two e4m3 values (low byte first) as two fp16 values: exact
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t pair) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(pair), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+
+// programmatic dependent launch: let the next kernel of the stream start; wait for the previous one's results
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+}  // namespace mkw

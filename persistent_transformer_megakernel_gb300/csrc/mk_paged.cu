@@ -1,0 +1,1018 @@
+// Operators over a paged KV cache that several sequences share (mk_paged_append,
+// mk_paged_attention, and the copy behind mk_export_kv).
+#include "mk_paged.h"
+
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <type_traits>
+
+#include "mk_mma.cuh"
+
+namespace mkv {
+
+constexpr int kMaxDevices = 64;
+
+__device__ __forceinline__ void report(int32_t *status, int code) {
+  if (status) atomicCAS(status, 0, code);
+}
+
+// ---------------------------------------------------------------------------
+// Append: q, k and v heads of n tokens, normalised, rotated and stored.
+//
+// Bound by bytes: every element is read once and written once; the arithmetic
+// is a sum of squares and one rotation.  D / 2 / N threads hold one head, each
+// N consecutive elements of the first half and the N elements half a head
+// further, the pairs of the rotation, so that every load and store is 16 bytes
+// of an input row and the pair meets in one thread; the squares are summed over
+// the head's threads by shuffles.  A thread that would need a page outside the
+// cache or a rotary row outside the table writes nothing.
+// ---------------------------------------------------------------------------
+
+struct AppendParams {
+  const void *q, *k, *v;
+  void *q_out, *k_cache, *v_cache;
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head, out_row, out_head;
+  int64_t page_stride, head_stride, slot_stride, table_stride;
+  const int32_t *table, *seqs, *slots, *positions;
+  const float2 *rope;
+  const uint16_t *q_norm, *k_norm;
+  const float *k_scale, *v_scale;
+  int32_t *status;
+  int n, hq, hkv, n_pages, page_size, table_rows, table_cols, rope_rows, rope_mode, sec0, sec1, sec2;
+  int seq0, slot0;             // slots == NULL: row i is slot slot0 + i of sequence seq0
+  float eps;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+template <class T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void load(const float *p, float *x) {
+    const float4 f = *reinterpret_cast<const float4 *>(p);
+    x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+  }
+  static __device__ __forceinline__ void store(float *p, const float *x) {
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float *x) {
+    const uint4 w = *reinterpret_cast<const uint4 *>(p);
+    x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
+    x[4] = bf16_lo(w.z), x[5] = bf16_hi(w.z), x[6] = bf16_lo(w.w), x[7] = bf16_hi(w.w);
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *x) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                                               pack_bf16(x[6], x[7]));
+  }
+};
+
+// N values to the cache: bf16, or e4m3 of value / scale
+template <int N>
+__device__ __forceinline__ void store_cache(__nv_bfloat16 *p, const float *x, float) {
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+  if constexpr (N == 8)
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  else
+    *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+}
+template <int N>
+__device__ __forceinline__ void store_cache(__nv_fp8_e4m3 *p, const float *x, float scale) {
+  uint32_t w[N / 4];
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] / scale, x[4 * i + 1] / scale), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] / scale, x[4 * i + 3] / scale), __NV_SATFINITE, __NV_E4M3);
+    w[i] = a | (b << 16);
+  }
+  if constexpr (N == 8)
+    *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t *>(p) = w[0];
+}
+
+constexpr int kAppendThreads = 256;
+
+template <class T, class C, int D>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
+  constexpr int N = Vec<T>::N, TPH = D / 2 / N;           // threads of one head
+  const int heads = p.hq + 2 * p.hkv;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / TPH) + threadIdx.x / TPH;
+  const int i0 = (threadIdx.x % TPH) * N;
+  const bool live = item < static_cast<int64_t>(p.n) * heads;
+  const int row = live ? static_cast<int>(item / heads) : 0, h = live ? static_cast<int>(item % heads) : 0;
+  const int slot = !live ? -1 : p.slots ? p.slots[row] : p.slot0 + row;
+  // every thread of a warp stays to the shuffles below; one with nothing to do works on zeros
+  bool ok = slot >= 0;
+  const bool is_q = h < p.hq, is_k = !is_q && h < p.hq + p.hkv;
+  const int kvh = is_q ? 0 : is_k ? h - p.hq : h - p.hq - p.hkv;
+  float lo[N], hi[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) lo[i] = hi[i] = 0.f;
+  if (ok) {
+    const T *src = is_q ? static_cast<const T *>(p.q) + row * p.q_row + h * p.q_head
+                        : is_k ? static_cast<const T *>(p.k) + row * p.k_row + kvh * p.k_head
+                               : static_cast<const T *>(p.v) + row * p.v_row + kvh * p.v_head;
+    Vec<T>::load(src + i0, lo);
+    Vec<T>::load(src + i0 + D / 2, hi);
+  }
+  int64_t dst = 0;
+  float2 cs[N];
+  if (ok) {
+    const int seq = p.seqs ? p.seqs[row] : p.slots ? row : p.seq0;
+    const int col = slot / p.page_size;
+    int page = -1;
+    if (seq >= 0 && seq < p.table_rows && col < p.table_cols) page = p.table[seq * p.table_stride + col];
+    if (page < 0 || page >= p.n_pages) {
+      ok = false;
+      report(p.status, MK_ERR_BAD_PAGE);
+    }
+    dst = page * p.page_stride + kvh * p.head_stride + (slot - col * p.page_size) * p.slot_stride;
+    if (p.rope) {
+      int at[3];
+      at[0] = p.positions ? p.positions[row] : slot;
+      at[1] = p.rope_mode ? p.positions[static_cast<int64_t>(p.n) + row] : at[0];
+      at[2] = p.rope_mode ? p.positions[2 * static_cast<int64_t>(p.n) + row] : at[0];
+      // refused for every head alike, so that a row is stored whole or not at all
+      if (at[0] < 0 || at[0] >= p.rope_rows || at[1] < 0 || at[1] >= p.rope_rows || at[2] < 0 || at[2] >= p.rope_rows) {
+        ok = false;
+        report(p.status, MK_ERR_BAD_POSITION);
+      } else if (is_q || is_k) {
+        if (p.rope_mode == 0) {
+          const float4 *r = reinterpret_cast<const float4 *>(p.rope + static_cast<int64_t>(at[0]) * (D / 2) + i0);
+#pragma unroll
+          for (int i = 0; i < N / 2; ++i) {
+            const float4 f = r[i];
+            cs[2 * i] = make_float2(f.x, f.y);
+            cs[2 * i + 1] = make_float2(f.z, f.w);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int j = i0 + i, m = j % 3;
+            const int stream = p.rope_mode == 1 ? (j >= p.sec0) + (j >= p.sec0 + p.sec1)
+                                                : (m == 1 && j < 3 * p.sec1) ? 1 : (m == 2 && j < 3 * p.sec2) ? 2 : 0;
+            cs[i] = p.rope[static_cast<int64_t>(stream == 0 ? at[0] : stream == 1 ? at[1] : at[2]) * (D / 2) + j];
+          }
+        }
+      }
+    }
+  }
+  const uint16_t *gain = is_q ? p.q_norm : is_k ? p.k_norm : nullptr;
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) ss += lo[i] * lo[i] + hi[i] * hi[i];
+#pragma unroll
+  for (int o = TPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if (!ok) return;
+  if (gain) {
+    const float r = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      lo[i] = lo[i] * r * bf16_lo(gain[i0 + i]);
+      hi[i] = hi[i] * r * bf16_lo(gain[i0 + D / 2 + i]);
+    }
+  }
+  if (p.rope && (is_q || is_k)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float a = lo[i], b = hi[i];
+      lo[i] = a * cs[i].x - b * cs[i].y;
+      hi[i] = b * cs[i].x + a * cs[i].y;
+    }
+  }
+  if (is_q) {
+    T *out = static_cast<T *>(p.q_out) + row * p.out_row + h * p.out_head;
+    Vec<T>::store(out + i0, lo);
+    Vec<T>::store(out + i0 + D / 2, hi);
+  } else {
+    C *out = static_cast<C *>(is_k ? p.k_cache : p.v_cache) + dst;
+    const float *scales = is_k ? p.k_scale : p.v_scale;
+    const float scale = scales ? scales[kvh] : 1.0f;
+    store_cache<N>(out + i0, lo, scale);
+    store_cache<N>(out + i0 + D / 2, hi, scale);
+  }
+}
+
+template <class T, class C, int D>
+int launch_append(const AppendParams &p, cudaStream_t s) {
+  constexpr int per_cta = kAppendThreads / (D / 2 / Vec<T>::N);
+  const int64_t items = static_cast<int64_t>(p.n) * (static_cast<int64_t>(p.hq) + 2 * static_cast<int64_t>(p.hkv));
+  const int64_t ctas = (items + per_cta - 1) / per_cta;
+  if (p.hq > (1 << 20) || p.hkv > (1 << 20) || ctas > INT32_MAX) return MK_ERR_UNSUPPORTED;
+  append_kernel<T, C, D><<<static_cast<unsigned>(ctas), kAppendThreads, 0, s>>>(p);
+  if (cudaPeekAtLastError() != cudaSuccess) {
+    cudaGetLastError();
+    return MK_ERR_CUDA;
+  }
+  return MK_OK;
+}
+
+int run_append(const AppendParams &p, int dtype, int cache, int d, cudaStream_t s) {
+  using B = __nv_bfloat16;
+  using E = __nv_fp8_e4m3;
+  if (dtype == MK_F32) {
+    if (cache == MK_BF16) return d == 64 ? launch_append<float, B, 64>(p, s) : launch_append<float, B, 128>(p, s);
+    return d == 64 ? launch_append<float, E, 64>(p, s) : launch_append<float, E, 128>(p, s);
+  }
+  if (cache == MK_BF16) return d == 64 ? launch_append<B, B, 64>(p, s) : launch_append<B, B, 128>(p, s);
+  return d == 64 ? launch_append<B, E, 64>(p, s) : launch_append<B, E, 128>(p, s);
+}
+
+// ---------------------------------------------------------------------------
+// Attention of one token per row.
+//
+// Per row and kv head the scores s_p = scale q.k_p and the weighted sum of the
+// values are taken in one pass over the cache with a running maximum m and sum
+// l (kept in log2 units): o = sum 2^(s_p - m) v_p, rescaled when m grows.  Bound
+// by the cache's bytes.
+//
+// The query heads of a kv head (up to 16 a pass) are the 16 rows of 16x8x16 matrix
+// products, so that the cache is read once for the whole group.  bf16 keys and
+// values multiply bf16 terms: a bf16 query is one term, an fp32 query three, and
+// the probabilities two terms (three for fp32 outputs), which keeps the result as
+// exact as fp32 products would.  e4m3 keys and values become fp16, exactly; the
+// query row is scaled by a power of two into fp16's range (one term, two for
+// fp32) and the probabilities by 2^14.  Each tile's value sums start from zero
+// and are added to the running ones by an fp32 multiply-add: matrix products
+// truncate what they add to an accumulator, which over thousands of tiles would
+// show.
+//
+// Work: the tiles (POS slots of one row and kv head) of all rows, in order, are
+// cut into equal ranges for the CTAs and these for their 8 warps, whatever the
+// lengths.  A warp streams its range through its own ring of shared memory with
+// asynchronous 16-byte copies and never waits for another warp until the end.
+// What a warp has of a row at its range's ends is joined with its neighbours'
+// in shared memory, what a CTA has at its ends through the workspace by
+// join_kernel, always in order: the same lengths give the same bits.
+// ---------------------------------------------------------------------------
+
+constexpr int kWarps = 8, kAttnThreads = 32 * kWarps;
+constexpr int kMinTilesPerCta = 16;
+constexpr int kMaxSmem = 230400;       // dynamic; the static part is below 2 KB, a CTA's limit 227 KB
+
+struct AttnParams {
+  const void *q, *k, *v;
+  void *out;
+  float *lse;
+  int64_t q_row, q_head, out_row, out_head, page_stride, head_stride, slot_stride, table_stride;
+  const int32_t *table, *lengths;
+  const float *k_scale, *v_scale;
+  int32_t *status;
+  int4 *records;       // [grid] {row, virtual head, last CTA, 1} of a row that goes on in the next CTA
+  float *parts;        // [grid][2][gr][D + 4]: a row's middle or end (0) and its beginning (1)
+  int n, hq, hkv, group, n_pages, page_size, table_cols, window;
+  int blocks, vh;      // head blocks of 16 query heads a kv head, virtual heads hkv * blocks
+  int gr;              // query rows kept of a block: min(group, 16)
+  int stages;
+  float scale;
+};
+
+template <int D, bool FP8>
+struct Tile {
+  static constexpr int ES = FP8 ? 1 : 2, ROWB = D * ES, CPR = ROWB / 16;
+  static constexpr int POS = (D == 128 && !FP8) ? 16 : 32;
+  static constexpr int KBYTES = POS * ROWB, STAGE = 2 * KBYTES;
+  // 16-byte chunk `c` of row r: permuted so that the same chunk of 8 rows meets 8 different banks
+  static __device__ __forceinline__ int at(int r, int c) {
+    return r * ROWB + ((ROWB >= 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+  }
+};
+
+__device__ __forceinline__ float2 load_pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+__device__ __forceinline__ float2 load_pair(const __nv_bfloat16 *p) {
+  const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
+__device__ __forceinline__ void store_one(float *p, float x) { *p = x; }
+__device__ __forceinline__ void store_one(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+
+// tiles of a row: those that hold any of its slots [lo, hi)
+struct Span {
+  int lo, hi, first, count;
+};
+template <int POS>
+__device__ __forceinline__ Span span_of(const AttnParams &p, int len) {
+  Span s;
+  const bool fits = len <= static_cast<int64_t>(p.table_cols) * p.page_size;
+  s.hi = len > 0 && fits ? len : 0;
+  s.lo = p.window > 0 && s.hi > p.window ? s.hi - p.window : 0;
+  s.first = s.lo / POS;
+  s.count = s.hi > 0 ? (s.hi + POS - 1) / POS - s.first : 0;
+  return s;
+}
+
+// what the ring's reader needs to know of a tile
+struct TileInfo {
+  int row, vh, pos, lo, hi, flags;
+};
+constexpr int kFirst = 1, kLast = 2, kBad = 4;   // the row's first tile, its last, a page outside the cache
+
+struct PartInfo {
+  int row, vh, begins, ends;   // row < 0: no part
+};
+
+template <int D>
+constexpr int kPartStride = D + 4;      // o[D], m, l
+
+// the join of parts (m_j, l_j, o_j): m = max m_j, weights 2^(m_j - m)
+__device__ __forceinline__ float join_base(float m) { return m == -INFINITY ? 0.f : m; }
+
+template <class T>
+__device__ __forceinline__ void write_out(const AttnParams &p, int row, int head, int d, float o, float l, float vs) {
+  const float r = l == 0.f ? 0.f : 1.0f / l;
+  store_one(static_cast<T *>(p.out) + row * p.out_row + head * p.out_head + d, o * r * vs);
+}
+__device__ __forceinline__ void write_lse(const AttnParams &p, int row, int head, float m, float l) {
+  if (p.lse) p.lse[static_cast<int64_t>(row) * p.hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+template <class T, bool FP8, int D>
+__global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParams p) {
+  using TL = Tile<D, FP8>;
+  using Op = std::conditional_t<FP8, mkw::FP16Op, mkw::BF16Op>;
+  constexpr bool F32 = std::is_same<T, float>::value;
+  constexpr int TQ = F32 ? (FP8 ? 2 : 3) : 1, TP = F32 ? (FP8 ? 2 : 3) : (FP8 ? 1 : 2);
+  constexpr int POS = TL::POS, KS = D / 16, NT = D / 8, SN = POS / 8, PN = POS / 16, PST = kPartStride<D>;
+  constexpr float kShift = FP8 ? 14.f : 0.f;             // probabilities are scaled by 2^kShift
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ TileInfo s_tile[kWarps][3];
+  __shared__ PartInfo s_part[2 * kWarps];
+  __shared__ int s_scan[kAttnThreads], s_warp[kWarps];
+
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  mkw::launch_dependents();
+
+  // ---- tiles before every group of rows ------------------------------------
+  const int per = (p.n + kAttnThreads - 1) / kAttnThreads;   // rows a thread counts
+  int mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int r = tid * per + i;
+    if (r < p.n) mine += span_of<POS>(p, p.lengths[r]).count;
+  }
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) s_warp[w] = incl;
+  if (tid < 2 * kWarps) s_part[tid].row = -1;
+  __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < w) before += s_warp[i];
+    total += s_warp[i];
+  }
+  s_scan[tid] = before + incl - mine;                        // tiles of the rows before this thread's
+  __syncthreads();
+
+  const int64_t tiles = static_cast<int64_t>(total) * p.vh;
+  const int64_t wanted = (tiles + kMinTilesPerCta - 1) / kMinTilesPerCta;
+  const int ctas = static_cast<int>(wanted < 1 ? 1 : wanted < gridDim.x ? wanted : gridDim.x);
+  const int cta = blockIdx.x;
+  const int64_t c_begin = cta < ctas ? tiles * cta / ctas : 0, c_end = cta < ctas ? tiles * (cta + 1) / ctas : 0;
+  const int64_t begin = c_begin + (c_end - c_begin) * w / kWarps, end = c_begin + (c_end - c_begin) * (w + 1) / kWarps;
+  const int n_tiles = static_cast<int>(end - begin);
+
+  // ---- where this warp's range starts ---------------------------------------
+  int row = 0, vh = 0, tile = 0;
+  Span sp{0, 0, 0, 0};
+  if (n_tiles > 0) {
+    const int x = static_cast<int>(begin / p.vh);            // in [before(row), before(row) + count(row))
+    int a = 0, b = kAttnThreads;
+    while (b - a > 1) {
+      const int m = (a + b) >> 1;
+      if (s_scan[m] <= x) a = m; else b = m;
+    }
+    int at = s_scan[a];
+    row = a * per;
+    sp = span_of<POS>(p, p.lengths[row]);
+    while (at + sp.count <= x) {
+      at += sp.count;
+      sp = span_of<POS>(p, p.lengths[++row]);
+    }
+    const int64_t rest = begin - static_cast<int64_t>(at) * p.vh;
+    vh = static_cast<int>(rest / sp.count);
+    tile = static_cast<int>(rest - static_cast<int64_t>(vh) * sp.count);
+  }
+
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + w * p.stages * TL::STAGE;
+  const unsigned char *k_base = static_cast<const unsigned char *>(p.k), *v_base = static_cast<const unsigned char *>(p.v);
+
+  // page of this lane's slot in the tile the producer stands at
+  auto page_of = [&](int pos) {
+    int page = -1;
+    if (lane < POS && pos >= sp.lo && pos < sp.hi) page = p.table[row * p.table_stride + pos / p.page_size];
+    return page;
+  };
+  int next_page = n_tiles > 0 ? page_of((sp.first + tile) * POS + lane) : -1;
+  int produced = 0;
+  auto produce = [&]() {
+    const int pos0 = (sp.first + tile) * POS, pos = pos0 + lane;
+    const bool want = lane < POS && pos >= sp.lo && pos < sp.hi;
+    const bool fine = want && next_page >= 0 && next_page < p.n_pages;
+    const unsigned bad = __ballot_sync(0xffffffffu, want && !fine);
+    int64_t off = 0;
+    if (fine) off = (next_page * p.page_stride + (vh / p.blocks) * p.head_stride + (pos % p.page_size) * p.slot_stride) * TL::ES;
+    const unsigned have = __ballot_sync(0xffffffffu, fine);
+    const int stage = produced % p.stages;
+    const uint32_t ks = ring + stage * TL::STAGE, vs = ks + TL::KBYTES;
+#pragma unroll
+    for (int i = 0; i < POS * TL::CPR / 32; ++i) {
+      const int idx = i * 32 + lane, r = idx / TL::CPR, c = idx % TL::CPR;
+      const int64_t o = __shfl_sync(0xffffffffu, off, r) + c * 16;
+      const bool ok = (have >> r) & 1;
+      mkw::cp_async16(ks + TL::at(r, c), k_base + (ok ? o : 0), ok);
+      mkw::cp_async16(vs + TL::at(r, c), v_base + (ok ? o : 0), ok);
+    }
+    if (lane == 0) {
+      s_tile[w][stage] = TileInfo{row, vh, pos0, sp.lo, sp.hi,
+                                  (tile == 0 ? kFirst : 0) | (tile == sp.count - 1 ? kLast : 0) | (bad ? kBad : 0)};
+      if (bad) report(p.status, MK_ERR_BAD_PAGE);
+    }
+    ++produced;
+    if (produced < n_tiles) {
+      if (++tile == sp.count) {
+        tile = 0;
+        if (++vh == p.vh) {
+          vh = 0;
+          do sp = span_of<POS>(p, p.lengths[++row]);
+          while (sp.count == 0);
+        }
+      }
+      next_page = page_of((sp.first + tile) * POS + lane);
+    }
+  };
+  for (int i = 0; i < p.stages - 1; ++i) {
+    if (produced < n_tiles) produce();
+    mkw::cp_async_commit();
+  }
+
+  // ---- rows without tiles -----------------------------------------------------
+  for (int r = cta; r < p.n; r += gridDim.x) {
+    const int len = p.lengths[r];
+    if (len < 0 || span_of<POS>(p, len).count > 0) continue;
+    const float x = len == 0 ? 0.f : NAN;
+    if (len > 0 && tid == 0) report(p.status, MK_ERR_BAD_PAGE);
+    for (int i = tid; i < p.hq * D; i += kAttnThreads)
+      store_one(static_cast<T *>(p.out) + r * p.out_row + (i / D) * p.out_head + i % D, x);
+    if (p.lse)
+      for (int i = tid; i < p.hq; i += kAttnThreads) p.lse[static_cast<int64_t>(r) * p.hq + i] = len == 0 ? -INFINITY : NAN;
+  }
+
+  // ---- the warp's tiles ---------------------------------------------------------
+  uint32_t qf[TQ][KS][4];
+  float o[NT][4], m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f, mult0 = 0.f, mult1 = 0.f;
+  int rows = 0, head0 = 0, begins = 0;
+  float *first_part = reinterpret_cast<float *>(smem + kWarps * p.stages * TL::STAGE) + w * p.gr * PST;
+  float *last_part = reinterpret_cast<float *>(smem + w * p.stages * TL::STAGE);
+  for (int i = 0; i < n_tiles; ++i) {
+    if (produced < n_tiles) produce();
+    mkw::cp_async_commit();
+    if (p.stages == 3) mkw::cp_async_wait<2>(); else mkw::cp_async_wait<1>();
+    __syncwarp();
+    const int stage = i % p.stages;
+    const TileInfo ti = s_tile[w][stage];
+    const uint32_t kt = ring + stage * TL::STAGE, vt = kt + TL::KBYTES;
+
+    if (i == 0 || (ti.flags & kFirst)) {                    // a row's query heads
+      const int kvh = ti.vh / p.blocks, blk = ti.vh % p.blocks;
+      head0 = kvh * p.group + blk * 16;
+      rows = min(16, p.group - blk * 16);
+      begins = ti.flags & kFirst;
+      const T *q0 = static_cast<const T *>(p.q) + ti.row * p.q_row + (head0 + g) * p.q_head, *q1 = q0 + 8 * p.q_head;
+      float2 x[KS][4];
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        // bf16: k = 2t, 2t+1, 2t+8, 2t+9 of the step; e4m3: 4t .. 4t+3, as the key's 16-bit pairs hold them
+        const int d0 = 16 * s + (FP8 ? 4 * t : 2 * t), d1 = d0 + (FP8 ? 2 : 8);
+        x[s][0] = x[s][1] = x[s][2] = x[s][3] = make_float2(0.f, 0.f);
+        if (g < rows) x[s][0] = load_pair(q0 + d0), x[s][2] = load_pair(q0 + d1);
+        if (g + 8 < rows) x[s][1] = load_pair(q1 + d0), x[s][3] = load_pair(q1 + d1);
+      }
+      mult0 = mult1 = p.scale * 1.4426950408889634f * (FP8 && p.k_scale ? p.k_scale[kvh] : 1.f);
+      if constexpr (FP8) {
+        float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          a0 = fmaxf(a0, fmaxf(fmaxf(fabsf(x[s][0].x), fabsf(x[s][0].y)), fmaxf(fabsf(x[s][2].x), fabsf(x[s][2].y))));
+          a1 = fmaxf(a1, fmaxf(fmaxf(fabsf(x[s][1].x), fabsf(x[s][1].y)), fmaxf(fabsf(x[s][3].x), fabsf(x[s][3].y))));
+        }
+        a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 1));
+        a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
+        a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
+        a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
+        // largest element to [2^13, 2^14); the exponent of 2^e stays within fp32's
+        const int e0 = a0 > 0.f && a0 < INFINITY ? max(-126, min(126, 13 - ilogbf(a0))) : 0;
+        const int e1 = a1 > 0.f && a1 < INFINITY ? max(-126, min(126, 13 - ilogbf(a1))) : 0;
+        const float f0 = ldexpf(1.f, e0), f1 = ldexpf(1.f, e1);
+        mult0 *= ldexpf(1.f, -e0);
+        mult1 *= ldexpf(1.f, -e1);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          x[s][0].x *= f0, x[s][0].y *= f0, x[s][2].x *= f0, x[s][2].y *= f0;
+          x[s][1].x *= f1, x[s][1].y *= f1, x[s][3].x *= f1, x[s][3].y *= f1;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int u = 0; u < TQ; ++u) qf[u][s][j] = mkw::take_input_term(Op{}, x[s][j].x, x[s][j].y);
+#pragma unroll
+      for (int s = 0; s < NT; ++s) o[s][0] = o[s][1] = o[s][2] = o[s][3] = 0.f;
+      m0 = m1 = -INFINITY;
+      l0 = l1 = 0.f;
+    }
+
+    // scores of the tile: rows g, g + 8; slots 8 j + 2t, + 1
+    float sc[SN][4], sl[SN][4];
+#pragma unroll
+    for (int j = 0; j < SN; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) sc[j][c] = sl[j][c] = 0.f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      if constexpr (!FP8) {
+#pragma unroll
+        for (int nb = 0; nb < PN; ++nb) {
+          uint32_t f[4];
+          mkw::ldmatrix4(f, kt + TL::at(nb * 16 + ((lane >> 4) << 3) + (lane & 7), 2 * s + ((lane >> 3) & 1)));
+          mkw::mma(Op{}, sc[2 * nb], qf[0][s], f[0], f[1]);
+          mkw::mma(Op{}, sc[2 * nb + 1], qf[0][s], f[2], f[3]);
+#pragma unroll
+          for (int u = TQ - 1; u > 0; --u) {
+            mkw::mma(Op{}, sl[2 * nb], qf[u][s], f[0], f[1]);
+            mkw::mma(Op{}, sl[2 * nb + 1], qf[u][s], f[2], f[3]);
+          }
+        }
+      } else {
+        uint32_t f[4];
+        mkw::ldmatrix4(f, kt + TL::at(lane, s));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t b0 = mkw::e4m3x2_to_half2(f[j] & 0xffffu), b1 = mkw::e4m3x2_to_half2(f[j] >> 16);
+          mkw::mma(Op{}, sc[j], qf[0][s], b0, b1);
+          if constexpr (TQ > 1) mkw::mma(Op{}, sl[j], qf[1][s], b0, b1);
+        }
+      }
+    }
+    const bool edge = ti.pos < ti.lo || ti.pos + POS > ti.hi;
+    float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < SN; ++j) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float s = sc[j][c];
+        if constexpr (TQ > 1) s += sl[j][c];
+        s *= c < 2 ? mult0 : mult1;
+        if (edge) {
+          const int pos = ti.pos + 8 * j + 2 * t + (c & 1);
+          if (pos < ti.lo || pos >= ti.hi) s = -INFINITY;
+        }
+        sc[j][c] = s;
+      }
+      x0 = fmaxf(x0, fmaxf(sc[j][0], sc[j][1]));
+      x1 = fmaxf(x1, fmaxf(sc[j][2], sc[j][3]));
+    }
+    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+    const float n0 = fmaxf(m0, x0 - kShift), n1 = fmaxf(m1, x1 - kShift);
+    const float b0 = join_base(n0), b1 = join_base(n1);
+    const float al0 = exp2f(m0 - b0), al1 = exp2f(m1 - b1);
+    m0 = n0;
+    m1 = n1;
+    l0 *= al0;
+    l1 *= al1;
+    uint32_t pf[TP][PN][4];
+#pragma unroll
+    for (int nb = 0; nb < PN; ++nb) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int sj = 2 * nb + (j >> 1), sc0 = (j & 1) * 2;
+        float a = exp2f(sc[sj][sc0] - ((j & 1) ? b1 : b0)), b = exp2f(sc[sj][sc0 + 1] - ((j & 1) ? b1 : b0));
+        if (j & 1) l1 += a + b; else l0 += a + b;
+#pragma unroll
+        for (int u = 0; u < TP; ++u) pf[u][nb][j] = mkw::take_term(Op{}, a, b);
+      }
+    }
+    // values: output tiles 2c and 2c + 1 are the 16-byte chunks of that number (bf16) or the even and the odd
+    // elements of chunk c (e4m3)
+    auto add = [&](int c, float *e, float *f) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        o[2 * c][k] = o[2 * c][k] * (k < 2 ? al0 : al1) + e[k];
+        o[2 * c + 1][k] = o[2 * c + 1][k] * (k < 2 ? al0 : al1) + f[k];
+      }
+    };
+    const int vr = (((lane >> 3) & 1) << 3) + (lane & 7);
+    if constexpr (!FP8) {
+#pragma unroll
+      for (int c = 0; c < NT / 2; ++c) {
+        float e[4] = {0.f, 0.f, 0.f, 0.f}, f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int nb = 0; nb < PN; ++nb) {
+          uint32_t b[4];
+          mkw::ldmatrix4_trans(b, vt + TL::at(nb * 16 + vr, 2 * c + (lane >> 4)));
+#pragma unroll
+          for (int u = TP - 1; u >= 0; --u) {
+            mkw::mma(Op{}, e, pf[u][nb], b[0], b[1]);
+            mkw::mma(Op{}, f, pf[u][nb], b[2], b[3]);
+          }
+        }
+        add(c, e, f);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < NT / 2; c += 2) {
+        float e[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) e[k][0] = e[k][1] = e[k][2] = e[k][3] = 0.f;
+#pragma unroll
+        for (int nb = 0; nb < PN; ++nb) {
+          uint32_t r[4];
+          mkw::ldmatrix4_trans(r, vt + TL::at(nb * 16 + vr, c + (lane >> 4)));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t b[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t lo = mkw::e4m3x2_to_half2(r[2 * k + j] & 0xffffu), hi = mkw::e4m3x2_to_half2(r[2 * k + j] >> 16);
+              b[j] = __byte_perm(lo, hi, 0x5410);
+              b[2 + j] = __byte_perm(lo, hi, 0x7632);
+            }
+#pragma unroll
+            for (int u = TP - 1; u >= 0; --u) {
+              mkw::mma(Op{}, e[2 * k], pf[u][nb], b[0], b[1]);
+              mkw::mma(Op{}, e[2 * k + 1], pf[u][nb], b[2], b[3]);
+            }
+          }
+        }
+        add(c, e[0], e[1]);
+        add(c + 1, e[2], e[3]);
+      }
+    }
+    if (ti.flags & kBad) l0 = l1 = NAN;
+    __syncwarp();                                            // every lane has read the stage (and, at the end, the ring)
+
+    const bool ends = ti.flags & kLast;
+    if (ends || i == n_tiles - 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+      l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+      const bool whole = begins && ends;
+      float *part = ends ? first_part : last_part;
+      const float vsc = FP8 && p.v_scale ? p.v_scale[ti.vh / p.blocks] : 1.f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = g + 8 * k;
+        if (r >= rows) continue;
+        const float l = k ? l1 : l0, m = k ? m1 : m0;
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        T *out = static_cast<T *>(p.out) + ti.row * p.out_row + (head0 + r) * p.out_head;
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int d = FP8 ? 16 * (c >> 1) + 4 * t + 2 * j + (c & 1) : 8 * c + 2 * t + j;
+            const float x = o[c][2 * k + j];
+            if (whole) store_one(out + d, x * inv * vsc);
+            else part[r * PST + d] = x;
+          }
+        if (t == 0) {
+          if (whole) {
+            write_lse(p, ti.row, head0 + r, m, l);
+          } else {
+            part[r * PST + D] = m;
+            part[r * PST + D + 1] = l;
+          }
+        }
+      }
+      if (!whole && lane == 0) s_part[2 * w + (ends ? 0 : 1)] = PartInfo{ti.row, ti.vh, begins, ends};
+    }
+  }
+  mkw::cp_async_wait<0>();
+  if (tid == 0) p.records[cta] = make_int4(0, 0, 0, 0);
+  __syncthreads();
+
+  // ---- join the warps' parts, in order ---------------------------------------
+  for (int a = 0; a < 2 * kWarps;) {
+    const PartInfo pi = s_part[a];
+    if (pi.row < 0) {
+      ++a;
+      continue;
+    }
+    int b = a, ends = pi.ends;
+    for (int j = a + 1; j < 2 * kWarps; ++j) {
+      const PartInfo pj = s_part[j];
+      if (pj.row < 0) continue;
+      if (pj.row != pi.row || pj.vh != pi.vh) break;
+      b = j;
+      ends = pj.ends;
+    }
+    const int kvh = pi.vh / p.blocks, blk = pi.vh % p.blocks, h0 = kvh * p.group + blk * 16, nr = min(16, p.group - blk * 16);
+    const bool whole = pi.begins && ends;
+    const float vsc = FP8 && p.v_scale ? p.v_scale[kvh] : 1.f;
+    float *slot = p.parts + (static_cast<int64_t>(cta) * 2 + (pi.begins ? 1 : 0)) * p.gr * PST;
+    for (int i = tid; i < nr * D; i += kAttnThreads) {
+      const int r = i / D, d = i % D;
+      float m = -INFINITY, l = 0.f, x = 0.f;
+      auto at = [&](int j) {
+        const unsigned char *base = (j & 1) ? smem + (j >> 1) * p.stages * TL::STAGE
+                                            : smem + kWarps * p.stages * TL::STAGE + (j >> 1) * p.gr * PST * 4;
+        return reinterpret_cast<const float *>(base) + r * PST;
+      };
+      for (int j = a; j <= b; ++j)
+        if (s_part[j].row >= 0) m = fmaxf(m, at(j)[D]);
+      const float base = join_base(m);
+      for (int j = a; j <= b; ++j) {
+        if (s_part[j].row < 0) continue;
+        const float *pj = at(j), f = exp2f(pj[D] - base);
+        l += f * pj[D + 1];
+        x += f * pj[d];
+      }
+      if (whole) {
+        write_out<T>(p, pi.row, h0 + r, d, x, l, vsc);
+        if (d == 0) write_lse(p, pi.row, h0 + r, m, l);
+      } else {
+        slot[r * PST + d] = x;
+        if (d == 0) {
+          slot[r * PST + D] = m;
+          slot[r * PST + D + 1] = l;
+        }
+      }
+    }
+    if (pi.begins && !ends && tid == 0) {
+      // the last CTA with tiles of this row: the one that holds tile e - 1, e the row's end
+      int before_row = s_scan[pi.row / per];
+      for (int r = pi.row / per * per; r < pi.row; ++r) before_row += span_of<POS>(p, p.lengths[r]).count;
+      const int count = span_of<POS>(p, p.lengths[pi.row]).count;
+      const int64_t e = static_cast<int64_t>(before_row) * p.vh + static_cast<int64_t>(pi.vh + 1) * count;
+      const int last = static_cast<int>((e * ctas + tiles - 1) / tiles) - 1;
+      p.records[cta] = make_int4(pi.row, pi.vh, last, 1);
+    }
+    a = b + 1;
+  }
+}
+
+// Joins the rows that more than one CTA had a share of: CTA c takes the row that
+// begins in attend_kernel's CTA c and goes on in the next ones.
+template <class T, int D>
+__global__ void __launch_bounds__(kAttnThreads) join_kernel(const AttnParams p) {
+  constexpr int PST = kPartStride<D>;
+  mkw::wait_previous_kernel();
+  const int cta = blockIdx.x;
+  const int4 rec = p.records[cta];
+  if (!rec.w) return;
+  const int kvh = rec.y / p.blocks, blk = rec.y % p.blocks, h0 = kvh * p.group + blk * 16, nr = min(16, p.group - blk * 16);
+  const float vsc = p.v_scale ? p.v_scale[kvh] : 1.f;
+  const int n = rec.z - cta + 1;
+  for (int i = threadIdx.x; i < nr * D; i += kAttnThreads) {
+    const int r = i / D, d = i % D;
+    auto at = [&](int j) { return p.parts + (static_cast<int64_t>(cta + j) * 2 + (j == 0 ? 1 : 0)) * p.gr * PST + r * PST; };
+    float m = -INFINITY, l = 0.f, x = 0.f;
+    for (int j = 0; j < n; ++j) m = fmaxf(m, at(j)[D]);
+    const float base = join_base(m);
+    for (int j = 0; j < n; ++j) {
+      const float *pj = at(j), f = exp2f(pj[D] - base);
+      l += f * pj[D + 1];
+      x += f * pj[d];
+    }
+    write_out<T>(p, rec.x, h0 + r, d, x, l, vsc);
+    if (d == 0) write_lse(p, rec.x, h0 + r, m, l);
+  }
+}
+
+int sm_count(int *device) {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  if (device) *device = dev;
+  if (dev < 0 || dev >= kMaxDevices) return -1;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      return -1;
+    }
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+template <class T, bool FP8, int D>
+int launch_attend(AttnParams &p, int grid, int dev, cudaStream_t s) {
+  using TL = Tile<D, FP8>;
+  static std::atomic<uint64_t> ready{0};
+  // three stages of the ring where a group's parts leave room for them (every group of up to 8 query heads)
+  const int parts = kWarps * p.gr * kPartStride<D> * 4;
+  p.stages = kWarps * 3 * TL::STAGE + parts <= kMaxSmem ? 3 : 2;
+  const int smem = kWarps * p.stages * TL::STAGE + parts;
+  const void *fn = reinterpret_cast<const void *>(&attend_kernel<T, FP8, D>);
+  if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) {
+      cudaGetLastError();
+      return MK_ERR_CUDA;
+    }
+    ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
+  }
+  attend_kernel<T, FP8, D><<<grid, kAttnThreads, smem, s>>>(p);
+  if (cudaPeekAtLastError() != cudaSuccess) {
+    cudaGetLastError();
+    return MK_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kAttnThreads);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, join_kernel<T, D>, static_cast<const AttnParams>(p)) != cudaSuccess) {
+    cudaGetLastError();
+    return MK_ERR_CUDA;
+  }
+  return MK_OK;
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// an element stride (>= 0) that is a multiple of 16 bytes
+bool stride_ok(int64_t s, int elem) { return s >= 0 && s <= (int64_t{1} << 48) && s * elem % 16 == 0; }
+
+int check_cache(const mk_paged_kv *kv) {
+  if (!kv || !kv->k || !kv->v || !kv->table || (kv->dtype != MK_BF16 && kv->dtype != MK_E4M3)) return MK_ERR_INVALID_ARG;
+  if (kv->n_pages < 1 || kv->n_kv_heads < 1 || kv->page_size < 1 || kv->table_rows < 0 || kv->table_cols < 0 ||
+      kv->table_stride < 0)
+    return MK_ERR_INVALID_ARG;
+  const int es = kv->dtype == MK_E4M3 ? 1 : 2;
+  if (!aligned16(kv->k) || !aligned16(kv->v) || !stride_ok(kv->page_stride, es) || !stride_ok(kv->head_stride, es) ||
+      !stride_ok(kv->slot_stride, es))
+    return MK_ERR_INVALID_ARG;
+  if ((kv->k_scale == nullptr) != (kv->v_scale == nullptr) || (kv->k_scale && kv->dtype != MK_E4M3)) return MK_ERR_INVALID_ARG;
+  if (kv->head_dim != 64 && kv->head_dim != 128) return MK_ERR_UNSUPPORTED;
+  return MK_OK;
+}
+
+void fill_cache(AppendParams &p, const mk_paged_kv *kv) {
+  p.k_cache = kv->k;
+  p.v_cache = kv->v;
+  p.page_stride = kv->page_stride, p.head_stride = kv->head_stride, p.slot_stride = kv->slot_stride;
+  p.table = kv->table;
+  p.table_stride = kv->table_stride;
+  p.table_rows = kv->table_rows, p.table_cols = kv->table_cols;
+  p.n_pages = kv->n_pages, p.page_size = kv->page_size;
+  p.hkv = kv->n_kv_heads;
+  p.k_scale = kv->k_scale, p.v_scale = kv->v_scale;
+}
+
+int append_range(const mk_paged_kv *kv, const void *k, const void *v, int64_t row, int64_t head, int32_t count,
+                 int32_t seq, int32_t slot0, int32_t *status, cudaStream_t stream) {
+  AppendParams p = {};
+  fill_cache(p, kv);
+  p.k = k, p.v = v;
+  p.k_row = p.v_row = row, p.k_head = p.v_head = head;
+  p.n = count;
+  p.seq0 = seq, p.slot0 = slot0;
+  p.status = status;
+  return run_append(p, MK_BF16, kv->dtype, kv->head_dim, stream);
+}
+
+}  // namespace mkv
+
+using namespace mkv;
+
+extern "C" int mk_paged_append(const mk_paged_kv *kv, const mk_append_args *a, mk_stream stream) {
+  const int rc = check_cache(kv);
+  if (rc != MK_OK) return rc;
+  if (!a || a->n < 0 || a->n_q_heads < 0 || (a->dtype != MK_F32 && a->dtype != MK_BF16) || a->rope_mode < 0 ||
+      a->rope_mode > 2 || a->rope_rows < 0)
+    return MK_ERR_INVALID_ARG;
+  if (a->n == 0) return MK_OK;
+  const int es = a->dtype == MK_F32 ? 4 : 2;
+  if (!a->k || !a->v || !a->slots || !aligned16(a->k) || !aligned16(a->v) || !stride_ok(a->k_row, es) ||
+      !stride_ok(a->k_head, es) || !stride_ok(a->v_row, es) || !stride_ok(a->v_head, es))
+    return MK_ERR_INVALID_ARG;
+  if (a->n_q_heads > 0 && (!a->q || !a->q_out || !aligned16(a->q) || !aligned16(a->q_out) || !stride_ok(a->q_row, es) ||
+                           !stride_ok(a->q_head, es) || !stride_ok(a->out_row, es) || !stride_ok(a->out_head, es)))
+    return MK_ERR_INVALID_ARG;
+  if ((a->q_norm || a->k_norm) && !(a->rms_eps >= 0.f)) return MK_ERR_INVALID_ARG;
+  if (a->rope) {
+    if (!aligned16(a->rope)) return MK_ERR_INVALID_ARG;
+    if (a->rope_mode != 0 &&
+        (!a->positions || a->mrope_sections[0] < 0 || a->mrope_sections[1] < 0 || a->mrope_sections[2] < 0 ||
+         static_cast<int64_t>(a->mrope_sections[0]) + a->mrope_sections[1] + a->mrope_sections[2] != kv->head_dim / 2))
+      return MK_ERR_INVALID_ARG;
+  }
+  AppendParams p = {};
+  fill_cache(p, kv);
+  p.q = a->q, p.k = a->k, p.v = a->v, p.q_out = a->q_out;
+  p.q_row = a->q_row, p.q_head = a->q_head, p.k_row = a->k_row, p.k_head = a->k_head;
+  p.v_row = a->v_row, p.v_head = a->v_head, p.out_row = a->out_row, p.out_head = a->out_head;
+  p.seqs = a->seqs, p.slots = a->slots, p.positions = a->positions;
+  p.rope = reinterpret_cast<const float2 *>(a->rope);
+  p.rope_rows = a->rope_rows, p.rope_mode = a->rope_mode;
+  p.sec0 = a->mrope_sections[0], p.sec1 = a->mrope_sections[1], p.sec2 = a->mrope_sections[2];
+  p.q_norm = static_cast<const uint16_t *>(a->q_norm), p.k_norm = static_cast<const uint16_t *>(a->k_norm);
+  p.eps = a->rms_eps;
+  p.n = a->n, p.hq = a->n_q_heads;
+  p.status = a->status;
+  return run_append(p, a->dtype, kv->dtype, kv->head_dim, reinterpret_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+int64_t workspace_bytes(int grid, int group, int d) {
+  return static_cast<int64_t>(grid) * (16 + 2 * std::min(group, 16) * (d + 4) * 4);
+}
+
+int check_heads(int32_t hq, int32_t hkv, int32_t d) {
+  if (hkv < 1 || hq < 1 || hq % hkv) return MK_ERR_INVALID_ARG;
+  return d == 64 || d == 128 ? MK_OK : MK_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+extern "C" int64_t mk_paged_attention_workspace(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim) {
+  const int rc = check_heads(n_q_heads, n_kv_heads, head_dim);
+  if (rc != MK_OK) return rc;
+  const int grid = sm_count(nullptr);
+  return grid < 0 ? MK_ERR_CUDA : workspace_bytes(grid, n_q_heads / n_kv_heads, head_dim);
+}
+
+extern "C" int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args *a, mk_stream stream) {
+  int rc = check_cache(kv);
+  if (rc != MK_OK) return rc;
+  if (!a || a->n < 0 || a->n > kv->table_rows || (a->dtype != MK_F32 && a->dtype != MK_BF16) || a->window < 0 ||
+      !std::isfinite(a->scale))
+    return MK_ERR_INVALID_ARG;
+  rc = check_heads(a->n_q_heads, kv->n_kv_heads, kv->head_dim);
+  if (rc != MK_OK) return rc;
+  if (a->n == 0) return MK_OK;
+  const int es = a->dtype == MK_F32 ? 4 : 2;
+  if (!a->q || !a->out || !a->lengths || !a->workspace || !aligned16(a->q) || !aligned16(a->out) ||
+      !aligned16(a->workspace) || !stride_ok(a->q_row, es) || !stride_ok(a->q_head, es) || !stride_ok(a->out_row, es) ||
+      !stride_ok(a->out_head, es))
+    return MK_ERR_INVALID_ARG;
+  // slots and the tiles of one kv head over all rows are counted in 32 bits
+  const int64_t slots = static_cast<int64_t>(kv->table_cols) * kv->page_size;
+  if (slots > INT32_MAX - 64 || (slots + 15) / 16 * a->n > INT32_MAX || a->n_q_heads > (1 << 20)) return MK_ERR_UNSUPPORTED;
+  int dev = 0;
+  const int grid = sm_count(&dev);
+  if (grid < 0) return MK_ERR_CUDA;
+  AttnParams p = {};
+  p.group = a->n_q_heads / kv->n_kv_heads;
+  if (a->workspace_bytes < workspace_bytes(grid, p.group, kv->head_dim)) return MK_ERR_INVALID_ARG;
+  p.q = a->q, p.k = kv->k, p.v = kv->v, p.out = a->out, p.lse = a->lse;
+  p.q_row = a->q_row, p.q_head = a->q_head, p.out_row = a->out_row, p.out_head = a->out_head;
+  p.page_stride = kv->page_stride, p.head_stride = kv->head_stride, p.slot_stride = kv->slot_stride;
+  p.table = kv->table, p.table_stride = kv->table_stride, p.table_cols = kv->table_cols;
+  p.lengths = a->lengths;
+  p.k_scale = kv->k_scale, p.v_scale = kv->v_scale;
+  p.status = a->status;
+  p.records = static_cast<int4 *>(a->workspace);
+  p.parts = reinterpret_cast<float *>(p.records + grid);
+  p.n = a->n, p.hq = a->n_q_heads, p.hkv = kv->n_kv_heads;
+  p.n_pages = kv->n_pages, p.page_size = kv->page_size;
+  p.window = a->window;
+  p.blocks = (p.group + 15) / 16;
+  p.vh = p.hkv * p.blocks;
+  p.gr = std::min(p.group, 16);
+  p.scale = a->scale;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  using B = __nv_bfloat16;
+  if (a->dtype == MK_F32) {
+    if (kv->dtype == MK_BF16)
+      return kv->head_dim == 64 ? launch_attend<float, false, 64>(p, grid, dev, s) : launch_attend<float, false, 128>(p, grid, dev, s);
+    return kv->head_dim == 64 ? launch_attend<float, true, 64>(p, grid, dev, s) : launch_attend<float, true, 128>(p, grid, dev, s);
+  }
+  if (kv->dtype == MK_BF16)
+    return kv->head_dim == 64 ? launch_attend<B, false, 64>(p, grid, dev, s) : launch_attend<B, false, 128>(p, grid, dev, s);
+  return kv->head_dim == 64 ? launch_attend<B, true, 64>(p, grid, dev, s) : launch_attend<B, true, 128>(p, grid, dev, s);
+}
