@@ -16,6 +16,7 @@ from ._binding import (  # noqa: F401
     load_library,
     plan_for,
 )
+from . import serving  # noqa: F401
 from .serving import (  # noqa: F401
     check_status,
     matvec_q4,
