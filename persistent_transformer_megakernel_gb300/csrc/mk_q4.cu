@@ -15,7 +15,9 @@
 // 128 and multiples) of its rows at once, so that a product never mixes two
 // groups, and the x columns are staged in shared memory in that order.  Codes j
 // and j + 4 of a 32-bit word are taken out together: (w >> 4j) & 0x000f000f in the
-// low mantissa bits of the bf16 number 128, whose last place is 1, less 128 + zero.
+// low mantissa bits of the bf16 number 2^-5, whose last place is 2^-12, less 2^-5
+// and the zero in the same place.  The products are thus 2^-12 of their value
+// until the end, which keeps those of the largest finite x finite.
 //
 // The rows' tiles are dealt out to persistent CTAs; up to 8 warps share a tile's
 // k when there are too few tiles to fill the SMs.  Every warp keeps U blocks of
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) matvec_kernel(const Q4Params p) {
 #pragma unroll
       for (int c = 0; c < NT; ++c) acc[r][c][0] = acc[r][c][1] = acc[r][c][2] = acc[r][c][3] = 0.f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) z[r][h] = (0x4300u | (s.zero[r][h] & 15u)) * 0x10001u;      // 128 + zero, twice
+      for (int h = 0; h < 2; ++h) z[r][h] = (0x3d00u | (s.zero[r][h] & 15u)) * 0x10001u;      // 2^-5 + 2^-12 zero, twice
     }
     const int e0 = (b0 + blk) * (KB / 8) + t * WORDS;      // first 8-element block of this lane
 #pragma unroll
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) matvec_kernel(const Q4Params p) {
         for (int h = 0; h < 2; ++h) {
           const uint32_t v = reinterpret_cast<const uint32_t *>(&s.code[r][h])[i];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) a[j >> 1][(j & 1) * 2 + h] = minus(((v >> (4 * j)) & 0x000f000fu) | 0x43004300u, z[r][h]);
+          for (int j = 0; j < 4; ++j) a[j >> 1][(j & 1) * 2 + h] = minus(((v >> (4 * j)) & 0x000f000fu) | 0x3d003d00u, z[r][h]);
         }
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
@@ -242,6 +244,7 @@ __global__ void __launch_bounds__(kThreads) matvec_kernel(const Q4Params p) {
 #pragma unroll
       for (int u = TERMS - 1; u >= 0; --u)
         for (int j = 0; j < p.wk; ++j) y += red[(j * ROWS + r) * COLS + m * TERMS + u];
+      y *= 4096.f;
       if (row < p.n) {
         if (p.residual) y += to_float(static_cast<const T *>(p.residual)[(m0 + m) * p.residual_row + row]);
         put(static_cast<T *>(p.y) + (m0 + m) * p.y_row + row, y);
