@@ -19,9 +19,15 @@ from ._binding import (  # noqa: F401
 from . import serving  # noqa: F401
 from .serving import (  # noqa: F401
     check_status,
-    matvec_q4,
-    paged_append,
-    paged_attention,
     quantize_q4,
     rope_table,
 )
+
+
+def __getattr__(name: str):
+    # paged_append, paged_attention, matvec_q4: their module is loaded on first use
+    if name not in serving.NATIVE:
+        raise AttributeError("module %r has no attribute %r" % (__name__, name))
+    f = getattr(serving, name)
+    globals()[name] = f
+    return f

@@ -1,4 +1,5 @@
-"""Build libmk.so in-tree with nvcc for sm_103a (GB300).
+"""Build libmk.so in-tree with nvcc for sm_103a (GB300), and the Python module
+_mktorch.so that calls it on torch tensors with the host compiler.
 
 Each translation unit compiles in parallel, then nvcc links the shared
 library next to this file.  Nothing is installed anywhere else.
@@ -8,12 +9,14 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmk.so")
+MODULE = os.path.join(HERE, "_mktorch.so")
 SOURCES = ["mk_kernels_d128.cu", "mk_kernels_hidden1024.cu", "mk_kernels_hidden2048.cu", "mk_kernels_d64.cu",
            "mk_host.cu", "mk_embed.cu", "mk_prefill.cu", "mk_gemm.cu", "mk_pfattn.cu",
            "mk_paged.cu", "mk_q4.cu"]
@@ -34,8 +37,29 @@ def _run(cmd):
     return r.stdout + r.stderr
 
 
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _compile_module(obj: str) -> str:
+    inc = os.path.join(_torch_dir(), "include")
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
+    dirs = [inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    return _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *["-I" + d for d in dirs], "-c",
+                 os.path.join(CSRC, "mk_torch.cpp"), "-o", obj])
+
+
+def _link_module(obj: str) -> None:
+    lib = os.path.join(_torch_dir(), "lib")
+    tmp = MODULE + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L" + HERE, "-l:libmk.so", "-Wl,-rpath,$ORIGIN", "-L" + lib, "-Wl,-rpath," + lib,
+          "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
+    os.replace(tmp, MODULE)
+
+
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link libmk.so; returns its path."""
+    """Compile and link libmk.so and _mktorch.so; returns libmk.so's path."""
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
@@ -44,11 +68,15 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     def one(i):
         return _run([nvcc, *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, SOURCES[i]), "-o", objs[i]])
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    module_obj = os.path.join(OUT_DIR, "mk_torch.o")
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        module = ex.submit(_compile_module, module_obj)
         logs = list(ex.map(one, range(len(SOURCES))))
+        module.result()
     tmp = LIB + ".tmp"
     _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"])
     os.replace(tmp, LIB)
+    _link_module(module_obj)
     if verbose:
         for s, log in zip(SOURCES, logs):
             if log.strip():

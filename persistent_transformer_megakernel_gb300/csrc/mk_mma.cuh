@@ -82,6 +82,18 @@ __device__ __forceinline__ uint32_t take_input_term(FP16Op, float &x, float &y) 
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// the lower terms of a value times an infinity must not make NaN of it: a remainder of zero becomes a tiny one of the
+// value's sign
+__device__ __forceinline__ float signed_rest(float rest, float value) { return copysignf(fmaxf(fabsf(rest), 0x1p-120f), value); }
+// a term of probabilities (>= 0), not the last: by truncation, so that no remainder is negative
+__device__ __forceinline__ uint32_t take_weight_term(BF16Op, float &x, float &y) {
+  const uint32_t a = __float_as_uint(x) & 0xffff0000u, b = __float_as_uint(y) & 0xffff0000u;
+  x = fmaxf(x - __uint_as_float(a), 0x1p-120f);
+  y = fmaxf(y - __uint_as_float(b), 0x1p-120f);
+  return __byte_perm(a, b, 0x7632);
+}
+__device__ __forceinline__ uint32_t take_weight_term(FP16Op op, float &x, float &y) { return take_term(op, x, y); }
+
 // two e4m3 values (low byte first) as two fp16 values: exact
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t pair) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(pair), __NV_E4M3);

@@ -536,7 +536,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParam
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int u = 0; u < TQ; ++u) qf[u][s][j] = mkw::take_input_term(Op{}, x[s][j].x, x[s][j].y);
+          for (int u = 0; u < TQ; ++u) {
+            const float2 whole = x[s][j];
+            qf[u][s][j] = mkw::take_input_term(Op{}, x[s][j].x, x[s][j].y);
+            if (!FP8 && u + 1 < TQ) {
+              x[s][j].x = mkw::signed_rest(x[s][j].x, whole.x);
+              x[s][j].y = mkw::signed_rest(x[s][j].y, whole.y);
+            }
+          }
 #pragma unroll
       for (int s = 0; s < NT; ++s) o[s][0] = o[s][1] = o[s][2] = o[s][3] = 0.f;
       m0 = m1 = -INFINITY;
@@ -613,7 +620,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParam
         float a = exp2f(sc[sj][sc0] - ((j & 1) ? b1 : b0)), b = exp2f(sc[sj][sc0 + 1] - ((j & 1) ? b1 : b0));
         if (j & 1) l1 += a + b; else l0 += a + b;
 #pragma unroll
-        for (int u = 0; u < TP; ++u) pf[u][nb][j] = mkw::take_term(Op{}, a, b);
+        for (int u = 0; u < TP - 1; ++u) pf[u][nb][j] = mkw::take_weight_term(Op{}, a, b);
+        pf[TP - 1][nb][j] = mkw::take_term(Op{}, a, b);
       }
     }
     // values: output tiles 2c and 2c + 1 are the 16-byte chunks of that number (bf16) or the even and the odd

@@ -71,8 +71,9 @@ def attention(q, k_cache, v_cache, table, lengths, scale, window=0, k_scale=None
         # a score: up to 8 chained products of 16 terms and 8 roundings; e4m3 caches round an fp32 query to 22 bits
         s_err = a.amax(-1, keepdim=True) * (24 * 2.0 ** -23 + (2.0 ** -22 if fp8 else 0))
         tiles = (length - lo) / 16 + 2
-        # a probability's terms: 16 bits and more; an e4m3 cache with a bf16 query takes one term of 11
-        p_err = (2.0 ** -11 if q.dtype == torch.bfloat16 else 2.0 ** -22) if fp8 else 2.0 ** -16 if q.dtype == torch.bfloat16 else 2.0 ** -23
+        # a probability's terms.  bf16 cache and query: 8 bits truncated leave less than 2^-7, of which 8 rounded bits
+        # miss 2^-8 at most: 2^-15; three terms hold all 24 bits.  e4m3 cache: fp16 terms of 11 bits, one with a bf16 query
+        p_err = (2.0 ** -11 if q.dtype == torch.bfloat16 else 2.0 ** -22) if fp8 else 2.0 ** -15 if q.dtype == torch.bfloat16 else 2.0 ** -23
         # 2^x to 2^-21, a tile's sum of 96 products at most, a multiply-add a tile, three joins
         c = 2 * s_err + p_err + (16 + 96 + tiles) * 2.0 ** -23
         err[b] = (c * torch.einsum("hgn,hnd->hgd", e / l, v.abs())).reshape(hq, d)

@@ -48,6 +48,10 @@ def _rows(c, rows):
     return {k: (v[rows] if k in ("q", "lengths", "table") else v) for k, v in c.items()}
 
 
+def _but(c, length):
+    return dict(c, lengths=torch.full_like(c["lengths"], length))
+
+
 def _check(c, out, lse, scale=None, window=0, what="attention"):
     d = c["q"].shape[2]
     want, wlse, err, lerr = U.attention(c["q"], c["k_cache"], c["v_cache"], c["table"], c["lengths"],
@@ -195,6 +199,13 @@ def test_infinite_and_nan_scores():
     c["v_cache"][int(c["table"][1, 1]), 0, 2, 5] = float("inf")    # one value of row 1
     out, _ = _run(c)
     assert (out[1, :, 5] == math.inf).all() and torch.isfinite(out[1, :, :5]).all()
+    # a key that scores -inf has no weight
+    c = _case([40], 1, 1, 64, F32, BF16, 16, seed=17)
+    c["q"][0, 0, 9] = -1.0
+    want, wlse = _run(_but(c, 39))
+    c["k_cache"][int(c["table"][0, 39 // 16]), 0, 39 % 16, 9] = float("inf")
+    out, lse = _run(c)
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
 
 
 @pytest.mark.parametrize("x", [BF16, F32])

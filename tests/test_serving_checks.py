@@ -14,6 +14,14 @@ from persistent_transformer_megakernel_gb300 import serving as S
 BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 
 
+if not os.path.exists(mk.lib_path()) or not os.path.exists(os.path.join(os.path.dirname(mk.lib_path()), "_mktorch.so")):
+    from persistent_transformer_megakernel_gb300 import build
+    build.build()
+
+CACHE = dict(k_cache=torch.zeros((6, 2, 16, 64), dtype=BF16), v_cache=torch.zeros((6, 2, 16, 64), dtype=BF16),
+             table=torch.zeros((3, 4), dtype=torch.int32))
+
+
 def _kv(**kw):
     a = dict(k_cache=torch.zeros((6, 2, 16, 64), dtype=BF16), v_cache=torch.zeros((6, 2, 16, 64), dtype=BF16),
              table=torch.zeros((3, 4), dtype=torch.int32))
@@ -48,11 +56,11 @@ def test_cache_tensors():
 
 
 def _append(**kw):
-    a = dict(kv=_kv(), k=torch.zeros((3, 2, 64)), v=torch.zeros((3, 2, 64)), slots=torch.zeros(3, dtype=torch.int32), seqs=None,
+    a = dict(CACHE, k=torch.zeros((3, 2, 64)), v=torch.zeros((3, 2, 64)), slots=torch.zeros(3, dtype=torch.int32), seqs=None,
              q=torch.zeros((3, 4, 64)), q_out=torch.zeros((3, 4, 64)), rope=torch.zeros((10, 32, 2)), positions=None,
              mrope_sections=None, mrope_interleaved=False, q_norm=torch.zeros(64, dtype=BF16), k_norm=None, eps=1e-6, status=None)
     a.update(kw)
-    return S.append_struct(**a)
+    return B.mk_append_args.from_buffer_copy(S.native().check_append(**a))
 
 
 def test_append_tensors():
@@ -78,16 +86,23 @@ def test_append_tensors():
                 dict(positions=i32(3, 3)), dict(mrope_sections=(12, 10, 10)), dict(positions=i32(3, 3), mrope_sections=(12, 10, 9)),
                 dict(positions=i32(3, 3), mrope_sections=(42, -5, -5)), dict(positions=i32(3, 4), mrope_sections=(12, 10, 10)),
                 dict(rope=None, positions=i32(3)), dict(q_norm=torch.zeros(64)), dict(k_norm=torch.zeros(128, dtype=BF16)),
-                dict(status=i32(2))):
+                dict(status=i32(2)), dict(q=None), dict(eps=-1.0), dict(eps=float("nan")), dict(v=None), dict(mrope_sections=(16, 16))):
         with pytest.raises(ValueError):
             _append(**bad)
+    for bad in (dict(eps="x"), dict(positions=i32(3, 3), mrope_sections=3), dict(nonsense=1)):
+        with pytest.raises(TypeError):
+            _append(**bad)
+    with pytest.raises(TypeError):
+        mk.paged_append(stacked)
+    with pytest.raises(ValueError):                             # host tensors where device ones are needed
+        mk.paged_append(stacked[:, 4:6], stacked[:, 6:], *CACHE.values(), i32(3))
 
 
 def _attention(**kw):
-    a = dict(kv=_kv(), q=torch.zeros((3, 4, 64)), lengths=torch.zeros(3, dtype=torch.int32), scale=None, window=0,
+    a = dict(CACHE, q=torch.zeros((3, 4, 64)), lengths=torch.zeros(3, dtype=torch.int32), scale=None, window=0,
              out=torch.zeros((3, 4, 64)), lse=torch.zeros((3, 4)), status=None)
     a.update(kw)
-    return S.attention_struct(**a)
+    return B.mk_attention_args.from_buffer_copy(S.native().check_attention(**a))
 
 
 def test_attention_tensors():
@@ -98,16 +113,17 @@ def test_attention_tensors():
                 dict(q=torch.zeros((4, 4, 64)), out=torch.zeros((4, 4, 64)), lse=None, lengths=torch.zeros(4, dtype=torch.int32)),
                 dict(q=torch.zeros((3, 4, 64), dtype=torch.float16)), dict(out=torch.zeros((3, 4, 64), dtype=BF16)),
                 dict(out=torch.zeros((3, 2, 64))), dict(lse=torch.zeros((4, 3)).t()), dict(lse=torch.zeros((3, 4), dtype=BF16)),
-                dict(lengths=torch.zeros(3)), dict(lengths=torch.zeros(4, dtype=torch.int32)), dict(lengths=None), dict(window=-1)):
+                dict(lengths=torch.zeros(3)), dict(lengths=torch.zeros(4, dtype=torch.int32)), dict(lengths=None), dict(window=-1),
+                dict(scale=float("nan")), dict(scale=float("inf")), dict(q=None), dict(q=3)):
         with pytest.raises(ValueError):
             _attention(**bad)
 
 
 def _matvec(**kw):
     a = dict(x=torch.zeros((2, 128)), codes=torch.zeros((10, 64), dtype=torch.uint8), scales=torch.zeros((10, 2), dtype=BF16),
-             zeros=None, residual=None, y=torch.zeros((2, 10)))
+             zeros=None, residual=None, out=torch.zeros((2, 10)))
     a.update(kw)
-    return S.matvec_struct(**a)
+    return B.mk_matvec_q4_args.from_buffer_copy(S.native().check_matvec(**a))
 
 
 def test_matvec_tensors():
@@ -122,9 +138,19 @@ def test_matvec_tensors():
                 dict(scales=torch.zeros((10, 2))), dict(scales=torch.zeros((9, 2), dtype=BF16)), dict(scales=torch.zeros((10, 8), dtype=BF16)),
                 dict(scales=torch.zeros((10, 3), dtype=BF16)), dict(zeros=torch.zeros((10, 1), dtype=torch.uint8)),
                 dict(zeros=torch.zeros((10, 2))), dict(residual=torch.zeros((2, 9))), dict(residual=torch.zeros((2, 10), dtype=BF16)),
-                dict(y=torch.zeros((3, 10))), dict(y=torch.zeros((2, 10), dtype=BF16)), dict(y=torch.zeros((10, 2)).t())):
+                dict(out=torch.zeros((3, 10))), dict(out=torch.zeros((2, 10), dtype=BF16)), dict(out=torch.zeros((10, 2)).t())):
         with pytest.raises(ValueError):
             _matvec(**bad)
+    with pytest.raises(ValueError):                             # host tensors
+        mk.matvec_q4(torch.zeros((2, 128)), torch.zeros((10, 64), dtype=torch.uint8), torch.zeros((10, 2), dtype=BF16))
+
+
+def test_the_functions_describe_themselves():
+    import inspect
+    for f in (mk.paged_append, mk.paged_attention, mk.matvec_q4):
+        assert "stream" in inspect.signature(f).parameters and f.__name__ in f.__doc__
+    with pytest.raises(AttributeError):
+        mk.no_such_operator
 
 
 def _with(s, fields):
