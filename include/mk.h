@@ -376,7 +376,7 @@ typedef struct {
   int64_t q_row, q_head, k_row, k_head, v_row, v_head, out_row, out_head; /* strides, elements */
   const int32_t *seqs;         /* device [n] table row of each token row; NULL = row i is sequence i */
   const int32_t *slots;        /* device [n] token index p in its sequence; negative = a padding row,
-                                  nothing of which is read or written */
+                                  nothing of which is written */
   const float *rope;           /* device [rope_rows][head_dim / 2][2] cos, sin; NULL = no rotation */
   int32_t rope_rows;
   int32_t rope_mode;           /* as mk_config.rope_mode; 1 and 2 need positions and sections */
@@ -453,7 +453,7 @@ int mk_export_kv(mk_handle *h, int32_t layer, int32_t first, int32_t count, cons
  * zeros 0 .. 15; byte k / 2 of a row holds code k in its low four bits when k is
  * even, in its high four when k is odd. */
 typedef struct {
-  int32_t m, n, k;             /* y [m][n] = x [m][k] w[n][k]^T; m or n 0 is a no-op; k <= 32768 */
+  int32_t m, n, k;             /* y [m][n] = x [m][k] w[n][k]^T; m or n 0 is a no-op; k <= 24576 */
   int32_t group;               /* 32, 64 or a multiple of 128 that divides k */
   int32_t dtype;               /* of x, residual and y: MK_F32 or MK_BF16 */
   const void *x;               /* device [m][k] */

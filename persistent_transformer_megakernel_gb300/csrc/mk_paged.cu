@@ -23,12 +23,14 @@ __device__ __forceinline__ void report(int32_t *status, int code) {
 // Append: q, k and v heads of n tokens, normalised, rotated and stored.
 //
 // Bound by bytes: every element is read once and written once; the arithmetic
-// is a sum of squares and one rotation.  D / 2 / N threads hold one head, each
-// N consecutive elements of the first half and the N elements half a head
-// further, the pairs of the rotation, so that every load and store is 16 bytes
-// of an input row and the pair meets in one thread; the squares are summed over
-// the head's threads by shuffles.  A thread that would need a page outside the
-// cache or a rotary row outside the table writes nothing.
+// is a sum of squares and one rotation.  D / 2 / N threads hold a head, each N
+// consecutive elements of the first half and the N elements half a head further,
+// the pairs of the rotation, so that every load and store is 16 bytes of an input
+// row and a pair meets in one thread; the squares are summed over the head's
+// threads by shuffles.  A thread takes up to kHeads heads of its token: their
+// loads are on their way together, and the token's slot, page, cos and sin are
+// looked up once for them.  A thread that would need a page outside the cache or
+// a rotary row outside the table writes nothing.
 // ---------------------------------------------------------------------------
 
 struct AppendParams {
@@ -43,6 +45,7 @@ struct AppendParams {
   int32_t *status;
   int n, hq, hkv, n_pages, page_size, table_rows, table_cols, rope_rows, rope_mode, sec0, sec1, sec2;
   int seq0, slot0;             // slots == NULL: row i is slot slot0 + i of sequence seq0
+  int groups, rows;            // head groups (of up to kHeads heads) of a CTA and token rows of a CTA
   float eps;
 };
 
@@ -80,7 +83,7 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-// N values to the cache: bf16, or e4m3 of value / scale
+// N values to the cache: bf16, or e4m3 of value / scale (times the scale's reciprocal: a last place of fp32 away)
 template <int N>
 __device__ __forceinline__ void store_cache(__nv_bfloat16 *p, const float *x, float) {
   uint32_t w[N / 2];
@@ -92,12 +95,12 @@ __device__ __forceinline__ void store_cache(__nv_bfloat16 *p, const float *x, fl
     *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
 }
 template <int N>
-__device__ __forceinline__ void store_cache(__nv_fp8_e4m3 *p, const float *x, float scale) {
+__device__ __forceinline__ void store_cache(__nv_fp8_e4m3 *p, const float *x, float inv) {
   uint32_t w[N / 4];
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
-    const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] / scale, x[4 * i + 1] / scale), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] / scale, x[4 * i + 3] / scale), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
     w[i] = a | (b << 16);
   }
   if constexpr (N == 8)
@@ -106,31 +109,36 @@ __device__ __forceinline__ void store_cache(__nv_fp8_e4m3 *p, const float *x, fl
     *reinterpret_cast<uint32_t *>(p) = w[0];
 }
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 256, kHeads = 4;
 
 template <class T, class C, int D>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
   constexpr int N = Vec<T>::N, TPH = D / 2 / N;           // threads of one head
   const int heads = p.hq + 2 * p.hkv;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / TPH) + threadIdx.x / TPH;
-  const int i0 = (threadIdx.x % TPH) * N;
-  const bool live = item < static_cast<int64_t>(p.n) * heads;
-  const int row = live ? static_cast<int>(item / heads) : 0, h = live ? static_cast<int>(item % heads) : 0;
-  const int slot = !live ? -1 : p.slots ? p.slots[row] : p.slot0 + row;
+  const int item = threadIdx.x / TPH, i0 = (threadIdx.x % TPH) * N;
+  const int row_in = item / p.groups, step = (heads + kHeads - 1) / kHeads;
+  const int first = blockIdx.y * p.groups + item % p.groups;   // heads first, first + step, ...
+  const int64_t row64 = static_cast<int64_t>(blockIdx.x) * p.rows + row_in;
+  const bool live = row_in < p.rows && row64 < p.n && first < step;
+  const int row = live ? static_cast<int>(row64) : 0;
+
   // every thread of a warp stays to the shuffles below; one with nothing to do works on zeros
-  bool ok = slot >= 0;
-  const bool is_q = h < p.hq, is_k = !is_q && h < p.hq + p.hkv;
-  const int kvh = is_q ? 0 : is_k ? h - p.hq : h - p.hq - p.hkv;
-  float lo[N], hi[N];
+  float lo[kHeads][N], hi[kHeads][N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) lo[i] = hi[i] = 0.f;
-  if (ok) {
-    const T *src = is_q ? static_cast<const T *>(p.q) + row * p.q_row + h * p.q_head
-                        : is_k ? static_cast<const T *>(p.k) + row * p.k_row + kvh * p.k_head
-                               : static_cast<const T *>(p.v) + row * p.v_row + kvh * p.v_head;
-    Vec<T>::load(src + i0, lo);
-    Vec<T>::load(src + i0 + D / 2, hi);
+  for (int j = 0; j < kHeads; ++j) {
+    const int h = first + j * step;
+#pragma unroll
+    for (int i = 0; i < N; ++i) lo[j][i] = hi[j][i] = 0.f;
+    if (live && h < heads) {
+      const T *src = h < p.hq ? static_cast<const T *>(p.q) + row * p.q_row + h * p.q_head
+                              : h < p.hq + p.hkv ? static_cast<const T *>(p.k) + row * p.k_row + (h - p.hq) * p.k_head
+                                                 : static_cast<const T *>(p.v) + row * p.v_row + (h - p.hq - p.hkv) * p.v_head;
+      Vec<T>::load(src + i0, lo[j]);
+      Vec<T>::load(src + i0 + D / 2, hi[j]);
+    }
   }
+  const int slot = !live ? -1 : p.slots ? p.slots[row] : p.slot0 + row;
+  bool ok = slot >= 0;
   int64_t dst = 0;
   float2 cs[N];
   if (ok) {
@@ -138,11 +146,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     const int col = slot / p.page_size;
     int page = -1;
     if (seq >= 0 && seq < p.table_rows && col < p.table_cols) page = p.table[seq * p.table_stride + col];
-    if (page < 0 || page >= p.n_pages) {
-      ok = false;
-      report(p.status, MK_ERR_BAD_PAGE);
-    }
-    dst = page * p.page_stride + kvh * p.head_stride + (slot - col * p.page_size) * p.slot_stride;
     if (p.rope) {
       int at[3];
       at[0] = p.positions ? p.positions[row] : slot;
@@ -152,7 +155,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       if (at[0] < 0 || at[0] >= p.rope_rows || at[1] < 0 || at[1] >= p.rope_rows || at[2] < 0 || at[2] >= p.rope_rows) {
         ok = false;
         report(p.status, MK_ERR_BAD_POSITION);
-      } else if (is_q || is_k) {
+      } else if (first < p.hq + p.hkv) {
         if (p.rope_mode == 0) {
           const float4 *r = reinterpret_cast<const float4 *>(p.rope + static_cast<int64_t>(at[0]) * (D / 2) + i0);
 #pragma unroll
@@ -172,50 +175,64 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
         }
       }
     }
-  }
-  const uint16_t *gain = is_q ? p.q_norm : is_k ? p.k_norm : nullptr;
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) ss += lo[i] * lo[i] + hi[i] * hi[i];
-#pragma unroll
-  for (int o = TPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (!ok) return;
-  if (gain) {
-    const float r = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      lo[i] = lo[i] * r * bf16_lo(gain[i0 + i]);
-      hi[i] = hi[i] * r * bf16_lo(gain[i0 + D / 2 + i]);
+    if (page < 0 || page >= p.n_pages) {
+      if (ok) report(p.status, MK_ERR_BAD_PAGE);
+      ok = false;
     }
+    dst = page * p.page_stride + (slot - col * p.page_size) * p.slot_stride;
   }
-  if (p.rope && (is_q || is_k)) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float a = lo[i], b = hi[i];
-      lo[i] = a * cs[i].x - b * cs[i].y;
-      hi[i] = b * cs[i].x + a * cs[i].y;
+  for (int j = 0; j < kHeads; ++j) {
+    const int h = first + j * step;
+    const bool is_q = h < p.hq, is_k = !is_q && h < p.hq + p.hkv;
+    const uint16_t *gain = is_q ? p.q_norm : is_k ? p.k_norm : nullptr;
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) ss += lo[j][i] * lo[j][i] + hi[j][i] * hi[j][i];
+#pragma unroll
+    for (int o = TPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (!ok || h >= heads) continue;
+    if (gain) {
+      const float r = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        lo[j][i] = lo[j][i] * r * bf16_lo(gain[i0 + i]);
+        hi[j][i] = hi[j][i] * r * bf16_lo(gain[i0 + D / 2 + i]);
+      }
     }
-  }
-  if (is_q) {
-    T *out = static_cast<T *>(p.q_out) + row * p.out_row + h * p.out_head;
-    Vec<T>::store(out + i0, lo);
-    Vec<T>::store(out + i0 + D / 2, hi);
-  } else {
-    C *out = static_cast<C *>(is_k ? p.k_cache : p.v_cache) + dst;
-    const float *scales = is_k ? p.k_scale : p.v_scale;
-    const float scale = scales ? scales[kvh] : 1.0f;
-    store_cache<N>(out + i0, lo, scale);
-    store_cache<N>(out + i0 + D / 2, hi, scale);
+    if (p.rope && (is_q || is_k)) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float a = lo[j][i], b = hi[j][i];
+        lo[j][i] = a * cs[i].x - b * cs[i].y;
+        hi[j][i] = b * cs[i].x + a * cs[i].y;
+      }
+    }
+    if (is_q) {
+      T *out = static_cast<T *>(p.q_out) + row * p.out_row + h * p.out_head;
+      Vec<T>::store(out + i0, lo[j]);
+      Vec<T>::store(out + i0 + D / 2, hi[j]);
+    } else {
+      const int kvh = is_k ? h - p.hq : h - p.hq - p.hkv;
+      C *out = static_cast<C *>(is_k ? p.k_cache : p.v_cache) + dst + kvh * p.head_stride;
+      const float *scales = is_k ? p.k_scale : p.v_scale;
+      const float inv = scales ? 1.0f / scales[kvh] : 1.0f;
+      store_cache<N>(out + i0, lo[j], inv);
+      store_cache<N>(out + i0 + D / 2, hi[j], inv);
+    }
   }
 }
 
 template <class T, class C, int D>
-int launch_append(const AppendParams &p, cudaStream_t s) {
-  constexpr int per_cta = kAppendThreads / (D / 2 / Vec<T>::N);
-  const int64_t items = static_cast<int64_t>(p.n) * (static_cast<int64_t>(p.hq) + 2 * static_cast<int64_t>(p.hkv));
-  const int64_t ctas = (items + per_cta - 1) / per_cta;
-  if (p.hq > (1 << 20) || p.hkv > (1 << 20) || ctas > INT32_MAX) return MK_ERR_UNSUPPORTED;
-  append_kernel<T, C, D><<<static_cast<unsigned>(ctas), kAppendThreads, 0, s>>>(p);
+int launch_append(AppendParams p, cudaStream_t s) {
+  constexpr int items = kAppendThreads / (D / 2 / Vec<T>::N);   // head groups a CTA has threads for
+  if (p.hq > (1 << 20) || p.hkv > (1 << 20)) return MK_ERR_UNSUPPORTED;
+  const int groups = (p.hq + 2 * p.hkv + kHeads - 1) / kHeads;
+  p.groups = std::min(groups, items);
+  p.rows = items / p.groups;
+  const int ctas = (p.n - 1) / p.rows + 1, parts = (groups + p.groups - 1) / p.groups;
+  if (parts > 65535) return MK_ERR_UNSUPPORTED;
+  append_kernel<T, C, D><<<dim3(ctas, parts), kAppendThreads, 0, s>>>(p);
   if (cudaPeekAtLastError() != cudaSuccess) {
     cudaGetLastError();
     return MK_ERR_CUDA;
@@ -242,28 +259,34 @@ int run_append(const AppendParams &p, int dtype, int cache, int d, cudaStream_t 
 // l (kept in log2 units): o = sum 2^(s_p - m) v_p, rescaled when m grows.  Bound
 // by the cache's bytes.
 //
-// The query heads of a kv head (up to 16 a pass) are the 16 rows of 16x8x16 matrix
-// products, so that the cache is read once for the whole group.  bf16 keys and
-// values multiply bf16 terms: a bf16 query is one term, an fp32 query three, and
-// the probabilities two terms (three for fp32 outputs), which keeps the result as
-// exact as fp32 products would.  e4m3 keys and values become fp16, exactly; the
-// query row is scaled by a power of two into fp16's range (one term, two for
-// fp32) and the probabilities by 2^14.  Each tile's value sums start from zero
-// and are added to the running ones by an fp32 multiply-add: matrix products
-// truncate what they add to an accumulator, which over thousands of tiles would
-// show.
+// The cache is read once for all query heads of a kv head (up to 16 a pass): the
+// keys of 16 slots are the rows of a 16x8x16 matrix product and 8 query heads its
+// columns, and the values, transposed on the way out of shared memory, the rows
+// of a second one whose columns are the heads' probabilities.  Heads as columns
+// waste nothing on a group of up to 8 (twice the columns for 16), half of what
+// heads as rows would multiply.
+// bf16 keys and values multiply bf16 terms: a bf16 query is one term, an fp32
+// query three, and the probabilities two terms (three for fp32 outputs), which
+// keeps the result as exact as fp32 products would.  e4m3 keys and values become
+// fp16, exactly; the query row is scaled by a power of two into fp16's range (one
+// term, two for fp32) and the probabilities by 2^14.  Each tile's value sums
+// start from zero and are added to the running ones by an fp32 multiply-add:
+// matrix products truncate what they add to an accumulator, which over thousands
+// of tiles would show.
 //
 // Work: the tiles (POS slots of one row and kv head) of all rows, in order, are
-// cut into equal ranges for the CTAs and these for their 8 warps, whatever the
-// lengths.  A warp streams its range through its own ring of shared memory with
-// asynchronous 16-byte copies and never waits for another warp until the end.
-// What a warp has of a row at its range's ends is joined with its neighbours'
-// in shared memory, what a CTA has at its ends through the workspace by
-// join_kernel, always in order: the same lengths give the same bits.
+// cut into ranges of equal cost for the CTAs and these for their 8 warps,
+// whatever the lengths.  A warp streams its range through its own ring of shared
+// memory with asynchronous 16-byte copies and never waits for another warp until
+// the end.  What a warp has of a row at its range's ends is joined with its
+// neighbours' in shared memory, what a CTA has at its ends through the workspace
+// by join_kernel, always in order: the same lengths give the same bits.
 // ---------------------------------------------------------------------------
 
 constexpr int kWarps = 8, kAttnThreads = 32 * kWarps;
-constexpr int kMinTilesPerCta = 16;
+constexpr int kMinUnitsPerCta = 16;
+// what the start of a row and head costs (its queries' loads, its results' stores), in tiles
+constexpr int kRowCost = 2;
 constexpr int kMaxSmem = 230400;       // dynamic; the static part is below 2 KB, a CTA's limit 227 KB
 
 struct AttnParams {
@@ -278,7 +301,7 @@ struct AttnParams {
   float *parts;        // [grid][2][gr][D + 4]: a row's middle or end (0) and its beginning (1)
   int n, hq, hkv, group, n_pages, page_size, table_cols, window;
   int blocks, vh;      // head blocks of 16 query heads a kv head, virtual heads hkv * blocks
-  int gr;              // query rows kept of a block: min(group, 16)
+  int gr;              // query heads of a block: min(group, 16)
   int stages;
   float scale;
 };
@@ -302,9 +325,10 @@ __device__ __forceinline__ float2 load_pair(const __nv_bfloat16 *p) {
 __device__ __forceinline__ void store_one(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store_one(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
-// tiles of a row: those that hold any of its slots [lo, hi)
+// tiles of a row: those that hold any of its slots [lo, hi), and their cost, the row's start included
 struct Span {
   int lo, hi, first, count;
+  __device__ __forceinline__ int cost() const { return count ? count + kRowCost : 0; }
 };
 template <int POS>
 __device__ __forceinline__ Span span_of(const AttnParams &p, int len) {
@@ -321,7 +345,8 @@ __device__ __forceinline__ Span span_of(const AttnParams &p, int len) {
 struct TileInfo {
   int row, vh, pos, lo, hi, flags;
 };
-constexpr int kFirst = 1, kLast = 2, kBad = 4;   // the row's first tile, its last, a page outside the cache
+// the row's first tile, its last, a page outside the cache, the last tile of the warp
+constexpr int kFirst = 1, kLast = 2, kBad = 4, kEnd = 8;
 
 struct PartInfo {
   int row, vh, begins, ends;   // row < 0: no part
@@ -333,6 +358,7 @@ constexpr int kPartStride = D + 4;      // o[D], m, l
 // the join of parts (m_j, l_j, o_j): m = max m_j, weights 2^(m_j - m)
 __device__ __forceinline__ float join_base(float m) { return m == -INFINITY ? 0.f : m; }
 
+// o / l and the log-sum-exp of one finished element
 template <class T>
 __device__ __forceinline__ void write_out(const AttnParams &p, int row, int head, int d, float o, float l, float vs) {
   const float r = l == 0.f ? 0.f : 1.0f / l;
@@ -342,13 +368,26 @@ __device__ __forceinline__ void write_lse(const AttnParams &p, int row, int head
   if (p.lse) p.lse[static_cast<int64_t>(row) * p.hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-template <class T, bool FP8, int D>
+// over the 8 rows of a column of a product: lanes with the same t
+__device__ __forceinline__ float column_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float column_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+// HB: blocks of 8 query heads
+template <class T, bool FP8, int D, int HB>
 __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParams p) {
   using TL = Tile<D, FP8>;
   using Op = std::conditional_t<FP8, mkw::FP16Op, mkw::BF16Op>;
   constexpr bool F32 = std::is_same<T, float>::value;
   constexpr int TQ = F32 ? (FP8 ? 2 : 3) : 1, TP = F32 ? (FP8 ? 2 : 3) : (FP8 ? 1 : 2);
-  constexpr int POS = TL::POS, KS = D / 16, NT = D / 8, SN = POS / 8, PN = POS / 16, PST = kPartStride<D>;
+  constexpr int POS = TL::POS, KS = D / 16, DB = D / 16, PN = POS / 16, PST = kPartStride<D>;
   constexpr float kShift = FP8 ? 14.f : 0.f;             // probabilities are scaled by 2^kShift
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ TileInfo s_tile[kWarps][3];
@@ -358,12 +397,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParam
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   mkw::launch_dependents();
 
-  // ---- tiles before every group of rows ------------------------------------
+  // ---- cost of the rows before every group of rows ---------------------------
   const int per = (p.n + kAttnThreads - 1) / kAttnThreads;   // rows a thread counts
   int mine = 0;
   for (int i = 0; i < per; ++i) {
     const int r = tid * per + i;
-    if (r < p.n) mine += span_of<POS>(p, p.lengths[r]).count;
+    if (r < p.n) mine += span_of<POS>(p, p.lengths[r]).cost();
   }
   int incl = mine;
 #pragma unroll
@@ -380,22 +419,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParam
     if (i < w) before += s_warp[i];
     total += s_warp[i];
   }
-  s_scan[tid] = before + incl - mine;                        // tiles of the rows before this thread's
+  s_scan[tid] = before + incl - mine;                        // cost of the rows before this thread's
   __syncthreads();
 
-  const int64_t tiles = static_cast<int64_t>(total) * p.vh;
-  const int64_t wanted = (tiles + kMinTilesPerCta - 1) / kMinTilesPerCta;
+  // Units: a row and head of cost c covers c of them, tile j the (kRowCost + j)th.  A warp has the tiles whose unit is
+  // in its range.
+  const int64_t units = static_cast<int64_t>(total) * p.vh;
+  const int64_t wanted = (units + kMinUnitsPerCta - 1) / kMinUnitsPerCta;
   const int ctas = static_cast<int>(wanted < 1 ? 1 : wanted < gridDim.x ? wanted : gridDim.x);
   const int cta = blockIdx.x;
-  const int64_t c_begin = cta < ctas ? tiles * cta / ctas : 0, c_end = cta < ctas ? tiles * (cta + 1) / ctas : 0;
+  const int64_t c_begin = cta < ctas ? units * cta / ctas : 0, c_end = cta < ctas ? units * (cta + 1) / ctas : 0;
   const int64_t begin = c_begin + (c_end - c_begin) * w / kWarps, end = c_begin + (c_end - c_begin) * (w + 1) / kWarps;
-  const int n_tiles = static_cast<int>(end - begin);
+  int left = static_cast<int>(end - begin);                  // units from the tile the producer stands at to the range's end
 
   // ---- where this warp's range starts ---------------------------------------
   int row = 0, vh = 0, tile = 0;
   Span sp{0, 0, 0, 0};
-  if (n_tiles > 0) {
-    const int x = static_cast<int>(begin / p.vh);            // in [before(row), before(row) + count(row))
+  if (left > 0) {
+    const int x = static_cast<int>(begin / p.vh);            // in [before(row), before(row) + cost(row))
     int a = 0, b = kAttnThreads;
     while (b - a > 1) {
       const int m = (a + b) >> 1;
@@ -404,13 +445,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParam
     int at = s_scan[a];
     row = a * per;
     sp = span_of<POS>(p, p.lengths[row]);
-    while (at + sp.count <= x) {
-      at += sp.count;
+    while (at + sp.cost() <= x) {
+      at += sp.cost();
       sp = span_of<POS>(p, p.lengths[++row]);
     }
     const int64_t rest = begin - static_cast<int64_t>(at) * p.vh;
-    vh = static_cast<int>(rest / sp.count);
-    tile = static_cast<int>(rest - static_cast<int64_t>(vh) * sp.count);
+    vh = static_cast<int>(rest / sp.cost());
+    tile = static_cast<int>(rest - static_cast<int64_t>(vh) * sp.cost()) - kRowCost;
+    if (tile < 0) left += tile, tile = 0;                    // from the row's start on: its cost comes first
   }
 
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + w * p.stages * TL::STAGE;
@@ -422,46 +464,68 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParam
     if (lane < POS && pos >= sp.lo && pos < sp.hi) page = p.table[row * p.table_stride + pos / p.page_size];
     return page;
   };
-  int next_page = n_tiles > 0 ? page_of((sp.first + tile) * POS + lane) : -1;
-  int produced = 0;
+  int next_page = left > 0 ? page_of((sp.first + tile) * POS + lane) : -1;
+  int in_stage = 0;                                          // the producer's stage
+  const int r0 = lane / TL::CPR, c0 = lane % TL::CPR;        // this lane's first slot of a tile and its chunk
+  const int64_t lane_off = r0 * p.slot_stride * TL::ES + c0 * 16, row_step = 32 / TL::CPR * p.slot_stride * TL::ES;
   auto produce = [&]() {
     const int pos0 = (sp.first + tile) * POS, pos = pos0 + lane;
     const bool want = lane < POS && pos >= sp.lo && pos < sp.hi;
     const bool fine = want && next_page >= 0 && next_page < p.n_pages;
-    const unsigned bad = __ballot_sync(0xffffffffu, want && !fine);
-    int64_t off = 0;
-    if (fine) off = (next_page * p.page_stride + (vh / p.blocks) * p.head_stride + (pos % p.page_size) * p.slot_stride) * TL::ES;
+    const int slot = pos % p.page_size;
     const unsigned have = __ballot_sync(0xffffffffu, fine);
-    const int stage = produced % p.stages;
-    const uint32_t ks = ring + stage * TL::STAGE, vs = ks + TL::KBYTES;
+    const bool bad = __any_sync(0xffffffffu, want && !fine);
+    const uint32_t ks = ring + in_stage * TL::STAGE;
+    int64_t off = 0;
+    if (fine) off = (next_page * p.page_stride + (vh / p.blocks) * p.head_stride + slot * p.slot_stride) * TL::ES;
+    if (have == (POS == 32 ? 0xffffffffu : 0xffffu) && __shfl_sync(0xffffffffu, slot, 0) + POS <= p.page_size) {
+      // a whole tile inside a page: its slots are one stride apart
+      const int64_t o = __shfl_sync(0xffffffffu, off, 0) + lane_off;
+      const unsigned char *ka = k_base + o, *va = v_base + o;
 #pragma unroll
-    for (int i = 0; i < POS * TL::CPR / 32; ++i) {
-      const int idx = i * 32 + lane, r = idx / TL::CPR, c = idx % TL::CPR;
-      const int64_t o = __shfl_sync(0xffffffffu, off, r) + c * 16;
-      const bool ok = (have >> r) & 1;
-      mkw::cp_async16(ks + TL::at(r, c), k_base + (ok ? o : 0), ok);
-      mkw::cp_async16(vs + TL::at(r, c), v_base + (ok ? o : 0), ok);
+      for (int i = 0; i < POS * TL::CPR / 32; ++i) {
+        const int r = i * (32 / TL::CPR) + r0;
+        mkw::cp_async16(ks + TL::at(r, c0), ka);
+        mkw::cp_async16(ks + TL::KBYTES + TL::at(r, c0), va);
+        ka += row_step;
+        va += row_step;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < POS * TL::CPR / 32; ++i) {
+        const int r = i * (32 / TL::CPR) + r0;
+        const int64_t o = __shfl_sync(0xffffffffu, off, r) + c0 * 16;
+        const bool ok = (have >> r) & 1;
+        mkw::cp_async16(ks + TL::at(r, c0), k_base + (ok ? o : 0), ok);
+        mkw::cp_async16(ks + TL::KBYTES + TL::at(r, c0), v_base + (ok ? o : 0), ok);
+      }
     }
-    if (lane == 0) {
-      s_tile[w][stage] = TileInfo{row, vh, pos0, sp.lo, sp.hi,
-                                  (tile == 0 ? kFirst : 0) | (tile == sp.count - 1 ? kLast : 0) | (bad ? kBad : 0)};
-      if (bad) report(p.status, MK_ERR_BAD_PAGE);
-    }
-    ++produced;
-    if (produced < n_tiles) {
-      if (++tile == sp.count) {
-        tile = 0;
-        if (++vh == p.vh) {
-          vh = 0;
+    int flags = (tile == 0 ? kFirst : 0) | (bad ? kBad : 0);
+    const int at_row = row, at_vh = vh, lo = sp.lo, hi = sp.hi;
+    --left;
+    if (++tile == sp.count) {
+      flags |= kLast;
+      left -= kRowCost;
+      tile = 0;
+      if (++vh == p.vh) {
+        vh = 0;
+        if (left > 0) {
           do sp = span_of<POS>(p, p.lengths[++row]);
           while (sp.count == 0);
         }
       }
-      next_page = page_of((sp.first + tile) * POS + lane);
     }
+    if (left > 0) next_page = page_of((sp.first + tile) * POS + lane);
+    else flags |= kEnd;
+    if (lane == 0) {
+      s_tile[w][in_stage] = TileInfo{at_row, at_vh, pos0, lo, hi, flags};
+      if (bad) report(p.status, MK_ERR_BAD_PAGE);
+    }
+    if (++in_stage == p.stages) in_stage = 0;
   };
+  const bool any = left > 0;
   for (int i = 0; i < p.stages - 1; ++i) {
-    if (produced < n_tiles) produce();
+    if (left > 0) produce();
     mkw::cp_async_commit();
   }
 
@@ -478,245 +542,238 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParam
   }
 
   // ---- the warp's tiles ---------------------------------------------------------
-  uint32_t qf[TQ][KS][4];
-  float o[NT][4], m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f, mult0 = 0.f, mult1 = 0.f;
+  // columns: heads 8 hb + g in the query's fragments, 8 hb + 2t and 2t + 1 in scores, states and outputs
+  uint32_t qf[TQ][KS][HB][2];
+  float o[DB][HB][4], m[HB][2], l[HB][2], mult[HB][2];
   int rows = 0, head0 = 0, begins = 0;
   float *first_part = reinterpret_cast<float *>(smem + kWarps * p.stages * TL::STAGE) + w * p.gr * PST;
   float *last_part = reinterpret_cast<float *>(smem + w * p.stages * TL::STAGE);
-  for (int i = 0; i < n_tiles; ++i) {
-    if (produced < n_tiles) produce();
+  int stage = 0;
+  bool start = true;
+  for (bool more = any; more;) {
+    if (left > 0) produce();
     mkw::cp_async_commit();
     if (p.stages == 3) mkw::cp_async_wait<2>(); else mkw::cp_async_wait<1>();
     __syncwarp();
-    const int stage = i % p.stages;
     const TileInfo ti = s_tile[w][stage];
     const uint32_t kt = ring + stage * TL::STAGE, vt = kt + TL::KBYTES;
+    if (++stage == p.stages) stage = 0;
+    more = !(ti.flags & kEnd);
 
-    if (i == 0 || (ti.flags & kFirst)) {                    // a row's query heads
+    if (start) {                                             // a row's query heads
+      start = false;
       const int kvh = ti.vh / p.blocks, blk = ti.vh % p.blocks;
       head0 = kvh * p.group + blk * 16;
-      rows = min(16, p.group - blk * 16);
+      rows = min(8 * HB, p.group - blk * 16);
       begins = ti.flags & kFirst;
-      const T *q0 = static_cast<const T *>(p.q) + ti.row * p.q_row + (head0 + g) * p.q_head, *q1 = q0 + 8 * p.q_head;
-      float2 x[KS][4];
+      const float to_log2 = p.scale * 1.4426950408889634f * (FP8 && p.k_scale ? p.k_scale[kvh] : 1.f);
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        // bf16: k = 2t, 2t+1, 2t+8, 2t+9 of the step; e4m3: 4t .. 4t+3, as the key's 16-bit pairs hold them
-        const int d0 = 16 * s + (FP8 ? 4 * t : 2 * t), d1 = d0 + (FP8 ? 2 : 8);
-        x[s][0] = x[s][1] = x[s][2] = x[s][3] = make_float2(0.f, 0.f);
-        if (g < rows) x[s][0] = load_pair(q0 + d0), x[s][2] = load_pair(q0 + d1);
-        if (g + 8 < rows) x[s][1] = load_pair(q1 + d0), x[s][3] = load_pair(q1 + d1);
-      }
-      mult0 = mult1 = p.scale * 1.4426950408889634f * (FP8 && p.k_scale ? p.k_scale[kvh] : 1.f);
-      if constexpr (FP8) {
-        float a0 = 0.f, a1 = 0.f;
+      for (int hb = 0; hb < HB; ++hb) {
+        const int h = 8 * hb + g;
+        const T *q = static_cast<const T *>(p.q) + ti.row * p.q_row + (head0 + h) * p.q_head;
+        float2 x[KS][2];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-          a0 = fmaxf(a0, fmaxf(fmaxf(fabsf(x[s][0].x), fabsf(x[s][0].y)), fmaxf(fabsf(x[s][2].x), fabsf(x[s][2].y))));
-          a1 = fmaxf(a1, fmaxf(fmaxf(fabsf(x[s][1].x), fabsf(x[s][1].y)), fmaxf(fabsf(x[s][3].x), fabsf(x[s][3].y))));
+          // bf16: k = 2t, 2t+1, 2t+8, 2t+9 of the step; e4m3: 4t .. 4t+3, as the key's 16-bit pairs hold them
+          const int d0 = 16 * s + (FP8 ? 4 * t : 2 * t), d1 = d0 + (FP8 ? 2 : 8);
+          x[s][0] = x[s][1] = make_float2(0.f, 0.f);
+          if (h < rows) x[s][0] = load_pair(q + d0), x[s][1] = load_pair(q + d1);
         }
-        a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 1));
-        a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
-        a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
-        a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
-        // largest element to [2^13, 2^14); the exponent of 2^e stays within fp32's
-        const int e0 = a0 > 0.f && a0 < INFINITY ? max(-126, min(126, 13 - ilogbf(a0))) : 0;
-        const int e1 = a1 > 0.f && a1 < INFINITY ? max(-126, min(126, 13 - ilogbf(a1))) : 0;
-        const float f0 = ldexpf(1.f, e0), f1 = ldexpf(1.f, e1);
-        mult0 *= ldexpf(1.f, -e0);
-        mult1 *= ldexpf(1.f, -e1);
+        mult[hb][0] = mult[hb][1] = to_log2;
+        if constexpr (FP8) {
+          float a = 0.f;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          x[s][0].x *= f0, x[s][0].y *= f0, x[s][2].x *= f0, x[s][2].y *= f0;
-          x[s][1].x *= f1, x[s][1].y *= f1, x[s][3].x *= f1, x[s][3].y *= f1;
+          for (int s = 0; s < KS; ++s)
+            a = fmaxf(a, fmaxf(fmaxf(fabsf(x[s][0].x), fabsf(x[s][0].y)), fmaxf(fabsf(x[s][1].x), fabsf(x[s][1].y))));
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+          // largest element to [2^13, 2^14); the exponent of 2^e stays within fp32's
+          const int e = a > 0.f && a < INFINITY ? max(-126, min(126, 13 - ilogbf(a))) : 0;
+          const float f = ldexpf(1.f, e), back = ldexpf(1.f, -e);
+#pragma unroll
+          for (int s = 0; s < KS; ++s) x[s][0].x *= f, x[s][0].y *= f, x[s][1].x *= f, x[s][1].y *= f;
+          mult[hb][0] *= __shfl_sync(0xffffffffu, back, 8 * t);
+          mult[hb][1] *= __shfl_sync(0xffffffffu, back, 8 * t + 4);
         }
-      }
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int u = 0; u < TQ; ++u) {
-            const float2 whole = x[s][j];
-            qf[u][s][j] = mkw::take_input_term(Op{}, x[s][j].x, x[s][j].y);
-            if (!FP8 && u + 1 < TQ) {
-              x[s][j].x = mkw::signed_rest(x[s][j].x, whole.x);
-              x[s][j].y = mkw::signed_rest(x[s][j].y, whole.y);
+            for (int u = 0; u < TQ; ++u) {
+              const float2 whole = x[s][j];
+              qf[u][s][hb][j] = mkw::take_input_term(Op{}, x[s][j].x, x[s][j].y);
+              if (!FP8 && u + 1 < TQ) {
+                x[s][j].x = mkw::signed_rest(x[s][j].x, whole.x);
+                x[s][j].y = mkw::signed_rest(x[s][j].y, whole.y);
+              }
             }
-          }
 #pragma unroll
-      for (int s = 0; s < NT; ++s) o[s][0] = o[s][1] = o[s][2] = o[s][3] = 0.f;
-      m0 = m1 = -INFINITY;
-      l0 = l1 = 0.f;
+        for (int c = 0; c < DB; ++c) o[c][hb][0] = o[c][hb][1] = o[c][hb][2] = o[c][hb][3] = 0.f;
+        m[hb][0] = m[hb][1] = -INFINITY;
+        l[hb][0] = l[hb][1] = 0.f;
+      }
     }
 
-    // scores of the tile: rows g, g + 8; slots 8 j + 2t, + 1
-    float sc[SN][4], sl[SN][4];
+    // ---- scores: slots 16 nb + g, + 8 by heads 2t, 2t + 1 -----------------------
+    // two sums a block (even and odd steps; the first term and the others), for shorter chains
+    float sc[PN][HB][4], sl[PN][HB][4];
 #pragma unroll
-    for (int j = 0; j < SN; ++j)
+    for (int s = 0; s < KS; s += 2) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) sc[j][c] = sl[j][c] = 0.f;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      if constexpr (!FP8) {
-#pragma unroll
-        for (int nb = 0; nb < PN; ++nb) {
+      for (int nb = 0; nb < PN; ++nb) {
+        uint32_t a[2][4];
+        const int r = nb * 16 + (lane & 15);
+        if constexpr (!FP8) {
+          mkw::ldmatrix4(a[0], kt + TL::at(r, 2 * s + (lane >> 4)));
+          mkw::ldmatrix4(a[1], kt + TL::at(r, 2 * s + 2 + (lane >> 4)));
+        } else {
           uint32_t f[4];
-          mkw::ldmatrix4(f, kt + TL::at(nb * 16 + ((lane >> 4) << 3) + (lane & 7), 2 * s + ((lane >> 3) & 1)));
-          mkw::mma(Op{}, sc[2 * nb], qf[0][s], f[0], f[1]);
-          mkw::mma(Op{}, sc[2 * nb + 1], qf[0][s], f[2], f[3]);
+          mkw::ldmatrix4(f, kt + TL::at(r, s + (lane >> 4)));
 #pragma unroll
-          for (int u = TQ - 1; u > 0; --u) {
-            mkw::mma(Op{}, sl[2 * nb], qf[u][s], f[0], f[1]);
-            mkw::mma(Op{}, sl[2 * nb + 1], qf[u][s], f[2], f[3]);
+          for (int j = 0; j < 2; ++j) {
+            a[j][0] = mkw::e4m3x2_to_half2(f[2 * j] & 0xffffu), a[j][2] = mkw::e4m3x2_to_half2(f[2 * j] >> 16);
+            a[j][1] = mkw::e4m3x2_to_half2(f[2 * j + 1] & 0xffffu), a[j][3] = mkw::e4m3x2_to_half2(f[2 * j + 1] >> 16);
           }
         }
-      } else {
-        uint32_t f[4];
-        mkw::ldmatrix4(f, kt + TL::at(lane, s));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t b0 = mkw::e4m3x2_to_half2(f[j] & 0xffffu), b1 = mkw::e4m3x2_to_half2(f[j] >> 16);
-          mkw::mma(Op{}, sc[j], qf[0][s], b0, b1);
-          if constexpr (TQ > 1) mkw::mma(Op{}, sl[j], qf[1][s], b0, b1);
+        for (int hb = 0; hb < HB; ++hb) {
+          float *c = sc[nb][hb], *e = sl[nb][hb];
+          if constexpr (TQ == 1) {
+            if (s == 0) {
+              mkw::mma_zero(Op{}, c, a[0], qf[0][s][hb][0], qf[0][s][hb][1]);
+              mkw::mma_zero(Op{}, e, a[1], qf[0][s + 1][hb][0], qf[0][s + 1][hb][1]);
+            } else {
+              mkw::mma(Op{}, c, a[0], qf[0][s][hb][0], qf[0][s][hb][1]);
+              mkw::mma(Op{}, e, a[1], qf[0][s + 1][hb][0], qf[0][s + 1][hb][1]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (s + j == 0) mkw::mma_zero(Op{}, c, a[j], qf[0][s + j][hb][0], qf[0][s + j][hb][1]);
+              else mkw::mma(Op{}, c, a[j], qf[0][s + j][hb][0], qf[0][s + j][hb][1]);
+#pragma unroll
+              for (int u = TQ - 1; u > 0; --u) {
+                if (s + j == 0 && u == TQ - 1) mkw::mma_zero(Op{}, e, a[j], qf[u][s + j][hb][0], qf[u][s + j][hb][1]);
+                else mkw::mma(Op{}, e, a[j], qf[u][s + j][hb][0], qf[u][s + j][hb][1]);
+              }
+            }
+          }
         }
       }
     }
     const bool edge = ti.pos < ti.lo || ti.pos + POS > ti.hi;
-    float x0 = -INFINITY, x1 = -INFINITY;
+    float alpha[HB][2];
+    uint32_t pf[TP][PN][HB][2];
 #pragma unroll
-    for (int j = 0; j < SN; ++j) {
+    for (int hb = 0; hb < HB; ++hb) {
+      float x[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float s = sc[j][c];
-        if constexpr (TQ > 1) s += sl[j][c];
-        s *= c < 2 ? mult0 : mult1;
-        if (edge) {
-          const int pos = ti.pos + 8 * j + 2 * t + (c & 1);
-          if (pos < ti.lo || pos >= ti.hi) s = -INFINITY;
+      for (int nb = 0; nb < PN; ++nb)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float s = (sc[nb][hb][c] + sl[nb][hb][c]) * mult[hb][c & 1];
+          if (edge) {
+            const int pos = ti.pos + 16 * nb + g + (c >> 1) * 8;
+            if (pos < ti.lo || pos >= ti.hi) s = -INFINITY;
+          }
+          sc[nb][hb][c] = s;
+          x[c & 1] = fmaxf(x[c & 1], s);
         }
-        sc[j][c] = s;
+      float base[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float n = fmaxf(m[hb][j], column_max(x[j]) - kShift);
+        base[j] = join_base(n);
+        alpha[hb][j] = mkw::exp2_fast(m[hb][j] - base[j]);
+        m[hb][j] = n;
+        l[hb][j] *= alpha[hb][j];
       }
-      x0 = fmaxf(x0, fmaxf(sc[j][0], sc[j][1]));
-      x1 = fmaxf(x1, fmaxf(sc[j][2], sc[j][3]));
+#pragma unroll
+      for (int nb = 0; nb < PN; ++nb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float a = mkw::exp2_fast(sc[nb][hb][2 * j] - base[0]), b = mkw::exp2_fast(sc[nb][hb][2 * j + 1] - base[1]);
+          l[hb][0] += a;
+          l[hb][1] += b;
+#pragma unroll
+          for (int u = 0; u < TP - 1; ++u) pf[u][nb][hb][j] = mkw::transpose8(mkw::take_weight_term(Op{}, a, b));
+          pf[TP - 1][nb][hb][j] = mkw::transpose8(mkw::take_term(Op{}, a, b));
+        }
     }
-    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-    const float n0 = fmaxf(m0, x0 - kShift), n1 = fmaxf(m1, x1 - kShift);
-    const float b0 = join_base(n0), b1 = join_base(n1);
-    const float al0 = exp2f(m0 - b0), al1 = exp2f(m1 - b1);
-    m0 = n0;
-    m1 = n1;
-    l0 *= al0;
-    l1 *= al1;
-    uint32_t pf[TP][PN][4];
+
+    // ---- values: block c of 16 elements by heads 2t, 2t + 1; rows g and g + 8 of a block are its elements of that
+    // number (bf16) or elements 2g and 2g + 1 (e4m3, whose 16-bit pairs the transposition keeps together) ----------
 #pragma unroll
-    for (int nb = 0; nb < PN; ++nb) {
+    for (int c = 0; c < DB; ++c) {
+      float e[HB][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int sj = 2 * nb + (j >> 1), sc0 = (j & 1) * 2;
-        float a = exp2f(sc[sj][sc0] - ((j & 1) ? b1 : b0)), b = exp2f(sc[sj][sc0 + 1] - ((j & 1) ? b1 : b0));
-        if (j & 1) l1 += a + b; else l0 += a + b;
+      for (int nb = 0; nb < PN; ++nb) {
+        uint32_t a[4];
+        if constexpr (!FP8) {
+          mkw::ldmatrix4_trans(a, vt + TL::at(nb * 16 + ((lane >> 4) << 3) + (lane & 7), 2 * c + ((lane >> 3) & 1)));
+        } else {
+          uint32_t f[2];
+          mkw::ldmatrix2_trans(f, vt + TL::at(nb * 16 + (lane & 15), c));
 #pragma unroll
-        for (int u = 0; u < TP - 1; ++u) pf[u][nb][j] = mkw::take_weight_term(Op{}, a, b);
-        pf[TP - 1][nb][j] = mkw::take_term(Op{}, a, b);
-      }
-    }
-    // values: output tiles 2c and 2c + 1 are the 16-byte chunks of that number (bf16) or the even and the odd
-    // elements of chunk c (e4m3)
-    auto add = [&](int c, float *e, float *f) {
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t lo = mkw::e4m3x2_to_half2(f[j] & 0xffffu), hi = mkw::e4m3x2_to_half2(f[j] >> 16);
+            a[2 * j] = __byte_perm(lo, hi, 0x5410);
+            a[2 * j + 1] = __byte_perm(lo, hi, 0x7632);
+          }
+        }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        o[2 * c][k] = o[2 * c][k] * (k < 2 ? al0 : al1) + e[k];
-        o[2 * c + 1][k] = o[2 * c + 1][k] * (k < 2 ? al0 : al1) + f[k];
-      }
-    };
-    const int vr = (((lane >> 3) & 1) << 3) + (lane & 7);
-    if constexpr (!FP8) {
-#pragma unroll
-      for (int c = 0; c < NT / 2; ++c) {
-        float e[4] = {0.f, 0.f, 0.f, 0.f}, f[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int nb = 0; nb < PN; ++nb) {
-          uint32_t b[4];
-          mkw::ldmatrix4_trans(b, vt + TL::at(nb * 16 + vr, 2 * c + (lane >> 4)));
+        for (int hb = 0; hb < HB; ++hb)
 #pragma unroll
           for (int u = TP - 1; u >= 0; --u) {
-            mkw::mma(Op{}, e, pf[u][nb], b[0], b[1]);
-            mkw::mma(Op{}, f, pf[u][nb], b[2], b[3]);
+            if (nb == 0 && u == TP - 1) mkw::mma_zero(Op{}, e[hb], a, pf[u][nb][hb][0], pf[u][nb][hb][1]);
+            else mkw::mma(Op{}, e[hb], a, pf[u][nb][hb][0], pf[u][nb][hb][1]);
           }
-        }
-        add(c, e, f);
       }
-    } else {
 #pragma unroll
-      for (int c = 0; c < NT / 2; c += 2) {
-        float e[4][4];
+      for (int hb = 0; hb < HB; ++hb)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) e[k][0] = e[k][1] = e[k][2] = e[k][3] = 0.f;
-#pragma unroll
-        for (int nb = 0; nb < PN; ++nb) {
-          uint32_t r[4];
-          mkw::ldmatrix4_trans(r, vt + TL::at(nb * 16 + vr, c + (lane >> 4)));
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t b[4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t lo = mkw::e4m3x2_to_half2(r[2 * k + j] & 0xffffu), hi = mkw::e4m3x2_to_half2(r[2 * k + j] >> 16);
-              b[j] = __byte_perm(lo, hi, 0x5410);
-              b[2 + j] = __byte_perm(lo, hi, 0x7632);
-            }
-#pragma unroll
-            for (int u = TP - 1; u >= 0; --u) {
-              mkw::mma(Op{}, e[2 * k], pf[u][nb], b[0], b[1]);
-              mkw::mma(Op{}, e[2 * k + 1], pf[u][nb], b[2], b[3]);
-            }
-          }
-        }
-        add(c, e[0], e[1]);
-        add(c + 1, e[2], e[3]);
-      }
+        for (int k = 0; k < 4; ++k) o[c][hb][k] = o[c][hb][k] * alpha[hb][k & 1] + e[hb][k];
     }
-    if (ti.flags & kBad) l0 = l1 = NAN;
+    if (ti.flags & kBad) {
+#pragma unroll
+      for (int hb = 0; hb < HB; ++hb) l[hb][0] = l[hb][1] = NAN;
+    }
     __syncwarp();                                            // every lane has read the stage (and, at the end, the ring)
 
     const bool ends = ti.flags & kLast;
-    if (ends || i == n_tiles - 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-      l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if (ends || !more) {
+      start = true;
       const bool whole = begins && ends;
       float *part = ends ? first_part : last_part;
       const float vsc = FP8 && p.v_scale ? p.v_scale[ti.vh / p.blocks] : 1.f;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int r = g + 8 * k;
-        if (r >= rows) continue;
-        const float l = k ? l1 : l0, m = k ? m1 : m0;
-        const float inv = l == 0.f ? 0.f : 1.0f / l;
-        T *out = static_cast<T *>(p.out) + ti.row * p.out_row + (head0 + r) * p.out_head;
+      for (int hb = 0; hb < HB; ++hb)
 #pragma unroll
-        for (int c = 0; c < NT; ++c)
+        for (int k = 0; k < 2; ++k) {
+          const int h = 8 * hb + 2 * t + k;
+          const float sum = column_sum(l[hb][k]);
+          if (h >= rows) continue;
+          const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+          T *out = static_cast<T *>(p.out) + ti.row * p.out_row + (head0 + h) * p.out_head;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int d = FP8 ? 16 * (c >> 1) + 4 * t + 2 * j + (c & 1) : 8 * c + 2 * t + j;
-            const float x = o[c][2 * k + j];
-            if (whole) store_one(out + d, x * inv * vsc);
-            else part[r * PST + d] = x;
-          }
-        if (t == 0) {
-          if (whole) {
-            write_lse(p, ti.row, head0 + r, m, l);
-          } else {
-            part[r * PST + D] = m;
-            part[r * PST + D + 1] = l;
+          for (int c = 0; c < DB; ++c)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int d = 16 * c + (FP8 ? 2 * g + j : g + 8 * j);
+              const float x = o[c][hb][2 * j + k];
+              if (whole) store_one(out + d, x * inv * vsc);
+              else part[h * PST + d] = x;
+            }
+          if (g == 0) {
+            if (whole) {
+              write_lse(p, ti.row, head0 + h, m[hb][k], sum);
+            } else {
+              part[h * PST + D] = m[hb][k];
+              part[h * PST + D + 1] = sum;
+            }
           }
         }
-      }
       if (!whole && lane == 0) s_part[2 * w + (ends ? 0 : 1)] = PartInfo{ti.row, ti.vh, begins, ends};
     }
   }
@@ -745,39 +802,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParam
     float *slot = p.parts + (static_cast<int64_t>(cta) * 2 + (pi.begins ? 1 : 0)) * p.gr * PST;
     for (int i = tid; i < nr * D; i += kAttnThreads) {
       const int r = i / D, d = i % D;
-      float m = -INFINITY, l = 0.f, x = 0.f;
+      float mx = -INFINITY, sum = 0.f, x = 0.f;
       auto at = [&](int j) {
         const unsigned char *base = (j & 1) ? smem + (j >> 1) * p.stages * TL::STAGE
                                             : smem + kWarps * p.stages * TL::STAGE + (j >> 1) * p.gr * PST * 4;
         return reinterpret_cast<const float *>(base) + r * PST;
       };
       for (int j = a; j <= b; ++j)
-        if (s_part[j].row >= 0) m = fmaxf(m, at(j)[D]);
-      const float base = join_base(m);
+        if (s_part[j].row >= 0) mx = fmaxf(mx, at(j)[D]);
+      const float base = join_base(mx);
       for (int j = a; j <= b; ++j) {
         if (s_part[j].row < 0) continue;
-        const float *pj = at(j), f = exp2f(pj[D] - base);
-        l += f * pj[D + 1];
+        const float *pj = at(j), f = mkw::exp2_fast(pj[D] - base);
+        sum += f * pj[D + 1];
         x += f * pj[d];
       }
       if (whole) {
-        write_out<T>(p, pi.row, h0 + r, d, x, l, vsc);
-        if (d == 0) write_lse(p, pi.row, h0 + r, m, l);
+        write_out<T>(p, pi.row, h0 + r, d, x, sum, vsc);
+        if (d == 0) write_lse(p, pi.row, h0 + r, mx, sum);
       } else {
         slot[r * PST + d] = x;
         if (d == 0) {
-          slot[r * PST + D] = m;
-          slot[r * PST + D + 1] = l;
+          slot[r * PST + D] = mx;
+          slot[r * PST + D + 1] = sum;
         }
       }
     }
     if (pi.begins && !ends && tid == 0) {
-      // the last CTA with tiles of this row: the one that holds tile e - 1, e the row's end
+      // the last CTA with tiles of this row: the one whose range holds unit e - 1, e the row's end
       int before_row = s_scan[pi.row / per];
-      for (int r = pi.row / per * per; r < pi.row; ++r) before_row += span_of<POS>(p, p.lengths[r]).count;
-      const int count = span_of<POS>(p, p.lengths[pi.row]).count;
-      const int64_t e = static_cast<int64_t>(before_row) * p.vh + static_cast<int64_t>(pi.vh + 1) * count;
-      const int last = static_cast<int>((e * ctas + tiles - 1) / tiles) - 1;
+      for (int r = pi.row / per * per; r < pi.row; ++r) before_row += span_of<POS>(p, p.lengths[r]).cost();
+      const int cost = span_of<POS>(p, p.lengths[pi.row]).cost();
+      const int64_t e = static_cast<int64_t>(before_row) * p.vh + static_cast<int64_t>(pi.vh + 1) * cost;
+      const int last = static_cast<int>((e * ctas + units - 1) / units) - 1;
       p.records[cta] = make_int4(pi.row, pi.vh, last, 1);
     }
     a = b + 1;
@@ -803,7 +860,7 @@ __global__ void __launch_bounds__(kAttnThreads) join_kernel(const AttnParams p) 
     for (int j = 0; j < n; ++j) m = fmaxf(m, at(j)[D]);
     const float base = join_base(m);
     for (int j = 0; j < n; ++j) {
-      const float *pj = at(j), f = exp2f(pj[D] - base);
+      const float *pj = at(j), f = mkw::exp2_fast(pj[D] - base);
       l += f * pj[D + 1];
       x += f * pj[d];
     }
@@ -832,15 +889,15 @@ int sm_count(int *device) {
   return n;
 }
 
-template <class T, bool FP8, int D>
-int launch_attend(AttnParams &p, int grid, int dev, cudaStream_t s) {
+template <class T, bool FP8, int D, int HB>
+int launch_heads(AttnParams &p, int grid, int dev, cudaStream_t s) {
   using TL = Tile<D, FP8>;
   static std::atomic<uint64_t> ready{0};
   // three stages of the ring where a group's parts leave room for them (every group of up to 8 query heads)
   const int parts = kWarps * p.gr * kPartStride<D> * 4;
   p.stages = kWarps * 3 * TL::STAGE + parts <= kMaxSmem ? 3 : 2;
   const int smem = kWarps * p.stages * TL::STAGE + parts;
-  const void *fn = reinterpret_cast<const void *>(&attend_kernel<T, FP8, D>);
+  const void *fn = reinterpret_cast<const void *>(&attend_kernel<T, FP8, D, HB>);
   if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) {
       cudaGetLastError();
@@ -848,7 +905,7 @@ int launch_attend(AttnParams &p, int grid, int dev, cudaStream_t s) {
     }
     ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
   }
-  attend_kernel<T, FP8, D><<<grid, kAttnThreads, smem, s>>>(p);
+  attend_kernel<T, FP8, D, HB><<<grid, kAttnThreads, smem, s>>>(p);
   if (cudaPeekAtLastError() != cudaSuccess) {
     cudaGetLastError();
     return MK_ERR_CUDA;
@@ -867,6 +924,11 @@ int launch_attend(AttnParams &p, int grid, int dev, cudaStream_t s) {
     return MK_ERR_CUDA;
   }
   return MK_OK;
+}
+
+template <class T, bool FP8, int D>
+int launch_attend(AttnParams &p, int grid, int dev, cudaStream_t s) {
+  return p.gr <= 8 ? launch_heads<T, FP8, D, 1>(p, grid, dev, s) : launch_heads<T, FP8, D, 2>(p, grid, dev, s);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -988,9 +1050,9 @@ extern "C" int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args
       !aligned16(a->workspace) || !stride_ok(a->q_row, es) || !stride_ok(a->q_head, es) || !stride_ok(a->out_row, es) ||
       !stride_ok(a->out_head, es))
     return MK_ERR_INVALID_ARG;
-  // slots and the tiles of one kv head over all rows are counted in 32 bits
+  // slots and the cost of one kv head over all rows are counted in 32 bits
   const int64_t slots = static_cast<int64_t>(kv->table_cols) * kv->page_size;
-  if (slots > INT32_MAX - 64 || (slots + 15) / 16 * a->n > INT32_MAX || a->n_q_heads > (1 << 20)) return MK_ERR_UNSUPPORTED;
+  if (slots > INT32_MAX - 64 || ((slots + 15) / 16 + kRowCost) * a->n > INT32_MAX || a->n_q_heads > (1 << 20)) return MK_ERR_UNSUPPORTED;
   int dev = 0;
   const int grid = sm_count(&dev);
   if (grid < 0) return MK_ERR_CUDA;
