@@ -55,11 +55,6 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t *r, uint32_t addr) {
                : "memory");
 }
 
-// two matrices: lanes 0 .. 15 pass the addresses (the others' are ignored)
-__device__ __forceinline__ void ldmatrix2_trans(uint32_t *r, uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
-}
-
 // the transpose of an 8x8 matrix of 16-bit elements held a row a quad: lane 4 g + t has (g, 2t), (g, 2t + 1) before and
 // (2t, g), (2t + 1, g) after
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -125,10 +120,11 @@ __device__ __forceinline__ uint32_t take_weight_term(BF16Op, float &x, float &y)
 }
 __device__ __forceinline__ uint32_t take_weight_term(FP16Op op, float &x, float &y) { return take_term(op, x, y); }
 
-// two e4m3 values (low byte first) as two fp16 values: exact
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t pair) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(pair), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// four e4m3 values (lowest byte first) as two pairs of fp16 values: exact
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t x, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
@@ -138,5 +134,18 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
 // programmatic dependent launch: let the next kernel of the stream start; wait for the previous one's results
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// a cluster's CTAs: all their threads meet, shared memory written before is seen after
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// a float of the shared memory of the cluster's CTA `rank`, at the place of `p` in this one
+__device__ __forceinline__ float load_remote(const float *p, int rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
 
 }  // namespace mkw

@@ -7,6 +7,8 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <functional>
+#include <mutex>
 #include <type_traits>
 
 #include "mk_mma.cuh"
@@ -274,20 +276,44 @@ int run_append(const AppendParams &p, int dtype, int cache, int d, cudaStream_t 
 // matrix products truncate what they add to an accumulator, which over thousands
 // of tiles would show.
 //
-// Work: the tiles (POS slots of one row and kv head) of all rows, in order, are
-// cut into ranges of equal cost for the CTAs and these for their 8 warps,
-// whatever the lengths.  A warp streams its range through its own ring of shared
-// memory with asynchronous 16-byte copies and never waits for another warp until
-// the end.  What a warp has of a row at its range's ends is joined with its
-// neighbours' in shared memory, what a CTA has at its ends through the workspace
-// by join_kernel, always in order: the same lengths give the same bits.
+// Work: a warp has a range of tiles (POS slots of one row and kv head), streams
+// it through its own ring of shared memory with asynchronous 16-byte copies and
+// never waits for another warp until the end.  The ranges depend on the lengths,
+// which only the device knows, in one of three ways that the host chooses:
+//   - one row: a cluster of CTAs for each kv head, joined through their shared
+//     memory.
+//   - short rows (by the table's width): the tiles of all rows, in order, cut
+//     into ranges of equal cost for the CTAs, moved to where a row and head
+//     begins, and these for their warps; joined in shared memory.
+//   - else the same with the CTAs' ranges as they fall: what a CTA has of a row
+//     at its range's ends goes through the workspace to join_kernel.
+// Parts are joined in order: the same lengths give the same bits.
 // ---------------------------------------------------------------------------
 
 constexpr int kWarps = 8, kAttnThreads = 32 * kWarps;
 constexpr int kMinUnitsPerCta = 16;
 // what the start of a row and head costs (its queries' loads, its results' stores), in tiles
 constexpr int kRowCost = 2;
+// rows of up to so many tiles are not cut over CTAs
+constexpr int kShortTiles = 64;
 constexpr int kMaxSmem = 230400;       // dynamic; the static part is below 2 KB, a CTA's limit 227 KB
+
+// division of 0 <= n < 2^31 by a constant of the call
+struct Divisor {
+  uint32_t value, mul;
+  int shift;
+  __host__ void set(int d) {
+    value = d;
+    shift = 0;
+    while ((int64_t{1} << shift) < d) ++shift;
+    // n mul / 2^(31 + shift) with mul = 2^(31 + shift) / d rounded up: exact below 2^31
+    mul = d == 1 ? 0 : static_cast<uint32_t>(((uint64_t{1} << (31 + shift)) + d - 1) / d);
+    --shift;
+  }
+  __device__ __forceinline__ int quotient(int n) const { return value == 1 ? n : static_cast<int>(__umulhi(n, mul) >> shift); }
+};
+
+enum { kByCluster, kWhole, kJoined };  // how rows are dealt out: the three ways above
 
 struct AttnParams {
   const void *q, *k, *v;
@@ -299,10 +325,13 @@ struct AttnParams {
   int32_t *status;
   int4 *records;       // [grid] {row, virtual head, last CTA, 1} of a row that goes on in the next CTA
   float *parts;        // [grid][2][gr][D + 4]: a row's middle or end (0) and its beginning (1)
-  int n, hq, hkv, group, n_pages, page_size, table_cols, window;
+  Divisor page_size;
+  int n, hq, hkv, group, n_pages, capacity, window;   // capacity: slots of a table row
   int blocks, vh;      // head blocks of 16 query heads a kv head, virtual heads hkv * blocks
   int gr;              // query heads of a block: min(group, 16)
   int stages;
+  int way, cluster;
+  int dense;           // a page's slots of a head lie one behind the other
   float scale;
 };
 
@@ -311,10 +340,12 @@ struct Tile {
   static constexpr int ES = FP8 ? 1 : 2, ROWB = D * ES, CPR = ROWB / 16;
   static constexpr int POS = (D == 128 && !FP8) ? 16 : 32;
   static constexpr int KBYTES = POS * ROWB, STAGE = 2 * KBYTES;
-  // 16-byte chunk `c` of row r: permuted so that the same chunk of 8 rows meets 8 different banks
-  static __device__ __forceinline__ int at(int r, int c) {
-    return r * ROWB + ((ROWB >= 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
-  }
+  // 16-byte chunk c of row r is in place c ^ turn(r), so that the same chunk of 8 rows meets 8 different banks
+  static __host__ __device__ constexpr int turn(int r) { return ROWB >= 128 ? r & 7 : (r >> 1) & 3; }
+  static __device__ __forceinline__ int at(int r, int c) { return r * ROWB + ((c ^ turn(r)) << 4); }
+  // copies of a tile: lane l fills place l % CPR of row i ROWS + l / CPR, i < COPIES; turn() of these rows, apart from
+  // the lane's part, takes TURNS values
+  static constexpr int ROWS = 32 / CPR, COPIES = POS / ROWS, TURNS = ROWB == 256 ? 4 : ROWB == 128 ? 2 : 1;
 };
 
 __device__ __forceinline__ float2 load_pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
@@ -333,17 +364,26 @@ struct Span {
 template <int POS>
 __device__ __forceinline__ Span span_of(const AttnParams &p, int len) {
   Span s;
-  const bool fits = len <= static_cast<int64_t>(p.table_cols) * p.page_size;
-  s.hi = len > 0 && fits ? len : 0;
+  s.hi = len > 0 && len <= p.capacity ? len : 0;
   s.lo = p.window > 0 && s.hi > p.window ? s.hi - p.window : 0;
   s.first = s.lo / POS;
   s.count = s.hi > 0 ? (s.hi + POS - 1) / POS - s.first : 0;
   return s;
 }
 
+// the ith of `parts` shares of `total`, as equal as whole numbers are: its beginning, and the share that has unit u
+__device__ __forceinline__ int share_begin(int total, int parts, int i) {
+  const int q = total / parts, r = total - q * parts;
+  return i * q + min(i, r);
+}
+__device__ __forceinline__ int share_of(int total, int parts, int u) {
+  const int q = total / parts, r = total - q * parts, big = r * (q + 1);
+  return u < big ? u / (q + 1) : r + (u - big) / q;
+}
+
 // what the ring's reader needs to know of a tile
 struct TileInfo {
-  int row, vh, pos, lo, hi, flags;
+  int pos, lo, hi, flags, row, vh;
 };
 // the row's first tile, its last, a page outside the cache, the last tile of the warp
 constexpr int kFirst = 1, kLast = 2, kBad = 4, kEnd = 8;
@@ -368,6 +408,8 @@ __device__ __forceinline__ void write_lse(const AttnParams &p, int row, int head
   if (p.lse) p.lse[static_cast<int64_t>(row) * p.hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
+__device__ __forceinline__ int kvh_of(const AttnParams &p, int vh) { return vh / p.blocks; }
+
 // over the 8 rows of a column of a product: lanes with the same t
 __device__ __forceinline__ float column_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
@@ -382,7 +424,7 @@ __device__ __forceinline__ float column_sum(float x) {
 
 // HB: blocks of 8 query heads
 template <class T, bool FP8, int D, int HB>
-__global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_constant__ AttnParams p) {
   using TL = Tile<D, FP8>;
   using Op = std::conditional_t<FP8, mkw::FP16Op, mkw::BF16Op>;
   constexpr bool F32 = std::is_same<T, float>::value;
@@ -395,130 +437,162 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParam
   __shared__ int s_scan[kAttnThreads], s_warp[kWarps];
 
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  mkw::launch_dependents();
-
-  // ---- cost of the rows before every group of rows ---------------------------
-  const int per = (p.n + kAttnThreads - 1) / kAttnThreads;   // rows a thread counts
-  int mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int r = tid * per + i;
-    if (r < p.n) mine += span_of<POS>(p, p.lengths[r]).cost();
-  }
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) s_warp[w] = incl;
-  if (tid < 2 * kWarps) s_part[tid].row = -1;
-  __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < w) before += s_warp[i];
-    total += s_warp[i];
-  }
-  s_scan[tid] = before + incl - mine;                        // cost of the rows before this thread's
-  __syncthreads();
-
-  // Units: a row and head of cost c covers c of them, tile j the (kRowCost + j)th.  A warp has the tiles whose unit is
-  // in its range.
-  const int64_t units = static_cast<int64_t>(total) * p.vh;
-  const int64_t wanted = (units + kMinUnitsPerCta - 1) / kMinUnitsPerCta;
-  const int ctas = static_cast<int>(wanted < 1 ? 1 : wanted < gridDim.x ? wanted : gridDim.x);
   const int cta = blockIdx.x;
-  const int64_t c_begin = cta < ctas ? units * cta / ctas : 0, c_end = cta < ctas ? units * (cta + 1) / ctas : 0;
-  const int64_t begin = c_begin + (c_end - c_begin) * w / kWarps, end = c_begin + (c_end - c_begin) * (w + 1) / kWarps;
-  int left = static_cast<int>(end - begin);                  // units from the tile the producer stands at to the range's end
+  if (p.way == kJoined) mkw::launch_dependents();
+  if (tid < 2 * kWarps) s_part[tid].row = -1;
 
-  // ---- where this warp's range starts ---------------------------------------
-  int row = 0, vh = 0, tile = 0;
+  // ---- the warp's range: where it starts, and how much it covers -------------------
+  int row = 0, vh = 0, tile = 0, left = 0;                   // left: units from the tile the producer stands at to the range's end
   Span sp{0, 0, 0, 0};
-  if (left > 0) {
-    const int x = static_cast<int>(begin / p.vh);            // in [before(row), before(row) + cost(row))
-    int a = 0, b = kAttnThreads;
-    while (b - a > 1) {
-      const int m = (a + b) >> 1;
-      if (s_scan[m] <= x) a = m; else b = m;
+  int per = 0, units = 0, ctas = 0;
+  if (p.way == kByCluster) {
+    vh = cta / p.cluster;                                    // the cluster's kv head (and head block)
+    sp = span_of<POS>(p, p.lengths[0]);
+    const int i = cta % p.cluster * kWarps + w;
+    tile = share_begin(sp.count, p.cluster * kWarps, i);
+    left = share_begin(sp.count, p.cluster * kWarps, i + 1) - tile;
+    __syncthreads();
+  } else {
+    // Units: a row and head of cost c covers c of them, tile j the (kRowCost + j)th.  A warp has the tiles whose unit
+    // is in its range.  First the cost of the rows before every group of rows.
+    per = (p.n + kAttnThreads - 1) / kAttnThreads;           // rows a thread counts
+    int mine = 0;
+    for (int i = 0; i < per; ++i) {
+      const int r = tid * per + i;
+      if (r < p.n) mine += span_of<POS>(p, p.lengths[r]).cost();
     }
-    int at = s_scan[a];
-    row = a * per;
-    sp = span_of<POS>(p, p.lengths[row]);
-    while (at + sp.cost() <= x) {
-      at += sp.cost();
-      sp = span_of<POS>(p, p.lengths[++row]);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
     }
-    const int64_t rest = begin - static_cast<int64_t>(at) * p.vh;
-    vh = static_cast<int>(rest / sp.cost());
-    tile = static_cast<int>(rest - static_cast<int64_t>(vh) * sp.cost()) - kRowCost;
-    if (tile < 0) left += tile, tile = 0;                    // from the row's start on: its cost comes first
+    if (lane == 31) s_warp[w] = incl;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < w) before += s_warp[i];
+      total += s_warp[i];
+    }
+    s_scan[tid] = before + incl - mine;                      // cost of the rows before this thread's
+    __syncthreads();
+    units = total * p.vh;
+    ctas = max(1, min(static_cast<int>(gridDim.x), (units - 1) / kMinUnitsPerCta + 1));
+
+    // the row and head that has unit u, and where in it u is
+    auto find = [&](int u, int &f_row, int &f_vh, Span &f_sp) {
+      const int x = u / p.vh;                                // in [before(row), before(row) + cost(row))
+      int a = 0, b = kAttnThreads;
+      while (b - a > 1) {
+        const int m = (a + b) >> 1;
+        if (s_scan[m] <= x) a = m; else b = m;
+      }
+      int at = s_scan[a];
+      f_row = a * per;
+      f_sp = span_of<POS>(p, p.lengths[f_row]);
+      while (at + f_sp.cost() <= x) {
+        at += f_sp.cost();
+        f_sp = span_of<POS>(p, p.lengths[++f_row]);
+      }
+      const int rest = u - at * p.vh;
+      f_vh = rest / f_sp.cost();
+      return rest - f_vh * f_sp.cost();
+    };
+    int c_begin = 0, c_end = 0;
+    if (cta < ctas) {
+      c_begin = share_begin(units, ctas, cta);
+      c_end = share_begin(units, ctas, cta + 1);
+      if (p.way == kWhole) {
+        // to the next row and head's beginning
+        int r, h;
+        Span s;
+        if (c_begin > 0) {
+          const int in = find(c_begin, r, h, s);
+          if (in > 0) c_begin += s.cost() - in;
+        }
+        if (c_end < units) {
+          const int in = find(c_end, r, h, s);
+          if (in > 0) c_end += s.cost() - in;
+        }
+      }
+    }
+    const int begin = c_begin + share_begin(c_end - c_begin, kWarps, w);
+    left = c_begin + share_begin(c_end - c_begin, kWarps, w + 1) - begin;
+    if (left > 0) {
+      tile = find(begin, row, vh, sp) - kRowCost;
+      if (tile < 0) left += tile, tile = 0;                  // from the row's start on: its cost comes first
+    }
   }
 
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + w * p.stages * TL::STAGE;
-  const unsigned char *k_base = static_cast<const unsigned char *>(p.k), *v_base = static_cast<const unsigned char *>(p.v);
+  const unsigned char *k_base = static_cast<const unsigned char *>(p.k);
+  const int64_t to_v = static_cast<const unsigned char *>(p.v) - k_base;
 
-  // page of this lane's slot in the tile the producer stands at
-  auto page_of = [&](int pos) {
-    int page = -1;
-    if (lane < POS && pos >= sp.lo && pos < sp.hi) page = p.table[row * p.table_stride + pos / p.page_size];
-    return page;
+  // the producer's place besides row, vh, tile: its kv head and block, this lane's slot in its page and that page
+  int kvh = vh / p.blocks, blk = vh - kvh * p.blocks, slot = 0, page = -1;
+  auto look_up = [&]() {
+    const int pos = (sp.first + tile) * POS + lane, col = p.page_size.quotient(pos);
+    slot = pos - col * static_cast<int>(p.page_size.value);
+    page = -1;
+    if (lane < POS && pos >= sp.lo && pos < sp.hi) page = p.table[row * p.table_stride + col];
   };
-  int next_page = left > 0 ? page_of((sp.first + tile) * POS + lane) : -1;
+  if (left > 0) look_up();
   int in_stage = 0;                                          // the producer's stage
-  const int r0 = lane / TL::CPR, c0 = lane % TL::CPR;        // this lane's first slot of a tile and its chunk
-  const int64_t lane_off = r0 * p.slot_stride * TL::ES + c0 * 16, row_step = 32 / TL::CPR * p.slot_stride * TL::ES;
+  const int r0 = lane / TL::CPR, place = lane % TL::CPR;     // this lane's first slot of a tile and its place in every row
   auto produce = [&]() {
     const int pos0 = (sp.first + tile) * POS, pos = pos0 + lane;
     const bool want = lane < POS && pos >= sp.lo && pos < sp.hi;
-    const bool fine = want && next_page >= 0 && next_page < p.n_pages;
-    const int slot = pos % p.page_size;
-    const unsigned have = __ballot_sync(0xffffffffu, fine);
+    const bool fine = static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages);
+    const unsigned have = __ballot_sync(0xffffffffu, want && fine);
     const bool bad = __any_sync(0xffffffffu, want && !fine);
-    const uint32_t ks = ring + in_stage * TL::STAGE;
     int64_t off = 0;
-    if (fine) off = (next_page * p.page_stride + (vh / p.blocks) * p.head_stride + slot * p.slot_stride) * TL::ES;
-    if (have == (POS == 32 ? 0xffffffffu : 0xffffu) && __shfl_sync(0xffffffffu, slot, 0) + POS <= p.page_size) {
-      // a whole tile inside a page: its slots are one stride apart
-      const int64_t o = __shfl_sync(0xffffffffu, off, 0) + lane_off;
-      const unsigned char *ka = k_base + o, *va = v_base + o;
+    if (want && fine) off = (page * p.page_stride + kvh * p.head_stride + slot * p.slot_stride) * TL::ES;
+    const uint32_t ks = ring + in_stage * TL::STAGE + r0 * TL::ROWB + place * 16;
+    if (p.dense && have == (POS == 32 ? 0xffffffffu : 0xffffu) &&
+        __shfl_sync(0xffffffffu, slot, 0) + POS <= static_cast<int>(p.page_size.value)) {
+      // a whole tile inside a page: its bytes follow one another
+      const unsigned char *from = k_base + __shfl_sync(0xffffffffu, off, 0) + r0 * TL::ROWB;
 #pragma unroll
-      for (int i = 0; i < POS * TL::CPR / 32; ++i) {
-        const int r = i * (32 / TL::CPR) + r0;
-        mkw::cp_async16(ks + TL::at(r, c0), ka);
-        mkw::cp_async16(ks + TL::KBYTES + TL::at(r, c0), va);
-        ka += row_step;
-        va += row_step;
+      for (int v = 0; v < TL::TURNS; ++v) {
+        const unsigned char *ka = from + ((place ^ TL::turn(r0) ^ TL::turn(v * TL::ROWS)) << 4), *va = ka + to_v;
+#pragma unroll
+        for (int i = v; i < TL::COPIES; i += TL::TURNS) {
+          mkw::cp_async16(ks + i * TL::ROWS * TL::ROWB, ka + i * TL::ROWS * TL::ROWB);
+          mkw::cp_async16(ks + TL::KBYTES + i * TL::ROWS * TL::ROWB, va + i * TL::ROWS * TL::ROWB);
+        }
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < POS * TL::CPR / 32; ++i) {
-        const int r = i * (32 / TL::CPR) + r0;
-        const int64_t o = __shfl_sync(0xffffffffu, off, r) + c0 * 16;
+#pragma unroll 2
+      for (int i = 0; i < TL::COPIES; ++i) {
+        const int r = i * TL::ROWS + r0;
+        const int64_t o = __shfl_sync(0xffffffffu, off, r) + ((place ^ TL::turn(r)) << 4);
         const bool ok = (have >> r) & 1;
-        mkw::cp_async16(ks + TL::at(r, c0), k_base + (ok ? o : 0), ok);
-        mkw::cp_async16(ks + TL::KBYTES + TL::at(r, c0), v_base + (ok ? o : 0), ok);
+        const unsigned char *ka = k_base + (ok ? o : 0);
+        mkw::cp_async16(ks + i * TL::ROWS * TL::ROWB, ka, ok);
+        mkw::cp_async16(ks + TL::KBYTES + i * TL::ROWS * TL::ROWB, ka + to_v, ok);
       }
     }
-    int flags = (tile == 0 ? kFirst : 0) | (bad ? kBad : 0);
-    const int at_row = row, at_vh = vh, lo = sp.lo, hi = sp.hi;
+    TileInfo ti{pos0, sp.lo, sp.hi, (tile == 0 ? kFirst : 0) | (bad ? kBad : 0), row, vh};
     --left;
     if (++tile == sp.count) {
-      flags |= kLast;
+      ti.flags |= kLast;
       left -= kRowCost;
       tile = 0;
-      if (++vh == p.vh) {
-        vh = 0;
+      ++vh;
+      if (++blk == p.blocks) blk = 0, ++kvh;
+      if (vh == p.vh) {
+        vh = kvh = 0;
         if (left > 0) {
           do sp = span_of<POS>(p, p.lengths[++row]);
           while (sp.count == 0);
         }
       }
     }
-    if (left > 0) next_page = page_of((sp.first + tile) * POS + lane);
-    else flags |= kEnd;
+    if (left > 0) look_up();
+    else ti.flags |= kEnd;
     if (lane == 0) {
-      s_tile[w][in_stage] = TileInfo{at_row, at_vh, pos0, lo, hi, flags};
+      s_tile[w][in_stage] = ti;
       if (bad) report(p.status, MK_ERR_BAD_PAGE);
     }
     if (++in_stage == p.stages) in_stage = 0;
@@ -562,11 +636,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParam
 
     if (start) {                                             // a row's query heads
       start = false;
-      const int kvh = ti.vh / p.blocks, blk = ti.vh % p.blocks;
-      head0 = kvh * p.group + blk * 16;
-      rows = min(8 * HB, p.group - blk * 16);
+      const int q_kvh = kvh_of(p, ti.vh), q_blk = ti.vh - q_kvh * p.blocks;
+      head0 = q_kvh * p.group + q_blk * 16;
+      rows = min(8 * HB, p.group - q_blk * 16);
       begins = ti.flags & kFirst;
-      const float to_log2 = p.scale * 1.4426950408889634f * (FP8 && p.k_scale ? p.k_scale[kvh] : 1.f);
+      const float to_log2 = p.scale * 1.4426950408889634f * (FP8 && p.k_scale ? p.k_scale[q_kvh] : 1.f);
 #pragma unroll
       for (int hb = 0; hb < HB; ++hb) {
         const int h = 8 * hb + g;
@@ -632,8 +706,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParam
           mkw::ldmatrix4(f, kt + TL::at(r, s + (lane >> 4)));
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            a[j][0] = mkw::e4m3x2_to_half2(f[2 * j] & 0xffffu), a[j][2] = mkw::e4m3x2_to_half2(f[2 * j] >> 16);
-            a[j][1] = mkw::e4m3x2_to_half2(f[2 * j + 1] & 0xffffu), a[j][3] = mkw::e4m3x2_to_half2(f[2 * j + 1] >> 16);
+            mkw::e4m3x4_to_half2(f[2 * j], a[j][0], a[j][2]);
+            mkw::e4m3x4_to_half2(f[2 * j + 1], a[j][1], a[j][3]);
           }
         }
 #pragma unroll
@@ -704,36 +778,38 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParam
 
     // ---- values: block c of 16 elements by heads 2t, 2t + 1; rows g and g + 8 of a block are its elements of that
     // number (bf16) or elements 2g and 2g + 1 (e4m3, whose 16-bit pairs the transposition keeps together) ----------
+    constexpr int CB = FP8 ? 2 : 1;                          // blocks a matrix load brings
 #pragma unroll
-    for (int c = 0; c < DB; ++c) {
-      float e[HB][4];
+    for (int c = 0; c < DB; c += CB) {
+      float e[CB][HB][4];
 #pragma unroll
       for (int nb = 0; nb < PN; ++nb) {
-        uint32_t a[4];
+        uint32_t a[CB][4];
         if constexpr (!FP8) {
-          mkw::ldmatrix4_trans(a, vt + TL::at(nb * 16 + ((lane >> 4) << 3) + (lane & 7), 2 * c + ((lane >> 3) & 1)));
+          mkw::ldmatrix4_trans(a[0], vt + TL::at(nb * 16 + ((lane >> 4) << 3) + (lane & 7), 2 * c + ((lane >> 3) & 1)));
         } else {
-          uint32_t f[2];
-          mkw::ldmatrix2_trans(f, vt + TL::at(nb * 16 + (lane & 15), c));
+          uint32_t f[4];
+          mkw::ldmatrix4_trans(f, vt + TL::at(nb * 16 + (lane & 15), c + (lane >> 4)));
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t lo = mkw::e4m3x2_to_half2(f[j] & 0xffffu), hi = mkw::e4m3x2_to_half2(f[j] >> 16);
-            a[2 * j] = __byte_perm(lo, hi, 0x5410);
-            a[2 * j + 1] = __byte_perm(lo, hi, 0x7632);
-          }
+          for (int j = 0; j < 4; ++j)                        // bytes (slot, element) 00 01 10 11 to 00 10 01 11
+            mkw::e4m3x4_to_half2(__byte_perm(f[j], 0, 0x3120), a[j >> 1][2 * (j & 1)], a[j >> 1][2 * (j & 1) + 1]);
         }
+#pragma unroll
+        for (int k = 0; k < CB; ++k)
+#pragma unroll
+          for (int hb = 0; hb < HB; ++hb)
+#pragma unroll
+            for (int u = TP - 1; u >= 0; --u) {
+              if (nb == 0 && u == TP - 1) mkw::mma_zero(Op{}, e[k][hb], a[k], pf[u][nb][hb][0], pf[u][nb][hb][1]);
+              else mkw::mma(Op{}, e[k][hb], a[k], pf[u][nb][hb][0], pf[u][nb][hb][1]);
+            }
+      }
+#pragma unroll
+      for (int k = 0; k < CB; ++k)
 #pragma unroll
         for (int hb = 0; hb < HB; ++hb)
 #pragma unroll
-          for (int u = TP - 1; u >= 0; --u) {
-            if (nb == 0 && u == TP - 1) mkw::mma_zero(Op{}, e[hb], a, pf[u][nb][hb][0], pf[u][nb][hb][1]);
-            else mkw::mma(Op{}, e[hb], a, pf[u][nb][hb][0], pf[u][nb][hb][1]);
-          }
-      }
-#pragma unroll
-      for (int hb = 0; hb < HB; ++hb)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[c][hb][k] = o[c][hb][k] * alpha[hb][k & 1] + e[hb][k];
+          for (int j = 0; j < 4; ++j) o[c + k][hb][j] = o[c + k][hb][j] * alpha[hb][j & 1] + e[k][hb][j];
     }
     if (ti.flags & kBad) {
 #pragma unroll
@@ -744,9 +820,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParam
     const bool ends = ti.flags & kLast;
     if (ends || !more) {
       start = true;
-      const bool whole = begins && ends;
+      // (a cluster's parts are joined at the end, whole rows among them)
+      const bool whole = begins && ends && p.way != kByCluster;
       float *part = ends ? first_part : last_part;
-      const float vsc = FP8 && p.v_scale ? p.v_scale[ti.vh / p.blocks] : 1.f;
+      const float vsc = FP8 && p.v_scale ? p.v_scale[kvh_of(p, ti.vh)] : 1.f;
 #pragma unroll
       for (int hb = 0; hb < HB; ++hb)
 #pragma unroll
@@ -778,10 +855,63 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParam
     }
   }
   mkw::cp_async_wait<0>();
-  if (tid == 0) p.records[cta] = make_int4(0, 0, 0, 0);
+  if (p.way == kJoined && tid == 0) p.records[cta] = make_int4(0, 0, 0, 0);
   __syncthreads();
 
   // ---- join the warps' parts, in order ---------------------------------------
+  // where the jth part is: the ring of its warp (a part that does not end its row), or the space beside the rings
+  auto part_at = [&](int j) {
+    return reinterpret_cast<float *>((j & 1) ? smem + (j >> 1) * p.stages * TL::STAGE
+                                             : smem + kWarps * p.stages * TL::STAGE + (j >> 1) * p.gr * PST * 4);
+  };
+  if (p.way == kByCluster) {
+    // all parts are of one row and head; an empty part weighs nothing
+    if (!sp.count) return;                                   // (every CTA of the cluster alike)
+    const int head0 = kvh_of(p, cta / p.cluster) * p.group + cta / p.cluster % p.blocks * 16;
+    const int nr = min(16, p.group - cta / p.cluster % p.blocks * 16);
+    const float vsc = FP8 && p.v_scale ? p.v_scale[kvh_of(p, cta / p.cluster)] : 1.f;
+    float *mine = reinterpret_cast<float *>(smem + kWarps * (p.stages * TL::STAGE + p.gr * PST * 4));   // [gr][PST]
+    for (int i = tid; i < nr * D; i += kAttnThreads) {
+      const int r = i / D, d = i % D;
+      float mx = -INFINITY, sum = 0.f, x = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2 * kWarps; ++j)
+        if (s_part[j].row >= 0) mx = fmaxf(mx, part_at(j)[r * PST + D]);
+      const float base = join_base(mx);
+#pragma unroll
+      for (int j = 0; j < 2 * kWarps; ++j)
+        if (s_part[j].row >= 0) {
+          const float *pj = part_at(j) + r * PST, f = mkw::exp2_fast(pj[D] - base);
+          sum += f * pj[D + 1];
+          x += f * pj[d];
+        }
+      mine[r * PST + d] = x;
+      if (d == 0) {
+        mine[r * PST + D] = mx;
+        mine[r * PST + D + 1] = sum;
+      }
+    }
+    mkw::cluster_meet();
+    for (int i = cta % p.cluster * kAttnThreads + tid; i < nr * D; i += p.cluster * kAttnThreads) {
+      const int r = i / D, d = i % D;
+      float mx = -INFINITY, sum = 0.f, x = 0.f, m_j[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (j < p.cluster) mx = fmaxf(mx, m_j[j] = mkw::load_remote(mine + r * PST + D, j));
+      const float base = join_base(mx);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (j < p.cluster) {
+          const float f = mkw::exp2_fast(m_j[j] - base);
+          sum += f * mkw::load_remote(mine + r * PST + D + 1, j);
+          x += f * mkw::load_remote(mine + r * PST + d, j);
+        }
+      write_out<T>(p, 0, head0 + r, d, x, sum, vsc);
+      if (d == 0) write_lse(p, 0, head0 + r, mx, sum);
+    }
+    mkw::cluster_meet();                                     // the others' shared memory is read until here
+    return;
+  }
   for (int a = 0; a < 2 * kWarps;) {
     const PartInfo pi = s_part[a];
     if (pi.row < 0) {
@@ -796,45 +926,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParam
       b = j;
       ends = pj.ends;
     }
-    const int kvh = pi.vh / p.blocks, blk = pi.vh % p.blocks, h0 = kvh * p.group + blk * 16, nr = min(16, p.group - blk * 16);
+    const int head0 = kvh_of(p, pi.vh) * p.group + pi.vh % p.blocks * 16, nr = min(16, p.group - pi.vh % p.blocks * 16);
     const bool whole = pi.begins && ends;
-    const float vsc = FP8 && p.v_scale ? p.v_scale[kvh] : 1.f;
-    float *slot = p.parts + (static_cast<int64_t>(cta) * 2 + (pi.begins ? 1 : 0)) * p.gr * PST;
+    const float vsc = FP8 && p.v_scale ? p.v_scale[kvh_of(p, pi.vh)] : 1.f;
+    float *slot_at = p.parts + (static_cast<int64_t>(cta) * 2 + (pi.begins ? 1 : 0)) * p.gr * PST;
     for (int i = tid; i < nr * D; i += kAttnThreads) {
       const int r = i / D, d = i % D;
       float mx = -INFINITY, sum = 0.f, x = 0.f;
-      auto at = [&](int j) {
-        const unsigned char *base = (j & 1) ? smem + (j >> 1) * p.stages * TL::STAGE
-                                            : smem + kWarps * p.stages * TL::STAGE + (j >> 1) * p.gr * PST * 4;
-        return reinterpret_cast<const float *>(base) + r * PST;
-      };
       for (int j = a; j <= b; ++j)
-        if (s_part[j].row >= 0) mx = fmaxf(mx, at(j)[D]);
+        if (s_part[j].row >= 0) mx = fmaxf(mx, part_at(j)[r * PST + D]);
       const float base = join_base(mx);
       for (int j = a; j <= b; ++j) {
         if (s_part[j].row < 0) continue;
-        const float *pj = at(j), f = mkw::exp2_fast(pj[D] - base);
+        const float *pj = part_at(j) + r * PST, f = mkw::exp2_fast(pj[D] - base);
         sum += f * pj[D + 1];
         x += f * pj[d];
       }
       if (whole) {
-        write_out<T>(p, pi.row, h0 + r, d, x, sum, vsc);
-        if (d == 0) write_lse(p, pi.row, h0 + r, mx, sum);
+        write_out<T>(p, pi.row, head0 + r, d, x, sum, vsc);
+        if (d == 0) write_lse(p, pi.row, head0 + r, mx, sum);
       } else {
-        slot[r * PST + d] = x;
+        slot_at[r * PST + d] = x;
         if (d == 0) {
-          slot[r * PST + D] = mx;
-          slot[r * PST + D + 1] = sum;
+          slot_at[r * PST + D] = mx;
+          slot_at[r * PST + D + 1] = sum;
         }
       }
     }
     if (pi.begins && !ends && tid == 0) {
-      // the last CTA with tiles of this row: the one whose range holds unit e - 1, e the row's end
+      // the last CTA with tiles of this row: the one whose range holds the row's last unit
       int before_row = s_scan[pi.row / per];
       for (int r = pi.row / per * per; r < pi.row; ++r) before_row += span_of<POS>(p, p.lengths[r]).cost();
       const int cost = span_of<POS>(p, p.lengths[pi.row]).cost();
-      const int64_t e = static_cast<int64_t>(before_row) * p.vh + static_cast<int64_t>(pi.vh + 1) * cost;
-      const int last = static_cast<int>((e * ctas + units - 1) / units) - 1;
+      const int last = share_of(units, ctas, before_row * p.vh + (pi.vh + 1) * cost - 1);
       p.records[cta] = make_int4(pi.row, pi.vh, last, 1);
     }
     a = b + 1;
@@ -842,30 +966,60 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const AttnParam
 }
 
 // Joins the rows that more than one CTA had a share of: CTA c takes the row that
-// begins in attend_kernel's CTA c and goes on in the next ones.
+// begins in attend_kernel's CTA c and goes on in the next ones.  Four elements a
+// thread; threads left over share the parts.
 template <class T, int D>
-__global__ void __launch_bounds__(kAttnThreads) join_kernel(const AttnParams p) {
-  constexpr int PST = kPartStride<D>;
+__global__ void __launch_bounds__(kAttnThreads) join_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int PST = kPartStride<D>, Q = D / 4;
+  __shared__ float s_m[kAttnThreads], s_l[kAttnThreads];
+  __shared__ float4 s_x[kAttnThreads];
   mkw::wait_previous_kernel();
   const int cta = blockIdx.x;
   const int4 rec = p.records[cta];
   if (!rec.w) return;
-  const int kvh = rec.y / p.blocks, blk = rec.y % p.blocks, h0 = kvh * p.group + blk * 16, nr = min(16, p.group - blk * 16);
-  const float vsc = p.v_scale ? p.v_scale[kvh] : 1.f;
-  const int n = rec.z - cta + 1;
-  for (int i = threadIdx.x; i < nr * D; i += kAttnThreads) {
-    const int r = i / D, d = i % D;
-    auto at = [&](int j) { return p.parts + (static_cast<int64_t>(cta + j) * 2 + (j == 0 ? 1 : 0)) * p.gr * PST + r * PST; };
-    float m = -INFINITY, l = 0.f, x = 0.f;
-    for (int j = 0; j < n; ++j) m = fmaxf(m, at(j)[D]);
-    const float base = join_base(m);
-    for (int j = 0; j < n; ++j) {
-      const float *pj = at(j), f = mkw::exp2_fast(pj[D] - base);
-      l += f * pj[D + 1];
-      x += f * pj[d];
+  const int head0 = kvh_of(p, rec.y) * p.group + rec.y % p.blocks * 16, nr = min(16, p.group - rec.y % p.blocks * 16);
+  const float vsc = p.v_scale ? p.v_scale[kvh_of(p, rec.y)] : 1.f;
+  const int n = rec.z - cta + 1, rows = kAttnThreads / Q;    // query heads at a time
+  const int shares = max(1, rows / nr), share = threadIdx.x / Q / nr;
+  const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int r0 = 0; r0 < nr; r0 += rows) {
+    const int r = r0 + threadIdx.x / Q % nr, q = threadIdx.x % Q;
+    const bool live = share < shares && r < nr;
+    float m = -INFINITY, l = 0.f;
+    float4 x = none;
+    if (live) {
+#pragma unroll 4
+      for (int j = share; j < n; j += shares) {
+        const float *part = p.parts + (static_cast<int64_t>(cta + j) * 2 + (j == 0 ? 1 : 0)) * p.gr * PST + r * PST;
+        const float4 v = *reinterpret_cast<const float4 *>(part + 4 * q);
+        const float mj = part[D], lj = part[D + 1], mx = fmaxf(m, mj), base = join_base(mx);
+        const float f = mkw::exp2_fast(m - base), fj = mkw::exp2_fast(mj - base);
+        m = mx;
+        l = l * f + lj * fj;
+        x = make_float4(x.x * f + v.x * fj, x.y * f + v.y * fj, x.z * f + v.z * fj, x.w * f + v.w * fj);
+      }
     }
-    write_out<T>(p, rec.x, h0 + r, d, x, l, vsc);
-    if (d == 0) write_lse(p, rec.x, h0 + r, m, l);
+    s_m[threadIdx.x] = m;
+    s_l[threadIdx.x] = l;
+    s_x[threadIdx.x] = x;
+    __syncthreads();
+    if (live && share == 0) {
+      for (int s = 1; s < shares; ++s) {
+        const int o = threadIdx.x + s * nr * Q;
+        const float mj = s_m[o], mx = fmaxf(m, mj), base = join_base(mx);
+        const float f = mkw::exp2_fast(m - base), fj = mkw::exp2_fast(mj - base);
+        const float4 v = s_x[o];
+        m = mx;
+        l = l * f + s_l[o] * fj;
+        x = make_float4(x.x * f + v.x * fj, x.y * f + v.y * fj, x.z * f + v.z * fj, x.w * f + v.w * fj);
+      }
+      write_out<T>(p, rec.x, head0 + r, 4 * q, x.x, l, vsc);
+      write_out<T>(p, rec.x, head0 + r, 4 * q + 1, x.y, l, vsc);
+      write_out<T>(p, rec.x, head0 + r, 4 * q + 2, x.z, l, vsc);
+      write_out<T>(p, rec.x, head0 + r, 4 * q + 3, x.w, l, vsc);
+      if (q == 0) write_lse(p, rec.x, head0 + r, m, l);
+    }
+    __syncthreads();
   }
 }
 
@@ -889,35 +1043,73 @@ int sm_count(int *device) {
   return n;
 }
 
+// How a kernel can be launched on a device, looked up at its first launch there: clusters[i] clusters of 2^(i + 1) CTAs
+// fit on it at once.
+struct Ready {
+  std::once_flag once;
+  bool ok = false;
+  int clusters[4] = {};
+};
+
+void make_ready(Ready &r, const void *fn) {
+  r.ok = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) == cudaSuccess &&
+         cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+  for (int i = 0; i < 4 && r.ok; ++i) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2 << i;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2 << i);
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = kMaxSmem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&r.clusters[i], fn, &cfg) != cudaSuccess) r.clusters[i] = 0;
+  }
+  cudaGetLastError();
+}
+
 template <class T, bool FP8, int D, int HB>
 int launch_heads(AttnParams &p, int grid, int dev, cudaStream_t s) {
   using TL = Tile<D, FP8>;
-  static std::atomic<uint64_t> ready{0};
-  // three stages of the ring where a group's parts leave room for them (every group of up to 8 query heads)
-  const int parts = kWarps * p.gr * kPartStride<D> * 4;
-  p.stages = kWarps * 3 * TL::STAGE + parts <= kMaxSmem ? 3 : 2;
-  const int smem = kWarps * p.stages * TL::STAGE + parts;
-  const void *fn = reinterpret_cast<const void *>(&attend_kernel<T, FP8, D, HB>);
-  if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) {
-      cudaGetLastError();
-      return MK_ERR_CUDA;
-    }
-    ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
+  static Ready ready[kMaxDevices];
+  const auto fn = &attend_kernel<T, FP8, D, HB>;
+  Ready &r = ready[dev];
+  std::call_once(r.once, make_ready, std::ref(r), reinterpret_cast<const void *>(fn));
+  if (!r.ok) return MK_ERR_CUDA;
+  const int64_t tiles = (p.window > 0 ? std::min(p.window, p.capacity) : p.capacity) / TL::POS + 2;   // of a row at most
+  p.way = tiles <= kShortTiles ? kWhole : kJoined;
+  p.cluster = 1;
+  if (p.n == 1) {
+    // the largest clusters of which there is one for each head at once, as long as their warps have a tile each
+    for (int i = 0; i < 4 && p.vh <= r.clusters[i] && (i == 0 || tiles > p.cluster * kWarps); ++i) p.cluster = 2 << i;
+    if (p.cluster > 1) p.way = kByCluster;
   }
-  attend_kernel<T, FP8, D, HB><<<grid, kAttnThreads, smem, s>>>(p);
-  if (cudaPeekAtLastError() != cudaSuccess) {
+  // three stages of the ring where the parts leave room for them (every group of up to 8 query heads)
+  const int parts = (kWarps + (p.way == kByCluster ? 1 : 0)) * p.gr * kPartStride<D> * 4;
+  p.stages = kWarps * 3 * TL::STAGE + parts <= kMaxSmem ? 3 : 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  cfg.gridDim = dim3(p.way == kByCluster ? p.vh * p.cluster : grid);
+  cfg.blockDim = dim3(kAttnThreads);
+  cfg.dynamicSmemBytes = kWarps * p.stages * TL::STAGE + parts;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  if (p.way == kByCluster) {
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = p.cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.numAttrs = 1;
+  }
+  if (cudaLaunchKernelEx(&cfg, fn, static_cast<const AttnParams>(p)) != cudaSuccess) {
     cudaGetLastError();
     return MK_ERR_CUDA;
   }
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr;
+  if (p.way != kJoined) return MK_OK;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kAttnThreads);
-  cfg.stream = s;
-  cfg.attrs = &attr;
+  cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, join_kernel<T, D>, static_cast<const AttnParams>(p)) != cudaSuccess) {
     cudaGetLastError();
@@ -1050,9 +1242,11 @@ extern "C" int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args
       !aligned16(a->workspace) || !stride_ok(a->q_row, es) || !stride_ok(a->q_head, es) || !stride_ok(a->out_row, es) ||
       !stride_ok(a->out_head, es))
     return MK_ERR_INVALID_ARG;
-  // slots and the cost of one kv head over all rows are counted in 32 bits
+  // slots and the cost of all rows and heads are counted in 32 bits
   const int64_t slots = static_cast<int64_t>(kv->table_cols) * kv->page_size;
-  if (slots > INT32_MAX - 64 || ((slots + 15) / 16 + kRowCost) * a->n > INT32_MAX || a->n_q_heads > (1 << 20)) return MK_ERR_UNSUPPORTED;
+  if (slots > INT32_MAX - 64 || a->n_q_heads > (1 << 20) ||
+      (slots / 16 + 2 + kRowCost) * a->n > INT32_MAX / (kv->n_kv_heads * ((a->n_q_heads / kv->n_kv_heads + 15) / 16)))
+    return MK_ERR_UNSUPPORTED;
   int dev = 0;
   const int grid = sm_count(&dev);
   if (grid < 0) return MK_ERR_CUDA;
@@ -1062,14 +1256,17 @@ extern "C" int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args
   p.q = a->q, p.k = kv->k, p.v = kv->v, p.out = a->out, p.lse = a->lse;
   p.q_row = a->q_row, p.q_head = a->q_head, p.out_row = a->out_row, p.out_head = a->out_head;
   p.page_stride = kv->page_stride, p.head_stride = kv->head_stride, p.slot_stride = kv->slot_stride;
-  p.table = kv->table, p.table_stride = kv->table_stride, p.table_cols = kv->table_cols;
+  p.table = kv->table, p.table_stride = kv->table_stride;
+  p.capacity = static_cast<int>(slots);
+  p.dense = kv->slot_stride == kv->head_dim;
   p.lengths = a->lengths;
   p.k_scale = kv->k_scale, p.v_scale = kv->v_scale;
   p.status = a->status;
   p.records = static_cast<int4 *>(a->workspace);
   p.parts = reinterpret_cast<float *>(p.records + grid);
   p.n = a->n, p.hq = a->n_q_heads, p.hkv = kv->n_kv_heads;
-  p.n_pages = kv->n_pages, p.page_size = kv->page_size;
+  p.n_pages = kv->n_pages;
+  p.page_size.set(kv->page_size);
   p.window = a->window;
   p.blocks = (p.group + 15) / 16;
   p.vh = p.hkv * p.blocks;

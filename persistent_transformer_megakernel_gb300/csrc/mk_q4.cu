@@ -114,18 +114,6 @@ __device__ __forceinline__ void stage8(const __nv_bfloat16 *x, unsigned char *to
                                               __byte_perm(w.y, w.w, 0x5410), __byte_perm(w.y, w.w, 0x7632));
 }
 
-__device__ __forceinline__ void cluster_meet() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// a float of the shared memory of the cluster's CTA `rank`, at the place of `p` in this one
-__device__ __forceinline__ float load_remote(const float *p, int rank) {
-  uint32_t a;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
-}
-
 template <class T, int NT, int RT, int G, int U>
 __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) matvec_kernel(const Q4Params p) {
   using L = Layout<G>;
@@ -318,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) matvec_kernel(const
         for (int j = 1; j < kWarps; ++j) y += red[j * ROWS * COLS + i];
         red[i] = y;
       }
-      cluster_meet();
+      mkw::cluster_meet();
     }
     if (rank == 0) {
       for (int i = wk * 32 + lane; i < ROWS * mr; i += 32 * p.wk) {
@@ -328,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) matvec_kernel(const
         for (int u = TERMS - 1; u >= 0; --u) {
           const float *at = red + r * COLS + m * TERMS + u;
           if (p.cluster > 1) {
-            for (int j = 0; j < p.cluster; ++j) y += load_remote(at, j);
+            for (int j = 0; j < p.cluster; ++j) y += mkw::load_remote(at, j);
           } else {
             for (int j = 0; j < p.wk; ++j) y += at[j * ROWS * COLS];
           }
@@ -340,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) matvec_kernel(const
         }
       }
     }
-    if (p.cluster > 1) cluster_meet();
+    if (p.cluster > 1) mkw::cluster_meet();
     else meet();
     tile += step;
   };

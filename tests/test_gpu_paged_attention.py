@@ -294,3 +294,44 @@ def test_offsets_past_32_bits():
     out = mk.paged_attention(c["q"].cuda(), kc, vc, torch.tensor([use], dtype=torch.int32, device="cuda"), c["lengths"].cuda(),
                              k_scale=c["k_scale"].cuda(), v_scale=c["v_scale"].cuda(), lse=lse)
     _check(c, out, lse)
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (16, 8), (48, 16), (64, 64), (100, 100), (160, 160), (40, 2)])
+@pytest.mark.parametrize("length", [0, 1, 16, 300, 4000])
+def test_one_row(hq, hkv, length):
+    # one sequence: clusters of CTAs for each kv head, of every size, and more heads than there are clusters for
+    c = _case([length], hq, hkv, 128, BF16, BF16, 16, seed=length + hq)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    _check(c, *_run(c, status=status))
+    mk.check_status(status)
+    wide = dict(c, table=torch.cat([c["table"], torch.full((1, 600), 2 ** 30, dtype=torch.int32)], 1))
+    _check(c, *_run(wide, status=status))                   # a table for more tokens than there are
+    mk.check_status(status)
+    if length:
+        wide["table"][0, (length - 1) // 16] = -3
+        out, lse = _run(wide, status=status)
+        assert status.item() == -10 and torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+def test_one_row_left_alone_and_past_the_table():
+    c = _case([40], 4, 2, 64, F32, E4M3, 8, seed=18)
+    out, lse = torch.full((1, 4, 64), 5.0, device="cuda"), torch.full((1, 4), 5.0, device="cuda")
+    c["lengths"][0] = -1
+    mk.paged_attention(**_dev(c), out=out, lse=lse)
+    assert (out == 5).all() and (lse == 5).all()
+    c["lengths"][0] = 41
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mk.paged_attention(**_dev(c), out=out, lse=lse, status=status)
+    assert status.item() == -10 and torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("x,cache", [(BF16, BF16), (F32, E4M3)])
+def test_wide_tables_of_short_rows(window, x, cache):
+    # the same rows by a table that fits them (rows kept whole) and by a wide one (rows cut where they fall)
+    lengths = [int(v) for v in np.random.default_rng(5).integers(0, 700, 60)]
+    c = _case(lengths, 8, 4, 64, x, cache, 24, seed=19)
+    want = _run(c, window=window)
+    _check(c, *want, window=window)
+    wide = dict(c, table=torch.cat([c["table"], torch.full((60, 900), -1, dtype=torch.int32)], 1))
+    _check(c, *_run(wide, window=window), window=window)
