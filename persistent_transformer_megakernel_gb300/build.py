@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libmk.so")
 MODULE = os.path.join(HERE, "_mktorch.so")
 SOURCES = ["mk_kernels_d128.cu", "mk_kernels_hidden1024.cu", "mk_kernels_hidden2048.cu", "mk_kernels_d64.cu",
            "mk_host.cu", "mk_embed.cu", "mk_prefill.cu", "mk_gemm.cu", "mk_pfattn.cu",
-           "mk_paged.cu", "mk_q4.cu"]
+           "mk_paged.cu", "mk_q4.cu", "mk_q4_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 

@@ -15,6 +15,21 @@
 
 namespace mkw {
 
+// division of 0 <= n < 2^31 by a constant of the call
+struct Divisor {
+  uint32_t value, mul;
+  int shift;
+  __host__ void set(int d) {
+    value = d;
+    shift = 0;
+    while ((int64_t{1} << shift) < d) ++shift;
+    // n mul / 2^(31 + shift) with mul = 2^(31 + shift) / d rounded up: exact below 2^31
+    mul = d == 1 ? 0 : static_cast<uint32_t>(((uint64_t{1} << (31 + shift)) + d - 1) / d);
+    --shift;
+  }
+  __device__ __forceinline__ int quotient(int n) const { return value == 1 ? n : static_cast<int>(__umulhi(n, mul) >> shift); }
+};
+
 struct BF16Op {};
 struct FP16Op {};
 

@@ -298,21 +298,6 @@ constexpr int kRowCost = 2;
 constexpr int kShortTiles = 64;
 constexpr int kMaxSmem = 230400;       // dynamic; the static part is below 2 KB, a CTA's limit 227 KB
 
-// division of 0 <= n < 2^31 by a constant of the call
-struct Divisor {
-  uint32_t value, mul;
-  int shift;
-  __host__ void set(int d) {
-    value = d;
-    shift = 0;
-    while ((int64_t{1} << shift) < d) ++shift;
-    // n mul / 2^(31 + shift) with mul = 2^(31 + shift) / d rounded up: exact below 2^31
-    mul = d == 1 ? 0 : static_cast<uint32_t>(((uint64_t{1} << (31 + shift)) + d - 1) / d);
-    --shift;
-  }
-  __device__ __forceinline__ int quotient(int n) const { return value == 1 ? n : static_cast<int>(__umulhi(n, mul) >> shift); }
-};
-
 enum { kByCluster, kWhole, kJoined };  // how rows are dealt out: the three ways above
 
 struct AttnParams {
@@ -325,7 +310,7 @@ struct AttnParams {
   int32_t *status;
   int4 *records;       // [grid] {row, virtual head, last CTA, 1} of a row that goes on in the next CTA
   float *parts;        // [grid][2][gr][D + 4]: a row's middle or end (0) and its beginning (1)
-  Divisor page_size;
+  mkw::Divisor page_size;
   int n, hq, hkv, group, n_pages, capacity, window;   // capacity: slots of a table row
   int blocks, vh;      // head blocks of 16 query heads a kv head, virtual heads hkv * blocks
   int gr;              // query heads of a block: min(group, 16)

@@ -1,0 +1,519 @@
+// Matrix-vector products with 4-bit weights (mk_matvec_q4): the kernel and its launch for one type of x.
+//
+// y[m][n] = sum_k x[m][k] scale[n][k / group] (code[n][k] - zero[n][k / group])
+//
+// Bound by the weights' bytes: N K / 2 plus the scales.  A warp takes 16 weight
+// rows (32 where there are enough rows for every warp) as the rows of 16x8x16 matrix
+// products and the x rows as their columns, 8 a tile.  A code minus its
+// zero is a small whole number, exact in fp16.  An x row is scaled by the power
+// of two that brings its largest finite value to 2^14 .. 2^15 (undone at the end):
+// a bf16 value then is one fp16 term, an fp32 value two of 11 bits in two columns,
+// down to 2^-29 of the row's largest and from there on to 2^-40 of it.  Products
+// are summed in fp32 over a block's part of one group, multiplied by the group's
+// scale and added to the row's sum in fp32.
+//
+// A warp's block is 128 elements of k of its rows, 64 bytes a row, which it copies
+// ahead through its own ring of shared memory; registers as the
+// place of what is on its way made the loop a copy per slot, and fetching its
+// instructions took as long as the loop.  Where an element of k sits in a matrix
+// product is free as long as both operands agree: lane t of a quad takes, of each
+// row, four 32-bit words of 8 codes, 16 bytes in a row where one group covers the
+// block, 8 bytes of each of two groups of 64, 4 of each of four groups of 32, so
+// that a product never mixes two groups.  The x columns are staged in shared memory
+// with each 8 elements in the order 0 4 1 5 2 6 3 7: codes j and j + 4 of a word are
+// taken out together, for even j from the low four mantissa bits of the fp16 number
+// 1024, less 1024 + zero, for odd j from the next four, times 1/16, less 64 + zero;
+// so one shift serves four pairs (the integer pipe is the busiest).
+//
+// One persistent CTA of 16 warps an SM, so that x is staged once an SM (for 8 rows
+// that is a third of the work of a 1.7B-shaped gate and up projection).  The rows'
+// tiles are dealt out to its warps; 2 to 16 of them share a tile's k where that
+// deals the blocks out more evenly, their sums added in order.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "../../include/mk.h"
+#include "mk_mma.cuh"
+#include "mk_q4.h"
+
+namespace mkq {
+
+constexpr int kWarps = 16, kThreads = 32 * kWarps, kBlock = 128;
+constexpr int kRing = 8192;            // bytes of codes a warp has room for: 8 blocks of 16 rows
+constexpr int kMaxSmem = 225 * 1024;   // dynamic shared memory of a CTA
+constexpr int red_bytes(int nt, int rt) { return kWarps * 16 * rt * 8 * nt * 4; }   // sums of the warps
+
+// G: 32, 64, or 128 for every multiple of it
+template <int G>
+struct Layout {
+  static constexpr int groups = kBlock / G;             // of a block
+  // Pitch of the staged columns beyond a multiple of 128 bytes: with it the 8 lanes of a shared-memory phase (two
+  // columns, the four lanes of a quad) meet 8 different 16-byte banks.
+  static constexpr int pad = G == 128 ? 32 : G == 64 ? 16 : 64;
+  // the 8 elements of k, within a block, of word w of lane t, and where a column has them
+  static __device__ __forceinline__ int eighth(int t, int w) {
+    return G == 128 ? 4 * t + w : G == 64 ? 8 * (w >> 1) + 2 * t + (w & 1) : 4 * w + t;
+  }
+  static __device__ __forceinline__ int staged(int b) { return G == 128 ? b ^ ((b >> 3) & 1) : b; }
+};
+
+// where chunk c (16 bytes, 32 codes) of row r of a block is in the ring: so that words of any of the three kinds of the
+// rows of a phase meet different banks
+__device__ __forceinline__ int chunk_at(int r, int c) { return r * 64 + ((c ^ ((r & 2) | ((r >> 2) & 1))) << 4); }
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float *p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+
+
+// eight elements of x as they are in memory, their values, and the largest magnitude's bits as a float's
+template <class T>
+struct Eight;
+template <>
+struct Eight<float> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const float *p) { a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1]; }
+  __device__ __forceinline__ void values(float *x) const {
+    const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[i]);
+  }
+  __device__ __forceinline__ uint32_t largest() const {
+    constexpr uint32_t M = 0x7fffffffu;
+    return max(max(max(a.x & M, a.y & M), max(a.z & M, a.w & M)), max(max(b.x & M, b.y & M), max(b.z & M, b.w & M)));
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void values(float *x) const {
+    const uint32_t v[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(v[i] << 16);
+      x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ uint32_t largest() const {
+    constexpr uint32_t M = 0x7fff7fffu;
+    const uint32_t x = __vmaxu2(__vmaxu2(a.x & M, a.y & M), __vmaxu2(a.z & M, a.w & M));
+    return max(x << 16, x & 0xffff0000u);
+  }
+};
+
+template <class T>
+constexpr int kTerms = std::is_same<T, float>::value ? 2 : 1;
+
+__device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b) {
+  const __half2 r = __hadd2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b), *reinterpret_cast<const __half2 *>(&c));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+template <class T, int NT, int RT, int G, bool ZEROS>
+__global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_constant__ Q4Params p) {
+  using L = Layout<G>;
+  constexpr int TERMS = kTerms<T>, GB = L::groups, Q = G == 32 ? 2 : 1;
+  constexpr int ROWS = 16 * RT, COLS = 8 * NT, STAGE = ROWS * 64, STAGES = kRing / STAGE;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint32_t s_max[COLS];
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int wn = w / p.wk, wk = w % p.wk, per_cta = kWarps / p.wk;
+  const int m0 = blockIdx.y * p.pass_rows, mr = min(p.pass_rows, p.m - m0), cols = mr * TERMS;
+  unsigned char *ring = smem + w * kRing, *xs = smem + kWarps * kRing;
+  float *red = reinterpret_cast<float *>(xs + p.pass_rows * TERMS * p.pitch) + wn * p.wk * ROWS * COLS;   // sums of the warps of this tile
+
+  // this warp's slice of the blocks of k, its tiles
+  const int b0 = p.blocks * wk / p.wk, nb = p.blocks * (wk + 1) / p.wk - b0;
+  const int tile0 = blockIdx.x * per_cta + wn, step = gridDim.x * per_cta;
+  const int rounds = tile0 < p.tiles ? (p.tiles - tile0 + step - 1) / step : 0;
+  const int items = rounds * nb;
+
+  // ---- codes: this lane copies chunk t of rows g, g + 8, ... of every block ----------------------------------
+  const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  int c_tile = tile0, c_blk = 0, c_left = items, c_stage = 0;    // the copies' place
+  const unsigned char *code_at[2 * RT];
+  auto copy = [&]() {
+    if (c_left > 0) {
+      --c_left;
+      if (c_blk == 0) {
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r) {
+          const int64_t row = min(c_tile * ROWS + 8 * r + g, p.n - 1);             // rows past the last are read as it and not stored
+          code_at[r] = p.codes + row * (p.k / 2) + b0 * (kBlock / 2) + t * 16;
+        }
+      }
+      const bool there = G == 128 || (b0 + c_blk) * kBlock + t * 32 < p.k;
+#pragma unroll
+      for (int r = 0; r < 2 * RT; ++r) {
+        const uint32_t to = ring_at + c_stage * STAGE + chunk_at(8 * r + g, t);
+        if (G == 128) mkw::cp_async16(to, code_at[r]);
+        else mkw::cp_async16(to, there ? code_at[r] : p.codes, there);
+        code_at[r] += kBlock / 2;
+      }
+      if (++c_blk == nb) c_blk = 0, c_tile += step;
+      if (++c_stage == STAGES) c_stage = 0;
+    }
+    mkw::cp_async_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < STAGES - 1; ++i) copy();
+
+  // ---- scales (and zeros, in the upper half) of a block: lane l those of row l % 16, of the first or (l / 16) second
+  // group of a pair; two blocks ahead -----------------------------------------------------------------------------
+  struct Scales {
+    uint32_t v[RT][Q];
+  };
+  int s_tile = tile0, s_blk = 0, s_left = items;
+  int64_t group_at[RT];
+  auto look_up = [&]() {
+    Scales s;
+    if (s_left > 0) {
+      --s_left;
+      if (s_blk == 0) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) group_at[r] = static_cast<int64_t>(min(s_tile * ROWS + 16 * r + (lane & 15), p.n - 1)) * p.groups;
+      }
+      const int grp = G == 128 ? p.blocks_a_group.quotient(b0 + s_blk) : (b0 + s_blk) * GB + (lane >> 4);
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          s.v[r][q] = 0;
+          if (G == 128 || grp + 2 * q < p.groups) {
+            s.v[r][q] = p.scales[group_at[r] + grp + 2 * q];
+            if (ZEROS) s.v[r][q] |= static_cast<uint32_t>(p.zeros[group_at[r] + grp + 2 * q] & 15) << 16;
+          }
+        }
+      if (++s_blk == nb) s_blk = 0, s_tile += step;
+    }
+    return s;
+  };
+  Scales next = look_up(), after = look_up();
+
+  // ---- the x rows as columns of fp16 terms, zeros past k
+  const T *x = static_cast<const T *>(p.x) + m0 * p.x_row;
+  const int eighths = p.blocks * (kBlock / 8), last = p.k / 8, all = mr * eighths;
+  constexpr int KEEP = 4;                                  // eighths a thread keeps in registers between the two passes
+  if (tid < COLS) s_max[tid] = 0;
+  __syncthreads();
+  auto read = [&](int i, Eight<T> &e) {                    // eighth i % eighths of row i / eighths, if it is there
+    const int r = p.eighths.quotient(i), b = i - r * eighths;
+    if (b < last) e.load(x + r * p.x_row + b * 8);
+    return b < last ? r : -1;
+  };
+  Eight<T> kept[KEEP];
+  auto largest = [&](const Eight<T> &e, int r) {           // (a warp's eighths may be of several rows)
+    const uint32_t mx = r >= 0 ? e.largest() : 0u;
+    const unsigned same = __match_any_sync(0xffffffffu, r);
+    const uint32_t top = __reduce_max_sync(same, mx);
+    if (r >= 0 && lane == __ffs(same) - 1) atomicMax(&s_max[r], top);
+  };
+  const int slots = (all + kThreads - 1) / kThreads;
+#pragma unroll
+  for (int j = 0; j < KEEP; ++j) {
+    const int i = tid + j * kThreads;
+    if (j < slots) {
+      const int r = i < all ? read(i, kept[j]) : -1;
+      largest(kept[j], r);
+    }
+  }
+#pragma unroll 1
+  for (int j = KEEP; j < slots; ++j) {
+    const int i = tid + j * kThreads;
+    Eight<T> e;
+    const int r = i < all ? read(i, e) : -1;
+    largest(e, r);
+  }
+  __syncthreads();
+  // infinities (or NaN) in a row: its largest finite value; rare, so one warp a row
+  for (int r = w; r < mr; r += kWarps) {
+    if (s_max[r] < 0x7f800000u) continue;
+    uint32_t mx = 0;
+    for (int b = lane; b < last; b += 32) {
+      Eight<T> e;
+      float v[8];
+      e.load(x + r * p.x_row + b * 8);
+      e.values(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t a = __float_as_uint(v[j]) & 0x7fffffffu;
+        if (a < 0x7f800000u) mx = max(mx, a);
+      }
+    }
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    __syncwarp();
+    if (lane == 0) s_max[r] = mx;
+  }
+  __syncthreads();
+  auto exponent = [&](int r) {                             // of the power of two that a row is multiplied by
+    const float mx = __uint_as_float(s_max[r]);
+    return mx > 0.f ? max(-126, min(126, 14 - ilogbf(mx))) : 0;
+  };
+  auto stage = [&](int i, const Eight<T> &e) {
+    const int r = p.eighths.quotient(i), b = i - r * eighths;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (b < last) e.values(v);
+    const float f = ldexpf(1.f, exponent(r));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= f;
+    unsigned char *to = xs + r * TERMS * p.pitch + L::staged(b) * 16;
+#pragma unroll
+    for (int u = 0; u < TERMS; ++u) {
+      uint4 o;
+      o.x = mkw::take_input_term(mkw::FP16Op{}, v[0], v[4]);
+      o.y = mkw::take_input_term(mkw::FP16Op{}, v[1], v[5]);
+      o.z = mkw::take_input_term(mkw::FP16Op{}, v[2], v[6]);
+      o.w = mkw::take_input_term(mkw::FP16Op{}, v[3], v[7]);
+      *reinterpret_cast<uint4 *>(to + u * p.pitch) = o;
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < KEEP; ++j) {
+    const int i = tid + j * kThreads;
+    if (i < all) stage(i, kept[j]);
+  }
+#pragma unroll 1
+  for (int i = tid + KEEP * kThreads; i < all; i += kThreads) {
+    Eight<T> e;
+    read(i, e);
+    stage(i, e);
+  }
+  __syncthreads();
+
+  float sum[RT][NT][4];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int c = 0; c < NT; ++c) sum[r][c][0] = sum[r][c][1] = sum[r][c][2] = sum[r][c][3] = 0.f;
+  int tile = tile0, blk = 0, at_stage = 0;
+  const unsigned char *column[NT];
+  float back[NT][2];                                       // undo the powers of two of this lane's columns
+#pragma unroll
+  for (int c = 0; c < NT; ++c) {
+    column[c] = xs + (c * 8 + g < cols ? c * 8 + g : 0) * p.pitch;   // a column that is none computes what nobody stores
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int m = (c * 8 + 2 * t + j) / TERMS;
+      back[c][j] = m < mr ? ldexpf(1.f, -exponent(m)) : 0.f;
+    }
+  }
+
+  auto compute = [&](const Scales &sc) {
+    const unsigned char *codes = ring + at_stage * STAGE;
+    uint32_t v[RT][2][4];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = 16 * r + 8 * h + g;
+        if constexpr (G == 128) {
+          const uint4 a = *reinterpret_cast<const uint4 *>(codes + chunk_at(row, t));
+          v[r][h][0] = a.x, v[r][h][1] = a.y, v[r][h][2] = a.z, v[r][h][3] = a.w;
+        } else if constexpr (G == 64) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint2 a = *reinterpret_cast<const uint2 *>(codes + chunk_at(row, 2 * j + (t >> 1)) + (t & 1) * 8);
+            v[r][h][2 * j] = a.x, v[r][h][2 * j + 1] = a.y;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[r][h][j] = *reinterpret_cast<const uint32_t *>(codes + chunk_at(row, j) + t * 4);
+        }
+      }
+    const int e0 = (b0 + blk) * (kBlock / 8);
+    float acc[RT][NT][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {                          // words; a group ends with every (4 / GB)th
+      uint4 b[NT];
+#pragma unroll
+      for (int c = 0; c < NT; ++c) b[c] = *reinterpret_cast<const uint4 *>(column[c] + e0 * 16 + L::staged(L::eighth(t, i)) * 16);
+      const int grp = i * GB / 4;
+      const bool fresh = i % (4 / GB) == 0, done = (i + 1) % (4 / GB) == 0;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        uint32_t a[2][4], s[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t low = 0xe408e408u, high = 0xd480d480u;  // -(1024 + zero) and -(64 + zero), twice
+          if (ZEROS || done) s[h] = __shfl_sync(0xffffffffu, sc.v[r][grp >> 1], (grp & 1) * 16 + 8 * h + g);
+          if (ZEROS) {
+            low = (0xe400u | (s[h] >> 16)) * 0x10001u;
+            high = (0xd400u | (s[h] >> 16 << 4)) * 0x10001u;
+          }
+          const uint32_t x0 = v[r][h][i], x1 = x0 >> 8;
+          a[0][h] = add_half2((x0 & 0x000f000fu) | 0x64006400u, low);
+          a[0][2 + h] = fma_half2((x0 & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, high);
+          a[1][h] = add_half2((x1 & 0x000f000fu) | 0x64006400u, low);
+          a[1][2 + h] = fma_half2((x1 & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, high);
+        }
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+          if (fresh) mkw::mma_zero(mkw::FP16Op{}, acc[r][c], a[0], b[c].x, b[c].y);
+          else mkw::mma(mkw::FP16Op{}, acc[r][c], a[0], b[c].x, b[c].y);
+          mkw::mma(mkw::FP16Op{}, acc[r][c], a[1], b[c].z, b[c].w);
+        }
+        if (done) {
+          const float s0 = __uint_as_float(s[0] << 16), s1 = __uint_as_float(s[1] << 16);
+#pragma unroll
+          for (int c = 0; c < NT; ++c) {
+            sum[r][c][0] += s0 * acc[r][c][0];
+            sum[r][c][1] += s0 * acc[r][c][1];
+            sum[r][c][2] += s1 * acc[r][c][2];
+            sum[r][c][3] += s1 * acc[r][c][3];
+          }
+        }
+      }
+    }
+  };
+  auto store = [&](int row, int m, float y) {
+    if (row >= p.n || m >= mr) return;
+    if (p.residual) y += to_float(static_cast<const T *>(p.residual)[(m0 + m) * p.residual_row + row]);
+    put(static_cast<T *>(p.y) + (m0 + m) * p.y_row + row, y);
+  };
+  // a tile's sums: a lane has rows g and g + 8 by columns 2t and 2t + 1, which are the two terms of one x row or two x rows
+  auto finish = [&]() {
+    if (p.wk > 1) {
+      // over the warps that share the tile, each adding up its part of the lanes' values
+      float4 *mine = reinterpret_cast<float4 *>(red) + lane;
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+          mine[((r * NT + c) * p.wk + wk) * 32] = make_float4(sum[r][c][0], sum[r][c][1], sum[r][c][2], sum[r][c][3]);
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + wn), "r"(32 * p.wk) : "memory");
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+          if ((r * NT + c) % p.wk == wk) {
+            float4 y = mine[(r * NT + c) * p.wk * 32];
+            for (int j = 1; j < p.wk; ++j) {
+              const float4 z = mine[((r * NT + c) * p.wk + j) * 32];
+              y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+            }
+            sum[r][c][0] = y.x, sum[r][c][1] = y.y, sum[r][c][2] = y.z, sum[r][c][3] = y.w;
+          }
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + wn), "r"(32 * p.wk) : "memory");
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        if (p.wk == 1 || (r * NT + c) % p.wk == wk) {
+          const int row = tile * ROWS + r * 16 + g;
+          if constexpr (TERMS == 2) {
+            const int m = c * 4 + t;
+            store(row, m, (sum[r][c][1] + sum[r][c][0]) * back[c][0]);
+            store(row + 8, m, (sum[r][c][3] + sum[r][c][2]) * back[c][0]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              store(row, c * 8 + 2 * t + j, sum[r][c][j] * back[c][j]);
+              store(row + 8, c * 8 + 2 * t + j, sum[r][c][2 + j] * back[c][j]);
+            }
+          }
+        }
+        sum[r][c][0] = sum[r][c][1] = sum[r][c][2] = sum[r][c][3] = 0.f;
+      }
+    tile += step;
+  };
+
+  if (nb == 0) {                                           // fewer blocks than warps: this one only joins in
+    for (int i = 0; i < rounds; ++i) finish();
+    return;
+  }
+#pragma unroll 1
+  for (int i = 0; i < items; ++i) {
+    copy();
+    const Scales now = next;
+    next = after;
+    after = look_up();
+    mkw::cp_async_wait<STAGES - 1>();
+    __syncwarp();
+    compute(now);
+    __syncwarp();                                          // every lane has read the stage
+    if (++at_stage == STAGES) at_stage = 0;
+    if (++blk == nb) {
+      blk = 0;
+      finish();
+    }
+  }
+  mkw::cp_async_wait<0>();
+}
+
+template <class T, int NT, int RT, int G, bool ZEROS>
+int launch(Q4Params p, int sms, int dev, cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};
+  const auto fn = &matvec_kernel<T, NT, RT, G, ZEROS>;
+  if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) {
+      cudaGetLastError();
+      return MK_ERR_CUDA;
+    }
+    ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
+  }
+  p.tiles = (p.n + 16 * RT - 1) / (16 * RT);
+  p.pitch = p.blocks * kBlock * 2 + Layout<G>::pad;
+  // the sharing of k that leaves the busiest warp the fewest blocks, fewer warps a tile where that is equal
+  int64_t best = 0;
+  for (int wk = 1; wk <= kWarps; wk *= 2) {
+    const int64_t per_round = static_cast<int64_t>(sms) * (kWarps / wk), rounds = (p.tiles + per_round - 1) / per_round;
+    const int64_t cost = rounds * ((p.blocks + wk - 1) / wk);
+    if (wk == 1 || cost < best) best = cost, p.wk = wk;
+  }
+  // x rows of a pass: as many as its columns hold and shared memory has room for
+  const int red = p.wk > 1 ? red_bytes(NT, RT) : 0;
+  p.pass_rows = std::min({p.m, 8 * NT / kTerms<T>, (kMaxSmem - kWarps * kRing - red) / p.pitch / kTerms<T>});
+  const int smem = kWarps * kRing + red + p.pass_rows * kTerms<T> * p.pitch;
+  const int passes = (p.m + p.pass_rows - 1) / p.pass_rows;
+  if (passes > 65535) return MK_ERR_UNSUPPORTED;
+  const int per_cta = kWarps / p.wk, want = (p.tiles + per_cta - 1) / per_cta;
+  fn<<<dim3(std::min(want, sms), passes), kThreads, smem, s>>>(p);
+  if (cudaPeekAtLastError() != cudaSuccess) {
+    cudaGetLastError();
+    return MK_ERR_CUDA;
+  }
+  return MK_OK;
+}
+
+template <class T, int NT, int RT, bool ZEROS>
+int by_group(Q4Params &p, int group, int sms, int dev, cudaStream_t s) {
+  if (group == 32) return launch<T, NT, RT, 32, ZEROS>(p, sms, dev, s);
+  if (group == 64) return launch<T, NT, RT, 64, ZEROS>(p, sms, dev, s);
+  p.blocks_a_group.set(group / kBlock);
+  return launch<T, NT, RT, 128, ZEROS>(p, sms, dev, s);
+}
+
+template <class T, bool ZEROS>
+int by_rows(Q4Params &p, int group, int sms, int dev, cudaStream_t s) {
+  p.blocks = (p.k + kBlock - 1) / kBlock;
+  p.eighths.set(p.blocks * (kBlock / 8));
+  const int cols = p.m > 32 ? 32 : p.m * kTerms<T>;
+  auto room = [&](int nt) { return (kMaxSmem - kWarps * kRing - red_bytes(nt, 1)) / (p.blocks * kBlock * 2 + 64); };
+  if (cols <= 8 || room(2) < 16) {
+    // 32 rows a tile, whose matrix products share what is read of x, where every warp has one of them
+    if (p.n / 32 >= sms * kWarps && p.m <= 8 / kTerms<T>) return by_group<T, 1, 2, ZEROS>(p, group, sms, dev, s);
+    return by_group<T, 1, 1, ZEROS>(p, group, sms, dev, s);
+  }
+  // four column tiles where shared memory has room for more columns than two have
+  if (cols <= 16 || room(4) < 24) return by_group<T, 2, 1, ZEROS>(p, group, sms, dev, s);
+  return by_group<T, 4, 1, ZEROS>(p, group, sms, dev, s);
+}
+
+template <class T>
+int run(Q4Params &p, int group, int sms, int dev, cudaStream_t s) {
+  return p.zeros ? by_rows<T, true>(p, group, sms, dev, s) : by_rows<T, false>(p, group, sms, dev, s);
+}
+
+}  // namespace mkq

@@ -65,7 +65,7 @@ def test_many_rounds_of_tiles(x):
 
 @pytest.mark.parametrize("m,x", [(1, F32), (2, F32), (7, BF16)])
 def test_the_longest_rows(m, x):
-    _run(m, 40, 24576, 128, x, seed=3)                      # fp32: one x row a pass
+    _run(m, 40, 20480, 128, x, seed=3)                      # fp32: one x row a pass
 
 
 def test_strides_and_residual_in_place():
@@ -90,7 +90,22 @@ def test_infinities_and_nan_stay_in_their_rows():
     x = torch.ones((4, 128))
     x[1, 5], x[2, 6], x[3, 0] = float("inf"), float("nan"), 3.4e38
     y = mk.matvec_q4(x.cuda(), codes.cuda(), scales.cuda()).cpu()
+    z = torch.ones((1, 128))
+    z[0, 5], z[0, 9] = float("inf"), -1e30                  # finite values beside an infinity do not become one
+    assert (mk.matvec_q4(z.cuda(), codes.cuda(), scales.cuda()) == float("inf")).all()
     assert torch.isfinite(y[0]).all() and (y[1] == float("inf")).all() and torch.isnan(y[2]).all() and torch.isfinite(y[3]).all()
+
+
+@pytest.mark.parametrize("mag", [2.0 ** -90, 2.0 ** -20, 2.0 ** 80])
+def test_rows_of_any_magnitude(mag):
+    # a row is brought into fp16's range by a power of two: results do not depend on its size, nor on other rows'
+    codes, scales, z = (t.cuda() for t in _weights(200, 512, 64, True, seed=11))
+    x = torch.randn((3, 512), generator=torch.Generator().manual_seed(2)).cuda()
+    want = mk.matvec_q4(x, codes, scales, zeros=z)
+    x[1] *= mag
+    got = mk.matvec_q4(x, codes, scales, zeros=z)
+    got[1] /= mag
+    assert torch.equal(got, want)
 
 
 def test_nothing_to_do():
