@@ -29,7 +29,7 @@ __device__ __forceinline__ void report(int32_t *status, int code) {
 // consecutive elements of the first half and the N elements half a head further,
 // the pairs of the rotation, so that every load and store is 16 bytes of an input
 // row and a pair meets in one thread; the squares are summed over the head's
-// threads by shuffles.  A thread takes up to kHeads heads of its token: their
+// threads by shuffles.  A thread takes 1 or 4 heads of its token: their
 // loads are on their way together, and the token's slot, page, cos and sin are
 // looked up once for them.  A thread that would need a page outside the cache or
 // a rotary row outside the table writes nothing.
@@ -45,9 +45,11 @@ struct AppendParams {
   const uint16_t *q_norm, *k_norm;
   const float *k_scale, *v_scale;
   int32_t *status;
-  int n, hq, hkv, n_pages, page_size, table_rows, table_cols, rope_rows, rope_mode, sec0, sec1, sec2;
+  mkw::Divisor page_size;
+  int n, hq, hkv, n_pages, table_rows, table_cols, rope_rows, rope_mode, sec0, sec1, sec2;
   int seq0, slot0;             // slots == NULL: row i is slot slot0 + i of sequence seq0
-  int groups, rows;            // head groups (of up to kHeads heads) of a CTA and token rows of a CTA
+  mkw::Divisor groups;         // groups of heads (a thread's) of a CTA
+  int rows, step;              // token rows of a CTA, groups of heads of a row
   float eps;
 };
 
@@ -58,30 +60,28 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// 16 bytes of a row: N values, as they are in memory and as numbers
 template <class T>
 struct Vec;
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void load(const float *p, float *x) {
-    const float4 f = *reinterpret_cast<const float4 *>(p);
-    x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+  static __device__ __forceinline__ void numbers(const uint4 &w, float *x) {
+    x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
   }
-  static __device__ __forceinline__ void store(float *p, const float *x) {
-    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  static __device__ __forceinline__ uint4 bits(const float *x) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
   }
 };
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float *x) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(p);
+  static __device__ __forceinline__ void numbers(const uint4 &w, float *x) {
     x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
     x[4] = bf16_lo(w.z), x[5] = bf16_hi(w.z), x[6] = bf16_lo(w.w), x[7] = bf16_hi(w.w);
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *x) {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                                               pack_bf16(x[6], x[7]));
+  static __device__ __forceinline__ uint4 bits(const float *x) {
+    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
   }
 };
 
@@ -111,48 +111,64 @@ __device__ __forceinline__ void store_cache(__nv_fp8_e4m3 *p, const float *x, fl
     *reinterpret_cast<uint32_t *>(p) = w[0];
 }
 
-constexpr int kAppendThreads = 256, kHeads = 4;
+constexpr int kAppendThreads = 256;
 
-template <class T, class C, int D>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
+template <int N>
+__device__ __forceinline__ void load_gains(const uint16_t *p, float *x) {
+  if constexpr (N == 8) {
+    Vec<__nv_bfloat16>::numbers(*reinterpret_cast<const uint4 *>(p), x);
+  } else {
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
+  }
+}
+
+// H: heads a thread takes.  4 for many tokens, at three CTAs an SM (20011 tokens of 32 heads of 128, bf16 to e4m3: 68 us;
+// 81 us at two, 81 us with 2 heads at four, 99 us with 1 at five); 1 where all threads are resident at once anyway (one
+// token 3.1 us against 3.8, 256 tokens 3.8 against 4.8)
+template <class T, class C, int D, int H>
+__global__ void __launch_bounds__(kAppendThreads, H == 1 ? 4 : 3) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int N = Vec<T>::N, TPH = D / 2 / N;           // threads of one head
   const int heads = p.hq + 2 * p.hkv;
   const int item = threadIdx.x / TPH, i0 = (threadIdx.x % TPH) * N;
-  const int row_in = item / p.groups, step = (heads + kHeads - 1) / kHeads;
-  const int first = blockIdx.y * p.groups + item % p.groups;   // heads first, first + step, ...
+  const int row_in = p.groups.quotient(item), step = p.step;
+  const int first = blockIdx.y * static_cast<int>(p.groups.value) + item - row_in * static_cast<int>(p.groups.value);   // heads first, first + step, ...
   const int64_t row64 = static_cast<int64_t>(blockIdx.x) * p.rows + row_in;
   const bool live = row_in < p.rows && row64 < p.n && first < step;
   const int row = live ? static_cast<int>(row64) : 0;
 
-  // every thread of a warp stays to the shuffles below; one with nothing to do works on zeros
-  float lo[kHeads][N], hi[kHeads][N];
-#pragma unroll
-  for (int j = 0; j < kHeads; ++j) {
-    const int h = first + j * step;
-#pragma unroll
-    for (int i = 0; i < N; ++i) lo[j][i] = hi[j][i] = 0.f;
-    if (live && h < heads) {
-      const T *src = h < p.hq ? static_cast<const T *>(p.q) + row * p.q_row + h * p.q_head
-                              : h < p.hq + p.hkv ? static_cast<const T *>(p.k) + row * p.k_row + (h - p.hq) * p.k_head
-                                                 : static_cast<const T *>(p.v) + row * p.v_row + (h - p.hq - p.hkv) * p.v_head;
-      Vec<T>::load(src + i0, lo[j]);
-      Vec<T>::load(src + i0 + D / 2, hi[j]);
+  const int slot = !live ? -1 : p.slots ? p.slots[row] : p.slot0 + row;
+  const int seq = p.seqs ? p.seqs[row] : p.slots ? row : p.seq0;
+  int at[3] = {slot, slot, slot};
+  if (p.positions) {
+    at[0] = at[1] = at[2] = p.positions[row];
+    if (p.rope_mode) {
+      at[1] = p.positions[static_cast<int64_t>(p.n) + row];
+      at[2] = p.positions[2 * static_cast<int64_t>(p.n) + row];
     }
   }
-  const int slot = !live ? -1 : p.slots ? p.slots[row] : p.slot0 + row;
+  // every thread of a warp stays to the shuffles below; one with nothing to do works on zeros
+  uint4 lo[H], hi[H];
+#pragma unroll
+  for (int j = 0; j < H; ++j) {
+    const int h = first + j * step;
+    lo[j] = hi[j] = make_uint4(0, 0, 0, 0);
+    if (live && h < heads) {
+      const T *src = (h < p.hq ? static_cast<const T *>(p.q) + row * p.q_row + h * p.q_head
+                               : h < p.hq + p.hkv ? static_cast<const T *>(p.k) + row * p.k_row + (h - p.hq) * p.k_head
+                                                  : static_cast<const T *>(p.v) + row * p.v_row + (h - p.hq - p.hkv) * p.v_head) + i0;
+      lo[j] = __ldcs(reinterpret_cast<const uint4 *>(src));
+      hi[j] = __ldcs(reinterpret_cast<const uint4 *>(src + D / 2));
+    }
+  }
   bool ok = slot >= 0;
   int64_t dst = 0;
   float2 cs[N];
   if (ok) {
-    const int seq = p.seqs ? p.seqs[row] : p.slots ? row : p.seq0;
-    const int col = slot / p.page_size;
+    const int col = p.page_size.quotient(slot);
     int page = -1;
     if (seq >= 0 && seq < p.table_rows && col < p.table_cols) page = p.table[seq * p.table_stride + col];
     if (p.rope) {
-      int at[3];
-      at[0] = p.positions ? p.positions[row] : slot;
-      at[1] = p.rope_mode ? p.positions[static_cast<int64_t>(p.n) + row] : at[0];
-      at[2] = p.rope_mode ? p.positions[2 * static_cast<int64_t>(p.n) + row] : at[0];
       // refused for every head alike, so that a row is stored whole or not at all
       if (at[0] < 0 || at[0] >= p.rope_rows || at[1] < 0 || at[1] >= p.rope_rows || at[2] < 0 || at[2] >= p.rope_rows) {
         ok = false;
@@ -181,65 +197,82 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       if (ok) report(p.status, MK_ERR_BAD_PAGE);
       ok = false;
     }
-    dst = page * p.page_stride + (slot - col * p.page_size) * p.slot_stride;
+    dst = page * p.page_stride + (slot - col * static_cast<int>(p.page_size.value)) * p.slot_stride;
   }
 #pragma unroll
-  for (int j = 0; j < kHeads; ++j) {
+  for (int j = 0; j < H; ++j) {
     const int h = first + j * step;
     const bool is_q = h < p.hq, is_k = !is_q && h < p.hq + p.hkv;
     const uint16_t *gain = is_q ? p.q_norm : is_k ? p.k_norm : nullptr;
-    float ss = 0.f;
+    float a[N], b[N];
+    Vec<T>::numbers(lo[j], a);
+    Vec<T>::numbers(hi[j], b);
+    if (p.q_norm || p.k_norm) {                            // (the same for the whole grid)
+      float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) ss += lo[j][i] * lo[j][i] + hi[j][i] * hi[j][i];
+      for (int i = 0; i < N; ++i) ss += a[i] * a[i] + b[i] * b[i];
 #pragma unroll
-    for (int o = TPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!ok || h >= heads) continue;
-    if (gain) {
-      const float r = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
+      for (int o = TPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (gain) {
+        const float r = rsqrtf(ss * (1.0f / D) + p.eps);
+        float ga[N], gb[N];
+        load_gains<N>(gain + i0, ga);
+        load_gains<N>(gain + i0 + D / 2, gb);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        lo[j][i] = lo[j][i] * r * bf16_lo(gain[i0 + i]);
-        hi[j][i] = hi[j][i] * r * bf16_lo(gain[i0 + D / 2 + i]);
+        for (int i = 0; i < N; ++i) {
+          a[i] *= r * ga[i];
+          b[i] *= r * gb[i];
+        }
       }
     }
+    if (!ok || h >= heads) continue;
     if (p.rope && (is_q || is_k)) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float a = lo[j][i], b = hi[j][i];
-        lo[j][i] = a * cs[i].x - b * cs[i].y;
-        hi[j][i] = b * cs[i].x + a * cs[i].y;
+        const float x = a[i], y = b[i];
+        a[i] = x * cs[i].x - y * cs[i].y;
+        b[i] = y * cs[i].x + x * cs[i].y;
       }
     }
     if (is_q) {
-      T *out = static_cast<T *>(p.q_out) + row * p.out_row + h * p.out_head;
-      Vec<T>::store(out + i0, lo[j]);
-      Vec<T>::store(out + i0 + D / 2, hi[j]);
+      T *out = static_cast<T *>(p.q_out) + row * p.out_row + h * p.out_head + i0;
+      *reinterpret_cast<uint4 *>(out) = Vec<T>::bits(a);
+      *reinterpret_cast<uint4 *>(out + D / 2) = Vec<T>::bits(b);
     } else {
       const int kvh = is_k ? h - p.hq : h - p.hq - p.hkv;
-      C *out = static_cast<C *>(is_k ? p.k_cache : p.v_cache) + dst + kvh * p.head_stride;
+      C *out = static_cast<C *>(is_k ? p.k_cache : p.v_cache) + dst + kvh * p.head_stride + i0;
       const float *scales = is_k ? p.k_scale : p.v_scale;
-      const float inv = scales ? 1.0f / scales[kvh] : 1.0f;
-      store_cache<N>(out + i0, lo[j], inv);
-      store_cache<N>(out + i0 + D / 2, hi[j], inv);
+      const float inv = scales ? __frcp_rn(scales[kvh]) : 1.0f;
+      store_cache<N>(out, a, inv);
+      store_cache<N>(out + D / 2, b, inv);
     }
   }
 }
 
-template <class T, class C, int D>
-int launch_append(AppendParams p, cudaStream_t s) {
+template <class T, class C, int D, int H>
+int launch_heads_of(AppendParams p, cudaStream_t s) {
   constexpr int items = kAppendThreads / (D / 2 / Vec<T>::N);   // head groups a CTA has threads for
-  if (p.hq > (1 << 20) || p.hkv > (1 << 20)) return MK_ERR_UNSUPPORTED;
-  const int groups = (p.hq + 2 * p.hkv + kHeads - 1) / kHeads;
-  p.groups = std::min(groups, items);
-  p.rows = items / p.groups;
-  const int ctas = (p.n - 1) / p.rows + 1, parts = (groups + p.groups - 1) / p.groups;
+  p.step = (p.hq + 2 * p.hkv + H - 1) / H;
+  const int groups = std::min(p.step, items);
+  p.groups.set(groups);
+  p.rows = items / groups;
+  const int ctas = (p.n - 1) / p.rows + 1, parts = (p.step + groups - 1) / groups;
   if (parts > 65535) return MK_ERR_UNSUPPORTED;
-  append_kernel<T, C, D><<<dim3(ctas, parts), kAppendThreads, 0, s>>>(p);
+  append_kernel<T, C, D, H><<<dim3(ctas, parts), kAppendThreads, 0, s>>>(p);
   if (cudaPeekAtLastError() != cudaSuccess) {
     cudaGetLastError();
     return MK_ERR_CUDA;
   }
   return MK_OK;
+}
+
+template <class T, class C, int D>
+int launch_append(const AppendParams &p, cudaStream_t s) {
+  if (p.hq > (1 << 20) || p.hkv > (1 << 20)) return MK_ERR_UNSUPPORTED;
+  const int sms = sm_count(nullptr);
+  if (sms < 0) return MK_ERR_CUDA;
+  const int64_t threads = static_cast<int64_t>(p.n) * (p.hq + 2 * p.hkv) * (D / 2 / Vec<T>::N);
+  return threads <= static_cast<int64_t>(sms) * 4 * kAppendThreads ? launch_heads_of<T, C, D, 1>(p, s) : launch_heads_of<T, C, D, 4>(p, s);
 }
 
 int run_append(const AppendParams &p, int dtype, int cache, int d, cudaStream_t s) {
@@ -1134,7 +1167,8 @@ void fill_cache(AppendParams &p, const mk_paged_kv *kv) {
   p.table = kv->table;
   p.table_stride = kv->table_stride;
   p.table_rows = kv->table_rows, p.table_cols = kv->table_cols;
-  p.n_pages = kv->n_pages, p.page_size = kv->page_size;
+  p.n_pages = kv->n_pages;
+  p.page_size.set(kv->page_size);
   p.hkv = kv->n_kv_heads;
   p.k_scale = kv->k_scale, p.v_scale = kv->v_scale;
 }
@@ -1169,7 +1203,7 @@ extern "C" int mk_paged_append(const mk_paged_kv *kv, const mk_append_args *a, m
   if (a->n_q_heads > 0 && (!a->q || !a->q_out || !aligned16(a->q) || !aligned16(a->q_out) || !stride_ok(a->q_row, es) ||
                            !stride_ok(a->q_head, es) || !stride_ok(a->out_row, es) || !stride_ok(a->out_head, es)))
     return MK_ERR_INVALID_ARG;
-  if ((a->q_norm || a->k_norm) && !(a->rms_eps >= 0.f)) return MK_ERR_INVALID_ARG;
+  if ((a->q_norm || a->k_norm) && (!(a->rms_eps >= 0.f) || !aligned16(a->q_norm) || !aligned16(a->k_norm))) return MK_ERR_INVALID_ARG;
   if (a->rope) {
     if (!aligned16(a->rope)) return MK_ERR_INVALID_ARG;
     if (a->rope_mode != 0 &&

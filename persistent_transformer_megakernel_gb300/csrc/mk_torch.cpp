@@ -300,6 +300,7 @@ mk_append_args append_args(PyObject *const *o, const mk_paged_kv &kv, const c10:
   }
   a.q_norm = vector(o[A_QN], "q_norm", at::kBFloat16, d, dev);
   a.k_norm = vector(o[A_KN], "k_norm", at::kBFloat16, d, dev);
+  need(reinterpret_cast<uintptr_t>(a.q_norm) % 16 == 0 && reinterpret_cast<uintptr_t>(a.k_norm) % 16 == 0, "q_norm and k_norm must start on 16 bytes");
   a.rms_eps = o[A_EPS] ? static_cast<float>(number(o[A_EPS])) : 1e-6f;
   need(a.rms_eps >= 0.f, "eps must not be negative");
   a.status = static_cast<int32_t *>(vector(o[A_STATUS], "status", at::kInt, 1, dev));

@@ -85,7 +85,7 @@ def test_append_tensors():
                 dict(rope=torch.zeros((10, 64, 2))), dict(rope=torch.zeros((10, 32, 2), dtype=torch.float64)), dict(positions=i32(2)),
                 dict(positions=i32(3, 3)), dict(mrope_sections=(12, 10, 10)), dict(positions=i32(3, 3), mrope_sections=(12, 10, 9)),
                 dict(positions=i32(3, 3), mrope_sections=(42, -5, -5)), dict(positions=i32(3, 4), mrope_sections=(12, 10, 10)),
-                dict(rope=None, positions=i32(3)), dict(q_norm=torch.zeros(64)), dict(k_norm=torch.zeros(128, dtype=BF16)),
+                dict(rope=None, positions=i32(3)), dict(q_norm=torch.zeros(64)), dict(k_norm=torch.zeros(128, dtype=BF16)), dict(k_norm=torch.zeros(65, dtype=BF16)[1:]),
                 dict(status=i32(2)), dict(q=None), dict(eps=-1.0), dict(eps=float("nan")), dict(v=None), dict(mrope_sections=(16, 16))):
         with pytest.raises(ValueError):
             _append(**bad)
@@ -191,7 +191,7 @@ def test_argument_errors_of_the_c_entry_points():
     assert append(kv(head_dim=96), app()) == -2 and attend(kv(head_dim=96), att()) == -2
     for f in (dict(n=-1), dict(dtype=2), dict(n=1, k=None), dict(n=1, v=8), dict(n=1, slots=None), dict(n=1, k_row=130), dict(n=1, v_head=-4),
               dict(n=1, n_q_heads=2), dict(rope_mode=3), dict(rope_rows=-1), dict(n=1, rope=16, rope_rows=4, rope_mode=1),
-              dict(n=1, k_norm=16, rms_eps=-1.0), dict(n=1, rope=8, rope_rows=4)):
+              dict(n=1, k_norm=16, rms_eps=-1.0), dict(n=1, q_norm=18, rms_eps=0.0), dict(n=1, rope=8, rope_rows=4)):
         assert append(kv(), app(**f)) == -1, f
     for f in (dict(n=4), dict(n=-1), dict(dtype=2), dict(window=-1), dict(n_q_heads=3), dict(n_q_heads=0), dict(scale=float("nan")),
               dict(scale=float("inf")), dict(n=1, q=None), dict(n=1, out=20), dict(n=1, lengths=None), dict(n=1, workspace=None),
