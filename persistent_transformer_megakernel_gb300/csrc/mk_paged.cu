@@ -111,7 +111,7 @@ __device__ __forceinline__ void store_cache(__nv_fp8_e4m3 *p, const float *x, fl
     *reinterpret_cast<uint32_t *>(p) = w[0];
 }
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 
 template <int N>
 __device__ __forceinline__ void load_gains(const uint16_t *p, float *x) {
@@ -123,11 +123,11 @@ __device__ __forceinline__ void load_gains(const uint16_t *p, float *x) {
   }
 }
 
-// H: heads a thread takes.  4 for many tokens, at three CTAs an SM (20011 tokens of 32 heads of 128, bf16 to e4m3: 68 us;
-// 81 us at two, 81 us with 2 heads at four, 99 us with 1 at five); 1 where all threads are resident at once anyway (one
-// token 3.1 us against 3.8, 256 tokens 3.8 against 4.8)
+// H: heads a thread takes.  4 for many tokens, 768 threads an SM (20011 tokens of 32 heads of 128, bf16 to e4m3: 62 us;
+// at 512 a fifth longer, with 2 heads and 1024 as well, with 1 and 1280 two fifths); 1 where all threads are resident at
+// once anyway (one token 2.8 us against 3.5, 256 tokens 3.4 against 4.5)
 template <class T, class C, int D, int H>
-__global__ void __launch_bounds__(kAppendThreads, H == 1 ? 4 : 3) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, H == 1 ? 8 : 6) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int N = Vec<T>::N, TPH = D / 2 / N;           // threads of one head
   const int heads = p.hq + 2 * p.hkv;
   const int item = threadIdx.x / TPH, i0 = (threadIdx.x % TPH) * N;
@@ -272,7 +272,7 @@ int launch_append(const AppendParams &p, cudaStream_t s) {
   const int sms = sm_count(nullptr);
   if (sms < 0) return MK_ERR_CUDA;
   const int64_t threads = static_cast<int64_t>(p.n) * (p.hq + 2 * p.hkv) * (D / 2 / Vec<T>::N);
-  return threads <= static_cast<int64_t>(sms) * 4 * kAppendThreads ? launch_heads_of<T, C, D, 1>(p, s) : launch_heads_of<T, C, D, 4>(p, s);
+  return threads <= static_cast<int64_t>(sms) * 8 * kAppendThreads ? launch_heads_of<T, C, D, 1>(p, s) : launch_heads_of<T, C, D, 4>(p, s);
 }
 
 int run_append(const AppendParams &p, int dtype, int cache, int d, cudaStream_t s) {

@@ -123,10 +123,11 @@ __device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c
 template <class T, int NT, int RT, int G, bool ZEROS>
 __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_constant__ Q4Params p) {
   using L = Layout<G>;
-  constexpr int TERMS = kTerms<T>, GB = L::groups, Q = G == 32 ? 2 : 1;
+  constexpr int TERMS = kTerms<T>, GB = L::groups;
   constexpr int ROWS = 16 * RT, COLS = 8 * NT, STAGE = ROWS * 64, STAGES = kRing / STAGE;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint32_t s_max[COLS];
+  __shared__ float s_to[COLS], s_back[COLS];               // the powers of two that x rows are multiplied by, and their inverses
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int wn = w / p.wk, wk = w % p.wk, per_cta = kWarps / p.wk;
   const int m0 = blockIdx.y * p.pass_rows, mr = min(p.pass_rows, p.m - m0), cols = mr * TERMS;
@@ -169,32 +170,44 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
 #pragma unroll 1
   for (int i = 0; i < STAGES - 1; ++i) copy();
 
-  // ---- scales (and zeros, in the upper half) of a block: lane l those of row l % 16, of the first or (l / 16) second
-  // group of a pair; two blocks ahead -----------------------------------------------------------------------------
+  // ---- scales and zeros of a block, two blocks ahead: lane l has those of row l % ROWS, at once where they lie on a
+  // boundary of their size ------------------------------------------------------------------------------------------
   struct Scales {
-    uint32_t v[RT][Q];
+    uint32_t pair[G == 32 ? 2 : 1], zeros;               // bf16 of two groups, a byte a group
   };
   int s_tile = tile0, s_blk = 0, s_left = items;
-  int64_t group_at[RT];
+  int64_t group_at = 0;
   auto look_up = [&]() {
     Scales s;
     if (s_left > 0) {
       --s_left;
-      if (s_blk == 0) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) group_at[r] = static_cast<int64_t>(min(s_tile * ROWS + 16 * r + (lane & 15), p.n - 1)) * p.groups;
-      }
-      const int grp = G == 128 ? p.blocks_a_group.quotient(b0 + s_blk) : (b0 + s_blk) * GB + (lane >> 4);
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-          s.v[r][q] = 0;
-          if (G == 128 || grp + 2 * q < p.groups) {
-            s.v[r][q] = p.scales[group_at[r] + grp + 2 * q];
-            if (ZEROS) s.v[r][q] |= static_cast<uint32_t>(p.zeros[group_at[r] + grp + 2 * q] & 15) << 16;
-          }
+      if (s_blk == 0) group_at = static_cast<int64_t>(min(s_tile * ROWS + lane % ROWS, p.n - 1)) * p.groups;
+      const int blk = b0 + s_blk;
+      const int64_t at = group_at + (G == 128 ? p.blocks_a_group.quotient(blk) : blk * GB);
+      const uint16_t *sc = p.scales + at;
+      const uint8_t *z = p.zeros + at;
+      if (G == 128) {
+        s.pair[0] = *sc;
+        if (ZEROS) s.zeros = *z;
+      } else if (p.vec && (blk + 1) * GB <= p.groups) {
+        if constexpr (G == 64) {
+          s.pair[0] = *reinterpret_cast<const uint32_t *>(sc);
+          if (ZEROS) s.zeros = *reinterpret_cast<const uint16_t *>(z);
+        } else if constexpr (G == 32) {
+          const uint2 v = *reinterpret_cast<const uint2 *>(sc);
+          s.pair[0] = v.x, s.pair[1] = v.y;
+          if (ZEROS) s.zeros = *reinterpret_cast<const uint32_t *>(z);
         }
+      } else {
+        s.zeros = 0;
+#pragma unroll
+        for (int i = 0; i < GB; ++i) {
+          const bool there = blk * GB + i < p.groups;    // a scale of 0 past the end
+          const uint32_t v = there ? sc[i] : 0u;
+          s.pair[i / 2] = i % 2 ? s.pair[i / 2] | (v << 16) : v;
+          if (ZEROS && there) s.zeros |= static_cast<uint32_t>(z[i]) << (8 * i);
+        }
+      }
       if (++s_blk == nb) s_blk = 0, s_tile += step;
     }
     return s;
@@ -213,11 +226,14 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
     return b < last ? r : -1;
   };
   Eight<T> kept[KEEP];
-  auto largest = [&](const Eight<T> &e, int r) {           // (a warp's eighths may be of several rows)
+  auto largest = [&](const Eight<T> &e, int r) {
     const uint32_t mx = r >= 0 ? e.largest() : 0u;
-    const unsigned same = __match_any_sync(0xffffffffu, r);
-    const uint32_t top = __reduce_max_sync(same, mx);
-    if (r >= 0 && lane == __ffs(same) - 1) atomicMax(&s_max[r], top);
+    if (__all_sync(0xffffffffu, r == __shfl_sync(0xffffffffu, r, 0))) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, mx);
+      if (lane == 0 && r >= 0) atomicMax(&s_max[r], top);
+    } else if (r >= 0) {                                   // eighths of several rows
+      atomicMax(&s_max[r], mx);
+    }
   };
   const int slots = (all + kThreads - 1) / kThreads;
 #pragma unroll
@@ -236,35 +252,32 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
     largest(e, r);
   }
   __syncthreads();
-  // infinities (or NaN) in a row: its largest finite value; rare, so one warp a row
   for (int r = w; r < mr; r += kWarps) {
-    if (s_max[r] < 0x7f800000u) continue;
-    uint32_t mx = 0;
-    for (int b = lane; b < last; b += 32) {
-      Eight<T> e;
-      float v[8];
-      e.load(x + r * p.x_row + b * 8);
-      e.values(v);
+    uint32_t mx = s_max[r];
+    if (mx >= 0x7f800000u) {                               // infinities (or NaN) in the row: its largest finite value
+      mx = 0;
+      for (int b = lane; b < last; b += 32) {
+        Eight<T> e;
+        float v[8];
+        e.load(x + r * p.x_row + b * 8);
+        e.values(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t a = __float_as_uint(v[j]) & 0x7fffffffu;
-        if (a < 0x7f800000u) mx = max(mx, a);
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t a = __float_as_uint(v[j]) & 0x7fffffffu;
+          if (a < 0x7f800000u) mx = max(mx, a);
+        }
       }
+      mx = __reduce_max_sync(0xffffffffu, mx);
     }
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    __syncwarp();
-    if (lane == 0) s_max[r] = mx;
+    const int e = mx ? max(-126, min(126, 14 - ilogbf(__uint_as_float(mx)))) : 0;
+    if (lane == 0) s_to[r] = ldexpf(1.f, e), s_back[r] = ldexpf(1.f, -e);
   }
   __syncthreads();
-  auto exponent = [&](int r) {                             // of the power of two that a row is multiplied by
-    const float mx = __uint_as_float(s_max[r]);
-    return mx > 0.f ? max(-126, min(126, 14 - ilogbf(mx))) : 0;
-  };
   auto stage = [&](int i, const Eight<T> &e) {
     const int r = p.eighths.quotient(i), b = i - r * eighths;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (b < last) e.values(v);
-    const float f = ldexpf(1.f, exponent(r));
+    const float f = s_to[r];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= f;
     unsigned char *to = xs + r * TERMS * p.pitch + L::staged(b) * 16;
@@ -305,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int m = (c * 8 + 2 * t + j) / TERMS;
-      back[c][j] = m < mr ? ldexpf(1.f, -exponent(m)) : 0.f;
+      back[c][j] = m < mr ? s_back[m] : 0.f;
     }
   }
 
@@ -333,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
       }
     const int e0 = (b0 + blk) * (kBlock / 8);
     float acc[RT][NT][4];
+    uint32_t pair[RT][2], zeros[RT][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {                          // words; a group ends with every (4 / GB)th
       uint4 b[NT];
@@ -342,14 +356,16 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
       const bool fresh = i % (4 / GB) == 0, done = (i + 1) % (4 / GB) == 0;
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        uint32_t a[2][4], s[2];
+        uint32_t a[2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          if (i == 0 && ZEROS) zeros[r][h] = __shfl_sync(0xffffffffu, sc.zeros, 16 * r + 8 * h + g) & 0x0f0f0f0fu;
+          if (done && grp % 2 == 0) pair[r][h] = __shfl_sync(0xffffffffu, sc.pair[grp / 2], 16 * r + 8 * h + g);
           uint32_t low = 0xe408e408u, high = 0xd480d480u;  // -(1024 + zero) and -(64 + zero), twice
-          if (ZEROS || done) s[h] = __shfl_sync(0xffffffffu, sc.v[r][grp >> 1], (grp & 1) * 16 + 8 * h + g);
           if (ZEROS) {
-            low = (0xe400u | (s[h] >> 16)) * 0x10001u;
-            high = (0xd400u | (s[h] >> 16 << 4)) * 0x10001u;
+            const uint32_t z = __byte_perm(zeros[r][h], 0, 0x4040 | grp * 0x0101);
+            low = z | 0xe400e400u;
+            high = z * 16 + 0xd400d400u;
           }
           const uint32_t x0 = v[r][h][i], x1 = x0 >> 8;
           a[0][h] = add_half2((x0 & 0x000f000fu) | 0x64006400u, low);
@@ -364,14 +380,13 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
           mkw::mma(mkw::FP16Op{}, acc[r][c], a[1], b[c].z, b[c].w);
         }
         if (done) {
-          const float s0 = __uint_as_float(s[0] << 16), s1 = __uint_as_float(s[1] << 16);
+          float s[2];
 #pragma unroll
-          for (int c = 0; c < NT; ++c) {
-            sum[r][c][0] += s0 * acc[r][c][0];
-            sum[r][c][1] += s0 * acc[r][c][1];
-            sum[r][c][2] += s1 * acc[r][c][2];
-            sum[r][c][3] += s1 * acc[r][c][3];
-          }
+          for (int h = 0; h < 2; ++h) s[h] = __uint_as_float(grp % 2 ? pair[r][h] & 0xffff0000u : pair[r][h] << 16);
+#pragma unroll
+          for (int c = 0; c < NT; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[r][c][j] += s[j / 2] * acc[r][c][j];
         }
       }
     }
@@ -465,6 +480,9 @@ int launch(Q4Params p, int sms, int dev, cudaStream_t s) {
   }
   p.tiles = (p.n + 16 * RT - 1) / (16 * RT);
   p.pitch = p.blocks * kBlock * 2 + Layout<G>::pad;
+  constexpr int per = kBlock / G;
+  p.vec = p.groups % per == 0 && reinterpret_cast<uintptr_t>(p.scales) % (2 * per) == 0 &&
+          reinterpret_cast<uintptr_t>(p.zeros) % per == 0;
   // the sharing of k that leaves the busiest warp the fewest blocks, fewer warps a tile where that is equal
   int64_t best = 0;
   for (int wk = 1; wk <= kWarps; wk *= 2) {

@@ -23,6 +23,7 @@ struct Q4Params {
   int wk;               // warps that share a tile's k: 1, 2, 4, 8 or 16
   int tiles;            // tiles of 16 RT rows
   int pitch;            // bytes from staged column to column
+  int vec;              // a block's scales (and zeros) of a row can be loaded at once
 };
 
 // launch for x of one type (group: codes a scale)
