@@ -120,6 +120,13 @@ __device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+// four bits of each half of x, in the place of `mask`, as the low mantissa bits of 1024 in fp16: one operation
+__device__ __forceinline__ uint32_t take_codes(uint32_t x, uint32_t mask) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "r"(mask), "r"(0x64006400u));
+  return r;
+}
+
 template <class T, int NT, int RT, int G, bool ZEROS>
 __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_constant__ Q4Params p) {
   using L = Layout<G>;
@@ -368,10 +375,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
             high = z * 16 + 0xd400d400u;
           }
           const uint32_t x0 = v[r][h][i], x1 = x0 >> 8;
-          a[0][h] = add_half2((x0 & 0x000f000fu) | 0x64006400u, low);
-          a[0][2 + h] = fma_half2((x0 & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, high);
-          a[1][h] = add_half2((x1 & 0x000f000fu) | 0x64006400u, low);
-          a[1][2 + h] = fma_half2((x1 & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, high);
+          a[0][h] = add_half2(take_codes(x0, 0x000f000fu), low);
+          a[0][2 + h] = fma_half2(take_codes(x0, 0x00f000f0u), 0x2c002c00u, high);
+          a[1][h] = add_half2(take_codes(x1, 0x000f000fu), low);
+          a[1][2 + h] = fma_half2(take_codes(x1, 0x00f000f0u), 0x2c002c00u, high);
         }
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
