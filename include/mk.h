@@ -453,7 +453,7 @@ int mk_export_kv(mk_handle *h, int32_t layer, int32_t first, int32_t count, cons
  * zeros 0 .. 15; byte k / 2 of a row holds code k in its low four bits when k is
  * even, in its high four when k is odd. */
 typedef struct {
-  int32_t m, n, k;             /* y [m][n] = x [m][k] w[n][k]^T; m or n 0 is a no-op; k <= 20480 */
+  int32_t m, n, k;             /* y [m][n] = x [m][k] w[n][k]^T; m or n 0 is a no-op; k <= 32768 */
   int32_t group;               /* 32, 64 or a multiple of 128 that divides k */
   int32_t dtype;               /* of x, residual and y: MK_F32 or MK_BF16 */
   const void *x;               /* device [m][k] */

@@ -5,7 +5,7 @@
 
 namespace mkq {
 
-constexpr int kMaxK = 20480;           // an fp32 row's two columns of this length still fit
+constexpr int kMaxK = 32768;           // an fp32 row's two columns of this length still fit
 
 int run_f32(Q4Params &p, int group, int sms, int dev, cudaStream_t s) { return run<float>(p, group, sms, dev, s); }
 

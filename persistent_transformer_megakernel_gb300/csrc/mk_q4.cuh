@@ -44,7 +44,7 @@
 namespace mkq {
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps, kBlock = 128;
-constexpr int kRing = 8192;            // bytes of codes a warp has room for: 8 blocks of 16 rows
+constexpr int kRing = 4096;            // bytes of codes a warp has room for: 4 blocks of 16 rows (twice as many measured slower)
 constexpr int kMaxSmem = 225 * 1024;   // dynamic shared memory of a CTA
 constexpr int red_bytes(int nt, int rt) { return kWarps * 16 * rt * 8 * nt * 4; }   // sums of the warps
 

@@ -65,7 +65,7 @@ def test_many_rounds_of_tiles(x):
 
 @pytest.mark.parametrize("m,x", [(1, F32), (2, F32), (7, BF16)])
 def test_the_longest_rows(m, x):
-    _run(m, 40, 20480, 128, x, seed=3)                      # fp32: one x row a pass
+    _run(m, 40, 32768, 128, x, seed=3)                      # fp32: one x row a pass
 
 
 def test_strides_and_residual_in_place():

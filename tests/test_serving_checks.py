@@ -207,7 +207,7 @@ def test_argument_errors_of_the_c_entry_points():
     for f in (dict(m=-1), dict(n=-1), dict(k=0), dict(group=0), dict(group=96), dict(dtype=2), dict(m=1, x=None), dict(m=1, x=8),
               dict(m=1, codes=24), dict(m=1, scales=None), dict(m=1, y=None), dict(m=1, x_row=130), dict(m=1, y_row=-1)):
         assert mv(**f) == -1, f
-    assert mv(group=16) == -2 and mv(group=128, k=32768) == -2 and mv(k=192, group=192) == -2
+    assert mv(group=16) == -2 and mv(group=128, k=32896) == -2 and mv(k=192, group=192) == -2
     assert lib.mk_export_kv(None, 0, 0, 0, None, 0, 0, None) == -1
 
 
