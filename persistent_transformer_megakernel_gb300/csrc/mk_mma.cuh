@@ -123,9 +123,16 @@ __device__ __forceinline__ uint32_t take_input_term(FP16Op, float &x, float &y) 
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// the lower terms of a value times an infinity must not make NaN of it: a remainder of zero becomes a tiny one of the
-// value's sign
-__device__ __forceinline__ float signed_rest(float rest, float value) { return copysignf(fmaxf(fabsf(rest), 0x1p-120f), value); }
+// a term, not the last, of a value that may meet an infinity: what remains is never zero (an infinity times it would be
+// NaN) but of the value's sign, and tiny where nothing remains
+__device__ __forceinline__ uint32_t take_query_term(BF16Op, float &x, float &y) {
+  const uint32_t a = __float_as_uint(x) & 0xffff0000u, b = __float_as_uint(y) & 0xffff0000u;
+  const float tx = __uint_as_float((a & 0x80000000u) | 0x03800000u), ty = __uint_as_float((b & 0x80000000u) | 0x03800000u);
+  x = x == __uint_as_float(a) ? tx : x - __uint_as_float(a);
+  y = y == __uint_as_float(b) ? ty : y - __uint_as_float(b);
+  return __byte_perm(a, b, 0x7632);
+}
+__device__ __forceinline__ uint32_t take_query_term(FP16Op op, float &x, float &y) { return take_input_term(op, x, y); }
 // a term of probabilities (>= 0), not the last: by truncation, so that no remainder is negative
 __device__ __forceinline__ uint32_t take_weight_term(BF16Op, float &x, float &y) {
   const uint32_t a = __float_as_uint(x) & 0xffff0000u, b = __float_as_uint(y) & 0xffff0000u;
@@ -151,16 +158,14 @@ __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontr
 __device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // a cluster's CTAs: all their threads meet, shared memory written before is seen after
-__device__ __forceinline__ void cluster_meet() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// a float of the shared memory of the cluster's CTA `rank`, at the place of `p` in this one
-__device__ __forceinline__ float load_remote(const float *p, int rank) {
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// the shared memory of the cluster's CTA `rank` at the place of `p` in this one, and a store there
+__device__ __forceinline__ uint32_t remote(const void *p, int rank) {
   uint32_t a;
-  float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
+  return a;
 }
+__device__ __forceinline__ void store_remote(uint32_t at, float x) { asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory"); }
 
 }  // namespace mkw

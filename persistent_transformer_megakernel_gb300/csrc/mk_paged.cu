@@ -345,7 +345,7 @@ struct AttnParams {
   float *parts;        // [grid][2][gr][D + 4]: a row's middle or end (0) and its beginning (1)
   mkw::Divisor page_size;
   int n, hq, hkv, group, n_pages, capacity, window;   // capacity: slots of a table row
-  int blocks, vh;      // head blocks of 16 query heads a kv head, virtual heads hkv * blocks
+  mkw::Divisor blocks, vh;   // head blocks of 16 query heads a kv head, virtual heads hkv * blocks
   int gr;              // query heads of a block: min(group, 16)
   int stages;
   int way, cluster;
@@ -366,11 +366,23 @@ struct Tile {
   static constexpr int ROWS = 32 / CPR, COPIES = POS / ROWS, TURNS = ROWB == 256 ? 4 : ROWB == 128 ? 2 : 1;
 };
 
-__device__ __forceinline__ float2 load_pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
-__device__ __forceinline__ float2 load_pair(const __nv_bfloat16 *p) {
-  const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
-  return make_float2(bf16_lo(w), bf16_hi(w));
-}
+// two elements as they are in memory, and their values
+template <class T>
+struct Pair;
+template <>
+struct Pair<float> {
+  using type = float2;
+  static __device__ __forceinline__ type load(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+  static __device__ __forceinline__ type none() { return make_float2(0.f, 0.f); }
+  static __device__ __forceinline__ float2 values(type x) { return x; }
+};
+template <>
+struct Pair<__nv_bfloat16> {
+  using type = uint32_t;
+  static __device__ __forceinline__ type load(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint32_t *>(p); }
+  static __device__ __forceinline__ type none() { return 0u; }
+  static __device__ __forceinline__ float2 values(type w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+};
 __device__ __forceinline__ void store_one(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store_one(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
@@ -416,17 +428,70 @@ constexpr int kPartStride = D + 4;      // o[D], m, l
 // the join of parts (m_j, l_j, o_j): m = max m_j, weights 2^(m_j - m)
 __device__ __forceinline__ float join_base(float m) { return m == -INFINITY ? 0.f : m; }
 
-// o / l and the log-sum-exp of one finished element
-template <class T>
-__device__ __forceinline__ void write_out(const AttnParams &p, int row, int head, int d, float o, float l, float vs) {
-  const float r = l == 0.f ? 0.f : 1.0f / l;
-  store_one(static_cast<T *>(p.out) + row * p.out_row + head * p.out_head + d, o * r * vs);
-}
 __device__ __forceinline__ void write_lse(const AttnParams &p, int row, int head, float m, float l) {
   if (p.lse) p.lse[static_cast<int64_t>(row) * p.hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-__device__ __forceinline__ int kvh_of(const AttnParams &p, int vh) { return vh / p.blocks; }
+// a virtual head's kv head, first query head and number of query heads
+struct Heads {
+  int kvh, first, count;
+};
+__device__ __forceinline__ Heads heads_of(const AttnParams &p, int vh) {
+  Heads h;
+  h.kvh = p.blocks.quotient(vh);
+  const int blk = vh - h.kvh * static_cast<int>(p.blocks.value);
+  h.first = h.kvh * p.group + blk * 16;
+  h.count = min(16, p.group - blk * 16);
+  return h;
+}
+
+// Join n <= 32 parts of a query head, in order, by a warp: lane l gets elements l D / 32 ..; at(j) is the jth part's
+// o[D], m, l, or null.
+template <int D, class At>
+__device__ __forceinline__ void join_parts(int lane, int n, At at, float &m, float &l, float (&x)[D / 32]) {
+  const float *mine = lane < n ? at(lane) : nullptr;
+  const unsigned there = __ballot_sync(0xffffffffu, mine != nullptr);
+  const float mj = mine ? mine[D] : -INFINITY, lj = mine ? mine[D + 1] : 0.f;
+  m = mj;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float f = mkw::exp2_fast(mj - join_base(m));
+  l = mine ? f * lj : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) x[k] = 0.f;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const float fj = __shfl_sync(0xffffffffu, f, j);
+    if (!(there >> j & 1)) continue;
+    const float *part = at(j) + lane * (D / 32);
+    if constexpr (D == 128) {
+      const float4 v = *reinterpret_cast<const float4 *>(part);
+      x[0] += fj * v.x, x[1] += fj * v.y, x[2] += fj * v.z, x[3] += fj * v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2 *>(part);
+      x[0] += fj * v.x, x[1] += fj * v.y;
+    }
+  }
+}
+
+__device__ __forceinline__ void store_row(float *p, const float (&x)[4]) { *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]); }
+__device__ __forceinline__ void store_row(float *p, const float (&x)[2]) { *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]); }
+__device__ __forceinline__ void store_row(__nv_bfloat16 *p, const float (&x)[4]) {
+  *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+}
+__device__ __forceinline__ void store_row(__nv_bfloat16 *p, const float (&x)[2]) { *reinterpret_cast<uint32_t *>(p) = pack_bf16(x[0], x[1]); }
+
+// a joined query head: o / l and the log-sum-exp
+template <class T, int D>
+__device__ __forceinline__ void write_head(const AttnParams &p, int lane, int row, int head, float m, float l, float (&x)[D / 32], float vs) {
+  const float r = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) x[k] *= r * vs;
+  store_row(static_cast<T *>(p.out) + row * p.out_row + head * p.out_head + lane * (D / 32), x);
+  if (lane == 0) write_lse(p, row, head, m, l);
+}
 
 // over the 8 rows of a column of a product: lanes with the same t
 __device__ __forceinline__ float column_max(float x) {
@@ -464,6 +529,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
   Span sp{0, 0, 0, 0};
   int per = 0, units = 0, ctas = 0;
   if (p.way == kByCluster) {
+    mkw::cluster_arrive();                                   // (to be waited for before the others' memory is written)
     vh = cta / p.cluster;                                    // the cluster's kv head (and head block)
     sp = span_of<POS>(p, p.lengths[0]);
     const int i = cta % p.cluster * kWarps + w;
@@ -495,17 +561,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
     }
     s_scan[tid] = before + incl - mine;                      // cost of the rows before this thread's
     __syncthreads();
-    units = total * p.vh;
+    units = total * static_cast<int>(p.vh.value);
     ctas = max(1, min(static_cast<int>(gridDim.x), (units - 1) / kMinUnitsPerCta + 1));
 
     // the row and head that has unit u, and where in it u is
     auto find = [&](int u, int &f_row, int &f_vh, Span &f_sp) {
-      const int x = u / p.vh;                                // in [before(row), before(row) + cost(row))
-      int a = 0, b = kAttnThreads;
-      while (b - a > 1) {
-        const int m = (a + b) >> 1;
-        if (s_scan[m] <= x) a = m; else b = m;
-      }
+      const int x = p.vh.quotient(u);                        // in [before(row), before(row) + cost(row))
+      // the last of the 256 sums that is not above x: of every eighth, then of eight
+      int a = __popc(__ballot_sync(0xffffffffu, s_scan[8 * lane] <= x)) * 8 - 8;
+      a += __popc(__ballot_sync(0xffffffffu, lane < 8 && s_scan[a + (lane & 7)] <= x)) - 1;
       int at = s_scan[a];
       f_row = a * per;
       f_sp = span_of<POS>(p, p.lengths[f_row]);
@@ -513,7 +577,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
         at += f_sp.cost();
         f_sp = span_of<POS>(p, p.lengths[++f_row]);
       }
-      const int rest = u - at * p.vh;
+      const int rest = u - at * static_cast<int>(p.vh.value);
       f_vh = rest / f_sp.cost();
       return rest - f_vh * f_sp.cost();
     };
@@ -548,7 +612,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
   const int64_t to_v = static_cast<const unsigned char *>(p.v) - k_base;
 
   // the producer's place besides row, vh, tile: its kv head and block, this lane's slot in its page and that page
-  int kvh = vh / p.blocks, blk = vh - kvh * p.blocks, slot = 0, page = -1;
+  int kvh = p.blocks.quotient(vh), blk = vh - kvh * static_cast<int>(p.blocks.value), slot = 0, page = -1;
   auto look_up = [&]() {
     const int pos = (sp.first + tile) * POS + lane, col = p.page_size.quotient(pos);
     slot = pos - col * static_cast<int>(p.page_size.value);
@@ -598,8 +662,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
       left -= kRowCost;
       tile = 0;
       ++vh;
-      if (++blk == p.blocks) blk = 0, ++kvh;
-      if (vh == p.vh) {
+      if (++blk == static_cast<int>(p.blocks.value)) blk = 0, ++kvh;
+      if (vh == static_cast<int>(p.vh.value)) {
         vh = kvh = 0;
         if (left > 0) {
           do sp = span_of<POS>(p, p.lengths[++row]);
@@ -615,7 +679,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
     }
     if (++in_stage == p.stages) in_stage = 0;
   };
+  // ---- a row's query heads as they are in memory: asked for before the tiles, else their answer waits behind those ----
+  // columns: heads 8 hb + g in the query's fragments, 8 hb + 2t and 2t + 1 in scores, states and outputs
+  typename Pair<T>::type raw[KS][HB][2];
+  auto load_query = [&](int q_row, int q_vh) {
+    const Heads h = heads_of(p, q_vh);
+    const T *q = static_cast<const T *>(p.q) + q_row * p.q_row + (h.first + g) * p.q_head;
+#pragma unroll
+    for (int hb = 0; hb < HB; ++hb)
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        // bf16: k = 2t, 2t+1, 2t+8, 2t+9 of the step; e4m3: 4t .. 4t+3, as the key's 16-bit pairs hold them
+        const int d0 = 16 * s + (FP8 ? 4 * t : 2 * t), d1 = d0 + (FP8 ? 2 : 8);
+        const bool there = 8 * hb + g < h.count;
+        raw[s][hb][0] = there ? Pair<T>::load(q + 8 * hb * p.q_head + d0) : Pair<T>::none();
+        raw[s][hb][1] = there ? Pair<T>::load(q + 8 * hb * p.q_head + d1) : Pair<T>::none();
+      }
+  };
+  // (16 heads of 128 fp32 elements have no registers to wait in)
+  constexpr bool EARLY = !(F32 && HB == 2 && D == 128);
   const bool any = left > 0;
+  if (EARLY && any) load_query(row, vh);
   for (int i = 0; i < p.stages - 1; ++i) {
     if (left > 0) produce();
     mkw::cp_async_commit();
@@ -634,7 +718,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
   }
 
   // ---- the warp's tiles ---------------------------------------------------------
-  // columns: heads 8 hb + g in the query's fragments, 8 hb + 2t and 2t + 1 in scores, states and outputs
   uint32_t qf[TQ][KS][HB][2];
   float o[DB][HB][4], m[HB][2], l[HB][2], mult[HB][2];
   int rows = 0, head0 = 0, begins = 0;
@@ -654,23 +737,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
 
     if (start) {                                             // a row's query heads
       start = false;
-      const int q_kvh = kvh_of(p, ti.vh), q_blk = ti.vh - q_kvh * p.blocks;
-      head0 = q_kvh * p.group + q_blk * 16;
-      rows = min(8 * HB, p.group - q_blk * 16);
+      if (!EARLY) load_query(ti.row, ti.vh);
+      const Heads h = heads_of(p, ti.vh);
+      head0 = h.first;
+      rows = h.count;
       begins = ti.flags & kFirst;
-      const float to_log2 = p.scale * 1.4426950408889634f * (FP8 && p.k_scale ? p.k_scale[q_kvh] : 1.f);
+      const float to_log2 = p.scale * 1.4426950408889634f * (FP8 && p.k_scale ? p.k_scale[h.kvh] : 1.f);
 #pragma unroll
       for (int hb = 0; hb < HB; ++hb) {
-        const int h = 8 * hb + g;
-        const T *q = static_cast<const T *>(p.q) + ti.row * p.q_row + (head0 + h) * p.q_head;
         float2 x[KS][2];
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          // bf16: k = 2t, 2t+1, 2t+8, 2t+9 of the step; e4m3: 4t .. 4t+3, as the key's 16-bit pairs hold them
-          const int d0 = 16 * s + (FP8 ? 4 * t : 2 * t), d1 = d0 + (FP8 ? 2 : 8);
-          x[s][0] = x[s][1] = make_float2(0.f, 0.f);
-          if (h < rows) x[s][0] = load_pair(q + d0), x[s][1] = load_pair(q + d1);
-        }
+        for (int s = 0; s < KS; ++s) x[s][0] = Pair<T>::values(raw[s][hb][0]), x[s][1] = Pair<T>::values(raw[s][hb][1]);
         mult[hb][0] = mult[hb][1] = to_log2;
         if constexpr (FP8) {
           float a = 0.f;
@@ -692,14 +769,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int u = 0; u < TQ; ++u) {
-              const float2 whole = x[s][j];
-              qf[u][s][hb][j] = mkw::take_input_term(Op{}, x[s][j].x, x[s][j].y);
-              if (!FP8 && u + 1 < TQ) {
-                x[s][j].x = mkw::signed_rest(x[s][j].x, whole.x);
-                x[s][j].y = mkw::signed_rest(x[s][j].y, whole.y);
-              }
-            }
+            for (int u = 0; u < TQ; ++u)
+              qf[u][s][hb][j] = u + 1 < TQ ? mkw::take_query_term(Op{}, x[s][j].x, x[s][j].y) : mkw::take_input_term(Op{}, x[s][j].x, x[s][j].y);
 #pragma unroll
         for (int c = 0; c < DB; ++c) o[c][hb][0] = o[c][hb][1] = o[c][hb][2] = o[c][hb][3] = 0.f;
         m[hb][0] = m[hb][1] = -INFINITY;
@@ -841,7 +912,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
       // (a cluster's parts are joined at the end, whole rows among them)
       const bool whole = begins && ends && p.way != kByCluster;
       float *part = ends ? first_part : last_part;
-      const float vsc = FP8 && p.v_scale ? p.v_scale[kvh_of(p, ti.vh)] : 1.f;
+      const float vsc = FP8 && p.v_scale ? p.v_scale[heads_of(p, ti.vh).kvh] : 1.f;
 #pragma unroll
       for (int hb = 0; hb < HB; ++hb)
 #pragma unroll
@@ -870,174 +941,115 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
           }
         }
       if (!whole && lane == 0) s_part[2 * w + (ends ? 0 : 1)] = PartInfo{ti.row, ti.vh, begins, ends};
+      if (EARLY && more) load_query(s_tile[w][stage].row, s_tile[w][stage].vh);   // (the next tile has been asked for, and written down)
     }
   }
   mkw::cp_async_wait<0>();
   if (p.way == kJoined && tid == 0) p.records[cta] = make_int4(0, 0, 0, 0);
   __syncthreads();
 
-  // ---- join the warps' parts, in order ---------------------------------------
+  // ---- join the warps' parts, in order, a query head of a row a warp -----------------------------------------
   // where the jth part is: the ring of its warp (a part that does not end its row), or the space beside the rings
   auto part_at = [&](int j) {
-    return reinterpret_cast<float *>((j & 1) ? smem + (j >> 1) * p.stages * TL::STAGE
-                                             : smem + kWarps * p.stages * TL::STAGE + (j >> 1) * p.gr * PST * 4);
+    return reinterpret_cast<const float *>((j & 1) ? smem + (j >> 1) * p.stages * TL::STAGE
+                                                   : smem + kWarps * p.stages * TL::STAGE + (j >> 1) * p.gr * PST * 4);
   };
+  const PartInfo mine = lane < 2 * kWarps ? s_part[lane] : PartInfo{-1, 0, 0, 0};
+  const unsigned valid = __ballot_sync(0xffffffffu, mine.row >= 0);
+  float mx, sum, x[D / 32];
   if (p.way == kByCluster) {
-    // all parts are of one row and head; an empty part weighs nothing
-    if (!sp.count) return;                                   // (every CTA of the cluster alike)
-    const int head0 = kvh_of(p, cta / p.cluster) * p.group + cta / p.cluster % p.blocks * 16;
-    const int nr = min(16, p.group - cta / p.cluster % p.blocks * 16);
-    const float vsc = FP8 && p.v_scale ? p.v_scale[kvh_of(p, cta / p.cluster)] : 1.f;
-    float *mine = reinterpret_cast<float *>(smem + kWarps * (p.stages * TL::STAGE + p.gr * PST * 4));   // [gr][PST]
-    for (int i = tid; i < nr * D; i += kAttnThreads) {
-      const int r = i / D, d = i % D;
-      float mx = -INFINITY, sum = 0.f, x = 0.f;
+    // All parts are of one row and head.  Query head r goes to CTA r % cluster, which joins what all have of it.
+    const int rank = cta % p.cluster;
+    const Heads h = heads_of(p, cta / p.cluster);
+    float *inbox = reinterpret_cast<float *>(smem + kWarps * (p.stages * TL::STAGE + p.gr * PST * 4));   // [CTA][query head / cluster][PST]
+    const int owned = (p.gr + p.cluster - 1) / p.cluster;
+    mkw::cluster_wait();
+    for (int r = w; r < h.count; r += kWarps) {
+      join_parts<D>(lane, 2 * kWarps, [&](int j) { return valid >> j & 1 ? part_at(j) + r * PST : nullptr; }, mx, sum, x);
+      const uint32_t to = mkw::remote(inbox + (rank * owned + r / p.cluster) * PST, r % p.cluster);
 #pragma unroll
-      for (int j = 0; j < 2 * kWarps; ++j)
-        if (s_part[j].row >= 0) mx = fmaxf(mx, part_at(j)[r * PST + D]);
-      const float base = join_base(mx);
-#pragma unroll
-      for (int j = 0; j < 2 * kWarps; ++j)
-        if (s_part[j].row >= 0) {
-          const float *pj = part_at(j) + r * PST, f = mkw::exp2_fast(pj[D] - base);
-          sum += f * pj[D + 1];
-          x += f * pj[d];
-        }
-      mine[r * PST + d] = x;
-      if (d == 0) {
-        mine[r * PST + D] = mx;
-        mine[r * PST + D + 1] = sum;
+      for (int k = 0; k < D / 32; ++k) mkw::store_remote(to + (lane * (D / 32) + k) * 4, x[k]);
+      if (lane == 0) {
+        mkw::store_remote(to + D * 4, mx);
+        mkw::store_remote(to + D * 4 + 4, sum);
       }
     }
-    mkw::cluster_meet();
-    for (int i = cta % p.cluster * kAttnThreads + tid; i < nr * D; i += p.cluster * kAttnThreads) {
-      const int r = i / D, d = i % D;
-      float mx = -INFINITY, sum = 0.f, x = 0.f, m_j[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (j < p.cluster) mx = fmaxf(mx, m_j[j] = mkw::load_remote(mine + r * PST + D, j));
-      const float base = join_base(mx);
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (j < p.cluster) {
-          const float f = mkw::exp2_fast(m_j[j] - base);
-          sum += f * mkw::load_remote(mine + r * PST + D + 1, j);
-          x += f * mkw::load_remote(mine + r * PST + d, j);
-        }
-      write_out<T>(p, 0, head0 + r, d, x, sum, vsc);
-      if (d == 0) write_lse(p, 0, head0 + r, mx, sum);
+    mkw::cluster_arrive();
+    mkw::cluster_wait();
+    if (!sp.count) return;
+    const float vsc = FP8 && p.v_scale ? p.v_scale[h.kvh] : 1.f;
+    for (int i = w; i < owned; i += kWarps) {
+      const int r = i * p.cluster + rank;
+      if (r >= h.count) break;
+      join_parts<D>(lane, p.cluster, [&](int j) { return inbox + (j * owned + i) * PST; }, mx, sum, x);
+      write_head<T, D>(p, lane, 0, h.first + r, mx, sum, x, vsc);
     }
-    mkw::cluster_meet();                                     // the others' shared memory is read until here
     return;
   }
-  for (int a = 0; a < 2 * kWarps;) {
-    const PartInfo pi = s_part[a];
-    if (pi.row < 0) {
-      ++a;
+  // a group: consecutive parts of the same row and head; lane j says whether part j begins one
+  const unsigned below = valid & ((1u << lane) - 1u);
+  const int prev = below ? 31 - __clz(below) : lane;
+  const int prev_row = __shfl_sync(0xffffffffu, mine.row, prev), prev_vh = __shfl_sync(0xffffffffu, mine.vh, prev);
+  const unsigned starts = __ballot_sync(0xffffffffu, mine.row >= 0 && (!below || prev_row != mine.row || prev_vh != mine.vh));
+  const int items = __popc(starts) * p.gr;
+  for (int i = w; i < items; i += kWarps) {
+    const int group = i / p.gr, r = i - group * p.gr;
+    unsigned rest = starts;
+    for (int k = 0; k < group; ++k) rest &= rest - 1u;
+    const int a = __ffs(rest) - 1;                           // the group's first part
+    const unsigned later = starts & ~((2u << a) - 1u), in_group = valid & ~((1u << a) - 1u) & (later ? (later & -later) - 1u : ~0u);
+    const int b = 31 - __clz(in_group);                      // and its last
+    const int row_of = __shfl_sync(0xffffffffu, mine.row, a), vh_of = __shfl_sync(0xffffffffu, mine.vh, a);
+    const int first = __shfl_sync(0xffffffffu, mine.begins, a), ends = __shfl_sync(0xffffffffu, mine.ends, b);
+    const Heads h = heads_of(p, vh_of);
+    if (r >= h.count) continue;
+    join_parts<D>(lane, b - a + 1, [&](int j) { return in_group >> (a + j) & 1 ? part_at(a + j) + r * PST : nullptr; }, mx, sum, x);
+    if (first && ends) {
+      write_head<T, D>(p, lane, row_of, h.first + r, mx, sum, x, FP8 && p.v_scale ? p.v_scale[h.kvh] : 1.f);
       continue;
     }
-    int b = a, ends = pi.ends;
-    for (int j = a + 1; j < 2 * kWarps; ++j) {
-      const PartInfo pj = s_part[j];
-      if (pj.row < 0) continue;
-      if (pj.row != pi.row || pj.vh != pi.vh) break;
-      b = j;
-      ends = pj.ends;
-    }
-    const int head0 = kvh_of(p, pi.vh) * p.group + pi.vh % p.blocks * 16, nr = min(16, p.group - pi.vh % p.blocks * 16);
-    const bool whole = pi.begins && ends;
-    const float vsc = FP8 && p.v_scale ? p.v_scale[kvh_of(p, pi.vh)] : 1.f;
-    float *slot_at = p.parts + (static_cast<int64_t>(cta) * 2 + (pi.begins ? 1 : 0)) * p.gr * PST;
-    for (int i = tid; i < nr * D; i += kAttnThreads) {
-      const int r = i / D, d = i % D;
-      float mx = -INFINITY, sum = 0.f, x = 0.f;
-      for (int j = a; j <= b; ++j)
-        if (s_part[j].row >= 0) mx = fmaxf(mx, part_at(j)[r * PST + D]);
-      const float base = join_base(mx);
-      for (int j = a; j <= b; ++j) {
-        if (s_part[j].row < 0) continue;
-        const float *pj = part_at(j) + r * PST, f = mkw::exp2_fast(pj[D] - base);
-        sum += f * pj[D + 1];
-        x += f * pj[d];
-      }
-      if (whole) {
-        write_out<T>(p, pi.row, head0 + r, d, x, sum, vsc);
-        if (d == 0) write_lse(p, pi.row, head0 + r, mx, sum);
-      } else {
-        slot_at[r * PST + d] = x;
-        if (d == 0) {
-          slot_at[r * PST + D] = mx;
-          slot_at[r * PST + D + 1] = sum;
-        }
+    float *to = p.parts + ((static_cast<int64_t>(cta) * 2 + (first ? 1 : 0)) * p.gr + r) * PST;
+    store_row(to + lane * (D / 32), x);
+    if (lane == 0) {
+      to[D] = mx;
+      to[D + 1] = sum;
+      if (first && r == 0) {
+        // the last CTA with tiles of this row: the one whose range holds the row's last unit
+        int before_row = s_scan[row_of / per];
+        for (int k = row_of / per * per; k < row_of; ++k) before_row += span_of<POS>(p, p.lengths[k]).cost();
+        const int cost = span_of<POS>(p, p.lengths[row_of]).cost();
+        const int last = share_of(units, ctas, before_row * static_cast<int>(p.vh.value) + (vh_of + 1) * cost - 1);
+        p.records[cta] = make_int4(row_of, vh_of, last, 1);
       }
     }
-    if (pi.begins && !ends && tid == 0) {
-      // the last CTA with tiles of this row: the one whose range holds the row's last unit
-      int before_row = s_scan[pi.row / per];
-      for (int r = pi.row / per * per; r < pi.row; ++r) before_row += span_of<POS>(p, p.lengths[r]).cost();
-      const int cost = span_of<POS>(p, p.lengths[pi.row]).cost();
-      const int last = share_of(units, ctas, before_row * p.vh + (pi.vh + 1) * cost - 1);
-      p.records[cta] = make_int4(pi.row, pi.vh, last, 1);
-    }
-    a = b + 1;
   }
 }
 
 // Joins the rows that more than one CTA had a share of: CTA c takes the row that
-// begins in attend_kernel's CTA c and goes on in the next ones.  Four elements a
-// thread; threads left over share the parts.
+// begins in attend_kernel's CTA c and goes on in the next ones, a query head a warp.
 template <class T, int D>
 __global__ void __launch_bounds__(kAttnThreads) join_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int PST = kPartStride<D>, Q = D / 4;
-  __shared__ float s_m[kAttnThreads], s_l[kAttnThreads];
-  __shared__ float4 s_x[kAttnThreads];
+  constexpr int PST = kPartStride<D>;
+  const int cta = blockIdx.x, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   mkw::wait_previous_kernel();
-  const int cta = blockIdx.x;
   const int4 rec = p.records[cta];
   if (!rec.w) return;
-  const int head0 = kvh_of(p, rec.y) * p.group + rec.y % p.blocks * 16, nr = min(16, p.group - rec.y % p.blocks * 16);
-  const float vsc = p.v_scale ? p.v_scale[kvh_of(p, rec.y)] : 1.f;
-  const int n = rec.z - cta + 1, rows = kAttnThreads / Q;    // query heads at a time
-  const int shares = max(1, rows / nr), share = threadIdx.x / Q / nr;
-  const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int r0 = 0; r0 < nr; r0 += rows) {
-    const int r = r0 + threadIdx.x / Q % nr, q = threadIdx.x % Q;
-    const bool live = share < shares && r < nr;
-    float m = -INFINITY, l = 0.f;
-    float4 x = none;
-    if (live) {
-#pragma unroll 4
-      for (int j = share; j < n; j += shares) {
-        const float *part = p.parts + (static_cast<int64_t>(cta + j) * 2 + (j == 0 ? 1 : 0)) * p.gr * PST + r * PST;
-        const float4 v = *reinterpret_cast<const float4 *>(part + 4 * q);
-        const float mj = part[D], lj = part[D + 1], mx = fmaxf(m, mj), base = join_base(mx);
-        const float f = mkw::exp2_fast(m - base), fj = mkw::exp2_fast(mj - base);
-        m = mx;
-        l = l * f + lj * fj;
-        x = make_float4(x.x * f + v.x * fj, x.y * f + v.y * fj, x.z * f + v.z * fj, x.w * f + v.w * fj);
-      }
+  const Heads h = heads_of(p, rec.y);
+  const float vsc = p.v_scale ? p.v_scale[h.kvh] : 1.f;
+  const int n = rec.z - cta + 1;
+  for (int r = w; r < h.count; r += kWarps) {
+    float m = -INFINITY, l = 0.f, x[D / 32] = {};
+    for (int j0 = 0; j0 < n; j0 += 32) {
+      float mj, lj, xj[D / 32];
+      join_parts<D>(lane, min(32, n - j0),
+                    [&](int j) { return p.parts + ((static_cast<int64_t>(cta + j0 + j) * 2 + (j0 + j == 0 ? 1 : 0)) * p.gr + r) * PST; }, mj, lj, xj);
+      const float mx = fmaxf(m, mj), base = join_base(mx), f = mkw::exp2_fast(m - base), fj = mkw::exp2_fast(mj - base);
+      m = mx;
+      l = l * f + lj * fj;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) x[k] = x[k] * f + xj[k] * fj;
     }
-    s_m[threadIdx.x] = m;
-    s_l[threadIdx.x] = l;
-    s_x[threadIdx.x] = x;
-    __syncthreads();
-    if (live && share == 0) {
-      for (int s = 1; s < shares; ++s) {
-        const int o = threadIdx.x + s * nr * Q;
-        const float mj = s_m[o], mx = fmaxf(m, mj), base = join_base(mx);
-        const float f = mkw::exp2_fast(m - base), fj = mkw::exp2_fast(mj - base);
-        const float4 v = s_x[o];
-        m = mx;
-        l = l * f + s_l[o] * fj;
-        x = make_float4(x.x * f + v.x * fj, x.y * f + v.y * fj, x.z * f + v.z * fj, x.w * f + v.w * fj);
-      }
-      write_out<T>(p, rec.x, head0 + r, 4 * q, x.x, l, vsc);
-      write_out<T>(p, rec.x, head0 + r, 4 * q + 1, x.y, l, vsc);
-      write_out<T>(p, rec.x, head0 + r, 4 * q + 2, x.z, l, vsc);
-      write_out<T>(p, rec.x, head0 + r, 4 * q + 3, x.w, l, vsc);
-      if (q == 0) write_lse(p, rec.x, head0 + r, m, l);
-    }
-    __syncthreads();
+    write_head<T, D>(p, lane, rec.x, h.first + r, m, l, x, vsc);
   }
 }
 
@@ -1101,15 +1113,16 @@ int launch_heads(AttnParams &p, int grid, int dev, cudaStream_t s) {
   p.cluster = 1;
   if (p.n == 1) {
     // the largest clusters of which there is one for each head at once, as long as their warps have a tile each
-    for (int i = 0; i < 4 && p.vh <= r.clusters[i] && (i == 0 || tiles > p.cluster * kWarps); ++i) p.cluster = 2 << i;
+    for (int i = 0; i < 4 && static_cast<int>(p.vh.value) <= r.clusters[i] && (i == 0 || tiles > p.cluster * kWarps); ++i) p.cluster = 2 << i;
     if (p.cluster > 1) p.way = kByCluster;
   }
   // three stages of the ring where the parts leave room for them (every group of up to 8 query heads)
-  const int parts = (kWarps + (p.way == kByCluster ? 1 : 0)) * p.gr * kPartStride<D> * 4;
+  const int inbox = p.way == kByCluster ? p.cluster * ((p.gr + p.cluster - 1) / p.cluster) : 0;
+  const int parts = (kWarps * p.gr + inbox) * kPartStride<D> * 4;
   p.stages = kWarps * 3 * TL::STAGE + parts <= kMaxSmem ? 3 : 2;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
-  cfg.gridDim = dim3(p.way == kByCluster ? p.vh * p.cluster : grid);
+  cfg.gridDim = dim3(p.way == kByCluster ? static_cast<int>(p.vh.value) * p.cluster : grid);
   cfg.blockDim = dim3(kAttnThreads);
   cfg.dynamicSmemBytes = kWarps * p.stages * TL::STAGE + parts;
   cfg.stream = s;
@@ -1287,8 +1300,8 @@ extern "C" int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args
   p.n_pages = kv->n_pages;
   p.page_size.set(kv->page_size);
   p.window = a->window;
-  p.blocks = (p.group + 15) / 16;
-  p.vh = p.hkv * p.blocks;
+  p.blocks.set((p.group + 15) / 16);
+  p.vh.set(p.hkv * ((p.group + 15) / 16));
   p.gr = std::min(p.group, 16);
   p.scale = a->scale;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
