@@ -401,15 +401,16 @@ __device__ __forceinline__ Span span_of(const AttnParams &p, int len) {
   return s;
 }
 
-// the ith of `parts` shares of `total`, as equal as whole numbers are: its beginning, and the share that has unit u
-__device__ __forceinline__ int share_begin(int total, int parts, int i) {
-  const int q = total / parts, r = total - q * parts;
-  return i * q + min(i, r);
-}
-__device__ __forceinline__ int share_of(int total, int parts, int u) {
-  const int q = total / parts, r = total - q * parts, big = r * (q + 1);
-  return u < big ? u / (q + 1) : r + (u - big) / q;
-}
+// `total` in equal shares, as equal as whole numbers are: where the ith begins, and which one has unit u
+struct Shares {
+  int each, more;   // units of a share, and how many of the first have one more
+  __device__ __forceinline__ Shares(int total, int parts) : each(total / parts), more(total - each * parts) {}
+  __device__ __forceinline__ int begin(int i) const { return i * each + min(i, more); }
+  __device__ __forceinline__ int of(int u) const {
+    const int big = more * (each + 1);
+    return u < big ? u / (each + 1) : more + (u - big) / each;
+  }
+};
 
 // what the ring's reader needs to know of a tile
 struct TileInfo {
@@ -445,13 +446,13 @@ __device__ __forceinline__ Heads heads_of(const AttnParams &p, int vh) {
   return h;
 }
 
-// Join n <= 32 parts of a query head, in order, by a warp: lane l gets elements l D / 32 ..; at(j) is the jth part's
-// o[D], m, l, or null.
-template <int D, class At>
-__device__ __forceinline__ void join_parts(int lane, int n, At at, float &m, float &l, float (&x)[D / 32]) {
-  const float *mine = lane < n ? at(lane) : nullptr;
-  const unsigned there = __ballot_sync(0xffffffffu, mine != nullptr);
-  const float mj = mine ? mine[D] : -INFINITY, lj = mine ? mine[D + 1] : 0.f;
+// Join parts of a query head, in order, by a warp: lane l gets elements l D / 32 ..; lane j of `there` knows where its
+// part's o[D], m, l are, in bytes from `base`.
+template <int D>
+__device__ __forceinline__ void join_parts(int lane, unsigned there, const void *base, int mine_at, float &m, float &l, float (&x)[D / 32]) {
+  auto at = [&](int bytes) { return reinterpret_cast<const float *>(static_cast<const unsigned char *>(base) + bytes); };
+  const bool mine = there >> lane & 1;
+  const float mj = mine ? at(mine_at)[D] : -INFINITY, lj = mine ? at(mine_at)[D + 1] : 0.f;
   m = mj;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -461,11 +462,11 @@ __device__ __forceinline__ void join_parts(int lane, int n, At at, float &m, flo
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) x[k] = 0.f;
-#pragma unroll 4
-  for (int j = 0; j < n; ++j) {
+#pragma unroll 2
+  for (unsigned rest = there; rest; rest &= rest - 1u) {
+    const int j = __ffs(rest) - 1;
     const float fj = __shfl_sync(0xffffffffu, f, j);
-    if (!(there >> j & 1)) continue;
-    const float *part = at(j) + lane * (D / 32);
+    const float *part = at(__shfl_sync(0xffffffffu, mine_at, j)) + lane * (D / 32);
     if constexpr (D == 128) {
       const float4 v = *reinterpret_cast<const float4 *>(part);
       x[0] += fj * v.x, x[1] += fj * v.y, x[2] += fj * v.z, x[3] += fj * v.w;
@@ -533,8 +534,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
     vh = cta / p.cluster;                                    // the cluster's kv head (and head block)
     sp = span_of<POS>(p, p.lengths[0]);
     const int i = cta % p.cluster * kWarps + w;
-    tile = share_begin(sp.count, p.cluster * kWarps, i);
-    left = share_begin(sp.count, p.cluster * kWarps, i + 1) - tile;
+    const Shares shares(sp.count, p.cluster * kWarps);
+    tile = shares.begin(i);
+    left = shares.begin(i + 1) - tile;
     __syncthreads();
   } else {
     // Units: a row and head of cost c covers c of them, tile j the (kRowCost + j)th.  A warp has the tiles whose unit
@@ -564,46 +566,45 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
     units = total * static_cast<int>(p.vh.value);
     ctas = max(1, min(static_cast<int>(gridDim.x), (units - 1) / kMinUnitsPerCta + 1));
 
-    // the row and head that has unit u, and where in it u is
-    auto find = [&](int u, int &f_row, int &f_vh, Span &f_sp) {
+    // The row and head that has a unit, and where in it that is: for where the CTA's range begins and ends, if these are
+    // moved to where a row and head begins, then for the warp's beginning.
+    int c_begin = 0, c_end = 0, begin = 0;
+    if (cta < ctas) {
+      const Shares shares(units, ctas);
+      c_begin = shares.begin(cta);
+      c_end = shares.begin(cta + 1);
+    }
+#pragma unroll 1
+    for (int step = p.way == kWhole ? 0 : 2; step < 3; ++step) {
+      if (step == 2) {
+        const int range = c_end - c_begin;
+        begin = c_begin + range * w / kWarps;
+        left = c_begin + range * (w + 1) / kWarps - begin;
+        if (left <= 0) break;
+      }
+      const int u = step == 0 ? c_begin : step == 1 ? c_end : begin;
+      if (u >= units) continue;
       const int x = p.vh.quotient(u);                        // in [before(row), before(row) + cost(row))
       // the last of the 256 sums that is not above x: of every eighth, then of eight
       int a = __popc(__ballot_sync(0xffffffffu, s_scan[8 * lane] <= x)) * 8 - 8;
       a += __popc(__ballot_sync(0xffffffffu, lane < 8 && s_scan[a + (lane & 7)] <= x)) - 1;
       int at = s_scan[a];
-      f_row = a * per;
-      f_sp = span_of<POS>(p, p.lengths[f_row]);
-      while (at + f_sp.cost() <= x) {
-        at += f_sp.cost();
-        f_sp = span_of<POS>(p, p.lengths[++f_row]);
+      row = a * per;
+      sp = span_of<POS>(p, p.lengths[row]);
+#pragma unroll 1
+      while (at + sp.cost() <= x) {
+        at += sp.cost();
+        sp = span_of<POS>(p, p.lengths[++row]);
       }
-      const int rest = u - at * static_cast<int>(p.vh.value);
-      f_vh = rest / f_sp.cost();
-      return rest - f_vh * f_sp.cost();
-    };
-    int c_begin = 0, c_end = 0;
-    if (cta < ctas) {
-      c_begin = share_begin(units, ctas, cta);
-      c_end = share_begin(units, ctas, cta + 1);
-      if (p.way == kWhole) {
-        // to the next row and head's beginning
-        int r, h;
-        Span s;
-        if (c_begin > 0) {
-          const int in = find(c_begin, r, h, s);
-          if (in > 0) c_begin += s.cost() - in;
-        }
-        if (c_end < units) {
-          const int in = find(c_end, r, h, s);
-          if (in > 0) c_end += s.cost() - in;
-        }
+      const int rest = u - at * static_cast<int>(p.vh.value), cost = sp.cost();
+      vh = rest / cost;
+      const int in = rest - vh * cost;
+      if (step == 0 && in > 0) c_begin += cost - in;
+      if (step == 1 && in > 0) c_end += cost - in;
+      if (step == 2) {
+        tile = in - kRowCost;
+        if (tile < 0) left += tile, tile = 0;                // from the row's start on: its cost comes first
       }
-    }
-    const int begin = c_begin + share_begin(c_end - c_begin, kWarps, w);
-    left = c_begin + share_begin(c_end - c_begin, kWarps, w + 1) - begin;
-    if (left > 0) {
-      tile = find(begin, row, vh, sp) - kRowCost;
-      if (tile < 0) left += tile, tile = 0;                  // from the row's start on: its cost comes first
     }
   }
 
@@ -700,21 +701,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
   constexpr bool EARLY = !(F32 && HB == 2 && D == 128);
   const bool any = left > 0;
   if (EARLY && any) load_query(row, vh);
-  for (int i = 0; i < p.stages - 1; ++i) {
-    if (left > 0) produce();
-    mkw::cp_async_commit();
-  }
 
   // ---- rows without tiles -----------------------------------------------------
-  for (int r = cta; r < p.n; r += gridDim.x) {
+#pragma unroll 1
+  for (int r = cta * kWarps + w; r < p.n; r += gridDim.x * kWarps) {
     const int len = p.lengths[r];
     if (len < 0 || span_of<POS>(p, len).count > 0) continue;
-    const float x = len == 0 ? 0.f : NAN;
-    if (len > 0 && tid == 0) report(p.status, MK_ERR_BAD_PAGE);
-    for (int i = tid; i < p.hq * D; i += kAttnThreads)
-      store_one(static_cast<T *>(p.out) + r * p.out_row + (i / D) * p.out_head + i % D, x);
-    if (p.lse)
-      for (int i = tid; i < p.hq; i += kAttnThreads) p.lse[static_cast<int64_t>(r) * p.hq + i] = len == 0 ? -INFINITY : NAN;
+    const float l = len == 0 ? 0.f : NAN;
+    if (len > 0 && lane == 0) report(p.status, MK_ERR_BAD_PAGE);
+#pragma unroll 1
+    for (int h = 0; h < p.hq; ++h) {
+      float x[D / 32] = {};
+      write_head<T, D>(p, lane, r, h, 0.f, l, x, 1.f);
+    }
   }
 
   // ---- the warp's tiles ---------------------------------------------------------
@@ -723,11 +722,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
   int rows = 0, head0 = 0, begins = 0;
   float *first_part = reinterpret_cast<float *>(smem + kWarps * p.stages * TL::STAGE) + w * p.gr * PST;
   float *last_part = reinterpret_cast<float *>(smem + w * p.stages * TL::STAGE);
-  int stage = 0;
+  int stage = 0, ahead = 1 - p.stages;                       // the first stages - 1 rounds only produce
   bool start = true;
-  for (bool more = any; more;) {
+#pragma unroll 1
+  for (bool more = any; more; ++ahead) {
     if (left > 0) produce();
     mkw::cp_async_commit();
+    if (ahead < 0) continue;
     if (p.stages == 3) mkw::cp_async_wait<2>(); else mkw::cp_async_wait<1>();
     __syncwarp();
     const TileInfo ti = s_tile[w][stage];
@@ -949,79 +950,82 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
   __syncthreads();
 
   // ---- join the warps' parts, in order, a query head of a row a warp -----------------------------------------
-  // where the jth part is: the ring of its warp (a part that does not end its row), or the space beside the rings
-  auto part_at = [&](int j) {
-    return reinterpret_cast<const float *>((j & 1) ? smem + (j >> 1) * p.stages * TL::STAGE
-                                                   : smem + kWarps * p.stages * TL::STAGE + (j >> 1) * p.gr * PST * 4);
-  };
+  // lane j knows the jth part, and where it is: the ring of its warp (a part that does not end its row), or the space
+  // beside the rings
   const PartInfo mine = lane < 2 * kWarps ? s_part[lane] : PartInfo{-1, 0, 0, 0};
   const unsigned valid = __ballot_sync(0xffffffffu, mine.row >= 0);
-  float mx, sum, x[D / 32];
-  if (p.way == kByCluster) {
-    // All parts are of one row and head.  Query head r goes to CTA r % cluster, which joins what all have of it.
-    const int rank = cta % p.cluster;
-    const Heads h = heads_of(p, cta / p.cluster);
-    float *inbox = reinterpret_cast<float *>(smem + kWarps * (p.stages * TL::STAGE + p.gr * PST * 4));   // [CTA][query head / cluster][PST]
-    const int owned = (p.gr + p.cluster - 1) / p.cluster;
-    mkw::cluster_wait();
-    for (int r = w; r < h.count; r += kWarps) {
-      join_parts<D>(lane, 2 * kWarps, [&](int j) { return valid >> j & 1 ? part_at(j) + r * PST : nullptr; }, mx, sum, x);
-      const uint32_t to = mkw::remote(inbox + (rank * owned + r / p.cluster) * PST, r % p.cluster);
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) mkw::store_remote(to + (lane * (D / 32) + k) * 4, x[k]);
-      if (lane == 0) {
-        mkw::store_remote(to + D * 4, mx);
-        mkw::store_remote(to + D * 4 + 4, sum);
-      }
-    }
-    mkw::cluster_arrive();
-    mkw::cluster_wait();
-    if (!sp.count) return;
-    const float vsc = FP8 && p.v_scale ? p.v_scale[h.kvh] : 1.f;
-    for (int i = w; i < owned; i += kWarps) {
-      const int r = i * p.cluster + rank;
-      if (r >= h.count) break;
-      join_parts<D>(lane, p.cluster, [&](int j) { return inbox + (j * owned + i) * PST; }, mx, sum, x);
-      write_head<T, D>(p, lane, 0, h.first + r, mx, sum, x, vsc);
-    }
-    return;
-  }
+  const int beside = kWarps * p.stages * TL::STAGE;
+  int mine_at = (lane & 1) ? (lane >> 1) * p.stages * TL::STAGE : beside + (lane >> 1) * p.gr * PST * 4;
   // a group: consecutive parts of the same row and head; lane j says whether part j begins one
   const unsigned below = valid & ((1u << lane) - 1u);
   const int prev = below ? 31 - __clz(below) : lane;
   const int prev_row = __shfl_sync(0xffffffffu, mine.row, prev), prev_vh = __shfl_sync(0xffffffffu, mine.vh, prev);
   const unsigned starts = __ballot_sync(0xffffffffu, mine.row >= 0 && (!below || prev_row != mine.row || prev_vh != mine.vh));
-  const int items = __popc(starts) * p.gr;
-  for (int i = w; i < items; i += kWarps) {
-    const int group = i / p.gr, r = i - group * p.gr;
-    unsigned rest = starts;
-    for (int k = 0; k < group; ++k) rest &= rest - 1u;
-    const int a = __ffs(rest) - 1;                           // the group's first part
-    const unsigned later = starts & ~((2u << a) - 1u), in_group = valid & ~((1u << a) - 1u) & (later ? (later & -later) - 1u : ~0u);
-    const int b = 31 - __clz(in_group);                      // and its last
-    const int row_of = __shfl_sync(0xffffffffu, mine.row, a), vh_of = __shfl_sync(0xffffffffu, mine.vh, a);
-    const int first = __shfl_sync(0xffffffffu, mine.begins, a), ends = __shfl_sync(0xffffffffu, mine.ends, b);
-    const Heads h = heads_of(p, vh_of);
-    if (r >= h.count) continue;
-    join_parts<D>(lane, b - a + 1, [&](int j) { return in_group >> (a + j) & 1 ? part_at(a + j) + r * PST : nullptr; }, mx, sum, x);
-    if (first && ends) {
-      write_head<T, D>(p, lane, row_of, h.first + r, mx, sum, x, FP8 && p.v_scale ? p.v_scale[h.kvh] : 1.f);
-      continue;
-    }
-    float *to = p.parts + ((static_cast<int64_t>(cta) * 2 + (first ? 1 : 0)) * p.gr + r) * PST;
-    store_row(to + lane * (D / 32), x);
-    if (lane == 0) {
-      to[D] = mx;
-      to[D + 1] = sum;
-      if (first && r == 0) {
-        // the last CTA with tiles of this row: the one whose range holds the row's last unit
-        int before_row = s_scan[row_of / per];
-        for (int k = row_of / per * per; k < row_of; ++k) before_row += span_of<POS>(p, p.lengths[k]).cost();
-        const int cost = span_of<POS>(p, p.lengths[row_of]).cost();
-        const int last = share_of(units, ctas, before_row * static_cast<int>(p.vh.value) + (vh_of + 1) * cost - 1);
-        p.records[cta] = make_int4(row_of, vh_of, last, 1);
+  int items = __popc(starts) * p.gr;
+  // A cluster's parts are all of one row and head.  Query head r goes to the inbox of CTA r % cluster, which in a second
+  // round joins what all have of it.
+  const int owned = p.way == kByCluster ? (p.gr + p.cluster - 1) / p.cluster : 0, inbox = beside + kWarps * p.gr * PST * 4;   // [CTA][owned][PST]
+  const int rank = p.way == kByCluster ? cta % p.cluster : 0;
+  if (p.way == kByCluster) {
+    items = p.gr;
+    mkw::cluster_wait();
+  }
+#pragma unroll 1
+  for (int round = 0;; ++round) {
+#pragma unroll 1
+    for (int i = w; i < items; i += kWarps) {
+      int group = i / p.gr, r = i - group * p.gr, a = 0, b = 0, row_of = 0, vh_of = cta / p.cluster, first = 1, ends = 1;
+      unsigned in_group = valid;
+      if (p.way == kByCluster) {
+        if (round == 1) in_group = (1u << p.cluster) - 1u, r = i;
+      } else {
+        unsigned rest = starts;
+        for (int k = 0; k < group; ++k) rest &= rest - 1u;
+        a = __ffs(rest) - 1;                                 // the group's first part
+        const unsigned later = rest & (rest - 1u);
+        in_group = valid & ~((1u << a) - 1u) & (later ? (later & -later) - 1u : ~0u);
+        b = 31 - __clz(in_group);                            // and its last
+        row_of = __shfl_sync(0xffffffffu, mine.row, a), vh_of = __shfl_sync(0xffffffffu, mine.vh, a);
+        first = __shfl_sync(0xffffffffu, mine.begins, a), ends = __shfl_sync(0xffffffffu, mine.ends, b);
+      }
+      const Heads h = heads_of(p, vh_of);
+      float mx, sum, x[D / 32];
+      join_parts<D>(lane, in_group, smem, mine_at + r * PST * 4, mx, sum, x);
+      if (p.way == kByCluster && round == 1) r = r * p.cluster + rank;
+      if (r >= h.count) continue;
+      if (p.way == kByCluster && round == 0) {
+        const uint32_t to = mkw::remote(smem + inbox + (rank * owned + r / p.cluster) * PST * 4, r % p.cluster);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) mkw::store_remote(to + (lane * (D / 32) + k) * 4, x[k]);
+        if (lane == 0) {
+          mkw::store_remote(to + D * 4, mx);
+          mkw::store_remote(to + D * 4 + 4, sum);
+        }
+      } else if (first && ends) {
+        if (sp.count || p.way != kByCluster)                 // (a row without tokens is written above)
+          write_head<T, D>(p, lane, row_of, h.first + r, mx, sum, x, FP8 && p.v_scale ? p.v_scale[h.kvh] : 1.f);
+      } else {
+        float *to = p.parts + ((static_cast<int64_t>(cta) * 2 + (first ? 1 : 0)) * p.gr + r) * PST;
+        store_row(to + lane * (D / 32), x);
+        if (lane == 0) {
+          to[D] = mx;
+          to[D + 1] = sum;
+          if (first && r == 0) {
+            // the last CTA with tiles of this row: the one whose range holds the row's last unit
+            int before_row = s_scan[row_of / per];
+#pragma unroll 1
+            for (int k = row_of / per * per; k < row_of; ++k) before_row += span_of<POS>(p, p.lengths[k]).cost();
+            const int cost = span_of<POS>(p, p.lengths[row_of]).cost();
+            p.records[cta] = make_int4(row_of, vh_of, Shares(units, ctas).of(before_row * static_cast<int>(p.vh.value) + (vh_of + 1) * cost - 1), 1);
+          }
+        }
       }
     }
+    if (p.way != kByCluster || round == 1) return;
+    mkw::cluster_arrive();
+    mkw::cluster_wait();
+    items = owned;
+    mine_at = inbox + lane * owned * PST * 4;
   }
 }
 
@@ -1041,8 +1045,9 @@ __global__ void __launch_bounds__(kAttnThreads) join_kernel(const __grid_constan
     float m = -INFINITY, l = 0.f, x[D / 32] = {};
     for (int j0 = 0; j0 < n; j0 += 32) {
       float mj, lj, xj[D / 32];
-      join_parts<D>(lane, min(32, n - j0),
-                    [&](int j) { return p.parts + ((static_cast<int64_t>(cta + j0 + j) * 2 + (j0 + j == 0 ? 1 : 0)) * p.gr + r) * PST; }, mj, lj, xj);
+      const unsigned there = n - j0 >= 32 ? ~0u : (1u << (n - j0)) - 1u;
+      join_parts<D>(lane, there, p.parts + (static_cast<int64_t>(cta + j0) * 2 * p.gr + r) * PST,
+                    (lane * 2 + (j0 + lane == 0 ? 1 : 0)) * p.gr * PST * 4, mj, lj, xj);
       const float mx = fmaxf(m, mj), base = join_base(mx), f = mkw::exp2_fast(m - base), fj = mkw::exp2_fast(mj - base);
       m = mx;
       l = l * f + lj * fj;
