@@ -446,7 +446,28 @@ __device__ __forceinline__ Heads heads_of(const AttnParams &p, int vh) {
   return h;
 }
 
-// Join parts of a query head, in order, by a warp: lane l gets elements l D / 32 ..; lane j of `there` knows where its
+// Join parts of a query head in shared memory, in order, by a warp: lane l gets elements l D / 32 ..; lane j of `there`
+// knows the byte `mine_at` where its part's o[D], m, l are.  (Small on purpose: code that runs once a launch takes as
+// long as it is.)
+template <int D>
+__device__ __forceinline__ void join_shared(int lane, unsigned there, const unsigned char *smem, int mine_at, float &m, float &l, float (&x)[D / 32]) {
+  m = -INFINITY;
+  l = 0.f;
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) x[k] = 0.f;
+#pragma unroll 1
+  for (; there; there &= there - 1u) {
+    const float *part = reinterpret_cast<const float *>(smem + __shfl_sync(0xffffffffu, mine_at, __ffs(there) - 1));
+    const float mj = part[D], lj = part[D + 1], mx = fmaxf(m, mj), base = join_base(mx);
+    const float f = mkw::exp2_fast(m - base), fj = mkw::exp2_fast(mj - base);
+    m = mx;
+    l = l * f + lj * fj;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) x[k] = x[k] * f + part[lane * (D / 32) + k] * fj;
+  }
+}
+
+// The same in global memory: lane l gets elements l D / 32 ..; lane j of `there` knows where its
 // part's o[D], m, l are, in bytes from `base`.
 template <int D>
 __device__ __forceinline__ void join_parts(int lane, unsigned there, const void *base, int mine_at, float &m, float &l, float (&x)[D / 32]) {
@@ -487,9 +508,9 @@ __device__ __forceinline__ void store_row(__nv_bfloat16 *p, const float (&x)[2])
 // a joined query head: o / l and the log-sum-exp
 template <class T, int D>
 __device__ __forceinline__ void write_head(const AttnParams &p, int lane, int row, int head, float m, float l, float (&x)[D / 32], float vs) {
-  const float r = l == 0.f ? 0.f : 1.0f / l;
+  const float r = (l == 0.f ? 0.f : __frcp_rn(l)) * vs;
 #pragma unroll
-  for (int k = 0; k < D / 32; ++k) x[k] *= r * vs;
+  for (int k = 0; k < D / 32; ++k) x[k] *= r;
   store_row(static_cast<T *>(p.out) + row * p.out_row + head * p.out_head + lane * (D / 32), x);
   if (lane == 0) write_lse(p, row, head, m, l);
 }
@@ -518,7 +539,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ TileInfo s_tile[kWarps][3];
   __shared__ PartInfo s_part[2 * kWarps];
-  __shared__ int s_scan[kAttnThreads], s_warp[kWarps];
+  __shared__ int s_scan[kAttnThreads], s_warp[kWarps], s_range[2];
 
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int cta = blockIdx.x;
@@ -575,15 +596,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
       c_end = shares.begin(cta + 1);
     }
 #pragma unroll 1
-    for (int step = p.way == kWhole ? 0 : 2; step < 3; ++step) {
-      if (step == 2) {
+    for (int step = p.way == kWhole ? 0 : 1; step < 2; ++step) {
+      int u = w == 0 ? c_begin : c_end;                      // step 0: by the first two warps
+      if (step == 0) {
+        if (w < 2 && lane == 0) s_range[w] = u;
+      } else {
+        if (p.way == kWhole) {
+          __syncthreads();
+          c_begin = s_range[0], c_end = s_range[1];
+        }
         const int range = c_end - c_begin;
-        begin = c_begin + range * w / kWarps;
+        u = begin = c_begin + range * w / kWarps;
         left = c_begin + range * (w + 1) / kWarps - begin;
         if (left <= 0) break;
       }
-      const int u = step == 0 ? c_begin : step == 1 ? c_end : begin;
-      if (u >= units) continue;
+      if (u >= units || (step == 0 && w >= 2)) continue;
       const int x = p.vh.quotient(u);                        // in [before(row), before(row) + cost(row))
       // the last of the 256 sums that is not above x: of every eighth, then of eight
       int a = __popc(__ballot_sync(0xffffffffu, s_scan[8 * lane] <= x)) * 8 - 8;
@@ -599,16 +626,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
       const int rest = u - at * static_cast<int>(p.vh.value), cost = sp.cost();
       vh = rest / cost;
       const int in = rest - vh * cost;
-      if (step == 0 && in > 0) c_begin += cost - in;
-      if (step == 1 && in > 0) c_end += cost - in;
-      if (step == 2) {
+      if (step == 0) {
+        if (in > 0 && lane == 0) s_range[w] = u + cost - in;
+      } else {
         tile = in - kRowCost;
         if (tile < 0) left += tile, tile = 0;                // from the row's start on: its cost comes first
       }
     }
   }
 
-  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + w * p.stages * TL::STAGE;
+  const uint32_t smem_at = static_cast<uint32_t>(__cvta_generic_to_shared(smem)), ring = smem_at + w * p.stages * TL::STAGE;
   const unsigned char *k_base = static_cast<const unsigned char *>(p.k);
   const int64_t to_v = static_cast<const unsigned char *>(p.v) - k_base;
 
@@ -720,8 +747,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
   uint32_t qf[TQ][KS][HB][2];
   float o[DB][HB][4], m[HB][2], l[HB][2], mult[HB][2];
   int rows = 0, head0 = 0, begins = 0;
-  float *first_part = reinterpret_cast<float *>(smem + kWarps * p.stages * TL::STAGE) + w * p.gr * PST;
-  float *last_part = reinterpret_cast<float *>(smem + w * p.stages * TL::STAGE);
   int stage = 0, ahead = 1 - p.stages;                       // the first stages - 1 rounds only produce
   bool start = true;
 #pragma unroll 1
@@ -910,37 +935,42 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
     const bool ends = ti.flags & kLast;
     if (ends || !more) {
       start = true;
-      // (a cluster's parts are joined at the end, whole rows among them)
+      // A whole row of the warp is stored from the stage just read, 8 query heads at a time; a part stays where the join
+      // finds it (a cluster's parts are all joined at the end).
       const bool whole = begins && ends && p.way != kByCluster;
-      float *part = ends ? first_part : last_part;
-      const float vsc = FP8 && p.v_scale ? p.v_scale[heads_of(p, ti.vh).kvh] : 1.f;
+      float *part = reinterpret_cast<float *>(smem + w * p.stages * TL::STAGE);
+      if (ends) part = reinterpret_cast<float *>(whole ? smem + (kt - smem_at) : smem + kWarps * p.stages * TL::STAGE + w * p.gr * PST * 4);
 #pragma unroll
-      for (int hb = 0; hb < HB; ++hb)
+      for (int hb = 0; hb < HB; ++hb) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int h = 8 * hb + 2 * t + k;
           const float sum = column_sum(l[hb][k]);
-          if (h >= rows) continue;
-          const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-          T *out = static_cast<T *>(p.out) + ti.row * p.out_row + (head0 + h) * p.out_head;
+          if (h < rows) {
+            float *to = part + (whole ? h - 8 * hb : h) * PST;
+            if (g == 0) to[D] = m[hb][k], to[D + 1] = sum;
+            to += FP8 ? 2 * g : g;
 #pragma unroll
-          for (int c = 0; c < DB; ++c)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int d = 16 * c + (FP8 ? 2 * g + j : g + 8 * j);
-              const float x = o[c][hb][2 * j + k];
-              if (whole) store_one(out + d, x * inv * vsc);
-              else part[h * PST + d] = x;
-            }
-          if (g == 0) {
-            if (whole) {
-              write_lse(p, ti.row, head0 + h, m[hb][k], sum);
-            } else {
-              part[h * PST + D] = m[hb][k];
-              part[h * PST + D + 1] = sum;
+            for (int c = 0; c < DB; ++c) {
+              to[16 * c] = o[c][hb][k];
+              to[16 * c + (FP8 ? 1 : 8)] = o[c][hb][2 + k];
             }
           }
         }
+        __syncwarp();
+        if (whole) {
+          const float vsc = FP8 && p.v_scale ? p.v_scale[heads_of(p, ti.vh).kvh] : 1.f;
+#pragma unroll 1
+          for (int h = 0; h < min(8, rows - 8 * hb); ++h) {
+            const float *from = part + h * PST;
+            float x[D / 32];
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) x[k] = from[lane * (D / 32) + k];
+            write_head<T, D>(p, lane, ti.row, head0 + 8 * hb + h, from[D], from[D + 1], x, vsc);
+          }
+          __syncwarp();
+        }
+      }
       if (!whole && lane == 0) s_part[2 * w + (ends ? 0 : 1)] = PartInfo{ti.row, ti.vh, begins, ends};
       if (EARLY && more) load_query(s_tile[w][stage].row, s_tile[w][stage].vh);   // (the next tile has been asked for, and written down)
     }
@@ -977,7 +1007,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
       int group = i / p.gr, r = i - group * p.gr, a = 0, b = 0, row_of = 0, vh_of = cta / p.cluster, first = 1, ends = 1;
       unsigned in_group = valid;
       if (p.way == kByCluster) {
-        if (round == 1) in_group = (1u << p.cluster) - 1u, r = i;
+        if (round == 1) in_group = (1u << p.cluster) - 1u;
       } else {
         unsigned rest = starts;
         for (int k = 0; k < group; ++k) rest &= rest - 1u;
@@ -990,8 +1020,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
       }
       const Heads h = heads_of(p, vh_of);
       float mx, sum, x[D / 32];
-      join_parts<D>(lane, in_group, smem, mine_at + r * PST * 4, mx, sum, x);
-      if (p.way == kByCluster && round == 1) r = r * p.cluster + rank;
+      join_shared<D>(lane, in_group, smem, mine_at + r * PST * 4, mx, sum, x);
+      if (round == 1) r = i * p.cluster + rank;
       if (r >= h.count) continue;
       if (p.way == kByCluster && round == 0) {
         const uint32_t to = mkw::remote(smem + inbox + (rank * owned + r / p.cluster) * PST * 4, r % p.cluster);
