@@ -153,9 +153,11 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// programmatic dependent launch: let the next kernel of the stream start; wait for the previous one's results
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Programmatic dependent launch: the first statement of every kernel here, before it reads or writes anything.  The next
+// kernel of the stream, if it is launched so too, may be set up from now on; what the previous one did is seen after it.
+__device__ __forceinline__ void follow_previous_kernel() {
+  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+}
 
 // a cluster's CTAs: all their threads meet, shared memory written before is seen after
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }

@@ -11,6 +11,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "mk_launch_after.h"
 #include "mk_mma.cuh"
 
 namespace mkv {
@@ -129,6 +130,7 @@ __device__ __forceinline__ void load_gains(const uint16_t *p, float *x) {
 template <class T, class C, int D, int H>
 __global__ void __launch_bounds__(kAppendThreads, H == 1 ? 8 : 6) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int N = Vec<T>::N, TPH = D / 2 / N;           // threads of one head
+  mkw::follow_previous_kernel();
   const int heads = p.hq + 2 * p.hkv;
   const int item = threadIdx.x / TPH, i0 = (threadIdx.x % TPH) * N;
   const int row_in = p.groups.quotient(item), step = p.step;
@@ -258,12 +260,7 @@ int launch_heads_of(AppendParams p, cudaStream_t s) {
   p.rows = items / groups;
   const int ctas = (p.n - 1) / p.rows + 1, parts = (p.step + groups - 1) / groups;
   if (parts > 65535) return MK_ERR_UNSUPPORTED;
-  append_kernel<T, C, D, H><<<dim3(ctas, parts), kAppendThreads, 0, s>>>(p);
-  if (cudaPeekAtLastError() != cudaSuccess) {
-    cudaGetLastError();
-    return MK_ERR_CUDA;
-  }
-  return MK_OK;
+  return mkw::launch_after(&append_kernel<T, C, D, H>, dim3(ctas, parts), kAppendThreads, 0, s, p);
 }
 
 template <class T, class C, int D>
@@ -543,7 +540,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
 
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int cta = blockIdx.x;
-  if (p.way == kJoined) mkw::launch_dependents();
+  mkw::follow_previous_kernel();
   if (tid < 2 * kWarps) s_part[tid].row = -1;
 
   // ---- the warp's range: where it starts, and how much it covers -------------------
@@ -1065,7 +1062,7 @@ template <class T, int D>
 __global__ void __launch_bounds__(kAttnThreads) join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int PST = kPartStride<D>;
   const int cta = blockIdx.x, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  mkw::wait_previous_kernel();
+  mkw::follow_previous_kernel();
   const int4 rec = p.records[cta];
   if (!rec.w) return;
   const Heads h = heads_of(p, rec.y);
@@ -1155,33 +1152,10 @@ int launch_heads(AttnParams &p, int grid, int dev, cudaStream_t s) {
   const int inbox = p.way == kByCluster ? p.cluster * ((p.gr + p.cluster - 1) / p.cluster) : 0;
   const int parts = (kWarps * p.gr + inbox) * kPartStride<D> * 4;
   p.stages = kWarps * 3 * TL::STAGE + parts <= kMaxSmem ? 3 : 2;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr;
-  cfg.gridDim = dim3(p.way == kByCluster ? static_cast<int>(p.vh.value) * p.cluster : grid);
-  cfg.blockDim = dim3(kAttnThreads);
-  cfg.dynamicSmemBytes = kWarps * p.stages * TL::STAGE + parts;
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  if (p.way == kByCluster) {
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = p.cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.numAttrs = 1;
-  }
-  if (cudaLaunchKernelEx(&cfg, fn, static_cast<const AttnParams>(p)) != cudaSuccess) {
-    cudaGetLastError();
-    return MK_ERR_CUDA;
-  }
-  if (p.way != kJoined) return MK_OK;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.dynamicSmemBytes = 0;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, join_kernel<T, D>, static_cast<const AttnParams>(p)) != cudaSuccess) {
-    cudaGetLastError();
-    return MK_ERR_CUDA;
-  }
-  return MK_OK;
+  const int ctas = p.way == kByCluster ? static_cast<int>(p.vh.value) * p.cluster : grid, smem = kWarps * p.stages * TL::STAGE + parts;
+  const int rc = mkw::launch_after(fn, dim3(ctas), kAttnThreads, smem, s, p, p.cluster);
+  if (rc != MK_OK || p.way != kJoined) return rc;
+  return mkw::launch_after(&join_kernel<T, D>, dim3(grid), kAttnThreads, 0, s, p);
 }
 
 template <class T, bool FP8, int D>

@@ -38,6 +38,7 @@
 #include <type_traits>
 
 #include "../../include/mk.h"
+#include "mk_launch_after.h"
 #include "mk_mma.cuh"
 #include "mk_q4.h"
 
@@ -135,6 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint32_t s_max[COLS];
   __shared__ float s_to[COLS], s_back[COLS];               // the powers of two that x rows are multiplied by, and their inverses
+  mkw::follow_previous_kernel();
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int wn = w / p.wk, wk = w % p.wk, per_cta = kWarps / p.wk;
   const int m0 = blockIdx.y * p.pass_rows, mr = min(p.pass_rows, p.m - m0), cols = mr * TERMS;
@@ -504,12 +506,7 @@ int launch(Q4Params p, int sms, int dev, cudaStream_t s) {
   const int passes = (p.m + p.pass_rows - 1) / p.pass_rows;
   if (passes > 65535) return MK_ERR_UNSUPPORTED;
   const int per_cta = kWarps / p.wk, want = (p.tiles + per_cta - 1) / per_cta;
-  fn<<<dim3(std::min(want, sms), passes), kThreads, smem, s>>>(p);
-  if (cudaPeekAtLastError() != cudaSuccess) {
-    cudaGetLastError();
-    return MK_ERR_CUDA;
-  }
-  return MK_OK;
+  return mkw::launch_after(fn, dim3(std::min(want, sms), passes), kThreads, smem, s, p);
 }
 
 template <class T, int NT, int RT, bool ZEROS>
