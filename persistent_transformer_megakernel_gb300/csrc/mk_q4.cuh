@@ -149,6 +149,37 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
   const int rounds = tile0 < p.tiles ? (p.tiles - tile0 + step - 1) / step : 0;
   const int items = rounds * nb;
 
+  // ---- x, and the largest value of every row.  The weights are asked for when x is there: before, its answer waits
+  // behind theirs ------------------------------------------------------------------------------------------------
+  const T *x = static_cast<const T *>(p.x) + m0 * p.x_row;
+  const int eighths = p.blocks * (kBlock / 8), last = p.k / 8, all = mr * eighths;
+  auto read = [&](int i, Eight<T> &e) {                    // eighth i % eighths of row i / eighths, if it is there
+    const int r = p.eighths.quotient(i), b = i - r * eighths;
+    if (b < last) e.load(x + r * p.x_row + b * 8);
+    return b < last ? r : -1;
+  };
+  if (tid < COLS) s_max[tid] = 0;
+  __syncthreads();
+  constexpr int AT_ONCE = 4;
+#pragma unroll 1
+  for (int i0 = tid; i0 - tid < all; i0 += AT_ONCE * kThreads) {
+    Eight<T> e[AT_ONCE];
+    int row[AT_ONCE];
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) row[j] = i0 + j * kThreads < all ? read(i0 + j * kThreads, e[j]) : -1;
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) {
+      if (i0 - tid + j * kThreads >= all) break;
+      const uint32_t mx = row[j] >= 0 ? e[j].largest() : 0u;
+      if (__all_sync(0xffffffffu, row[j] == __shfl_sync(0xffffffffu, row[j], 0))) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, mx);
+        if (lane == 0 && row[j] >= 0) atomicMax(&s_max[row[j]], top);
+      } else if (row[j] >= 0) {                            // eighths of several rows
+        atomicMax(&s_max[row[j]], mx);
+      }
+    }
+  }
+
   // ---- codes: this lane copies chunk t of rows g, g + 8, ... of every block ----------------------------------
   const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   int c_tile = tile0, c_blk = 0, c_left = items, c_stage = 0;    // the copies' place
@@ -223,43 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
   };
   Scales next = look_up(), after = look_up();
 
-  // ---- the x rows as columns of fp16 terms, zeros past k
-  const T *x = static_cast<const T *>(p.x) + m0 * p.x_row;
-  const int eighths = p.blocks * (kBlock / 8), last = p.k / 8, all = mr * eighths;
-  constexpr int KEEP = 4;                                  // eighths a thread keeps in registers between the two passes
-  if (tid < COLS) s_max[tid] = 0;
-  __syncthreads();
-  auto read = [&](int i, Eight<T> &e) {                    // eighth i % eighths of row i / eighths, if it is there
-    const int r = p.eighths.quotient(i), b = i - r * eighths;
-    if (b < last) e.load(x + r * p.x_row + b * 8);
-    return b < last ? r : -1;
-  };
-  Eight<T> kept[KEEP];
-  auto largest = [&](const Eight<T> &e, int r) {
-    const uint32_t mx = r >= 0 ? e.largest() : 0u;
-    if (__all_sync(0xffffffffu, r == __shfl_sync(0xffffffffu, r, 0))) {
-      const uint32_t top = __reduce_max_sync(0xffffffffu, mx);
-      if (lane == 0 && r >= 0) atomicMax(&s_max[r], top);
-    } else if (r >= 0) {                                   // eighths of several rows
-      atomicMax(&s_max[r], mx);
-    }
-  };
-  const int slots = (all + kThreads - 1) / kThreads;
-#pragma unroll
-  for (int j = 0; j < KEEP; ++j) {
-    const int i = tid + j * kThreads;
-    if (j < slots) {
-      const int r = i < all ? read(i, kept[j]) : -1;
-      largest(kept[j], r);
-    }
-  }
-#pragma unroll 1
-  for (int j = KEEP; j < slots; ++j) {
-    const int i = tid + j * kThreads;
-    Eight<T> e;
-    const int r = i < all ? read(i, e) : -1;
-    largest(e, r);
-  }
+  // ---- the x rows as columns of fp16 terms, zeros past k ----------------------------------------------------
   __syncthreads();
   for (int r = w; r < mr; r += kWarps) {
     uint32_t mx = s_max[r];
@@ -282,10 +277,17 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
     if (lane == 0) s_to[r] = ldexpf(1.f, e), s_back[r] = ldexpf(1.f, -e);
   }
   __syncthreads();
-  auto stage = [&](int i, const Eight<T> &e) {
+  // (read again, from the L1, in a loop that is not unrolled: held in registers the code is four times as long, and
+  // fetching it takes longer)
+#pragma unroll 1
+  for (int i = tid; i < all; i += kThreads) {
     const int r = p.eighths.quotient(i), b = i - r * eighths;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (b < last) e.values(v);
+    if (b < last) {
+      Eight<T> e;
+      e.load(x + r * p.x_row + b * 8);
+      e.values(v);
+    }
     const float f = s_to[r];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= f;
@@ -299,17 +301,6 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
       o.w = mkw::take_input_term(mkw::FP16Op{}, v[3], v[7]);
       *reinterpret_cast<uint4 *>(to + u * p.pitch) = o;
     }
-  };
-#pragma unroll
-  for (int j = 0; j < KEEP; ++j) {
-    const int i = tid + j * kThreads;
-    if (i < all) stage(i, kept[j]);
-  }
-#pragma unroll 1
-  for (int i = tid + KEEP * kThreads; i < all; i += kThreads) {
-    Eight<T> e;
-    read(i, e);
-    stage(i, e);
   }
   __syncthreads();
 
