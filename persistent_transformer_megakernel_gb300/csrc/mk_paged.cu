@@ -1169,9 +1169,9 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool stride_ok(int64_t s, int elem) { return s >= 0 && s <= (int64_t{1} << 48) && s * elem % 16 == 0; }
 
 int check_cache(const mk_paged_kv *kv) {
-  if (!kv || !kv->k || !kv->v || !kv->table || (kv->dtype != MK_BF16 && kv->dtype != MK_E4M3)) return MK_ERR_INVALID_ARG;
+  if (!kv || !kv->k || !kv->v || (kv->dtype != MK_BF16 && kv->dtype != MK_E4M3)) return MK_ERR_INVALID_ARG;
   if (kv->n_pages < 1 || kv->n_kv_heads < 1 || kv->page_size < 1 || kv->table_rows < 0 || kv->table_cols < 0 ||
-      kv->table_stride < 0)
+      kv->table_stride < 0 || (!kv->table && kv->table_rows > 0 && kv->table_cols > 0))
     return MK_ERR_INVALID_ARG;
   const int es = kv->dtype == MK_E4M3 ? 1 : 2;
   if (!aligned16(kv->k) || !aligned16(kv->v) || !stride_ok(kv->page_stride, es) || !stride_ok(kv->head_stride, es) ||

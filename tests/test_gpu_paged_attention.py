@@ -150,6 +150,9 @@ def test_empty_calls():
     assert (mk.paged_attention(**c, lse=lse) == 0).all() and (lse == -math.inf).all()
     none = dict(c, q=c["q"][:0], lengths=c["lengths"][:0])
     assert mk.paged_attention(**none).shape == (0, 4, 64)
+    for t in (c["table"][:, :0], c["table"][:0, :0]):              # no pages, no rows
+        r = t.shape[0]
+        assert (mk.paged_attention(**dict(c, q=c["q"][:r], lengths=c["lengths"][:r], table=t)) == 0).all()
 
 
 def test_strides_and_layouts():

@@ -4,6 +4,9 @@ paged one (``export_kv``), then every layer as 4-bit projections,
 ``paged_append``, ``paged_attention`` for all sequences at once -- against the
 decoder's own steps of each sequence and its hidden states."""
 import ctypes as C
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -138,3 +141,33 @@ def test_exported_tokens_in_an_8_bit_cache():
         want = (a / sc[:, None, None]).clamp(-448, 448).to(torch.float8_e4m3fn).float()
         assert torch.equal(b[:, 9:39], want)
         assert (b[:, :9] == 3).all() and (b[:, 39:] == 3).all()
+
+
+def test_first_calls_inside_a_capture():
+    # a new process whose first call of each operator is captured: nothing that a capture forbids happens there
+    code = """
+import torch
+import persistent_transformer_megakernel_gb300 as mk
+kc, vc = (torch.randn((8, 2, 16, 64), device="cuda").bfloat16() for _ in range(2))
+table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+wide = torch.zeros((2, 4000), dtype=torch.int32, device="cuda")
+n = torch.tensor([50, 7], dtype=torch.int32, device="cuda")
+q = torch.randn((2, 4, 64), device="cuda")
+codes, scales = torch.zeros((40, 64), dtype=torch.uint8, device="cuda"), torch.ones((40, 2), device="cuda").bfloat16()
+x = torch.randn((2, 128), device="cuda")
+torch.cuda.synchronize()
+def step():
+    k = mk.paged_append(q[:, :2], q[:, 2:], kc, vc, table, n, q=q)
+    return [k, mk.paged_attention(k, kc, vc, table, n), mk.paged_attention(k, kc, vc, wide, n),
+            mk.paged_attention(k[:1], kc, vc, table[:1], n[:1]), mk.matvec_q4(x, codes, scales)]
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = step()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
