@@ -326,7 +326,11 @@ constexpr int kMinUnitsPerCta = 16;
 constexpr int kRowCost = 2;
 // rows of up to so many tiles are not cut over CTAs
 constexpr int kShortTiles = 64;
-constexpr int kMaxSmem = 230400;       // dynamic; the static part is below 2 KB, a CTA's limit 227 KB
+// Tiles of a warp's ring: one being read, one on its way, 64 KB an SM.  A third only crowds the memory (a warp's copies
+// wait longer and the last warps end later): 64 rows of up to 8192 tokens took 55.5 us with it, 53.4 without; 16 rows of
+// 32768 in e4m3 168 and 158.
+constexpr int kStages = 2;
+constexpr int kMaxSmem = 212992;       // dynamic, of 16 query heads and their inbox; the static part is below 2 KB
 
 enum { kByCluster, kWhole, kJoined };  // how rows are dealt out: the three ways above
 
@@ -344,7 +348,6 @@ struct AttnParams {
   int n, hq, hkv, group, n_pages, capacity, window;   // capacity: slots of a table row
   mkw::Divisor blocks, vh;   // head blocks of 16 query heads a kv head, virtual heads hkv * blocks
   int gr;              // query heads of a block: min(group, 16)
-  int stages;
   int way, cluster;
   int dense;           // a page's slots of a head lie one behind the other
   float scale;
@@ -380,8 +383,6 @@ struct Pair<__nv_bfloat16> {
   static __device__ __forceinline__ type none() { return 0u; }
   static __device__ __forceinline__ float2 values(type w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 };
-__device__ __forceinline__ void store_one(float *p, float x) { *p = x; }
-__device__ __forceinline__ void store_one(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
 // tiles of a row: those that hold any of its slots [lo, hi), and their cost, the row's start included
 struct Span {
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
   constexpr int POS = TL::POS, KS = D / 16, DB = D / 16, PN = POS / 16, PST = kPartStride<D>;
   constexpr float kShift = FP8 ? 14.f : 0.f;             // probabilities are scaled by 2^kShift
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ TileInfo s_tile[kWarps][3];
+  __shared__ TileInfo s_tile[kWarps][kStages];
   __shared__ PartInfo s_part[2 * kWarps];
   __shared__ int s_scan[kAttnThreads], s_warp[kWarps], s_range[2];
 
@@ -632,7 +633,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
     }
   }
 
-  const uint32_t smem_at = static_cast<uint32_t>(__cvta_generic_to_shared(smem)), ring = smem_at + w * p.stages * TL::STAGE;
+  const uint32_t smem_at = static_cast<uint32_t>(__cvta_generic_to_shared(smem)), ring = smem_at + w * kStages * TL::STAGE;
   const unsigned char *k_base = static_cast<const unsigned char *>(p.k);
   const int64_t to_v = static_cast<const unsigned char *>(p.v) - k_base;
 
@@ -702,7 +703,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
       s_tile[w][in_stage] = ti;
       if (bad) report(p.status, MK_ERR_BAD_PAGE);
     }
-    if (++in_stage == p.stages) in_stage = 0;
+    in_stage ^= 1;
   };
   // ---- a row's query heads as they are in memory: asked for before the tiles, else their answer waits behind those ----
   // columns: heads 8 hb + g in the query's fragments, 8 hb + 2t and 2t + 1 in scores, states and outputs
@@ -744,18 +745,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
   uint32_t qf[TQ][KS][HB][2];
   float o[DB][HB][4], m[HB][2], l[HB][2], mult[HB][2];
   int rows = 0, head0 = 0, begins = 0;
-  int stage = 0, ahead = 1 - p.stages;                       // the first stages - 1 rounds only produce
+  int stage = 0, ahead = 1 - kStages;                        // the first round only produces
   bool start = true;
 #pragma unroll 1
   for (bool more = any; more; ++ahead) {
     if (left > 0) produce();
     mkw::cp_async_commit();
     if (ahead < 0) continue;
-    if (p.stages == 3) mkw::cp_async_wait<2>(); else mkw::cp_async_wait<1>();
+    mkw::cp_async_wait<kStages - 1>();
     __syncwarp();
     const TileInfo ti = s_tile[w][stage];
     const uint32_t kt = ring + stage * TL::STAGE, vt = kt + TL::KBYTES;
-    if (++stage == p.stages) stage = 0;
+    stage ^= 1;
     more = !(ti.flags & kEnd);
 
     if (start) {                                             // a row's query heads
@@ -935,8 +936,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
       // A whole row of the warp is stored from the stage just read, 8 query heads at a time; a part stays where the join
       // finds it (a cluster's parts are all joined at the end).
       const bool whole = begins && ends && p.way != kByCluster;
-      float *part = reinterpret_cast<float *>(smem + w * p.stages * TL::STAGE);
-      if (ends) part = reinterpret_cast<float *>(whole ? smem + (kt - smem_at) : smem + kWarps * p.stages * TL::STAGE + w * p.gr * PST * 4);
+      float *part = reinterpret_cast<float *>(smem + w * kStages * TL::STAGE);
+      if (ends) part = reinterpret_cast<float *>(whole ? smem + (kt - smem_at) : smem + kWarps * kStages * TL::STAGE + w * p.gr * PST * 4);
 #pragma unroll
       for (int hb = 0; hb < HB; ++hb) {
 #pragma unroll
@@ -981,8 +982,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
   // beside the rings
   const PartInfo mine = lane < 2 * kWarps ? s_part[lane] : PartInfo{-1, 0, 0, 0};
   const unsigned valid = __ballot_sync(0xffffffffu, mine.row >= 0);
-  const int beside = kWarps * p.stages * TL::STAGE;
-  int mine_at = (lane & 1) ? (lane >> 1) * p.stages * TL::STAGE : beside + (lane >> 1) * p.gr * PST * 4;
+  const int beside = kWarps * kStages * TL::STAGE;
+  int mine_at = (lane & 1) ? (lane >> 1) * kStages * TL::STAGE : beside + (lane >> 1) * p.gr * PST * 4;
   // a group: consecutive parts of the same row and head; lane j says whether part j begins one
   const unsigned below = valid & ((1u << lane) - 1u);
   const int prev = below ? 31 - __clz(below) : lane;
@@ -1148,11 +1149,10 @@ int launch_heads(AttnParams &p, int grid, int dev, cudaStream_t s) {
     for (int i = 0; i < 4 && static_cast<int>(p.vh.value) <= r.clusters[i] && (i == 0 || tiles > p.cluster * kWarps); ++i) p.cluster = 2 << i;
     if (p.cluster > 1) p.way = kByCluster;
   }
-  // three stages of the ring where the parts leave room for them (every group of up to 8 query heads)
   const int inbox = p.way == kByCluster ? p.cluster * ((p.gr + p.cluster - 1) / p.cluster) : 0;
+  static_assert(kWarps * kStages * TL::STAGE + (kWarps * 16 + 16) * kPartStride<D> * 4 <= kMaxSmem, "16 heads, 16 CTAs");
   const int parts = (kWarps * p.gr + inbox) * kPartStride<D> * 4;
-  p.stages = kWarps * 3 * TL::STAGE + parts <= kMaxSmem ? 3 : 2;
-  const int ctas = p.way == kByCluster ? static_cast<int>(p.vh.value) * p.cluster : grid, smem = kWarps * p.stages * TL::STAGE + parts;
+  const int ctas = p.way == kByCluster ? static_cast<int>(p.vh.value) * p.cluster : grid, smem = kWarps * kStages * TL::STAGE + parts;
   const int rc = mkw::launch_after(fn, dim3(ctas), kAttnThreads, smem, s, p, p.cluster);
   if (rc != MK_OK || p.way != kJoined) return rc;
   return mkw::launch_after(&join_kernel<T, D>, dim3(grid), kAttnThreads, 0, s, p);
