@@ -152,6 +152,9 @@ __device__ __forceinline__ void e4m3x4_to_half2(uint32_t x, uint32_t &lo, uint32
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
 
 // Programmatic dependent launch: the first statement of every kernel here, before it reads or writes anything.  The next
 // kernel of the stream, if it is launched so too, may be set up from now on; what the previous one did is seen after it.

@@ -26,14 +26,20 @@ __device__ __forceinline__ void report(int32_t *status, int code) {
 // Append: q, k and v heads of n tokens, normalised, rotated and stored.
 //
 // Bound by bytes: every element is read once and written once; the arithmetic
-// is a sum of squares and one rotation.  D / 2 / N threads hold a head, each N
-// consecutive elements of the first half and the N elements half a head further,
-// the pairs of the rotation, so that every load and store is 16 bytes of an input
-// row and a pair meets in one thread; the squares are summed over the head's
-// threads by shuffles.  A thread takes 1 or 4 heads of its token: their
-// loads are on their way together, and the token's slot, page, cos and sin are
-// looked up once for them.  A thread that would need a page outside the cache or
-// a rotary row outside the table writes nothing.
+// is a sum of squares and one rotation, on two fp32 numbers an instruction.
+// D / 2 / N threads hold a head, each N consecutive elements of the first half
+// and the N elements half a head further, the pairs of the rotation, so that
+// every load and store is 16 bytes of an input row and a pair meets in one
+// thread; the squares are summed over the head's threads by shuffles.  A token
+// that would need a page outside the cache or a rotary row outside the table is
+// not written.
+// Two kernels: for few tokens a thread for every part of every head (one token
+// 2.8 us, 256 of 32 heads 3.5), for many persistent warps that copy ahead (20011
+// tokens of 32 heads of 128, bf16 to e4m3, 291 MB: 50 us, 5.8 TB/s).  They meet
+// where the threads of the first are no longer resident at once (about 450
+// tokens: 384 take 3.7 and 4.4 us, 512 4.7 both ways); the first kernel with 4
+// heads a thread took 62 us for the 20011, its threads waiting for slot, page and
+// elements one after the other.
 // ---------------------------------------------------------------------------
 
 struct AppendParams {
@@ -49,8 +55,11 @@ struct AppendParams {
   mkw::Divisor page_size;
   int n, hq, hkv, n_pages, table_rows, table_cols, rope_rows, rope_mode, sec0, sec1, sec2;
   int seq0, slot0;             // slots == NULL: row i is slot slot0 + i of sequence seq0
-  mkw::Divisor groups;         // groups of heads (a thread's) of a CTA
-  int rows, step;              // token rows of a CTA, groups of heads of a row
+  mkw::Divisor groups;         // few tokens: heads of a CTA
+  int rows;                    // and its token rows
+  mkw::Divisor parts;          // many: warps of a token
+  int streams;                 // tokens at once
+  int q_groups, kv_groups;     // groups of heads (a thread's) of q, of k and of v
   float eps;
 };
 
@@ -61,49 +70,74 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// 16 bytes of a row: N values, as they are in memory and as numbers
+// two fp32 numbers that one instruction works on
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 numbers_of(Two x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// 16 bytes of a row: N values, as they are in memory and as pairs of numbers
 template <class T>
 struct Vec;
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void numbers(const uint4 &w, float *x) {
-    x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
+  static __device__ __forceinline__ void numbers(const uint4 &w, Two *x) {
+    x[0] = two(__uint_as_float(w.x), __uint_as_float(w.y)), x[1] = two(__uint_as_float(w.z), __uint_as_float(w.w));
   }
-  static __device__ __forceinline__ uint4 bits(const float *x) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  static __device__ __forceinline__ uint4 bits(const Two *x) {
+    const float2 a = numbers_of(x[0]), b = numbers_of(x[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
   }
 };
+__device__ __forceinline__ uint32_t pack_bf16(Two x) {
+  const float2 f = numbers_of(x);
+  return pack_bf16(f.x, f.y);
+}
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void numbers(const uint4 &w, float *x) {
-    x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
-    x[4] = bf16_lo(w.z), x[5] = bf16_hi(w.z), x[6] = bf16_lo(w.w), x[7] = bf16_hi(w.w);
+  static __device__ __forceinline__ void numbers(const uint4 &w, Two *x) {
+    x[0] = two(bf16_lo(w.x), bf16_hi(w.x)), x[1] = two(bf16_lo(w.y), bf16_hi(w.y));
+    x[2] = two(bf16_lo(w.z), bf16_hi(w.z)), x[3] = two(bf16_lo(w.w), bf16_hi(w.w));
   }
-  static __device__ __forceinline__ uint4 bits(const float *x) {
-    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+  static __device__ __forceinline__ uint4 bits(const Two *x) {
+    return make_uint4(pack_bf16(x[0]), pack_bf16(x[1]), pack_bf16(x[2]), pack_bf16(x[3]));
   }
 };
 
-// N values to the cache: bf16, or e4m3 of value / scale (times the scale's reciprocal: a last place of fp32 away)
+// N values to the cache: bf16, or e4m3
 template <int N>
-__device__ __forceinline__ void store_cache(__nv_bfloat16 *p, const float *x, float) {
-  uint32_t w[N / 2];
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+__device__ __forceinline__ void store_cache(__nv_bfloat16 *p, const Two *x) {
   if constexpr (N == 8)
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(p) = Vec<__nv_bfloat16>::bits(x);
   else
-    *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(x[0]), pack_bf16(x[1]));
 }
 template <int N>
-__device__ __forceinline__ void store_cache(__nv_fp8_e4m3 *p, const float *x, float inv) {
+__device__ __forceinline__ void store_cache(__nv_fp8_e4m3 *p, const Two *x) {
   uint32_t w[N / 4];
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
-    const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t a = __nv_cvt_float2_to_fp8x2(numbers_of(x[2 * i]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t b = __nv_cvt_float2_to_fp8x2(numbers_of(x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
     w[i] = a | (b << 16);
   }
   if constexpr (N == 8)
@@ -112,164 +146,350 @@ __device__ __forceinline__ void store_cache(__nv_fp8_e4m3 *p, const float *x, fl
     *reinterpret_cast<uint32_t *>(p) = w[0];
 }
 
-constexpr int kAppendThreads = 128;
+constexpr int kAppendThreads = 128, kAppendCtas = 6;
+
+// a kernel's largest dynamic shared memory on a device, set at its first launch there
+struct MaxSmem {
+  std::once_flag once;
+  bool ok = false;
+  bool set(const void *fn, int bytes) {
+    std::call_once(once, [&] {
+      ok = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+      if (!ok) cudaGetLastError();
+    });
+    return ok;
+  }
+};
 
 template <int N>
-__device__ __forceinline__ void load_gains(const uint16_t *p, float *x) {
-  if constexpr (N == 8) {
+__device__ __forceinline__ void load_gains(const uint16_t *p, Two *x) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) x[i] = two(1.f, 1.f);
+  } else if constexpr (N == 8) {
     Vec<__nv_bfloat16>::numbers(*reinterpret_cast<const uint4 *>(p), x);
   } else {
     const uint2 w = *reinterpret_cast<const uint2 *>(p);
-    x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
+    x[0] = two(bf16_lo(w.x), bf16_hi(w.x)), x[1] = two(bf16_lo(w.y), bf16_hi(w.y));
   }
 }
 
-// H: heads a thread takes.  4 for many tokens, 768 threads an SM (20011 tokens of 32 heads of 128, bf16 to e4m3: 62 us;
-// at 512 a fifth longer, with 2 heads and 1024 as well, with 1 and 1280 two fifths); 1 where all threads are resident at
-// once anyway (one token 2.8 us against 3.5, 256 tokens 3.4 against 4.5)
-template <class T, class C, int D, int H>
-__global__ void __launch_bounds__(kAppendThreads, H == 1 ? 8 : 6) append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int N = Vec<T>::N, TPH = D / 2 / N;           // threads of one head
-  mkw::follow_previous_kernel();
-  const int heads = p.hq + 2 * p.hkv;
-  const int item = threadIdx.x / TPH, i0 = (threadIdx.x % TPH) * N;
-  const int row_in = p.groups.quotient(item), step = p.step;
-  const int first = blockIdx.y * static_cast<int>(p.groups.value) + item - row_in * static_cast<int>(p.groups.value);   // heads first, first + step, ...
-  const int64_t row64 = static_cast<int64_t>(blockIdx.x) * p.rows + row_in;
-  const bool live = row_in < p.rows && row64 < p.n && first < step;
-  const int row = live ? static_cast<int>(row64) : 0;
-
-  const int slot = !live ? -1 : p.slots ? p.slots[row] : p.slot0 + row;
-  const int seq = p.seqs ? p.seqs[row] : p.slots ? row : p.seq0;
-  int at[3] = {slot, slot, slot};
+// a token's slot, sequence and rows of the rotary table
+struct Token {
+  int slot, seq, at[3];
+};
+__device__ __forceinline__ Token token_of(const AppendParams &p, int row) {
+  Token t;
+  t.slot = p.slots ? p.slots[row] : p.slot0 + row;
+  t.seq = p.seqs ? p.seqs[row] : p.slots ? row : p.seq0;
+  t.at[0] = t.at[1] = t.at[2] = t.slot;
   if (p.positions) {
-    at[0] = at[1] = at[2] = p.positions[row];
+    t.at[0] = t.at[1] = t.at[2] = p.positions[row];
     if (p.rope_mode) {
-      at[1] = p.positions[static_cast<int64_t>(p.n) + row];
-      at[2] = p.positions[2 * static_cast<int64_t>(p.n) + row];
+      t.at[1] = p.positions[static_cast<int64_t>(p.n) + row];
+      t.at[2] = p.positions[2 * static_cast<int64_t>(p.n) + row];
     }
   }
-  // every thread of a warp stays to the shuffles below; one with nothing to do works on zeros
-  uint4 lo[H], hi[H];
-#pragma unroll
-  for (int j = 0; j < H; ++j) {
-    const int h = first + j * step;
-    lo[j] = hi[j] = make_uint4(0, 0, 0, 0);
-    if (live && h < heads) {
-      const T *src = (h < p.hq ? static_cast<const T *>(p.q) + row * p.q_row + h * p.q_head
-                               : h < p.hq + p.hkv ? static_cast<const T *>(p.k) + row * p.k_row + (h - p.hq) * p.k_head
-                                                  : static_cast<const T *>(p.v) + row * p.v_row + (h - p.hq - p.hkv) * p.v_head) + i0;
-      lo[j] = __ldcs(reinterpret_cast<const uint4 *>(src));
-      hi[j] = __ldcs(reinterpret_cast<const uint4 *>(src + D / 2));
-    }
+  return t;
+}
+// its element offset in the cache (of head 0), < 0 for a token that is not stored: refused for every head alike, so that
+// it is stored whole or not at all
+__device__ __forceinline__ int64_t place_of(const AppendParams &p, const Token &t) {
+  if (t.slot < 0) return -1;
+  const int col = p.page_size.quotient(t.slot);
+  int page = -1;
+  if (t.seq >= 0 && t.seq < p.table_rows && col < p.table_cols) page = p.table[t.seq * p.table_stride + col];
+  if (p.rope && (t.at[0] < 0 || t.at[0] >= p.rope_rows || t.at[1] < 0 || t.at[1] >= p.rope_rows || t.at[2] < 0 || t.at[2] >= p.rope_rows)) {
+    report(p.status, MK_ERR_BAD_POSITION);
+    return -1;
   }
-  bool ok = slot >= 0;
-  int64_t dst = 0;
-  float2 cs[N];
-  if (ok) {
-    const int col = p.page_size.quotient(slot);
-    int page = -1;
-    if (seq >= 0 && seq < p.table_rows && col < p.table_cols) page = p.table[seq * p.table_stride + col];
-    if (p.rope) {
-      // refused for every head alike, so that a row is stored whole or not at all
-      if (at[0] < 0 || at[0] >= p.rope_rows || at[1] < 0 || at[1] >= p.rope_rows || at[2] < 0 || at[2] >= p.rope_rows) {
-        ok = false;
-        report(p.status, MK_ERR_BAD_POSITION);
-      } else if (first < p.hq + p.hkv) {
-        if (p.rope_mode == 0) {
-          const float4 *r = reinterpret_cast<const float4 *>(p.rope + static_cast<int64_t>(at[0]) * (D / 2) + i0);
-#pragma unroll
-          for (int i = 0; i < N / 2; ++i) {
-            const float4 f = r[i];
-            cs[2 * i] = make_float2(f.x, f.y);
-            cs[2 * i + 1] = make_float2(f.z, f.w);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int j = i0 + i, m = j % 3;
-            const int stream = p.rope_mode == 1 ? (j >= p.sec0) + (j >= p.sec0 + p.sec1)
-                                                : (m == 1 && j < 3 * p.sec1) ? 1 : (m == 2 && j < 3 * p.sec2) ? 2 : 0;
-            cs[i] = p.rope[static_cast<int64_t>(stream == 0 ? at[0] : stream == 1 ? at[1] : at[2]) * (D / 2) + j];
-          }
-        }
-      }
-    }
-    if (page < 0 || page >= p.n_pages) {
-      if (ok) report(p.status, MK_ERR_BAD_PAGE);
-      ok = false;
-    }
-    dst = page * p.page_stride + (slot - col * static_cast<int>(p.page_size.value)) * p.slot_stride;
+  if (page < 0 || page >= p.n_pages) {
+    report(p.status, MK_ERR_BAD_PAGE);
+    return -1;
   }
-#pragma unroll
-  for (int j = 0; j < H; ++j) {
-    const int h = first + j * step;
-    const bool is_q = h < p.hq, is_k = !is_q && h < p.hq + p.hkv;
-    const uint16_t *gain = is_q ? p.q_norm : is_k ? p.k_norm : nullptr;
-    float a[N], b[N];
-    Vec<T>::numbers(lo[j], a);
-    Vec<T>::numbers(hi[j], b);
-    if (p.q_norm || p.k_norm) {                            // (the same for the whole grid)
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) ss += a[i] * a[i] + b[i] * b[i];
-#pragma unroll
-      for (int o = TPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (gain) {
-        const float r = rsqrtf(ss * (1.0f / D) + p.eps);
-        float ga[N], gb[N];
-        load_gains<N>(gain + i0, ga);
-        load_gains<N>(gain + i0 + D / 2, gb);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          a[i] *= r * ga[i];
-          b[i] *= r * gb[i];
-        }
-      }
-    }
-    if (!ok || h >= heads) continue;
-    if (p.rope && (is_q || is_k)) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float x = a[i], y = b[i];
-        a[i] = x * cs[i].x - y * cs[i].y;
-        b[i] = y * cs[i].x + x * cs[i].y;
-      }
-    }
-    if (is_q) {
-      T *out = static_cast<T *>(p.q_out) + row * p.out_row + h * p.out_head + i0;
-      *reinterpret_cast<uint4 *>(out) = Vec<T>::bits(a);
-      *reinterpret_cast<uint4 *>(out + D / 2) = Vec<T>::bits(b);
-    } else {
-      const int kvh = is_k ? h - p.hq : h - p.hq - p.hkv;
-      C *out = static_cast<C *>(is_k ? p.k_cache : p.v_cache) + dst + kvh * p.head_stride + i0;
-      const float *scales = is_k ? p.k_scale : p.v_scale;
-      const float inv = scales ? __frcp_rn(scales[kvh]) : 1.0f;
-      store_cache<N>(out, a, inv);
-      store_cache<N>(out + D / 2, b, inv);
-    }
-  }
+  return page * p.page_stride + (t.slot - col * static_cast<int>(p.page_size.value)) * p.slot_stride;
+}
+// the position stream that rotates pair j
+__device__ __forceinline__ int stream_of(const AppendParams &p, int j) {
+  const int m = j % 3;
+  return p.rope_mode == 1 ? (j >= p.sec0) + (j >= p.sec0 + p.sec1) : (m == 1 && j < 3 * p.sec1) ? 1 : (m == 2 && j < 3 * p.sec2) ? 2 : 0;
 }
 
-template <class T, class C, int D, int H>
-int launch_heads_of(AppendParams p, cudaStream_t s) {
-  constexpr int items = kAppendThreads / (D / 2 / Vec<T>::N);   // head groups a CTA has threads for
-  p.step = (p.hq + 2 * p.hkv + H - 1) / H;
-  const int groups = std::min(p.step, items);
-  p.groups.set(groups);
-  p.rows = items / groups;
-  const int ctas = (p.n - 1) / p.rows + 1, parts = (p.step + groups - 1) / groups;
-  if (parts > 65535) return MK_ERR_UNSUPPORTED;
-  return mkw::launch_after(&append_kernel<T, C, D, H>, dim3(ctas, parts), kAppendThreads, 0, s, p);
+// a thread's head or heads: i of q, of k or of v; byte addresses of its part of the first one, without the row's
+struct AppendHeads {
+  bool is_q, is_v;
+  int i, count;                // the first head, and how many there are of its kind
+  const unsigned char *src;
+  unsigned char *out;
+  int64_t src_row, src_head, out_row, out_head;
+  const uint16_t *gain;
+  const float *scales;
+};
+template <class T, class C>
+__device__ __forceinline__ AppendHeads append_heads(const AppendParams &p, int i, int q, int kv, int i0) {
+  AppendHeads h;
+  h.is_q = i < q;
+  h.is_v = i >= q + kv;
+  h.i = i - (h.is_q ? 0 : h.is_v ? q + kv : q);
+  h.count = h.is_q ? p.hq : p.hkv;
+  h.src_row = (h.is_q ? p.q_row : h.is_v ? p.v_row : p.k_row) * static_cast<int64_t>(sizeof(T));
+  h.src_head = (h.is_q ? p.q_head : h.is_v ? p.v_head : p.k_head) * static_cast<int64_t>(sizeof(T));
+  h.src = static_cast<const unsigned char *>(h.is_q ? p.q : h.is_v ? p.v : p.k) + h.i * h.src_head + i0 * sizeof(T);
+  h.out_row = h.is_q ? p.out_row * static_cast<int64_t>(sizeof(T)) : 0;
+  h.out_head = h.is_q ? p.out_head * static_cast<int64_t>(sizeof(T)) : p.head_stride * static_cast<int64_t>(sizeof(C));
+  h.out = static_cast<unsigned char *>(h.is_q ? p.q_out : h.is_v ? p.v_cache : p.k_cache) + h.i * h.out_head + i0 * (h.is_q ? sizeof(T) : sizeof(C));
+  h.gain = h.is_q ? p.q_norm : h.is_v ? nullptr : p.k_norm;
+  h.scales = h.is_q ? nullptr : h.is_v ? p.v_scale : p.k_scale;
+  return h;
+}
+
+// Gains, and times cos and sin: with them a pair of elements x, y becomes r (x xa + y ya), r (y yb + x xb).
+template <int N>
+struct Turn {
+  Two xa[N / 2], ya[N / 2], xb[N / 2], yb[N / 2];
+  __device__ __forceinline__ void set(int i, Two ga, Two gb, float4 f) {   // cos and sin of pairs 2 i and 2 i + 1
+    const Two c = two(f.x, f.z);
+    xa[i] = mul2(ga, c);
+    ya[i] = mul2(gb, two(-f.y, -f.w));
+    xb[i] = mul2(ga, two(f.y, f.w));
+    yb[i] = mul2(gb, c);
+  }
+};
+
+// 1 / rms of a head, by all its threads
+template <int D, int N>
+__device__ __forceinline__ float norm_factor(const Two *x, const Two *y, float eps) {
+  Two sq = two(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) sq = fma2(y[i], y[i], fma2(x[i], x[i], sq));
+  const float2 f = numbers_of(sq);
+  float ss = f.x + f.y;
+#pragma unroll
+  for (int o = D / 4 / N; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  return rsqrtf(ss * (1.0f / D) + eps);
 }
 
 template <class T, class C, int D>
-int launch_append(const AppendParams &p, cudaStream_t s) {
+__device__ __forceinline__ void store_head(const AppendHeads &h, unsigned char *out, Two *x, Two *y, float r, const Turn<Vec<T>::N> &t, bool rotated) {
+  constexpr int N = Vec<T>::N;
+  const Two r2 = two(r, r);
+  if (rotated) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const Two a = fma2(y[i], t.ya[i], mul2(x[i], t.xa[i])), b = fma2(x[i], t.xb[i], mul2(y[i], t.yb[i]));
+      x[i] = mul2(a, r2), y[i] = mul2(b, r2);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) x[i] = mul2(mul2(x[i], t.xa[i]), r2), y[i] = mul2(mul2(y[i], t.yb[i]), r2);
+  }
+  if (h.is_q) {
+    *reinterpret_cast<uint4 *>(out) = Vec<T>::bits(x);
+    *reinterpret_cast<uint4 *>(out + D / 2 * sizeof(T)) = Vec<T>::bits(y);
+  } else {
+    store_cache<N>(reinterpret_cast<C *>(out), x);
+    store_cache<N>(reinterpret_cast<C *>(out) + D / 2, y);
+  }
+}
+
+// Few tokens: one head a thread.
+template <class T, class C, int D>
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int N = Vec<T>::N, TPH = D / 2 / N;           // threads of one head
+  mkw::follow_previous_kernel();
+  const int item = threadIdx.x / TPH, i0 = (threadIdx.x % TPH) * N, heads = p.hq + 2 * p.hkv;
+  const int row_in = p.groups.quotient(item);
+  const int head = blockIdx.y * static_cast<int>(p.groups.value) + item - row_in * static_cast<int>(p.groups.value);
+  const int64_t row64 = static_cast<int64_t>(blockIdx.x) * p.rows + row_in;
+  // every thread of a warp stays to the shuffles below; one with nothing to do works on zeros
+  const bool live = row_in < p.rows && row64 < p.n && head < heads;
+  const int64_t row = live ? row64 : 0;
+  Token token;
+  if (live) token = token_of(p, static_cast<int>(row));
+  const AppendHeads h = append_heads<T, C>(p, live ? head : 0, p.hq, p.hkv, i0);
+  uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+  if (live) {
+    lo = __ldcs(reinterpret_cast<const uint4 *>(h.src + row * h.src_row));
+    hi = __ldcs(reinterpret_cast<const uint4 *>(h.src + row * h.src_row + D / 2 * sizeof(T)));
+  }
+  Two ga[N / 2], gb[N / 2];
+  load_gains<N>(h.gain ? h.gain + i0 : nullptr, ga);
+  load_gains<N>(h.gain ? h.gain + i0 + D / 2 : nullptr, gb);
+  const int64_t dst = live ? place_of(p, token) : -1;
+  const bool rotated = p.rope && !h.is_v;
+  float4 cs[N / 2] = {};
+  if (rotated && dst >= 0) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      if (p.rope_mode == 0) {
+        cs[i] = *reinterpret_cast<const float4 *>(p.rope + static_cast<int64_t>(token.at[0]) * (D / 2) + i0 + 2 * i);
+      } else {
+        const float2 a = p.rope[static_cast<int64_t>(token.at[stream_of(p, i0 + 2 * i)]) * (D / 2) + i0 + 2 * i];
+        const float2 b = p.rope[static_cast<int64_t>(token.at[stream_of(p, i0 + 2 * i + 1)]) * (D / 2) + i0 + 2 * i + 1];
+        cs[i] = make_float4(a.x, a.y, b.x, b.y);
+      }
+    }
+  }
+  Two x[N / 2], y[N / 2];
+  Vec<T>::numbers(lo, x);
+  Vec<T>::numbers(hi, y);
+  float r = 1.f;
+  if (p.q_norm || p.k_norm) {                              // (the same for the whole grid)
+    const float f = norm_factor<D, N>(x, y, p.eps);
+    if (h.gain) r = f;
+  }
+  if (dst < 0) return;
+  // e4m3 holds value / scale, here times the scale's reciprocal: a last place of fp32 away
+  if (h.scales) r *= __frcp_rn(h.scales[h.i]);
+  Turn<N> t;
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    if (rotated) t.set(i, ga[i], gb[i], cs[i]);
+    else t.xa[i] = ga[i], t.yb[i] = gb[i];
+  }
+  store_head<T, C, D>(h, h.out + row * h.out_row + (h.is_q ? 0 : dst * static_cast<int64_t>(sizeof(C))), x, y, r, t, rotated);
+}
+
+// Many tokens: a warp has 32 / TPH groups of up to 4 heads, the same ones of every `streams`th token, so that what
+// depends on the heads stays in registers; a token's elements, cos and sin are on their way to shared memory while
+// those of the one before are worked on.  A thread copies the elements it needs itself; cos and sin are the warp's (read
+// by each head's threads they were a third of the reads: 58 us).  12 warps an SM: 16 had 54 us, 8 56.
+constexpr int kStreamWarps = 12, kStreamHeads = 4;
+constexpr int kStreamPieces = 2 * kStreamHeads + 1;       // 16 bytes each, of a thread, a token
+// where the 16 bytes i (of N / 2) of cos and sin of a head's tth thread are, so that 8 threads meet 8 different banks
+template <int N>
+__device__ __forceinline__ int turn_at(int t, int i) {
+  constexpr int CH = N / 2;
+  return (CH * t + (i ^ (t / (8 / CH) % CH))) * 16;
+}
+template <class T, class C, int D>
+__global__ void __launch_bounds__(32 * kStreamWarps, 1) append_many_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int N = Vec<T>::N, TPH = D / 2 / N, STAGE = kStreamPieces * 512;
+  extern __shared__ __align__(128) unsigned char smem[];
+  mkw::follow_previous_kernel();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, i0 = lane % TPH * N;
+  const int warp = blockIdx.x * kStreamWarps + w, first = p.parts.quotient(warp), part = warp - first * static_cast<int>(p.parts.value);
+  if (first >= p.streams || first >= p.n) return;
+  int group = part * (32 / TPH) + lane / TPH;
+  const int groups = p.q_groups + 2 * p.kv_groups;
+  const bool live = group < groups;
+  AppendHeads h = append_heads<T, C>(p, live ? group : 0, p.q_groups, p.kv_groups, i0);
+  if (!live) h.count = 0;
+  const int step = h.is_q ? p.q_groups : p.kv_groups;     // heads i, i + step, ...
+  const bool rotated = p.rope && !h.is_v;
+  Two ga[N / 2], gb[N / 2];
+  load_gains<N>(h.gain ? h.gain + i0 : nullptr, ga);
+  load_gains<N>(h.gain ? h.gain + i0 + D / 2 : nullptr, gb);
+
+  float inv[kStreamHeads];                                 // (e4m3 holds value / scale, here times the scale's reciprocal)
+#pragma unroll
+  for (int j = 0; j < kStreamHeads; ++j) inv[j] = h.scales && h.i + j * step < h.count ? __frcp_rn(h.scales[h.i + j * step]) : 1.f;
+
+  const int count = (p.n - 1 - first) / p.streams + 1;
+  unsigned char *ring = smem + w * 2 * STAGE + lane * 16;
+  const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  const bool turned = __any_sync(0xffffffffu, rotated && h.count);
+  const uint32_t turn = ring_at - lane * 16 + 2 * kStreamHeads * 512 + turn_at<N>(lane / (N / 2), lane % (N / 2));   // this lane copies
+  Token batch;                                             // token 32 b + lane of the warp's
+  int64_t batch_dst = -1;
+  int64_t next_dst = -1;
+  auto produce = [&](int k) {
+    const int64_t row = first + static_cast<int64_t>(k) * p.streams;
+    if ((k & 31) == 0) {
+      batch_dst = -1;
+      if (k + lane < count) {
+        batch = token_of(p, static_cast<int>(row + static_cast<int64_t>(lane) * p.streams));
+        batch_dst = place_of(p, batch);
+      }
+    }
+    next_dst = __shfl_sync(0xffffffffu, batch_dst, k & 31);
+    int at[3];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) at[j] = __shfl_sync(0xffffffffu, batch.at[j], k & 31);
+    if (next_dst < 0) return;
+    const uint32_t stage = ring_at + (k & 1) * STAGE;
+    const unsigned char *src = h.src + row * h.src_row;
+#pragma unroll
+    for (int j = 0; j < kStreamHeads; ++j) {
+      if (h.i + j * step < h.count) {
+        mkw::cp_async16(stage + 2 * j * 512, src);
+        mkw::cp_async16(stage + (2 * j + 1) * 512, src + D / 2 * sizeof(T));
+      }
+      src += step * h.src_head;
+    }
+    if (!turned || lane >= D / 4) return;
+    const uint32_t to = turn + (k & 1) * STAGE;
+    const int j = 2 * lane;                                // pairs j and j + 1
+    if (p.rope_mode == 0) {
+      mkw::cp_async16(to, p.rope + static_cast<int64_t>(at[0]) * (D / 2) + j);
+    } else {
+      const int s0 = stream_of(p, j), s1 = stream_of(p, j + 1);
+      mkw::cp_async8(to, p.rope + static_cast<int64_t>(s0 == 0 ? at[0] : s0 == 1 ? at[1] : at[2]) * (D / 2) + j);
+      mkw::cp_async8(to + 8, p.rope + static_cast<int64_t>(s1 == 0 ? at[0] : s1 == 1 ? at[1] : at[2]) * (D / 2) + j + 1);
+    }
+  };
+  produce(0);
+  mkw::cp_async_commit();
+#pragma unroll 1
+  for (int k = 0; k < count; ++k) {
+    const int64_t dst = next_dst;
+    __syncwarp();                                          // all have read what the next token's cos and sin replace
+    if (k + 1 < count) produce(k + 1);
+    mkw::cp_async_commit();
+    mkw::cp_async_wait<1>();
+    __syncwarp();
+    if (dst < 0) continue;
+    const unsigned char *stage = ring + (k & 1) * STAGE;
+    Turn<N> t;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      if (rotated) t.set(i, ga[i], gb[i], *reinterpret_cast<const float4 *>(stage - lane * 16 + 2 * kStreamHeads * 512 + turn_at<N>(lane % TPH, i)));
+      else t.xa[i] = ga[i], t.yb[i] = gb[i];
+    }
+    unsigned char *out = h.out + (h.is_q ? (first + static_cast<int64_t>(k) * p.streams) * h.out_row : dst * static_cast<int64_t>(sizeof(C)));
+#pragma unroll
+    for (int j = 0; j < kStreamHeads; ++j) {
+      Two x[N / 2], y[N / 2];
+      Vec<T>::numbers(*reinterpret_cast<const uint4 *>(stage + 2 * j * 512), x);
+      Vec<T>::numbers(*reinterpret_cast<const uint4 *>(stage + (2 * j + 1) * 512), y);
+      float r = inv[j];
+      if (p.q_norm || p.k_norm) {
+        const float f = norm_factor<D, N>(x, y, p.eps);   // (of whatever the memory holds where there is no head)
+        if (h.gain) r *= f;
+      }
+      if (h.i + j * step < h.count) {
+        store_head<T, C, D>(h, out, x, y, r, t, rotated);
+      }
+      out += step * h.out_head;
+    }
+  }
+}
+
+template <class T, class C, int D>
+int launch_append(AppendParams p, cudaStream_t s) {
   if (p.hq > (1 << 20) || p.hkv > (1 << 20)) return MK_ERR_UNSUPPORTED;
-  const int sms = sm_count(nullptr);
+  constexpr int TPH = D / 2 / Vec<T>::N, items = kAppendThreads / TPH;
+  int dev = 0;
+  const int sms = sm_count(&dev), heads = p.hq + 2 * p.hkv;
   if (sms < 0) return MK_ERR_CUDA;
-  const int64_t threads = static_cast<int64_t>(p.n) * (p.hq + 2 * p.hkv) * (D / 2 / Vec<T>::N);
-  return threads <= static_cast<int64_t>(sms) * 8 * kAppendThreads ? launch_heads_of<T, C, D, 1>(p, s) : launch_heads_of<T, C, D, 4>(p, s);
+  p.q_groups = (p.hq + kStreamHeads - 1) / kStreamHeads;
+  p.kv_groups = (p.hkv + kStreamHeads - 1) / kStreamHeads;
+  const int parts = (p.q_groups + 2 * p.kv_groups + 32 / TPH - 1) / (32 / TPH);   // warps of a token
+  if (static_cast<int64_t>(p.n) * heads * TPH > static_cast<int64_t>(sms) * kAppendCtas * kAppendThreads && parts <= sms * kStreamWarps) {
+    static MaxSmem ready[kMaxDevices];
+    constexpr int smem = kStreamWarps * 2 * kStreamPieces * 512;
+    const auto fn = &append_many_kernel<T, C, D>;
+    if (!ready[dev].set(reinterpret_cast<const void *>(fn), smem)) return MK_ERR_CUDA;
+    p.parts.set(parts);
+    p.streams = sms * kStreamWarps / parts;
+    return mkw::launch_after(fn, dim3(sms), 32 * kStreamWarps, smem, s, p);
+  }
+  const int groups = std::min(heads, items);
+  p.groups.set(groups);
+  p.rows = items / groups;
+  const int ctas = (p.n - 1) / p.rows + 1, per_row = (heads + groups - 1) / groups;
+  if (per_row > 65535) return MK_ERR_UNSUPPORTED;
+  return mkw::launch_after(&append_kernel<T, C, D>, dim3(ctas, per_row), kAppendThreads, 0, s, p);
 }
 
 int run_append(const AppendParams &p, int dtype, int cache, int d, cudaStream_t s) {
