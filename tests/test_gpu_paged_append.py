@@ -210,3 +210,60 @@ def test_captured_and_replayed():
         mk.paged_append(k, v, k2, v2, table, slots, q=q, q_out=q2, rope=rope)
         torch.cuda.synchronize()
         assert torch.equal(kc, k2) and torch.equal(vc, v2) and torch.equal(q_out, q2)
+
+
+# Token counts past which persistent warps take the tokens (a thread for every part of every head would no longer be
+# resident): heads in whole and broken groups of 4, rows without queries, more tokens than a warp looks up at once.
+@pytest.mark.parametrize("x,cache,hq,hkv,d,n,rope,interleaved,norm", [
+    (BF16, E4M3, 16, 8, 128, 700, "slots", False, True),
+    (F32, BF16, 16, 8, 128, 300, (24, 20, 20), True, True),
+    (BF16, BF16, 9, 3, 64, 2100, (12, 10, 10), False, True),
+    (F32, E4M3, 5, 5, 64, 1100, "positions", False, False),
+    (BF16, BF16, 0, 2, 128, 3800, None, False, True),
+    (F32, E4M3, 33, 1, 128, 250, None, False, False),
+    (BF16, E4M3, 64, 64, 128, 120, "slots", False, False),
+    (BF16, BF16, 2, 1, 64, 59000, "slots", False, True)])
+def test_many_tokens(x, cache, hq, hkv, d, n, rope, interleaved, norm):
+    seqs = [i % 3 for i in range(n)]
+    slots = [i // 3 for i in range(n)]
+    for i in (5, 77, n - 1):
+        slots[i] = -1
+    _run(x, cache, hq, hkv, d, seqs, slots, 20, norm=norm, rope=rope, interleaved=interleaved, seed=12)
+
+
+@pytest.mark.parametrize("layout", [None, "nhd"])
+def test_many_tokens_and_some_that_are_refused(layout):
+    n = 600
+    seqs = [i % 3 for i in range(n)]
+    slots = [i // 3 for i in range(n)]
+    pos = torch.tensor(slots)
+    pos[40], pos[333] = 10 ** 6, -1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def edit(table, total):
+        table[0, 1], table[2, 0] = total, -5
+    _run(BF16, E4M3, 24, 4, 128, seqs, slots, 16, rope="positions", seed=13, status=status, positions=pos, table_edit=edit,
+         layout=layout, inplace=layout is not None)
+    assert status.item() in (-9, -10)
+
+
+def test_many_tokens_captured_and_replayed():
+    g0 = torch.Generator().manual_seed(0)
+    n = 1000
+    kc, vc = (torch.zeros((70, 8, 16, 128), dtype=BF16, device="cuda") for _ in range(2))
+    table = torch.arange(70, dtype=torch.int32, device="cuda").view(1, 70)
+    slots, seqs = (torch.zeros(n, dtype=torch.int32, device="cuda") for _ in range(2))
+    q, k, v = (torch.randn((n, h, 128), generator=g0).to(BF16).cuda() for h in (16, 8, 8))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q_out = mk.paged_append(k, v, kc, vc, table, slots, seqs=seqs, q=q)
+    order = torch.randperm(n, generator=g0).to(torch.int32)
+    for _ in range(3):
+        slots.copy_(order)
+        graph.replay()
+        torch.cuda.synchronize()
+        at = order.long().cuda()
+        for c, r in ((kc, k), (vc, v)):
+            assert torch.equal(c[at // 16, :, at % 16], r)
+        assert torch.equal(q_out, q)
+        order = order.roll(1)
