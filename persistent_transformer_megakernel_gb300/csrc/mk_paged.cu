@@ -542,8 +542,11 @@ int run_append(const AppendParams &p, int dtype, int cache, int d, cudaStream_t 
 
 constexpr int kWarps = 8, kAttnThreads = 32 * kWarps;
 constexpr int kMinUnitsPerCta = 16;
-// what the start of a row and head costs (its queries' loads, its results' stores), in tiles
-constexpr int kRowCost = 2;
+// What the start and end of a row and head cost (its queries' loads, its results' stores), in tiles: more the more query
+// heads there are.  64 rows of up to 8192 tokens took 86 us with 2 for 128 query heads on 8, 66 with 8 (and 58.9 and 56.8 for 64
+// on 8, with 2 and 4); 256 short rows of 4 heads on 1 take 9.6 with 2, 10.3 with 3.
+constexpr int row_cost(int heads) { return heads / 2 > 2 ? heads / 2 : 2; }
+constexpr int kMaxRowCost = row_cost(16);
 // rows of up to so many tiles are not cut over CTAs
 constexpr int kShortTiles = 64;
 // Tiles of a warp's ring: one being read, one on its way, 64 KB an SM.  A third only crowds the memory (a warp's copies
@@ -568,6 +571,7 @@ struct AttnParams {
   int n, hq, hkv, group, n_pages, capacity, window;   // capacity: slots of a table row
   mkw::Divisor blocks, vh;   // head blocks of 16 query heads a kv head, virtual heads hkv * blocks
   int gr;              // query heads of a block: min(group, 16)
+  int row_cost;
   int way, cluster;
   int dense;           // a page's slots of a head lie one behind the other
   float scale;
@@ -606,8 +610,7 @@ struct Pair<__nv_bfloat16> {
 
 // tiles of a row: those that hold any of its slots [lo, hi), and their cost, the row's start included
 struct Span {
-  int lo, hi, first, count;
-  __device__ __forceinline__ int cost() const { return count ? count + kRowCost : 0; }
+  int lo, hi, first, count, cost;
 };
 template <int POS>
 __device__ __forceinline__ Span span_of(const AttnParams &p, int len) {
@@ -616,6 +619,7 @@ __device__ __forceinline__ Span span_of(const AttnParams &p, int len) {
   s.lo = p.window > 0 && s.hi > p.window ? s.hi - p.window : 0;
   s.first = s.lo / POS;
   s.count = s.hi > 0 ? (s.hi + POS - 1) / POS - s.first : 0;
+  s.cost = s.count ? s.count + p.row_cost : 0;
   return s;
 }
 
@@ -701,7 +705,7 @@ __device__ __forceinline__ void join_parts(int lane, unsigned there, const void 
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) x[k] = 0.f;
-#pragma unroll 2
+#pragma unroll 8
   for (unsigned rest = there; rest; rest &= rest - 1u) {
     const int j = __ffs(rest) - 1;
     const float fj = __shfl_sync(0xffffffffu, f, j);
@@ -766,7 +770,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
 
   // ---- the warp's range: where it starts, and how much it covers -------------------
   int row = 0, vh = 0, tile = 0, left = 0;                   // left: units from the tile the producer stands at to the range's end
-  Span sp{0, 0, 0, 0};
+  Span sp{0, 0, 0, 0, 0};
   int per = 0, units = 0, ctas = 0;
   if (p.way == kByCluster) {
     mkw::cluster_arrive();                                   // (to be waited for before the others' memory is written)
@@ -778,13 +782,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
     left = shares.begin(i + 1) - tile;
     __syncthreads();
   } else {
-    // Units: a row and head of cost c covers c of them, tile j the (kRowCost + j)th.  A warp has the tiles whose unit
+    // Units: a row and head of cost c covers c of them, tile j the (row_cost + j)th.  A warp has the tiles whose unit
     // is in its range.  First the cost of the rows before every group of rows.
     per = (p.n + kAttnThreads - 1) / kAttnThreads;           // rows a thread counts
     int mine = 0;
     for (int i = 0; i < per; ++i) {
       const int r = tid * per + i;
-      if (r < p.n) mine += span_of<POS>(p, p.lengths[r]).cost();
+      if (r < p.n) mine += span_of<POS>(p, p.lengths[r]).cost;
     }
     int incl = mine;
 #pragma unroll
@@ -837,17 +841,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
       row = a * per;
       sp = span_of<POS>(p, p.lengths[row]);
 #pragma unroll 1
-      while (at + sp.cost() <= x) {
-        at += sp.cost();
+      while (at + sp.cost <= x) {
+        at += sp.cost;
         sp = span_of<POS>(p, p.lengths[++row]);
       }
-      const int rest = u - at * static_cast<int>(p.vh.value), cost = sp.cost();
+      const int rest = u - at * static_cast<int>(p.vh.value), cost = sp.cost;
       vh = rest / cost;
       const int in = rest - vh * cost;
       if (step == 0) {
         if (in > 0 && lane == 0) s_range[w] = u + cost - in;
       } else {
-        tile = in - kRowCost;
+        tile = in - p.row_cost;
         if (tile < 0) left += tile, tile = 0;                // from the row's start on: its cost comes first
       }
     }
@@ -905,7 +909,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
     --left;
     if (++tile == sp.count) {
       ti.flags |= kLast;
-      left -= kRowCost;
+      left -= p.row_cost;
       tile = 0;
       ++vh;
       if (++blk == static_cast<int>(p.blocks.value)) blk = 0, ++kvh;
@@ -949,13 +953,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
 
   // ---- rows without tiles -----------------------------------------------------
 #pragma unroll 1
-  for (int r = cta * kWarps + w; r < p.n; r += gridDim.x * kWarps) {
+  for (int r = cta; r < p.n; r += gridDim.x) {
     const int len = p.lengths[r];
     if (len < 0 || span_of<POS>(p, len).count > 0) continue;
     const float l = len == 0 ? 0.f : NAN;
     if (len > 0 && lane == 0) report(p.status, MK_ERR_BAD_PAGE);
 #pragma unroll 1
-    for (int h = 0; h < p.hq; ++h) {
+    for (int h = w; h < p.hq; h += kWarps) {
       float x[D / 32] = {};
       write_head<T, D>(p, lane, r, h, 0.f, l, x, 1.f);
     }
@@ -1262,8 +1266,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
             // the last CTA with tiles of this row: the one whose range holds the row's last unit
             int before_row = s_scan[row_of / per];
 #pragma unroll 1
-            for (int k = row_of / per * per; k < row_of; ++k) before_row += span_of<POS>(p, p.lengths[k]).cost();
-            const int cost = span_of<POS>(p, p.lengths[row_of]).cost();
+            for (int k = row_of / per * per; k < row_of; ++k) before_row += span_of<POS>(p, p.lengths[k]).cost;
+            const int cost = span_of<POS>(p, p.lengths[row_of]).cost;
             p.records[cta] = make_int4(row_of, vh_of, Shares(units, ctas).of(before_row * static_cast<int>(p.vh.value) + (vh_of + 1) * cost - 1), 1);
           }
         }
@@ -1289,7 +1293,7 @@ __global__ void __launch_bounds__(kAttnThreads) join_kernel(const __grid_constan
   const Heads h = heads_of(p, rec.y);
   const float vsc = p.v_scale ? p.v_scale[h.kvh] : 1.f;
   const int n = rec.z - cta + 1;
-  for (int r = w; r < h.count; r += kWarps) {
+  if (const int r = blockIdx.y * kWarps + w; r < h.count) {
     float m = -INFINITY, l = 0.f, x[D / 32] = {};
     for (int j0 = 0; j0 < n; j0 += 32) {
       float mj, lj, xj[D / 32];
@@ -1375,7 +1379,7 @@ int launch_heads(AttnParams &p, int grid, int dev, cudaStream_t s) {
   const int ctas = p.way == kByCluster ? static_cast<int>(p.vh.value) * p.cluster : grid, smem = kWarps * kStages * TL::STAGE + parts;
   const int rc = mkw::launch_after(fn, dim3(ctas), kAttnThreads, smem, s, p, p.cluster);
   if (rc != MK_OK || p.way != kJoined) return rc;
-  return mkw::launch_after(&join_kernel<T, D>, dim3(grid), kAttnThreads, 0, s, p);
+  return mkw::launch_after(&join_kernel<T, D>, dim3(grid, (p.gr + kWarps - 1) / kWarps), kAttnThreads, 0, s, p);
 }
 
 template <class T, bool FP8, int D>
@@ -1506,7 +1510,7 @@ extern "C" int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args
   // slots and the cost of all rows and heads are counted in 32 bits
   const int64_t slots = static_cast<int64_t>(kv->table_cols) * kv->page_size;
   if (slots > INT32_MAX - 64 || a->n_q_heads > (1 << 20) ||
-      (slots / 16 + 2 + kRowCost) * a->n > INT32_MAX / (kv->n_kv_heads * ((a->n_q_heads / kv->n_kv_heads + 15) / 16)))
+      (slots / 16 + 2 + kMaxRowCost) * a->n > INT32_MAX / (kv->n_kv_heads * ((a->n_q_heads / kv->n_kv_heads + 15) / 16)))
     return MK_ERR_UNSUPPORTED;
   int dev = 0;
   const int grid = sm_count(&dev);
@@ -1532,6 +1536,7 @@ extern "C" int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args
   p.blocks.set((p.group + 15) / 16);
   p.vh.set(p.hkv * ((p.group + 15) / 16));
   p.gr = std::min(p.group, 16);
+  p.row_cost = row_cost(p.gr);
   p.scale = a->scale;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   using B = __nv_bfloat16;
