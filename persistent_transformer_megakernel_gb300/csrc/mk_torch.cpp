@@ -14,6 +14,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -390,8 +391,8 @@ PyObject *paged_attention(PyObject *const *o) {
   if (a.n) {
     a.workspace_bytes = mk_paged_attention_workspace(a.n_q_heads, kv.n_kv_heads, kv.head_dim);
     if (a.workspace_bytes < 0) throw Failed{static_cast<int>(a.workspace_bytes), "mk_paged_attention_workspace"};
-    const at::Tensor ws = at::empty({a.workspace_bytes}, at::TensorOptions().dtype(at::kByte).device(dev));
-    a.workspace = ws.data_ptr();
+    const c10::DataPtr workspace = c10::cuda::CUDACachingAllocator::get()->allocate(a.workspace_bytes);   // (of the current device and stream)
+    a.workspace = workspace.get();
     enqueue("mk_paged_attention", [&] { return mk_paged_attention(&kv, &a, on.stream); });
   }
   return o[T_OUT] ? given(o[T_OUT]) : THPVariable_Wrap(made);
