@@ -538,6 +538,9 @@ int run_append(const AppendParams &p, int dtype, int cache, int d, cudaStream_t 
 //   - else the same with the CTAs' ranges as they fall: what a CTA has of a row
 //     at its range's ends goes through the workspace to join_kernel.
 // Parts are joined in order: the same lengths give the same bits.
+// Measured: 16 query heads on 8 of 128, 64 rows of 0 to 8192 tokens in bf16 (306 MB) 53 us, 5.7 TB/s; 16 rows of 30 to
+// 32 k in e4m3 (1034 MB) 157 us, 6.6 TB/s; one row of 257 tokens 6.9 us, of 5119 12.6 (fp32 queries); 256 rows of up to
+// 300 tokens, 8 heads on 2 of 64, 9.5 us.
 // ---------------------------------------------------------------------------
 
 constexpr int kWarps = 8, kAttnThreads = 32 * kWarps;

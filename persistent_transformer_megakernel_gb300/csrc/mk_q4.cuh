@@ -29,6 +29,10 @@
 // that is a third of the work of a 1.7B-shaped gate and up projection).  The rows'
 // tiles are dealt out to its warps; 2 to 16 of them share a tile's k where that
 // deals the blocks out more evenly, their sums added in order.
+//
+// Measured: 1 x 151936 x 1024, groups of 128 (80 MB) 17.5 us, 4.6 TB/s: instructions beside bytes; 8 x 12288 x 2048,
+// groups of 32 with zeros, bf16 x, 10.7 us and 3 x 2048 x 6144, groups of 64, 7.6 us: instructions and the staging of x;
+// 1 x 4096 x 1024 3.8 us: latency.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -122,6 +122,12 @@ void *vector(PyObject *o, const char *name, c10::ScalarType type, int64_t n, con
   return t.data_ptr();
 }
 
+// a tensor that is written: no two of its first two dimensions' rows may be the same memory
+void apart(const at::Tensor &t, const char *name) {
+  for (int i : {0, 1})
+    if (t.size(i) > 1 && t.stride(i) == 0) throw Bad{std::string(name) + " must not be expanded: it is written"};
+}
+
 // row and head strides of [n][heads][d]: the last dimension contiguous, every row on 16 bytes
 void heads(const at::Tensor &t, const char *name, int64_t n, int64_t d, int64_t h, c10::ScalarType type, const c10::Device &dev,
            int64_t *row, int64_t *head) {
@@ -236,6 +242,8 @@ Signature append_sig = {"paged_append", 6, 6, 20,
                          "mrope_interleaved", "q_norm", "k_norm", "eps", "k_scale", "v_scale", "status", "stream"}, {}};
 
 mk_append_args append_args(PyObject *const *o, const mk_paged_kv &kv, const c10::Device &dev) {
+  need((kv.n_pages == 1 || kv.page_stride) && (kv.n_kv_heads == 1 || kv.head_stride) && (kv.page_size == 1 || kv.slot_stride),
+       "the cache must not be expanded: it is written");
   const at::Tensor &k = tensor(o[A_K], "k"), &v = tensor(o[A_V], "v");
   const auto type = k.scalar_type();
   need(type == at::kFloat || type == at::kBFloat16, "k must be fp32 or bf16");
@@ -258,6 +266,7 @@ mk_append_args append_args(PyObject *const *o, const mk_paged_kv &kv, const c10:
       const at::Tensor &out = tensor(o[A_QOUT], "q_out");
       heads(out, "q_out", n, d, a.n_q_heads ? a.n_q_heads : -1, type, dev, &a.out_row, &a.out_head);
       need(out.size(1) == q.size(1), "q_out must have q's heads");
+      apart(out, "q_out");
       a.q_out = out.data_ptr();
     }
   } else {
@@ -356,6 +365,7 @@ mk_attention_args attention_args(PyObject *const *o, const mk_paged_kv &kv, cons
   if (o[T_OUT]) {
     const at::Tensor &out = tensor(o[T_OUT], "out");
     heads(out, "out", n, d, hq, type, dev, &a.out_row, &a.out_head);
+    apart(out, "out");
     a.out = out.data_ptr();
   }
   if (o[T_LSE]) {
@@ -443,8 +453,11 @@ mk_matvec_q4_args matvec_args(PyObject *const *o, bool on_device, c10::Device *d
     const at::Tensor &t = tensor(o[i], i == M_OUT ? "out" : "residual");
     if (t.dim() != 2 || t.size(0) != m || t.size(1) != n || t.scalar_type() != type || t.device() != dev || (t.stride(1) != 1 && n > 1))
       throw Bad{std::string(i == M_OUT ? "out" : "residual") + " must be [" + std::to_string(m) + "][" + std::to_string(n) + "] of x's dtype on its device, rows contiguous"};
-    if (i == M_OUT) a.y = t.data_ptr(), a.y_row = t.stride(0);
-    else a.residual = t.data_ptr(), a.residual_row = t.stride(0);
+    if (i == M_OUT) {
+      apart(t, "out");
+      need(t.data_ptr() != a.x || !m || !n, "out must not be x, which is read until the last of it is written");
+      a.y = t.data_ptr(), a.y_row = t.stride(0);
+    } else a.residual = t.data_ptr(), a.residual_row = t.stride(0);
   }
   *device = dev;
   return a;

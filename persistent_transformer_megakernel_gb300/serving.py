@@ -4,7 +4,7 @@
 the projections, each one call of the C ABI (``include/mk.h``).  They enqueue on
 the stream and return; what only the device can see (a page id outside the
 cache, a position outside the rotary table) goes to an optional ``status`` word
-that ``check_status`` turns into an ``MKError``.
+that ``check_status`` turns into an ``MKError``.  They have no gradients.
 
 The three are functions of the module ``_mktorch`` (``csrc/mk_torch.cpp``), which
 checks the tensors of a call against what the kernels read and write (a wrong

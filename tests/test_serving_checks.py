@@ -234,3 +234,20 @@ def test_rope_table():
     a = U.rotary(torch.arange(5), 64)
     assert t.shape == (5, 32, 2) and t.dtype == F32
     assert torch.equal(t[..., 0], a.cos().float()) and torch.equal(t[..., 1], a.sin().float())
+
+
+def test_what_is_written_is_not_expanded():
+    for kw in (dict(q_out=torch.zeros((1, 4, 64)).expand(3, -1, -1)), dict(q_out=torch.zeros((3, 1, 64)).expand(-1, 4, -1)),
+               dict(k_cache=torch.zeros((1, 2, 16, 64), dtype=BF16).expand(6, -1, -1, -1), v_cache=torch.zeros((1, 2, 16, 64), dtype=BF16).expand(6, -1, -1, -1))):
+        with pytest.raises(ValueError, match="expanded"):
+            _append(**kw)
+    for out in (torch.zeros((1, 4, 64)).expand(3, -1, -1), torch.zeros((3, 1, 64)).expand(-1, 4, -1)):
+        with pytest.raises(ValueError, match="expanded"):
+            _attention(q=torch.zeros((3, 4, 64)), out=out)
+    x = torch.zeros((3, 128))
+    codes, scales = torch.zeros((128, 64), dtype=torch.uint8), torch.zeros((128, 2), dtype=BF16)
+    with pytest.raises(ValueError, match="expanded"):
+        _matvec(x=x, codes=codes, scales=scales, residual=None, zeros=None, out=torch.zeros((1, 128)).expand(3, -1))
+    with pytest.raises(ValueError, match="must not be x"):
+        _matvec(x=x, codes=codes, scales=scales, residual=None, zeros=None, out=x)
+    _matvec(x=x, codes=codes, scales=scales, residual=x, zeros=None, out=torch.zeros((3, 128)))
