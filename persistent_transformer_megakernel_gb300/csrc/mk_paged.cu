@@ -7,16 +7,12 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
-#include <functional>
-#include <mutex>
 #include <type_traits>
 
 #include "mk_launch_after.h"
 #include "mk_mma.cuh"
 
 namespace mkv {
-
-constexpr int kMaxDevices = 64;
 
 __device__ __forceinline__ void report(int32_t *status, int code) {
   if (status) atomicCAS(status, 0, code);
@@ -147,19 +143,6 @@ __device__ __forceinline__ void store_cache(__nv_fp8_e4m3 *p, const Two *x) {
 }
 
 constexpr int kAppendThreads = 128, kAppendCtas = 6;
-
-// a kernel's largest dynamic shared memory on a device, set at its first launch there
-struct MaxSmem {
-  std::once_flag once;
-  bool ok = false;
-  bool set(const void *fn, int bytes) {
-    std::call_once(once, [&] {
-      ok = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
-      if (!ok) cudaGetLastError();
-    });
-    return ok;
-  }
-};
 
 template <int N>
 __device__ __forceinline__ void load_gains(const uint16_t *p, Two *x) {
@@ -476,10 +459,10 @@ int launch_append(AppendParams p, cudaStream_t s) {
   p.kv_groups = (p.hkv + kStreamHeads - 1) / kStreamHeads;
   const int parts = (p.q_groups + 2 * p.kv_groups + 32 / TPH - 1) / (32 / TPH);   // warps of a token
   if (static_cast<int64_t>(p.n) * heads * TPH > static_cast<int64_t>(sms) * kAppendCtas * kAppendThreads && parts <= sms * kStreamWarps) {
-    static MaxSmem ready[kMaxDevices];
+    static mkw::Ready ready[mkw::kMaxDevices];
     constexpr int smem = kStreamWarps * 2 * kStreamPieces * 512;
     const auto fn = &append_many_kernel<T, C, D>;
-    if (!ready[dev].set(reinterpret_cast<const void *>(fn), smem)) return MK_ERR_CUDA;
+    if (!ready[dev].get(reinterpret_cast<const void *>(fn), 32 * kStreamWarps, smem)) return MK_ERR_CUDA;
     p.parts.set(parts);
     p.streams = sms * kStreamWarps / parts;
     return mkw::launch_after(fn, dim3(sms), 32 * kStreamWarps, smem, s, p);
@@ -1314,14 +1297,14 @@ __global__ void __launch_bounds__(kAttnThreads) join_kernel(const __grid_constan
 }
 
 int sm_count(int *device) {
-  static std::atomic<int> known[kMaxDevices];
+  static std::atomic<int> known[mkw::kMaxDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return -1;
   }
   if (device) *device = dev;
-  if (dev < 0 || dev >= kMaxDevices) return -1;
+  if (dev < 0 || dev >= mkw::kMaxDevices) return -1;
   int n = known[dev].load(std::memory_order_relaxed);
   if (n == 0) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
@@ -1333,41 +1316,13 @@ int sm_count(int *device) {
   return n;
 }
 
-// How a kernel can be launched on a device, looked up at its first launch there: clusters[i] clusters of 2^(i + 1) CTAs
-// fit on it at once.
-struct Ready {
-  std::once_flag once;
-  bool ok = false;
-  int clusters[4] = {};
-};
-
-void make_ready(Ready &r, const void *fn) {
-  r.ok = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) == cudaSuccess &&
-         cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
-  for (int i = 0; i < 4 && r.ok; ++i) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2 << i;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.gridDim = dim3(2 << i);
-    cfg.blockDim = dim3(kAttnThreads);
-    cfg.dynamicSmemBytes = kMaxSmem;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&r.clusters[i], fn, &cfg) != cudaSuccess) r.clusters[i] = 0;
-  }
-  cudaGetLastError();
-}
-
 template <class T, bool FP8, int D, int HB>
 int launch_heads(AttnParams &p, int grid, int dev, cudaStream_t s) {
   using TL = Tile<D, FP8>;
-  static Ready ready[kMaxDevices];
+  static mkw::Ready ready[mkw::kMaxDevices];
   const auto fn = &attend_kernel<T, FP8, D, HB>;
-  Ready &r = ready[dev];
-  std::call_once(r.once, make_ready, std::ref(r), reinterpret_cast<const void *>(fn));
-  if (!r.ok) return MK_ERR_CUDA;
+  mkw::Ready &r = ready[dev];
+  if (!r.get(reinterpret_cast<const void *>(fn), kAttnThreads, kMaxSmem)) return MK_ERR_CUDA;
   const int64_t tiles = (p.window > 0 ? std::min(p.window, p.capacity) : p.capacity) / TL::POS + 2;   // of a row at most
   p.way = tiles <= kShortTiles ? kWhole : kJoined;
   p.cluster = 1;

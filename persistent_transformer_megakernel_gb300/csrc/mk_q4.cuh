@@ -28,17 +28,19 @@
 // One persistent CTA of 16 warps an SM, so that x is staged once an SM (for 8 rows
 // that is a third of the work of a 1.7B-shaped gate and up projection).  The rows'
 // tiles are dealt out to its warps; 2 to 16 of them share a tile's k where that
-// deals the blocks out more evenly, their sums added in order.
+// deals the blocks out more evenly, their sums added in order.  Where x is large
+// beside the weights, reading and staging all of it in every SM is most of the
+// time: there clusters of four CTAs take a quarter of k each, and add the sums of
+// their tiles in order through their shared memory.
 //
 // Measured: 1 x 151936 x 1024, groups of 128 (80 MB) 17.5 us, 4.6 TB/s: instructions beside bytes; 8 x 12288 x 2048,
-// groups of 32 with zeros, bf16 x, 10.7 us and 3 x 2048 x 6144, groups of 64, 7.6 us: instructions and the staging of x;
-// 1 x 4096 x 1024 3.8 us: latency.
+// groups of 32 with zeros, bf16 x, 10.8 us and 3 x 2048 x 6144, groups of 64, 7.5 us: instructions and the staging of x;
+// 1 x 4096 x 1024 3.9 us: latency.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 #include "../../include/mk.h"
@@ -51,6 +53,7 @@ namespace mkq {
 constexpr int kWarps = 16, kThreads = 32 * kWarps, kBlock = 128;
 constexpr int kRing = 4096;            // bytes of codes a warp has room for: 4 blocks of 16 rows (twice as many measured slower)
 constexpr int kMaxSmem = 225 * 1024;   // dynamic shared memory of a CTA
+constexpr int kMaxInbox = 16384;       // of a cluster's CTA, for the tiles that it joins
 constexpr int red_bytes(int nt, int rt) { return kWarps * 16 * rt * 8 * nt * 4; }   // sums of the warps
 
 // G: 32, 64, or 128 for every multiple of it
@@ -132,7 +135,8 @@ __device__ __forceinline__ uint32_t take_codes(uint32_t x, uint32_t mask) {
   return r;
 }
 
-template <class T, int NT, int RT, int G, bool ZEROS>
+// C: CTAs of a cluster, which have a slice of k each
+template <class T, int NT, int RT, int G, bool ZEROS, int C>
 __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_constant__ Q4Params p) {
   using L = Layout<G>;
   constexpr int TERMS = kTerms<T>, GB = L::groups;
@@ -141,22 +145,25 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
   __shared__ uint32_t s_max[COLS];
   __shared__ float s_to[COLS], s_back[COLS];               // the powers of two that x rows are multiplied by, and their inverses
   mkw::follow_previous_kernel();
+  if (C > 1) mkw::cluster_arrive();                        // (waited for before the others' memory is written)
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int rank = blockIdx.x % C, cluster = blockIdx.x / C, clusters = gridDim.x / C;
   const int wn = w / p.wk, wk = w % p.wk, per_cta = kWarps / p.wk;
   const int m0 = blockIdx.y * p.pass_rows, mr = min(p.pass_rows, p.m - m0), cols = mr * TERMS;
   unsigned char *ring = smem + w * kRing, *xs = smem + kWarps * kRing;
   float *red = reinterpret_cast<float *>(xs + p.pass_rows * TERMS * p.pitch) + wn * p.wk * ROWS * COLS;   // sums of the warps of this tile
 
-  // this warp's slice of the blocks of k, its tiles
-  const int b0 = p.blocks * wk / p.wk, nb = p.blocks * (wk + 1) / p.wk - b0;
-  const int tile0 = blockIdx.x * per_cta + wn, step = gridDim.x * per_cta;
+  // the CTA's blocks of k, this warp's slice of them, its tiles
+  const int c0 = p.blocks * rank / C, cb = p.blocks * (rank + 1) / C - c0;
+  const int b0 = cb * wk / p.wk, nb = cb * (wk + 1) / p.wk - b0;
+  const int tile0 = cluster * per_cta + wn, step = clusters * per_cta;
   const int rounds = tile0 < p.tiles ? (p.tiles - tile0 + step - 1) / step : 0;
   const int items = rounds * nb;
 
   // ---- x, and the largest value of every row.  The weights are asked for when x is there: before, its answer waits
   // behind theirs ------------------------------------------------------------------------------------------------
-  const T *x = static_cast<const T *>(p.x) + m0 * p.x_row;
-  const int eighths = p.blocks * (kBlock / 8), last = p.k / 8, all = mr * eighths;
+  const T *x = static_cast<const T *>(p.x) + m0 * p.x_row + c0 * kBlock;
+  const int eighths = p.eighths.value, last = C == 1 ? p.k / 8 : min(p.k / 8 - c0 * (kBlock / 8), cb * (kBlock / 8)), all = mr * eighths;
   auto read = [&](int i, Eight<T> &e) {                    // eighth i % eighths of row i / eighths, if it is there
     const int r = p.eighths.quotient(i), b = i - r * eighths;
     if (b < last) e.load(x + r * p.x_row + b * 8);
@@ -195,10 +202,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
 #pragma unroll
         for (int r = 0; r < 2 * RT; ++r) {
           const int64_t row = min(c_tile * ROWS + 8 * r + g, p.n - 1);             // rows past the last are read as it and not stored
-          code_at[r] = p.codes + row * (p.k / 2) + b0 * (kBlock / 2) + t * 16;
+          code_at[r] = p.codes + row * (p.k / 2) + (c0 + b0) * (kBlock / 2) + t * 16;
         }
       }
-      const bool there = G == 128 || (b0 + c_blk) * kBlock + t * 32 < p.k;
+      const bool there = G == 128 || (c0 + b0 + c_blk) * kBlock + t * 32 < p.k;
 #pragma unroll
       for (int r = 0; r < 2 * RT; ++r) {
         const uint32_t to = ring_at + c_stage * STAGE + chunk_at(8 * r + g, t);
@@ -226,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
     if (s_left > 0) {
       --s_left;
       if (s_blk == 0) group_at = static_cast<int64_t>(min(s_tile * ROWS + lane % ROWS, p.n - 1)) * p.groups;
-      const int blk = b0 + s_blk;
+      const int blk = c0 + b0 + s_blk;
       const int64_t at = group_at + (G == 128 ? p.blocks_a_group.quotient(blk) : blk * GB);
       const uint16_t *sc = p.scales + at;
       const uint8_t *z = p.zeros + at;
@@ -400,7 +407,22 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
     if (p.residual) y += to_float(static_cast<const T *>(p.residual)[(m0 + m) * p.residual_row + row]);
     put(static_cast<T *>(p.y) + (m0 + m) * p.y_row + row, y);
   };
-  // a tile's sums: a lane has rows g and g + 8 by columns 2t and 2t + 1, which are the two terms of one x row or two x rows
+  // a part of a tile's sums: a lane has rows g and g + 8 by columns 2t and 2t + 1, the two terms of one x row or two x rows
+  auto store_part = [&](int row, int c, float4 y) {
+    if constexpr (TERMS == 2) {
+      store(row, c * 4 + t, y.y + y.x);
+      store(row + 8, c * 4 + t, y.w + y.z);
+    } else {
+      store(row, c * 8 + 2 * t, y.x);
+      store(row, c * 8 + 2 * t + 1, y.y);
+      store(row + 8, c * 8 + 2 * t, y.z);
+      store(row + 8, c * 8 + 2 * t + 1, y.w);
+    }
+  };
+  // A cluster's CTAs have a slice of k each of the same tiles: what each has of the jth of a CTA's tiles goes to the inbox of
+  // CTA j % C, in place j / C.
+  float4 *inbox = reinterpret_cast<float4 *>(smem + p.inbox);   // [place][CTA][RT NT][32 lanes]
+  int round = 0;
   auto finish = [&]() {
     if (p.wk > 1) {
       // over the warps that share the tile, each adding up its part of the lanes' values
@@ -430,28 +452,24 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
 #pragma unroll
       for (int c = 0; c < NT; ++c) {
         if (p.wk == 1 || (r * NT + c) % p.wk == wk) {
-          const int row = tile * ROWS + r * 16 + g;
-          if constexpr (TERMS == 2) {
-            const int m = c * 4 + t;
-            store(row, m, (sum[r][c][1] + sum[r][c][0]) * back[c][0]);
-            store(row + 8, m, (sum[r][c][3] + sum[r][c][2]) * back[c][0]);
+          const float4 y = make_float4(sum[r][c][0] * back[c][0], sum[r][c][1] * back[c][1], sum[r][c][2] * back[c][0], sum[r][c][3] * back[c][1]);
+          if constexpr (C == 1) {
+            store_part(tile * ROWS + r * 16 + g, c, y);
           } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              store(row, c * 8 + 2 * t + j, sum[r][c][j] * back[c][j]);
-              store(row + 8, c * 8 + 2 * t + j, sum[r][c][2 + j] * back[c][j]);
-            }
+            const int j = round * per_cta + wn;
+            const uint32_t to = mkw::remote(inbox + ((j / C * C + rank) * RT * NT + r * NT + c) * 32 + lane, j % C);
+            mkw::store_remote(to, y.x), mkw::store_remote(to + 4, y.y), mkw::store_remote(to + 8, y.z), mkw::store_remote(to + 12, y.w);
           }
         }
         sum[r][c][0] = sum[r][c][1] = sum[r][c][2] = sum[r][c][3] = 0.f;
       }
     tile += step;
+    ++round;
   };
 
-  if (nb == 0) {                                           // fewer blocks than warps: this one only joins in
+  if (C > 1) mkw::cluster_wait();
+  if (nb == 0)                                             // fewer blocks than warps: this one only joins in
     for (int i = 0; i < rounds; ++i) finish();
-    return;
-  }
 #pragma unroll 1
   for (int i = 0; i < items; ++i) {
     copy();
@@ -469,39 +487,68 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
     }
   }
   mkw::cp_async_wait<0>();
+  if constexpr (C == 1) return;
+  mkw::cluster_arrive();
+  mkw::cluster_wait();
+  // the slices' sums, in order, by a warp each 16 rows and 8 columns
+#pragma unroll 1
+  for (int i = w;; i += kWarps) {
+    const int part = i % (RT * NT), place = i / (RT * NT), j = place * C + rank, at = cluster * per_cta + j % per_cta + j / per_cta * step;
+    if (j / per_cta * step + cluster * per_cta >= p.tiles) break;
+    if (at >= p.tiles) continue;
+    float4 y = inbox[(place * C * RT * NT + part) * 32 + lane];
+#pragma unroll 1
+    for (int c = 1; c < C; ++c) {
+      const float4 z = inbox[((place * C + c) * RT * NT + part) * 32 + lane];
+      y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+    }
+    store_part(at * ROWS + part / NT * 16 + g, part % NT, y);
+  }
 }
 
-template <class T, int NT, int RT, int G, bool ZEROS>
-int launch(Q4Params p, int sms, int dev, cudaStream_t s) {
-  static std::atomic<uint64_t> ready{0};
-  const auto fn = &matvec_kernel<T, NT, RT, G, ZEROS>;
-  if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
-    if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) {
-      cudaGetLastError();
-      return MK_ERR_CUDA;
-    }
-    ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
-  }
+template <class T, int NT, int RT, int G, bool ZEROS, int C>
+int launch_as(Q4Params p, int sms, int dev, cudaStream_t s) {
+  static_assert(C == 1 || C == 4);
+  static mkw::Ready ready[mkw::kMaxDevices];
+  const auto fn = &matvec_kernel<T, NT, RT, G, ZEROS, C>;
+  mkw::Ready &r = ready[dev];
+  if (!r.get(reinterpret_cast<const void *>(fn), kThreads, kMaxSmem)) return MK_ERR_CUDA;
   p.tiles = (p.n + 16 * RT - 1) / (16 * RT);
-  p.pitch = p.blocks * kBlock * 2 + Layout<G>::pad;
   constexpr int per = kBlock / G;
   p.vec = p.groups % per == 0 && reinterpret_cast<uintptr_t>(p.scales) % (2 * per) == 0 &&
           reinterpret_cast<uintptr_t>(p.zeros) % per == 0;
+  const int clusters = C == 1 ? sms : r.clusters[1];
+  if constexpr (C > 1) {
+    // (the inbox is 16 RT rows of every tile of a CTA)
+    if (clusters < 1 || p.tiles / clusters * RT * NT * 512 > kMaxInbox) return launch_as<T, NT, RT, G, ZEROS, 1>(p, sms, dev, s);
+  }
+  const int blocks = (p.blocks + C - 1) / C;   // of a CTA
+  p.pitch = blocks * kBlock * 2 + Layout<G>::pad;
+  p.eighths.set(blocks * (kBlock / 8));
   // the sharing of k that leaves the busiest warp the fewest blocks, fewer warps a tile where that is equal
   int64_t best = 0;
   for (int wk = 1; wk <= kWarps; wk *= 2) {
-    const int64_t per_round = static_cast<int64_t>(sms) * (kWarps / wk), rounds = (p.tiles + per_round - 1) / per_round;
-    const int64_t cost = rounds * ((p.blocks + wk - 1) / wk);
+    const int64_t per_round = static_cast<int64_t>(clusters) * (kWarps / wk), rounds = (p.tiles + per_round - 1) / per_round;
+    const int64_t cost = rounds * ((blocks + wk - 1) / wk);
     if (wk == 1 || cost < best) best = cost, p.wk = wk;
   }
+  const int per_cta = kWarps / p.wk, want = std::min((p.tiles + per_cta - 1) / per_cta, clusters);
   // x rows of a pass: as many as its columns hold and shared memory has room for
-  const int red = p.wk > 1 ? red_bytes(NT, RT) : 0;
-  p.pass_rows = std::min({p.m, 8 * NT / kTerms<T>, (kMaxSmem - kWarps * kRing - red) / p.pitch / kTerms<T>});
-  const int smem = kWarps * kRing + red + p.pass_rows * kTerms<T> * p.pitch;
+  const int red = p.wk > 1 ? red_bytes(NT, RT) : 0, rounds = (p.tiles + want * per_cta - 1) / (want * per_cta);
+  const int inbox = C > 1 ? (rounds * per_cta + C - 1) / C * C * RT * NT * 512 : 0;
+  p.pass_rows = std::min({p.m, 8 * NT / kTerms<T>, (kMaxSmem - kWarps * kRing - red - inbox) / p.pitch / kTerms<T>});
+  p.inbox = kWarps * kRing + red + p.pass_rows * kTerms<T> * p.pitch;
   const int passes = (p.m + p.pass_rows - 1) / p.pass_rows;
   if (passes > 65535) return MK_ERR_UNSUPPORTED;
-  const int per_cta = kWarps / p.wk, want = (p.tiles + per_cta - 1) / per_cta;
-  return mkw::launch_after(fn, dim3(std::min(want, sms), passes), kThreads, smem, s, p);
+  return mkw::launch_after(fn, dim3(want * C, passes), kThreads, p.inbox + inbox, s, p, C);
+}
+
+template <class T, int NT, int RT, int G, bool ZEROS>
+int launch(const Q4Params &p, int sms, int dev, cudaStream_t s) {
+  if constexpr (RT == 1) {
+    if (p.cluster > 1) return launch_as<T, NT, RT, G, ZEROS, 4>(p, sms, dev, s);
+  }
+  return launch_as<T, NT, RT, G, ZEROS, 1>(p, sms, dev, s);
 }
 
 template <class T, int NT, int RT, bool ZEROS>
@@ -515,9 +562,15 @@ int by_group(Q4Params &p, int group, int sms, int dev, cudaStream_t s) {
 template <class T, bool ZEROS>
 int by_rows(Q4Params &p, int group, int sms, int dev, cudaStream_t s) {
   p.blocks = (p.k + kBlock - 1) / kBlock;
-  p.eighths.set(p.blocks * (kBlock / 8));
+  // Clusters of 4 CTAs with a quarter of k each, where what is staged of x is 48 KB and as much as a CTA's codes.  (8 x
+  // 2048 x 6144 in bf16 7.4 us against 11.1 with all of x in every CTA, 16 x 4096 x 4096 9.7 and 14.1, 2 x 1024 x 16384 in
+  // fp32 7.3 and 12.3, 8 x 4096 x 6144 in bf16, 1.2 times the codes, 9.5 and 12.5, 3 x 2048 x 6144 in fp32 7.5 and 7.6; but
+  // 3 x 4096 x 6144 in fp32, 0.9 times, 9.2 both ways, 2 x 4096 x 8192 in fp32, 0.6 times, 10.2 and 10.0, 8 x 12288 x 2048
+  // in bf16, 33 KB, 11.7 and 10.8: a cluster's launch alone costs 1 us.  Clusters of 2 or 8 were slower where clusters paid.)
+  const int64_t staged = static_cast<int64_t>(p.m) * p.k * kTerms<T> * 2, codes = static_cast<int64_t>(p.n) * p.k / 2 / sms;
+  p.cluster = staged >= 49152 && staged >= codes ? 4 : 1;
   const int cols = p.m > 32 ? 32 : p.m * kTerms<T>;
-  auto room = [&](int nt) { return (kMaxSmem - kWarps * kRing - red_bytes(nt, 1)) / (p.blocks * kBlock * 2 + 64); };
+  auto room = [&](int nt) { return (kMaxSmem - kWarps * kRing - red_bytes(nt, 1) - (p.cluster > 1 ? kMaxInbox : 0)) / ((p.blocks + p.cluster - 1) / p.cluster * kBlock * 2 + 64); };
   if (cols <= 8 || room(2) < 16) {
     // 32 rows a tile, whose matrix products share what is read of x, where every warp has one of them
     if (p.n / 32 >= sms * kWarps && p.m <= 8 / kTerms<T>) return by_group<T, 1, 2, ZEROS>(p, group, sms, dev, s);

@@ -17,8 +17,10 @@ struct Q4Params {
   int64_t x_row, residual_row, y_row;
   int m, n, k, groups;
   mkw::Divisor blocks_a_group;   // groups of 128 and more
-  mkw::Divisor eighths;          // 8-element parts of the blocks of k
+  mkw::Divisor eighths;          // 8-element parts of a CTA's blocks of k, room for them
   int blocks;           // of k, the last one maybe short
+  int cluster;          // CTAs that have a slice of k each
+  int inbox;            // byte where the others' sums are put
   int pass_rows;        // x rows of one pass (blockIdx.y)
   int wk;               // warps that share a tile's k: 1, 2, 4, 8 or 16
   int tiles;            // tiles of 16 RT rows

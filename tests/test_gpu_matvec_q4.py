@@ -141,3 +141,51 @@ def test_quantised_weights(zeros):
     x = torch.randn((2, 256), generator=torch.Generator().manual_seed(10))
     y = mk.matvec_q4(x.cuda(), q[0], q[1], zeros=q[2] if zeros else None)
     _check(y, x, U.dequantize(*q), None, "quantised")
+
+
+# What is staged of x outweighs the weights: clusters of four CTAs with a slice of k each (fewer blocks than CTAs, blocks that
+# do not divide by four, a broken last block, many tiles a cluster, several passes, one row of the longest k).
+@pytest.mark.parametrize("x", [BF16, F32])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("m,n,k,group", [
+    (100, 50, 256, 64), (200, 33, 128, 128), (60, 131, 416, 32), (40, 300, 640, 128), (30, 17, 1088, 64), (16, 2100, 4096, 128),
+    (8, 2048, 6144, 32), (12, 5120, 5120, 64), (7, 16, 4480, 128), (33, 1000, 2944, 64)])
+def test_slices_of_k(x, zeros, m, n, k, group):
+    _run(m, n, k, group, x, zeros, residual=True, seed=21)
+
+
+def test_slices_of_k_with_special_values():
+    m, k = 48, 768
+    codes, scales, _ = _weights(70, k, 32, False, seed=22)
+    codes[:] = 0x9A                                         # every weight is positive
+    x = torch.ones((m, k))
+    x[1, 5], x[2, 700], x[3, 0], x[3, 767] = float("inf"), float("nan"), 3e38, -3e38
+    x[4], x[5, :400], x[6, 200:] = 0.0, 0.0, 1e-30          # nothing at all, in some slices, next to nothing in others
+    x[7, 3], x[7, 640] = float("inf"), -float("inf")
+    w = U.dequantize(codes, scales)
+    y = mk.matvec_q4(x.cuda(), codes.cuda(), scales.cuda()).cpu()
+    assert (y[1] == float("inf")).all() and torch.isnan(y[2]).all() and torch.isnan(y[7]).all() and (y[4] == 0).all()
+    rest = [0, 3, 5, 6] + list(range(8, m))
+    _check(y[rest], x[rest], w, None, "rows beside the special ones")
+
+
+def test_slices_of_k_same_bits_on_streams_and_in_graphs():
+    codes, scales, z = (t.cuda() for t in _weights(900, 2048, 64, True, seed=23))
+    x = torch.randn((20, 2048), generator=torch.Generator().manual_seed(24)).cuda()
+    res = torch.randn((20, 900), generator=torch.Generator().manual_seed(25)).cuda()
+    want = mk.matvec_q4(x, codes, scales, zeros=z, residual=res)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = [mk.matvec_q4(x, codes, scales, zeros=z, residual=res, stream=s) for _ in range(3)]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    y = torch.empty_like(res)
+    with torch.cuda.graph(g):
+        y.copy_(res)
+        mk.matvec_q4(x, codes, scales, zeros=z, residual=y, out=y)   # in place
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+    for t in got:
+        assert torch.equal(t, want)
