@@ -555,6 +555,7 @@ struct AttnParams {
   float *parts;        // [grid][2][gr][D + 4]: a row's middle or end (0) and its beginning (1)
   mkw::Divisor page_size;
   int n, hq, hkv, group, n_pages, capacity, window;   // capacity: slots of a table row
+  mkw::Divisor chunks;       // of 16 query heads
   mkw::Divisor blocks, vh;   // head blocks of 16 query heads a kv head, virtual heads hkv * blocks
   int gr;              // query heads of a block: min(group, 16)
   int row_cost;
@@ -937,15 +938,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
   const bool any = left > 0;
   if (EARLY && any) load_query(row, vh);
 
-  // ---- rows without tiles -----------------------------------------------------
+  // ---- rows without tiles, 16 query heads a warp --------------------------------
 #pragma unroll 1
-  for (int r = cta; r < p.n; r += gridDim.x) {
-    const int len = p.lengths[r];
+  for (int i = cta * kWarps + w; i < p.n * static_cast<int>(p.chunks.value); i += gridDim.x * kWarps) {
+    const int r = p.chunks.quotient(i), h0 = 16 * (i - r * static_cast<int>(p.chunks.value)), len = p.lengths[r];
     if (len < 0 || span_of<POS>(p, len).count > 0) continue;
     const float l = len == 0 ? 0.f : NAN;
     if (len > 0 && lane == 0) report(p.status, MK_ERR_BAD_PAGE);
 #pragma unroll 1
-    for (int h = w; h < p.hq; h += kWarps) {
+    for (int h = h0; h < min(p.hq, h0 + 16); ++h) {
       float x[D / 32] = {};
       write_head<T, D>(p, lane, r, h, 0.f, l, x, 1.f);
     }
@@ -1491,6 +1492,7 @@ extern "C" int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args
   p.n_pages = kv->n_pages;
   p.page_size.set(kv->page_size);
   p.window = a->window;
+  p.chunks.set((p.hq + 15) / 16);
   p.blocks.set((p.group + 15) / 16);
   p.vh.set(p.hkv * ((p.group + 15) / 16));
   p.gr = std::min(p.group, 16);
