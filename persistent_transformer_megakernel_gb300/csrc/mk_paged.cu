@@ -655,6 +655,16 @@ __device__ __forceinline__ Heads heads_of(const AttnParams &p, int vh) {
   return h;
 }
 
+// a lane's part of a row of D fp32 elements, on a boundary of its size
+__device__ __forceinline__ void load_part(const float *p, float (&x)[4]) {
+  const float4 v = *reinterpret_cast<const float4 *>(p);
+  x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+}
+__device__ __forceinline__ void load_part(const float *p, float (&x)[2]) {
+  const float2 v = *reinterpret_cast<const float2 *>(p);
+  x[0] = v.x, x[1] = v.y;
+}
+
 // Join parts of a query head in shared memory, in order, by a warp: lane l gets elements l D / 32 ..; lane j of `there`
 // knows the byte `mine_at` where its part's o[D], m, l are.  (Small on purpose: code that runs once a launch takes as
 // long as it is.)
@@ -667,12 +677,14 @@ __device__ __forceinline__ void join_shared(int lane, unsigned there, const unsi
 #pragma unroll 1
   for (; there; there &= there - 1u) {
     const float *part = reinterpret_cast<const float *>(smem + __shfl_sync(0xffffffffu, mine_at, __ffs(there) - 1));
+    float xj[D / 32];
+    load_part(part + lane * (D / 32), xj);
     const float mj = part[D], lj = part[D + 1], mx = fmaxf(m, mj), base = join_base(mx);
     const float f = mkw::exp2_fast(m - base), fj = mkw::exp2_fast(mj - base);
     m = mx;
     l = l * f + lj * fj;
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) x[k] = x[k] * f + part[lane * (D / 32) + k] * fj;
+    for (int k = 0; k < D / 32; ++k) x[k] = x[k] * f + xj[k] * fj;
   }
 }
 
@@ -697,13 +709,10 @@ __device__ __forceinline__ void join_parts(int lane, unsigned there, const void 
     const int j = __ffs(rest) - 1;
     const float fj = __shfl_sync(0xffffffffu, f, j);
     const float *part = at(__shfl_sync(0xffffffffu, mine_at, j)) + lane * (D / 32);
-    if constexpr (D == 128) {
-      const float4 v = *reinterpret_cast<const float4 *>(part);
-      x[0] += fj * v.x, x[1] += fj * v.y, x[2] += fj * v.z, x[3] += fj * v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2 *>(part);
-      x[0] += fj * v.x, x[1] += fj * v.y;
-    }
+    float xj[D / 32];
+    load_part(part, xj);
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) x[k] += fj * xj[k];
   }
 }
 
@@ -1173,8 +1182,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
           for (int h = 0; h < min(8, rows - 8 * hb); ++h) {
             const float *from = part + h * PST;
             float x[D / 32];
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) x[k] = from[lane * (D / 32) + k];
+            load_part(from + lane * (D / 32), x);
             write_head<T, D>(p, lane, ti.row, head0 + 8 * hb + h, from[D], from[D + 1], x, vsc);
           }
           __syncwarp();
