@@ -432,6 +432,17 @@ typedef struct {
  * them), MK_ERR_UNSUPPORTED (head_dim, more than 2^31 tiles of work), MK_ERR_CUDA. */
 int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args *a, mk_stream stream);
 
+/* mk_paged_attention for callers with an allocator of their own: `workspace` is
+ * called, at most once and before anything is enqueued, with `context` and the
+ * bytes of a workspace if the call needs one (one row, and rows of up to about a
+ * thousand slots, need none); the arguments' workspace and workspace_bytes are
+ * not looked at.  Its result is device memory on a 16-byte boundary that is the
+ * call's own until the stream has passed it, or NULL (MK_ERR_NO_MEMORY).  It must
+ * return: an exception must not pass through this call. */
+typedef void *(*mk_workspace_fn)(void *context, int64_t bytes);
+int mk_paged_attention_ask(const mk_paged_kv *kv, const mk_attention_args *a, mk_workspace_fn workspace,
+                           void *context, mk_stream stream);
+
 /* Bytes of workspace any mk_paged_attention call with these heads needs on the
  * current device (it does not depend on rows or lengths).  MK_ERR_INVALID_ARG,
  * MK_ERR_UNSUPPORTED or MK_ERR_CUDA as a negative result. */

@@ -103,10 +103,12 @@ class mk_matvec_q4_args(C.Structure):
 
 
 #: every symbol include/mk.h declares
+WORKSPACE_FN = C.CFUNCTYPE(C.c_void_p, C.c_void_p, C.c_int64)    # (context, bytes)
+
 EXPORTS = ("mk_create", "mk_reset_kv", "mk_decode", "mk_prefill", "mk_decode_start", "mk_decode_wait",
            "mk_mailbox_read", "mk_decode_host", "mk_get_info", "mk_embed_sum",
            "mk_embed_sum_noalloc", "mk_destroy", "mk_error_string", "mk_plan_for", "mk_paged_append",
-           "mk_paged_attention", "mk_paged_attention_workspace", "mk_export_kv", "mk_matvec_q4")
+           "mk_paged_attention", "mk_paged_attention_ask", "mk_paged_attention_workspace", "mk_export_kv", "mk_matvec_q4")
 
 _lib = None
 
@@ -139,6 +141,7 @@ def load_library(path: Optional[str] = None):
     lib.mk_embed_sum_noalloc.argtypes = [vp, i32, i32, vp, i32, i32, vp, vp, i32, vp, vp]
     lib.mk_paged_append.argtypes = [C.POINTER(mk_paged_kv), C.POINTER(mk_append_args), vp]
     lib.mk_paged_attention.argtypes = [C.POINTER(mk_paged_kv), C.POINTER(mk_attention_args), vp]
+    lib.mk_paged_attention_ask.argtypes = [C.POINTER(mk_paged_kv), C.POINTER(mk_attention_args), WORKSPACE_FN, vp, vp]
     lib.mk_paged_attention_workspace.argtypes = [i32, i32, i32]
     lib.mk_export_kv.argtypes = [vp, i32, i32, i32, C.POINTER(mk_paged_kv), i32, i32, vp]
     lib.mk_matvec_q4.argtypes = [C.POINTER(mk_matvec_q4_args), vp]

@@ -523,7 +523,7 @@ int run_append(const AppendParams &p, int dtype, int cache, int d, cudaStream_t 
 // Parts are joined in order: the same lengths give the same bits.
 // Measured: 16 query heads on 8 of 128, 64 rows of 0 to 8192 tokens in bf16 (306 MB) 53 us, 5.7 TB/s; 16 rows of 30 to
 // 32 k in e4m3 (1034 MB) 157 us, 6.6 TB/s; one row of 257 tokens 6.9 us, of 5119 12.6 (fp32 queries); 256 rows of up to
-// 300 tokens, 8 heads on 2 of 64, 9.5 us.
+// 300 tokens, 8 heads on 2 of 64, 9.4 us.
 // ---------------------------------------------------------------------------
 
 constexpr int kWarps = 8, kAttnThreads = 32 * kWarps;
@@ -1325,8 +1325,16 @@ int sm_count(int *device) {
   return n;
 }
 
+// where a call's workspace comes from: the caller's, or his function, asked only if the call needs one
+struct Workspace {
+  void *given;
+  mk_workspace_fn ask;
+  void *context;
+  int64_t bytes;
+};
+
 template <class T, bool FP8, int D, int HB>
-int launch_heads(AttnParams &p, int grid, int dev, cudaStream_t s) {
+int launch_heads(AttnParams &p, const Workspace &ws, int grid, int dev, cudaStream_t s) {
   using TL = Tile<D, FP8>;
   static mkw::Ready ready[mkw::kMaxDevices];
   const auto fn = &attend_kernel<T, FP8, D, HB>;
@@ -1344,14 +1352,20 @@ int launch_heads(AttnParams &p, int grid, int dev, cudaStream_t s) {
   static_assert(kWarps * kStages * TL::STAGE + (kWarps * 16 + 16) * kPartStride<D> * 4 <= kMaxSmem, "16 heads, 16 CTAs");
   const int parts = (kWarps * p.gr + inbox) * kPartStride<D> * 4;
   const int ctas = p.way == kByCluster ? static_cast<int>(p.vh.value) * p.cluster : grid, smem = kWarps * kStages * TL::STAGE + parts;
+  if (p.way == kJoined) {
+    p.records = static_cast<int4 *>(ws.ask ? ws.ask(ws.context, ws.bytes) : ws.given);
+    if (!p.records) return MK_ERR_NO_MEMORY;
+    if (reinterpret_cast<uintptr_t>(p.records) & 15u) return MK_ERR_INVALID_ARG;
+    p.parts = reinterpret_cast<float *>(p.records + grid);
+  }
   const int rc = mkw::launch_after(fn, dim3(ctas), kAttnThreads, smem, s, p, p.cluster);
   if (rc != MK_OK || p.way != kJoined) return rc;
   return mkw::launch_after(&join_kernel<T, D>, dim3(grid, (p.gr + kWarps - 1) / kWarps), kAttnThreads, 0, s, p);
 }
 
 template <class T, bool FP8, int D>
-int launch_attend(AttnParams &p, int grid, int dev, cudaStream_t s) {
-  return p.gr <= 8 ? launch_heads<T, FP8, D, 1>(p, grid, dev, s) : launch_heads<T, FP8, D, 2>(p, grid, dev, s);
+int launch_attend(AttnParams &p, const Workspace &ws, int grid, int dev, cudaStream_t s) {
+  return p.gr <= 8 ? launch_heads<T, FP8, D, 1>(p, ws, grid, dev, s) : launch_heads<T, FP8, D, 2>(p, ws, grid, dev, s);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -1460,7 +1474,9 @@ extern "C" int64_t mk_paged_attention_workspace(int32_t n_q_heads, int32_t n_kv_
   return grid < 0 ? MK_ERR_CUDA : workspace_bytes(grid, n_q_heads / n_kv_heads, head_dim);
 }
 
-extern "C" int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args *a, mk_stream stream) {
+namespace {
+
+int attention(const mk_paged_kv *kv, const mk_attention_args *a, mk_stream stream, mk_workspace_fn ask, void *context) {
   int rc = check_cache(kv);
   if (rc != MK_OK) return rc;
   if (!a || a->n < 0 || a->n > kv->table_rows || (a->dtype != MK_F32 && a->dtype != MK_BF16) || a->window < 0 ||
@@ -1470,8 +1486,8 @@ extern "C" int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args
   if (rc != MK_OK) return rc;
   if (a->n == 0) return MK_OK;
   const int es = a->dtype == MK_F32 ? 4 : 2;
-  if (!a->q || !a->out || !a->lengths || !a->workspace || !aligned16(a->q) || !aligned16(a->out) ||
-      !aligned16(a->workspace) || !stride_ok(a->q_row, es) || !stride_ok(a->q_head, es) || !stride_ok(a->out_row, es) ||
+  if (!a->q || !a->out || !a->lengths || (!ask && !a->workspace) || !aligned16(a->q) || !aligned16(a->out) ||
+      (!ask && !aligned16(a->workspace)) || !stride_ok(a->q_row, es) || !stride_ok(a->q_head, es) || !stride_ok(a->out_row, es) ||
       !stride_ok(a->out_head, es))
     return MK_ERR_INVALID_ARG;
   // slots and the cost of all rows and heads are counted in 32 bits
@@ -1484,7 +1500,8 @@ extern "C" int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args
   if (grid < 0) return MK_ERR_CUDA;
   AttnParams p = {};
   p.group = a->n_q_heads / kv->n_kv_heads;
-  if (a->workspace_bytes < workspace_bytes(grid, p.group, kv->head_dim)) return MK_ERR_INVALID_ARG;
+  const Workspace ws = {a->workspace, ask, context, workspace_bytes(grid, p.group, kv->head_dim)};
+  if (!ask && a->workspace_bytes < ws.bytes) return MK_ERR_INVALID_ARG;
   p.q = a->q, p.k = kv->k, p.v = kv->v, p.out = a->out, p.lse = a->lse;
   p.q_row = a->q_row, p.q_head = a->q_head, p.out_row = a->out_row, p.out_head = a->out_head;
   p.page_stride = kv->page_stride, p.head_stride = kv->head_stride, p.slot_stride = kv->slot_stride;
@@ -1494,8 +1511,6 @@ extern "C" int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args
   p.lengths = a->lengths;
   p.k_scale = kv->k_scale, p.v_scale = kv->v_scale;
   p.status = a->status;
-  p.records = static_cast<int4 *>(a->workspace);
-  p.parts = reinterpret_cast<float *>(p.records + grid);
   p.n = a->n, p.hq = a->n_q_heads, p.hkv = kv->n_kv_heads;
   p.n_pages = kv->n_pages;
   p.page_size.set(kv->page_size);
@@ -1510,10 +1525,21 @@ extern "C" int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args
   using B = __nv_bfloat16;
   if (a->dtype == MK_F32) {
     if (kv->dtype == MK_BF16)
-      return kv->head_dim == 64 ? launch_attend<float, false, 64>(p, grid, dev, s) : launch_attend<float, false, 128>(p, grid, dev, s);
-    return kv->head_dim == 64 ? launch_attend<float, true, 64>(p, grid, dev, s) : launch_attend<float, true, 128>(p, grid, dev, s);
+      return kv->head_dim == 64 ? launch_attend<float, false, 64>(p, ws, grid, dev, s) : launch_attend<float, false, 128>(p, ws, grid, dev, s);
+    return kv->head_dim == 64 ? launch_attend<float, true, 64>(p, ws, grid, dev, s) : launch_attend<float, true, 128>(p, ws, grid, dev, s);
   }
   if (kv->dtype == MK_BF16)
-    return kv->head_dim == 64 ? launch_attend<B, false, 64>(p, grid, dev, s) : launch_attend<B, false, 128>(p, grid, dev, s);
-  return kv->head_dim == 64 ? launch_attend<B, true, 64>(p, grid, dev, s) : launch_attend<B, true, 128>(p, grid, dev, s);
+    return kv->head_dim == 64 ? launch_attend<B, false, 64>(p, ws, grid, dev, s) : launch_attend<B, false, 128>(p, ws, grid, dev, s);
+  return kv->head_dim == 64 ? launch_attend<B, true, 64>(p, ws, grid, dev, s) : launch_attend<B, true, 128>(p, ws, grid, dev, s);
+}
+
+}  // namespace
+
+extern "C" int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args *a, mk_stream stream) {
+  return attention(kv, a, stream, nullptr, nullptr);
+}
+
+extern "C" int mk_paged_attention_ask(const mk_paged_kv *kv, const mk_attention_args *a, mk_workspace_fn workspace, void *context,
+                                      mk_stream stream) {
+  return workspace ? attention(kv, a, stream, workspace, context) : MK_ERR_INVALID_ARG;
 }

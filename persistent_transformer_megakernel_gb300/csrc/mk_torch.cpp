@@ -21,6 +21,7 @@
 
 #include <cmath>
 #include <cstring>
+#include <exception>
 #include <optional>
 #include <string>
 
@@ -385,6 +386,22 @@ mk_attention_args attention_args(PyObject *const *o, const mk_paged_kv &kv, cons
   return a;
 }
 
+// a workspace from torch's allocator, of the current device and stream; what it throws does not pass the C entry point
+struct Memory {
+  c10::DataPtr held;
+  std::exception_ptr error;
+
+  static void *ask(void *context, int64_t bytes) {
+    Memory &m = *static_cast<Memory *>(context);
+    try {
+      m.held = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
+    } catch (...) {
+      m.error = std::current_exception();
+    }
+    return m.held.get();
+  }
+};
+
 PyObject *paged_attention(PyObject *const *o) {
   c10::Device dev(c10::kCPU);
   const mk_paged_kv kv = cache(o[T_KC], o[T_VC], o[T_TABLE], o[T_KS], o[T_VS], true, &dev);
@@ -399,11 +416,13 @@ PyObject *paged_attention(PyObject *const *o) {
     a.out_head = made.stride(1);
   }
   if (a.n) {
-    a.workspace_bytes = mk_paged_attention_workspace(a.n_q_heads, kv.n_kv_heads, kv.head_dim);
-    if (a.workspace_bytes < 0) throw Failed{static_cast<int>(a.workspace_bytes), "mk_paged_attention_workspace"};
-    const c10::DataPtr workspace = c10::cuda::CUDACachingAllocator::get()->allocate(a.workspace_bytes);   // (of the current device and stream)
-    a.workspace = workspace.get();
-    enqueue("mk_paged_attention", [&] { return mk_paged_attention(&kv, &a, on.stream); });
+    Memory workspace;
+    try {
+      enqueue("mk_paged_attention", [&] { return mk_paged_attention_ask(&kv, &a, &Memory::ask, &workspace, on.stream); });
+    } catch (const Failed &) {
+      if (workspace.error) std::rethrow_exception(workspace.error);
+      throw;
+    }
   }
   return o[T_OUT] ? given(o[T_OUT]) : THPVariable_Wrap(made);
 }

@@ -338,3 +338,37 @@ def test_wide_tables_of_short_rows(window, x, cache):
     _check(c, *want, window=window)
     wide = dict(c, table=torch.cat([c["table"], torch.full((60, 900), -1, dtype=torch.int32)], 1))
     _check(c, *_run(wide, window=window), window=window)
+
+
+def test_a_workspace_is_asked_for_where_it_is_needed():
+    import ctypes as C
+    B = mk._binding
+    lib = B.load_library()
+    asked, held = [], []
+
+    def give(context, n):
+        asked.append(n)
+        held.append(torch.empty(n, dtype=torch.uint8, device="cuda"))
+        return held[-1].data_ptr()
+    give, refuse = B.WORKSPACE_FN(give), B.WORKSPACE_FN(lambda context, n: None)
+    hq, hkv, d, page = 4, 2, 64, 16
+    g = torch.Generator().manual_seed(0)
+    kc, vc = (torch.randn((300, hkv, page, d), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    # rows of up to 64 tiles of 32 slots (heads of 64) are not cut: 100 pages are 50 tiles, 300 are 150
+    for rows, cols, needed in ((1, 300, 0), (3, 20, 0), (3, 100, 0), (3, 300, 1)):
+        table = torch.arange(rows * cols, dtype=torch.int32, device="cuda").view(rows, cols) % 300
+        lengths = torch.full((rows,), cols * page - 5, dtype=torch.int32, device="cuda")
+        q = torch.randn((rows, hq, d), generator=g).cuda()
+        want = mk.paged_attention(q, kc, vc, table, lengths)
+        out = torch.zeros_like(q)
+        kv = mk.serving.paged_struct(kc, vc, table)
+        a = B.mk_attention_args.from_buffer_copy(mk.serving.native().check_attention(q, kc, vc, table, lengths, out=out))
+        asked.clear()
+        stream = torch.cuda.current_stream().cuda_stream
+        assert lib.mk_paged_attention_ask(C.byref(kv), C.byref(a), give, None, stream) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and asked == [lib.mk_paged_attention_workspace(hq, hkv, d)] * needed
+        out.zero_()
+        assert lib.mk_paged_attention_ask(C.byref(kv), C.byref(a), refuse, None, stream) == (-8 if needed else 0)
+        torch.cuda.synchronize()
+        assert torch.equal(out, torch.zeros_like(q) if needed else want)   # refused before anything is enqueued

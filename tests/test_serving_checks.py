@@ -251,3 +251,19 @@ def test_what_is_written_is_not_expanded():
     with pytest.raises(ValueError, match="must not be x"):
         _matvec(x=x, codes=codes, scales=scales, residual=None, zeros=None, out=x)
     _matvec(x=x, codes=codes, scales=scales, residual=x, zeros=None, out=torch.zeros((3, 128)))
+
+
+def test_a_call_that_asks_for_its_workspace_checks_the_same():
+    lib = B.load_library()
+    asked = []
+    ask = B.WORKSPACE_FN(lambda context, n: asked.append(n))
+    kv = B.mk_paged_kv.from_buffer_copy(bytes(_kv()))
+    a = _attention(lse=None)
+    for field, value in (("n", 4), ("q", None), ("lengths", None), ("dtype", 7), ("scale", float("inf")), ("n_q_heads", 3)):
+        b = B.mk_attention_args.from_buffer_copy(bytes(a))
+        setattr(b, field, value)
+        assert lib.mk_paged_attention_ask(C.byref(kv), C.byref(b), ask, None, None) == -1
+    assert lib.mk_paged_attention_ask(C.byref(kv), C.byref(a), B.WORKSPACE_FN(0), None, None) == -1
+    assert lib.mk_paged_attention_ask(None, C.byref(a), ask, None, None) == -1
+    a.n = 0
+    assert lib.mk_paged_attention_ask(C.byref(kv), C.byref(a), ask, None, None) == 0 and not asked
