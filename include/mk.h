@@ -434,9 +434,9 @@ int mk_paged_attention(const mk_paged_kv *kv, const mk_attention_args *a, mk_str
 
 /* mk_paged_attention for callers with an allocator of their own: `workspace` is
  * called, at most once and before anything is enqueued, with `context` and the
- * bytes of a workspace if the call needs one (one row, and rows of up to about a
- * thousand slots, need none); the arguments' workspace and workspace_bytes are
- * not looked at.  Its result is device memory on a 16-byte boundary that is the
+ * bytes of a workspace if the call needs one (rows of up to about a thousand
+ * slots, and one row of not too many heads, need none); the arguments' workspace
+ * and workspace_bytes are not looked at.  Its result is device memory on a 16-byte boundary that is the
  * call's own until the stream has passed it, or NULL (MK_ERR_NO_MEMORY).  It must
  * return: an exception must not pass through this call. */
 typedef void *(*mk_workspace_fn)(void *context, int64_t bytes);
