@@ -123,21 +123,24 @@ __device__ __forceinline__ uint32_t take_input_term(FP16Op, float &x, float &y) 
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// a term, not the last, of a value that may meet an infinity: what remains is never zero (an infinity times it would be
-// NaN) but of the value's sign, and tiny where nothing remains
+// a term, not the last, of a value that may meet an infinity: what remains of a value that is not zero is not zero either
+// (an infinity times it would be NaN) but of its sign, 2^-30 of the term where nothing remains: below fp32's last place
+// whatever the value is multiplied by.  Zero stays zero.
+constexpr float kNothingLeft = 0x1p-30f;
 __device__ __forceinline__ uint32_t take_query_term(BF16Op, float &x, float &y) {
   const uint32_t a = __float_as_uint(x) & 0xffff0000u, b = __float_as_uint(y) & 0xffff0000u;
-  const float tx = __uint_as_float((a & 0x80000000u) | 0x03800000u), ty = __uint_as_float((b & 0x80000000u) | 0x03800000u);
-  x = x == __uint_as_float(a) ? tx : x - __uint_as_float(a);
-  y = y == __uint_as_float(b) ? ty : y - __uint_as_float(b);
+  const float fa = __uint_as_float(a), fb = __uint_as_float(b);
+  x = x == fa ? fa * kNothingLeft : x - fa;
+  y = y == fb ? fb * kNothingLeft : y - fb;
   return __byte_perm(a, b, 0x7632);
 }
 __device__ __forceinline__ uint32_t take_query_term(FP16Op op, float &x, float &y) { return take_input_term(op, x, y); }
 // a term of probabilities (>= 0), not the last: by truncation, so that no remainder is negative
 __device__ __forceinline__ uint32_t take_weight_term(BF16Op, float &x, float &y) {
   const uint32_t a = __float_as_uint(x) & 0xffff0000u, b = __float_as_uint(y) & 0xffff0000u;
-  x = fmaxf(x - __uint_as_float(a), 0x1p-120f);
-  y = fmaxf(y - __uint_as_float(b), 0x1p-120f);
+  const float fa = __uint_as_float(a), fb = __uint_as_float(b);
+  x = fmaxf(x - fa, fa * kNothingLeft);
+  y = fmaxf(y - fb, fb * kNothingLeft);
   return __byte_perm(a, b, 0x7632);
 }
 __device__ __forceinline__ uint32_t take_weight_term(FP16Op op, float &x, float &y) { return take_term(op, x, y); }
