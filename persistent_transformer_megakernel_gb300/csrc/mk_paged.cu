@@ -504,10 +504,12 @@ int run_append(const AppendParams &p, int dtype, int cache, int d, cudaStream_t 
 // query three, and the probabilities two terms (three for fp32 outputs), which
 // keeps the result as exact as fp32 products would.  e4m3 keys and values become
 // fp16, exactly; the query row is scaled by a power of two into fp16's range (one
-// term, two for fp32) and the probabilities by 2^14.  Each tile's value sums
-// start from zero and are added to the running ones by an fp32 multiply-add:
-// matrix products truncate what they add to an accumulator, which over thousands
-// of tiles would show.
+// term, two for fp32) and the probabilities by 2^14.  Over a bf16 cache they are
+// multiplied by a power of two of at most 1 / the tokens a row may have: values
+// near bf16's largest would else overflow in the sum that the weights' sum has yet
+// to divide.  Each tile's value sums start from zero and are added to the running
+// ones by an fp32 multiply-add: matrix products truncate what they add to an
+// accumulator, which over thousands of tiles would show.
 //
 // Work: a warp has a range of tiles (POS slots of one row and kv head), streams
 // it through its own ring of shared memory with asynchronous 16-byte copies and
@@ -562,6 +564,7 @@ struct AttnParams {
   int way, cluster;
   int dense;           // a page's slots of a head lie one behind the other
   float scale;
+  float shrink, grow;  // what a probability is multiplied by on the way into the sums, and its inverse: powers of two
 };
 
 template <int D, bool FP8>
@@ -639,7 +642,7 @@ constexpr int kPartStride = D + 4;      // o[D], m, l
 __device__ __forceinline__ float join_base(float m) { return m == -INFINITY ? 0.f : m; }
 
 __device__ __forceinline__ void write_lse(const AttnParams &p, int row, int head, float m, float l) {
-  if (p.lse) p.lse[static_cast<int64_t>(row) * p.hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  if (p.lse) p.lse[static_cast<int64_t>(row) * p.hq + head] = l == 0.f ? -INFINITY : (m + log2f(l * p.grow)) * 0.69314718055994531f;
 }
 
 // a virtual head's kv head, first query head and number of query heads
@@ -1101,6 +1104,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           float a = mkw::exp2_fast(sc[nb][hb][2 * j] - base[0]), b = mkw::exp2_fast(sc[nb][hb][2 * j + 1] - base[1]);
+          if constexpr (!FP8) a *= p.shrink, b *= p.shrink;
           l[hb][0] += a;
           l[hb][1] += b;
 #pragma unroll
@@ -1521,6 +1525,10 @@ int attention(const mk_paged_kv *kv, const mk_attention_args *a, mk_stream strea
   p.gr = std::min(p.group, 16);
   p.row_cost = row_cost(p.gr);
   p.scale = a->scale;
+  int spare = 0;                                             // 2^spare: as many tokens as a row may have, or more
+  for (const int tokens = p.window > 0 ? std::min(p.window, p.capacity) : p.capacity; (int64_t{1} << spare) < tokens;) ++spare;
+  if (kv->dtype != MK_BF16) spare = 0;                       // (e4m3 values are far from fp32's largest)
+  p.shrink = std::ldexp(1.f, -spare), p.grow = std::ldexp(1.f, spare);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   using B = __nv_bfloat16;
   if (a->dtype == MK_F32) {

@@ -1,5 +1,7 @@
 """``paged_attention`` with finite keys and values up to bf16's largest: tokens
-without weight and query elements of zero."""
+without weight, query elements of zero, and rows whose values are all of that
+size (the weighted sum stays in range although the sum before its division by
+the weights' would not)."""
 import numpy as np
 import pytest
 import torch
@@ -60,3 +62,15 @@ def test_keys_against_query_elements_of_zero(x, huge, d):
     q[:, :, 5], q[:, :, d - 1] = 0.0, -0.0
     k[:, :, :, 5], k[:, :, ::3, d - 1] = huge, -huge
     _call(q, k, v, [50, 33])
+
+
+@pytest.mark.parametrize("x", [BF16, F32])
+@pytest.mark.parametrize("lengths,width", [([1], None), ([300], None), ([300, 77, 1], None), ([2500, 40, 1200], 300)])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 128), (2, 2, 64), (16, 1, 128)])
+def test_rows_of_the_largest_values(x, lengths, width, hq, hkv, d):
+    q, k, v = _inputs(len(lengths), max(lengths), x, 3, hq, hkv, d)
+    q, k = q * 0.1, k * 0.1                                 # every token has weight
+    v.fill_(LARGEST)
+    v[:, :, :, 1::2] = -LARGEST
+    v[:, :, ::2, 3] *= -1.0                                 # and one element whose sum cancels
+    _call(q.to(x), k, v, lengths, width=width)
