@@ -479,8 +479,10 @@ typedef struct {
 } mk_matvec_q4_args;
 
 /* y = x w^T (+ residual) for a few rows x, accumulated in fp32 and rounded once.
- * Made for decode (m of 1 to some tens); further rows read the weights again.  A
- * zero above 15 counts modulo 16.  Errors: MK_ERR_INVALID_ARG,
+ * x and the codes enter the products as they are (of x elements below 2^-141 of
+ * their row's largest, bits below 2^-165 of it may be lost).  Made for decode (m
+ * of 1 to some tens); further rows read the weights again.  A zero above 15
+ * counts modulo 16.  Errors: MK_ERR_INVALID_ARG,
  * MK_ERR_UNSUPPORTED (group, k), MK_ERR_CUDA. */
 int mk_matvec_q4(const mk_matvec_q4_args *a, mk_stream stream);
 

@@ -5,12 +5,15 @@
 // Bound by the weights' bytes: N K / 2 plus the scales.  A warp takes 16 weight
 // rows (32 where there are enough rows for every warp) as the rows of 16x8x16 matrix
 // products and the x rows as their columns, 8 a tile.  A code minus its
-// zero is a small whole number, exact in fp16.  An x row is scaled by the power
-// of two that brings its largest finite value to 2^14 .. 2^15 (undone at the end):
-// a bf16 value then is one fp16 term, an fp32 value two of 11 bits in two columns,
-// down to 2^-29 of the row's largest and from there on to 2^-40 of it.  Products
-// are summed in fp32 over a block's part of one group, multiplied by the group's
-// scale and added to the row's sum in fp32.
+// zero is a small whole number, exact in bf16.  A bf16 value of x is one term of a
+// product, an fp32 value three of 8 bits, all of it; so what an element is worth does
+// not depend on its neighbours.  (fp16 terms after a power of two a row took fewer
+// instructions, but what is below 2^-31 of its row's largest lost bits and below 2^-40
+// all, whatever the largest one's weight.)  An x row is still multiplied by the power of two
+// that brings its largest finite value to 2^32 .. 2^33 (undone at the end), so that
+// fp32's largest values stay finite in the sums; only an element below 2^-141 of its row's
+// largest loses bits by it.  Products are summed in fp32 over a block's part of one
+// group, multiplied by the group's scale and added to the row's sum in fp32.
 //
 // A warp's block is 128 elements of k of its rows, 64 bytes a row, which it copies
 // ahead through its own ring of shared memory; registers as the
@@ -21,9 +24,9 @@
 // block, 8 bytes of each of two groups of 64, 4 of each of four groups of 32, so
 // that a product never mixes two groups.  The x columns are staged in shared memory
 // with each 8 elements in the order 0 4 1 5 2 6 3 7: codes j and j + 4 of a word are
-// taken out together, for even j from the low four mantissa bits of the fp16 number
-// 1024, less 1024 + zero, for odd j from the next four, times 1/16, less 64 + zero;
-// so one shift serves four pairs (the integer pipe is the busiest).
+// taken out together, as the low four mantissa bits of the bf16 number 128, less
+// 128 + zero (a published way to make floats of small integers: the mantissa's last
+// places of a number whose unit is 1).
 //
 // One persistent CTA of 16 warps an SM, so that x is staged once an SM (for 8 rows
 // that is a third of the work of a 1.7B-shaped gate and up projection).  The rows'
@@ -33,9 +36,9 @@
 // time: there clusters of four CTAs take a quarter of k each, and add the sums of
 // their tiles in order through their shared memory.
 //
-// Measured: 1 x 151936 x 1024, groups of 128 (80 MB) 17.5 us, 4.6 TB/s: instructions beside bytes; 8 x 12288 x 2048,
-// groups of 32 with zeros, bf16 x, 10.8 us and 3 x 2048 x 6144, groups of 64, 7.5 us: instructions and the staging of x;
-// 1 x 4096 x 1024 3.9 us: latency.
+// Measured (graph replays, weights that stay in the L2 but for the first): 1 x 151936 x 1024, groups of 128 (80 MB) 18.8 us,
+// 4.3 TB/s: instructions beside bytes (17.4 with fp16 terms); 8 x 12288 x 2048, groups of 32 with zeros, bf16 x, 11.0 us
+// (10.7) and 3 x 2048 x 6144, groups of 64, 7.9 us (7.5): instructions and the staging of x; 1 x 4096 x 1024 4.1 us: latency.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -53,8 +56,8 @@ namespace mkq {
 constexpr int kWarps = 16, kThreads = 32 * kWarps, kBlock = 128;
 constexpr int kRing = 4096;            // bytes of codes a warp has room for: 4 blocks of 16 rows (twice as many measured slower)
 constexpr int kMaxSmem = 225 * 1024;   // dynamic shared memory of a CTA
-constexpr int kMaxInbox = 16384;       // of a cluster's CTA, for the tiles that it joins
-constexpr int red_bytes(int nt, int rt) { return kWarps * 16 * rt * 8 * nt * 4; }   // sums of the warps
+constexpr int kMaxInbox = 32768;       // of a cluster's CTA, for the tiles that it joins
+constexpr int red_bytes(int parts, int rt) { return kWarps * rt * parts * 512; }   // sums of the warps
 
 // G: 32, 64, or 128 for every multiple of it
 template <int G>
@@ -117,41 +120,73 @@ struct Eight<__nv_bfloat16> {
 };
 
 template <class T>
-constexpr int kTerms = std::is_same<T, float>::value ? 2 : 1;
+constexpr int kTerms = std::is_same<T, float>::value ? 3 : 1;
 
-__device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b) {
-  const __half2 r = __hadd2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
-  return *reinterpret_cast<const uint32_t *>(&r);
-}
-__device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c) {
-  const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b), *reinterpret_cast<const __half2 *>(&c));
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// four bits of each half of x, in the place of `mask`, as the low mantissa bits of 1024 in fp16: one operation
-__device__ __forceinline__ uint32_t take_codes(uint32_t x, uint32_t mask) {
+// the low four bits of each half of x as the last mantissa bits of 128 in bf16: one operation
+__device__ __forceinline__ uint32_t take_codes(uint32_t x) {
   uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "r"(mask), "r"(0x64006400u));
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "r"(0x000f000fu), "r"(0x43004300u));
   return r;
 }
+
+// Which x row and term column `col` of tile c is, and which x rows' sums a lane has in the end.
+// One term: column by column.  Three: the terms of an x row are in columns of one lane (of columns 2t and 2t + 1 of every
+// tile), which adds them up: two x rows a lane for every three tiles; one for two; with a single tile two lanes share one.
+template <class T, int NT>
+struct Columns {
+  static constexpr int rows = 8 * NT, parts = NT;         // x rows; 16-byte parts of a lane's sums
+  static __device__ __forceinline__ int row(int c, int col) { return 8 * c + col; }
+  static __device__ __forceinline__ int term(int, int) { return 0; }
+  static __device__ __forceinline__ int row_of_part(int t, int o, int j) { return 8 * o + 2 * t + j; }   // -1: none
+  static __device__ __forceinline__ float4 part(const float (&s)[NT][4], int o) { return make_float4(s[o][0], s[o][1], s[o][2], s[o][3]); }
+};
+template <int NT>
+struct Columns<float, NT> {
+  static_assert(NT == 1 || NT == 2 || NT % 3 == 0);
+  static constexpr int rows = NT == 1 ? 2 : NT == 2 ? 4 : NT / 3 * 8, parts = NT < 3 ? 1 : NT / 3;
+  static __device__ __forceinline__ int row(int c, int col) { return NT == 1 ? col / 4 : (2 * c + (col & 1)) / 3 * 4 + col / 2; }
+  static __device__ __forceinline__ int term(int c, int col) { return NT == 1 ? col % 4 : (2 * c + (col & 1)) % 3; }   // 3: none
+  static __device__ __forceinline__ int row_of_part(int t, int o, int j) {
+    return NT == 1 ? (j || t % 2 ? -1 : t / 2) : NT == 2 ? (j ? -1 : t) : (2 * o + j) * 4 + t;
+  }
+  // the least term first
+  static __device__ __forceinline__ float4 part(const float (&s)[NT][4], int o) {
+    if constexpr (NT == 1) {
+      const float a = __shfl_xor_sync(0xffffffffu, s[0][0], 1), b = __shfl_xor_sync(0xffffffffu, s[0][2], 1);
+      return make_float4(a + s[0][1] + s[0][0], 0.f, b + s[0][3] + s[0][2], 0.f);
+    } else {
+      auto sum = [&](int j, int h) {
+        const int f = 3 * (2 * o + j);                    // terms f, f + 1, f + 2 of the lane's columns
+        return s[(f + 2) / 2][2 * h + f % 2] + s[(f + 1) / 2][2 * h + (f + 1) % 2] + s[f / 2][2 * h + f % 2];
+      };
+      return NT == 2 ? make_float4(sum(0, 0), 0.f, sum(0, 1), 0.f) : make_float4(sum(0, 0), sum(1, 0), sum(0, 1), sum(1, 1));
+    }
+  }
+};
 
 // C: CTAs of a cluster, which have a slice of k each
 template <class T, int NT, int RT, int G, bool ZEROS, int C>
 __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_constant__ Q4Params p) {
   using L = Layout<G>;
-  constexpr int TERMS = kTerms<T>, GB = L::groups;
-  constexpr int ROWS = 16 * RT, COLS = 8 * NT, STAGE = ROWS * 64, STAGES = kRing / STAGE;
+  using X = Columns<T, NT>;
+  constexpr int TERMS = kTerms<T>, GB = L::groups, PARTS = RT * X::parts;
+  constexpr int ROWS = 16 * RT, STAGE = ROWS * 64, STAGES = kRing / STAGE;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ uint32_t s_max[COLS];
-  __shared__ float s_to[COLS], s_back[COLS];               // the powers of two that x rows are multiplied by, and their inverses
+  __shared__ uint32_t s_max[X::rows];
+  __shared__ float s_to[X::rows], s_back[X::rows];               // the powers of two that x rows are multiplied by, and their inverses
   mkw::follow_previous_kernel();
   if (C > 1) mkw::cluster_arrive();                        // (waited for before the others' memory is written)
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int rank = blockIdx.x % C, cluster = blockIdx.x / C, clusters = gridDim.x / C;
   const int wn = w / p.wk, wk = w % p.wk, per_cta = kWarps / p.wk;
-  const int m0 = blockIdx.y * p.pass_rows, mr = min(p.pass_rows, p.m - m0), cols = mr * TERMS;
+  const int m0 = blockIdx.y * p.pass_rows, mr = min(p.pass_rows, p.m - m0);
   unsigned char *ring = smem + w * kRing, *xs = smem + kWarps * kRing;
-  float *red = reinterpret_cast<float *>(xs + p.pass_rows * TERMS * p.pitch) + wn * p.wk * ROWS * COLS;   // sums of the warps of this tile
+  float *red = reinterpret_cast<float *>(xs + p.pass_rows * TERMS * p.pitch) + wn * p.wk * PARTS * 128;   // sums of the warps of this tile
 
   // the CTA's blocks of k, this warp's slice of them, its tiles
   const int c0 = p.blocks * rank / C, cb = p.blocks * (rank + 1) / C - c0;
@@ -169,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
     if (b < last) e.load(x + r * p.x_row + b * 8);
     return b < last ? r : -1;
   };
-  if (tid < COLS) s_max[tid] = 0;
+  if (tid < X::rows) s_max[tid] = 0;
   __syncthreads();
   constexpr int AT_ONCE = 4;
 #pragma unroll 1
@@ -265,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
   };
   Scales next = look_up(), after = look_up();
 
-  // ---- the x rows as columns of fp16 terms, zeros past k ----------------------------------------------------
+  // ---- the x rows as columns of bf16 terms, zeros past k ----------------------------------------------------
   __syncthreads();
   for (int r = w; r < mr; r += kWarps) {
     uint32_t mx = s_max[r];
@@ -284,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
       }
       mx = __reduce_max_sync(0xffffffffu, mx);
     }
-    const int e = mx ? max(-126, min(126, 14 - ilogbf(__uint_as_float(mx)))) : 0;
+    const int e = mx ? min(126, 32 - ilogbf(__uint_as_float(mx))) : 0;
     if (lane == 0) s_to[r] = ldexpf(1.f, e), s_back[r] = ldexpf(1.f, -e);
   }
   __syncthreads();
@@ -306,10 +341,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
 #pragma unroll
     for (int u = 0; u < TERMS; ++u) {
       uint4 o;
-      o.x = mkw::take_input_term(mkw::FP16Op{}, v[0], v[4]);
-      o.y = mkw::take_input_term(mkw::FP16Op{}, v[1], v[5]);
-      o.z = mkw::take_input_term(mkw::FP16Op{}, v[2], v[6]);
-      o.w = mkw::take_input_term(mkw::FP16Op{}, v[3], v[7]);
+      o.x = mkw::take_input_term(mkw::BF16Op{}, v[0], v[4]);
+      o.y = mkw::take_input_term(mkw::BF16Op{}, v[1], v[5]);
+      o.z = mkw::take_input_term(mkw::BF16Op{}, v[2], v[6]);
+      o.w = mkw::take_input_term(mkw::BF16Op{}, v[3], v[7]);
       *reinterpret_cast<uint4 *>(to + u * p.pitch) = o;
     }
   }
@@ -322,15 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
     for (int c = 0; c < NT; ++c) sum[r][c][0] = sum[r][c][1] = sum[r][c][2] = sum[r][c][3] = 0.f;
   int tile = tile0, blk = 0, at_stage = 0;
   const unsigned char *column[NT];
-  float back[NT][2];                                       // undo the powers of two of this lane's columns
 #pragma unroll
   for (int c = 0; c < NT; ++c) {
-    column[c] = xs + (c * 8 + g < cols ? c * 8 + g : 0) * p.pitch;   // a column that is none computes what nobody stores
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int m = (c * 8 + 2 * t + j) / TERMS;
-      back[c][j] = m < mr ? s_back[m] : 0.f;
-    }
+    const int m = X::row(c, g), u = X::term(c, g);
+    column[c] = xs + (m < mr && u < TERMS ? m * TERMS + u : 0) * p.pitch;   // a column that is none computes what nobody stores
   }
 
   auto compute = [&](const Scales &sc) {
@@ -372,23 +402,19 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
         for (int h = 0; h < 2; ++h) {
           if (i == 0 && ZEROS) zeros[r][h] = __shfl_sync(0xffffffffu, sc.zeros, 16 * r + 8 * h + g) & 0x0f0f0f0fu;
           if (done && grp % 2 == 0) pair[r][h] = __shfl_sync(0xffffffffu, sc.pair[grp / 2], 16 * r + 8 * h + g);
-          uint32_t low = 0xe408e408u, high = 0xd480d480u;  // -(1024 + zero) and -(64 + zero), twice
-          if (ZEROS) {
-            const uint32_t z = __byte_perm(zeros[r][h], 0, 0x4040 | grp * 0x0101);
-            low = z | 0xe400e400u;
-            high = z * 16 + 0xd400d400u;
-          }
-          const uint32_t x0 = v[r][h][i], x1 = x0 >> 8;
-          a[0][h] = add_half2(take_codes(x0, 0x000f000fu), low);
-          a[0][2 + h] = fma_half2(take_codes(x0, 0x00f000f0u), 0x2c002c00u, high);
-          a[1][h] = add_half2(take_codes(x1, 0x000f000fu), low);
-          a[1][2 + h] = fma_half2(take_codes(x1, 0x00f000f0u), 0x2c002c00u, high);
+          // -(128 + zero), twice
+          const uint32_t less = ZEROS ? __byte_perm(zeros[r][h], 0, 0x4040 | grp * 0x0101) | 0xc300c300u : 0xc308c308u;
+          const uint32_t w0 = v[r][h][i];
+          a[0][h] = add_bf16x2(take_codes(w0), less);
+          a[0][2 + h] = add_bf16x2(take_codes(w0 >> 4), less);
+          a[1][h] = add_bf16x2(take_codes(w0 >> 8), less);
+          a[1][2 + h] = add_bf16x2(take_codes(w0 >> 12), less);
         }
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
-          if (fresh) mkw::mma_zero(mkw::FP16Op{}, acc[r][c], a[0], b[c].x, b[c].y);
-          else mkw::mma(mkw::FP16Op{}, acc[r][c], a[0], b[c].x, b[c].y);
-          mkw::mma(mkw::FP16Op{}, acc[r][c], a[1], b[c].z, b[c].w);
+          if (fresh) mkw::mma_zero(mkw::BF16Op{}, acc[r][c], a[0], b[c].x, b[c].y);
+          else mkw::mma(mkw::BF16Op{}, acc[r][c], a[0], b[c].x, b[c].y);
+          mkw::mma(mkw::BF16Op{}, acc[r][c], a[1], b[c].z, b[c].w);
         }
         if (done) {
           float s[2];
@@ -407,61 +433,62 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
     if (p.residual) y += to_float(static_cast<const T *>(p.residual)[(m0 + m) * p.residual_row + row]);
     put(static_cast<T *>(p.y) + (m0 + m) * p.y_row + row, y);
   };
-  // a part of a tile's sums: a lane has rows g and g + 8 by columns 2t and 2t + 1, the two terms of one x row or two x rows
-  auto store_part = [&](int row, int c, float4 y) {
-    if constexpr (TERMS == 2) {
-      store(row, c * 4 + t, y.y + y.x);
-      store(row + 8, c * 4 + t, y.w + y.z);
-    } else {
-      store(row, c * 8 + 2 * t, y.x);
-      store(row, c * 8 + 2 * t + 1, y.y);
-      store(row + 8, c * 8 + 2 * t, y.z);
-      store(row + 8, c * 8 + 2 * t + 1, y.w);
+  // a part of a tile's sums: a lane has rows g and g + 8 of one or two x rows
+  auto store_part = [&](int row, int o, float4 y) {
+    const int ma = X::row_of_part(t, o, 0), mb = X::row_of_part(t, o, 1);
+    if (ma >= 0) {
+      store(row, ma, y.x);
+      store(row + 8, ma, y.z);
+    }
+    if (mb >= 0) {
+      store(row, mb, y.y);
+      store(row + 8, mb, y.w);
     }
   };
   // A cluster's CTAs have a slice of k each of the same tiles: what each has of the jth of a CTA's tiles goes to the inbox of
   // CTA j % C, in place j / C.
-  float4 *inbox = reinterpret_cast<float4 *>(smem + p.inbox);   // [place][CTA][RT NT][32 lanes]
+  float4 *inbox = reinterpret_cast<float4 *>(smem + p.inbox);   // [place][CTA][PARTS][32 lanes]
   int round = 0;
   auto finish = [&]() {
+    float4 y[PARTS];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+#pragma unroll
+      for (int o = 0; o < X::parts; ++o) y[r * X::parts + o] = X::part(sum[r], o);
+#pragma unroll
+      for (int c = 0; c < NT; ++c) sum[r][c][0] = sum[r][c][1] = sum[r][c][2] = sum[r][c][3] = 0.f;
+    }
     if (p.wk > 1) {
       // over the warps that share the tile, each adding up its part of the lanes' values
       float4 *mine = reinterpret_cast<float4 *>(red) + lane;
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-          mine[((r * NT + c) * p.wk + wk) * 32] = make_float4(sum[r][c][0], sum[r][c][1], sum[r][c][2], sum[r][c][3]);
+      for (int i = 0; i < PARTS; ++i) mine[(i * p.wk + wk) * 32] = y[i];
       asm volatile("bar.sync %0, %1;" ::"r"(1 + wn), "r"(32 * p.wk) : "memory");
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-          if ((r * NT + c) % p.wk == wk) {
-            float4 y = mine[(r * NT + c) * p.wk * 32];
-            for (int j = 1; j < p.wk; ++j) {
-              const float4 z = mine[((r * NT + c) * p.wk + j) * 32];
-              y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
-            }
-            sum[r][c][0] = y.x, sum[r][c][1] = y.y, sum[r][c][2] = y.z, sum[r][c][3] = y.w;
+      for (int i = 0; i < PARTS; ++i)
+        if (i % p.wk == wk) {
+          y[i] = mine[i * p.wk * 32];
+          for (int j = 1; j < p.wk; ++j) {
+            const float4 z = mine[(i * p.wk + j) * 32];
+            y[i].x += z.x, y[i].y += z.y, y[i].z += z.z, y[i].w += z.w;
           }
+        }
       asm volatile("bar.sync %0, %1;" ::"r"(1 + wn), "r"(32 * p.wk) : "memory");
     }
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        if (p.wk == 1 || (r * NT + c) % p.wk == wk) {
-          const float4 y = make_float4(sum[r][c][0] * back[c][0], sum[r][c][1] * back[c][1], sum[r][c][2] * back[c][0], sum[r][c][3] * back[c][1]);
-          if constexpr (C == 1) {
-            store_part(tile * ROWS + r * 16 + g, c, y);
-          } else {
-            const int j = round * per_cta + wn;
-            const uint32_t to = mkw::remote(inbox + ((j / C * C + rank) * RT * NT + r * NT + c) * 32 + lane, j % C);
-            mkw::store_remote(to, y.x), mkw::store_remote(to + 4, y.y), mkw::store_remote(to + 8, y.z), mkw::store_remote(to + 12, y.w);
-          }
+    for (int i = 0; i < PARTS; ++i)
+      if (p.wk == 1 || i % p.wk == wk) {
+        // undo the powers of two of the x rows
+        const int o = i % X::parts, ma = X::row_of_part(t, o, 0), mb = X::row_of_part(t, o, 1);
+        const float fa = ma >= 0 && ma < mr ? s_back[ma] : 0.f, fb = mb >= 0 && mb < mr ? s_back[mb] : 0.f;
+        y[i].x *= fa, y[i].y *= fb, y[i].z *= fa, y[i].w *= fb;
+        if constexpr (C == 1) {
+          store_part(tile * ROWS + i / X::parts * 16 + g, o, y[i]);
+        } else {
+          const int j = round * per_cta + wn;
+          const uint32_t to = mkw::remote(inbox + ((j / C * C + rank) * PARTS + i) * 32 + lane, j % C);
+          mkw::store_remote(to, y[i].x), mkw::store_remote(to + 4, y[i].y), mkw::store_remote(to + 8, y[i].z), mkw::store_remote(to + 12, y[i].w);
         }
-        sum[r][c][0] = sum[r][c][1] = sum[r][c][2] = sum[r][c][3] = 0.f;
       }
     tile += step;
     ++round;
@@ -493,22 +520,31 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
   // the slices' sums, in order, by a warp each 16 rows and 8 columns
 #pragma unroll 1
   for (int i = w;; i += kWarps) {
-    const int part = i % (RT * NT), place = i / (RT * NT), j = place * C + rank, at = cluster * per_cta + j % per_cta + j / per_cta * step;
+    const int part = i % PARTS, place = i / PARTS, j = place * C + rank, at = cluster * per_cta + j % per_cta + j / per_cta * step;
     if (j / per_cta * step + cluster * per_cta >= p.tiles) break;
     if (at >= p.tiles) continue;
-    float4 y = inbox[(place * C * RT * NT + part) * 32 + lane];
+    float4 y = inbox[(place * C * PARTS + part) * 32 + lane];
 #pragma unroll 1
     for (int c = 1; c < C; ++c) {
-      const float4 z = inbox[((place * C + c) * RT * NT + part) * 32 + lane];
+      const float4 z = inbox[((place * C + c) * PARTS + part) * 32 + lane];
       y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
     }
-    store_part(at * ROWS + part / NT * 16 + g, part % NT, y);
+    store_part(at * ROWS + part / X::parts * 16 + g, part % X::parts, y);
   }
 }
+
+// bytes from staged column to column, of a CTA's blocks of k
+template <int G>
+int pitch_of(int blocks) { return blocks * kBlock * 2 + Layout<G>::pad; }
+
+// a launch that cannot be: clusters that do not fit, more tiles than an inbox holds, no room for one x row
+constexpr int kRefused = 1;
 
 template <class T, int NT, int RT, int G, bool ZEROS, int C>
 int launch_as(Q4Params p, int sms, int dev, cudaStream_t s) {
   static_assert(C == 1 || C == 4);
+  using X = Columns<T, NT>;
+  constexpr int PARTS = RT * X::parts;
   static mkw::Ready ready[mkw::kMaxDevices];
   const auto fn = &matvec_kernel<T, NT, RT, G, ZEROS, C>;
   mkw::Ready &r = ready[dev];
@@ -518,12 +554,9 @@ int launch_as(Q4Params p, int sms, int dev, cudaStream_t s) {
   p.vec = p.groups % per == 0 && reinterpret_cast<uintptr_t>(p.scales) % (2 * per) == 0 &&
           reinterpret_cast<uintptr_t>(p.zeros) % per == 0;
   const int clusters = C == 1 ? sms : r.clusters[1];
-  if constexpr (C > 1) {
-    // (the inbox is 16 RT rows of every tile of a CTA)
-    if (clusters < 1 || p.tiles / clusters * RT * NT * 512 > kMaxInbox) return launch_as<T, NT, RT, G, ZEROS, 1>(p, sms, dev, s);
-  }
+  if (clusters < 1) return kRefused;
   const int blocks = (p.blocks + C - 1) / C;   // of a CTA
-  p.pitch = blocks * kBlock * 2 + Layout<G>::pad;
+  p.pitch = pitch_of<G>(blocks);
   p.eighths.set(blocks * (kBlock / 8));
   // the sharing of k that leaves the busiest warp the fewest blocks, fewer warps a tile where that is equal
   int64_t best = 0;
@@ -534,13 +567,15 @@ int launch_as(Q4Params p, int sms, int dev, cudaStream_t s) {
   }
   const int per_cta = kWarps / p.wk, want = std::min((p.tiles + per_cta - 1) / per_cta, clusters);
   // x rows of a pass: as many as its columns hold and shared memory has room for
-  const int red = p.wk > 1 ? red_bytes(NT, RT) : 0, rounds = (p.tiles + want * per_cta - 1) / (want * per_cta);
-  const int inbox = C > 1 ? (rounds * per_cta + C - 1) / C * C * RT * NT * 512 : 0;
-  p.pass_rows = std::min({p.m, 8 * NT / kTerms<T>, (kMaxSmem - kWarps * kRing - red - inbox) / p.pitch / kTerms<T>});
+  const int red = p.wk > 1 ? red_bytes(X::parts, RT) : 0, rounds = (p.tiles + want * per_cta - 1) / (want * per_cta);
+  const int64_t inbox = C > 1 ? (static_cast<int64_t>(rounds) * per_cta + C - 1) / C * C * PARTS * 512 : 0;
+  if (inbox > kMaxInbox) return kRefused;
+  p.pass_rows = std::min({p.m, X::rows, (kMaxSmem - kWarps * kRing - red - static_cast<int>(inbox)) / p.pitch / kTerms<T>});
+  if (p.pass_rows < 1) return kRefused;
   p.inbox = kWarps * kRing + red + p.pass_rows * kTerms<T> * p.pitch;
-  const int passes = (p.m + p.pass_rows - 1) / p.pass_rows;
+  const int passes = (p.m - 1) / p.pass_rows + 1;
   if (passes > 65535) return MK_ERR_UNSUPPORTED;
-  return mkw::launch_after(fn, dim3(want * C, passes), kThreads, p.inbox + inbox, s, p, C);
+  return mkw::launch_after(fn, dim3(want * C, passes), kThreads, p.inbox + static_cast<int>(inbox), s, p, C);
 }
 
 template <class T, int NT, int RT, int G, bool ZEROS>
@@ -559,26 +594,66 @@ int by_group(Q4Params &p, int group, int sms, int dev, cudaStream_t s) {
   return launch<T, NT, RT, 128, ZEROS>(p, sms, dev, s);
 }
 
+// passes over the weights with NT column tiles, 16 RT rows a tile and clusters of c CTAs; 0: not one x row fits
+template <class T, int NT, int RT = 1>
+int passes_of(const Q4Params &p, int c) {
+  const int room = kMaxSmem - kWarps * kRing - red_bytes(Columns<T, NT>::parts, RT) - (c > 1 ? kMaxInbox : 0);
+  const int rows = std::min(Columns<T, NT>::rows, room / pitch_of<32>((p.blocks + c - 1) / c) / kTerms<T>);
+  return rows < 1 ? 0 : (p.m - 1) / rows + 1;
+}
+
+template <class T, bool ZEROS>
+int by_columns(Q4Params &p, int group, int sms, int dev, cudaStream_t s) {
+  // the fewest passes, and of these the fewest columns
+  constexpr int A = std::is_same<T, float>::value ? 3 : 4, B = std::is_same<T, float>::value ? 6 : 4;
+  const int one = passes_of<T, 1>(p, p.cluster), two = passes_of<T, 2>(p, p.cluster), some = passes_of<T, A>(p, p.cluster), most = passes_of<T, B>(p, p.cluster);
+  const int fewest = std::min({one ? one : INT32_MAX, two ? two : INT32_MAX, some ? some : INT32_MAX, most ? most : INT32_MAX});
+  if (fewest == INT32_MAX) return kRefused;
+  if (one == fewest) {
+    // 32 rows a tile, whose matrix products share what is read of x, where every warp has one of them
+    if (p.cluster == 1 && p.n / 32 >= sms * kWarps && passes_of<T, 1, 2>(p, 1) == 1) return by_group<T, 1, 2, ZEROS>(p, group, sms, dev, s);
+    return by_group<T, 1, 1, ZEROS>(p, group, sms, dev, s);
+  }
+  if (two == fewest) return by_group<T, 2, 1, ZEROS>(p, group, sms, dev, s);
+  if (some == fewest) return by_group<T, A, 1, ZEROS>(p, group, sms, dev, s);
+  return by_group<T, B, 1, ZEROS>(p, group, sms, dev, s);
+}
+
 template <class T, bool ZEROS>
 int by_rows(Q4Params &p, int group, int sms, int dev, cudaStream_t s) {
   p.blocks = (p.k + kBlock - 1) / kBlock;
-  // Clusters of 4 CTAs with a quarter of k each, where what is staged of x is 48 KB and as much as a CTA's codes.  (8 x
-  // 2048 x 6144 in bf16 7.4 us against 11.1 with all of x in every CTA, 16 x 4096 x 4096 9.7 and 14.1, 2 x 1024 x 16384 in
-  // fp32 7.3 and 12.3, 8 x 4096 x 6144 in bf16, 1.2 times the codes, 9.5 and 12.5, 3 x 2048 x 6144 in fp32 7.5 and 7.6; but
-  // 3 x 4096 x 6144 in fp32, 0.9 times, 9.2 both ways, 2 x 4096 x 8192 in fp32, 0.6 times, 10.2 and 10.0, 8 x 12288 x 2048
-  // in bf16, 33 KB, 11.7 and 10.8: a cluster's launch alone costs 1 us.  Clusters of 2 or 8 were slower where clusters paid.)
+  // Clusters of 4 CTAs with a quarter of k each, where what is staged of x is 48 KB and as much as a CTA's codes.  (In clusters
+  // and with all of x in every CTA: 8 x 2048 x 6144 in bf16 8.2 and 11.9 us, 16 x 4096 x 4096 10.8 and 15.5, 8 x 4096 x 6144,
+  // 1.2 times the codes, 10.4 and 13.8, 2 x 1024 x 16384 in fp32 8.6 and 11.7, 3 x 4096 x 6144, 1.3 times, 10.4 and 11.8, 12 x
+  // 12288 x 2048 18.7 and 21.6; but 2 x 4096 x 6144, 0.9 times, 9.4 and 9.2, 1 x 2048 x 8192, 0.9 times, 7.7 both ways, 16 x
+  // 12288 x 2048 in bf16, 0.8 times, 14.4 and 12.8, 8 x 12288 x 2048, 32 KB, 12.3 and 11.0: a cluster's launch alone costs
+  // 1 us.  Clusters of 2 or 8 were slower where clusters paid.)
   const int64_t staged = static_cast<int64_t>(p.m) * p.k * kTerms<T> * 2, codes = static_cast<int64_t>(p.n) * p.k / 2 / sms;
-  p.cluster = staged >= 49152 && staged >= codes ? 4 : 1;
-  const int cols = p.m > 32 ? 32 : p.m * kTerms<T>;
-  auto room = [&](int nt) { return (kMaxSmem - kWarps * kRing - red_bytes(nt, 1) - (p.cluster > 1 ? kMaxInbox : 0)) / ((p.blocks + p.cluster - 1) / p.cluster * kBlock * 2 + 64); };
-  if (cols <= 8 || room(2) < 16) {
-    // 32 rows a tile, whose matrix products share what is read of x, where every warp has one of them
-    if (p.n / 32 >= sms * kWarps && p.m <= 8 / kTerms<T>) return by_group<T, 1, 2, ZEROS>(p, group, sms, dev, s);
-    return by_group<T, 1, 1, ZEROS>(p, group, sms, dev, s);
+  const bool fits = passes_of<T, 1>(p, 1) > 0;
+  p.cluster = !fits || (staged >= 49152 && staged >= codes) ? 4 : 1;
+  if (fits) {
+    int rc = by_columns<T, ZEROS>(p, group, sms, dev, s);
+    if (rc == kRefused && p.cluster > 1) {
+      p.cluster = 1;
+      rc = by_columns<T, ZEROS>(p, group, sms, dev, s);
+    }
+    return rc == kRefused ? MK_ERR_UNSUPPORTED : rc;
   }
-  // four column tiles where shared memory has room for more columns than two have
-  if (cols <= 16 || room(4) < 24) return by_group<T, 2, 1, ZEROS>(p, group, sms, dev, s);
-  return by_group<T, 4, 1, ZEROS>(p, group, sms, dev, s);
+  // x rows of which not one fits in a CTA (fp32, k above 25 thousand): always in clusters, the weights' rows in launches
+  // of as many as their inboxes hold
+  constexpr int kRows = 16384;
+  for (int64_t n0 = 0; n0 < p.n; n0 += kRows) {
+    Q4Params q = p;
+    q.n = static_cast<int>(std::min<int64_t>(kRows, p.n - n0));
+    q.codes += n0 * (p.k / 2);
+    q.scales += n0 * p.groups;
+    if (q.zeros) q.zeros += n0 * p.groups;
+    q.y = static_cast<T *>(q.y) + n0;
+    if (q.residual) q.residual = static_cast<const T *>(q.residual) + n0;
+    const int rc = by_columns<T, ZEROS>(q, group, sms, dev, s);
+    if (rc != MK_OK) return rc == kRefused ? MK_ERR_UNSUPPORTED : rc;
+  }
+  return MK_OK;
 }
 
 template <class T>
