@@ -95,12 +95,12 @@ def test_window(window, cache):
 
 
 @pytest.mark.parametrize("x,cache,hq,hkv,lengths", [
-    (F32, BF16, 16, 8, [5119]),                     # one row over many CTAs
-    (F32, BF16, 2, 1, [20011]),                     # and one kv head over all of them
+    (F32, BF16, 16, 8, [5119]),                     # one row: a cluster of CTAs for each kv head
+    (F32, BF16, 2, 1, [20011]),                     # and a single one, of one kv head
     (BF16, BF16, 16, 8, [3000, 1, 0, 777, 2049]),
     (BF16, E4M3, 8, 2, [9001, 40]),
     (F32, E4M3, 12, 1, [4097, 4096, 4095]),         # more than 8 query heads a kv head
-    (F32, BF16, 16, 1, [2000, 31]),                 # two ring stages
+    (F32, BF16, 16, 1, [2000, 31]),                 # and the largest states in registers
 ])
 def test_rows_joined_over_ctas(x, cache, hq, hkv, lengths):
     c = _case(lengths, hq, hkv, 128, x, cache, 16, seed=3)
