@@ -79,9 +79,14 @@ def quantize_q4(w: torch.Tensor, group: int = 64, zeros: bool = False):
     return codes, scale
 
 
-def check_status(status: torch.Tensor) -> None:
+def check_status(status: torch.Tensor, stream=None) -> None:
     """Wait for and raise the error that a paged operator has left in ``status``
-    (int32 [1], zeroed before the call); nothing if there is none."""
-    code = int(status.item())
+    (int32 [1], zeroed before the call); nothing if there is none.  ``stream`` is
+    the operator's, where that was not the current one."""
+    if stream is None:
+        code = int(status.item())
+    else:
+        with torch.cuda.stream(stream):                  # the word is copied, and waited for, behind the operator
+            code = int(status.item())
     if code:
         raise B.MKError(code, "paged operator")
