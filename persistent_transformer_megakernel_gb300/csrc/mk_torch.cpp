@@ -281,6 +281,7 @@ mk_append_args append_args(PyObject *const *o, const mk_paged_kv &kv, const c10:
     const at::Tensor &r = tensor(o[A_ROPE], "rope");
     need(r.dim() == 3 && r.size(1) == d / 2 && r.size(2) == 2 && r.scalar_type() == at::kFloat && r.is_contiguous() && r.device() == dev && on16(r),
          "rope must be the contiguous fp32 [rows][head_dim / 2][2] of rope_table");
+    need(r.size(0) > 0, "rope has no rows");                 // (its address would be that of no table: no rotation)
     a.rope = static_cast<const float *>(r.data_ptr());
     a.rope_rows = small(r.size(0), "rope");
     if (o[A_SECTIONS]) {
