@@ -372,7 +372,8 @@ typedef struct {
   int32_t dtype;               /* of q, k, v and q_out: MK_F32 or MK_BF16 */
   int32_t n_q_heads;           /* heads of q; 0 = no q */
   const void *q, *k, *v;       /* device [n][heads][head_dim] */
-  void *q_out;                 /* device [n][n_q_heads][head_dim]; may be q itself (same strides) */
+  void *q_out;                 /* device [n][n_q_heads][head_dim]; may be q itself (same strides), else
+                                  no part of q, k, v or the cache */
   int64_t q_row, q_head, k_row, k_head, v_row, v_head, out_row, out_head; /* strides, elements */
   const int32_t *seqs;         /* device [n] table row of each token row; NULL = row i is sequence i */
   const int32_t *slots;        /* device [n] token index p in its sequence; negative = a padding row,
@@ -393,7 +394,8 @@ typedef struct {
  * with norm(x) = x / sqrt(mean(x^2) + eps) * gain per head, rope turning the
  * pairs (i, i + head_dim / 2), all in fp32 and rounded once (to nearest even,
  * MK_E4M3 saturating at +-448).  One row (a decode step's token) or many
- * (prompts: seqs and slots say where each row goes).  A slot may be written by
+ * (prompts: seqs and slots say where each row goes).  The keys' and the values'
+ * memory is not the same, and no input is in a slot that the call writes.  A slot may be written by
  * at most one row of a call; with two, each element is one of theirs.  A row
  * whose sequence, slot or page is outside the table or the cache
  * (MK_ERR_BAD_PAGE) or whose position is outside the rotary table
@@ -406,9 +408,11 @@ typedef struct {
   int32_t dtype;               /* of q and out: MK_F32 or MK_BF16 */
   int32_t n_q_heads;           /* a multiple of n_kv_heads; head j reads kv head j / (n_q_heads / n_kv_heads) */
   const void *q;               /* device [n][n_q_heads][head_dim] */
-  void *out;                   /* device, the same shape; may be q itself (same strides) */
+  void *out;                   /* device, the same shape; may be q itself (same strides), else no part
+                                  of it or the cache */
   int64_t q_row, q_head, out_row, out_head; /* strides, elements */
-  float *lse;                  /* device [n][n_q_heads] log of the softmax's sum, or NULL */
+  float *lse;                  /* device [n][n_q_heads] log of the softmax's sum, or NULL; no part of q
+                                  or out */
   const int32_t *lengths;      /* device [n] tokens a row reads, its own included; 0 = none, negative =
                                   a padding row, whose outputs are left as they were */
   int32_t window;              /* > 0: only the last `window` of them; 0 = all */
@@ -472,9 +476,10 @@ typedef struct {
   const void *codes;           /* device uint8 [n][k / 2], contiguous */
   const void *scales;          /* device bf16 [n][k / group], contiguous */
   const uint8_t *zeros;        /* device [n][k / group], contiguous; NULL = 8 everywhere */
-  const void *residual;        /* device [m][n] added to the products, or NULL; may be y itself */
+  const void *residual;        /* device [m][n] added to the products, or NULL; may be y itself (same
+                                  stride) */
   int64_t residual_row;
-  void *y;                     /* device [m][n] */
+  void *y;                     /* device [m][n]; no part of x, and of the residual all or none */
   int64_t y_row;               /* residual_row and y_row need no alignment */
 } mk_matvec_q4_args;
 

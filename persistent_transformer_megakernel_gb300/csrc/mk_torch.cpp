@@ -24,6 +24,7 @@
 #include <exception>
 #include <optional>
 #include <string>
+#include <utility>
 
 #include "../../include/mk.h"
 
@@ -123,10 +124,83 @@ void *vector(PyObject *o, const char *name, c10::ScalarType type, int64_t n, con
   return t.data_ptr();
 }
 
-// a tensor that is written: no two of its first two dimensions' rows may be the same memory
-void apart(const at::Tensor &t, const char *name) {
-  for (int i : {0, 1})
+// ---- memory that is written --------------------------------------------------------
+
+// A tensor's bytes: pieces of `inner` bytes at multiples of up to three strides (zero strides and dimensions of one
+// element add none).
+struct Region {
+  uintptr_t at;
+  int64_t inner, extent;       // of a piece, and from the first byte to the last
+  int64_t size[3], stride[3];
+  int dims = 0;
+
+  Region(const at::Tensor &t, int64_t inner_elements) {
+    const int64_t es = static_cast<int64_t>(t.element_size());
+    at = reinterpret_cast<uintptr_t>(t.data_ptr());
+    inner = extent = inner_elements * es;
+    if (t.numel() == 0) inner = extent = 0;
+    for (int64_t i = 0; i + 1 < t.dim(); ++i) {
+      if (t.size(i) <= 1 || t.stride(i) == 0) continue;
+      size[dims] = t.size(i), stride[dims] = t.stride(i) * es;
+      extent += (size[dims] - 1) * stride[dims];
+      ++dims;
+    }
+  }
+  // from the first byte to the last of what lies between multiples of strides of `cut` and more
+  int64_t below(int64_t cut) const {
+    int64_t e = inner;
+    for (int i = 0; i < dims; ++i)
+      if (stride[i] < cut) e += (size[i] - 1) * stride[i];
+    return e;
+  }
+  bool operator==(const Region &o) const {
+    if (at != o.at || inner != o.inner || dims != o.dims) return false;
+    for (int i = 0; i < dims; ++i)
+      if (size[i] != o.size[i] || stride[i] != o.stride[i]) return false;
+    return true;
+  }
+};
+
+int64_t common(int64_t a, int64_t b) {
+  while (b) std::swap(a %= b, b);
+  return a;
+}
+
+// Whether two tensors certainly share no byte: one lies behind the other, or, modulo what the strides of `cut` and more
+// have in common, what lies between them does (rows of one buffer, heads of one row, slots of one page).
+bool disjoint(const Region &a, const Region &b) {
+  if (a.extent == 0 || b.extent == 0 || a.at + a.extent <= b.at || b.at + b.extent <= a.at) return true;
+  for (const Region *r : {&a, &b})
+    for (int i = 0; i < r->dims; ++i) {
+      const int64_t cut = r->stride[i];
+      int64_t g = 0;
+      for (const Region *o : {&a, &b})
+        for (int j = 0; j < o->dims; ++j)
+          if (o->stride[j] >= cut) g = common(o->stride[j], g);
+      const int64_t from = b.at >= a.at ? static_cast<int64_t>((b.at - a.at) % g) : (g - static_cast<int64_t>((a.at - b.at) % g)) % g;
+      if (a.below(cut) <= from && from + b.below(cut) <= g) return true;
+    }
+  return false;
+}
+
+// a tensor that is written: no two of its elements may be the same memory
+Region written(const at::Tensor &t, const char *name, int64_t inner) {
+  for (int64_t i = 0; i + 1 < t.dim(); ++i)
     if (t.size(i) > 1 && t.stride(i) == 0) throw Bad{std::string(name) + " must not be expanded: it is written"};
+  const Region r(t, inner);
+  int64_t done = 0;                                        // every stride beyond what the smaller ones reach
+  for (int k = 0; k < r.dims; ++k) {
+    int64_t next = INT64_MAX;
+    int equal = 0;
+    for (int i = 0; i < r.dims; ++i) {
+      if (r.stride[i] > done && r.stride[i] < next) next = r.stride[i], equal = 1;
+      else if (r.stride[i] == next) ++equal;
+    }
+    if (next == INT64_MAX) break;
+    if (equal > 1 || next < r.below(next)) throw Bad{std::string(name) + " must not overlap itself: it is written"};
+    done = next;
+  }
+  return r;
 }
 
 // row and head strides of [n][heads][d]: the last dimension contiguous, every row on 16 bytes
@@ -243,8 +317,9 @@ Signature append_sig = {"paged_append", 6, 6, 20,
                          "mrope_interleaved", "q_norm", "k_norm", "eps", "k_scale", "v_scale", "status", "stream"}, {}};
 
 mk_append_args append_args(PyObject *const *o, const mk_paged_kv &kv, const c10::Device &dev) {
-  need((kv.n_pages == 1 || kv.page_stride) && (kv.n_kv_heads == 1 || kv.head_stride) && (kv.page_size == 1 || kv.slot_stride),
-       "the cache must not be expanded: it is written");
+  const at::Tensor &k_cache = THPVariable_Unpack(o[A_KC]), &v_cache = THPVariable_Unpack(o[A_VC]);
+  const Region kc = written(k_cache, "k_cache", kv.head_dim), vc = written(v_cache, "v_cache", kv.head_dim);
+  need(disjoint(kc, vc), "k_cache and v_cache must not overlap: they are written");
   const at::Tensor &k = tensor(o[A_K], "k"), &v = tensor(o[A_V], "v");
   const auto type = k.scalar_type();
   need(type == at::kFloat || type == at::kBFloat16, "k must be fp32 or bf16");
@@ -267,7 +342,10 @@ mk_append_args append_args(PyObject *const *o, const mk_paged_kv &kv, const c10:
       const at::Tensor &out = tensor(o[A_QOUT], "q_out");
       heads(out, "q_out", n, d, a.n_q_heads ? a.n_q_heads : -1, type, dev, &a.out_row, &a.out_head);
       need(out.size(1) == q.size(1), "q_out must have q's heads");
-      apart(out, "q_out");
+      const Region r = written(out, "q_out", d), of_q(q, d);
+      need(r == of_q || disjoint(r, of_q), "q_out must be q itself or not overlap it");
+      need(disjoint(r, Region(k, d)) && disjoint(r, Region(v, d)) && disjoint(r, kc) && disjoint(r, vc),
+           "q_out must not overlap k, v or the cache");
       a.q_out = out.data_ptr();
     }
   } else {
@@ -367,13 +445,17 @@ mk_attention_args attention_args(PyObject *const *o, const mk_paged_kv &kv, cons
   if (o[T_OUT]) {
     const at::Tensor &out = tensor(o[T_OUT], "out");
     heads(out, "out", n, d, hq, type, dev, &a.out_row, &a.out_head);
-    apart(out, "out");
+    const Region r = written(out, "out", d), of_q(q, d);
+    need(r == of_q || disjoint(r, of_q), "out must be q itself or not overlap it");
+    need(disjoint(r, Region(THPVariable_Unpack(o[T_KC]), d)) && disjoint(r, Region(THPVariable_Unpack(o[T_VC]), d)), "out must not overlap the cache");
     a.out = out.data_ptr();
   }
   if (o[T_LSE]) {
     const at::Tensor &lse = tensor(o[T_LSE], "lse");
     need(lse.dim() == 2 && lse.size(0) == n && lse.size(1) == hq && lse.scalar_type() == at::kFloat && lse.device() == dev && lse.is_contiguous(),
          "lse must be a contiguous fp32 [rows][heads] on q's device");
+    const Region r(lse, hq);
+    need(disjoint(r, Region(q, d)) && (!o[T_OUT] || disjoint(r, Region(THPVariable_Unpack(o[T_OUT]), d))), "lse must not overlap q or out");
     a.lse = static_cast<float *>(lse.data_ptr());
   }
   need(o[T_LENGTHS], "lengths are needed");
@@ -474,8 +556,12 @@ mk_matvec_q4_args matvec_args(PyObject *const *o, bool on_device, c10::Device *d
     if (t.dim() != 2 || t.size(0) != m || t.size(1) != n || t.scalar_type() != type || t.device() != dev || (t.stride(1) != 1 && n > 1))
       throw Bad{std::string(i == M_OUT ? "out" : "residual") + " must be [" + std::to_string(m) + "][" + std::to_string(n) + "] of x's dtype on its device, rows contiguous"};
     if (i == M_OUT) {
-      apart(t, "out");
-      need(t.data_ptr() != a.x || !m || !n, "out must not be x, which is read until the last of it is written");
+      const Region r = written(t, "out", n);
+      need(disjoint(r, Region(x, k)), "out must not be x or overlap it: x is read until the last of out is written");
+      if (o[M_RESIDUAL]) {
+        const Region of(THPVariable_Unpack(o[M_RESIDUAL]), n);
+        need(r == of || disjoint(r, of), "out must be residual itself or not overlap it");
+      }
       a.y = t.data_ptr(), a.y_row = t.stride(0);
     } else a.residual = t.data_ptr(), a.residual_row = t.stride(0);
   }
@@ -551,7 +637,8 @@ PyMethodDef methods[] = {
 row and head strides on 16 bytes) to their slots of the paged cache, with
 RMSNorm by the gains ``q_norm`` / ``k_norm`` (bf16 [d]) and the rotation by
 ``rope`` (``rope_table``) on the way, and return the queries ``q`` treated alike
-(into ``q_out``, which may be ``q``; a new tensor by default; None without ``q``).
+(into ``q_out``, which may be ``q`` but overlap no other tensor of the call; a new
+tensor by default; None without ``q``).
 
 ``k_cache`` and ``v_cache`` are [n_pages][kv heads][page_size][d] of bf16 or
 float8_e4m3fn (equal strides, the first three dimensions in any order in
@@ -570,15 +657,15 @@ name the same slot of the cache.  What the device finds wrong goes to
 ``mk_paged_attention``: attention of one new token per row, ``q`` [n][heads][d]
 (fp32 or bf16), over the first ``lengths[i]`` (the last ``window`` of them,
 if not 0) tokens of row i of ``table``; the cache as for ``paged_append``.
-Returns ``out`` like ``q`` (it may be ``q``); ``lse`` fp32 [n][heads] receives
-the log of each softmax's sum.  ``scale`` is 1 / sqrt(d) by default.  A row of
+Returns ``out`` like ``q`` (it may be ``q``, but not overlap it otherwise);
+``lse`` fp32 [n][heads] receives the log of each softmax's sum.  ``scale`` is 1 / sqrt(d) by default.  A row of
 length 0 gives zeros and -inf, one of negative length is left as it was.)"),
     method<&matvec_sig, &matvec_q4>("matvec_q4", R"(matvec_q4(x, codes, scales, *, zeros=None, residual=None, out=None, stream=None)
 --
 
 ``mk_matvec_q4``: ``x`` [rows][k] (fp32 or bf16) times the transpose of the
 4-bit weights of ``quantize_q4``, plus ``residual`` [rows][n] (which may be
-``out``).  ``codes`` uint8 [n][k / 2], ``scales`` bf16 and ``zeros`` uint8 (8
+``out``; ``out`` must not overlap ``x``).  ``codes`` uint8 [n][k / 2], ``scales`` bf16 and ``zeros`` uint8 (8
 everywhere if None) [n][k / group].)"),
     method<&append_sig, &check_append>("check_append", "The checks of paged_append; the bytes of its mk_append_args."),
     method<&attention_sig, &check_attention>("check_attention", "The checks of paged_attention; the bytes of its mk_attention_args."),

@@ -47,3 +47,99 @@ def test_a_rotary_table_without_rows():
     for kw in (dict(), dict(positions=_i32(3)), dict(positions=_i32(3, 3), mrope_sections=(12, 10, 10))):
         with pytest.raises(ValueError, match="rope"):
             _append(rope=torch.zeros((0, 32, 2)), **kw)
+
+
+def test_queries_are_written_in_place_or_apart():
+    buf = torch.zeros(4000)
+    q = buf[:768].view(3, 4, 64)
+    for make in (lambda out: _append(q=q, q_out=out), lambda out: _attention(q=q, out=out)):
+        make(q)                                             # itself
+        make(buf[768:1536].view(3, 4, 64))                  # behind it
+        for out in (buf[64:832].view(3, 4, 64), buf[4:772].view(3, 4, 64),
+                    torch.as_strided(buf, (3, 4, 64), (320, 64, 1)), torch.as_strided(buf, (3, 4, 64), (64, 192, 1)),
+                    torch.as_strided(buf, (3, 4, 64), (256, 64, 1), 512)):
+            with pytest.raises(ValueError, match="overlap"):
+                make(out)
+    # pieces of the same rows: beside one another, heads between heads, the halves of a buffer of heads
+    wide = torch.zeros((3, 8, 64))
+    for a, b in ((wide[:, :4], wide[:, 4:]), (wide[:, ::2], wide[:, 1::2])):
+        for x, y in ((a, b), (b, a)):
+            _append(q=x, q_out=y)
+            _attention(q=x, out=y)
+    two = torch.zeros((3, 4, 128))
+    _attention(q=two[..., :64], out=two[..., 64:])
+    by_head = torch.zeros((8, 3, 64)).transpose(0, 1)
+    _attention(q=by_head[:, :4], out=by_head[:, 4:])
+    with pytest.raises(ValueError, match="overlap"):
+        _attention(q=wide[:, :4], out=wide[:, 2:6])
+
+
+def test_queries_are_not_written_over_keys_values_or_the_cache():
+    qkv = torch.zeros((3, 8, 64))
+    a = dict(q=qkv[:, :4], k=qkv[:, 4:6], v=qkv[:, 6:])
+    _append(**a, q_out=qkv[:, :4])
+    for out in (qkv[:, 2:6], qkv[:, 4:]):
+        with pytest.raises(ValueError, match="overlap"):
+            _append(**a, q_out=out)
+    cache = torch.zeros((6, 2, 16, 64), dtype=BF16)
+    b = dict(k_cache=torch.zeros_like(cache), v_cache=cache, q=torch.zeros((3, 4, 64), dtype=BF16))
+    out = cache[1, 0, :12].view(3, 4, 64)
+    with pytest.raises(ValueError, match="overlap"):
+        _attention(**b, out=out)
+    with pytest.raises(ValueError, match="overlap"):
+        _append(**b, k=torch.zeros((3, 2, 64), dtype=BF16), v=torch.zeros((3, 2, 64), dtype=BF16), q_out=out)
+
+
+def test_caches_that_are_written_are_two():
+    one = torch.zeros((6, 2, 16, 64), dtype=BF16)
+    both = torch.zeros((6, 2, 16, 2, 64), dtype=BF16)
+    _append(k_cache=both[:, 0].transpose(1, 2), v_cache=both[:, 1].transpose(1, 2))
+    slots = torch.zeros((6, 2, 16, 128), dtype=BF16)
+    _append(k_cache=slots[..., :64], v_cache=slots[..., 64:])
+    pair = torch.zeros((2, 6, 2, 16, 64), dtype=BF16)
+    _append(k_cache=pair[0], v_cache=pair[1])
+    _attention(k_cache=one, v_cache=one)                    # only read: keys may be the values
+    flat = torch.zeros(20000, dtype=BF16)
+    for k, v in ((one, one), (flat[:12288].view(6, 2, 16, 64), flat[2048:14336].view(6, 2, 16, 64)),
+                 (torch.as_strided(flat, (6, 2, 16, 64), (2048, 1024, 32, 1)), torch.zeros(20000, dtype=BF16).as_strided((6, 2, 16, 64), (2048, 1024, 32, 1))),
+                 (torch.as_strided(flat, (6, 2, 16, 64), (1024, 1024, 64, 1)), torch.zeros(20000, dtype=BF16).as_strided((6, 2, 16, 64), (1024, 1024, 64, 1)))):
+        with pytest.raises(ValueError, match="overlap"):
+            _append(k_cache=k, v_cache=v)
+
+
+def test_outputs_that_overlap_themselves():
+    flat = torch.zeros(4000)
+    for strides in ((256, 32, 1), (128, 64, 1), (64, 64, 1), (60, 256, 1)):
+        for make in (lambda out: _append(q_out=out), lambda out: _attention(out=out)):
+            with pytest.raises(ValueError, match="overlap|16 bytes"):
+                make(torch.as_strided(flat, (3, 4, 64), strides))
+    _attention(out=torch.as_strided(flat, (3, 4, 64), (64, 192, 1)))
+    with pytest.raises(ValueError, match="overlap"):
+        _matvec(out=torch.as_strided(flat, (3, 10), (9, 1)))
+    _matvec(out=torch.as_strided(flat, (3, 10), (10, 1)))
+
+
+def test_the_sums_log_is_apart():
+    buf = torch.zeros(2000)
+    q = buf[:768].view(3, 4, 64)
+    _attention(q=q, lse=buf[768:780].view(3, 4))
+    with pytest.raises(ValueError, match="lse"):
+        _attention(q=q, lse=buf[760:772].view(3, 4))
+    with pytest.raises(ValueError, match="lse"):
+        _attention(out=q, lse=buf[:12].view(3, 4))
+
+
+def test_products_are_written_apart_from_x_and_in_place_of_the_residual():
+    buf = torch.zeros((3, 512))
+    x = buf[:, :128]
+    square = dict(codes=torch.zeros((128, 64), dtype=torch.uint8), scales=torch.zeros((128, 2), dtype=BF16))
+    _matvec(x=x, **square, out=buf[:, 128:256])
+    for out in (buf[:, 4:132], buf[:, 127:255], x, torch.as_strided(buf, (3, 128), (500, 1), 300), buf.view(-1)[60:444].view(3, 128)):
+        with pytest.raises(ValueError, match="must not be x"):
+            _matvec(x=x, **square, out=out)
+    r = buf[:, 200:328]
+    _matvec(x=x, **square, residual=r, out=r)
+    _matvec(x=x, **square, residual=r, out=buf[:, 384:])
+    for out in (buf[:, 201:329], buf[:, 328 - 1:328 + 127], torch.as_strided(buf, (3, 128), (513, 1), 200)):
+        with pytest.raises(ValueError, match="overlap"):
+            _matvec(x=x, **square, residual=r, out=out)
