@@ -203,6 +203,9 @@ Region written(const at::Tensor &t, const char *name, int64_t inner) {
   return r;
 }
 
+// a stride that is used: 0 of a dimension of one element, whose stride torch leaves as it came
+int64_t step(const at::Tensor &t, int64_t i) { return t.size(i) > 1 ? t.stride(i) : 0; }
+
 // row and head strides of [n][heads][d]: the last dimension contiguous, every row on 16 bytes
 void heads(const at::Tensor &t, const char *name, int64_t n, int64_t d, int64_t h, c10::ScalarType type, const c10::Device &dev,
            int64_t *row, int64_t *head) {
@@ -212,12 +215,11 @@ void heads(const at::Tensor &t, const char *name, int64_t n, int64_t d, int64_t 
   if (s[0] != n || s[2] != d || (h > 0 && s[1] != h))
     throw Bad{std::string(name) + " must have " + std::to_string(n) + " rows of " + (h > 0 ? std::to_string(h) + " " : "") +
               "heads of " + std::to_string(d) + " elements"};
-  const auto st = t.strides();
   const int64_t unit = type == at::kFloat ? 4 : 8;
-  if (n && (st[2] != 1 || st[0] % unit || st[1] % unit || reinterpret_cast<uintptr_t>(t.data_ptr()) % 16))
+  *row = step(t, 0);
+  *head = step(t, 1);
+  if (n && (t.stride(2) != 1 || *row % unit || *head % unit || reinterpret_cast<uintptr_t>(t.data_ptr()) % 16))
     throw Bad{std::string(name) + ": the last dimension must be contiguous and every row start on 16 bytes"};
-  *row = st[0];
-  *head = st[1];
 }
 
 bool on16(const at::Tensor &t) { return reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0; }
@@ -228,13 +230,15 @@ mk_paged_kv cache(PyObject *ko, PyObject *vo, PyObject *to, PyObject *kso, PyObj
   const c10::Device dev = k.device();
   need(k.dim() == 4 && (type == at::kBFloat16 || type == at::kFloat8_e4m3fn),
        "k_cache must be [n_pages][n_kv_heads][page_size][head_dim] of bf16 or float8_e4m3fn");
-  need(v.sizes() == k.sizes() && v.strides() == k.strides() && v.scalar_type() == type && v.device() == dev,
+  need(v.sizes() == k.sizes() && v.scalar_type() == type && v.device() == dev && v.stride(3) == k.stride(3) && step(v, 0) == step(k, 0) &&
+           step(v, 1) == step(k, 1) && step(v, 2) == step(k, 2),
        "v_cache must have k_cache's shape, strides, dtype and device");
   need(!on_device || dev.is_cuda(), "the cache must be on a CUDA device");
-  const auto s = k.sizes(), st = k.strides();
+  const auto s = k.sizes();
+  const int64_t page = step(k, 0), head = step(k, 1), slot = step(k, 2);
   need(s[3] == 64 || s[3] == 128, "head_dim must be 64 or 128");
   const int64_t unit = type == at::kBFloat16 ? 8 : 16;
-  need(s[0] > 0 && s[1] > 0 && s[2] > 0 && st[3] == 1 && st[0] % unit == 0 && st[1] % unit == 0 && st[2] % unit == 0 && on16(k) && on16(v),
+  need(s[0] > 0 && s[1] > 0 && s[2] > 0 && k.stride(3) == 1 && page % unit == 0 && head % unit == 0 && slot % unit == 0 && on16(k) && on16(v),
        "the cache's last dimension must be contiguous and every slot start on 16 bytes");
   need(table.dim() == 2 && table.scalar_type() == at::kInt && table.device() == dev && (table.stride(1) == 1 || table.size(1) <= 1),
        "table must be int32 [rows][pages] on the cache's device, its rows contiguous");
@@ -245,7 +249,7 @@ mk_paged_kv cache(PyObject *ko, PyObject *vo, PyObject *to, PyObject *kso, PyObj
   c.v = v.data_ptr();
   c.dtype = type == at::kBFloat16 ? MK_BF16 : MK_E4M3;
   c.n_pages = small(s[0], "k_cache"), c.n_kv_heads = small(s[1], "k_cache"), c.page_size = small(s[2], "k_cache"), c.head_dim = static_cast<int32_t>(s[3]);
-  c.page_stride = st[0], c.head_stride = st[1], c.slot_stride = st[2];
+  c.page_stride = page, c.head_stride = head, c.slot_stride = s[2] > 1 ? slot : s[3];   // (slots one behind the other, if there is one)
   c.k_scale = static_cast<const float *>(vector(kso, "k_scale", at::kFloat, s[1], dev));
   c.v_scale = static_cast<const float *>(vector(vso, "v_scale", at::kFloat, s[1], dev));
   c.table = static_cast<const int32_t *>(table.data_ptr());
@@ -539,10 +543,10 @@ mk_matvec_q4_args matvec_args(PyObject *const *o, bool on_device, c10::Device *d
   mk_matvec_q4_args a = {};
   a.m = small(m, "x"), a.n = small(n, "codes"), a.k = small(k, "x"), a.group = small(group, "group");
   a.dtype = type_of(type);
-  need(!m || (x.stride(1) == 1 && x.stride(0) % (type == at::kFloat ? 4 : 8) == 0 && on16(x)),
+  need(!m || (x.stride(1) == 1 && step(x, 0) % (type == at::kFloat ? 4 : 8) == 0 && on16(x)),
        "x's last dimension must be contiguous and every row start on 16 bytes");
   a.x = x.data_ptr();
-  a.x_row = x.stride(0);
+  a.x_row = step(x, 0);
   a.codes = codes.data_ptr();
   a.scales = scales.data_ptr();
   if (o[M_ZEROS]) {
@@ -562,8 +566,8 @@ mk_matvec_q4_args matvec_args(PyObject *const *o, bool on_device, c10::Device *d
         const Region of(THPVariable_Unpack(o[M_RESIDUAL]), n);
         need(r == of || disjoint(r, of), "out must be residual itself or not overlap it");
       }
-      a.y = t.data_ptr(), a.y_row = t.stride(0);
-    } else a.residual = t.data_ptr(), a.residual_row = t.stride(0);
+      a.y = t.data_ptr(), a.y_row = step(t, 0);
+    } else a.residual = t.data_ptr(), a.residual_row = step(t, 0);
   }
   *device = dev;
   return a;

@@ -143,3 +143,29 @@ def test_products_are_written_apart_from_x_and_in_place_of_the_residual():
     for out in (buf[:, 201:329], buf[:, 328 - 1:328 + 127], torch.as_strided(buf, (3, 128), (513, 1), 200)):
         with pytest.raises(ValueError, match="overlap"):
             _matvec(x=x, **square, residual=r, out=out)
+
+
+def test_strides_of_single_rows_and_heads_do_not_matter():
+    # a dimension of one element has a stride that is never used
+    odd = torch.zeros(2000)
+    row = torch.as_strided(odd, (1, 4, 64), (257, 64, 1))
+    a = _append(k=torch.as_strided(odd, (1, 2, 64), (131, 64, 1)), v=torch.as_strided(odd, (1, 2, 64), (7, 64, 1)), slots=_i32(1), q=row,
+                q_out=torch.as_strided(torch.zeros(2000), (1, 4, 64), (3, 64, 1)))
+    assert a.n == 1 and a.k_row % 4 == a.v_row % 4 == a.q_row % 4 == a.out_row % 4 == 0
+    a = _attention(q=row, lengths=_i32(1), out=row)
+    assert a.q_row == a.out_row
+    head = torch.as_strided(odd, (3, 1, 64), (64, 1, 1))
+    one = dict(k_cache=torch.zeros((6, 1, 16, 64), dtype=BF16), v_cache=torch.zeros((6, 1, 16, 64), dtype=BF16))
+    assert _attention(**one, q=head, out=torch.as_strided(torch.zeros(300), (3, 1, 64), (64, 5, 1))).q_head % 4 == 0
+    # in place by another view of the same memory
+    _attention(q=row, lengths=_i32(1), out=torch.as_strided(odd, (1, 4, 64), (256, 64, 1)))
+    a = _matvec(x=torch.as_strided(odd, (1, 128), (129, 1)), out=torch.as_strided(torch.zeros(64), (1, 10), (3, 1)),
+                residual=torch.as_strided(torch.zeros(64), (1, 10), (1, 1)))
+    assert a.m == 1 and a.x_row % 4 == 0
+    flat = torch.zeros(5000, dtype=BF16)
+    kv = S.paged_struct(torch.as_strided(flat, (1, 1, 16, 64), (3, 5, 64, 1)), torch.as_strided(flat[2048:], (1, 1, 16, 64), (1024, 1024, 64, 1)),
+                        _i32(3, 4), on_device=False)
+    assert kv.page_stride % 8 == kv.head_stride % 8 == 0 and kv.slot_stride == 64
+    for bad in (dict(k=torch.as_strided(odd, (3, 2, 64), (131, 64, 1))), dict(q=torch.as_strided(odd, (3, 4, 64), (257, 64, 1)))):
+        with pytest.raises(ValueError, match="16 bytes"):
+            _append(**bad)
