@@ -470,8 +470,9 @@ class Decoder:
             raise ValueError("the paged cache must be on %s" % self.device)
         count = self.position - first if count is None else count
         with torch.cuda.device(self.device):
-            _check(self.lib.mk_export_kv(self.h, layer, first, count, C.byref(kv), seq, slot, _stream_ptr(stream)),
-                   "mk_export_kv")
+            rc = self.lib.mk_export_kv(self.h, layer, first, count, C.byref(kv), seq, slot, _stream_ptr(stream))
+        torch.autograd.graph.increment_version([t for t in (k_cache, v_cache) if not t.is_inference()])
+        _check(rc, "mk_export_kv")
 
     def decode_start(self, in_ids=None, n_steps: int = 0, *, out: Optional[torch.Tensor] = None,
                      stream_ids: bool = True, per_op=False, embeds: Optional[torch.Tensor] = None,

@@ -14,6 +14,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -91,9 +92,20 @@ struct Signature {
   }
 };
 
+// a tensor that autograd does not follow: none of the operators has a backward, and none may be left out unnoticed
 const at::Tensor &tensor(PyObject *o, const char *name) {
   if (!o || !THPVariable_Check(o)) throw Bad{std::string(name) + " must be a tensor"};
-  return THPVariable_Unpack(o);
+  const at::Tensor &t = THPVariable_Unpack(o);
+  if (t.requires_grad() && c10::GradMode::is_enabled())
+    throw Bad{std::string(name) + " requires grad, and this operator has no gradient: call it under torch.no_grad()"};
+  return t;
+}
+
+// what a call has written counts as changed for autograd graphs that saved it
+void changed(PyObject *o) {
+  if (!o) return;
+  const at::Tensor &t = THPVariable_Unpack(o);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
 double number(PyObject *o) {
@@ -414,7 +426,10 @@ PyObject *paged_append(PyObject *const *o) {
     a.out_row = made.stride(0);
     a.out_head = made.stride(1);
   }
-  if (a.n) enqueue("mk_paged_append", [&] { return mk_paged_append(&kv, &a, on.stream); });
+  if (a.n) {
+    enqueue("mk_paged_append", [&] { return mk_paged_append(&kv, &a, on.stream); });
+    for (int i : {A_KC, A_VC, A_QOUT, A_STATUS}) changed(o[i]);
+  }
   if (!o[A_Q]) Py_RETURN_NONE;
   return o[A_QOUT] ? given(o[A_QOUT]) : THPVariable_Wrap(made);
 }
@@ -510,6 +525,7 @@ PyObject *paged_attention(PyObject *const *o) {
       if (workspace.error) std::rethrow_exception(workspace.error);
       throw;
     }
+    for (int i : {T_OUT, T_LSE, T_STATUS}) changed(o[i]);
   }
   return o[T_OUT] ? given(o[T_OUT]) : THPVariable_Wrap(made);
 }
@@ -583,7 +599,10 @@ PyObject *matvec_q4(PyObject *const *o) {
     a.y = made.data_ptr();
     a.y_row = a.n;
   }
-  if (a.m && a.n) enqueue("mk_matvec_q4", [&] { return mk_matvec_q4(&a, on.stream); });
+  if (a.m && a.n) {
+    enqueue("mk_matvec_q4", [&] { return mk_matvec_q4(&a, on.stream); });
+    changed(o[M_OUT]);
+  }
   return o[M_OUT] ? given(o[M_OUT]) : THPVariable_Wrap(made);
 }
 

@@ -4,7 +4,9 @@
 the projections, each one call of the C ABI (``include/mk.h``).  They enqueue on
 the stream and return; what only the device can see (a page id outside the
 cache, a position outside the rotary table) goes to an optional ``status`` word
-that ``check_status`` turns into an ``MKError``.  They have no gradients.
+that ``check_status`` turns into an ``MKError``.  They have no gradients:
+a tensor that requires them is refused unless gradients are off
+(``torch.no_grad``).
 
 The three are functions of the module ``_mktorch`` (``csrc/mk_torch.cpp``), which
 checks the tensors of a call against what the kernels read and write (a wrong
@@ -60,6 +62,7 @@ def quantize_q4(w: torch.Tensor, group: int = 64, zeros: bool = False):
     bf16 [n][k / group])`` with codes 0 .. 15 around 8, or, with ``zeros``, a zero
     point of each group as a third tensor (uint8), which uses all 16 codes of a
     group that is not centred.  Codes are the nearest to w over the rounded scale."""
+    w = w.detach()
     n, k = w.shape
     if not (group in (32, 64) or (group > 0 and group % 128 == 0)) or k % group:
         raise ValueError("the group must be 32, 64 or a multiple of 128, and divide k (%d)" % k)

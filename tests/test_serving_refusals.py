@@ -169,3 +169,36 @@ def test_strides_of_single_rows_and_heads_do_not_matter():
     for bad in (dict(k=torch.as_strided(odd, (3, 2, 64), (131, 64, 1))), dict(q=torch.as_strided(odd, (3, 4, 64), (257, 64, 1)))):
         with pytest.raises(ValueError, match="16 bytes"):
             _append(**bad)
+
+
+def test_inputs_that_require_gradients():
+    # there is no backward: a call that would record one is refused, one under no_grad is not
+    def grad(t):
+        return t.clone().requires_grad_()
+    x = torch.zeros((3, 4, 64))
+    calls = [(_append, dict(k=torch.zeros((3, 2, 64)))), (_append, dict(v=torch.zeros((3, 2, 64)))), (_append, dict(q=x)), (_append, dict(q_out=x)),
+             (_append, dict(rope=torch.zeros((4, 32, 2)))), (_append, dict(q_norm=torch.zeros(64, dtype=BF16))),
+             (_append, dict(k_norm=torch.zeros(64, dtype=BF16))), (_append, dict(k_cache=_cache()["k_cache"])), (_append, dict(v_cache=_cache()["v_cache"])),
+             (_attention, dict(q=x)), (_attention, dict(out=x)), (_attention, dict(lse=torch.zeros((3, 4)))), (_attention, dict(v_cache=_cache()["v_cache"])),
+             (_matvec, dict(x=torch.zeros((3, 128)))), (_matvec, dict(residual=torch.zeros((3, 10)))), (_matvec, dict(out=torch.zeros((3, 10)))),
+             (_matvec, dict(scales=torch.zeros((10, 2), dtype=BF16)))]
+    for f, kw in calls:
+        with torch.no_grad():
+            f(**{k: grad(v) for k, v in kw.items()})
+        with torch.inference_mode():
+            f(**{k: grad(v) for k, v in kw.items()})
+        for t in (grad, lambda v: grad(v)[:]):              # a leaf, a view of one
+            with pytest.raises(ValueError, match="%s.*gradient" % list(kw)[0]):
+                f(**{k: t(v) for k, v in kw.items()})
+    fp8 = torch.zeros((6, 2, 16, 64), dtype=E4M3)
+    with pytest.raises(ValueError, match="gradient"):
+        _attention(k_cache=fp8, v_cache=fp8, k_scale=torch.ones(2).requires_grad_(), v_scale=torch.ones(2))
+
+
+def test_quantised_weights_of_a_parameter():
+    w = torch.nn.Parameter(torch.randn((10, 128), generator=torch.Generator().manual_seed(0)))
+    for zeros in (False, True):
+        got = mk.quantize_q4(w, 64, zeros)
+        assert not any(t.requires_grad for t in got)
+        assert all(torch.equal(a, b) for a, b in zip(got, mk.quantize_q4(w.detach(), 64, zeros)))
+        _matvec(codes=got[0], scales=got[1], zeros=got[2] if zeros else None)
