@@ -66,7 +66,7 @@ def quantize_q4(w: torch.Tensor, group: int = 64, zeros: bool = False):
     n, k = w.shape
     if not (group in (32, 64) or (group > 0 and group % 128 == 0)) or k % group:
         raise ValueError("the group must be 32, 64 or a multiple of 128, and divide k (%d)" % k)
-    x = w.float().view(n, k // group, group)
+    x = w.float().reshape(n, k // group, group)
     if zeros:
         lo, hi = x.amin(-1).clamp_max(0.0), x.amax(-1).clamp_min(0.0)
         scale = ((hi - lo) / 15.0).bfloat16()
