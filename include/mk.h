@@ -338,7 +338,9 @@ int mk_embed_sum_noalloc(const void *books, int32_t n_books, int32_t book_rows, 
  *
  * They differ from the handle's calls in one way: they enqueue on `stream` and
  * return, allocate nothing, keep nothing between calls and can be captured into
- * a CUDA graph.  Argument errors are returned before anything is enqueued.
+ * a CUDA graph (mk_export_kv is a call of the handle: it allocates a word, waits
+ * and makes the handle's device current).  Argument errors are returned before
+ * anything is enqueued.
  * What only the device sees (a page id outside the cache, a position outside
  * the table) is written to *status if it is not NULL -- the first error's code;
  * the caller zeroes it -- and no address outside the caller's buffers is formed.

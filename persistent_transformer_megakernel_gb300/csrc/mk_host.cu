@@ -831,6 +831,7 @@ int mk_export_kv(mk_handle *h, int32_t layer, int32_t first, int32_t count, cons
   if (seq < 0 || seq >= kv->table_rows) return MK_ERR_INVALID_ARG;
   if (kv->n_kv_heads != h->cfg.n_kv_heads || kv->head_dim != h->cfg.head_dim) return MK_ERR_UNSUPPORTED;
   if (count == 0) return MK_OK;
+  if (cudaSetDevice(h->device) != cudaSuccess) return MK_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int *d_status = nullptr;
   if (cudaMallocAsync(&d_status, sizeof(int), s) != cudaSuccess) {
