@@ -58,8 +58,10 @@ def _link_module(obj: str) -> None:
     os.replace(tmp, MODULE)
 
 
-def build(verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link libmk.so and _mktorch.so; returns libmk.so's path."""
+def build(verbose: bool = False, ptxas_info: bool = False, module: bool = True) -> str:
+    """Compile and link libmk.so and, unless ``module`` is false, _mktorch.so;
+    returns libmk.so's path.  libmk.so needs nvcc alone and is there even if
+    _mktorch.so, which needs torch, Python's headers and g++, raises."""
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
@@ -70,13 +72,19 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
 
     module_obj = os.path.join(OUT_DIR, "mk_torch.o")
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        module = ex.submit(_compile_module, module_obj)
+        made = ex.submit(_compile_module, module_obj) if module else None
         logs = list(ex.map(one, range(len(SOURCES))))
-        module.result()
-    tmp = LIB + ".tmp"
-    _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"])
-    os.replace(tmp, LIB)
-    _link_module(module_obj)
+        tmp = LIB + ".tmp"
+        _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"])
+        os.replace(tmp, LIB)
+        if module:
+            try:
+                made.result()
+                _link_module(module_obj)
+            except (ImportError, OSError, RuntimeError) as e:
+                if os.path.exists(MODULE):               # one of an earlier build may expect another libmk.so
+                    os.remove(MODULE)
+                raise RuntimeError("%s is built, _mktorch.so (the serving operators on torch tensors) is not: %s" % (LIB, e)) from e
     if verbose:
         for s, log in zip(SOURCES, logs):
             if log.strip():
@@ -85,5 +93,5 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
 
 
 if __name__ == "__main__":
-    build(verbose=True, ptxas_info="-v" in sys.argv)
+    build(verbose=True, ptxas_info="-v" in sys.argv, module="--library" not in sys.argv)   # --library: libmk.so alone
     print(LIB)
