@@ -363,7 +363,7 @@ typedef struct {
   int32_t n_pages, n_kv_heads, page_size, head_dim;
   int64_t page_stride, head_stride, slot_stride;
   const float *k_scale, *v_scale; /* MK_E4M3: device [n_kv_heads], what a stored value is multiplied
-                                     by; both or neither (NULL = 1).  MK_BF16: NULL */
+                                     by (not subnormal); both or neither (NULL = 1).  MK_BF16: NULL */
   const int32_t *table;        /* device [table_rows][table_cols] page ids */
   int32_t table_rows, table_cols;
   int64_t table_stride;        /* elements from row to row; 0 = every row the same pages */
@@ -426,10 +426,13 @@ typedef struct {
 
 /* Attention of one new token per row over the paged cache:
  *   out = sum_p softmax_p(scale * q.k[p]) v[p],  lse = log sum_p exp(scale * q.k[p])
- * over p in [max(0, length - window), length).  The work of all rows is cut
+ * over p in [max(0, length - window), length).  The work of several rows is cut
  * into equal shares over the SMs whatever the lengths (read on the device, so
- * that a captured call follows them), and the shares of a row are joined in a
- * fixed order: the same inputs give the same bits.  A row with no tokens gives
+ * that a captured call follows them); rows of up to about a thousand slots are
+ * not cut, and a single row has at most 16 SMs a kv head.  The shares of a row are
+ * joined in a fixed order: the same inputs give the same bits.  Scores are fp32
+ * numbers (a q.k beyond their range is an infinity); over an MK_E4M3 cache, query
+ * elements are rounded to 2^-38 of their head's largest and fp32 ones to 22 bits.  A row with no tokens gives
  * zeros and lse -inf.  Slots at and past a row's length are never read into a
  * result, whatever they hold.  A row with a page id outside the cache, or a
  * length past table_cols * page_size, gives NaN and MK_ERR_BAD_PAGE.  Several
@@ -487,7 +490,8 @@ typedef struct {
 
 /* y = x w^T (+ residual) for a few rows x, accumulated in fp32 and rounded once.
  * x and the codes enter the products as they are (of x elements below 2^-141 of
- * their row's largest, bits below 2^-165 of it may be lost).  Made for decode (m
+ * their row's largest, bits below 2^-165 of it may be lost; scales of 2^80 and
+ * more may overflow in a sum whose result would not).  Made for decode (m
  * of 1 to some tens); further rows read the weights again.  A zero above 15
  * counts modulo 16.  Errors: MK_ERR_INVALID_ARG,
  * MK_ERR_UNSUPPORTED (group, k), MK_ERR_CUDA. */
