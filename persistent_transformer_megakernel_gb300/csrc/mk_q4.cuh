@@ -57,7 +57,7 @@ constexpr int kWarps = 16, kThreads = 32 * kWarps, kBlock = 128;
 constexpr int kRing = 4096;            // bytes of codes a warp has room for: 4 blocks of 16 rows (twice as many measured slower)
 constexpr int kMaxSmem = 225 * 1024;   // dynamic shared memory of a CTA
 constexpr int kMaxInbox = 32768;       // of a cluster's CTA, for the tiles that it joins
-constexpr int red_bytes(int parts, int rt) { return kWarps * rt * parts * 512; }   // sums of the warps
+constexpr int red_bytes(int parts) { return kWarps * parts * 512; }   // sums of the warps
 
 // G: 32, 64, or 128 for every multiple of it
 template <int G>
@@ -540,11 +540,36 @@ int pitch_of(int blocks) { return blocks * kBlock * 2 + Layout<G>::pad; }
 // a launch that cannot be: clusters that do not fit, more tiles than an inbox holds, no room for one x row
 constexpr int kRefused = 1;
 
+// How a launch's CTAs (or clusters of c, `units` of them at once) share the tiles, and what shared memory leaves room for.
+struct Plan {
+  int wk, want, red, inbox;    // warps a tile, CTAs or clusters, bytes of the warps' sums and of the inbox
+  int rows;                    // x rows of a pass: as many as the columns hold and there is room for; 0: none, or no inbox
+};
+template <class T, int NT, int RT>
+Plan plan_of(const Q4Params &p, int tiles, int blocks, int pitch, int c, int units) {
+  constexpr int PARTS = RT * Columns<T, NT>::parts;
+  Plan r = {};
+  // the sharing of k that leaves the busiest warp the fewest blocks, fewer warps a tile where that is equal
+  int64_t best = 0;
+  for (int wk = 1; wk <= kWarps; wk *= 2) {
+    const int64_t per_round = static_cast<int64_t>(units) * (kWarps / wk), rounds = (tiles + per_round - 1) / per_round;
+    const int64_t cost = rounds * ((blocks + wk - 1) / wk);
+    if (wk == 1 || cost < best) best = cost, r.wk = wk;
+  }
+  const int per_cta = kWarps / r.wk;
+  r.want = std::min((tiles + per_cta - 1) / per_cta, units);
+  r.red = r.wk > 1 ? red_bytes(PARTS) : 0;
+  const int64_t rounds = (tiles + static_cast<int64_t>(r.want) * per_cta - 1) / (static_cast<int64_t>(r.want) * per_cta);
+  const int64_t inbox = c > 1 ? (rounds * per_cta + c - 1) / c * c * PARTS * 512 : 0;
+  if (inbox > kMaxInbox) return r;
+  r.inbox = static_cast<int>(inbox);
+  r.rows = std::min({p.m, Columns<T, NT>::rows, (kMaxSmem - kWarps * kRing - r.red - r.inbox) / pitch / kTerms<T>});
+  return r;
+}
+
 template <class T, int NT, int RT, int G, bool ZEROS, int C>
 int launch_as(Q4Params p, int sms, int dev, cudaStream_t s) {
   static_assert(C == 1 || C == 4);
-  using X = Columns<T, NT>;
-  constexpr int PARTS = RT * X::parts;
   static mkw::Ready ready[mkw::kMaxDevices];
   const auto fn = &matvec_kernel<T, NT, RT, G, ZEROS, C>;
   mkw::Ready &r = ready[dev];
@@ -558,24 +583,13 @@ int launch_as(Q4Params p, int sms, int dev, cudaStream_t s) {
   const int blocks = (p.blocks + C - 1) / C;   // of a CTA
   p.pitch = pitch_of<G>(blocks);
   p.eighths.set(blocks * (kBlock / 8));
-  // the sharing of k that leaves the busiest warp the fewest blocks, fewer warps a tile where that is equal
-  int64_t best = 0;
-  for (int wk = 1; wk <= kWarps; wk *= 2) {
-    const int64_t per_round = static_cast<int64_t>(clusters) * (kWarps / wk), rounds = (p.tiles + per_round - 1) / per_round;
-    const int64_t cost = rounds * ((blocks + wk - 1) / wk);
-    if (wk == 1 || cost < best) best = cost, p.wk = wk;
-  }
-  const int per_cta = kWarps / p.wk, want = std::min((p.tiles + per_cta - 1) / per_cta, clusters);
-  // x rows of a pass: as many as its columns hold and shared memory has room for
-  const int red = p.wk > 1 ? red_bytes(X::parts, RT) : 0, rounds = (p.tiles + want * per_cta - 1) / (want * per_cta);
-  const int64_t inbox = C > 1 ? (static_cast<int64_t>(rounds) * per_cta + C - 1) / C * C * PARTS * 512 : 0;
-  if (inbox > kMaxInbox) return kRefused;
-  p.pass_rows = std::min({p.m, X::rows, (kMaxSmem - kWarps * kRing - red - static_cast<int>(inbox)) / p.pitch / kTerms<T>});
-  if (p.pass_rows < 1) return kRefused;
-  p.inbox = kWarps * kRing + red + p.pass_rows * kTerms<T> * p.pitch;
+  const Plan plan = plan_of<T, NT, RT>(p, p.tiles, blocks, p.pitch, C, clusters);
+  if (plan.rows < 1) return kRefused;
+  p.wk = plan.wk, p.pass_rows = plan.rows;
+  p.inbox = kWarps * kRing + plan.red + p.pass_rows * kTerms<T> * p.pitch;
   const int passes = (p.m - 1) / p.pass_rows + 1;
   if (passes > 65535) return MK_ERR_UNSUPPORTED;
-  return mkw::launch_after(fn, dim3(want * C, passes), kThreads, p.inbox + static_cast<int>(inbox), s, p, C);
+  return mkw::launch_after(fn, dim3(plan.want * C, passes), kThreads, p.inbox + plan.inbox, s, p, C);
 }
 
 template <class T, int NT, int RT, int G, bool ZEROS>
@@ -594,11 +608,12 @@ int by_group(Q4Params &p, int group, int sms, int dev, cudaStream_t s) {
   return launch<T, NT, RT, 128, ZEROS>(p, sms, dev, s);
 }
 
-// passes over the weights with NT column tiles, 16 RT rows a tile and clusters of c CTAs; 0: not one x row fits
+// passes over the weights with NT column tiles, 16 RT rows a tile and clusters of c CTAs (if all SMs can be in one); 0: not
+// one x row fits
 template <class T, int NT, int RT = 1>
-int passes_of(const Q4Params &p, int c) {
-  const int room = kMaxSmem - kWarps * kRing - red_bytes(Columns<T, NT>::parts, RT) - (c > 1 ? kMaxInbox : 0);
-  const int rows = std::min(Columns<T, NT>::rows, room / pitch_of<32>((p.blocks + c - 1) / c) / kTerms<T>);
+int passes_of(const Q4Params &p, int c, int sms) {
+  const int blocks = (p.blocks + c - 1) / c;
+  const int rows = plan_of<T, NT, RT>(p, (p.n + 16 * RT - 1) / (16 * RT), blocks, pitch_of<32>(blocks), c, std::max(1, sms / c)).rows;
   return rows < 1 ? 0 : (p.m - 1) / rows + 1;
 }
 
@@ -606,14 +621,16 @@ template <class T, bool ZEROS>
 int by_columns(Q4Params &p, int group, int sms, int dev, cudaStream_t s) {
   // the fewest passes, and of these the fewest columns
   constexpr int A = std::is_same<T, float>::value ? 3 : 4, B = std::is_same<T, float>::value ? 6 : 4;
-  const int one = passes_of<T, 1>(p, p.cluster), two = passes_of<T, 2>(p, p.cluster), some = passes_of<T, A>(p, p.cluster), most = passes_of<T, B>(p, p.cluster);
-  const int fewest = std::min({one ? one : INT32_MAX, two ? two : INT32_MAX, some ? some : INT32_MAX, most ? most : INT32_MAX});
-  if (fewest == INT32_MAX) return kRefused;
-  if (one == fewest) {
+  const int one = passes_of<T, 1>(p, p.cluster, sms);
+  if (one == 1) {
     // 32 rows a tile, whose matrix products share what is read of x, where every warp has one of them
-    if (p.cluster == 1 && p.n / 32 >= sms * kWarps && passes_of<T, 1, 2>(p, 1) == 1) return by_group<T, 1, 2, ZEROS>(p, group, sms, dev, s);
+    if (p.cluster == 1 && p.n / 32 >= sms * kWarps && passes_of<T, 1, 2>(p, 1, sms) == 1) return by_group<T, 1, 2, ZEROS>(p, group, sms, dev, s);
     return by_group<T, 1, 1, ZEROS>(p, group, sms, dev, s);
   }
+  const int two = passes_of<T, 2>(p, p.cluster, sms), some = passes_of<T, A>(p, p.cluster, sms), most = passes_of<T, B>(p, p.cluster, sms);
+  const int fewest = std::min({one ? one : INT32_MAX, two ? two : INT32_MAX, some ? some : INT32_MAX, most ? most : INT32_MAX});
+  if (fewest == INT32_MAX) return kRefused;
+  if (one == fewest) return by_group<T, 1, 1, ZEROS>(p, group, sms, dev, s);
   if (two == fewest) return by_group<T, 2, 1, ZEROS>(p, group, sms, dev, s);
   if (some == fewest) return by_group<T, A, 1, ZEROS>(p, group, sms, dev, s);
   return by_group<T, B, 1, ZEROS>(p, group, sms, dev, s);
@@ -629,7 +646,7 @@ int by_rows(Q4Params &p, int group, int sms, int dev, cudaStream_t s) {
   // 12288 x 2048 in bf16, 0.8 times, 14.4 and 12.8, 8 x 12288 x 2048, 32 KB, 12.3 and 11.0: a cluster's launch alone costs
   // 1 us.  Clusters of 2 or 8 were slower where clusters paid.)
   const int64_t staged = static_cast<int64_t>(p.m) * p.k * kTerms<T> * 2, codes = static_cast<int64_t>(p.n) * p.k / 2 / sms;
-  const bool fits = passes_of<T, 1>(p, 1) > 0;
+  const bool fits = (kMaxSmem - kWarps * kRing - red_bytes(Columns<T, 1>::parts)) / pitch_of<32>(p.blocks) >= kTerms<T>;   // an x row in a CTA
   p.cluster = !fits || (staged >= 49152 && staged >= codes) ? 4 : 1;
   if (fits) {
     int rc = by_columns<T, ZEROS>(p, group, sms, dev, s);
