@@ -29,8 +29,8 @@ __device__ __forceinline__ void report(int32_t *status, int code) {
 // thread; the squares are summed over the head's threads by shuffles.  A token
 // that would need a page outside the cache or a rotary row outside the table is
 // not written.
-// Two kernels: for few tokens a thread for every part of every head (one token
-// 2.8 us, 256 of 32 heads 3.5), for many persistent warps that copy ahead (20011
+// Two kernels: for few tokens a thread for every part of every head (in graphs, one
+// token 2.7 us, 256 of 32 heads 3.5), for many persistent warps that copy ahead (20011
 // tokens of 32 heads of 128, bf16 to e4m3, 291 MB: 50 us, 5.8 TB/s).  They meet
 // where the threads of the first are no longer resident at once (about 450
 // tokens: 384 take 3.7 and 4.4 us, 512 4.7 both ways); the first kernel with 4
@@ -527,9 +527,10 @@ int run_append(const AppendParams &p, int dtype, int cache, int d, cudaStream_t 
 //   - else the same with the CTAs' ranges as they fall: what a CTA has of a row
 //     at its range's ends goes through the workspace to join_kernel.
 // Parts are joined in order: the same lengths give the same bits.
-// Measured (graph replays; a loop of plain calls takes 9 us for one short row): 16 query heads on 8 of 128, 64 rows of 0 to 8192 tokens in bf16 (306 MB) 53 us, 5.7 TB/s; 16 rows of 30 to
-// 32 k in e4m3 (1034 MB) 157 us, 6.6 TB/s; one row of 257 tokens 6.9 us, of 5119 12.6 (fp32 queries); 256 rows of up to
-// 300 tokens, 8 heads on 2 of 64, 9.4 us.
+// Measured (graph replays; where a call is shorter than its launch a loop of plain calls takes longer, 8 to 9 us for one
+// row of 257 tokens): 16 query heads on 8 of 128, 64 rows of 0 to 8192 tokens in bf16 (306 MB) 53 us, 5.7 TB/s; 16 rows of
+// 30 to 32 k in e4m3 (1034 MB) 158 us, 6.5 TB/s; one row of 257 tokens 6.8 us, of 5119 12.6 (fp32 queries); 256 rows of up
+// to 300 tokens, 8 heads on 2 of 64, 9.6 us.
 // ---------------------------------------------------------------------------
 
 constexpr int kWarps = 8, kAttnThreads = 32 * kWarps;
