@@ -18,6 +18,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -638,11 +639,8 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyObject *kw
       PyErr_SetObject(mk_error, err);
       Py_DECREF(err);
     }
-  } catch (const c10::Error &e) {
-    const char *what = e.what_without_backtrace();
-    PyErr_SetString(PyExc_RuntimeError, what);
-  } catch (const std::exception &e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {                                          // torch's own: out of memory among them
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

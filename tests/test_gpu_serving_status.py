@@ -44,3 +44,20 @@ def test_an_error_on_a_side_stream(op):
     mk.paged_append(x, x, kc, vc, table, one, status=status, stream=torch.cuda.current_stream())
     mk.check_status(status, stream=torch.cuda.current_stream())
     mk.check_status(status)
+
+
+def test_out_of_memory_is_torchs_own_error():
+    # the result of this call is 34 GB, which the process is not allowed; nothing of that size exists
+    n = 1 << 20
+    kc = torch.zeros((1, 64, 4, 128), dtype=BF16, device="cuda")
+    q = torch.zeros((1, 64, 128), device="cuda").expand(n, -1, -1)
+    table = torch.zeros((1, 1), dtype=torch.int32, device="cuda").expand(n, -1)
+    lengths = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    torch.cuda.set_per_process_memory_fraction(0.02)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            mk.paged_attention(q, kc, kc, table, lengths)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    out = mk.paged_attention(q[:2], kc, kc, table[:2], lengths[:2] + 2)
+    assert (out == 0).all()
