@@ -40,7 +40,8 @@ extern "C" {
 #define MK_OK               0
 #define MK_ERR_INVALID_ARG (-1)  /* bad pointer, size or option, checked on the host */
 #define MK_ERR_UNSUPPORTED (-2)  /* shape or launch geometry this build does not handle */
-#define MK_ERR_KV_FULL     (-3)  /* position + forwards would pass max_seq (host check) */
+#define MK_ERR_KV_FULL     (-3)  /* position + forwards would pass max_seq (host check); a step that
+                                    mk_paged_plan has no room for (found on the device) */
 #define MK_ERR_BAD_TOKEN   (-4)  /* id >= vocab_in, or a sentinel row outside the buffer
                                     (found on the device; later forwards are skipped) */
 #define MK_ERR_TIMEOUT     (-5)  /* a device wait (grid barrier, ring, merge) ran past
@@ -422,11 +423,13 @@ typedef struct {
   void *workspace;             /* device, 16-byte aligned; the call's own until the stream has passed it */
   int64_t workspace_bytes;     /* at least mk_paged_attention_workspace */
   int32_t *status;             /* device, or NULL */
+  int32_t sinks;               /* with a window: the first `sinks` tokens stay visible beside it; else unused */
 } mk_attention_args;
 
 /* Attention of one new token per row over the paged cache:
  *   out = sum_p softmax_p(scale * q.k[p]) v[p],  lse = log sum_p exp(scale * q.k[p])
- * over p in [max(0, length - window), length).  The work of several rows is cut
+ * over p in [max(0, length - window), length) and, with a window, p in
+ * [0, min(sinks, length)).  The work of several rows is cut
  * into equal shares over the SMs whatever the lengths (read on the device, so
  * that a captured call follows them); rows of up to about a thousand slots are
  * not cut, and a single row has at most 16 SMs a kv head.  The shares of a row are
@@ -456,6 +459,84 @@ int mk_paged_attention_ask(const mk_paged_kv *kv, const mk_attention_args *a, mk
  * current device (it does not depend on rows or lengths).  MK_ERR_INVALID_ARG,
  * MK_ERR_UNSUPPORTED or MK_ERR_CUDA as a negative result. */
 int64_t mk_paged_attention_workspace(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim);
+
+typedef struct {
+  int32_t n;                   /* sequences, one per table row: 0 <= n <= table_rows; at most 16384 */
+  int32_t rows;                /* of q and out */
+  int32_t dtype;               /* of q and out: MK_BF16 (MK_F32: MK_ERR_UNSUPPORTED; mk_paged_attention takes it, a row
+                                  for each token) */
+  int32_t n_q_heads;           /* a multiple of n_kv_heads */
+  const void *q;               /* device [rows][n_q_heads][head_dim] */
+  void *out;                   /* device, the same shape; may be q itself (same strides), else no part of it or the cache */
+  int64_t q_row, q_head, out_row, out_head; /* strides, elements */
+  float *lse;                  /* device [rows][n_q_heads], or NULL; no part of q or out */
+  const int32_t *starts;       /* device [n + 1], not decreasing: sequence i has rows [starts[i], starts[i + 1]); other rows
+                                  are left as they were */
+  const int32_t *lengths;      /* device [n] tokens of each sequence, those of its rows included; negative = its rows are
+                                  padding, left as they were */
+  int32_t window, sinks;       /* as for mk_paged_attention, at each row's own place */
+  float scale;
+  void *workspace;             /* device, 16-byte aligned; the call's own until the stream has passed it */
+  int64_t workspace_bytes;     /* at least mk_paged_prompt_attention_workspace (rows that see few tokens need none) */
+  int32_t *status;             /* device, or NULL */
+} mk_prompt_args;
+
+/* Causal attention of the last tokens of each sequence over the paged cache, their
+ * own keys and values (appended before) included: row r of sequence i is its token
+ *   t = lengths[i] - (starts[i + 1] - starts[i]) + r - starts[i]
+ * and sees tokens p <= t, with a window those of (t - window, t] and [0, sinks).
+ * Whole prompts (lengths = rows), chunks behind what is cached, drafted tokens.
+ * Scores and sums are fp32; the weights multiply the values rounded to bf16,
+ * over an MK_E4M3 cache to fp16, and query elements there to 2^-38 of their head's
+ * largest.  The same inputs give the same bits.  A row that sees nothing (t < 0)
+ * gives zeros and lse -inf; tokens that a row does not see are never read into
+ * its result, whatever they hold.  A row that sees a page id outside the cache, or
+ * whose sequence is longer than table_cols * page_size, gives NaN and MK_ERR_BAD_PAGE;
+ * a sequence whose starts are outside rows or decrease is skipped (MK_ERR_BAD_PAGE).
+ * Rows whose results are infinite or NaN take a slow path.  Errors:
+ * MK_ERR_INVALID_ARG, MK_ERR_UNSUPPORTED (dtype, head_dim, sizes), MK_ERR_CUDA; in
+ * *status also MK_ERR_TIMEOUT if a wait inside the kernel ran out. */
+int mk_paged_prompt_attention(const mk_paged_kv *kv, const mk_prompt_args *a, mk_stream stream);
+
+/* The same as mk_paged_attention_ask is to mk_paged_attention. */
+int mk_paged_prompt_attention_ask(const mk_paged_kv *kv, const mk_prompt_args *a, mk_workspace_fn workspace,
+                                  void *context, mk_stream stream);
+
+/* Bytes of workspace any mk_paged_prompt_attention call needs on the current
+ * device, or a negative error. */
+int64_t mk_paged_prompt_attention_workspace(int32_t head_dim);
+
+typedef struct {
+  int32_t n;                   /* sequences; at most 16384 */
+  int32_t rows;                /* token rows of seqs and slots; n without counts */
+  int32_t page_size;
+  const int32_t *lengths;      /* device [n] tokens that each sequence has; negative = a padding row, which gets none */
+  const int32_t *counts;       /* device [n] tokens that it gets (negative = 0), or NULL = one each */
+  int32_t *table;              /* device [n][table_cols] page ids, extended in place */
+  int32_t table_cols;
+  int64_t table_stride;
+  const int32_t *free;         /* device [free_count] pages that may be taken */
+  int32_t free_count;
+  const int32_t *used;         /* device [1] how many of them are taken already */
+  int32_t *seqs, *slots;       /* device [rows] each token row's sequence and slot; rows without a token: -1 */
+  int32_t *starts;             /* device [n + 1] first row of each sequence, and the end */
+  int32_t *totals;             /* device [n] lengths + counts; may be lengths */
+  int32_t *used_out;           /* device [1]; may be used */
+  int32_t *status;             /* device, or NULL */
+} mk_plan_args;
+
+/* Plan a step: give each sequence's new tokens their rows, slots and, where its
+ * last page is full, pages: token p of sequence i is in page table[i][p / page_size],
+ * which is the next of `free` (counted through the sequences in order) if the
+ * sequence had no such page.  With counts the rows are the sequences' tokens one
+ * behind the other (for mk_paged_append with seqs and mk_paged_prompt_attention);
+ * without, row i is sequence i (mk_paged_attention: totals are its lengths), and
+ * starts are 0, 1, .. n.  A step that does not fit (rows, free pages or table_cols)
+ * is not made: MK_ERR_KV_FULL in *status, no tokens for anyone, table, totals and
+ * used_out as before.  Apart from the pairs named, outputs overlap nothing else
+ * of the call.  Errors: MK_ERR_INVALID_ARG, MK_ERR_UNSUPPORTED (n, rows near 2^31),
+ * MK_ERR_CUDA. */
+int mk_paged_plan(const mk_plan_args *a, mk_stream stream);
 
 /* Copy cached tokens [first, first + count) of layer `layer` from the handle's
  * own cache to slots [slot, slot + count) of sequence `seq` of a paged cache of
@@ -496,6 +577,81 @@ typedef struct {
  * counts modulo 16.  Errors: MK_ERR_INVALID_ARG,
  * MK_ERR_UNSUPPORTED (group, k), MK_ERR_CUDA. */
 int mk_matvec_q4(const mk_matvec_q4_args *a, mk_stream stream);
+
+/* ---- 8-bit floating-point products with block scales ------------------------
+ * For the projections of many rows (prompts, large batches).  Both operands are
+ * MK_E4M3 codes that stand for code * scale: of a row of x each 128 elements have a
+ * scale, of w each 128 x 128 block (the last block of a row or column may be
+ * shorter). */
+typedef struct {
+  int32_t m, k;                /* rows; 0 is a no-op.  k: a multiple of 16 */
+  int32_t dtype;               /* of x: MK_F32 or MK_BF16 */
+  const void *x;               /* device [m][k]; rows on 16 bytes */
+  int64_t x_row;               /* row strides, elements */
+  void *codes;                 /* device MK_E4M3 [m][k]; rows on 16 bytes; no part of x or scales */
+  int64_t codes_row;
+  float *scales;               /* device [m][(k + 127) / 128]; no part of x */
+  int64_t scales_row;
+} mk_quantize_fp8_args;
+
+/* scale = largest |x| of the 128 / 448 as fp32 (1 for a block of zeros), code = x
+ * / scale as fp32, rounded to nearest even and saturating.  NaN stays NaN and does
+ * not count for the scale.  Errors: MK_ERR_INVALID_ARG, MK_ERR_CUDA. */
+int mk_quantize_fp8(const mk_quantize_fp8_args *a, mk_stream stream);
+
+typedef struct {
+  int32_t m, n, k;             /* y [m][n] = x [m][k] w [n][k]^T; m or n 0 is a no-op; k a multiple of 16 */
+  int32_t dtype;               /* of residual and y: MK_F32 or MK_BF16 */
+  const void *x;               /* device MK_E4M3 [m][k]; rows on 16 bytes, not overlapping */
+  int64_t x_row;               /* row strides, elements */
+  const float *x_scale;        /* device [m][(k + 127) / 128] */
+  int64_t x_scale_row;
+  const void *w;               /* device MK_E4M3 [n][k]; rows on 16 bytes, not overlapping */
+  int64_t w_row;
+  const float *w_scale;        /* device [(n + 127) / 128][(k + 127) / 128], contiguous */
+  const void *residual;        /* device [m][n] added to the products, or NULL; may be y itself (same stride) */
+  int64_t residual_row;
+  void *y;                     /* device [m][n]; no part of x, w or the scales, of the residual all or none */
+  int64_t y_row;
+  int32_t *status;             /* device, or NULL: MK_ERR_TIMEOUT if a wait inside the kernel ran out */
+} mk_matmul_fp8_args;
+
+/* y[t][j] = sum_b x_scale[t][b] w_scale[j / 128][b] sum_{k in block b} x[t][k] w[j][k]
+ * (+ residual): a block's products are summed by the tensor cores, the blocks in
+ * fp32, rounded once.  The same inputs give the same bits.  Errors:
+ * MK_ERR_INVALID_ARG, MK_ERR_UNSUPPORTED (sizes near 2^31), MK_ERR_CUDA. */
+int mk_matmul_fp8(const mk_matmul_fp8_args *a, mk_stream stream);
+
+/* ---- logits ------------------------------------------------------------------ */
+typedef struct {
+  int32_t n, vocab;            /* rows, tokens; 0 is a no-op */
+  int32_t dtype;               /* of x and out: MK_F32 or MK_BF16 */
+  const void *x;               /* device [n][vocab] logits */
+  void *out;                   /* device [n][vocab]; may be x itself (same stride), else no part of it */
+  int64_t x_row, out_row;      /* row strides, elements (any) */
+  const int32_t *tokens;       /* device [n][columns] each row's history; ids outside the vocabulary do not count */
+  int64_t tokens_row;
+  int32_t columns;
+  const int32_t *lengths;      /* device [n] tokens of the history (at most columns count), or NULL = columns;
+                                  negative = a padding row, whose logits in out are left as they were */
+  const int32_t *prompts;      /* device [n] how many of them are the prompt, or NULL = none */
+  const float *repetition, *presence, *frequency; /* device [n], or NULL = 1, 0, 0 */
+  const int32_t *bias_ids;     /* device [n][biases] tokens; ids outside the vocabulary do not count */
+  const float *bias;           /* device [n][biases] */
+  int64_t ids_row, bias_row;
+  int32_t biases;
+  const int32_t *mask;         /* device [n][(vocab + 31) / 32], bit t % 32 of word t / 32 set = allowed; or NULL */
+  int64_t mask_row;            /* 0 = the same mask for every row */
+} mk_logits_args;
+
+/* Adjust logits before a token is chosen, in this order:
+ *   in the history:                    x = x > 0 ? x / repetition : x * repetition
+ *   c > 0 times in it behind the prompt: x = x - frequency c - presence
+ *   x = x + the biases of the token (in their order), x = -inf if it is not allowed
+ * in fp32, rounded once; a token that none of them touches is copied.  A row whose
+ * mask allows nothing is -inf throughout.  Errors: MK_ERR_INVALID_ARG,
+ * MK_ERR_UNSUPPORTED (sizes near 2^31), MK_ERR_CUDA. */
+int mk_adjust_logits(const mk_logits_args *a, mk_stream stream);
 
 /* Free everything the handle owns (not the borrowed weights): the end of the
  * handle lifecycle that mk_create starts.  NULL is a no-op; always MK_OK. */

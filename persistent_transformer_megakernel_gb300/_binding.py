@@ -92,7 +92,43 @@ class mk_attention_args(C.Structure):
                 ("out", C.c_void_p), ("q_row", C.c_int64), ("q_head", C.c_int64), ("out_row", C.c_int64),
                 ("out_head", C.c_int64), ("lse", C.c_void_p), ("lengths", C.c_void_p), ("window", C.c_int32),
                 ("scale", C.c_float), ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64),
-                ("status", C.c_void_p)]
+                ("status", C.c_void_p), ("sinks", C.c_int32)]
+
+
+class mk_plan_args(C.Structure):
+    _fields_ = [("n", C.c_int32), ("rows", C.c_int32), ("page_size", C.c_int32), ("lengths", C.c_void_p), ("counts", C.c_void_p),
+                ("table", C.c_void_p), ("table_cols", C.c_int32), ("table_stride", C.c_int64), ("free", C.c_void_p),
+                ("free_count", C.c_int32), ("used", C.c_void_p), ("seqs", C.c_void_p), ("slots", C.c_void_p),
+                ("starts", C.c_void_p), ("totals", C.c_void_p), ("used_out", C.c_void_p), ("status", C.c_void_p)]
+
+
+class mk_prompt_args(C.Structure):
+    _fields_ = [("n", C.c_int32), ("rows", C.c_int32), ("dtype", C.c_int32), ("n_q_heads", C.c_int32), ("q", C.c_void_p),
+                ("out", C.c_void_p), ("q_row", C.c_int64), ("q_head", C.c_int64), ("out_row", C.c_int64),
+                ("out_head", C.c_int64), ("lse", C.c_void_p), ("starts", C.c_void_p), ("lengths", C.c_void_p),
+                ("window", C.c_int32), ("sinks", C.c_int32), ("scale", C.c_float), ("workspace", C.c_void_p),
+                ("workspace_bytes", C.c_int64), ("status", C.c_void_p)]
+
+
+class mk_quantize_fp8_args(C.Structure):
+    _fields_ = [("m", C.c_int32), ("k", C.c_int32), ("dtype", C.c_int32), ("x", C.c_void_p), ("x_row", C.c_int64),
+                ("codes", C.c_void_p), ("codes_row", C.c_int64), ("scales", C.c_void_p), ("scales_row", C.c_int64)]
+
+
+class mk_matmul_fp8_args(C.Structure):
+    _fields_ = [("m", C.c_int32), ("n", C.c_int32), ("k", C.c_int32), ("dtype", C.c_int32), ("x", C.c_void_p),
+                ("x_row", C.c_int64), ("x_scale", C.c_void_p), ("x_scale_row", C.c_int64), ("w", C.c_void_p),
+                ("w_row", C.c_int64), ("w_scale", C.c_void_p), ("residual", C.c_void_p), ("residual_row", C.c_int64),
+                ("y", C.c_void_p), ("y_row", C.c_int64), ("status", C.c_void_p)]
+
+
+class mk_logits_args(C.Structure):
+    _fields_ = [("n", C.c_int32), ("vocab", C.c_int32), ("dtype", C.c_int32), ("x", C.c_void_p), ("out", C.c_void_p),
+                ("x_row", C.c_int64), ("out_row", C.c_int64), ("tokens", C.c_void_p), ("tokens_row", C.c_int64),
+                ("columns", C.c_int32), ("lengths", C.c_void_p), ("prompts", C.c_void_p), ("repetition", C.c_void_p),
+                ("presence", C.c_void_p), ("frequency", C.c_void_p), ("bias_ids", C.c_void_p), ("bias", C.c_void_p),
+                ("ids_row", C.c_int64), ("bias_row", C.c_int64), ("biases", C.c_int32), ("mask", C.c_void_p),
+                ("mask_row", C.c_int64)]
 
 
 class mk_matvec_q4_args(C.Structure):
@@ -108,7 +144,9 @@ WORKSPACE_FN = C.CFUNCTYPE(C.c_void_p, C.c_void_p, C.c_int64)    # (context, byt
 EXPORTS = ("mk_create", "mk_reset_kv", "mk_decode", "mk_prefill", "mk_decode_start", "mk_decode_wait",
            "mk_mailbox_read", "mk_decode_host", "mk_get_info", "mk_embed_sum",
            "mk_embed_sum_noalloc", "mk_destroy", "mk_error_string", "mk_plan_for", "mk_paged_append",
-           "mk_paged_attention", "mk_paged_attention_ask", "mk_paged_attention_workspace", "mk_export_kv", "mk_matvec_q4")
+           "mk_paged_attention", "mk_paged_attention_ask", "mk_paged_attention_workspace", "mk_export_kv", "mk_matvec_q4",
+           "mk_paged_plan", "mk_paged_prompt_attention", "mk_paged_prompt_attention_ask",
+           "mk_paged_prompt_attention_workspace", "mk_quantize_fp8", "mk_matmul_fp8", "mk_adjust_logits")
 
 _lib = None
 
@@ -145,6 +183,13 @@ def load_library(path: Optional[str] = None):
     lib.mk_paged_attention_workspace.argtypes = [i32, i32, i32]
     lib.mk_export_kv.argtypes = [vp, i32, i32, i32, C.POINTER(mk_paged_kv), i32, i32, vp]
     lib.mk_matvec_q4.argtypes = [C.POINTER(mk_matvec_q4_args), vp]
+    lib.mk_paged_plan.argtypes = [C.POINTER(mk_plan_args), vp]
+    lib.mk_paged_prompt_attention.argtypes = [C.POINTER(mk_paged_kv), C.POINTER(mk_prompt_args), vp]
+    lib.mk_paged_prompt_attention_ask.argtypes = [C.POINTER(mk_paged_kv), C.POINTER(mk_prompt_args), WORKSPACE_FN, vp, vp]
+    lib.mk_paged_prompt_attention_workspace.argtypes = [i32]
+    lib.mk_quantize_fp8.argtypes = [C.POINTER(mk_quantize_fp8_args), vp]
+    lib.mk_matmul_fp8.argtypes = [C.POINTER(mk_matmul_fp8_args), vp]
+    lib.mk_adjust_logits.argtypes = [C.POINTER(mk_logits_args), vp]
     lib.mk_destroy.argtypes = [vp]
     lib.mk_error_string.argtypes = [C.c_int]
     lib.mk_error_string.restype = C.c_char_p
@@ -152,6 +197,7 @@ def load_library(path: Optional[str] = None):
         if name != "mk_error_string":
             getattr(lib, name).restype = C.c_int
     lib.mk_paged_attention_workspace.restype = i64
+    lib.mk_paged_prompt_attention_workspace.restype = i64
     if path is None:
         _lib = lib
     return lib

@@ -562,6 +562,7 @@ struct AttnParams {
   float *parts;        // [grid][2][gr][D + 4]: a row's middle or end (0) and its beginning (1)
   mkw::Divisor page_size;
   int n, hq, hkv, group, n_pages, capacity, window;   // capacity: slots of a table row
+  int sinks;                 // first tokens that a window leaves visible
   mkw::Divisor chunks;       // of 16 query heads
   mkw::Divisor blocks, vh;   // head blocks of 16 query heads a kv head, virtual heads hkv * blocks
   int gr;              // query heads of a block: min(group, 16)
@@ -603,17 +604,21 @@ struct Pair<__nv_bfloat16> {
   static __device__ __forceinline__ float2 values(type w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 };
 
-// tiles of a row: those that hold any of its slots [lo, hi), and their cost, the row's start included
+// tiles of a row: those that hold any of its slots [lo, hi), before them, where a window leaves first tokens visible,
+// `head` tiles of those, and the cost of all, the row's start included
 struct Span {
-  int lo, hi, first, count, cost;
+  int lo, hi, head, skip, count, cost;
+  __device__ __forceinline__ int number(int j) const { return j < head ? j : j + skip; }   // of the row's jth tile
 };
 template <int POS>
 __device__ __forceinline__ Span span_of(const AttnParams &p, int len) {
   Span s;
   s.hi = len > 0 && len <= p.capacity ? len : 0;
   s.lo = p.window > 0 && s.hi > p.window ? s.hi - p.window : 0;
-  s.first = s.lo / POS;
-  s.count = s.hi > 0 ? (s.hi + POS - 1) / POS - s.first : 0;
+  const int first = s.lo / POS;
+  s.head = min((p.sinks + POS - 1) / POS, first);
+  s.skip = first - s.head;
+  s.count = s.hi > 0 ? (s.hi + POS - 1) / POS - s.skip : 0;
   s.cost = s.count ? s.count + p.row_cost : 0;
   return s;
 }
@@ -774,7 +779,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
 
   // ---- the warp's range: where it starts, and how much it covers -------------------
   int row = 0, vh = 0, tile = 0, left = 0;                   // left: units from the tile the producer stands at to the range's end
-  Span sp{0, 0, 0, 0, 0};
+  Span sp{0, 0, 0, 0, 0, 0};
   int per = 0, units = 0, ctas = 0;
   if (p.way == kByCluster) {
     mkw::cluster_arrive();                                   // (to be waited for before the others' memory is written)
@@ -868,17 +873,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
   // the producer's place besides row, vh, tile: its kv head and block, this lane's slot in its page and that page
   int kvh = p.blocks.quotient(vh), blk = vh - kvh * static_cast<int>(p.blocks.value), slot = 0, page = -1;
   auto look_up = [&]() {
-    const int pos = (sp.first + tile) * POS + lane, col = p.page_size.quotient(pos);
+    const int pos = sp.number(tile) * POS + lane, col = p.page_size.quotient(pos);
     slot = pos - col * static_cast<int>(p.page_size.value);
     page = -1;
-    if (lane < POS && pos >= sp.lo && pos < sp.hi) page = p.table[row * p.table_stride + col];
+    if (lane < POS && (pos >= sp.lo || pos < p.sinks) && pos < sp.hi) page = p.table[row * p.table_stride + col];
   };
   if (left > 0) look_up();
   int in_stage = 0;                                          // the producer's stage
   const int r0 = lane / TL::CPR, place = lane % TL::CPR;     // this lane's first slot of a tile and its place in every row
   auto produce = [&]() {
-    const int pos0 = (sp.first + tile) * POS, pos = pos0 + lane;
-    const bool want = lane < POS && pos >= sp.lo && pos < sp.hi;
+    const int pos0 = sp.number(tile) * POS, pos = pos0 + lane;
+    const bool want = lane < POS && (pos >= sp.lo || pos < p.sinks) && pos < sp.hi;
     const bool fine = static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages);
     const unsigned have = __ballot_sync(0xffffffffu, want && fine);
     const bool bad = __any_sync(0xffffffffu, want && !fine);
@@ -1077,7 +1082,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
         }
       }
     }
-    const bool edge = ti.pos < ti.lo || ti.pos + POS > ti.hi;
+    const bool edge = (ti.pos < ti.lo && ti.pos + POS > p.sinks) || ti.pos + POS > ti.hi;
     float alpha[HB][2];
     uint32_t pf[TP][PN][HB][2];
 #pragma unroll
@@ -1090,7 +1095,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
           float s = (sc[nb][hb][c] + sl[nb][hb][c]) * mult[hb][c & 1];
           if (edge) {
             const int pos = ti.pos + 16 * nb + g + (c >> 1) * 8;
-            if (pos < ti.lo || pos >= ti.hi) s = -INFINITY;
+            if ((pos < ti.lo && pos >= p.sinks) || pos >= ti.hi) s = -INFINITY;
           }
           sc[nb][hb][c] = s;
           x[c & 1] = fmaxf(x[c & 1], s);
@@ -1342,6 +1347,11 @@ struct Workspace {
   int64_t bytes;
 };
 
+// slots that a row reads at most
+int seen_at_most(const AttnParams &p) {
+  return p.window > 0 ? static_cast<int>(std::min<int64_t>(static_cast<int64_t>(p.window) + p.sinks, p.capacity)) : p.capacity;
+}
+
 template <class T, bool FP8, int D, int HB>
 int launch_heads(AttnParams &p, const Workspace &ws, int grid, int dev, cudaStream_t s) {
   using TL = Tile<D, FP8>;
@@ -1349,7 +1359,7 @@ int launch_heads(AttnParams &p, const Workspace &ws, int grid, int dev, cudaStre
   const auto fn = &attend_kernel<T, FP8, D, HB>;
   mkw::Ready &r = ready[dev];
   if (!r.get(reinterpret_cast<const void *>(fn), kAttnThreads, kMaxSmem)) return MK_ERR_CUDA;
-  const int64_t tiles = (p.window > 0 ? std::min(p.window, p.capacity) : p.capacity) / TL::POS + 2;   // of a row at most
+  const int64_t tiles = seen_at_most(p) / TL::POS + (p.sinks > 0 ? 3 : 2);   // of a row at most
   p.way = tiles <= kShortTiles ? kWhole : kJoined;
   p.cluster = 1;
   if (p.n == 1) {
@@ -1489,7 +1499,7 @@ int attention(const mk_paged_kv *kv, const mk_attention_args *a, mk_stream strea
   int rc = check_cache(kv);
   if (rc != MK_OK) return rc;
   if (!a || a->n < 0 || a->n > kv->table_rows || (a->dtype != MK_F32 && a->dtype != MK_BF16) || a->window < 0 ||
-      !std::isfinite(a->scale))
+      a->sinks < 0 || !std::isfinite(a->scale))
     return MK_ERR_INVALID_ARG;
   rc = check_heads(a->n_q_heads, kv->n_kv_heads, kv->head_dim);
   if (rc != MK_OK) return rc;
@@ -1524,6 +1534,7 @@ int attention(const mk_paged_kv *kv, const mk_attention_args *a, mk_stream strea
   p.n_pages = kv->n_pages;
   p.page_size.set(kv->page_size);
   p.window = a->window;
+  p.sinks = a->window > 0 ? std::min(a->sinks, p.capacity) : 0;   // (without a window all tokens are visible)
   p.chunks.set((p.hq + 15) / 16);
   p.blocks.set((p.group + 15) / 16);
   p.vh.set(p.hkv * ((p.group + 15) / 16));
@@ -1531,7 +1542,7 @@ int attention(const mk_paged_kv *kv, const mk_attention_args *a, mk_stream strea
   p.row_cost = row_cost(p.gr);
   p.scale = a->scale;
   int spare = 0;                                             // 2^spare: as many tokens as a row may have, or more
-  for (const int tokens = p.window > 0 ? std::min(p.window, p.capacity) : p.capacity; (int64_t{1} << spare) < tokens;) ++spare;
+  for (const int tokens = seen_at_most(p); (int64_t{1} << spare) < tokens;) ++spare;
   if (kv->dtype != MK_BF16) spare = 0;                       // (e4m3 values are far from fp32's largest)
   p.shrink = std::ldexp(1.f, -spare), p.grow = std::ldexp(1.f, spare);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -1,16 +1,19 @@
-"""Operators of a decode step of several sequences: a paged KV cache and 4-bit weights.
+"""Operators of a step of several sequences: a paged KV cache, 4-bit and 8-bit weights.
 
-``paged_append`` -> ``paged_attention`` over a page table, ``matvec_q4`` for
-the projections, each one call of the C ABI (``include/mk.h``).  They enqueue on
-the stream and return; what only the device can see (a page id outside the
+``paged_plan`` gives a step's tokens their rows, slots and pages;
+``paged_append`` -> ``paged_attention`` (single tokens) or
+``paged_prompt_attention`` (prompts) over a page table; ``matvec_q4`` (few
+rows) or ``quantize_fp8`` -> ``matmul_fp8`` (many) for the projections;
+``adjust_logits`` before a token is chosen.  Each is one call of the C ABI
+(``include/mk.h``).  They enqueue on the stream and return; what only the device can see (a page id outside the
 cache, a position outside the rotary table) goes to an optional ``status`` word
 that ``check_status`` turns into an ``MKError``.  They have no gradients:
 a tensor that requires them is refused unless gradients are off
 (``torch.no_grad``).
 
-The three are functions of the module ``_mktorch`` (``csrc/mk_torch.cpp``), which
-checks the tensors of a call against what the kernels read and write (a wrong
-one is a ``ValueError``).  It is loaded when the first of them is asked for, and
+They are functions of the module ``_mktorch`` (``csrc/mk_torch.cpp``,
+``csrc/mk_torch_prompts.h``), which checks the tensors of a call against what
+the kernels read and write (a wrong one is a ``ValueError``).  It is loaded when the first of them is asked for, and
 like the library it must have been built.
 """
 from __future__ import annotations
@@ -23,7 +26,8 @@ import torch
 
 from . import _binding as B
 
-NATIVE = ("paged_append", "paged_attention", "matvec_q4")
+NATIVE = ("paged_append", "paged_attention", "matvec_q4", "paged_plan", "paged_prompt_attention", "quantize_fp8", "matmul_fp8",
+          "adjust_logits")
 
 
 def native():
@@ -80,6 +84,23 @@ def quantize_q4(w: torch.Tensor, group: int = 64, zeros: bool = False):
     if zeros:
         return codes, scale, zero[..., 0].to(torch.uint8)
     return codes, scale
+
+
+def quantize_fp8_weight(w: torch.Tensor):
+    """8-bit codes of ``w`` [n][k] (k a multiple of 16), once per weight: ``(codes
+    float8_e4m3fn [n][k], scales fp32 [n / 128][k / 128], rounded up)``; a block of
+    128 x 128 has the scale largest / 448."""
+    w = w.detach()
+    n, k = w.shape
+    if k % 16 or k == 0:
+        raise ValueError("k (%d) must be a multiple of 16" % k)
+    nb, kb = -(-n // 128), -(-k // 128)
+    x = torch.nn.functional.pad(w.float(), (0, kb * 128 - k, 0, nb * 128 - n)).view(nb, 128, kb, 128)
+    largest = x.abs().amax((1, 3))
+    scales = largest / torch.full_like(largest, 448.0)
+    scales = torch.where(scales > 0, scales, torch.ones_like(scales))
+    codes = (x / scales[:, None, :, None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(nb * 128, kb * 128)[:n, :k]
+    return codes.contiguous(), scales
 
 
 def check_status(status: torch.Tensor, stream=None) -> None:
