@@ -596,7 +596,8 @@ typedef struct {
 
 /* scale = largest |x| of the 128 / 448 as fp32 (1 for a block of zeros), code = x
  * / scale as fp32, rounded to nearest even and saturating.  NaN stays NaN and does
- * not count for the scale.  Errors: MK_ERR_INVALID_ARG, MK_ERR_CUDA. */
+ * not count for the scale.  Errors: MK_ERR_INVALID_ARG, MK_ERR_UNSUPPORTED (2^31
+ * blocks and more), MK_ERR_CUDA. */
 int mk_quantize_fp8(const mk_quantize_fp8_args *a, mk_stream stream);
 
 typedef struct {

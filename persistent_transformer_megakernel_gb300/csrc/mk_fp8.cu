@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/mk.h"
 #include "mk_launch_after.h"
@@ -23,9 +24,11 @@ constexpr int kBlock = 128;
 // ---------------------------------------------------------------------------
 // Quantisation of rows: for each 128 of a row scale = largest / 448, code = x / scale rounded to e4m3.
 //
-// Bound by bytes: x read once, a byte an element and 4 a block written.  16 lanes have a block, 8 elements each; the
-// quotient is fp32's (a bf16 element over its scale is often half way between two codes: a reciprocal's last place would
-// decide which).
+// Bound by bytes: x read once, a byte an element and 4 a block written.  16 lanes have a block, 8 elements each, or four
+// blocks at a time, all asked for before the first is worked on.  The quotient is fp32's (a bf16 element over its scale is
+// often half way between two codes, so that a last place decides): the product with the reciprocal, corrected by its
+// remainder, which is the correctly rounded quotient if the reciprocal is (P. Markstein, Computation of elementary functions
+// on the IBM RISC System/6000 processor, 1990), away from the ends of the exponents' range.
 // ---------------------------------------------------------------------------
 
 struct QuantParams {
@@ -33,70 +36,96 @@ struct QuantParams {
   uint8_t *codes;
   float *scales;
   int64_t x_row, codes_row, scales_row;
-  int m, k, blocks;            // blocks of a row
-  int64_t items;               // m * blocks
+  int k;
+  mkw::Divisor blocks;         // of a row
+  int items;                   // blocks in all
 };
 
 constexpr int kQuantThreads = 256;
 
-__device__ __forceinline__ void load8(const float *p, bool hi, float (&x)[8]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = hi ? __ldcs(reinterpret_cast<const float4 *>(p) + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+__device__ __forceinline__ void numbers8(const float4 (&w)[2], float (&x)[8]) {
+  x[0] = w[0].x, x[1] = w[0].y, x[2] = w[0].z, x[3] = w[0].w, x[4] = w[1].x, x[5] = w[1].y, x[6] = w[1].z, x[7] = w[1].w;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, bool, float (&x)[8]) {
-  const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p));
+__device__ __forceinline__ void numbers8(const uint4 (&w)[1], float (&x)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float((&w.x)[i] << 16);
-    x[2 * i + 1] = __uint_as_float((&w.x)[i] & 0xffff0000u);
+    x[2 * i] = __uint_as_float((&w[0].x)[i] << 16);
+    x[2 * i + 1] = __uint_as_float((&w[0].x)[i] & 0xffff0000u);
   }
 }
 
-template <class T>
+// U: blocks that 16 lanes have at a time
+template <class T, int U>
 __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_constant__ QuantParams p) {
+  using Word = std::conditional_t<sizeof(T) == 4, float4, uint4>;
+  constexpr int WORDS = sizeof(T) / 2;
   mkw::follow_previous_kernel();
-  const int lane = threadIdx.x & 15;
-  const int64_t all = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 16);
-  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 16) + (threadIdx.x >> 4); i0 - (threadIdx.x >> 4) < p.items; i0 += all) {
-    const bool live = i0 < p.items;                        // (a warp's lanes stay together)
-    const int64_t i = live ? i0 : 0;
-    const int row = static_cast<int>(i / p.blocks), b = static_cast<int>(i - static_cast<int64_t>(row) * p.blocks);
-    const int at = b * kBlock + lane * 8;                  // k is a multiple of 16: 8 elements are there or not
-    float x[8] = {};
-    const bool there = live && at < p.k;
-    if (there) load8(static_cast<const T *>(p.x) + row * p.x_row + at, true, x);
-    float top = 0.f;
+  const int lane = threadIdx.x & 15, first = (static_cast<int>(blockIdx.x) * (kQuantThreads / 16) + (threadIdx.x >> 4)) * U;
+  int row[U], b[U];
+  bool there[U];
+  Word w[U][WORDS];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    row[i] = p.blocks.quotient(first + i);
+    b[i] = first + i - row[i] * static_cast<int>(p.blocks.value);
+    there[i] = first + i < p.items && b[i] * kBlock + lane * 8 < p.k;      // (k is a multiple of 16: 8 elements are there or not)
+#pragma unroll
+    for (int j = 0; j < WORDS; ++j) {
+      w[i][j] = Word{};
+      if (there[i]) w[i][j] = __ldcs(reinterpret_cast<const Word *>(static_cast<const T *>(p.x) + row[i] * p.x_row + b[i] * kBlock + lane * 8) + j);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    float x[8], top = 0.f;
+    numbers8(w[i], x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float scale = __fdiv_rn(top, 448.f);
     if (!(scale > 0.f)) scale = 1.f;
-    uint32_t w[2];
+    float y[8];
+    if (scale > 0x1p-60f && scale < 0x1p60f) {
+      const float r = __frcp_rn(scale);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[4 * e], scale), __fdiv_rn(x[4 * e + 1], scale)), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[4 * e + 2], scale), __fdiv_rn(x[4 * e + 3], scale)), __NV_SATFINITE, __NV_E4M3);
-      w[e] = a | c << 16;
+      for (int e = 0; e < 8; ++e) {
+        const float q = x[e] * r;
+        y[e] = fmaf(fmaf(-q, scale, x[e]), r, q);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = __fdiv_rn(x[e], scale);
     }
-    if (there) *reinterpret_cast<uint2 *>(p.codes + row * p.codes_row + at) = make_uint2(w[0], w[1]);
-    if (live && lane == 0) p.scales[row * p.scales_row + b] = scale;
+    uint32_t c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * e], y[2 * e + 1]), __NV_SATFINITE, __NV_E4M3);
+    if (there[i]) *reinterpret_cast<uint2 *>(p.codes + row[i] * p.codes_row + b[i] * kBlock + lane * 8) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    if (first + i < p.items && lane == 0) p.scales[row[i] * p.scales_row + b[i]] = scale;
   }
 }
 
 // ---------------------------------------------------------------------------
 // y[t][j] = sum_b xs[t][b] ws[j / 128][b] sum_{k in b} x[t][k] w[j][k]  (+ residual)
 //
-// A CTA has 128 rows of w (one row of weight scales) and BN rows of x.  The inner sums of a block of 128 are four tensor
-// instructions into one of two accumulators in tensor memory; eight warps take it out, multiply each column by its
-// scale xs ws and add it to fp32 sums in registers while the next block is multiplied into the other.
-// Roles: warp 0 asks for w and x by TMA, warp 1 multiplies, warps 2-9 add up, warps 10-11 bring the scales.
-// Few rows (m): K is shared by the CTAs of a cluster, whose sums are added in order through their shared memory.
+// A CTA has 128 rows of x and BN rows of w.  The inner sums of a block of 128 are four tensor instructions into one of the
+// accumulators in tensor memory (a row of x a lane, a row of w a column); eight warps take it out, multiply it by xs ws --
+// one number for all of a thread's columns -- and add it to fp32 sums in registers while the next block is multiplied into
+// others.  Warp 0 asks for x and w by TMA, warps 1 and 2 multiply, warp 3 brings the scales, warps 4-11 add up.
+// Bound by what surrounds the products (8192 x 12288 x 2048: 177 us, 2330 TFLOP/s): a block's four instructions take 256
+// clocks, taking its sums out of tensor memory about as many, and every hand-over between warps some 200 more.  So two
+// blocks are handed over at a time, and two warps multiply in turn, one waiting while the other's instructions run (one
+// warp: 186 us).  Tiles of 256 columns hold fewer accumulators and spill (230 us and more).
+// Pairs of CTAs that ask for shared tiles once (multicast) take 178 us for the same: not kept.
+// splits > 1 (few tiles): K is shared by the CTAs of a cluster, whose sums are added in order through their shared memory.
 // ---------------------------------------------------------------------------
 
-constexpr int kAddWarps = 8, kScaleWarps = 2, kWarps = 2 + kAddWarps + kScaleWarps, kThreads = 32 * kWarps;
-constexpr int kScaleSlots = 8;
-constexpr uint32_t kWTile = 128 * 128;
+constexpr int kRows = 128;     // of x (the MMA's M)
+constexpr int kColumns = 128;  // rows of w (its N)
+constexpr int kHelpers = 4, kAddWarps = 8, kWarps = kHelpers + kAddWarps, kThreads = 32 * kWarps;
+constexpr int kMmaWarps = 2;   // each a block in turn: the waits and commits of one pass while the other's products run
+constexpr int kGroup = 4, kGroups = 4;   // scales travel in groups of four blocks, four of them at most on their way
+constexpr uint32_t kXTile = kRows * 128;
 constexpr long long kWaitNs = 2000000000LL;
 
 struct MatmulParams {
@@ -105,49 +134,112 @@ struct MatmulParams {
   void *y;
   int32_t *status;
   int64_t x_scale_row, residual_row, y_row;
+  int64_t residual_map_row, y_map_row;   // as a tensor map has them
   int m, n, kb;                // kb: blocks of K
-  int tiles_n, tiles;          // tiles along n, in all
+  int tiles_m, tiles;          // tiles along m, in all
   int splits;                  // CTAs of a cluster that share a tile's K
+  int x_rows;                  // rows that a copy of x brings: no more than there are (what else is in a tile is no row's)
+  int tma;                     // rows of y and of the residual are on 16 bytes
+  int wide_scales;             // rows of x's scales on 16 bytes
 };
 
+// numbers of a row of sums that a cluster's CTAs leave each other (16 bytes of eight rows are in different banks)
 template <int BN>
+constexpr int kSplitRow = BN + 4;
+
+template <int BN, class T>
 struct Cfg {
-  static constexpr uint32_t XTILE = BN * 128, STAGE = kWTile + XTILE;
-  static constexpr int STAGES = BN >= 256 ? 4 : BN >= 128 ? 6 : 8;
-  static constexpr uint32_t SCALES = STAGES * STAGE;                       // behind the stages: [slot][BN]
-  static constexpr uint32_t CONTROL = SCALES + kScaleSlots * BN * 4;
-  static constexpr int SMEM = static_cast<int>(1024 + CONTROL + 512);
-  static constexpr int TCOLS = BN <= 16 ? 32 : 2 * BN;
+  static constexpr uint32_t STAGE = kXTile + BN * 128;
+  static constexpr int TCOLS = 512, SUMS = TCOLS / (2 * BN);               // pairs of accumulators
   static constexpr int COLS = BN / 2;                                      // of an adding warp
-  static_assert(SMEM <= 232448, "shared memory");
+  // results leave (and the residual comes) in boxes of 32 rows and 128 bytes, or what an adding warp has of a row
+  static constexpr int ROWB = COLS * sizeof(T) < 128 ? COLS * static_cast<int>(sizeof(T)) : 128, PIECE = ROWB / static_cast<int>(sizeof(T));
+  static constexpr int STAGES = BN >= 256 ? 3 : ROWB == 64 ? 5 : 4;
+  static constexpr uint32_t RESULTS = STAGES * STAGE;                      // behind the stages: a box an adding warp
+  static constexpr uint32_t SCALES = RESULTS + kAddWarps * 32 * ROWB;      // [group][row][4] of x, [group][2][4] of w
+  static constexpr uint32_t CONTROL = SCALES + kGroups * (kRows + 2) * 16;
+  static constexpr int SMEM = static_cast<int>(1024 + CONTROL + 512);
+  static_assert(SMEM <= 232448 && kRows * kSplitRow<BN> * 4 <= RESULTS, "shared memory");
 };
 
 __device__ __forceinline__ void fail(int32_t *status) {
   if (status) atomicCAS(status, 0, MK_ERR_TIMEOUT);
 }
-__device__ __forceinline__ float load_remote(uint32_t at) {
-  float x;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+__device__ __forceinline__ float4 load_remote4(uint32_t at) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at) : "memory");
   return x;
 }
+// places 0 .. N - 1 in turn, and the parity of the round
+template <int N>
+struct Turn {
+  int i = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) i = 0, parity ^= 1u;
+  }
+};
+// two fp32 sums and one factor: c += a f
+__device__ __forceinline__ void add_scaled(unsigned long long &c, uint32_t a0, uint32_t a1, unsigned long long f) {
+  unsigned long long a;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "r"(a0), "r"(a1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(f));
+}
+
+// 16 bytes of a row of results: N numbers
+template <class T>
+struct Out;
+template <>
+struct Out<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void add(const uint4 &r, float *y) {
+    y[0] += __uint_as_float(r.x), y[1] += __uint_as_float(r.y), y[2] += __uint_as_float(r.z), y[3] += __uint_as_float(r.w);
+  }
+  static __device__ __forceinline__ uint4 bits(const float *y) {
+    return make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
+  }
+};
+template <>
+struct Out<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void add(const uint4 &r, float *y) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[2 * i] += __uint_as_float((&r.x)[i] << 16);
+      y[2 * i + 1] += __uint_as_float((&r.x)[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 bits(const float *y) {
+    uint4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+      (&w.x)[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return w;
+  }
+};
 
 template <int BN, class T>
 __global__ void __launch_bounds__(kThreads, 1)
-    matmul_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, const __grid_constant__ MatmulParams p) {
-  using C = Cfg<BN>;
-  constexpr uint32_t kId = idesc_f32(128, BN);
+    matmul_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap ty,
+                  const __grid_constant__ CUtensorMap tr, const __grid_constant__ MatmulParams p) {
+  using C = Cfg<BN, T>;
+  constexpr int N = Out<T>::N, PIECE = C::PIECE, ROWB = C::ROWB;   // numbers in 16 bytes and in a row of a box, its bytes
+  constexpr uint32_t kId = idesc_f32(kRows, BN);
   extern __shared__ unsigned char smraw[];
   mkw::follow_previous_kernel();
   unsigned char *sm = smraw + ((1024u - (smem_addr(smraw) & 1023u)) & 1023u);
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::CONTROL), *empty = full + C::STAGES, *tfull = empty + C::STAGES, *tempty = tfull + 2,
-           *sfull = tempty + 2, *sempty = sfull + kScaleSlots;
-  uint32_t *tslot = reinterpret_cast<uint32_t *>(sempty + kScaleSlots);
-  float *scales = reinterpret_cast<float *>(sm + C::SCALES);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::CONTROL), *empty = full + C::STAGES, *tfull = empty + C::STAGES, *tempty = tfull + C::SUMS,
+           *sfull = tempty + C::SUMS, *sempty = sfull + kGroups, *rfull = sempty + kGroups;
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(rfull + kAddWarps);
+  float4 *scales = reinterpret_cast<float4 *>(sm + C::SCALES);             // a group: kRows of x, 2 of w
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], kAddWarps);
-    for (int i = 0; i < kScaleSlots; ++i) mbar_init(&sfull[i], kScaleWarps), mbar_init(&sempty[i], kAddWarps);
+    for (int i = 0; i < C::SUMS; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], kAddWarps);
+    for (int i = 0; i < kGroups; ++i) mbar_init(&sfull[i], 1), mbar_init(&sempty[i], kAddWarps);
+    for (int i = 0; i < kAddWarps; ++i) mbar_init(&rfull[i], 1);
     fence_mbar_init();
     prefetch_tmap(&tw);
     prefetch_tmap(&tx);
@@ -156,166 +248,281 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
 
-  const int rank = static_cast<int>(blockIdx.x) % p.splits, ctas = static_cast<int>(gridDim.x) / p.splits;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(p.kb) * rank / p.splits), kb1 = static_cast<int>(static_cast<int64_t>(p.kb) * (rank + 1) / p.splits);
-  const int first = static_cast<int>(blockIdx.x) / p.splits;
+  const int split = static_cast<int>(blockIdx.x) % p.splits, step = static_cast<int>(gridDim.x) / p.splits, first = static_cast<int>(blockIdx.x) / p.splits;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.kb) * split / p.splits), kb1 = static_cast<int>(static_cast<int64_t>(p.kb) * (split + 1) / p.splits);
+  auto row_of = [&](int tile) { return tile % p.tiles_m * kRows; };
+  auto column_of = [&](int tile) { return tile / p.tiles_m * BN; };
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < kHelpers) {
+    if (warp == 0) {
+      Turn<C::STAGES> at;
       int it = 0;
       bool ok = true;
-      for (int tile = first; tile < p.tiles && ok; tile += ctas) {
-        const int j0 = tile % p.tiles_n * 128, t0 = tile / p.tiles_n * BN;
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % C::STAGES;
-          if (it >= C::STAGES && !mbar_wait(&empty[s], (it / C::STAGES - 1) & 1, kWaitNs)) {
-            fail(p.status);
+      for (int tile = first; tile < p.tiles && ok; tile += step) {
+        const int t0 = row_of(tile), j0 = column_of(tile);
+        for (int kb = kb0; kb < kb1; ++kb, ++it, at.next()) {
+          const int s = at.i;
+          if (it >= C::STAGES && !__all_sync(0xffffffffu, mbar_wait(&empty[s], at.parity ^ 1u, kWaitNs))) {
+            if (lane == 0) fail(p.status);
             ok = false;
             break;
           }
-          mbar_expect_tx(&full[s], C::STAGE);
-          tma_load_2d(sm + s * C::STAGE, &tw, kb * kBlock, j0, &full[s]);
-          tma_load_2d(sm + s * C::STAGE + kWTile, &tx, kb * kBlock, t0, &full[s]);
+          unsigned char *to = sm + s * C::STAGE;
+          if (elect_one()) {
+            mbar_expect_tx(&full[s], p.x_rows * 128 + BN * 128);
+            tma_load_2d(to, &tx, kb * kBlock, t0, &full[s]);
+            tma_load_2d(to + kXTile, &tw, kb * kBlock, j0, &full[s]);
+          }
+          __syncwarp();
         }
       }
       // no copy may be on its way when the CTA ends
       for (int i = it - C::STAGES < 0 ? 0 : it - C::STAGES; i < it; ++i) mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1, kWaitNs);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      int it = 0;
+    } else if (warp <= kMmaWarps) {
+      // descriptors: the low words move with the stage, the high ones are constants
+      const uint32_t base = smem_addr(sm);
+      const uint32_t lo = static_cast<uint32_t>(desc_sw128(base)), hi = static_cast<uint32_t>(desc_sw128(base) >> 32);
+      Turn<C::STAGES> at;
+      Turn<C::SUMS> sums;
+      int pair = 0;
       bool ok = true;
-      for (int tile = first; tile < p.tiles && ok; tile += ctas)
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % C::STAGES, u = it & 1;
-          if (!mbar_wait(&full[s], (it / C::STAGES) & 1, kWaitNs) || (it >= 2 && !mbar_wait(&tempty[u], (it / 2 - 1) & 1, kWaitNs))) {
-            fail(p.status);
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!__all_sync(0xffffffffu, mbar_test(bar, parity)) && !__all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs))) {
+          if (lane == 0) fail(p.status);
+          ok = false;
+        }
+        return ok;
+      };
+      for (int tile = first; tile < p.tiles && ok; tile += step)
+        for (int kb = kb0; kb < kb1 && ok; kb += 2, ++pair, sums.next()) {
+          const bool two = kb + 1 < kb1;
+          if (pair % kMmaWarps != warp - 1) {
+            at.next();
+            if (two) at.next();
+            continue;
+          }
+          // (tempty's phase before its first is over as it begins)
+          if (!wait(&tempty[sums.i], sums.parity ^ 1u)) break;
+          for (int i = 0; i < 1 + two; ++i, at.next()) {
+            if (!wait(&full[at.i], at.parity)) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t x = lo + at.i * (C::STAGE >> 4), w = x + (kXTile >> 4), d = tmem + (sums.i * 2 + i) * BN;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_e4m3(d, desc_of(x + 2 * k, hi), desc_of(w + 2 * k, hi), kId, k != 0);
+              mma_commit(&empty[at.i]);
+              if (i == two) mma_commit(&tfull[sums.i]);
+            }
+            __syncwarp();
+          }
+        }
+      // every product is finished before tensor memory goes
+      for (int i = pair - C::SUMS < 0 ? 0 : pair - C::SUMS; i < pair && ok; ++i) mbar_wait(&tfull[i % C::SUMS], (i / C::SUMS) & 1, kWaitNs);
+    } else {
+      // scales: a lane has four rows of x; copies of two groups are on their way while a third is told of
+      constexpr int kAhead = 2;
+      Turn<kGroups> at, ready;
+      int g = 0, told = 0;
+      bool ok = true;
+      auto tell = [&](int upto) {
+        __syncwarp();
+        for (; told < upto; ++told, ready.next())
+          if (lane == 0) mbar_arrive(&sfull[ready.i]);
+      };
+      for (int tile = first; tile < p.tiles && ok; tile += step) {
+        const int t0 = row_of(tile) + lane, jb = column_of(tile) / kBlock;
+        for (int kb = kb0; kb < kb1; kb += kGroup, ++g, at.next()) {
+          if (g >= kGroups && !__all_sync(0xffffffffu, mbar_wait(&sempty[at.i], at.parity ^ 1u, kWaitNs))) {
+            if (lane == 0) fail(p.status);
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t a = smem_addr(sm + s * C::STAGE);
+          const uint32_t to = smem_addr(scales + at.i * (kRows + 2));
+          auto copy = [&](int place, const float *row, bool there, bool wide) {
+            if (wide && kb + 4 <= p.kb) {
+              mkw::cp_async16(to + place * 16, row + (there ? kb : 0), there);
+            } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_e4m3(tmem + u * BN, desc_sw128(a + 32 * k), desc_sw128(a + kWTile + 32 * k), kId, k != 0);
-          mma_commit(&empty[s]);
-          mma_commit(&tfull[u]);
-        }
-      // every product has been taken out (or abandoned, after the wait's limit) before tensor memory goes
-      for (int i = it - 2 < 0 ? 0 : it - 2; i < it; ++i) mbar_wait(&tfull[i & 1], (i / 2) & 1, kWaitNs);
-    }
-  } else if (warp >= 2 + kAddWarps) {
-    const int sw = warp - 2 - kAddWarps;
-    int it = 0;
-    bool ok = true;
-    for (int tile = first; tile < p.tiles && ok; tile += ctas) {
-      const int jb = tile % p.tiles_n, t0 = tile / p.tiles_n * BN;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int s = it % kScaleSlots;
-        const float ws = p.w_scale[static_cast<int64_t>(jb) * p.kb + kb];
-        float x[(BN + 63) / 64];
+              for (int e = 0; e < 4; ++e) {
+                const bool some = there && kb + e < kb1;
+                mkw::cp_async4(to + place * 16 + e * 4, row + (some ? kb + e : 0), some);
+              }
+            }
+          };
 #pragma unroll
-        for (int i = 0; i < (BN + 63) / 64; ++i) {
-          const int t = t0 + i * 64 + sw * 32 + lane;
-          x[i] = t < p.m ? p.x_scale[t * p.x_scale_row + kb] : 0.f;
+          for (int i = 0; i < 4; ++i) {
+            const bool there = t0 + 32 * i < p.m;
+            copy(lane + 32 * i, p.x_scale + (there ? (t0 + 32 * i) * p.x_scale_row : 0), there, p.wide_scales && kb0 % 4 == 0);
+          }
+          if (lane < 2) {
+            const bool there = (jb + lane) * kBlock < p.n;
+            copy(kRows + lane, p.w_scale + (there ? static_cast<int64_t>(jb + lane) * p.kb : 0), there, false);
+          }
+          mkw::cp_async_commit();
+          mkw::cp_async_wait<kAhead>();
+          if (g >= kAhead) tell(g - kAhead + 1);
         }
-        if (it >= kScaleSlots && !__all_sync(0xffffffffu, mbar_wait(&sempty[s], (it / kScaleSlots - 1) & 1, kWaitNs))) {
-          if (lane == 0) fail(p.status);
-          ok = false;
-          break;
-        }
-#pragma unroll
-        for (int i = 0; i < (BN + 63) / 64; ++i)
-          if (i * 64 + sw * 32 + lane < BN) scales[s * BN + i * 64 + sw * 32 + lane] = x[i] * ws;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sfull[s]);
       }
+      mkw::cp_async_wait<0>();
+      if (ok) tell(g);
     }
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;        // lanes of tensor memory, half of the columns
-    const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + half * C::COLS;
-    int it = 0;
+    const int q = warp & 3, part = (warp - kHelpers) >> 2; // lanes of tensor memory, half of the columns
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + part * C::COLS;
+    Turn<C::SUMS> sums;
+    Turn<kGroups> groups;
+    unsigned char *mine = sm + C::RESULTS + (warp - kHelpers) * 32 * ROWB;
+    uint64_t *loaded = rfull + (warp - kHelpers);
+    uint32_t load_parity = 0;
     bool ok = true;
-    for (int tile = first; tile < p.tiles; tile += ctas) {
-      const int j = tile % p.tiles_n * 128 + 32 * q + lane, t0 = tile / p.tiles_n * BN + half * C::COLS;
-      float acc[C::COLS];
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      if (!__all_sync(0xffffffffu, mbar_test(bar, parity)) && !__all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs))) {
+        if (lane == 0) fail(p.status);
+        ok = false;
+      }
+      return ok;
+    };
+    for (int tile = first; tile < p.tiles; tile += step) {
+      const int t = row_of(tile) + 32 * q + lane, j0 = column_of(tile) + part * C::COLS;
+      const bool idle = __all_sync(0xffffffffu, t >= p.m || j0 >= p.n);   // a warp without a result only takes part
+      unsigned long long acc[C::COLS / 2];
 #pragma unroll
-      for (int i = 0; i < C::COLS; ++i) acc[i] = 0.f;
-      for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
-        const int u = it & 1, s = it % kScaleSlots;
-        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[u], (it / 2) & 1, kWaitNs) && mbar_wait(&sfull[s], (it / kScaleSlots) & 1, kWaitNs))) {
-          if (lane == 0) fail(p.status);
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const float *sc = scales + s * BN + half * C::COLS;
-        constexpr int STEP = C::COLS < 32 ? C::COLS : 32;
-#pragma unroll
-        for (int c = 0; c < C::COLS; c += STEP) {
-          uint32_t v[32];
-          if constexpr (STEP == 32) {
-            tmem_ld32(at + u * BN + c, v);
-          } else if constexpr (STEP == 16) {
-            float f[16];
-            tmem_ld16(at + u * BN + c, f);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(f[i]);
-          } else {
-            tmem_ld8(at + u * BN + c, v);
-          }
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < STEP; i += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(sc + c + i);
-            acc[c + i] = fmaf(__uint_as_float(v[i]), f.x, acc[c + i]);
-            acc[c + i + 1] = fmaf(__uint_as_float(v[i + 1]), f.y, acc[c + i + 1]);
-            acc[c + i + 2] = fmaf(__uint_as_float(v[i + 2]), f.z, acc[c + i + 2]);
-            acc[c + i + 3] = fmaf(__uint_as_float(v[i + 3]), f.w, acc[c + i + 3]);
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
+      for (int i = 0; i < C::COLS / 2; ++i) acc[i] = 0ull;
+      // the residual comes to where the results will be, once what was there has been stored
+      const bool by_tma = p.tma && p.splits == 1 && !idle;
+      auto ask_residual = [&](int c) {
         if (lane == 0) {
-          mbar_arrive(&tempty[u]);
-          mbar_arrive(&sempty[s]);
+          bulk_wait_read();
+          mbar_expect_tx(loaded, 32 * ROWB);
+          tma_load_2d(mine, &tr, j0 + c, t - lane, loaded);
+        }
+      };
+      for (int kbg = kb0; kbg < kb1 && ok; kbg += kGroup, groups.next()) {
+        if (by_tma && p.residual && kbg + kGroup >= kb1) ask_residual(0);
+        const float4 *sc = scales + groups.i * (kRows + 2);
+        if (!wait(&sfull[groups.i], groups.parity)) break;
+        const float4 fx = sc[32 * q + lane], fw = sc[kRows + part * C::COLS / kBlock];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[groups.i]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (kbg + 2 * h >= kb1) break;
+          const bool two = kbg + 2 * h + 1 < kb1;
+          if (!wait(&tfull[sums.i], sums.parity)) break;
+          tc_fence_after();
+          if (!idle) {
+            const uint32_t from = at + sums.i * 2 * BN;
+            uint32_t v[2][32];
+            tmem_ld32(from, v[0]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (i == 1 && !two) break;
+              const float f = (&fx.x)[2 * h + i] * (&fw.x)[2 * h + i];
+              unsigned long long ff;
+              asm("mov.b64 %0, {%1, %1};" : "=l"(ff) : "f"(f));
+#pragma unroll
+              for (int c = 0; c < C::COLS; c += 32) {
+                uint32_t(&now)[32] = v[c / 32 & 1];
+                tmem_ld_wait(now);
+                if (c + 32 < C::COLS) tmem_ld32(from + i * BN + c + 32, v[(c / 32 + 1) & 1]);
+                else if (i == 0 && two) tmem_ld32(from + BN, v[(c / 32 + 1) & 1]);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) add_scaled(acc[c / 2 + e], now[2 * e], now[2 * e + 1], ff);
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[sums.i]);
+          sums.next();
         }
       }
       if (!ok) break;
-      if (p.splits == 1) {
-        if (j < p.n) {
+      auto sum = [&](int i) { return __uint_as_float(static_cast<uint32_t>(i & 1 ? acc[i / 2] >> 32 : acc[i / 2])); };
+      if (p.splits > 1) {
+        // (one tile a cluster; its stages have been read)
+        float4 *to = reinterpret_cast<float4 *>(reinterpret_cast<float *>(sm) + (32 * q + lane) * kSplitRow<BN> + part * C::COLS);
+        if (!idle) {
 #pragma unroll
-          for (int i = 0; i < C::COLS; ++i) {
-            const int t = t0 + i;
-            if (t >= p.m) break;
-            float y = acc[i];
-            if (p.residual) y += static_cast<float>(static_cast<const T *>(p.residual)[t * p.residual_row + j]);
-            static_cast<T *>(p.y)[t * p.y_row + j] = static_cast<T>(y);
+          for (int i = 0; i < C::COLS / 4; ++i) to[i] = make_float4(sum(4 * i), sum(4 * i + 1), sum(4 * i + 2), sum(4 * i + 3));
+        }
+      } else if (by_tma) {
+        // a box of 32 rows at a time: the residual is there, the results go out
+#pragma unroll
+        for (int c = 0; c < C::COLS; c += PIECE) {
+          if (!p.residual) {
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
+          } else {
+            if (c > 0) ask_residual(c);
+            __syncwarp();
+            if (!wait(loaded, load_parity)) break;
+            load_parity ^= 1u;
+          }
+#pragma unroll
+          for (int i = 0; i < PIECE / N; ++i) {
+            uint4 *at = reinterpret_cast<uint4 *>(mine + lane * ROWB + ((i ^ (ROWB == 128 ? lane & 7 : lane >> 1 & 3)) << 4));
+            float v[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] = sum(c + i * N + e);
+            if (p.residual) Out<T>::add(*at, v);
+            *at = Out<T>::bits(v);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            if (j0 + c < p.n) tma_store_2d(&ty, mine, j0 + c, t - lane);
+            bulk_commit();
           }
         }
-      } else {
-        // (one tile a cluster; its stages have been read)
-        float *mine = reinterpret_cast<float *>(sm);
+        if (!ok) break;
+      } else if (!idle) {
+        // rows that are not on 16 bytes: 16 columns of 32 rows at a time through shared memory, then element by element
 #pragma unroll
-        for (int i = 0; i < C::COLS; ++i) mine[(half * C::COLS + i) * 128 + 32 * q + lane] = acc[i];
+        for (int c = 0; c < C::COLS; c += 16) {
+          auto at = [&](int row, int col) { return reinterpret_cast<float *>(mine) + row * 16 + (col ^ ((row >> 1 & 3) << 2)); };
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(at(lane, i)) = make_float4(sum(c + i), sum(c + i + 1), sum(c + i + 2), sum(c + i + 3));
+          __syncwarp();
+          const int col = j0 + c + (lane & 15);
+          if (col < p.n)
+#pragma unroll 4
+            for (int row = lane >> 4; row < min(32, p.m - (t - lane)); row += 2) {
+              const int64_t r = t - lane + row;
+              float v = *at(row, lane & 15);
+              if (p.residual) v += static_cast<float>(static_cast<const T *>(p.residual)[r * p.residual_row + col]);
+              static_cast<T *>(p.y)[r * p.y_row + col] = static_cast<T>(v);
+            }
+          __syncwarp();
+        }
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
   if (p.splits > 1) {
     mkw::cluster_arrive();
     mkw::cluster_wait();
-    // columns rank, rank + splits, .. of the tile: the CTAs' sums in order
-    const int j0 = first % p.tiles_n * 128, t0 = first / p.tiles_n * BN;
-    for (int i = threadIdx.x; i < (BN - rank + p.splits - 1) / p.splits * 128; i += kThreads) {
-      const int c = rank + i / 128 * p.splits, j = j0 + i % 128, t = t0 + c;
-      if (c >= BN || t >= p.m || j >= p.n) continue;
-      const float *own = reinterpret_cast<const float *>(sm) + c * 128 + i % 128;
-      float y = 0.f;
-      for (int r = 0; r < p.splits; ++r) y += load_remote(mkw::remote(own, r));
-      if (p.residual) y += static_cast<float>(static_cast<const T *>(p.residual)[t * p.residual_row + j]);
-      static_cast<T *>(p.y)[t * p.y_row + j] = static_cast<T>(y);
+    // BN / splits columns each, four a thread: the CTAs' sums in order
+    const int t0 = first % p.tiles_m * kRows, j0 = first / p.tiles_m * BN, rows = min(kRows, p.m - t0), columns = BN / p.splits, fours = columns / 4;
+    for (int i = threadIdx.x; i < fours * rows; i += kThreads) {
+      const int t = i / fours, c = split * columns + i % fours * 4, col = j0 + c;
+      if (col >= p.n) continue;
+      const float *own = reinterpret_cast<const float *>(sm) + t * kSplitRow<BN> + c;
+      float4 part[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < p.splits) part[r] = load_remote4(mkw::remote(own, r));
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < p.splits) v[0] += part[r].x, v[1] += part[r].y, v[2] += part[r].z, v[3] += part[r].w;
+      T *y = static_cast<T *>(p.y) + (t0 + t) * p.y_row + col;
+      const T *res = p.residual ? static_cast<const T *>(p.residual) + (t0 + t) * p.residual_row + col : nullptr;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (col + e < p.n) y[e] = static_cast<T>(res ? v[e] + static_cast<float>(res[e]) : v[e]);
     }
     mkw::cluster_arrive();                                 // nobody leaves while its sums are read
     mkw::cluster_wait();
@@ -340,6 +547,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
+// rows of T, `row` apart, in boxes of 32 rows, 64 or 128 bytes of each
+template <class T>
+bool result_map(CUtensorMap *map, const void *base, int64_t columns, int64_t rows, int64_t row, int box_columns) {
+  const auto enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(rows)}, strides[1] = {static_cast<cuuint64_t>(row) * sizeof(T)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_columns), 32}, es[2] = {1, 1};
+  return enc(map, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, box_columns * sizeof(T) == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // rows of `inner` bytes, `row` apart, in boxes of 128 bytes by box_rows
 bool byte_map(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, int64_t row, int box_rows) {
   const auto enc = encoder();
@@ -352,20 +571,23 @@ bool byte_map(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, i
 
 template <int BN, class T>
 int launch(const mk_matmul_fp8_args *a, MatmulParams &p, int sms, int dev, cudaStream_t s) {
-  using C = Cfg<BN>;
+  using C = Cfg<BN, T>;
   static mkw::Ready ready[mkw::kMaxDevices];
   const auto fn = &matmul_kernel<BN, T>;
   mkw::Ready &r = ready[dev];
   if (!r.get(reinterpret_cast<const void *>(fn), kThreads, C::SMEM)) return MK_ERR_CUDA;
-  CUtensorMap tw, tx;
-  if (!byte_map(&tw, a->w, a->k, a->n, a->w_row, 128) || !byte_map(&tx, a->x, a->k, a->m, a->x_row, BN)) return MK_ERR_CUDA;
-  const int64_t tiles_n = (a->n + 127) / 128, tiles = tiles_n * ((static_cast<int64_t>(a->m) + BN - 1) / BN);
+  p.x_rows = std::min(kRows, (a->m + 7) / 8 * 8);
+  CUtensorMap tw, tx, ty = {}, tr = {};
+  if (p.tma && (!result_map<T>(&ty, a->y, a->n, a->m, p.y_map_row, C::PIECE) || (a->residual && !result_map<T>(&tr, a->residual, a->n, a->m, p.residual_map_row, C::PIECE))))
+    return MK_ERR_CUDA;
+  if (!byte_map(&tx, a->x, a->k, a->m, a->x_row, p.x_rows) || !byte_map(&tw, a->w, a->k, a->n, a->w_row, BN)) return MK_ERR_CUDA;
+  p.tiles_m = (a->m - 1) / kRows + 1;
+  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * ((a->n - 1) / BN + 1);
   if (tiles > INT32_MAX - 65536) return MK_ERR_UNSUPPORTED;
-  p.tiles_n = static_cast<int>(tiles_n), p.tiles = static_cast<int>(tiles);
+  p.tiles = static_cast<int>(tiles);
   p.splits = 1;
-  for (int i = 0; i < 3 && BN * 128 * 4 <= static_cast<int>(C::SCALES) && tiles * (2 << i) <= sms && p.kb >= 2 * (2 << i) && tiles <= r.clusters[i]; ++i)
-    p.splits = 2 << i;
-  const int ctas = p.splits > 1 ? p.tiles * p.splits : std::min(p.tiles, sms);
+  for (int i = 0; i < 3 && tiles * (2 << i) <= sms && p.kb >= 2 * (2 << i) && tiles <= r.clusters[i]; ++i) p.splits = 2 << i;
+  const int clusters = p.splits > 1 ? p.tiles : std::min(p.tiles, sms);
   cudaLaunchAttribute attr[2] = {};
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -373,25 +595,17 @@ int launch(const mk_matmul_fp8_args *a, MatmulParams &p, int sms, int dev, cudaS
   attr[1].val.clusterDim.x = p.splits;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(clusters * p.splits);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = p.splits > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, fn, tw, tx, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, fn, tx, tw, ty, tr, p) != cudaSuccess) {
     cudaGetLastError();
     return MK_ERR_CUDA;
   }
   return MK_OK;
-}
-
-template <class T>
-int launch_rows(const mk_matmul_fp8_args *a, MatmulParams &p, int sms, int dev, cudaStream_t s) {
-  if (a->m <= 16) return launch<16, T>(a, p, sms, dev, s);
-  if (a->m <= 64) return launch<64, T>(a, p, sms, dev, s);
-  const int64_t tiles = (a->n + 127) / 128 * ((static_cast<int64_t>(a->m) + 255) / 256);
-  return tiles < sms ? launch<128, T>(a, p, sms, dev, s) : launch<256, T>(a, p, sms, dev, s);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -411,13 +625,21 @@ extern "C" int mk_quantize_fp8(const mk_quantize_fp8_args *a, mk_stream stream) 
   QuantParams p = {};
   p.x = a->x, p.codes = static_cast<uint8_t *>(a->codes), p.scales = a->scales;
   p.x_row = a->x_row, p.codes_row = a->codes_row, p.scales_row = a->scales_row;
-  p.m = a->m, p.k = a->k, p.blocks = (a->k - 1) / kBlock + 1;
-  p.items = static_cast<int64_t>(p.m) * p.blocks;
-  const int64_t ctas = (p.items - 1) / (kQuantThreads / 16) + 1;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ctas, 32 * sms)));
+  p.k = a->k;
+  p.blocks.set((a->k - 1) / kBlock + 1);
+  const int64_t items = static_cast<int64_t>(a->m) * p.blocks.value;
+  if (items > INT32_MAX - 65536) return MK_ERR_UNSUPPORTED;
+  p.items = static_cast<int>(items);
+  // four blocks at a time where there are enough to fill the SMs several times over (8192 x 2048 in bf16: 11.2 us, one at a
+  // time 16), else one (8 x 1024: 1.5 us, 2.1 with four)
+  const bool many = items >= int64_t{4} * 16 * 16 * sms;
+  const int each = kQuantThreads / 16 * (many ? 4 : 1);
+  const dim3 grid(static_cast<unsigned>((items - 1) / each + 1));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (a->dtype == MK_F32) return mkw::launch_after(&quantize_kernel<float>, grid, kQuantThreads, 0, s, p);
-  return mkw::launch_after(&quantize_kernel<__nv_bfloat16>, grid, kQuantThreads, 0, s, p);
+  using B = __nv_bfloat16;
+  if (a->dtype == MK_F32)
+    return many ? mkw::launch_after(&quantize_kernel<float, 4>, grid, kQuantThreads, 0, s, p) : mkw::launch_after(&quantize_kernel<float, 1>, grid, kQuantThreads, 0, s, p);
+  return many ? mkw::launch_after(&quantize_kernel<B, 4>, grid, kQuantThreads, 0, s, p) : mkw::launch_after(&quantize_kernel<B, 1>, grid, kQuantThreads, 0, s, p);
 }
 
 extern "C" int mk_matmul_fp8(const mk_matmul_fp8_args *a, mk_stream stream) {
@@ -438,6 +660,12 @@ extern "C" int mk_matmul_fp8(const mk_matmul_fp8_args *a, mk_stream stream) {
   p.x_scale = a->x_scale, p.w_scale = a->w_scale, p.residual = a->residual, p.y = a->y, p.status = a->status;
   p.x_scale_row = a->x_scale_row, p.residual_row = a->residual_row, p.y_row = a->y_row;
   p.m = a->m, p.n = a->n, p.kb = (a->k - 1) / kBlock + 1;
+  // (an expanded residual has no stride that a tensor map takes; a single row may have any)
+  const int64_t one = (a->n * static_cast<int64_t>(es) + 15) / 16 * 16 / static_cast<int64_t>(es);
+  p.y_map_row = a->m == 1 ? one : a->y_row, p.residual_map_row = a->m == 1 ? one : a->residual_row;
+  auto mapped = [&](const void *t, int64_t row) { return aligned16(t) && row * es % 16 == 0 && row >= a->n && row < (int64_t{1} << 36); };
+  p.tma = mapped(a->y, p.y_map_row) && (!a->residual || mapped(a->residual, p.residual_map_row));
+  p.wide_scales = aligned16(a->x_scale) && a->x_scale_row % 4 == 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return a->dtype == MK_F32 ? launch_rows<float>(a, p, sms, dev, s) : launch_rows<__nv_bfloat16>(a, p, sms, dev, s);
+  return a->dtype == MK_F32 ? launch<kColumns, float>(a, p, sms, dev, s) : launch<kColumns, __nv_bfloat16>(a, p, sms, dev, s);
 }

@@ -159,6 +159,11 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// 4 bytes; with valid false nothing is read and zeros are written
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+
 // Programmatic dependent launch: the first statement of every kernel here, before it reads or writes anything.  The next
 // kernel of the stream, if it is launched so too, may be set up from now on; what the previous one did is seen after it.
 __device__ __forceinline__ void follow_previous_kernel() {

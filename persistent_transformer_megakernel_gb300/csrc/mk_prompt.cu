@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   __shared__ Task s_task;
   mkw::follow_previous_kernel();
   unsigned char *sm = smraw + ((1024u - (smem_addr(smraw) & 1023u)) & 1023u);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   int results = 0;
   const bool any = find_task(p, blockIdx.x, reinterpret_cast<int *>(sm + LY::Q), &s_task, &results);
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
 
   if (warp > kMmaWarp) {
     // ---- copies: a warp has 32 positions of a block, a lane looks one of them up ------------
@@ -462,32 +462,42 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     if (ok) tell(n_tiles);
   } else if (warp == kMmaWarp) {
     // ---- products: S = Q K^T of a tile, then O += P V with P where S was, so that the next S of the tile comes behind it
-    if (lane == 0 && b0 < b1) {
-      const uint32_t qa = smem_addr(Qs), kva = smem_addr(KVs);
+    if (b0 < b1) {
+      // descriptors: the low words move with the tile, the high ones are constants
+      const uint64_t kd = desc_sw128(smem_addr(KVs)), vd = desc_mn_sw128_at(smem_addr(KVs), kBlock * 128, 1024);
+      const uint32_t q_lo = static_cast<uint32_t>(desc_sw128(smem_addr(Qs))), k_lo = static_cast<uint32_t>(kd), v_lo = static_cast<uint32_t>(vd);
+      const uint32_t k_hi = static_cast<uint32_t>(kd >> 32), v_hi = static_cast<uint32_t>(vd >> 32);
       bool ok = true;
       uint32_t pph[2] = {0, 0};
       bool first[2] = {true, true};
       auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (ok && !mbar_wait(bar, parity, kWaitNs)) {
-          report(p.status, MK_ERR_TIMEOUT);
+        if (ok && !__all_sync(0xffffffffu, mbar_test(bar, parity)) && !__all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs))) {
+          if (lane == 0) report(p.status, MK_ERR_TIMEOUT);
           ok = false;
         }
         tc_fence_after();
         return ok;
       };
       auto scores = [&](int t, int n_tile) {
-        const uint32_t ka = kva + (n_tile % kSlots) * LY::TILE, qt = qa + t * LY::TILE;
+        if (elect_one()) {
+          const uint32_t k_at = k_lo + (n_tile % kSlots) * (LY::TILE >> 4), q_at = q_lo + t * (LY::TILE >> 4);
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint32_t off = (s >> 2) * (128 * 128) + (s & 3) * 32;
-          mma_bf16(tmem + t * LY::S_COLS, desc_sw128(qt + off), desc_sw128(ka + off), kIdS, s != 0);
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t off = ((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4;
+            mma_bf16(tmem + t * LY::S_COLS, desc_of(q_at + off, k_hi), desc_of(k_at + off, k_hi), kIdS, s != 0);
+          }
+          mma_commit(&sfull[t]);
         }
-        mma_commit(&sfull[t]);
+        __syncwarp();
+      };
+      auto release = [&](int n_tile) {
+        if (elect_one()) mma_commit(&empty[n_tile % kSlots]);
+        __syncwarp();
       };
       if (wait(&full[0], 0)) {
         for (int t = 0; t < 2; ++t)
           if (sees(t, x.number(b0))) scores(t, 0);
-        mma_commit(&empty[0]);
+        release(0);
       }
       for (int b = b0; b < b1 && ok; ++b) {
         const int j = b - b0, vt = 2 * j + 1, kt = 2 * j + 2;
@@ -497,22 +507,25 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           if (sees(t, x.number(b))) {
             if (!wait(&pfull[t], pph[t])) break;
             pph[t] ^= 1;
-            const uint32_t va = kva + (vt % kSlots) * LY::TILE;
+            if (elect_one()) {
+              const uint32_t v_at = v_lo + (vt % kSlots) * (LY::TILE >> 4);
 #pragma unroll
-            for (int s = 0; s < kBlock / 16; ++s)
-              mma_f16_ta(tmem + LY::O_COL + t * D, tmem + t * LY::S_COLS + s * 8, desc_mn_sw128_at(va + s * 2048, kBlock * 128, 1024), kIdO,
-                         !(first[t] && s == 0));
+              for (int s = 0; s < kBlock / 16; ++s)
+                mma_f16_ta(tmem + LY::O_COL + t * D, tmem + t * LY::S_COLS + s * 8, desc_of(v_at + s * (2048 >> 4), v_hi), kIdO, !(first[t] && s == 0));
+            }
+            __syncwarp();
             first[t] = false;
           }
           if (more && sees(t, x.number(b + 1)) && wait(&full[kt % kSlots], (kt / kSlots) & 1)) scores(t, kt);
         }
         if (more && !wait(&full[kt % kSlots], (kt / kSlots) & 1)) break;
-        mma_commit(&empty[vt % kSlots]);
-        if (more) mma_commit(&empty[kt % kSlots]);
+        release(vt);
+        if (more) release(kt);
       }
-      mma_commit(&ofull[0]);                               // all of it is done (also where a wait ran out)
+      if (elect_one()) mma_commit(&ofull[0]);              // all of it is done (also where a wait ran out)
+      __syncwarp();
       mbar_wait(&ofull[0], 0, kWaitNs);
-      mbar_arrive(&ofull[1]);
+      if (lane == 0) mbar_arrive(&ofull[1]);
     }
   } else {
     // ---- softmax ---------------------------------------------------------------------------
@@ -539,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       auto load = [&](int c, float (&v)[32]) {
         uint32_t u[32];
         tmem_ld32(s_at + c, u);
-        tmem_ld_wait();
+        tmem_ld_wait(u);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
         if (edge) {
@@ -568,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           for (int c = 0; c < D; c += 32) {
             uint32_t u[32];
             tmem_ld32(o_at + c, u);
-            tmem_ld_wait();
+            tmem_ld_wait(u);
 #pragma unroll
             for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
             tmem_st32(o_at + c, u);
@@ -618,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       float y[32];
       if (started && ok) {
         tmem_ld32(o_at + c, u);
-        tmem_ld_wait();
+        tmem_ld_wait(u);
       }
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
