@@ -477,7 +477,7 @@ typedef struct {
   int32_t window, sinks;       /* as for mk_paged_attention, at each row's own place */
   float scale;
   void *workspace;             /* device, 16-byte aligned; the call's own until the stream has passed it */
-  int64_t workspace_bytes;     /* at least mk_paged_prompt_attention_workspace (rows that see few tokens need none) */
+  int64_t workspace_bytes;     /* at least mk_paged_prompt_attention_workspace */
   int32_t *status;             /* device, or NULL */
 } mk_prompt_args;
 
@@ -502,9 +502,9 @@ int mk_paged_prompt_attention(const mk_paged_kv *kv, const mk_prompt_args *a, mk
 int mk_paged_prompt_attention_ask(const mk_paged_kv *kv, const mk_prompt_args *a, mk_workspace_fn workspace,
                                   void *context, mk_stream stream);
 
-/* Bytes of workspace any mk_paged_prompt_attention call needs on the current
- * device, or a negative error. */
-int64_t mk_paged_prompt_attention_workspace(int32_t head_dim);
+/* Bytes of workspace a mk_paged_prompt_attention call of these sizes needs on the
+ * current device at most, or a negative error. */
+int64_t mk_paged_prompt_attention_workspace(int32_t n, int32_t rows, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim);
 
 typedef struct {
   int32_t n;                   /* sequences; at most 16384 */

@@ -186,7 +186,7 @@ def load_library(path: Optional[str] = None):
     lib.mk_paged_plan.argtypes = [C.POINTER(mk_plan_args), vp]
     lib.mk_paged_prompt_attention.argtypes = [C.POINTER(mk_paged_kv), C.POINTER(mk_prompt_args), vp]
     lib.mk_paged_prompt_attention_ask.argtypes = [C.POINTER(mk_paged_kv), C.POINTER(mk_prompt_args), WORKSPACE_FN, vp, vp]
-    lib.mk_paged_prompt_attention_workspace.argtypes = [i32]
+    lib.mk_paged_prompt_attention_workspace.argtypes = [i32] * 5
     lib.mk_quantize_fp8.argtypes = [C.POINTER(mk_quantize_fp8_args), vp]
     lib.mk_matmul_fp8.argtypes = [C.POINTER(mk_matmul_fp8_args), vp]
     lib.mk_adjust_logits.argtypes = [C.POINTER(mk_logits_args), vp]

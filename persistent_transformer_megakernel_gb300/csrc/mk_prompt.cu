@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/mk.h"
 #include "mk_launch_after.h"
@@ -17,11 +18,10 @@ namespace mkprompt {
 
 using namespace mktc;
 
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kCopyWarps = 4, kWarps = kSoftWarps + 1 + kCopyWarps, kThreads = 32 * kWarps;
+constexpr int kSoftWarps = 8, kCopyWarps = 4, kWarps = kSoftWarps + 1 + kCopyWarps, kThreads = 32 * kWarps;
 constexpr int kRows = 128;            // of a query tile (the MMA's M); a CTA has two
 constexpr int kBlock = 128;           // cached positions of a step
-constexpr int kSlots = 4;             // key and value tiles in shared memory, in turn
-constexpr int kMaxSequences = 16384;
+constexpr int kMaxSequences = 16384, kTaskThreads = 1024;
 constexpr int kLeastBlocks = 8;       // an item of at most so many blocks is not split
 constexpr long long kWaitNs = 2000000000LL;
 
@@ -33,13 +33,16 @@ struct PromptParams {
   const int32_t *table, *starts, *lengths;
   const float *k_scale, *v_scale;
   int32_t *status;
-  int4 *records;               // [0].x: partial results in all; then of each {first row, tokens, virtual head, parts or 0}
-  float *parts;                // [partial result][2 kRows][D + 4]: O, maximum, sum
+  int4 *header;                // .x: tasks, .y: partial results in all
+  int4 *records;               // of each partial result {first row, tokens, virtual head, parts or 0}
+  struct Task *tasks;
+  float *parts;                // [partial result][tile][D + 2][kRows]: O, maximum, sum
   mkw::Divisor page_size, heads;   // heads: query heads of a tile's token
   int n, rows, hq, hkv, group, n_pages, capacity, window, sinks;
   int blocks, vh;              // head blocks of a kv head, virtual heads hkv * blocks
   int tokens;                  // of a tile: kRows / heads
-  int sms;
+  int sms, ctas;               // ctas: of the attention kernel, at least as many as there are tasks
+  int joins;                   // whether any item can be cut
   float scale;
 };
 
@@ -47,8 +50,9 @@ template <int D>
 struct Layout {
   static constexpr int ATOMS = D / 64;
   static constexpr uint32_t TILE = ATOMS * 128 * 128;      // 128 rows of D 16-bit elements
+  static constexpr int SLOTS = D == 128 ? 5 : 4;           // key and value tiles in shared memory, in turn
   static constexpr uint32_t CONTROL = 1024, Q = CONTROL, KV = Q + 2 * TILE;
-  static constexpr int SMEM = static_cast<int>(1024 + KV + kSlots * TILE);
+  static constexpr int SMEM = static_cast<int>(1024 + KV + SLOTS * TILE);
   static constexpr uint32_t S_COLS = kBlock, O_COL = 2 * S_COLS, TMEM_COLS = 512;
 };
 
@@ -84,9 +88,13 @@ __device__ __forceinline__ Pair pair_of(const PromptParams &p, int start, int co
   return x;
 }
 
-struct Task {
-  int seq, pair, vh, part, parts, slot;
+// A CTA's part of the work, 48 bytes: of a pair of tiles and a virtual head the blocks b0 .. b1 - 1.
+struct __align__(16) Task {
+  int row, count, pos, seq;    // as in Pair
+  int lo, head, skip, vh;
+  int b0, b1, slot, outside;   // slot: of the partial result, < 0: none, the task is whole; outside: longer than its row of the table
 };
+static_assert(sizeof(Task) == 48, "read as three 16-byte words");
 
 // exclusive sum over the block's threads, and the total
 __device__ __forceinline__ long long block_sum(long long x, long long *warps, long long &total) {
@@ -103,32 +111,32 @@ __device__ __forceinline__ long long block_sum(long long x, long long *warps, lo
   total = 0;
   long long before = 0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
+  for (int i = 0; i < kTaskThreads / 32; ++i) {
     if (i < w) before += warps[i];
     total += warps[i];
   }
   return before + s - x;
 }
 
-__device__ __forceinline__ int count_of(const PromptParams &p, int i, bool *bad) {
-  const int a = p.starts[i], b = p.starts[i + 1];
-  if (a < 0 || b < a || b > p.rows) {
-    *bad = true;
-    return 0;
-  }
-  return p.lengths[i] < 0 ? 0 : b - a;
-}
-
-// Task `index` in the order of sequences, their last rows (which see most) first; false if there are fewer.  Every item
-// (pair of tiles and virtual head) of more blocks than an equal share of all the work is cut into parts.
-__device__ bool find_task(const PromptParams &p, int index, int *before, Task *s_task, int *results) {
-  __shared__ long long s_warps[kWarps];
+// The tasks of a call, in the order of sequences, their last rows (which see most) first; CTA i of the attention kernel takes
+// task i.  Every item (pair of tiles and virtual head) of more blocks than an equal share of all the work is cut into parts.
+// One CTA: a call's lengths are on the device, and every CTA of the other kernel finding its own task took 3.5 us each.
+__global__ void __launch_bounds__(kTaskThreads) task_kernel(const __grid_constant__ PromptParams p) {
+  extern __shared__ int before[];                          // pairs before a sequence: [n + 1]
+  __shared__ long long s_warps[kTaskThreads / 32];
+  __shared__ int s_tasks, s_slots;
+  mkw::follow_previous_kernel();
   const int tid = threadIdx.x, n = p.n, step = 2 * p.tokens;
   bool bad = false;
-  for (int i = tid; i < n; i += kThreads) before[i] = (count_of(p, i, &bad) + step - 1) / step;
+  for (int i = tid; i < n; i += kTaskThreads) {
+    const int a = p.starts[i], b = p.starts[i + 1], length = p.lengths[i];
+    const bool fine = a >= 0 && b >= a && b <= p.rows;
+    bad |= !fine;
+    before[i] = fine && length >= 0 ? (b - a + step - 1) / step : 0;
+  }
   if (bad) report(p.status, MK_ERR_BAD_PAGE);
   __syncthreads();
-  const int per = (n + kThreads - 1) / kThreads, a = min(n, tid * per), b = min(n, a + per);
+  const int per = (n + kTaskThreads - 1) / kTaskThreads, a = min(n, tid * per), b = min(n, a + per);
   int mine = 0;
   for (int i = a; i < b; ++i) mine += before[i];
   long long total;
@@ -141,20 +149,19 @@ __device__ bool find_task(const PromptParams &p, int index, int *before, Task *s
   const int pairs = static_cast<int>(total);
   if (tid == 0) before[n] = pairs;
   __syncthreads();
-  const int share = (pairs + kThreads - 1) / kThreads, p0 = min(pairs, tid * share), p1 = min(pairs, p0 + share);
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (before[mid] <= p0) lo = mid;
+  const int share = (pairs + kTaskThreads - 1) / kTaskThreads, p0 = min(pairs, tid * share), p1 = min(pairs, p0 + share);
+  int i0 = 0, hi = n;
+  while (hi - i0 > 1) {
+    const int mid = (i0 + hi) >> 1;
+    if (before[mid] <= p0) i0 = mid;
     else hi = mid;
   }
-  const int i0 = lo;
-  long long cost = 0;
-  for (int pass = 0;; ++pass) {
-    // pass 0: all blocks; pass 1: tasks and partial results before this thread's; pass 2: the task
-    const long long limit = pass == 0 ? 0 : max(static_cast<long long>(kLeastBlocks), (total * p.vh + p.sms - 1) / p.sms);
-    long long sum = 0;
-    const long long from = pass == 2 ? cost : 0;
+  // pass 0: all blocks; pass 1: tasks and partial results before this thread's; pass 2: the tasks
+  int limit = INT32_MAX;
+  long long sum = 0;
+#pragma unroll 1
+  for (int pass = p.joins ? 0 : 1; pass < 3; ++pass) {
+    if (pass < 2) sum = 0;
     int i = i0, start = 0, count = 0, length = 0, of = -1;
     for (int x = p0; x < p1; ++x) {
       while (x >= before[i + 1]) ++i;
@@ -164,52 +171,87 @@ __device__ bool find_task(const PromptParams &p, int index, int *before, Task *s
         count = p.starts[i + 1] - start;
         length = p.lengths[i];
       }
-      const int t = before[i + 1] - 1 - x;
-      const int blocks = pair_of(p, start, count, length, t).blocks;
+      const Pair pair = pair_of(p, start, count, length, before[i + 1] - 1 - x);
       if (pass == 0) {
-        sum += blocks;
+        sum += pair.blocks;
         continue;
       }
-      const int parts = blocks > limit ? static_cast<int>((blocks + limit - 1) / limit) : 1, tasks = parts * p.vh;
+      const int parts = pair.blocks > limit ? (pair.blocks - 1) / limit + 1 : 1, tasks = parts * p.vh;
       if (pass == 2) {
-        const int first = static_cast<int>((from + sum) >> 32), slots = static_cast<int>(from + sum);
-        if (index >= first && index < first + tasks) {
-          const int k = index - first;
-          *s_task = Task{i, t, k / parts, k % parts, parts, parts > 1 ? slots + k : -1};
+        const int first = static_cast<int>(sum >> 32), slots = static_cast<int>(sum);
+        if (first + tasks > p.ctas) {                      // (starts that overlap: what is past the end is not done)
+          atomicMin(&s_tasks, first);
+          atomicMin(&s_slots, slots);
+        } else {
+          for (int k = 0, vh = 0, part = 0; k < tasks; ++k) {
+            const int slot = parts > 1 ? slots + k : -1;
+            Task t{pair.row, pair.count, pair.pos, i, pair.lo, pair.head, pair.skip, vh, 0, 0, slot, length > p.capacity};
+            t.b0 = static_cast<int>(static_cast<int64_t>(pair.blocks) * part / parts);
+            t.b1 = static_cast<int>(static_cast<int64_t>(pair.blocks) * (part + 1) / parts);
+            p.tasks[first + k] = t;
+            if (slot >= 0) p.records[slot] = make_int4(pair.row, pair.count, vh, part == 0 ? parts : 0);
+            if (++part == parts) part = 0, ++vh;
+          }
         }
       }
       sum += (static_cast<long long>(tasks) << 32) | (parts > 1 ? tasks : 0);
     }
     if (pass == 0) {
       block_sum(sum, s_warps, total);
+      limit = static_cast<int>(max(static_cast<long long>(kLeastBlocks), min(static_cast<long long>(INT32_MAX), (total * p.vh + p.sms - 1) / p.sms)));
     } else if (pass == 1) {
-      long long all;
-      cost = block_sum(sum, s_warps, all);
-      *results = static_cast<int>(all);
-      if (index >= static_cast<int>(all >> 32)) return false;
-    } else {
-      break;
+      sum = block_sum(sum, s_warps, total);
+      if (tid == 0) s_tasks = static_cast<int>(total >> 32), s_slots = static_cast<int>(total);
+      __syncthreads();
     }
   }
   __syncthreads();
-  return true;
+  if (tid == 0) *p.header = make_int4(s_tasks, s_slots, 0, 0);
 }
 
 // ---- the kernel ------------------------------------------------------------------------
 
+// two fp32 numbers that one instruction works on
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 numbers_of(Two x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // the 8 16-bit operands of a 16-byte piece of a bf16 query row: as they are, or times a power of two as fp16
 template <bool FP8>
 __device__ __forceinline__ uint4 query_piece(uint4 w, float f, uint32_t flip) {
   w.x ^= flip, w.y ^= flip, w.z ^= flip, w.w ^= flip;
-  if constexpr (!FP8) return w;
-  uint32_t r[4];
+  if constexpr (FP8) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t u = (&w.x)[i];
-    const __half2 h = __floats2half2_rn(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xffff0000u) * f);
-    r[i] = *reinterpret_cast<const uint32_t *>(&h);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = (&w.x)[i];
+      const __half2 h = __floats2half2_rn(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xffff0000u) * f);
+      (&w.x)[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
   }
-  return make_uint4(r[0], r[1], r[2], r[3]);
+  return w;
 }
 template <bool FP8>
 __device__ __forceinline__ uint32_t pack_weights(float a, float b) {
@@ -292,25 +334,33 @@ __device__ void row_alone(const PromptParams &p, const Task &task, const Pair &x
 template <bool FP8, int D>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
   using LY = Layout<D>;
+  constexpr int kSlots = LY::SLOTS;
   // over an 8-bit cache weights are fp16 numbers up to 2^15: the running maximum may lag by 1 (log2) behind 2^14; bf16
   // ones may lag by 8
   constexpr float kShift = FP8 ? 14.f : 0.f, kLag = FP8 ? 1.f : 8.f;
   constexpr uint32_t kIdS = FP8 ? idesc_f32(kRows, kBlock) : idesc_bf16_f32(kRows, kBlock);
   constexpr uint32_t kIdO = (FP8 ? idesc_f32(kRows, D) : idesc_bf16_f32(kRows, D)) | kBMajorN;
   extern __shared__ unsigned char smraw[];
-  __shared__ Task s_task;
-  mkw::follow_previous_kernel();
+  mkw::let_next_kernel_start();
   unsigned char *sm = smraw + ((1024u - (smem_addr(smraw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-
-  int results = 0;
-  const bool any = find_task(p, blockIdx.x, reinterpret_cast<int *>(sm + LY::Q), &s_task, &results);
-  if (blockIdx.x == 0 && tid == 0 && p.records) p.records[0] = make_int4(results, 0, 0, 0);
-  if (!any) return;
-  const Task task = s_task;
-  const int start = p.starts[task.seq], length = p.lengths[task.seq];
-  const Pair x = pair_of(p, start, p.starts[task.seq + 1] - start, length, task.pair);
-  const int b0 = static_cast<int>(static_cast<int64_t>(x.blocks) * task.part / task.parts), b1 = static_cast<int>(static_cast<int64_t>(x.blocks) * (task.part + 1) / task.parts);
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm), *empty = full + kSlots, *sfull = empty + kSlots, *pfull = sfull + 2, *ofull = pfull + 2;
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(ofull + 1);
+  unsigned char *Qs = sm + LY::Q, *KVs = sm + LY::KV;
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], kCopyWarps), mbar_init(&empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sfull[i], 1), mbar_init(&pfull[i], 4);
+    mbar_init(ofull, 1);
+    fence_mbar_init();
+  }
+  mkw::wait_for_previous_kernel();
+  const int4 *words = reinterpret_cast<const int4 *>(p.tasks + blockIdx.x);
+  const int4 w0 = words[0], w1 = words[1], w2 = words[2];    // (no more than what the workspace has; not a task's perhaps)
+  if (static_cast<int>(blockIdx.x) >= p.header->x) return;
+  const Task task{w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w, w2.x, w2.y, w2.z, w2.w};
+  const Pair x{task.row, task.count, task.pos, task.lo, task.head, task.skip, 0};
+  const int b0 = task.b0, b1 = task.b1;
+  const bool whole = task.slot < 0;
   const int kvh = task.vh / p.blocks, head0 = kvh * p.group + (task.vh - kvh * p.blocks) * static_cast<int>(p.heads.value);
   const int heads = min(static_cast<int>(p.heads.value), (kvh + 1) * p.group - head0);
   // the positions of a tile's first and last row, and whether any of its rows sees any of block b
@@ -320,17 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     const int from = b * kBlock;
     return x.count > tile * p.tokens && from <= last_of(tile) && (p.window == 0 || from + kBlock - 1 > first_of(tile) - p.window || from < p.sinks);
   };
-
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm), *empty = full + kSlots, *sfull = empty + kSlots, *pfull = sfull + 2, *ofull = pfull + 2;
-  uint32_t *tslot = reinterpret_cast<uint32_t *>(ofull + 2);
-  unsigned char *Qs = sm + LY::Q, *KVs = sm + LY::KV;
-  __syncthreads();                                         // (the sums of find_task were where Q goes)
-  if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], kCopyWarps), mbar_init(&empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&sfull[i], 1), mbar_init(&pfull[i], 4), mbar_init(&ofull[i], 1);
-    fence_mbar_init();
-  }
-  if (warp == kMmaWarp) tmem_alloc(tslot, LY::TMEM_COLS);
+  if (warp == kSoftWarps) tmem_alloc(tslot, LY::TMEM_COLS);
 
   // ---- softmax warps: a thread a row; its query to shared memory --------------------------
   const int tile = warp >> 2, r = (warp & 3) * 32 + lane;
@@ -370,10 +410,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
 
-  if (warp > kMmaWarp) {
+  if (warp > kSoftWarps) {
     // ---- copies: a warp has 32 positions of a block, a lane looks one of them up ------------
     constexpr int ES = FP8 ? 1 : 2, PIECES = D * ES / 16, ROWS = 32 / PIECES;   // 16-byte pieces of a row, rows a copy
-    const int cw = warp - kMmaWarp - 1;
+    const int cw = warp - kSoftWarps - 1;
     int n_tiles = 0, told = 0;                             // tiles asked for, tiles told of
     bool ok = true;
     auto tell = [&](int upto) {
@@ -452,87 +492,108 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
         if constexpr (FP8) {
           tell(n_tiles + 1);
-        } else if (n_tiles >= 2) {
-          mkw::cp_async_wait<2>();
-          tell(n_tiles - 1);
+        } else if (n_tiles >= 1) {
+          mkw::cp_async_wait<1>();
+          tell(n_tiles);
         }
       }
     }
     if constexpr (!FP8) mkw::cp_async_wait<0>();
     if (ok) tell(n_tiles);
-  } else if (warp == kMmaWarp) {
-    // ---- products: S = Q K^T of a tile, then O += P V with P where S was, so that the next S of the tile comes behind it
+  } else if (warp == kSoftWarps) {
+    // ---- products: S = Q K^T of a tile, then O += P V with P where S was, so that the next S of the tile comes behind it.
+    // The tiles in turn: one is multiplied while the other is in its softmax.  (A warp for each tile took longer: keys and
+    // values then stay until the later one has used them.)
     if (b0 < b1) {
       // descriptors: the low words move with the tile, the high ones are constants
       const uint64_t kd = desc_sw128(smem_addr(KVs)), vd = desc_mn_sw128_at(smem_addr(KVs), kBlock * 128, 1024);
       const uint32_t q_lo = static_cast<uint32_t>(desc_sw128(smem_addr(Qs))), k_lo = static_cast<uint32_t>(kd), v_lo = static_cast<uint32_t>(vd);
       const uint32_t k_hi = static_cast<uint32_t>(kd >> 32), v_hi = static_cast<uint32_t>(vd >> 32);
       bool ok = true;
-      uint32_t pph[2] = {0, 0};
-      bool first[2] = {true, true};
+      uint32_t pphase = 0, begun = 0;                      // a bit for each tile: parity of its weights' barrier, O has been written
+      int slot = 0;                                        // of the next key or value tile, and the parity of its round
+      uint32_t round = 0;
       auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (ok && !__all_sync(0xffffffffu, mbar_test(bar, parity)) && !__all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs))) {
+        if (!__all_sync(0xffffffffu, mbar_test(bar, parity)) && !__all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs))) {
           if (lane == 0) report(p.status, MK_ERR_TIMEOUT);
           ok = false;
         }
-        tc_fence_after();
         return ok;
       };
-      auto scores = [&](int t, int n_tile) {
-        if (elect_one()) {
-          const uint32_t k_at = k_lo + (n_tile % kSlots) * (LY::TILE >> 4), q_at = q_lo + t * (LY::TILE >> 4);
+      auto next = [&]() {
+        if (++slot == kSlots) slot = 0, round ^= 1u;
+      };
+      // bit t: whether any row of tile t sees the block
+      auto seen_by = [&](int blk) { return static_cast<uint32_t>(sees(0, blk)) | static_cast<uint32_t>(sees(1, blk)) << 1; };
+      auto scores = [&](int t, int k_slot, bool last) {
+        const uint32_t k_at = k_lo + k_slot * (LY::TILE >> 4), q_at = q_lo + t * (LY::TILE >> 4);
 #pragma unroll
-          for (int s = 0; s < D / 16; ++s) {
-            const uint32_t off = ((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4;
-            mma_bf16(tmem + t * LY::S_COLS, desc_of(q_at + off, k_hi), desc_of(k_at + off, k_hi), kIdS, s != 0);
-          }
-          mma_commit(&sfull[t]);
+        for (int s = 0; s < D / 16; ++s) {
+          const uint32_t off = ((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4;
+          mma_bf16(tmem + t * LY::S_COLS, desc_of(q_at + off, k_hi), desc_of(k_at + off, k_hi), kIdS, s != 0);
+        }
+        mma_commit(&sfull[t]);
+        if (last) mma_commit(&empty[k_slot]);
+      };
+      uint32_t seen = seen_by(x.number(b0));
+      if (wait(&full[0], 0)) {
+        tc_fence_after();
+        if (elect_one()) {
+          if (seen & 1) scores(0, 0, false);
+          if (seen & 2) scores(1, 0, false);
+          mma_commit(&empty[0]);
         }
         __syncwarp();
-      };
-      auto release = [&](int n_tile) {
-        if (elect_one()) mma_commit(&empty[n_tile % kSlots]);
-        __syncwarp();
-      };
-      if (wait(&full[0], 0)) {
-        for (int t = 0; t < 2; ++t)
-          if (sees(t, x.number(b0))) scores(t, 0);
-        release(0);
+        next();
       }
       for (int b = b0; b < b1 && ok; ++b) {
-        const int j = b - b0, vt = 2 * j + 1, kt = 2 * j + 2;
-        if (!wait(&full[vt % kSlots], (vt / kSlots) & 1)) break;
         const bool more = b + 1 < b1;
+        const uint32_t then = more ? seen_by(x.number(b + 1)) : 0u;
+        const int v_slot = slot;
+        if (!wait(&full[v_slot], round)) break;
+        next();
+        bool keys = false;
+#pragma unroll
         for (int t = 0; t < 2 && ok; ++t) {
-          if (sees(t, x.number(b))) {
-            if (!wait(&pfull[t], pph[t])) break;
-            pph[t] ^= 1;
-            if (elect_one()) {
-              const uint32_t v_at = v_lo + (vt % kSlots) * (LY::TILE >> 4);
+          if (seen >> t & 1) {
+            if (!wait(&pfull[t], pphase >> t & 1)) break;
+            pphase ^= 1u << t;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            if (seen >> t & 1) {
+              const uint32_t v_at = v_lo + v_slot * (LY::TILE >> 4);
 #pragma unroll
               for (int s = 0; s < kBlock / 16; ++s)
-                mma_f16_ta(tmem + LY::O_COL + t * D, tmem + t * LY::S_COLS + s * 8, desc_of(v_at + s * (2048 >> 4), v_hi), kIdO, !(first[t] && s == 0));
+                mma_f16_ta(tmem + LY::O_COL + t * D, tmem + t * LY::S_COLS + s * 8, desc_of(v_at + s * (2048 >> 4), v_hi), kIdO, (begun >> t & 1) || s != 0);
+            }
+            if (t == 1) mma_commit(&empty[v_slot]);
+          }
+          __syncwarp();
+          begun |= seen & (1u << t);
+          if (more) {
+            if (!keys && !wait(&full[slot], round)) break;
+            keys = true;
+            tc_fence_after();
+            if (elect_one()) {
+              if (then >> t & 1) scores(t, slot, t == 1);
+              else if (t == 1) mma_commit(&empty[slot]);
             }
             __syncwarp();
-            first[t] = false;
           }
-          if (more && sees(t, x.number(b + 1)) && wait(&full[kt % kSlots], (kt / kSlots) & 1)) scores(t, kt);
         }
-        if (more && !wait(&full[kt % kSlots], (kt / kSlots) & 1)) break;
-        release(vt);
-        if (more) release(kt);
+        if (more) next();
+        seen = then;
       }
-      if (elect_one()) mma_commit(&ofull[0]);              // all of it is done (also where a wait ran out)
+      if (elect_one()) mma_commit(ofull);                  // all of it is done (also where a wait ran out)
       __syncwarp();
-      mbar_wait(&ofull[0], 0, kWaitNs);
-      if (lane == 0) mbar_arrive(&ofull[1]);
+      mbar_wait(ofull, 0, kWaitNs);
     }
   } else {
     // ---- softmax ---------------------------------------------------------------------------
     const int pos = first_of(tile) + token;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t s_at = tmem + lanes + tile * LY::S_COLS, o_at = tmem + lanes + LY::O_COL + tile * D;
-    // the warp's rows see all of a block whose positions are in [row_lo, row_hi] (or first tokens up to it)
     const int hidden_below = p.window > 0 ? pos - p.window : -1;   // hidden: at <= hidden_below and not a first token
     float m = -INFINITY, l = 0.f;                          // m: of scores before to_log2
     uint32_t phase = 0;
@@ -540,37 +601,38 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     for (int b = b0; b < b1 && ok; ++b) {
       const int blk = x.number(b);
       if (!sees(tile, blk)) continue;
-      if (!__all_sync(0xffffffffu, mbar_wait(&sfull[tile], phase, kWaitNs))) {
+      if (!__all_sync(0xffffffffu, mbar_test(&sfull[tile], phase)) && !__all_sync(0xffffffffu, mbar_wait(&sfull[tile], phase, kWaitNs))) {
         if (lane == 0) report(p.status, MK_ERR_TIMEOUT);
         ok = false;
         break;
       }
       phase ^= 1;
       tc_fence_after();
+      // the scores twice, 32 at a time, the next ones on their way: all of them would not fit a thread's registers
+      uint32_t u[2][32];
+      tmem_ld32(s_at, u[0]);
       const int from = blk * kBlock;
       const bool edge = __any_sync(0xffffffffu, from + kBlock - 1 > pos || (from <= hidden_below && from + kBlock > p.sinks));
-      auto load = [&](int c, float (&v)[32]) {
-        uint32_t u[32];
-        tmem_ld32(s_at + c, u);
-        tmem_ld_wait(u);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+      auto hide = [&](int c, uint32_t (&v)[32]) {
         if (edge) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int at = from + c + i;
-            if (at > pos || (at <= hidden_below && at >= p.sinks)) v[i] = -INFINITY;
+            if (at > pos || (at <= hidden_below && at >= p.sinks)) v[i] = 0xff800000u;
           }
         }
       };
-      float mx = -INFINITY;
-#pragma unroll 1
-      for (int c = 0; c < kBlock; c += 32) {
-        float v[32];
-        load(c, v);
+      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, v[i]);
+      for (int c = 0; c < kBlock; c += 32) {
+        uint32_t(&now)[32] = u[c / 32 & 1];
+        tmem_ld_wait(now);
+        tmem_ld32(s_at + (c + 32) % kBlock, u[(c / 32 + 1) & 1]);   // (at the end the first ones again)
+        hide(c, now);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) top[i / 2 & 3] = max3(top[i / 2 & 3], __uint_as_float(now[i]), __uint_as_float(now[i + 1]));
       }
+      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
       const bool grows = (mx - m) * to_log2 > kLag;        // (also from -infinity; not if both are)
       if (__any_sync(0xffffffffu, grows)) {
         const float alpha = grows ? mkw::exp2_fast((m - mx) * to_log2) : 1.f;
@@ -579,51 +641,55 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (started) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
-            uint32_t u[32];
-            tmem_ld32(o_at + c, u);
-            tmem_ld_wait(u);
+            uint32_t o[32];
+            tmem_ld32(o_at + c, o);
+            tmem_ld_wait(o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
-            tmem_st32(o_at + c, u);
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(o_at + c, o);
           }
         }
       }
       started = true;
       const float base = m == -INFINITY ? 0.f : fmaf(-m, to_log2, kShift);
-#pragma unroll 1
+      const Two factor = two(to_log2, to_log2), shift = two(base, base);
+      Two sum = two(0.f, 0.f);
+      // P = 2^(S to_log2 + base).  (Some of the exponentials as polynomials on the multipliers, as these have time left in
+      // their own pipe: 12 to 50 % of them took 5 to 28 % longer, for the instructions.)
+#pragma unroll
       for (int c = 0; c < kBlock; c += 32) {
-        float v[32];
-        load(c, v);
+        uint32_t(&now)[32] = u[c / 32 & 1];
+        tmem_ld_wait(now);
+        if (c + 32 < kBlock) tmem_ld32(s_at + c + 32, u[(c / 32 + 1) & 1]);
+        hide(c, now);
         uint32_t w[16];
-        float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float a = mkw::exp2_fast(fmaf(v[2 * i], to_log2, base)), z = mkw::exp2_fast(fmaf(v[2 * i + 1], to_log2, base));
-          sum[0] += a;
-          sum[1] += z;
-          w[i] = pack_weights<FP8>(a, z);
+          float2 f = numbers_of(fma2(two(__uint_as_float(now[2 * i]), __uint_as_float(now[2 * i + 1])), factor, shift));
+          f.x = mkw::exp2_fast(f.x), f.y = mkw::exp2_fast(f.y);
+          sum = add2(sum, two(f.x, f.y));
+          w[i] = pack_weights<FP8>(f.x, f.y);
         }
-        l += sum[0] + sum[1];
-        tmem_st16(s_at + c / 2, w);
+        tmem_st16(s_at + c / 2, w);                        // (over scores that have been read)
       }
+      const float2 both = numbers_of(sum);
+      l += both.x + both.y;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&pfull[tile]);
     }
     // ---- results ------------------------------------------------------------------------------
-    if (b0 < b1 && !__all_sync(0xffffffffu, mbar_wait(&ofull[1], 0, kWaitNs))) {
+    if (b0 < b1 && !__all_sync(0xffffffffu, mbar_wait(ofull, 0, kWaitNs))) {
       if (lane == 0) report(p.status, MK_ERR_TIMEOUT);
       ok = false;
     }
     tc_fence_after();
-    const bool whole = task.parts == 1;
     const float vs = FP8 && p.v_scale ? p.v_scale[kvh] : 1.f;
-    const bool outside = length > p.capacity;              // a sequence longer than its row of the table
-    if (outside && lane == 0) report(p.status, MK_ERR_BAD_PAGE);
-    float *part = whole ? nullptr : p.parts + (static_cast<int64_t>(task.slot) * 2 * kRows + tile * kRows + r) * (D + 4);
+    if (task.outside && lane == 0) report(p.status, MK_ERR_BAD_PAGE);
+    float *part = whole ? nullptr : p.parts + (static_cast<int64_t>(task.slot) * 2 + tile) * (D + 2) * kRows + r;
     __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (x.row + index) * p.out_row + (head0 + head) * p.out_head;
-    const float inv = outside || !ok ? NAN : !whole ? 1.f : l == 0.f ? 0.f : __frcp_rn(l) * vs;
+    const float inv = task.outside || !ok ? NAN : !whole ? 1.f : l == 0.f ? 0.f : __frcp_rn(l) * vs;
     bool strange = false;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
@@ -638,31 +704,42 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         y[i] = (started && ok && l != 0.f ? __uint_as_float(u[i]) : 0.f) * inv;
         strange |= !(fabsf(y[i]) < INFINITY);
       }
-      if (live) {
-        if (whole) {
+      if (whole) {
+        // to where the warp's queries were, from there row by row
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4 *>(dst + c + 8 * i) =
-                make_uint4(pack_weights<false>(y[8 * i], y[8 * i + 1]), pack_weights<false>(y[8 * i + 2], y[8 * i + 3]),
-                           pack_weights<false>(y[8 * i + 4], y[8 * i + 5]), pack_weights<false>(y[8 * i + 6], y[8 * i + 7]));
-        } else {
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4 *>(Qs + tile * LY::TILE + piece_at(r, c / 8 + i)) =
+              make_uint4(pack_weights<false>(y[8 * i], y[8 * i + 1]), pack_weights<false>(y[8 * i + 2], y[8 * i + 3]),
+                         pack_weights<false>(y[8 * i + 4], y[8 * i + 5]), pack_weights<false>(y[8 * i + 6], y[8 * i + 7]));
+      } else if (live) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4 *>(part + c + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-        }
+        for (int i = 0; i < 32; ++i) part[(c + i) * kRows] = y[i];
+      }
+    }
+    if (whole) {
+      constexpr int PIECES = D / 8, ROWS = 32 / PIECES;
+      const unsigned alive = __ballot_sync(0xffffffffu, live);
+      const uint64_t to = reinterpret_cast<uint64_t>(dst);
+#pragma unroll 4
+      for (int i = 0; i < 32; i += ROWS) {
+        const int rr = i + lane / PIECES, c = lane % PIECES;
+        const uint64_t row_at = __shfl_sync(0xffffffffu, to, rr);
+        const uint4 w = *reinterpret_cast<const uint4 *>(Qs + tile * LY::TILE + piece_at((warp & 3) * 32 + rr, c));
+        if (alive >> rr & 1) *reinterpret_cast<uint4 *>(row_at + c * 16) = w;
       }
     }
     m = m == -INFINITY ? m : m * to_log2 - kShift;         // log2 units, as the sum is scaled
-    if (outside || !ok) m = l = NAN;
+    if (task.outside || !ok) m = l = NAN;
     if (live) {
-      if (!whole) part[D] = m, part[D + 1] = l;
+      if (!whole) part[D * kRows] = m, part[(D + 1) * kRows] = l;
       else if (p.lse) p.lse[static_cast<int64_t>(x.row + index) * p.hq + head0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     }
     strange |= !(fabsf(l) < INFINITY);
-    for (unsigned rest = __ballot_sync(0xffffffffu, strange && live && ok && !outside); rest; rest &= rest - 1u) {
-      const int from = __ffs(rest) - 1;
-      const int row = x.row + __shfl_sync(0xffffffffu, index, from), hd = head0 + __shfl_sync(0xffffffffu, head, from);
+    for (unsigned rest = __ballot_sync(0xffffffffu, strange && live && ok && !task.outside); rest; rest &= rest - 1u) {
+      const int of = __ffs(rest) - 1;
+      const int row = x.row + __shfl_sync(0xffffffffu, index, of), hd = head0 + __shfl_sync(0xffffffffu, head, of);
       float rm, rl, o[D / 32], shrink;
-      row_alone<FP8, D>(p, task, x, b0, b1, row, hd, __shfl_sync(0xffffffffu, pos, from), lane, rm, rl, o, shrink);
+      row_alone<FP8, D>(p, task, x, b0, b1, row, hd, __shfl_sync(0xffffffffu, pos, of), lane, rm, rl, o, shrink);
       // (the sum is of weights times shrink: as many log2 units less for the maximum)
       const float grow = 1.f / shrink;
       if (whole) {
@@ -672,69 +749,74 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int i = 0; i < D / 32; ++i) to[i] = __float2bfloat16_rn(o[i] * f * vs);
         if (lane == 0 && p.lse) p.lse[static_cast<int64_t>(row) * p.hq + hd] = rl == 0.f ? -INFINITY : (rm + log2f(rl * grow)) * 0.69314718055994531f;
       } else {
-        float *to = p.parts + (static_cast<int64_t>(task.slot) * 2 * kRows + tile * kRows + (warp & 3) * 32 + from) * (D + 4);
+        float *to = p.parts + (static_cast<int64_t>(task.slot) * 2 + tile) * (D + 2) * kRows + (warp & 3) * 32 + of;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) to[lane * (D / 32) + i] = o[i];
-        if (lane == 0) to[D] = rm + log2f(grow), to[D + 1] = rl;
+        for (int i = 0; i < D / 32; ++i) to[(lane * (D / 32) + i) * kRows] = o[i];
+        if (lane == 0) to[D * kRows] = rm + log2f(grow), to[(D + 1) * kRows] = rl;
       }
     }
-    if (!whole && tid == 0) p.records[1 + task.slot] = make_int4(x.row, x.count, task.vh, task.part == 0 ? task.parts : 0);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, LY::TMEM_COLS);
+  if (warp == kSoftWarps) tmem_dealloc(tmem, LY::TMEM_COLS);
 }
 
-// Joins the parts of an item, a row a warp: CTA (c, y) takes rows y 8 .. of the item whose first part is partial result c.
-constexpr int kJoinWarps = 8;
+// Joins the parts of an item, in order, a row a thread: CTA (c, y) takes 32 elements of the rows of tile y of the item whose
+// first part is partial result c.
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ PromptParams p) {
-  constexpr int E = D / 32;
+__global__ void __launch_bounds__(kRows) join_kernel(const __grid_constant__ PromptParams p) {
   mkw::follow_previous_kernel();
-  if (static_cast<int>(blockIdx.x) >= p.records[0].x) return;
-  const int4 rec = p.records[1 + blockIdx.x];
+  if (static_cast<int>(blockIdx.x) >= p.header->y) return;
+  const int4 rec = p.records[blockIdx.x];
   if (rec.w == 0) return;
-  const int lane = threadIdx.x & 31;
+  const int tile = blockIdx.y & 1, c = (blockIdx.y >> 1) * 32, r = threadIdx.x;
   const int kvh = rec.z / p.blocks, head0 = kvh * p.group + (rec.z - kvh * p.blocks) * static_cast<int>(p.heads.value);
   const int heads = min(static_cast<int>(p.heads.value), (kvh + 1) * p.group - head0);
-  const float vs = p.v_scale ? p.v_scale[kvh] : 1.f;
-  for (int i = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); i < 2 * kRows; i += gridDim.y * kJoinWarps) {
-    const int r = i % kRows, token = p.heads.quotient(r), head = r - token * static_cast<int>(p.heads.value), index = i / kRows * p.tokens + token;
-    if (token >= p.tokens || head >= heads || index >= rec.y) continue;
-    const float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 * kRows + i) * (D + 4);
-    float m = -INFINITY, l = 0.f, o[E] = {};
-#pragma unroll 2
-    for (int j = 0; j < rec.w; ++j, part += 2 * kRows * (D + 4)) {
-      const float mj = part[D], lj = part[D + 1];
-      float x[E];
+  const int token = p.heads.quotient(r), head = r - token * static_cast<int>(p.heads.value), index = tile * p.tokens + token;
+  if (token >= p.tokens || head >= heads || index >= rec.y) return;
+  const float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + tile) * (D + 2) * kRows + r;
+  float m = -INFINITY, l = 0.f, o[32] = {};
+  for (int j = 0; j < rec.w; ++j, part += 2 * (D + 2) * kRows) {
+    const float mj = part[D * kRows], lj = part[(D + 1) * kRows];
+    float x[32];
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = part[lane * E + e];
-      const float mx = fmaxf(m, mj), base = mx == -INFINITY ? 0.f : mx, f = mkw::exp2_fast(m - base), fj = mkw::exp2_fast(mj - base);
-      m = mx;
-      l = l * f + lj * fj;
+    for (int e = 0; e < 32; ++e) x[e] = part[(c + e) * kRows];
+    const float mx = fmaxf(m, mj), base = mx == -INFINITY ? 0.f : mx, f = mkw::exp2_fast(m - base), fj = mkw::exp2_fast(mj - base);
+    m = mx;
+    l = l * f + lj * fj;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * f + x[e] * fj;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l * vs;
-    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (rec.x + index) * p.out_row + (head0 + head) * p.out_head + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) dst[e] = __float2bfloat16_rn(o[e] * inv);
-    if (lane == 0 && p.lse) p.lse[static_cast<int64_t>(rec.x + index) * p.hq + head0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    for (int e = 0; e < 32; ++e) o[e] = o[e] * f + x[e] * fj;
   }
+  const float inv = l == 0.f ? 0.f : 1.f / l * (p.v_scale ? p.v_scale[kvh] : 1.f);
+  __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (rec.x + index) * p.out_row + (head0 + head) * p.out_head + c;
+#pragma unroll
+  for (int e = 0; e < 32; e += 8)
+    *reinterpret_cast<uint4 *>(dst + e) = make_uint4(pack_weights<false>(o[e] * inv, o[e + 1] * inv), pack_weights<false>(o[e + 2] * inv, o[e + 3] * inv),
+                                                     pack_weights<false>(o[e + 4] * inv, o[e + 5] * inv), pack_weights<false>(o[e + 6] * inv, o[e + 7] * inv));
+  if (c == 0 && p.lse) p.lse[static_cast<int64_t>(rec.x + index) * p.hq + head0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 template <bool FP8, int D>
-int launch(PromptParams &p, bool joins, int ctas, int dev, cudaStream_t s) {
-  static mkw::Ready ready[mkw::kMaxDevices];
+int launch(PromptParams &p, int dev, cudaStream_t s) {
+  static mkw::Ready ready[mkw::kMaxDevices], tasks_ready[mkw::kMaxDevices];
   const auto fn = &prompt_kernel<FP8, D>;
-  static_assert((kMaxSequences + 1) * 4 <= 2 * Layout<64>::TILE + kSlots * Layout<64>::TILE, "find_task's sums");
-  if (!ready[dev].get(reinterpret_cast<const void *>(fn), kThreads, Layout<D>::SMEM)) return MK_ERR_CUDA;
-  const int rc = mkw::launch_after(fn, dim3(ctas), kThreads, Layout<D>::SMEM, s, p);
-  if (rc != MK_OK || !joins) return rc;
-  return mkw::launch_after(&join_kernel<D>, dim3(2 * p.sms, 2 * kRows / kJoinWarps / 4), 32 * kJoinWarps, 0, s, p);
+  const auto tasks = &task_kernel;
+  if (!ready[dev].get(reinterpret_cast<const void *>(fn), kThreads, Layout<D>::SMEM) ||
+      !tasks_ready[dev].get(reinterpret_cast<const void *>(tasks), kTaskThreads, (kMaxSequences + 1) * 4))
+    return MK_ERR_CUDA;
+  int rc = mkw::launch_after(tasks, dim3(1), kTaskThreads, (p.n + 1) * 4, s, p);
+  if (rc == MK_OK) rc = mkw::launch_after(fn, dim3(p.ctas), kThreads, Layout<D>::SMEM, s, p);
+  if (rc != MK_OK || !p.joins) return rc;
+  return mkw::launch_after(&join_kernel<D>, dim3(2 * p.sms, 2 * D / 32), kRows, 0, s, p);
 }
 
-int64_t workspace_bytes(int sms, int d) { return (1 + 2 * static_cast<int64_t>(sms)) * 16 + 2 * static_cast<int64_t>(sms) * 2 * kRows * (d + 4) * 4; }
+// pairs of tiles of a call: a sequence has one that is not full
+int64_t pairs_of(int64_t n, int64_t rows, int tokens) { return std::min(rows, rows / (2 * tokens) + n); }
+
+// header, records, tasks (one for each item and for every share of the work one more), partial results
+int64_t workspace_bytes(int sms, int d, int64_t ctas) {
+  return 16 + 2 * static_cast<int64_t>(sms) * 16 + ctas * static_cast<int64_t>(sizeof(Task)) + 2 * static_cast<int64_t>(sms) * 2 * kRows * (d + 2) * 4;
+}
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool stride_ok(int64_t s, int elem) { return s >= 0 && s <= (int64_t{1} << 48) && s * elem % 16 == 0; }
@@ -743,10 +825,29 @@ bool stride_ok(int64_t s, int elem) { return s >= 0 && s <= (int64_t{1} << 48) &
 
 using namespace mkprompt;
 
-extern "C" int64_t mk_paged_prompt_attention_workspace(int32_t head_dim) {
+namespace {
+
+// tokens of a tile, virtual heads, and CTAs of a call; < 0: an error
+struct Shape {
+  int heads, blocks, tokens, vh;
+  int64_t ctas;
+  Shape(int64_t n, int64_t rows, int hq, int hkv, int sms) {
+    const int group = hq / hkv;
+    blocks = (group + kRows - 1) / kRows;
+    heads = (group + blocks - 1) / blocks;
+    tokens = kRows / heads;
+    vh = hkv * blocks;
+    ctas = pairs_of(n, rows, tokens) * vh + sms;
+  }
+};
+
+}  // namespace
+
+extern "C" int64_t mk_paged_prompt_attention_workspace(int32_t n, int32_t rows, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim) {
+  if (n < 0 || rows < 0 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads) return MK_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return MK_ERR_UNSUPPORTED;
   const int sms = mkv::sm_count(nullptr);
-  return sms < 0 ? MK_ERR_CUDA : workspace_bytes(sms, head_dim);
+  return sms < 0 ? MK_ERR_CUDA : workspace_bytes(sms, head_dim, Shape(n, rows, n_q_heads, n_kv_heads, sms).ctas);
 }
 
 namespace {
@@ -778,35 +879,35 @@ int prompt_attention(const mk_paged_kv *kv, const mk_prompt_args *a, mk_stream s
   p.page_size.set(kv->page_size);
   p.n = a->n, p.rows = a->rows, p.hq = a->n_q_heads, p.hkv = kv->n_kv_heads;
   p.group = p.hq / p.hkv;
-  p.blocks = (p.group + kRows - 1) / kRows;
-  const int heads = (p.group + p.blocks - 1) / p.blocks;
-  p.heads.set(heads);
-  p.vh = p.hkv * p.blocks;
-  p.tokens = kRows / heads;
+  const Shape shape(a->n, a->rows, p.hq, p.hkv, sms);
+  p.blocks = shape.blocks;
+  p.heads.set(shape.heads);
+  p.vh = shape.vh;
+  p.tokens = shape.tokens;
   p.n_pages = kv->n_pages;
   p.capacity = static_cast<int>(slots);
   p.window = a->window;
   p.sinks = a->window > 0 ? std::min(a->sinks, p.capacity) : 0;
   p.sms = sms;
   p.scale = a->scale;
-  // pairs of tiles: a sequence has one that is not full; a task more for every share of the work
-  const int64_t pairs = std::min<int64_t>(a->rows, a->rows / (2 * p.tokens) + a->n), ctas = pairs * p.vh + sms;
-  if (ctas > INT32_MAX) return MK_ERR_UNSUPPORTED;
+  if (shape.ctas > INT32_MAX) return MK_ERR_UNSUPPORTED;
+  p.ctas = static_cast<int>(shape.ctas);
   // blocks of an item: of all its row's tokens, or of the window, its own rows and the first tokens
   const int64_t span = p.window > 0 ? static_cast<int64_t>(p.window) + 2 * p.tokens + p.sinks + 3 * kBlock : slots + kBlock;
-  const bool joins = std::min<int64_t>(span, slots + kBlock) / kBlock > kLeastBlocks;
-  if (joins) {
-    const int64_t bytes = workspace_bytes(sms, kv->head_dim);
-    if (!ask && (!a->workspace || a->workspace_bytes < bytes)) return MK_ERR_INVALID_ARG;
-    p.records = static_cast<int4 *>(ask ? ask(context, bytes) : a->workspace);
-    if (!p.records) return MK_ERR_NO_MEMORY;
-    if (!aligned16(p.records)) return MK_ERR_INVALID_ARG;
-    p.parts = reinterpret_cast<float *>(p.records + 1 + 2 * sms);
-  }
+  p.joins = std::min<int64_t>(span, slots + kBlock) / kBlock > kLeastBlocks;
+  const int64_t bytes = workspace_bytes(sms, kv->head_dim, shape.ctas);
+  if (!ask && (!a->workspace || a->workspace_bytes < bytes)) return MK_ERR_INVALID_ARG;
+  // (what cannot be cut needs no room for partial results)
+  p.header = static_cast<int4 *>(ask ? ask(context, p.joins ? bytes : bytes - (workspace_bytes(sms, kv->head_dim, 0) - workspace_bytes(sms, -2, 0))) : a->workspace);
+  if (!p.header) return MK_ERR_NO_MEMORY;
+  if (!aligned16(p.header)) return MK_ERR_INVALID_ARG;
+  p.records = p.header + 1;
+  p.tasks = reinterpret_cast<Task *>(p.records + 2 * sms);
+  p.parts = reinterpret_cast<float *>(p.tasks + shape.ctas);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (kv->dtype == MK_BF16)
-    return kv->head_dim == 64 ? launch<false, 64>(p, joins, static_cast<int>(ctas), dev, s) : launch<false, 128>(p, joins, static_cast<int>(ctas), dev, s);
-  return kv->head_dim == 64 ? launch<true, 64>(p, joins, static_cast<int>(ctas), dev, s) : launch<true, 128>(p, joins, static_cast<int>(ctas), dev, s);
+    return kv->head_dim == 64 ? launch<false, 64>(p, dev, s) : launch<false, 128>(p, dev, s);
+  return kv->head_dim == 64 ? launch<true, 64>(p, dev, s) : launch<true, 128>(p, dev, s);
 }
 
 }  // namespace

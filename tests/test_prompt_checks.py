@@ -203,7 +203,7 @@ def test_argument_errors_of_the_c_entry_points():
     assert prompt(dtype=0) == -2 and prompt(rows=2 ** 31 - 1) == -2
     assert prompt(B.mk_paged_kv(16, 16, 1, 4, 2, 16, 96, 2048, 1024, 64, None, None, 16, 3, 4, 4)) == -2
     assert prompt(B.mk_paged_kv(16, 16, 1, 4, 2, 16, 64, 2048, 1024, 64, None, None, 16, 3, 2 ** 28, 4), rows=1) == -2
-    assert lib.mk_paged_prompt_attention_workspace(96) == -2
+    assert lib.mk_paged_prompt_attention_workspace(2, 9, 4, 2, 96) == -2 and lib.mk_paged_prompt_attention_workspace(2, 9, 3, 2, 64) == -1
     asked = []
     ask = B.WORKSPACE_FN(lambda context, n: asked.append(n))
     empty = B.mk_prompt_args(n=2, rows=0, dtype=1, n_q_heads=4, q=16, out=16, starts=16, lengths=16, scale=0.125)
