@@ -18,9 +18,10 @@ namespace mkprompt {
 
 using namespace mktc;
 
-constexpr int kSoftWarps = 8, kCopyWarps = 4, kWarps = kSoftWarps + 1 + kCopyWarps, kThreads = 32 * kWarps;
+constexpr int kSoftWarps = 8, kMmaWarps = 2, kCopyWarps = 4, kWarps = kSoftWarps + kMmaWarps + kCopyWarps, kThreads = 32 * kWarps;
 constexpr int kRows = 128;            // of a query tile (the MMA's M); a CTA has two
-constexpr int kBlock = 128;           // cached positions of a step
+constexpr int kBlock = 128;           // cached positions of a key or value tile
+constexpr int kHalf = 64;             // of a softmax step: a thread holds their scores in registers
 constexpr int kMaxSequences = 16384, kTaskThreads = 1024;
 constexpr int kLeastBlocks = 8;       // an item of at most so many blocks is not split
 constexpr long long kWaitNs = 2000000000LL;
@@ -338,19 +339,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   // over an 8-bit cache weights are fp16 numbers up to 2^15: the running maximum may lag by 1 (log2) behind 2^14; bf16
   // ones may lag by 8
   constexpr float kShift = FP8 ? 14.f : 0.f, kLag = FP8 ? 1.f : 8.f;
-  constexpr uint32_t kIdS = FP8 ? idesc_f32(kRows, kBlock) : idesc_bf16_f32(kRows, kBlock);
+  constexpr uint32_t kIdS = FP8 ? idesc_f32(kRows, kHalf) : idesc_bf16_f32(kRows, kHalf);
   constexpr uint32_t kIdO = (FP8 ? idesc_f32(kRows, D) : idesc_bf16_f32(kRows, D)) | kBMajorN;
   extern __shared__ unsigned char smraw[];
   mkw::let_next_kernel_start();
   unsigned char *sm = smraw + ((1024u - (smem_addr(smraw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm), *empty = full + kSlots, *sfull = empty + kSlots, *pfull = sfull + 2, *ofull = pfull + 2;
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm), *empty = full + kSlots, *sfull = empty + kSlots, *pfull = sfull + 4, *odone = pfull + 4, *ofull = odone + 4;   // [tile][half]
   uint32_t *tslot = reinterpret_cast<uint32_t *>(ofull + 1);
   unsigned char *Qs = sm + LY::Q, *KVs = sm + LY::KV;
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], kCopyWarps), mbar_init(&empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&sfull[i], 1), mbar_init(&pfull[i], 4);
-    mbar_init(ofull, 1);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], kCopyWarps), mbar_init(&empty[i], kMmaWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(&sfull[i], 1), mbar_init(&pfull[i], 4), mbar_init(&odone[i], 1);
+    mbar_init(ofull, kMmaWarps);
     fence_mbar_init();
   }
   mkw::wait_for_previous_kernel();
@@ -410,10 +411,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
 
-  if (warp > kSoftWarps) {
+  if (warp >= kSoftWarps + kMmaWarps) {
     // ---- copies: a warp has 32 positions of a block, a lane looks one of them up ------------
     constexpr int ES = FP8 ? 1 : 2, PIECES = D * ES / 16, ROWS = 32 / PIECES;   // 16-byte pieces of a row, rows a copy
-    const int cw = warp - kSoftWarps - 1;
+    const int cw = warp - kSoftWarps - kMmaWarps;
     int n_tiles = 0, told = 0;                             // tiles asked for, tiles told of
     bool ok = true;
     auto tell = [&](int upto) {
@@ -500,17 +501,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     }
     if constexpr (!FP8) mkw::cp_async_wait<0>();
     if (ok) tell(n_tiles);
-  } else if (warp == kSoftWarps) {
-    // ---- products: S = Q K^T of a tile, then O += P V with P where S was, so that the next S of the tile comes behind it.
-    // The tiles in turn: one is multiplied while the other is in its softmax.  (A warp for each tile took longer: keys and
-    // values then stay until the later one has used them.)
+  } else if (warp >= kSoftWarps) {
+    // ---- products: S = Q K^T for half a block of a tile, then O += P V with P where S was, so that the next S there comes
+    // behind it.  A tile has two such places: one is in its softmax while the other is multiplied.
     if (b0 < b1) {
       // descriptors: the low words move with the tile, the high ones are constants
       const uint64_t kd = desc_sw128(smem_addr(KVs)), vd = desc_mn_sw128_at(smem_addr(KVs), kBlock * 128, 1024);
       const uint32_t q_lo = static_cast<uint32_t>(desc_sw128(smem_addr(Qs))), k_lo = static_cast<uint32_t>(kd), v_lo = static_cast<uint32_t>(vd);
       const uint32_t k_hi = static_cast<uint32_t>(kd >> 32), v_hi = static_cast<uint32_t>(vd >> 32);
-      bool ok = true;
-      uint32_t pphase = 0, begun = 0;                      // a bit for each tile: parity of its weights' barrier, O has been written
+      const int t = warp - kSoftWarps;
+      bool ok = true, begun = false;                       // begun: O has been written
+      uint32_t phase = 0;
       int slot = 0;                                        // of the next key or value tile, and the parity of its round
       uint32_t round = 0;
       auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -523,65 +524,51 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       auto next = [&]() {
         if (++slot == kSlots) slot = 0, round ^= 1u;
       };
-      // bit t: whether any row of tile t sees the block
-      auto seen_by = [&](int blk) { return static_cast<uint32_t>(sees(0, blk)) | static_cast<uint32_t>(sees(1, blk)) << 1; };
-      auto scores = [&](int t, int k_slot, bool last) {
-        const uint32_t k_at = k_lo + k_slot * (LY::TILE >> 4), q_at = q_lo + t * (LY::TILE >> 4);
+      auto scores = [&](int h, int k_slot) {
+        const uint32_t k_at = k_lo + ((k_slot * LY::TILE + h * (kHalf * 128)) >> 4), q_at = q_lo + t * (LY::TILE >> 4);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
           const uint32_t off = ((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4;
-          mma_bf16(tmem + t * LY::S_COLS, desc_of(q_at + off, k_hi), desc_of(k_at + off, k_hi), kIdS, s != 0);
+          mma_bf16(tmem + t * LY::S_COLS + h * kHalf, desc_of(q_at + off, k_hi), desc_of(k_at + off, k_hi), kIdS, s != 0);
         }
-        mma_commit(&sfull[t]);
-        if (last) mma_commit(&empty[k_slot]);
+        mma_commit(&sfull[2 * t + h]);
       };
-      uint32_t seen = seen_by(x.number(b0));
+      bool seen = sees(t, x.number(b0));
       if (wait(&full[0], 0)) {
         tc_fence_after();
         if (elect_one()) {
-          if (seen & 1) scores(0, 0, false);
-          if (seen & 2) scores(1, 0, false);
+          if (seen) scores(0, 0), scores(1, 0);
           mma_commit(&empty[0]);
         }
         __syncwarp();
         next();
       }
       for (int b = b0; b < b1 && ok; ++b) {
-        const bool more = b + 1 < b1;
-        const uint32_t then = more ? seen_by(x.number(b + 1)) : 0u;
+        const bool more = b + 1 < b1, then = more && sees(t, x.number(b + 1));
         const int v_slot = slot;
         if (!wait(&full[v_slot], round)) break;
         next();
-        bool keys = false;
 #pragma unroll
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (seen >> t & 1) {
-            if (!wait(&pfull[t], pphase >> t & 1)) break;
-            pphase ^= 1u << t;
-          }
+        for (int h = 0; h < 2; ++h) {
+          if (seen && !wait(&pfull[2 * t + h], phase)) break;
+          if (more && h == 0 && !wait(&full[slot], round)) break;
           tc_fence_after();
           if (elect_one()) {
-            if (seen >> t & 1) {
-              const uint32_t v_at = v_lo + v_slot * (LY::TILE >> 4);
+            if (seen) {
+              const uint32_t v_at = v_lo + ((v_slot * LY::TILE + h * (kHalf * 128)) >> 4);
 #pragma unroll
-              for (int s = 0; s < kBlock / 16; ++s)
-                mma_f16_ta(tmem + LY::O_COL + t * D, tmem + t * LY::S_COLS + s * 8, desc_of(v_at + s * (2048 >> 4), v_hi), kIdO, (begun >> t & 1) || s != 0);
+              for (int s = 0; s < kHalf / 16; ++s)
+                mma_f16_ta(tmem + LY::O_COL + t * D, tmem + t * LY::S_COLS + h * kHalf + s * 8, desc_of(v_at + s * (2048 >> 4), v_hi), kIdO, begun || s != 0);
+              mma_commit(&odone[2 * t + h]);
             }
-            if (t == 1) mma_commit(&empty[v_slot]);
+            if (h == 1) mma_commit(&empty[v_slot]);
+            if (then) scores(h, slot);
+            if (more && h == 1) mma_commit(&empty[slot]);
           }
           __syncwarp();
-          begun |= seen & (1u << t);
-          if (more) {
-            if (!keys && !wait(&full[slot], round)) break;
-            keys = true;
-            tc_fence_after();
-            if (elect_one()) {
-              if (then >> t & 1) scores(t, slot, t == 1);
-              else if (t == 1) mma_commit(&empty[slot]);
-            }
-            __syncwarp();
-          }
+          begun |= seen;
         }
+        if (seen) phase ^= 1u;
         if (more) next();
         seen = then;
       }
@@ -596,88 +583,84 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     const uint32_t s_at = tmem + lanes + tile * LY::S_COLS, o_at = tmem + lanes + LY::O_COL + tile * D;
     const int hidden_below = p.window > 0 ? pos - p.window : -1;   // hidden: at <= hidden_below and not a first token
     float m = -INFINITY, l = 0.f;                          // m: of scores before to_log2
-    uint32_t phase = 0;
+    uint32_t phase = 0;                                    // parity of the blocks that the tile has seen
     bool started = false, ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      if (!__all_sync(0xffffffffu, mbar_test(bar, parity)) && !__all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs))) {
+        if (lane == 0) report(p.status, MK_ERR_TIMEOUT);
+        ok = false;
+      }
+      tc_fence_after();
+      return ok;
+    };
     for (int b = b0; b < b1 && ok; ++b) {
       const int blk = x.number(b);
       if (!sees(tile, blk)) continue;
-      if (!__all_sync(0xffffffffu, mbar_test(&sfull[tile], phase)) && !__all_sync(0xffffffffu, mbar_wait(&sfull[tile], phase, kWaitNs))) {
-        if (lane == 0) report(p.status, MK_ERR_TIMEOUT);
-        ok = false;
-        break;
-      }
-      phase ^= 1;
-      tc_fence_after();
-      // the scores twice, 32 at a time, the next ones on their way: all of them would not fit a thread's registers
-      uint32_t u[2][32];
-      tmem_ld32(s_at, u[0]);
-      const int from = blk * kBlock;
-      const bool edge = __any_sync(0xffffffffu, from + kBlock - 1 > pos || (from <= hidden_below && from + kBlock > p.sinks));
-      auto hide = [&](int c, uint32_t (&v)[32]) {
+#pragma unroll 1
+      for (int h = 0; h < 2 && ok; ++h) {
+        if (!wait(&sfull[2 * tile + h], phase)) break;
+        uint32_t u[2][32];
+        tmem_ld32(s_at + h * kHalf, u[0]);
+        tmem_ld32(s_at + h * kHalf + 32, u[1]);
+        const int from = blk * kBlock + h * kHalf;
+        const bool edge = __any_sync(0xffffffffu, from + kHalf - 1 > pos || (from <= hidden_below && from + kHalf > p.sinks));
+        tmem_ld_wait(u[0]);
+        tmem_ld_wait(u[1]);
         if (edge) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int at = from + c + i;
-            if (at > pos || (at <= hidden_below && at >= p.sinks)) v[i] = 0xff800000u;
+          for (int i = 0; i < kHalf; ++i) {
+            const int at = from + i;
+            if (at > pos || (at <= hidden_below && at >= p.sinks)) u[i / 32][i % 32] = 0xff800000u;
           }
         }
-      };
-      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < kBlock; c += 32) {
-        uint32_t(&now)[32] = u[c / 32 & 1];
-        tmem_ld_wait(now);
-        tmem_ld32(s_at + (c + 32) % kBlock, u[(c / 32 + 1) & 1]);   // (at the end the first ones again)
-        hide(c, now);
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) top[i / 2 & 3] = max3(top[i / 2 & 3], __uint_as_float(now[i]), __uint_as_float(now[i + 1]));
-      }
-      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      const bool grows = (mx - m) * to_log2 > kLag;        // (also from -infinity; not if both are)
-      if (__any_sync(0xffffffffu, grows)) {
-        const float alpha = grows ? mkw::exp2_fast((m - mx) * to_log2) : 1.f;
-        if (grows) m = mx;
-        l *= alpha;
-        if (started) {
+        for (int i = 0; i < kHalf; i += 2) top[i / 2 & 3] = max3(top[i / 2 & 3], __uint_as_float(u[i / 32][i % 32]), __uint_as_float(u[i / 32][i % 32 + 1]));
+        const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
+        const bool grows = (mx - m) * to_log2 > kLag;      // (also from -infinity; not if both are)
+        if (__any_sync(0xffffffffu, grows)) {
+          const float alpha = grows ? mkw::exp2_fast((m - mx) * to_log2) : 1.f;
+          if (grows) m = mx;
+          l *= alpha;
+          if (started) {
+            if (!wait(&odone[2 * tile + 1 - h], h ? phase : phase ^ 1u)) break;   // (the product of the half before may be on its way)
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_at + c, o);
-            tmem_ld_wait(o);
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_at + c, o);
+              tmem_ld_wait(o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(o_at + c, o);
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(o_at + c, o);
+            }
           }
         }
-      }
-      started = true;
-      const float base = m == -INFINITY ? 0.f : fmaf(-m, to_log2, kShift);
-      const Two factor = two(to_log2, to_log2), shift = two(base, base);
-      Two sum = two(0.f, 0.f);
-      // P = 2^(S to_log2 + base).  (Some of the exponentials as polynomials on the multipliers, as these have time left in
-      // their own pipe: 12 to 50 % of them took 5 to 28 % longer, for the instructions.)
+        started = true;
+        // P = 2^(S to_log2 + base).  (Some of the exponentials as polynomials on the multipliers, as these have time left in
+        // their own pipe: 12 to 50 % of them took 5 to 28 % longer, for the instructions.)
+        const float base = m == -INFINITY ? 0.f : fmaf(-m, to_log2, kShift);
+        const Two factor = two(to_log2, to_log2), shift = two(base, base);
+        Two sum = two(0.f, 0.f);
 #pragma unroll
-      for (int c = 0; c < kBlock; c += 32) {
-        uint32_t(&now)[32] = u[c / 32 & 1];
-        tmem_ld_wait(now);
-        if (c + 32 < kBlock) tmem_ld32(s_at + c + 32, u[(c / 32 + 1) & 1]);
-        hide(c, now);
-        uint32_t w[16];
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float2 f = numbers_of(fma2(two(__uint_as_float(now[2 * i]), __uint_as_float(now[2 * i + 1])), factor, shift));
-          f.x = mkw::exp2_fast(f.x), f.y = mkw::exp2_fast(f.y);
-          sum = add2(sum, two(f.x, f.y));
-          w[i] = pack_weights<FP8>(f.x, f.y);
+          for (int i = 0; i < 16; ++i) {
+            float2 f = numbers_of(fma2(two(__uint_as_float(u[c][2 * i]), __uint_as_float(u[c][2 * i + 1])), factor, shift));
+            f.x = mkw::exp2_fast(f.x), f.y = mkw::exp2_fast(f.y);
+            sum = add2(sum, two(f.x, f.y));
+            w[i] = pack_weights<FP8>(f.x, f.y);
+          }
+          tmem_st16(s_at + h * kHalf + c * 16, w);         // (where the scores were)
         }
-        tmem_st16(s_at + c / 2, w);                        // (over scores that have been read)
+        const float2 both = numbers_of(sum);
+        l += both.x + both.y;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[2 * tile + h]);
       }
-      const float2 both = numbers_of(sum);
-      l += both.x + both.y;
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[tile]);
+      phase ^= 1;
     }
     // ---- results ------------------------------------------------------------------------------
     if (b0 < b1 && !__all_sync(0xffffffffu, mbar_wait(ofull, 0, kWaitNs))) {
