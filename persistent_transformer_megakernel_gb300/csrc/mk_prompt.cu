@@ -381,27 +381,44 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const uint32_t flip = to_log2 < 0.f ? 0x80008000u : 0u;   // a negative factor's sign goes to the query
   to_log2 = fabsf(to_log2);
   if (warp < kSoftWarps) {
-    uint4 w[D / 8];
-    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) + (x.row + index) * p.q_row + (head0 + head) * p.q_head;
+    // a row's bytes together, as they are; where its numbers are to change, each thread then changes its own row's
+    constexpr int PIECES = D / 8, ROWS = 32 / PIECES;
+    unsigned char *mine = Qs + tile * LY::TILE;
+    const uint64_t src = reinterpret_cast<uint64_t>(static_cast<const __nv_bfloat16 *>(p.q) + (live ? (x.row + index) * p.q_row + (head0 + head) * p.q_head : 0));
+    const unsigned alive = __ballot_sync(0xffffffffu, live);
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c) w[c] = live ? *reinterpret_cast<const uint4 *>(src + c * 8) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 32; i += ROWS) {
+      const int rr = i + lane / PIECES, c = lane % PIECES;
+      const uint64_t from = __shfl_sync(0xffffffffu, src, rr);
+      mkw::cp_async16(smem_addr(mine + piece_at((warp & 3) * 32 + rr, c)), reinterpret_cast<const void *>(from + c * 16), alive >> rr & 1);
+    }
+    mkw::cp_async_commit();
+    mkw::cp_async_wait<0>();
+    __syncwarp();
     float f = 1.f;
     if constexpr (FP8) {
       // the row's largest element to [2^13, 2^14): fp16 holds what is at least 2^-38 of it
       float a = 0.f;
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c)
+#pragma unroll 4
+      for (int c = 0; c < PIECES; ++c) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(mine + piece_at(r, c));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t u = (&w[c].x)[i];
+          const uint32_t u = (&w.x)[i];
           a = fmaxf(a, fmaxf(fabsf(__uint_as_float(u << 16)), fabsf(__uint_as_float(u & 0xffff0000u))));
         }
+      }
       const int e = a > 0.f && a < INFINITY ? max(-126, min(126, 13 - ilogbf(a))) : 0;
       f = ldexpf(1.f, e);
       to_log2 *= ldexpf(1.f, -e);
     }
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4 *>(Qs + tile * LY::TILE + piece_at(r, c)) = query_piece<FP8>(w[c], f, flip);
+    if (FP8 || flip) {
+#pragma unroll 4
+      for (int c = 0; c < PIECES; ++c) {
+        uint4 *w = reinterpret_cast<uint4 *>(mine + piece_at(r, c));
+        *w = query_piece<FP8>(*w, f, flip);
+      }
+    }
     fence_to_tensor_cores();
   }
   // (a factor of 0 would make the -infinity of a hidden score NaN; the smallest normal one does what 0 does)
