@@ -22,7 +22,7 @@ constexpr int kSoftWarps = 8, kMmaWarps = 2, kCopyWarps = 4, kWarps = kSoftWarps
 constexpr int kRows = 128;            // of a query tile (the MMA's M); a CTA has two
 constexpr int kBlock = 128;           // cached positions of a key or value tile
 constexpr int kHalf = 64;             // of a softmax step: a thread holds their scores in registers
-constexpr int kMaxSequences = 16384, kTaskThreads = 1024;
+constexpr int kMaxSequences = 16384, kTaskThreads = 256;
 constexpr int kLeastBlocks = 8;       // an item of at most so many blocks is not split
 constexpr long long kWaitNs = 2000000000LL;
 
@@ -44,6 +44,7 @@ struct PromptParams {
   int tokens;                  // of a tile: kRows / heads
   int sms, ctas;               // ctas: of the attention kernel, at least as many as there are tasks
   int joins;                   // whether any item can be cut
+  int direct;                  // no task list: every CTA finds its task
   float scale;
 };
 
@@ -97,117 +98,149 @@ struct __align__(16) Task {
 };
 static_assert(sizeof(Task) == 48, "read as three 16-byte words");
 
-// exclusive sum over the block's threads, and the total
-__device__ __forceinline__ long long block_sum(long long x, long long *warps, long long &total) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  long long s = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += y;
+// parts of an item: part i has blocks begin(i) .. begin(i + 1) - 1
+struct Parts {
+  int count, each, more;
+  __device__ __forceinline__ Parts(int blocks, int limit) {
+    count = blocks > limit ? (blocks - 1) / limit + 1 : 1;
+    each = blocks / count;
+    more = blocks - each * count;
   }
-  __syncthreads();
-  if (lane == 31) warps[w] = s;
-  __syncthreads();
-  total = 0;
-  long long before = 0;
-#pragma unroll
-  for (int i = 0; i < kTaskThreads / 32; ++i) {
-    if (i < w) before += warps[i];
-    total += warps[i];
-  }
-  return before + s - x;
+  __device__ __forceinline__ int begin(int i) const { return i * each + min(i, more); }
+};
+
+// pairs of tiles of sequence i
+__device__ __forceinline__ int pairs_of(const PromptParams &p, int i, bool &bad) {
+  const int a = p.starts[i], b = p.starts[i + 1], length = p.lengths[i];
+  const bool fine = a >= 0 && b >= a && b <= p.rows;
+  bad |= !fine;
+  return fine && length >= 0 ? (b - a + 2 * p.tokens - 1) / (2 * p.tokens) : 0;
 }
 
 // The tasks of a call, in the order of sequences, their last rows (which see most) first; CTA i of the attention kernel takes
 // task i.  Every item (pair of tiles and virtual head) of more blocks than an equal share of all the work is cut into parts.
-// One CTA: a call's lengths are on the device, and every CTA of the other kernel finding its own task took 3.5 us each.
+// One CTA, as a call's lengths are on the device: every CTA of the other kernel finding its own task took 3.5 us each.  Where
+// nothing can be cut and a warp holds all sequences, that is quick, and this kernel is left out.
 __global__ void __launch_bounds__(kTaskThreads) task_kernel(const __grid_constant__ PromptParams p) {
   extern __shared__ int before[];                          // pairs before a sequence: [n + 1]
   __shared__ long long s_warps[kTaskThreads / 32];
   __shared__ int s_tasks, s_slots;
   mkw::follow_previous_kernel();
-  const int tid = threadIdx.x, n = p.n, step = 2 * p.tokens;
+  const int tid = threadIdx.x, lane = tid & 31, n = p.n;
   bool bad = false;
-  for (int i = tid; i < n; i += kTaskThreads) {
-    const int a = p.starts[i], b = p.starts[i + 1], length = p.lengths[i];
-    const bool fine = a >= 0 && b >= a && b <= p.rows;
-    bad |= !fine;
-    before[i] = fine && length >= 0 ? (b - a + step - 1) / step : 0;
-  }
+  for (int i = tid; i < n; i += kTaskThreads) before[i] = pairs_of(p, i, bad);
   if (bad) report(p.status, MK_ERR_BAD_PAGE);
-  __syncthreads();
   const int per = (n + kTaskThreads - 1) / kTaskThreads, a = min(n, tid * per), b = min(n, a + per);
-  int mine = 0;
-  for (int i = a; i < b; ++i) mine += before[i];
-  long long total;
-  int at = static_cast<int>(block_sum(mine, s_warps, total));
-  for (int i = a; i < b; ++i) {
-    const int c = before[i];
-    before[i] = at;
-    at += c;
-  }
-  const int pairs = static_cast<int>(total);
-  if (tid == 0) before[n] = pairs;
+  int p0 = 0, p1 = 0, i0 = 0, limit = INT32_MAX;
+  long long at = 0;
   __syncthreads();
-  const int share = (pairs + kTaskThreads - 1) / kTaskThreads, p0 = min(pairs, tid * share), p1 = min(pairs, p0 + share);
-  int i0 = 0, hi = n;
-  while (hi - i0 > 1) {
-    const int mid = (i0 + hi) >> 1;
-    if (before[mid] <= p0) i0 = mid;
-    else hi = mid;
-  }
-  // pass 0: all blocks; pass 1: tasks and partial results before this thread's; pass 2: the tasks
-  int limit = INT32_MAX;
-  long long sum = 0;
+  // Passes: 0 the pairs before this thread's sequences; then over its share of the pairs 1 their blocks, 2 its tasks (in the
+  // upper half) and partial results, 3 the same written down.  One copy of the loop and of the sum over threads: code that
+  // runs once takes as long as it is.
 #pragma unroll 1
-  for (int pass = p.joins ? 0 : 1; pass < 3; ++pass) {
-    if (pass < 2) sum = 0;
-    int i = i0, start = 0, count = 0, length = 0, of = -1;
-    for (int x = p0; x < p1; ++x) {
-      while (x >= before[i + 1]) ++i;
-      if (of != i) {
-        of = i;
-        start = p.starts[i];
-        count = p.starts[i + 1] - start;
-        length = p.lengths[i];
-      }
-      const Pair pair = pair_of(p, start, count, length, before[i + 1] - 1 - x);
-      if (pass == 0) {
-        sum += pair.blocks;
-        continue;
-      }
-      const int parts = pair.blocks > limit ? (pair.blocks - 1) / limit + 1 : 1, tasks = parts * p.vh;
-      if (pass == 2) {
-        const int first = static_cast<int>(sum >> 32), slots = static_cast<int>(sum);
-        if (first + tasks > p.ctas) {                      // (starts that overlap: what is past the end is not done)
-          atomicMin(&s_tasks, first);
-          atomicMin(&s_slots, slots);
-        } else {
-          for (int k = 0, vh = 0, part = 0; k < tasks; ++k) {
-            const int slot = parts > 1 ? slots + k : -1;
-            Task t{pair.row, pair.count, pair.pos, i, pair.lo, pair.head, pair.skip, vh, 0, 0, slot, length > p.capacity};
-            t.b0 = static_cast<int>(static_cast<int64_t>(pair.blocks) * part / parts);
-            t.b1 = static_cast<int>(static_cast<int64_t>(pair.blocks) * (part + 1) / parts);
-            p.tasks[first + k] = t;
-            if (slot >= 0) p.records[slot] = make_int4(pair.row, pair.count, vh, part == 0 ? parts : 0);
-            if (++part == parts) part = 0, ++vh;
+  for (int pass = 0; pass < 4; ++pass) {
+    if (pass == 1 && !p.joins) continue;
+    long long mine = 0;
+    if (pass == 0) {
+      for (int i = a; i < b; ++i) mine += before[i];
+    } else {
+      int i = i0, start = 0, count = 0, length = 0, of = -1;
+#pragma unroll 1
+      for (int x = p0; x < p1; ++x) {
+        while (x >= before[i + 1]) ++i;
+        if (of != i) {
+          of = i;
+          start = p.starts[i];
+          count = p.starts[i + 1] - start;
+          length = p.lengths[i];
+        }
+        const Pair pair = pair_of(p, start, count, length, before[i + 1] - 1 - x);
+        if (pass == 1) {
+          mine += pair.blocks;
+          continue;
+        }
+        const Parts parts(pair.blocks, limit);
+        const int tasks = parts.count * p.vh;
+        if (pass == 3) {
+          const int first = static_cast<int>((at + mine) >> 32), slots = static_cast<int>(at + mine);
+          if (first + tasks > p.ctas) {                    // (starts that overlap: what is past the end is not done)
+            atomicMin(&s_tasks, first);
+            atomicMin(&s_slots, slots);
+          } else {
+#pragma unroll 1
+            for (int k = 0, vh = 0, part = 0; k < tasks; ++k) {
+              const int slot = parts.count > 1 ? slots + k : -1;
+              p.tasks[first + k] = Task{pair.row, pair.count, pair.pos, i, pair.lo, pair.head, pair.skip, vh, parts.begin(part), parts.begin(part + 1), slot, length > p.capacity};
+              if (slot >= 0) p.records[slot] = make_int4(pair.row, pair.count, vh, part == 0 ? parts.count : 0);
+              if (++part == parts.count) part = 0, ++vh;
+            }
           }
         }
+        mine += (static_cast<long long>(tasks) << 32) | (parts.count > 1 ? tasks : 0);
       }
-      sum += (static_cast<long long>(tasks) << 32) | (parts > 1 ? tasks : 0);
+      if (pass == 3) break;
+    }
+    long long s = mine;                                    // before this thread's, and all
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    if (lane == 31) s_warps[tid >> 5] = s;
+    __syncthreads();
+    long long total = 0;
+    at = s - mine;
+#pragma unroll 1
+    for (int i = 0; i < kTaskThreads / 32; ++i) {
+      if (i < tid >> 5) at += s_warps[i];
+      total += s_warps[i];
     }
     if (pass == 0) {
-      block_sum(sum, s_warps, total);
-      limit = static_cast<int>(max(static_cast<long long>(kLeastBlocks), min(static_cast<long long>(INT32_MAX), (total * p.vh + p.sms - 1) / p.sms)));
-    } else if (pass == 1) {
-      sum = block_sum(sum, s_warps, total);
-      if (tid == 0) s_tasks = static_cast<int>(total >> 32), s_slots = static_cast<int>(total);
+      int pairs = static_cast<int>(at);
+      for (int i = a; i < b; ++i) {
+        const int c = before[i];
+        before[i] = pairs;
+        pairs += c;
+      }
+      pairs = static_cast<int>(total);
+      if (tid == 0) before[n] = pairs;
       __syncthreads();
+      const int share = (pairs + kTaskThreads - 1) / kTaskThreads;
+      p0 = min(pairs, tid * share), p1 = min(pairs, p0 + share);
+      for (int hi = n; hi - i0 > 1;) {                     // the sequence of the first of them
+        const int mid = (i0 + hi) >> 1;
+        if (before[mid] <= p0) i0 = mid;
+        else hi = mid;
+      }
+    } else if (pass == 1) {
+      limit = static_cast<int>(max(static_cast<long long>(kLeastBlocks), min(static_cast<long long>(INT32_MAX), (total * p.vh + p.sms - 1) / p.sms)));
+    } else if (tid == 0) {
+      s_tasks = static_cast<int>(total >> 32), s_slots = static_cast<int>(total);
     }
+    __syncthreads();
   }
   __syncthreads();
   if (tid == 0) *p.header = make_int4(s_tasks, s_slots, 0, 0);
+}
+
+// Task `index` of a call whose items are whole and whose sequences a warp holds, by every warp; count 0: there is none.
+__device__ __forceinline__ Task find_task(const PromptParams &p, int index, int lane) {
+  bool bad = false;
+  const int pairs = lane < p.n ? pairs_of(p, lane, bad) : 0;
+  if (__any_sync(0xffffffffu, bad) && index == 0) report(p.status, MK_ERR_BAD_PAGE);
+  int upto = pairs;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const int x = index / p.vh;
+  const unsigned behind = __ballot_sync(0xffffffffu, upto > x);
+  if (!behind) return Task{};
+  const int i = __ffs(behind) - 1, t = __shfl_sync(0xffffffffu, upto, i) - 1 - x;
+  const int start = p.starts[i], length = p.lengths[i];
+  const Pair pair = pair_of(p, start, p.starts[i + 1] - start, length, t);
+  return Task{pair.row, pair.count, pair.pos, i, pair.lo, pair.head, pair.skip, index - x * p.vh, 0, pair.blocks, -1, length > p.capacity};
 }
 
 // ---- the kernel ------------------------------------------------------------------------
@@ -355,10 +388,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     fence_mbar_init();
   }
   mkw::wait_for_previous_kernel();
-  const int4 *words = reinterpret_cast<const int4 *>(p.tasks + blockIdx.x);
-  const int4 w0 = words[0], w1 = words[1], w2 = words[2];    // (no more than what the workspace has; not a task's perhaps)
-  if (static_cast<int>(blockIdx.x) >= p.header->x) return;
-  const Task task{w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w, w2.x, w2.y, w2.z, w2.w};
+  Task task;
+  if (p.direct) {
+    task = find_task(p, blockIdx.x, lane);
+  } else {
+    const int4 *words = reinterpret_cast<const int4 *>(p.tasks + blockIdx.x);
+    const int4 w0 = words[0], w1 = words[1], w2 = words[2];  // (no more than what the workspace has; not a task's perhaps)
+    task = Task{w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w, w2.x, w2.y, w2.z, w2.w};
+    if (static_cast<int>(blockIdx.x) >= p.header->x) task.count = 0;
+  }
+  if (task.count == 0) return;
   const Pair x{task.row, task.count, task.pos, task.lo, task.head, task.skip, 0};
   const int b0 = task.b0, b1 = task.b1;
   const bool whole = task.slot < 0;
@@ -804,18 +843,19 @@ int launch(PromptParams &p, int dev, cudaStream_t s) {
   if (!ready[dev].get(reinterpret_cast<const void *>(fn), kThreads, Layout<D>::SMEM) ||
       !tasks_ready[dev].get(reinterpret_cast<const void *>(tasks), kTaskThreads, (kMaxSequences + 1) * 4))
     return MK_ERR_CUDA;
-  int rc = mkw::launch_after(tasks, dim3(1), kTaskThreads, (p.n + 1) * 4, s, p);
+  int rc = p.direct ? MK_OK : mkw::launch_after(tasks, dim3(1), kTaskThreads, (p.n + 1) * 4, s, p);
   if (rc == MK_OK) rc = mkw::launch_after(fn, dim3(p.ctas), kThreads, Layout<D>::SMEM, s, p);
   if (rc != MK_OK || !p.joins) return rc;
   return mkw::launch_after(&join_kernel<D>, dim3(2 * p.sms, 2 * D / 32), kRows, 0, s, p);
 }
 
 // pairs of tiles of a call: a sequence has one that is not full
-int64_t pairs_of(int64_t n, int64_t rows, int tokens) { return std::min(rows, rows / (2 * tokens) + n); }
+int64_t most_pairs(int64_t n, int64_t rows, int tokens) { return std::min(rows, rows / (2 * tokens) + n); }
 
+int64_t parts_bytes(int sms, int d) { return 2 * static_cast<int64_t>(sms) * 2 * kRows * (d + 2) * 4; }
 // header, records, tasks (one for each item and for every share of the work one more), partial results
 int64_t workspace_bytes(int sms, int d, int64_t ctas) {
-  return 16 + 2 * static_cast<int64_t>(sms) * 16 + ctas * static_cast<int64_t>(sizeof(Task)) + 2 * static_cast<int64_t>(sms) * 2 * kRows * (d + 2) * 4;
+  return 16 + 2 * static_cast<int64_t>(sms) * 16 + ctas * static_cast<int64_t>(sizeof(Task)) + parts_bytes(sms, d);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -837,7 +877,7 @@ struct Shape {
     heads = (group + blocks - 1) / blocks;
     tokens = kRows / heads;
     vh = hkv * blocks;
-    ctas = pairs_of(n, rows, tokens) * vh + sms;
+    ctas = most_pairs(n, rows, tokens) * vh + sms;
   }
 };
 
@@ -895,15 +935,19 @@ int prompt_attention(const mk_paged_kv *kv, const mk_prompt_args *a, mk_stream s
   // blocks of an item: of all its row's tokens, or of the window, its own rows and the first tokens
   const int64_t span = p.window > 0 ? static_cast<int64_t>(p.window) + 2 * p.tokens + p.sinks + 3 * kBlock : slots + kBlock;
   p.joins = std::min<int64_t>(span, slots + kBlock) / kBlock > kLeastBlocks;
+  // (77 tokens: TODO us, with a task list TODO; the same 32 times TODO and TODO)
+  p.direct = !p.joins && p.n <= 32;
   const int64_t bytes = workspace_bytes(sms, kv->head_dim, shape.ctas);
   if (!ask && (!a->workspace || a->workspace_bytes < bytes)) return MK_ERR_INVALID_ARG;
-  // (what cannot be cut needs no room for partial results)
-  p.header = static_cast<int4 *>(ask ? ask(context, p.joins ? bytes : bytes - (workspace_bytes(sms, kv->head_dim, 0) - workspace_bytes(sms, -2, 0))) : a->workspace);
-  if (!p.header) return MK_ERR_NO_MEMORY;
-  if (!aligned16(p.header)) return MK_ERR_INVALID_ARG;
-  p.records = p.header + 1;
-  p.tasks = reinterpret_cast<Task *>(p.records + 2 * sms);
-  p.parts = reinterpret_cast<float *>(p.tasks + shape.ctas);
+  if (!p.direct) {
+    // (what cannot be cut needs no room for partial results)
+    p.header = static_cast<int4 *>(ask ? ask(context, p.joins ? bytes : bytes - parts_bytes(sms, kv->head_dim)) : a->workspace);
+    if (!p.header) return MK_ERR_NO_MEMORY;
+    if (!aligned16(p.header)) return MK_ERR_INVALID_ARG;
+    p.records = p.header + 1;
+    p.tasks = reinterpret_cast<Task *>(p.records + 2 * sms);
+    p.parts = reinterpret_cast<float *>(p.tasks + shape.ctas);
+  }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (kv->dtype == MK_BF16)
     return kv->head_dim == 64 ? launch<false, 64>(p, dev, s) : launch<false, 128>(p, dev, s);
