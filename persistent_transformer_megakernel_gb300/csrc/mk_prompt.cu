@@ -146,37 +146,52 @@ __global__ void __launch_bounds__(kTaskThreads) task_kernel(const __grid_constan
     } else {
       int i = i0, start = 0, count = 0, length = 0, of = -1;
 #pragma unroll 1
-      for (int x = p0; x < p1; ++x) {
-        while (x >= before[i + 1]) ++i;
-        if (of != i) {
-          of = i;
-          start = p.starts[i];
-          count = p.starts[i + 1] - start;
-          length = p.lengths[i];
+      for (int x = p0; __any_sync(0xffffffffu, x < p1); ++x) {
+        Pair pair{};
+        Parts parts(0, 1);
+        int tasks = 0;
+        if (x < p1) {
+          while (x >= before[i + 1]) ++i;
+          if (of != i) {
+            of = i;
+            start = p.starts[i];
+            count = p.starts[i + 1] - start;
+            length = p.lengths[i];
+          }
+          pair = pair_of(p, start, count, length, before[i + 1] - 1 - x);
+          parts = Parts(pair.blocks, limit);
+          tasks = parts.count * p.vh;
         }
-        const Pair pair = pair_of(p, start, count, length, before[i + 1] - 1 - x);
-        if (pass == 1) {
+        if (pass == 1) {                                   // (the pass is the same for all lanes, whether they have a pair or not)
           mine += pair.blocks;
           continue;
         }
-        const Parts parts(pair.blocks, limit);
-        const int tasks = parts.count * p.vh;
-        if (pass == 3) {
-          const int first = static_cast<int>((at + mine) >> 32), slots = static_cast<int>(at + mine);
-          if (first + tasks > p.ctas) {                    // (starts that overlap: what is past the end is not done)
-            atomicMin(&s_tasks, first);
-            atomicMin(&s_slots, slots);
-          } else {
+        const int first = static_cast<int>((at + mine) >> 32), slots = static_cast<int>(at + mine);
+        mine += (static_cast<long long>(tasks) << 32) | (parts.count > 1 ? tasks : 0);
+        if (pass == 2) continue;
+        if (first + tasks > p.ctas) {                      // (starts that overlap: what is past the end is not done)
+          atomicMin(&s_tasks, first);
+          atomicMin(&s_slots, slots);
+          tasks = 0;
+        }
+        // the tasks of a lane's pair, by all of its warp
 #pragma unroll 1
-            for (int k = 0, vh = 0, part = 0; k < tasks; ++k) {
-              const int slot = parts.count > 1 ? slots + k : -1;
-              p.tasks[first + k] = Task{pair.row, pair.count, pair.pos, i, pair.lo, pair.head, pair.skip, vh, parts.begin(part), parts.begin(part + 1), slot, length > p.capacity};
-              if (slot >= 0) p.records[slot] = make_int4(pair.row, pair.count, vh, part == 0 ? parts.count : 0);
-              if (++part == parts.count) part = 0, ++vh;
-            }
+        for (unsigned rest = __ballot_sync(0xffffffffu, tasks > 0); rest; rest &= rest - 1u) {
+          auto of_lane = [&](int v) { return __shfl_sync(0xffffffffu, v, __ffs(rest) - 1); };
+          Task t{of_lane(pair.row), of_lane(pair.count), of_lane(pair.pos), of_lane(i), of_lane(pair.lo), of_lane(pair.head), of_lane(pair.skip), 0, 0, 0, 0,
+                 of_lane(length > p.capacity)};
+          Parts q = parts;
+          q.count = of_lane(parts.count), q.each = of_lane(parts.each), q.more = of_lane(parts.more);
+          const int to = of_lane(first), slot0 = of_lane(slots), all = of_lane(tasks);
+          for (int k = lane; k < all; k += 32) {
+            t.vh = k / q.count;
+            const int part = k - t.vh * q.count;
+            t.b0 = q.begin(part), t.b1 = q.begin(part + 1);
+            t.slot = q.count > 1 ? slot0 + k : -1;
+            p.tasks[to + k] = t;
+            if (t.slot >= 0) p.records[t.slot] = make_int4(t.row, t.count, t.vh, part == 0 ? q.count : 0);
           }
         }
-        mine += (static_cast<long long>(tasks) << 32) | (parts.count > 1 ? tasks : 0);
       }
       if (pass == 3) break;
     }
@@ -369,9 +384,9 @@ template <bool FP8, int D>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
   using LY = Layout<D>;
   constexpr int kSlots = LY::SLOTS;
-  // over an 8-bit cache weights are fp16 numbers up to 2^15: the running maximum may lag by 1 (log2) behind 2^14; bf16
-  // ones may lag by 8
-  constexpr float kShift = FP8 ? 14.f : 0.f, kLag = FP8 ? 1.f : 8.f;
+  // The running maximum may lag behind by kLag (log2), so that O is rarely rescaled.  Over an 8-bit cache weights are fp16
+  // numbers, scaled to 2^11 and up to 2^15 with the lag (what is below 2^-25 of the largest loses bits: 2^-36 of it at most).
+  constexpr float kShift = FP8 ? 11.f : 0.f, kLag = FP8 ? 4.f : 8.f;
   constexpr uint32_t kIdS = FP8 ? idesc_f32(kRows, kHalf) : idesc_bf16_f32(kRows, kHalf);
   constexpr uint32_t kIdO = (FP8 ? idesc_f32(kRows, D) : idesc_bf16_f32(kRows, D)) | kBMajorN;
   extern __shared__ unsigned char smraw[];
@@ -382,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   uint32_t *tslot = reinterpret_cast<uint32_t *>(ofull + 1);
   unsigned char *Qs = sm + LY::Q, *KVs = sm + LY::KV;
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], kCopyWarps), mbar_init(&empty[i], kMmaWarps);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], FP8 ? kCopyWarps / 2 : kCopyWarps), mbar_init(&empty[i], kMmaWarps);
     for (int i = 0; i < 4; ++i) mbar_init(&sfull[i], 1), mbar_init(&pfull[i], 4), mbar_init(&odone[i], 1);
     mbar_init(ofull, kMmaWarps);
     fence_mbar_init();
@@ -468,46 +483,51 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
 
   if (warp >= kSoftWarps + kMmaWarps) {
-    // ---- copies: a warp has 32 positions of a block, a lane looks one of them up ------------
+    // ---- copies: a lane looks up a position of a block ---------------------------------------
     constexpr int ES = FP8 ? 1 : 2, PIECES = D * ES / 16, ROWS = 32 / PIECES;   // 16-byte pieces of a row, rows a copy
     const int cw = warp - kSoftWarps - kMmaWarps;
-    int n_tiles = 0, told = 0;                             // tiles asked for, tiles told of
-    bool ok = true;
-    auto tell = [&](int upto) {
-      fence_to_tensor_cores();
-      __syncwarp();
-      for (; told < upto; ++told)
-        if (lane == 0) mbar_arrive(&full[told % kSlots]);
-    };
-    auto look_up = [&](int b) -> int64_t {                 // byte offset of this lane's slot; -1 not read, -2 bad
-      const int pos = x.number(b) * kBlock + cw * 32 + lane;
+    auto look_up = [&](int b, int i) -> int64_t {          // byte offset of position i of the block; -1 not read, -2 bad
+      const int pos = x.number(b) * kBlock + i;
       if (pos > last_of(1) || (pos < x.lo && pos >= p.sinks)) return -1;
       const int64_t at = slot_of(p, task.seq, pos);
       return at < 0 ? -2 : (at + kvh * p.head_stride) * ES;
     };
-    int64_t next = b0 < b1 ? look_up(b0) : -1;
-    for (int b = b0; b < b1 && ok; ++b) {
-      const int64_t at = next;
-      const bool bad = at == -2;
-      if (bad) report(p.status, MK_ERR_BAD_PAGE);
+    // a key that is not there is NaN: so are the scores of rows that see it
+    auto no_key = [&](unsigned char *to, int row) {
+      report(p.status, MK_ERR_BAD_PAGE);
+      for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4 *>(to + piece_at(row, c)) = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+    };
+    bool ok = true;
+    if constexpr (!FP8) {
+      // 32 positions a warp, keys and values in turn, one tile on its way while the one before is told of
+      int n_tiles = 0, told = 0;                           // tiles asked for, tiles told of
+      auto tell = [&](int upto) {
+        fence_to_tensor_cores();
+        __syncwarp();
+        for (; told < upto; ++told)
+          if (lane == 0) mbar_arrive(&full[told % kSlots]);
+      };
+      int64_t next = b0 < b1 ? look_up(b0, cw * 32 + lane) : -1;
+      for (int b = b0; b < b1 && ok; ++b) {
+        const int64_t at = next;
+        const bool bad = at == -2;
 #pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv, ++n_tiles) {
-        const int slot = n_tiles % kSlots;
-        if (n_tiles >= kSlots) {
-          const uint32_t parity = (n_tiles / kSlots - 1) & 1;
-          if (!__all_sync(0xffffffffu, mbar_try_wait(&empty[slot], parity))) {
-            if constexpr (!FP8) mkw::cp_async_wait<0>();
-            tell(n_tiles);
-            if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], parity, kWaitNs))) {
-              if (lane == 0) report(p.status, MK_ERR_TIMEOUT);
-              ok = false;
-              break;
+        for (int kv = 0; kv < 2; ++kv, ++n_tiles) {
+          const int slot = n_tiles % kSlots;
+          if (n_tiles >= kSlots) {
+            const uint32_t parity = (n_tiles / kSlots - 1) & 1;
+            if (!__all_sync(0xffffffffu, mbar_try_wait(&empty[slot], parity))) {
+              mkw::cp_async_wait<0>();
+              tell(n_tiles);
+              if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], parity, kWaitNs))) {
+                if (lane == 0) report(p.status, MK_ERR_TIMEOUT);
+                ok = false;
+                break;
+              }
             }
           }
-        }
-        const unsigned char *base = static_cast<const unsigned char *>(kv ? p.v : p.k);
-        unsigned char *to = KVs + slot * LY::TILE;
-        if constexpr (!FP8) {
+          const unsigned char *base = static_cast<const unsigned char *>(kv ? p.v : p.k);
+          unsigned char *to = KVs + slot * LY::TILE;
           const uint32_t to_at = smem_addr(to);
 #pragma unroll
           for (int i = 0; i < 32 / ROWS; ++i) {
@@ -516,47 +536,65 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             mkw::cp_async16(to_at + piece_at(cw * 32 + rr, c), base + (o < 0 ? 0 : o + c * 16), o >= 0);
           }
           mkw::cp_async_commit();
-        } else {
-#pragma unroll
-          for (int i0 = 0; i0 < 32 / ROWS; i0 += 4) {
-            uint4 w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int rr = (i0 + i) * ROWS + lane / PIECES, c = lane % PIECES;
-              const int64_t o = __shfl_sync(0xffffffffu, at, rr);
-              w[i] = o < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(base + o + c * 16);
+          if (kv == 0) {
+            if (__any_sync(0xffffffffu, bad)) {
+              mkw::cp_async_wait<0>();
+              __syncwarp();
+              if (bad) no_key(to, cw * 32 + lane);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int rr = (i0 + i) * ROWS + lane / PIECES, c = lane % PIECES;
-              uint32_t h[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) mkw::e4m3x4_to_half2((&w[i].x)[e], h[2 * e], h[2 * e + 1]);
-              *reinterpret_cast<uint4 *>(to + piece_at(cw * 32 + rr, 2 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
-              *reinterpret_cast<uint4 *>(to + piece_at(cw * 32 + rr, 2 * c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
-            }
+            if (b + 1 < b1) next = look_up(b + 1, cw * 32 + lane);
           }
-        }
-        if (kv == 0) {
-          if (__any_sync(0xffffffffu, bad)) {
-            // a key that is not there is NaN: so are the scores of rows that see it
-            if constexpr (!FP8) mkw::cp_async_wait<0>();
-            __syncwarp();
-            if (bad)
-              for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4 *>(to + piece_at(cw * 32 + lane, c)) = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+          if (n_tiles >= 1) {
+            mkw::cp_async_wait<1>();
+            tell(n_tiles);
           }
-          if (b + 1 < b1) next = look_up(b + 1);
-        }
-        if constexpr (FP8) {
-          tell(n_tiles + 1);
-        } else if (n_tiles >= 1) {
-          mkw::cp_async_wait<1>();
-          tell(n_tiles);
         }
       }
+      mkw::cp_async_wait<0>();
+      if (ok) tell(n_tiles);
+    } else {
+      // Through registers, to fp16.  Two warps have the keys and two the values, 64 positions each: what tells of a tile (the
+      // fence) waits for a warp's loads too, so that these are hidden by the other warps only.
+      constexpr int COPIES = 64 / ROWS;
+      const int kv = cw >> 1, row0 = (cw & 1) * 64;
+      const unsigned char *base = static_cast<const unsigned char *>(kv ? p.v : p.k);
+      int64_t next[2] = {-1, -1};
+      if (b0 < b1) next[0] = look_up(b0, row0 + lane), next[1] = look_up(b0, row0 + 32 + lane);
+      for (int b = b0; b < b1; ++b) {
+        const int64_t at[2] = {next[0], next[1]};
+        uint4 w[COPIES];
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+          const int rr = i * ROWS + lane / PIECES;
+          const int64_t o = __shfl_sync(0xffffffffu, at[i * ROWS / 32], rr & 31);
+          w[i] = o < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(base + o + lane % PIECES * 16);
+        }
+        if (b + 1 < b1) next[0] = look_up(b + 1, row0 + lane), next[1] = look_up(b + 1, row0 + 32 + lane);
+        const int n_tile = 2 * (b - b0) + kv, slot = n_tile % kSlots;
+        if (n_tile >= kSlots && !__all_sync(0xffffffffu, mbar_wait(&empty[slot], (n_tile / kSlots - 1) & 1, kWaitNs))) {
+          if (lane == 0) report(p.status, MK_ERR_TIMEOUT);
+          break;
+        }
+        unsigned char *to = KVs + slot * LY::TILE;
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+          const int rr = row0 + i * ROWS + lane / PIECES, c = lane % PIECES;
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mkw::e4m3x4_to_half2((&w[i].x)[e], h[2 * e], h[2 * e + 1]);
+          *reinterpret_cast<uint4 *>(to + piece_at(rr, 2 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4 *>(to + piece_at(rr, 2 * c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        if (kv == 0) {
+          __syncwarp();
+          if (at[0] == -2) no_key(to, row0 + lane);
+          if (at[1] == -2) no_key(to, row0 + 32 + lane);
+        }
+        fence_to_tensor_cores();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[slot]);
+      }
     }
-    if constexpr (!FP8) mkw::cp_async_wait<0>();
-    if (ok) tell(n_tiles);
   } else if (warp >= kSoftWarps) {
     // ---- products: S = Q K^T for half a block of a tile, then O += P V with P where S was, so that the next S there comes
     // behind it.  A tile has two such places: one is in its softmax while the other is multiplied.
@@ -800,38 +838,41 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   if (warp == kSoftWarps) tmem_dealloc(tmem, LY::TMEM_COLS);
 }
 
-// Joins the parts of an item, in order, a row a thread: CTA (c, y) takes 32 elements of the rows of tile y of the item whose
-// first part is partial result c.
+// Joins the parts of an item, in order: CTA (c, y) takes 32 elements of the rows of a tile of the item whose first part is
+// partial result c, a thread 8 elements of a row.
+constexpr int kJoin = 8, kJoinThreads = 4 * kRows;
 template <int D>
-__global__ void __launch_bounds__(kRows) join_kernel(const __grid_constant__ PromptParams p) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ PromptParams p) {
   mkw::follow_previous_kernel();
   if (static_cast<int>(blockIdx.x) >= p.header->y) return;
   const int4 rec = p.records[blockIdx.x];
   if (rec.w == 0) return;
-  const int tile = blockIdx.y & 1, c = (blockIdx.y >> 1) * 32, r = threadIdx.x;
+  const int tile = blockIdx.y & 1, c = (blockIdx.y >> 1) * 32 + threadIdx.x / kRows * kJoin, r = threadIdx.x % kRows;
   const int kvh = rec.z / p.blocks, head0 = kvh * p.group + (rec.z - kvh * p.blocks) * static_cast<int>(p.heads.value);
   const int heads = min(static_cast<int>(p.heads.value), (kvh + 1) * p.group - head0);
   const int token = p.heads.quotient(r), head = r - token * static_cast<int>(p.heads.value), index = tile * p.tokens + token;
   if (token >= p.tokens || head >= heads || index >= rec.y) return;
+  constexpr int64_t kPart = 2 * (D + 2) * kRows;
   const float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + tile) * (D + 2) * kRows + r;
-  float m = -INFINITY, l = 0.f, o[32] = {};
-  for (int j = 0; j < rec.w; ++j, part += 2 * (D + 2) * kRows) {
-    const float mj = part[D * kRows], lj = part[(D + 1) * kRows];
-    float x[32];
+  float m = -INFINITY, l = 0.f, o[kJoin] = {};
+#pragma unroll 4
+  for (int j = 0; j < rec.w; ++j) {
+    const float mj = part[j * kPart + D * kRows];
+    m = mj != mj || m != m ? NAN : fmaxf(m, mj);
+  }
+  const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+  for (int j = 0; j < rec.w; ++j) {
+    const float *at = part + j * kPart;
+    const float f = mkw::exp2_fast(at[D * kRows] - base);
+    l += at[(D + 1) * kRows] * f;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) x[e] = part[(c + e) * kRows];
-    const float mx = fmaxf(m, mj), base = mx == -INFINITY ? 0.f : mx, f = mkw::exp2_fast(m - base), fj = mkw::exp2_fast(mj - base);
-    m = mx;
-    l = l * f + lj * fj;
-#pragma unroll
-    for (int e = 0; e < 32; ++e) o[e] = o[e] * f + x[e] * fj;
+    for (int e = 0; e < kJoin; ++e) o[e] += at[(c + e) * kRows] * f;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l * (p.v_scale ? p.v_scale[kvh] : 1.f);
   __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (rec.x + index) * p.out_row + (head0 + head) * p.out_head + c;
-#pragma unroll
-  for (int e = 0; e < 32; e += 8)
-    *reinterpret_cast<uint4 *>(dst + e) = make_uint4(pack_weights<false>(o[e] * inv, o[e + 1] * inv), pack_weights<false>(o[e + 2] * inv, o[e + 3] * inv),
-                                                     pack_weights<false>(o[e + 4] * inv, o[e + 5] * inv), pack_weights<false>(o[e + 6] * inv, o[e + 7] * inv));
+  *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_weights<false>(o[0] * inv, o[1] * inv), pack_weights<false>(o[2] * inv, o[3] * inv),
+                                               pack_weights<false>(o[4] * inv, o[5] * inv), pack_weights<false>(o[6] * inv, o[7] * inv));
   if (c == 0 && p.lse) p.lse[static_cast<int64_t>(rec.x + index) * p.hq + head0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
@@ -846,7 +887,7 @@ int launch(PromptParams &p, int dev, cudaStream_t s) {
   int rc = p.direct ? MK_OK : mkw::launch_after(tasks, dim3(1), kTaskThreads, (p.n + 1) * 4, s, p);
   if (rc == MK_OK) rc = mkw::launch_after(fn, dim3(p.ctas), kThreads, Layout<D>::SMEM, s, p);
   if (rc != MK_OK || !p.joins) return rc;
-  return mkw::launch_after(&join_kernel<D>, dim3(2 * p.sms, 2 * D / 32), kRows, 0, s, p);
+  return mkw::launch_after(&join_kernel<D>, dim3(2 * p.sms, 2 * D / 32), kJoinThreads, 0, s, p);
 }
 
 // pairs of tiles of a call: a sequence has one that is not full

@@ -46,8 +46,9 @@ def masked_attention(q, k, v, see, scale, p_err, fp8):
         # products of 16 terms, each truncated, in tensor memory
         s_err = a.amax(1, keepdim=True) * 24 * 2.0 ** -23
         c = 2 * s_err + p_err + (64 + n / 8) * 2.0 ** -23
-        # over an 8-bit cache weights below 2^-28 of the largest are subnormal fp16 numbers
-        err[:, h] = c * (w @ vf.abs()) + (n * 2.0 ** -38 * vf.abs().amax() if fp8 else 0.0)
+        # over an 8-bit cache weights are fp16 numbers, the largest 2^11 at least: small ones are rounded by half a step of
+        # the subnormal numbers, 2^-25, which is 2^-36 of the largest
+        err[:, h] = c * (w @ vf.abs()) + (n * 2.0 ** -36 * vf.abs().amax() if fp8 else 0.0)
         lerr[:, h] = (2 * s_err[:, 0] + (64 + n / 32) * 2.0 ** -23) + 2.0 ** -22 * torch.where(some, lse[:, h].abs(), 0.0)
     return out, lse, err, lerr
 
