@@ -13,14 +13,15 @@
 namespace mklogits {
 
 // ---------------------------------------------------------------------------
-// One pass over the logits: y = penalties(x, how often the row's history holds the token) + bias, -inf where the mask's
-// bit is 0.
+// y = penalties(x, how often the row's history holds the token) + bias, -inf where the mask's bit is 0.
 //
 // Bound by the logits' bytes for a batch, by latency for one row.  A CTA has a slice of a row's vocabulary and a word of
-// shared memory for each of its tokens.  It asks for its logits first (up to four 16-byte loads a thread, all in
-// flight), then walks the row's whole history and counts the tokens of its slice by integer atomics (any order gives the
-// same counts) while those loads are on their way.  Biases are few: they set a bit of the word, and the thread that has
-// such a token adds up its entries in their order.  A token whose word is 0 is copied.
+// shared memory for each of its tokens.  It asks for its logits first (up to four 16-byte loads a thread, all in flight),
+// walks the row's whole history and counts the tokens of its slice by integer atomics (any order gives the same counts)
+// while those loads are on their way, stores the logits with the mask, and then goes over the tokens that it has counted:
+// those are few, and a warp that looked at each of its tokens on the way took four times as long (64 rows 28 us).  The one
+// who counts a token first writes it down; which order that gives does not matter, as each is adjusted on its own.  Biases
+// set a bit of the word, and who has such a token adds up its entries in their order.
 // ---------------------------------------------------------------------------
 
 constexpr int kThreads = 512;
@@ -43,9 +44,6 @@ template <>
 struct Piece<float> {
   static constexpr int N = 4;
   static __device__ __forceinline__ float value(const uint4 &w, int e) { return __uint_as_float((&w.x)[e]); }
-  static __device__ __forceinline__ uint4 bits(const float *y) {
-    return make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
-  }
   static __device__ __forceinline__ void put(uint4 &w, int e, float x) { (&w.x)[e] = __float_as_uint(x); }
 };
 template <>
@@ -54,13 +52,6 @@ struct Piece<__nv_bfloat16> {
   static __device__ __forceinline__ float value(const uint4 &w, int e) {
     const uint32_t u = (&w.x)[e >> 1];
     return __uint_as_float(e & 1 ? u & 0xffff0000u : u << 16);
-  }
-  static __device__ __forceinline__ uint32_t pair(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-  }
-  static __device__ __forceinline__ uint4 bits(const float *y) {
-    return make_uint4(pair(y[0], y[1]), pair(y[2], y[3]), pair(y[4], y[5]), pair(y[6], y[7]));
   }
   static __device__ __forceinline__ void put(uint4 &w, int e, __nv_bfloat16 x) {
     const uint32_t u = __bfloat16_as_ushort(x);
@@ -73,15 +64,16 @@ struct Piece<__nv_bfloat16> {
 template <class W>
 struct Word {
   static constexpr uint32_t kPrompt = sizeof(W) == 2 ? 0x8000u : 0x80000000u, kBias = kPrompt >> 1, kCount = kBias - 1;
-  // count, or mark, token t
-  static __device__ __forceinline__ void add(uint32_t *words, int t, uint32_t by) {
-    if (sizeof(W) == 2) atomicAdd(&words[t >> 1], by << (16 * (t & 1)));
-    else atomicAdd(&words[t], by);
+  // count, or mark, token t: whether it is the first time
+  static __device__ __forceinline__ bool add(uint32_t *words, int t, uint32_t by) {
+    if (sizeof(W) == 2) return (atomicAdd(&words[t >> 1], by << (16 * (t & 1))) >> (16 * (t & 1)) & 0xffffu) == 0;
+    return atomicAdd(&words[t], by) == 0;
   }
-  static __device__ __forceinline__ void mark(uint32_t *words, int t, uint32_t bit) {
-    if (sizeof(W) == 2) atomicOr(&words[t >> 1], bit << (16 * (t & 1)));
-    else atomicOr(&words[t], bit);
+  static __device__ __forceinline__ bool mark(uint32_t *words, int t, uint32_t bit) {
+    if (sizeof(W) == 2) return (atomicOr(&words[t >> 1], bit << (16 * (t & 1))) >> (16 * (t & 1)) & 0xffffu) == 0;
+    return atomicOr(&words[t], bit) == 0;
   }
+  static __device__ __forceinline__ uint32_t of(const uint32_t *words, int t) { return reinterpret_cast<const W *>(words)[t]; }
 };
 
 template <class T, class W>
@@ -122,82 +114,65 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
   if (p.presence) presence = p.presence[row];
   if (p.frequency) frequency = p.frequency[row];
   const bool counted = length > 0 && (repetition != 1.f || presence != 0.f || frequency != 0.f), marked = counted || p.biases > 0;
+  __shared__ int s_found;
+  uint16_t *found = reinterpret_cast<uint16_t *>(words + size * static_cast<int>(sizeof(W)) / 4);   // the slice's tokens that have a word
   if (marked) {
     for (int i = tid; i < size * static_cast<int>(sizeof(W)) / 16; i += kThreads) reinterpret_cast<uint4 *>(words)[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) s_found = 0;
     __syncthreads();
     if (counted) {
       const int32_t *tokens = p.tokens + row * p.tokens_row;
       const int prompt = p.prompts ? p.prompts[row] : 0;
 #pragma unroll 4
       for (int j = tid; j < length; j += kThreads) {
-        const int id = tokens[j];
-        const int64_t t = static_cast<int64_t>(id) - first;
-        if (id < 0 || t < 0 || t >= size) continue;
-        if (j < prompt) Wd::mark(words, static_cast<int>(t), Wd::kPrompt);
-        else Wd::add(words, static_cast<int>(t), 1);
+        const int id = tokens[j], t = id - first;          // (no overflow: first is not below -8)
+        if (id < 0 || id >= p.vocab || t < 0 || t >= size) continue;
+        if (j < prompt ? Wd::mark(words, t, Wd::kPrompt) : Wd::add(words, t, 1)) found[atomicAdd(&s_found, 1)] = static_cast<uint16_t>(t);
       }
     }
     for (int j = tid; j < p.biases; j += kThreads) {
-      const int id = p.bias_ids[row * p.ids_row + j];
-      const int64_t t = static_cast<int64_t>(id) - first;
-      if (id >= 0 && t >= 0 && t < size) Wd::mark(words, static_cast<int>(t), Wd::kBias);
+      const int id = p.bias_ids[row * p.ids_row + j], t = id - first;
+      if (id >= 0 && id < p.vocab && t >= 0 && t < size && Wd::mark(words, t, Wd::kBias)) found[atomicAdd(&s_found, 1)] = static_cast<uint16_t>(t);
     }
-    __syncthreads();
   }
   const uint32_t *mask = p.mask ? p.mask + row * p.mask_row : nullptr;
 #pragma unroll
   for (int k = 0; k < kMost; ++k) {
     if (k >= p.per) break;
-    const int piece = k * kThreads + tid, e0 = first + piece * N;
+    const int e0 = first + (k * kThreads + tid) * N;
     if (e0 >= p.vocab || e0 + N <= 0) continue;
-    uint32_t allowed = ~0u;                                // bits of the piece's elements
     if (mask) {
       const int a = max(e0, 0), z = min(e0 + N, p.vocab) - 1;
-      allowed = __funnelshift_r(mask[a >> 5], mask[z >> 5], a & 31) << (a - e0);
+      const uint32_t allowed = __funnelshift_r(mask[a >> 5], mask[z >> 5], a & 31) << (a - e0);   // bits of the piece's elements
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (!(allowed >> e & 1)) Piece<T>::put(raw[k], e, static_cast<T>(-INFINITY));
     }
-    uint32_t word[N];
-    uint32_t any = 0;
-    if (marked) {
-#pragma unroll
-      for (int i = 0; i < static_cast<int>(N * sizeof(W)) / 8; ++i) {
-        const uint2 u = reinterpret_cast<const uint2 *>(words)[piece * static_cast<int>(N * sizeof(W)) / 8 + i];
-        any |= u.x | u.y;
-        if constexpr (sizeof(W) == 2) {
-          word[4 * i] = u.x & 0xffffu, word[4 * i + 1] = u.x >> 16, word[4 * i + 2] = u.y & 0xffffu, word[4 * i + 3] = u.y >> 16;
-        } else {
-          word[2 * i] = u.x, word[2 * i + 1] = u.y;
-        }
-      }
-    }
-    float y[N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) y[e] = Piece<T>::value(raw[k], e);
-    if (any) {
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        if (!word[e]) continue;
-        const int count = word[e] & Wd::kCount;
-        if (count || (word[e] & Wd::kPrompt)) y[e] = y[e] > 0.f ? __fdiv_rn(y[e], repetition) : y[e] * repetition;
-        if (count) y[e] = __fsub_rn(__fsub_rn(y[e], __fmul_rn(frequency, static_cast<float>(count))), presence);
-        if (word[e] & Wd::kBias) {
-          float sum = 0.f;
-          for (int j = 0; j < p.biases; ++j)
-            if (p.bias_ids[row * p.ids_row + j] == e0 + e) sum += p.bias[row * p.bias_row + j];
-          y[e] += sum;
-        }
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (!(allowed >> e & 1)) y[e] = -INFINITY;
-    const uint4 w = Piece<T>::bits(y);
     if (together && e0 >= 0 && e0 + N <= p.vocab) {
-      *reinterpret_cast<uint4 *>(out + e0) = w;
+      *reinterpret_cast<uint4 *>(out + e0) = raw[k];
     } else {
 #pragma unroll
       for (int e = 0; e < N; ++e)
-        if (e0 + e >= 0 && e0 + e < p.vocab) out[e0 + e] = static_cast<T>(y[e]);
+        if (e0 + e >= 0 && e0 + e < p.vocab) out[e0 + e] = static_cast<T>(Piece<T>::value(raw[k], e));
     }
+  }
+  if (!marked) return;
+  __syncthreads();                                         // (in place, x is out: what is not masked has been put back as it was)
+  for (int i = tid; i < s_found; i += kThreads) {
+    const int t = found[i], id = first + t;
+    if (mask && !(mask[id >> 5] >> (id & 31) & 1)) continue;
+    const uint32_t word = Wd::of(words, t);
+    const int count = word & Wd::kCount;
+    float y = static_cast<float>(x[id]);
+    if (count || (word & Wd::kPrompt)) y = y > 0.f ? __fdiv_rn(y, repetition) : y * repetition;
+    if (count) y = __fsub_rn(__fsub_rn(y, __fmul_rn(frequency, static_cast<float>(count))), presence);
+    if (word & Wd::kBias) {
+      float sum = 0.f;
+      for (int j = 0; j < p.biases; ++j)
+        if (p.bias_ids[row * p.ids_row + j] == id) sum += p.bias[row * p.bias_row + j];
+      y += sum;
+    }
+    out[id] = static_cast<T>(y);
   }
 }
 
@@ -206,7 +181,7 @@ int launch(LogitsParams &p, int sms, int dev, cudaStream_t s) {
   constexpr int N = Piece<T>::N;
   static mkw::Ready ready[mkw::kMaxDevices];
   const auto fn = &adjust_kernel<T, W>;
-  const int most = kMost * kThreads * N * static_cast<int>(sizeof(W));
+  const int most = kMost * kThreads * N * static_cast<int>(sizeof(W) + 2);
   if (!ready[dev].get(reinterpret_cast<const void *>(fn), kThreads, most)) return MK_ERR_CUDA;
   // the largest slices that give every SM two CTAs: a slice walks the whole history
   const int64_t elements = static_cast<int64_t>(p.vocab) + N - 1;
@@ -216,7 +191,7 @@ int launch(LogitsParams &p, int sms, int dev, cudaStream_t s) {
   const int64_t ctas = slices(p.per) * p.n;
   if (ctas > INT32_MAX) return MK_ERR_UNSUPPORTED;
   p.slices = static_cast<int>(slices(p.per));
-  return mkw::launch_after(fn, dim3(static_cast<unsigned>(ctas)), kThreads, p.per * kThreads * N * static_cast<int>(sizeof(W)), s, p);
+  return mkw::launch_after(fn, dim3(static_cast<unsigned>(ctas)), kThreads, p.per * kThreads * N * static_cast<int>(sizeof(W) + 2), s, p);
 }
 
 }  // namespace mklogits

@@ -34,10 +34,10 @@ struct PromptParams {
   const int32_t *table, *starts, *lengths;
   const float *k_scale, *v_scale;
   int32_t *status;
-  int4 *header;                // .x: tasks, .y: partial results in all
-  int4 *records;               // of each partial result {first row, tokens, virtual head, parts or 0}
+  int4 *header;                // .x: tasks, .y: items that are cut
+  int4 *records;               // of each such item {first row, tokens, virtual head, first partial result and above its 16 bits the parts}
   struct Task *tasks;
-  float *parts;                // [partial result][tile][D + 2][kRows]: O, maximum, sum
+  float *parts;                // [partial result][tile][kRows][D + 4]: O, maximum, sum
   mkw::Divisor page_size, heads;   // heads: query heads of a tile's token
   int n, rows, hq, hkv, group, n_pages, capacity, window, sinks;
   int blocks, vh;              // head blocks of a kv head, virtual heads hkv * blocks
@@ -118,28 +118,30 @@ __device__ __forceinline__ int pairs_of(const PromptParams &p, int i, bool &bad)
 }
 
 // The tasks of a call, in the order of sequences, their last rows (which see most) first; CTA i of the attention kernel takes
-// task i.  Every item (pair of tiles and virtual head) of more blocks than an equal share of all the work is cut into parts.
+// task i.  An item (pair of tiles and virtual head) of more blocks than `limit` is cut into parts: the limit is an equal share
+// of all the work, twice that, or none, whichever promises the earliest end.
 // One CTA, as a call's lengths are on the device: every CTA of the other kernel finding its own task took 3.5 us each.  Where
 // nothing can be cut and a warp holds all sequences, that is quick, and this kernel is left out.
 __global__ void __launch_bounds__(kTaskThreads) task_kernel(const __grid_constant__ PromptParams p) {
   extern __shared__ int before[];                          // pairs before a sequence: [n + 1]
   __shared__ long long s_warps[kTaskThreads / 32];
-  __shared__ int s_tasks, s_slots;
+  __shared__ int s_tasks, s_items, s_most;
   mkw::follow_previous_kernel();
   const int tid = threadIdx.x, lane = tid & 31, n = p.n;
   bool bad = false;
+  if (tid == 0) s_most = 0;
   for (int i = tid; i < n; i += kTaskThreads) before[i] = pairs_of(p, i, bad);
   if (bad) report(p.status, MK_ERR_BAD_PAGE);
   const int per = (n + kTaskThreads - 1) / kTaskThreads, a = min(n, tid * per), b = min(n, a + per);
-  int p0 = 0, p1 = 0, i0 = 0, limit = INT32_MAX;
-  long long at = 0;
+  int p0 = 0, p1 = 0, i0 = 0, limit = INT32_MAX, share = INT32_MAX;
+  long long at = 0, blocks = 0;
   __syncthreads();
-  // Passes: 0 the pairs before this thread's sequences; then over its share of the pairs 1 their blocks, 2 its tasks (in the
-  // upper half) and partial results, 3 the same written down.  One copy of the loop and of the sum over threads: code that
-  // runs once takes as long as it is.
+  // Passes: 0 the pairs before this thread's sequences; then over its share of the pairs 1 their blocks, 2 their tasks with
+  // either limit, 3 its tasks (in the upper half), partial results and items that are cut, 4 the same written down.  One copy
+  // of the loop and of the sum over threads: code that runs once takes as long as it is.
 #pragma unroll 1
-  for (int pass = 0; pass < 4; ++pass) {
-    if (pass == 1 && !p.joins) continue;
+  for (int pass = 0; pass < 5; ++pass) {
+    if ((pass == 1 || pass == 2) && !p.joins) continue;
     long long mine = 0;
     if (pass == 0) {
       for (int i = a; i < b; ++i) mine += before[i];
@@ -162,16 +164,23 @@ __global__ void __launch_bounds__(kTaskThreads) task_kernel(const __grid_constan
           parts = Parts(pair.blocks, limit);
           tasks = parts.count * p.vh;
         }
-        if (pass == 1) {                                   // (the pass is the same for all lanes, whether they have a pair or not)
+        // (the pass is the same for all lanes, whether they have a pair or not)
+        if (pass == 1) {
           mine += pair.blocks;
+          if (pair.blocks > s_most) atomicMax(&s_most, pair.blocks);
           continue;
         }
-        const int first = static_cast<int>((at + mine) >> 32), slots = static_cast<int>(at + mine);
-        mine += (static_cast<long long>(tasks) << 32) | (parts.count > 1 ? tasks : 0);
-        if (pass == 2) continue;
+        if (pass == 2) {
+          if (tasks) mine += (static_cast<long long>(Parts(pair.blocks, share).count) << 32) | Parts(pair.blocks, 2 * share).count;
+          continue;
+        }
+        const int first = static_cast<int>((at + mine) >> 32), slots = static_cast<int>(at + mine) >> 16, items = static_cast<int>(at + mine) & 0xffff;
+        mine += static_cast<long long>(tasks) << 32;
+        if (parts.count > 1) mine += (tasks << 16) + p.vh;
+        if (pass == 3) continue;
         if (first + tasks > p.ctas) {                      // (starts that overlap: what is past the end is not done)
           atomicMin(&s_tasks, first);
-          atomicMin(&s_slots, slots);
+          atomicMin(&s_items, items);
           tasks = 0;
         }
         // the tasks of a lane's pair, by all of its warp
@@ -182,18 +191,18 @@ __global__ void __launch_bounds__(kTaskThreads) task_kernel(const __grid_constan
                  of_lane(length > p.capacity)};
           Parts q = parts;
           q.count = of_lane(parts.count), q.each = of_lane(parts.each), q.more = of_lane(parts.more);
-          const int to = of_lane(first), slot0 = of_lane(slots), all = of_lane(tasks);
+          const int to = of_lane(first), slot0 = of_lane(slots), item0 = of_lane(items), all = of_lane(tasks);
           for (int k = lane; k < all; k += 32) {
             t.vh = k / q.count;
             const int part = k - t.vh * q.count;
             t.b0 = q.begin(part), t.b1 = q.begin(part + 1);
             t.slot = q.count > 1 ? slot0 + k : -1;
             p.tasks[to + k] = t;
-            if (t.slot >= 0) p.records[t.slot] = make_int4(t.row, t.count, t.vh, part == 0 ? q.count : 0);
+            if (q.count > 1 && part == 0) p.records[item0 + t.vh] = make_int4(t.row, t.count, t.vh, q.count << 16 | t.slot);
           }
         }
       }
-      if (pass == 3) break;
+      if (pass == 4) break;
     }
     long long s = mine;                                    // before this thread's, and all
 #pragma unroll 1
@@ -220,22 +229,33 @@ __global__ void __launch_bounds__(kTaskThreads) task_kernel(const __grid_constan
       pairs = static_cast<int>(total);
       if (tid == 0) before[n] = pairs;
       __syncthreads();
-      const int share = (pairs + kTaskThreads - 1) / kTaskThreads;
-      p0 = min(pairs, tid * share), p1 = min(pairs, p0 + share);
+      const int each = (pairs + kTaskThreads - 1) / kTaskThreads;
+      p0 = min(pairs, tid * each), p1 = min(pairs, p0 + each);
       for (int hi = n; hi - i0 > 1;) {                     // the sequence of the first of them
         const int mid = (i0 + hi) >> 1;
         if (before[mid] <= p0) i0 = mid;
         else hi = mid;
       }
     } else if (pass == 1) {
-      limit = static_cast<int>(max(static_cast<long long>(kLeastBlocks), min(static_cast<long long>(INT32_MAX), (total * p.vh + p.sms - 1) / p.sms)));
+      blocks = total * p.vh;
+      share = static_cast<int>(max(static_cast<long long>(kLeastBlocks), min(static_cast<long long>(INT32_MAX / 2), (blocks + p.sms - 1) / p.sms)));
+    } else if (pass == 2) {
+      // In blocks: a task has kBegin of them to set up and store, a join takes kJoining.  Tasks that run all at once end with
+      // the longest; else the SMs' equal shares, and half the longest for what is uneven.
+      constexpr float kBegin = 4.f, kJoining = 3.f;
+      auto ends = [&](int most, long long tasks) {
+        const float longest = static_cast<float>(min(most, s_most)) + kBegin;
+        return (tasks <= p.sms ? longest : (static_cast<float>(blocks) + kBegin * tasks) / p.sms + longest / 2) + (most < s_most ? kJoining : 0.f);
+      };
+      const float one = ends(share, (total >> 32) * p.vh), twice = ends(2 * share, (total & 0xffffffff) * p.vh), none = ends(INT32_MAX, static_cast<long long>(before[n]) * p.vh);
+      limit = none <= one && none <= twice ? INT32_MAX : one <= twice ? share : 2 * share;
     } else if (tid == 0) {
-      s_tasks = static_cast<int>(total >> 32), s_slots = static_cast<int>(total);
+      s_tasks = static_cast<int>(total >> 32), s_items = static_cast<int>(total) & 0xffff;
     }
     __syncthreads();
   }
   __syncthreads();
-  if (tid == 0) *p.header = make_int4(s_tasks, s_slots, 0, 0);
+  if (tid == 0) *p.header = make_int4(s_tasks, s_items, 0, 0);
 }
 
 // Task `index` of a call whose items are whole and whose sequences a warp holds, by every warp; count 0: there is none.
@@ -764,51 +784,56 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     tc_fence_after();
     const float vs = FP8 && p.v_scale ? p.v_scale[kvh] : 1.f;
     if (task.outside && lane == 0) report(p.status, MK_ERR_BAD_PAGE);
-    float *part = whole ? nullptr : p.parts + (static_cast<int64_t>(task.slot) * 2 + tile) * (D + 2) * kRows + r;
+    float *part = whole ? nullptr : p.parts + ((static_cast<int64_t>(task.slot) * 2 + tile) * kRows + r) * (D + 4);
     __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (x.row + index) * p.out_row + (head0 + head) * p.out_head;
     const float inv = task.outside || !ok ? NAN : !whole ? 1.f : l == 0.f ? 0.f : __frcp_rn(l) * vs;
     bool strange = false;
+    // to where the warp's queries were, and from there a row's bytes together: rounded results, or half of fp32 ones at a time
+    constexpr int PIECES = D / 8, ROWS = 32 / PIECES;
+    const unsigned alive = __ballot_sync(0xffffffffu, live);
+    unsigned char *mine = Qs + tile * LY::TILE;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       uint32_t u[32];
-      float y[32];
       if (started && ok) {
         tmem_ld32(o_at + c, u);
         tmem_ld_wait(u);
       }
+      float y[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         y[i] = (started && ok && l != 0.f ? __uint_as_float(u[i]) : 0.f) * inv;
         strange |= !(fabsf(y[i]) < INFINITY);
       }
       if (whole) {
-        // to where the warp's queries were, from there row by row
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4 *>(Qs + tile * LY::TILE + piece_at(r, c / 8 + i)) =
+          *reinterpret_cast<uint4 *>(mine + piece_at(r, c / 8 + i)) =
               make_uint4(pack_weights<false>(y[8 * i], y[8 * i + 1]), pack_weights<false>(y[8 * i + 2], y[8 * i + 3]),
                          pack_weights<false>(y[8 * i + 4], y[8 * i + 5]), pack_weights<false>(y[8 * i + 6], y[8 * i + 7]));
-      } else if (live) {
+      } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) part[(c + i) * kRows] = y[i];
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4 *>(mine + piece_at(r, c % (D / 2) / 4 + i)) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
       }
-    }
-    if (whole) {
-      constexpr int PIECES = D / 8, ROWS = 32 / PIECES;
-      const unsigned alive = __ballot_sync(0xffffffffu, live);
-      const uint64_t to = reinterpret_cast<uint64_t>(dst);
+      const bool full_rows = whole ? c + 32 == D : (c + 32) % (D / 2) == 0;
+      if (full_rows) {
+        __syncwarp();
+        const uint64_t to = whole ? reinterpret_cast<uint64_t>(dst) : reinterpret_cast<uint64_t>(part + (c + 32 - D / 2));
 #pragma unroll 4
-      for (int i = 0; i < 32; i += ROWS) {
-        const int rr = i + lane / PIECES, c = lane % PIECES;
-        const uint64_t row_at = __shfl_sync(0xffffffffu, to, rr);
-        const uint4 w = *reinterpret_cast<const uint4 *>(Qs + tile * LY::TILE + piece_at((warp & 3) * 32 + rr, c));
-        if (alive >> rr & 1) *reinterpret_cast<uint4 *>(row_at + c * 16) = w;
+        for (int i = 0; i < 32; i += ROWS) {
+          const int rr = i + lane / PIECES, piece = lane % PIECES;
+          const uint64_t row_at = __shfl_sync(0xffffffffu, to, rr);
+          const uint4 w = *reinterpret_cast<const uint4 *>(mine + piece_at((warp & 3) * 32 + rr, piece));
+          if (alive >> rr & 1) *reinterpret_cast<uint4 *>(row_at + piece * 16) = w;
+        }
+        __syncwarp();
       }
     }
     m = m == -INFINITY ? m : m * to_log2 - kShift;         // log2 units, as the sum is scaled
     if (task.outside || !ok) m = l = NAN;
     if (live) {
-      if (!whole) part[D * kRows] = m, part[(D + 1) * kRows] = l;
+      if (!whole) part[D] = m, part[D + 1] = l;
       else if (p.lse) p.lse[static_cast<int64_t>(x.row + index) * p.hq + head0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     }
     strange |= !(fabsf(l) < INFINITY);
@@ -826,10 +851,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int i = 0; i < D / 32; ++i) to[i] = __float2bfloat16_rn(o[i] * f * vs);
         if (lane == 0 && p.lse) p.lse[static_cast<int64_t>(row) * p.hq + hd] = rl == 0.f ? -INFINITY : (rm + log2f(rl * grow)) * 0.69314718055994531f;
       } else {
-        float *to = p.parts + (static_cast<int64_t>(task.slot) * 2 + tile) * (D + 2) * kRows + (warp & 3) * 32 + of;
+        float *to = p.parts + ((static_cast<int64_t>(task.slot) * 2 + tile) * kRows + (warp & 3) * 32 + of) * (D + 4);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) to[(lane * (D / 32) + i) * kRows] = o[i];
-        if (lane == 0) to[D * kRows] = rm + log2f(grow), to[(D + 1) * kRows] = rl;
+        for (int i = 0; i < D / 32; ++i) to[lane * (D / 32) + i] = o[i];
+        if (lane == 0) to[D] = rm + log2f(grow), to[D + 1] = rl;
       }
     }
   }
@@ -838,42 +863,67 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   if (warp == kSoftWarps) tmem_dealloc(tmem, LY::TMEM_COLS);
 }
 
-// Joins the parts of an item, in order: CTA (c, y) takes 32 elements of the rows of a tile of the item whose first part is
-// partial result c, a thread 8 elements of a row.
-constexpr int kJoin = 8, kJoinThreads = 4 * kRows;
+// Joins the parts of items, in order, a row a warp, in units of 16 rows that the CTAs (two an SM: one that finds nothing costs
+// a microsecond in all) take in turn.  Up to 32 parts' maxima and sums are read at once, a lane each.
+constexpr int kJoinWarps = 16, kUnits = 2 * kRows / kJoinWarps;
+__device__ __forceinline__ void load_part(const float *p, float (&x)[4]) {
+  const float4 v = *reinterpret_cast<const float4 *>(p);
+  x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+}
+__device__ __forceinline__ void load_part(const float *p, float (&x)[2]) {
+  const float2 v = *reinterpret_cast<const float2 *>(p);
+  x[0] = v.x, x[1] = v.y;
+}
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ PromptParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ PromptParams p) {
+  constexpr int E = D / 32;
   mkw::follow_previous_kernel();
-  if (static_cast<int>(blockIdx.x) >= p.header->y) return;
-  const int4 rec = p.records[blockIdx.x];
-  if (rec.w == 0) return;
-  const int tile = blockIdx.y & 1, c = (blockIdx.y >> 1) * 32 + threadIdx.x / kRows * kJoin, r = threadIdx.x % kRows;
-  const int kvh = rec.z / p.blocks, head0 = kvh * p.group + (rec.z - kvh * p.blocks) * static_cast<int>(p.heads.value);
-  const int heads = min(static_cast<int>(p.heads.value), (kvh + 1) * p.group - head0);
-  const int token = p.heads.quotient(r), head = r - token * static_cast<int>(p.heads.value), index = tile * p.tokens + token;
-  if (token >= p.tokens || head >= heads || index >= rec.y) return;
-  constexpr int64_t kPart = 2 * (D + 2) * kRows;
-  const float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + tile) * (D + 2) * kRows + r;
-  float m = -INFINITY, l = 0.f, o[kJoin] = {};
-#pragma unroll 4
-  for (int j = 0; j < rec.w; ++j) {
-    const float mj = part[j * kPart + D * kRows];
-    m = mj != mj || m != m ? NAN : fmaxf(m, mj);
-  }
-  const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-  for (int j = 0; j < rec.w; ++j) {
-    const float *at = part + j * kPart;
-    const float f = mkw::exp2_fast(at[D * kRows] - base);
-    l += at[(D + 1) * kRows] * f;
+  const int lane = threadIdx.x & 31, units = p.header->y * kUnits;
+#pragma unroll 1
+  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int4 rec = p.records[unit / kUnits];
+    const int parts = rec.w >> 16, slot = rec.w & 0xffff, i = unit % kUnits * kJoinWarps + (threadIdx.x >> 5);
+    const int kvh = rec.z / p.blocks, head0 = kvh * p.group + (rec.z - kvh * p.blocks) * static_cast<int>(p.heads.value);
+    const int heads = min(static_cast<int>(p.heads.value), (kvh + 1) * p.group - head0);
+    const float vs = p.v_scale ? p.v_scale[kvh] : 1.f;
+    const int r = i % kRows, token = p.heads.quotient(r), head = r - token * static_cast<int>(p.heads.value), index = i / kRows * p.tokens + token;
+    if (token >= p.tokens || head >= heads || index >= rec.y) continue;
+    constexpr int64_t kPart = 2 * kRows * (D + 4);
+    const float *part = p.parts + static_cast<int64_t>(slot) * kPart + i * (D + 4);
+    float m = -INFINITY, l = 0.f, o[E] = {};
+    for (int j0 = 0; j0 < parts; j0 += 32) {
+      const bool mine = j0 + lane < parts;
+      const float mj = mine ? part[(j0 + lane) * kPart + D] : -INFINITY, lj = mine ? part[(j0 + lane) * kPart + D + 1] : 0.f;
+      float top = fmaxf(m, mj);
 #pragma unroll
-    for (int e = 0; e < kJoin; ++e) o[e] += at[(c + e) * kRows] * f;
+      for (int o2 = 16; o2 > 0; o2 >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
+      const float base = top == -INFINITY ? 0.f : top, f = mkw::exp2_fast(m - base), fj = mkw::exp2_fast(mj - base);
+      m = top;
+      l = l * f + lj * fj;                                 // (a lane's own; added up at the end)
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= f;
+      const int count = min(32, parts - j0);
+#pragma unroll 1
+      for (int j = 0; j < count; j += 8) {                 // eight parts' elements on their way together
+        float x[8][E];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) load_part(part + (j0 + min(j + k, count - 1)) * kPart + lane * E, x[k]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float w = __shfl_sync(0xffffffffu, fj, j + k & 31);   // (0 for a lane without a part)
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] += j + k < count ? x[k][e] * w : 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int o2 = 16; o2 > 0; o2 >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o2);
+    const float inv = l == 0.f ? 0.f : 1.f / l * vs;
+    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (rec.x + index) * p.out_row + (head0 + head) * p.out_head + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = pack_weights<false>(o[e] * inv, o[e + 1] * inv);
+    if (lane == 0 && p.lse) p.lse[static_cast<int64_t>(rec.x + index) * p.hq + head0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l * (p.v_scale ? p.v_scale[kvh] : 1.f);
-  __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (rec.x + index) * p.out_row + (head0 + head) * p.out_head + c;
-  *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_weights<false>(o[0] * inv, o[1] * inv), pack_weights<false>(o[2] * inv, o[3] * inv),
-                                               pack_weights<false>(o[4] * inv, o[5] * inv), pack_weights<false>(o[6] * inv, o[7] * inv));
-  if (c == 0 && p.lse) p.lse[static_cast<int64_t>(rec.x + index) * p.hq + head0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 template <bool FP8, int D>
@@ -887,16 +937,17 @@ int launch(PromptParams &p, int dev, cudaStream_t s) {
   int rc = p.direct ? MK_OK : mkw::launch_after(tasks, dim3(1), kTaskThreads, (p.n + 1) * 4, s, p);
   if (rc == MK_OK) rc = mkw::launch_after(fn, dim3(p.ctas), kThreads, Layout<D>::SMEM, s, p);
   if (rc != MK_OK || !p.joins) return rc;
-  return mkw::launch_after(&join_kernel<D>, dim3(2 * p.sms, 2 * D / 32), kJoinThreads, 0, s, p);
+  return mkw::launch_after(&join_kernel<D>, dim3(2 * p.sms), 32 * kJoinWarps, 0, s, p);
 }
 
 // pairs of tiles of a call: a sequence has one that is not full
 int64_t most_pairs(int64_t n, int64_t rows, int tokens) { return std::min(rows, rows / (2 * tokens) + n); }
 
-int64_t parts_bytes(int sms, int d) { return 2 * static_cast<int64_t>(sms) * 2 * kRows * (d + 2) * 4; }
-// header, records, tasks (one for each item and for every share of the work one more), partial results
+int64_t parts_bytes(int sms, int d) { return 2 * static_cast<int64_t>(sms) * 2 * kRows * (d + 4) * 4; }
+// header, records (an item that is cut has more than a share of the work: fewer of them than SMs), tasks (one for each item
+// and for every share of the work one more), partial results (at most two for every share)
 int64_t workspace_bytes(int sms, int d, int64_t ctas) {
-  return 16 + 2 * static_cast<int64_t>(sms) * 16 + ctas * static_cast<int64_t>(sizeof(Task)) + parts_bytes(sms, d);
+  return 16 + static_cast<int64_t>(sms) * 16 + ctas * static_cast<int64_t>(sizeof(Task)) + parts_bytes(sms, d);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -986,7 +1037,7 @@ int prompt_attention(const mk_paged_kv *kv, const mk_prompt_args *a, mk_stream s
     if (!p.header) return MK_ERR_NO_MEMORY;
     if (!aligned16(p.header)) return MK_ERR_INVALID_ARG;
     p.records = p.header + 1;
-    p.tasks = reinterpret_cast<Task *>(p.records + 2 * sms);
+    p.tasks = reinterpret_cast<Task *>(p.records + sms);
     p.parts = reinterpret_cast<float *>(p.tasks + shape.ctas);
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
