@@ -16,16 +16,16 @@ namespace mklogits {
 // y = penalties(x, how often the row's history holds the token) + bias, -inf where the mask's bit is 0.
 //
 // Bound by the logits' bytes for a batch, by latency for one row.  A CTA has a slice of a row's vocabulary and a word of
-// shared memory for each of its tokens.  It asks for its logits first (up to four 16-byte loads a thread, all in flight),
+// shared memory for each of its tokens.  It asks for its logits first (one or two 16-byte loads a thread, all in flight),
 // walks the row's whole history and counts the tokens of its slice by integer atomics (any order gives the same counts)
 // while those loads are on their way, stores the logits with the mask, and then goes over the tokens that it has counted:
-// those are few, and a warp that looked at each of its tokens on the way took four times as long (64 rows 28 us).  The one
+// those are few, and a warp that looked at each of its tokens on the way took longer (64 rows of 151936 28 us for 16).  The one
 // who counts a token first writes it down; which order that gives does not matter, as each is adjusted on its own.  Biases
 // set a bit of the word, and who has such a token adds up its entries in their order.
 // ---------------------------------------------------------------------------
 
-constexpr int kThreads = 512;
-constexpr int kMost = 4;       // 16-byte pieces a thread
+constexpr int kThreads = 1024;
+constexpr int kMost = 2;       // 16-byte pieces a thread
 
 struct LogitsParams {
   const void *x;

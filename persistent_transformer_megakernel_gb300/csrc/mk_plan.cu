@@ -6,6 +6,7 @@
 
 #include "../../include/mk.h"
 #include "mk_launch_after.h"
+#include "mk_paged.h"
 #include "mk_mma.cuh"
 
 namespace mkplan {
@@ -15,14 +16,17 @@ namespace mkplan {
 // each sequence its rows, those of the pages that it lacks its part of the free list; a row finds its sequence by
 // bisection of the first sums, a new page of the second.
 //
-// Bound by latency: a few hundred kilobytes at most, behind one chain of length -> sums -> place -> store.  One launch:
-// a cluster of CTAs, each of which forms all the sums in its own shared memory (reading n lengths twice is shorter than
-// passing sums around) and then writes its share of rows and pages.  The cluster meets once between reading and writing,
-// so that totals may be lengths and used_out used.
+// Bound by latency: a megabyte at most, behind one chain of length -> sums -> place -> store.  One launch of CTAs each of
+// which forms all the sums in its own shared memory (reading n lengths again is shorter than passing sums around) and then
+// writes its share of rows and pages.  Where totals are lengths or used_out is used, all reading has to end before the
+// first write: then the CTAs are one cluster, which meets once.  A step of one token each of 64 sequences 2.7 us; 512
+// prompts in 131072 rows 4.5 us (a cluster of 16 CTAs, two rounds of rows and more each, 7.9); 16384 sequences 13.3 (58
+// with a thread's sequences next to each other, 32 to a bank).
 // ---------------------------------------------------------------------------
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxSequences = 16384;
+constexpr int kRowsACta = 4 * kThreads;
 constexpr int smem_of(int n) { return (3 * n + 2) * 4; }
 
 struct PlanParams {
@@ -31,6 +35,7 @@ struct PlanParams {
   int64_t table_stride;
   mkw::Divisor page_size;
   int n, rows, free_count, table_cols;
+  int meet;                    // outputs in the place of inputs: the CTAs are one cluster
   int step;                    // no counts: a token each, row i is sequence i
   int wide;                    // seqs and slots on 16 bytes
 };
@@ -54,8 +59,11 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
   mkw::follow_previous_kernel();
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, n = p.n;
   int *rows_before = smem, *pages_before = smem + n + 1, *len = pages_before + n + 1;
+  // a warp's consecutive sequences, 32 at a time
+  const int per = (n + kThreads - 1) / kThreads * 32, first = min(n, w * per), last = min(n, first + per);
   bool bad = false;
-  for (int i = tid; i < n; i += kThreads) {
+  int64_t rows = 0, pages = 0;
+  for (int i = first + lane; i < last; i += 32) {
     const int l = p.lengths[i], c = l < 0 ? 0 : p.step ? 1 : max(p.counts[i], 0);
     const int64_t total = static_cast<int64_t>(max(l, 0)) + c;
     const int have = pages_of(p, l), need = total > INT32_MAX ? have : pages_of(p, static_cast<int>(total));
@@ -63,39 +71,42 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
     rows_before[i] = c;
     pages_before[i] = c > 0 ? need - have : 0;
     len[i] = l;
+    rows += c, pages += c > 0 ? need - have : 0;
   }
   const int used = p.used[0];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    rows += __shfl_xor_sync(0xffffffffu, rows, o);
+    pages += __shfl_xor_sync(0xffffffffu, pages, o);
+  }
+  if (lane == 0) s_rows[w] = rows, s_pages[w] = pages;
   bad = __syncthreads_or(bad);
 
-  // exclusive sums: a thread's consecutive sequences, its warp's threads, the warps
-  const int per = (n + kThreads - 1) / kThreads, first = min(n, tid * per), last = min(n, first + per);
-  int64_t rows = 0, pages = 0;
-  for (int i = first; i < last; ++i) rows += rows_before[i], pages += pages_before[i];
-  int64_t r = rows, g = pages;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t a = __shfl_up_sync(0xffffffffu, r, o), b = __shfl_up_sync(0xffffffffu, g, o);
-    if (lane >= o) r += a, g += b;
-  }
-  if (lane == 31) s_rows[w] = r, s_pages[w] = g;
-  __syncthreads();
-  r -= rows, g -= pages;
+  // exclusive sums: the warps before, 32 sequences before, the lanes before
+  int64_t r64 = 0, g64 = 0;
   rows = pages = 0;
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) {
-    if (i < w) r += s_rows[i], g += s_pages[i];
+    if (i == w) r64 = rows, g64 = pages;
     rows += s_rows[i], pages += s_pages[i];
   }
   const bool fits = !bad && rows <= p.rows && (pages == 0 || (used >= 0 && used + pages <= p.free_count));
-  for (int i = first; i < last; ++i) {
-    const int c = rows_before[i], q = pages_before[i];
-    rows_before[i] = fits ? static_cast<int>(r) : 0;
-    pages_before[i] = fits ? static_cast<int>(g) : 0;
-    r += c, g += q;
+  int r = static_cast<int>(r64), g = static_cast<int>(g64);   // within 32 bits where the step fits
+  for (int i = first; i < last; i += 32) {
+    const bool there = i + lane < last;
+    const int c = there && fits ? rows_before[i + lane] : 0, q = there && fits ? pages_before[i + lane] : 0;
+    int cs = c, qs = q;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, cs, o), b = __shfl_up_sync(0xffffffffu, qs, o);
+      if (lane >= o) cs += a, qs += b;
+    }
+    if (there) rows_before[i + lane] = fits ? r + cs - c : 0, pages_before[i + lane] = fits ? g + qs - q : 0;
+    r += __shfl_sync(0xffffffffu, cs, 31), g += __shfl_sync(0xffffffffu, qs, 31);
   }
   if (!fits) rows = pages = 0;
   if (tid == 0) rows_before[n] = static_cast<int>(rows), pages_before[n] = static_cast<int>(pages);
-  if (gridDim.x > 1) {
+  if (p.meet) {
     mkw::cluster_arrive();
     mkw::cluster_wait();
   }
@@ -170,8 +181,10 @@ extern "C" int mk_paged_plan(const mk_plan_args *a, mk_stream stream) {
   p.n = a->n, p.rows = a->rows, p.free_count = a->free_count, p.table_cols = a->table_cols;
   p.step = !a->counts && a->n > 0;
   p.wide = ((reinterpret_cast<uintptr_t>(a->seqs) | reinterpret_cast<uintptr_t>(a->slots)) & 15u) == 0;
-  // a CTA more for every 4096 rows (two rounds of four rows a thread), as far as a cluster reaches
-  int ctas = 1;
-  for (int i = 0; i < 4 && r.clusters[i] > 0 && a->rows > 4096 * ctas; ++i) ctas = 2 << i;
-  return mkw::launch_after(&plan_kernel, dim3(ctas), kThreads, smem_of(a->n), reinterpret_cast<cudaStream_t>(stream), p, ctas);
+  // A CTA for every kRowsACta rows, a round of four rows a thread, and no more than run at once (131072 rows 4.5 us; two
+  // rounds 5.3, half a round 5.0); in place one for every 4096, as far as a cluster reaches
+  p.meet = a->totals == a->lengths || a->used_out == a->used;
+  int ctas = p.meet ? 1 : std::max(1, std::min((a->rows - 1) / kRowsACta + 1, mkv::sm_count(&dev)));
+  for (int i = 0; p.meet && i < 4 && r.clusters[i] > 0 && a->rows > 4096 * ctas; ++i) ctas = 2 << i;
+  return mkw::launch_after(&plan_kernel, dim3(ctas), kThreads, smem_of(a->n), reinterpret_cast<cudaStream_t>(stream), p, p.meet ? ctas : 1);
 }
