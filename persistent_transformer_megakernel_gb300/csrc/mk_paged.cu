@@ -562,7 +562,6 @@ struct AttnParams {
   float *parts;        // [grid][2][gr][D + 4]: a row's middle or end (0) and its beginning (1)
   mkw::Divisor page_size;
   int n, hq, hkv, group, n_pages, capacity, window;   // capacity: slots of a table row
-  int sinks;                 // first tokens that a window leaves visible
   mkw::Divisor chunks;       // of 16 query heads
   mkw::Divisor blocks, vh;   // head blocks of 16 query heads a kv head, virtual heads hkv * blocks
   int gr;              // query heads of a block: min(group, 16)
@@ -571,6 +570,7 @@ struct AttnParams {
   int dense;           // a page's slots of a head lie one behind the other
   float scale;
   float shrink, grow;  // what a probability is multiplied by on the way into the sums, and its inverse: powers of two
+  int sinks;                 // first tokens that a window leaves visible
 };
 
 template <int D, bool FP8>
@@ -606,18 +606,18 @@ struct Pair<__nv_bfloat16> {
 
 // tiles of a row: those that hold any of its slots [lo, hi), before them, where a window leaves first tokens visible,
 // `head` tiles of those, and the cost of all, the row's start included
+template <bool SINKS>
 struct Span {
-  int lo, hi, head, skip, count, cost;
-  __device__ __forceinline__ int number(int j) const { return j < head ? j : j + skip; }   // of the row's jth tile
+  int lo, hi, skip, count, cost, head;
+  __device__ __forceinline__ int number(int j) const { return SINKS && j < head ? j : j + skip; }   // of the row's jth tile
 };
-template <int POS>
-__device__ __forceinline__ Span span_of(const AttnParams &p, int len) {
-  Span s;
+template <int POS, bool SINKS>
+__device__ __forceinline__ Span<SINKS> span_of(const AttnParams &p, int len) {
+  Span<SINKS> s;
   s.hi = len > 0 && len <= p.capacity ? len : 0;
   s.lo = p.window > 0 && s.hi > p.window ? s.hi - p.window : 0;
-  const int first = s.lo / POS;
-  s.head = min((p.sinks + POS - 1) / POS, first);
-  s.skip = first - s.head;
+  s.skip = s.lo / POS;
+  if (SINKS) s.head = min((p.sinks + POS - 1) / POS, s.skip), s.skip -= s.head;
   s.count = s.hi > 0 ? (s.hi + POS - 1) / POS - s.skip : 0;
   s.cost = s.count ? s.count + p.row_cost : 0;
   return s;
@@ -758,8 +758,9 @@ __device__ __forceinline__ float column_sum(float x) {
   return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
-// HB: blocks of 8 query heads
-template <class T, bool FP8, int D, int HB>
+// HB: blocks of 8 query heads; SINKS: first tokens may be visible (a kernel of its own: the calls without them took up to 5%
+// longer in one that looks, 32 rows of 128 heads on 8 in fp32 84.6 us for 80.2)
+template <class T, bool FP8, int D, int HB, bool SINKS>
 __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_constant__ AttnParams p) {
   using TL = Tile<D, FP8>;
   using Op = std::conditional_t<FP8, mkw::FP16Op, mkw::BF16Op>;
@@ -779,12 +780,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
 
   // ---- the warp's range: where it starts, and how much it covers -------------------
   int row = 0, vh = 0, tile = 0, left = 0;                   // left: units from the tile the producer stands at to the range's end
-  Span sp{0, 0, 0, 0, 0, 0};
+  Span<SINKS> sp{0, 0, 0, 0, 0, 0};
   int per = 0, units = 0, ctas = 0;
   if (p.way == kByCluster) {
     mkw::cluster_arrive();                                   // (to be waited for before the others' memory is written)
     vh = cta / p.cluster;                                    // the cluster's kv head (and head block)
-    sp = span_of<POS>(p, p.lengths[0]);
+    sp = span_of<POS, SINKS>(p, p.lengths[0]);
     const int i = cta % p.cluster * kWarps + w;
     const Shares shares(sp.count, p.cluster * kWarps);
     tile = shares.begin(i);
@@ -797,7 +798,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
     int mine = 0;
     for (int i = 0; i < per; ++i) {
       const int r = tid * per + i;
-      if (r < p.n) mine += span_of<POS>(p, p.lengths[r]).cost;
+      if (r < p.n) mine += span_of<POS, SINKS>(p, p.lengths[r]).cost;
     }
     int incl = mine;
 #pragma unroll
@@ -848,11 +849,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
       a += __popc(__ballot_sync(0xffffffffu, lane < 8 && s_scan[a + (lane & 7)] <= x)) - 1;
       int at = s_scan[a];
       row = a * per;
-      sp = span_of<POS>(p, p.lengths[row]);
+      sp = span_of<POS, SINKS>(p, p.lengths[row]);
 #pragma unroll 1
       while (at + sp.cost <= x) {
         at += sp.cost;
-        sp = span_of<POS>(p, p.lengths[++row]);
+        sp = span_of<POS, SINKS>(p, p.lengths[++row]);
       }
       const int rest = u - at * static_cast<int>(p.vh.value), cost = sp.cost;
       vh = rest / cost;
@@ -876,14 +877,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
     const int pos = sp.number(tile) * POS + lane, col = p.page_size.quotient(pos);
     slot = pos - col * static_cast<int>(p.page_size.value);
     page = -1;
-    if (lane < POS && (pos >= sp.lo || pos < p.sinks) && pos < sp.hi) page = p.table[row * p.table_stride + col];
+    if (lane < POS && (pos >= sp.lo || (SINKS && pos < p.sinks)) && pos < sp.hi) page = p.table[row * p.table_stride + col];
   };
   if (left > 0) look_up();
   int in_stage = 0;                                          // the producer's stage
   const int r0 = lane / TL::CPR, place = lane % TL::CPR;     // this lane's first slot of a tile and its place in every row
   auto produce = [&]() {
     const int pos0 = sp.number(tile) * POS, pos = pos0 + lane;
-    const bool want = lane < POS && (pos >= sp.lo || pos < p.sinks) && pos < sp.hi;
+    const bool want = lane < POS && (pos >= sp.lo || (SINKS && pos < p.sinks)) && pos < sp.hi;
     const bool fine = static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages);
     const unsigned have = __ballot_sync(0xffffffffu, want && fine);
     const bool bad = __any_sync(0xffffffffu, want && !fine);
@@ -925,7 +926,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
       if (vh == static_cast<int>(p.vh.value)) {
         vh = kvh = 0;
         if (left > 0) {
-          do sp = span_of<POS>(p, p.lengths[++row]);
+          do sp = span_of<POS, SINKS>(p, p.lengths[++row]);
           while (sp.count == 0);
         }
       }
@@ -964,7 +965,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
 #pragma unroll 1
   for (int i = cta * kWarps + w; i < p.n * static_cast<int>(p.chunks.value); i += gridDim.x * kWarps) {
     const int r = p.chunks.quotient(i), h0 = 16 * (i - r * static_cast<int>(p.chunks.value)), len = p.lengths[r];
-    if (len < 0 || span_of<POS>(p, len).count > 0) continue;
+    if (len < 0 || span_of<POS, SINKS>(p, len).count > 0) continue;
     const float l = len == 0 ? 0.f : NAN;
     if (len > 0 && lane == 0) report(p.status, MK_ERR_BAD_PAGE);
 #pragma unroll 1
@@ -1082,7 +1083,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
         }
       }
     }
-    const bool edge = (ti.pos < ti.lo && ti.pos + POS > p.sinks) || ti.pos + POS > ti.hi;
+    bool edge = ti.pos < ti.lo || ti.pos + POS > ti.hi;
+    if constexpr (SINKS) edge = edge && (ti.pos + POS > p.sinks || ti.pos + POS > ti.hi);
     float alpha[HB][2];
     uint32_t pf[TP][PN][HB][2];
 #pragma unroll
@@ -1095,7 +1097,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
           float s = (sc[nb][hb][c] + sl[nb][hb][c]) * mult[hb][c & 1];
           if (edge) {
             const int pos = ti.pos + 16 * nb + g + (c >> 1) * 8;
-            if ((pos < ti.lo && pos >= p.sinks) || pos >= ti.hi) s = -INFINITY;
+            if constexpr (SINKS) {
+              if ((pos < ti.lo && pos >= p.sinks) || pos >= ti.hi) s = -INFINITY;
+            } else {
+              if (pos < ti.lo || pos >= ti.hi) s = -INFINITY;
+            }
           }
           sc[nb][hb][c] = s;
           x[c & 1] = fmaxf(x[c & 1], s);
@@ -1275,8 +1281,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
             // the last CTA with tiles of this row: the one whose range holds the row's last unit
             int before_row = s_scan[row_of / per];
 #pragma unroll 1
-            for (int k = row_of / per * per; k < row_of; ++k) before_row += span_of<POS>(p, p.lengths[k]).cost;
-            const int cost = span_of<POS>(p, p.lengths[row_of]).cost;
+            for (int k = row_of / per * per; k < row_of; ++k) before_row += span_of<POS, SINKS>(p, p.lengths[k]).cost;
+            const int cost = span_of<POS, SINKS>(p, p.lengths[row_of]).cost;
             p.records[cta] = make_int4(row_of, vh_of, Shares(units, ctas).of(before_row * static_cast<int>(p.vh.value) + (vh_of + 1) * cost - 1), 1);
           }
         }
@@ -1352,14 +1358,14 @@ int seen_at_most(const AttnParams &p) {
   return p.window > 0 ? static_cast<int>(std::min<int64_t>(static_cast<int64_t>(p.window) + p.sinks, p.capacity)) : p.capacity;
 }
 
-template <class T, bool FP8, int D, int HB>
+template <class T, bool FP8, int D, int HB, bool SINKS>
 int launch_heads(AttnParams &p, const Workspace &ws, int grid, int dev, cudaStream_t s) {
   using TL = Tile<D, FP8>;
   static mkw::Ready ready[mkw::kMaxDevices];
-  const auto fn = &attend_kernel<T, FP8, D, HB>;
+  const auto fn = &attend_kernel<T, FP8, D, HB, SINKS>;
   mkw::Ready &r = ready[dev];
   if (!r.get(reinterpret_cast<const void *>(fn), kAttnThreads, kMaxSmem)) return MK_ERR_CUDA;
-  const int64_t tiles = seen_at_most(p) / TL::POS + (p.sinks > 0 ? 3 : 2);   // of a row at most
+  const int64_t tiles = seen_at_most(p) / TL::POS + (SINKS ? 3 : 2);   // of a row at most
   p.way = tiles <= kShortTiles ? kWhole : kJoined;
   p.cluster = 1;
   if (p.n == 1) {
@@ -1384,7 +1390,8 @@ int launch_heads(AttnParams &p, const Workspace &ws, int grid, int dev, cudaStre
 
 template <class T, bool FP8, int D>
 int launch_attend(AttnParams &p, const Workspace &ws, int grid, int dev, cudaStream_t s) {
-  return p.gr <= 8 ? launch_heads<T, FP8, D, 1>(p, ws, grid, dev, s) : launch_heads<T, FP8, D, 2>(p, ws, grid, dev, s);
+  if (p.sinks > 0) return p.gr <= 8 ? launch_heads<T, FP8, D, 1, true>(p, ws, grid, dev, s) : launch_heads<T, FP8, D, 2, true>(p, ws, grid, dev, s);
+  return p.gr <= 8 ? launch_heads<T, FP8, D, 1, false>(p, ws, grid, dev, s) : launch_heads<T, FP8, D, 2, false>(p, ws, grid, dev, s);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
