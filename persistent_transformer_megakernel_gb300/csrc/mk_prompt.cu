@@ -1027,7 +1027,7 @@ int prompt_attention(const mk_paged_kv *kv, const mk_prompt_args *a, mk_stream s
   // blocks of an item: of all its row's tokens, or of the window, its own rows and the first tokens
   const int64_t span = p.window > 0 ? static_cast<int64_t>(p.window) + 2 * p.tokens + p.sinks + 3 * kBlock : slots + kBlock;
   p.joins = std::min<int64_t>(span, slots + kBlock) / kBlock > kLeastBlocks;
-  // (77 tokens: TODO us, with a task list TODO; the same 32 times TODO and TODO)
+  // (77 tokens 8.8 us, with a task list 12.9; the same 32 times 17.7 and 22.0)
   p.direct = !p.joins && p.n <= 32;
   const int64_t bytes = workspace_bytes(sms, kv->head_dim, shape.ctas);
   if (!ask && (!a->workspace || a->workspace_bytes < bytes)) return MK_ERR_INVALID_ARG;
