@@ -422,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     mbar_init(ofull, kMmaWarps);
     fence_mbar_init();
   }
+  __syncthreads();
   mkw::wait_for_previous_kernel();
   Task task;
   if (p.direct) {
@@ -497,10 +498,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   }
   // (a factor of 0 would make the -infinity of a hidden score NaN; the smallest normal one does what 0 does)
   to_log2 = fmaxf(to_log2, 1.2e-38f);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
+  uint32_t tmem = 0;
+  if (warp < kSoftWarps + kMmaWarps) {                     // (the copies begin meanwhile)
+    tc_fence_before();
+    asm volatile("barrier.sync 1, %0;" ::"n"(32 * (kSoftWarps + kMmaWarps)) : "memory");
+    tc_fence_after();
+    tmem = __shfl_sync(0xffffffffu, *tslot, 0);
+  }
 
   if (warp >= kSoftWarps + kMmaWarps) {
     // ---- copies: a lane looks up a position of a block ---------------------------------------
@@ -527,10 +531,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (; told < upto; ++told)
           if (lane == 0) mbar_arrive(&full[told % kSlots]);
       };
+      const int64_t slot_bytes = p.slot_stride * ES, row_step = ROWS * slot_bytes, lane_off = lane / PIECES * slot_bytes + lane % PIECES * 16;
       int64_t next = b0 < b1 ? look_up(b0, cw * 32 + lane) : -1;
       for (int b = b0; b < b1 && ok; ++b) {
         const int64_t at = next;
         const bool bad = at == -2;
+        // Whether 16 positions each lie one behind the other, as in a page of as many slots: then a copy's address is the one
+        // before and a step (one prompt of 8192 tokens 195 us; each address from its position's own offset 207).  (An 8-bit
+        // cache, whose rows are half as long, gains nothing by it.)
+        const int64_t leading = __shfl_sync(0xffffffffu, at, lane & 16);
+        const bool runs = __all_sync(0xffffffffu, at >= 0 && at == leading + (lane & 15) * slot_bytes);
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv, ++n_tiles) {
           const int slot = n_tiles % kSlots;
@@ -549,11 +559,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           const unsigned char *base = static_cast<const unsigned char *>(kv ? p.v : p.k);
           unsigned char *to = KVs + slot * LY::TILE;
           const uint32_t to_at = smem_addr(to);
+          if (runs) {
 #pragma unroll
-          for (int i = 0; i < 32 / ROWS; ++i) {
-            const int rr = i * ROWS + lane / PIECES, c = lane % PIECES;
-            const int64_t o = __shfl_sync(0xffffffffu, at, rr);
-            mkw::cp_async16(to_at + piece_at(cw * 32 + rr, c), base + (o < 0 ? 0 : o + c * 16), o >= 0);
+            for (int half = 0; half < 2; ++half) {
+              const unsigned char *from = base + __shfl_sync(0xffffffffu, at, 16 * half) + lane_off;
+#pragma unroll
+              for (int i = 0; i < 16 / ROWS; ++i, from += row_step)
+                mkw::cp_async16(to_at + piece_at(cw * 32 + 16 * half + i * ROWS + lane / PIECES, lane % PIECES), from);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32 / ROWS; ++i) {
+              const int rr = i * ROWS + lane / PIECES, c = lane % PIECES;
+              const int64_t o = __shfl_sync(0xffffffffu, at, rr);
+              mkw::cp_async16(to_at + piece_at(cw * 32 + rr, c), base + (o < 0 ? 0 : o + c * 16), o >= 0);
+            }
           }
           mkw::cp_async_commit();
           if (kv == 0) {
@@ -1027,7 +1047,7 @@ int prompt_attention(const mk_paged_kv *kv, const mk_prompt_args *a, mk_stream s
   // blocks of an item: of all its row's tokens, or of the window, its own rows and the first tokens
   const int64_t span = p.window > 0 ? static_cast<int64_t>(p.window) + 2 * p.tokens + p.sinks + 3 * kBlock : slots + kBlock;
   p.joins = std::min<int64_t>(span, slots + kBlock) / kBlock > kLeastBlocks;
-  // (77 tokens 8.8 us, with a task list 12.9; the same 32 times 17.7 and 22.0)
+  // (77 tokens 8.5 us, with a task list 12.6; the same 32 times 17.9 and 22.2)
   p.direct = !p.joins && p.n <= 32;
   const int64_t bytes = workspace_bytes(sms, kv->head_dim, shape.ctas);
   if (!ask && (!a->workspace || a->workspace_bytes < bytes)) return MK_ERR_INVALID_ARG;
