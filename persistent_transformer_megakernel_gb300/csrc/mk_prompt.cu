@@ -240,6 +240,11 @@ __global__ void __launch_bounds__(kTaskThreads) task_kernel(const __grid_constan
       total += s_warps[i];
     }
     if (pass == 0) {
+      if (total > INT32_MAX / 2) {                         // (starts that overlap; the same for all threads)
+        if (tid == 0) report(p.status, MK_ERR_BAD_PAGE);
+        for (int i = a; i < b; ++i) before[i] = 0;
+        at = total = 0;
+      }
       int pairs = static_cast<int>(at);
       for (int i = a; i < b; ++i) {
         const int c = before[i];

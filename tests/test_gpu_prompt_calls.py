@@ -187,3 +187,36 @@ def test_what_is_written_counts_as_changed_and_no_gradients():
             f(leaf)
         with torch.no_grad():
             f(leaf)
+
+
+def test_more_than_2_to_the_31_elements():
+    # an input, a result and rows of logits that a 32-bit index does not reach, at rows before and behind that border
+    g = torch.Generator(device="cuda").manual_seed(5)
+    m, k = (1 << 31) // 2048 + 300, 2048
+    rows = [0, 1, (1 << 31) // k - 1, (1 << 31) // k, (1 << 31) // k + 1, m - 1]
+    x = torch.zeros((m, k), dtype=BF16, device="cuda")
+    x[rows] = torch.randn((len(rows), k), generator=g, device="cuda").to(BF16)
+    codes, scales = mk.quantize_fp8(x)
+    want, want_scales = mk.quantize_fp8(x[rows])
+    assert torch.equal(codes.view(torch.uint8)[rows], want.view(torch.uint8)) and torch.equal(scales[rows], want_scales)
+    assert not codes.view(torch.uint8)[2:500].any() and (scales[2:500] == 1).all()   # (a block of zeros)
+    w, ws = mk.quantize_fp8_weight(torch.randn((2056, 2048), generator=g, device="cuda"))
+    few = mk.matmul_fp8(want, want_scales, w, ws, dtype=torch.float32)
+    big = mk.matmul_fp8(codes, scales, w, ws, dtype=torch.float32)     # 8.6 GB and more
+    # (sums of few tiles are shared by CTAs: another order, at most 2048 / 128 partial sums of 128 terms)
+    bound = (want.float().abs() * want_scales.repeat_interleave(128, 1)) @ (w.float().abs() * ws.repeat_interleave(128, 1)[torch.arange(2056, device="cuda") // 128]).t()
+    assert ((big[rows] - few).abs() <= 40 * 2.0 ** -23 * bound + 1e-30).all() and not big[2:500].any()
+    # the same into a result whose rows are not on 16 bytes, where numbers leave one by one
+    wide = torch.zeros((m, 2057), dtype=torch.float32, device="cuda")
+    mk.matmul_fp8(codes, scales, w, ws, out=wide[:, :2056])
+    assert torch.equal(wide[:, :2056][rows], big[rows]) and not wide[:, 2056].any()
+    del x, codes, scales, big, wide
+    n, v = (1 << 31) // 50000 + 5, 50000
+    logits = torch.zeros((n, v), dtype=BF16, device="cuda")
+    at = [0, 7, n - 6, n - 5, n - 1]
+    logits[at] = torch.randn((len(at), v), generator=g, device="cuda").to(BF16)
+    ids = torch.randint(0, v, (n, 30), generator=g, device="cuda", dtype=torch.int32)
+    ones = torch.full((n,), 1.25, device="cuda")
+    got = mk.adjust_logits(logits, tokens=ids, repetition=ones, presence=ones, frequency=ones)
+    part = mk.adjust_logits(logits[at], tokens=ids[at], repetition=ones[:5], presence=ones[:5], frequency=ones[:5])
+    assert torch.equal(got[at], part)
