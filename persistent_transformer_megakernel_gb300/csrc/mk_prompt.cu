@@ -832,7 +832,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     float *part = whole ? nullptr : p.parts + ((static_cast<int64_t>(task.slot) * 2 + tile) * kRows + r) * (D + 4);
     __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (x.row + index) * p.out_row + (head0 + head) * p.out_head;
     const float inv = task.outside || !ok ? NAN : !whole ? 1.f : l == 0.f ? 0.f : __frcp_rn(l) * vs;
-    bool strange = false;
+    // whether the row is to be worked on alone: a sum or an element of O that is not finite
+    bool strange = !(fabsf(l) < INFINITY);
     // to where the warp's queries were, and from there a row's bytes together: rounded results, or half of fp32 ones at a time
     constexpr int PIECES = D / 8, ROWS = 32 / PIECES;
     const unsigned alive = __ballot_sync(0xffffffffu, live);
@@ -864,13 +865,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const bool full_rows = whole ? c + 32 == D : (c + 32) % (D / 2) == 0;
       if (full_rows) {
         __syncwarp();
+        // (an output may be its query, which row_alone reads again)
+        const unsigned put = alive & ~__ballot_sync(0xffffffffu, strange && whole && ok && !task.outside);
         const uint64_t to = whole ? reinterpret_cast<uint64_t>(dst) : reinterpret_cast<uint64_t>(part + (c + 32 - D / 2));
 #pragma unroll 4
         for (int i = 0; i < 32; i += ROWS) {
           const int rr = i + lane / PIECES, piece = lane % PIECES;
           const uint64_t row_at = __shfl_sync(0xffffffffu, to, rr);
           const uint4 w = *reinterpret_cast<const uint4 *>(mine + piece_at((warp & 3) * 32 + rr, piece));
-          if (alive >> rr & 1) *reinterpret_cast<uint4 *>(row_at + piece * 16) = w;
+          if (put >> rr & 1) *reinterpret_cast<uint4 *>(row_at + piece * 16) = w;
         }
         __syncwarp();
       }
@@ -881,7 +884,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       if (!whole) part[D] = m, part[D + 1] = l;
       else if (p.lse) p.lse[static_cast<int64_t>(x.row + index) * p.hq + head0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     }
-    strange |= !(fabsf(l) < INFINITY);
     for (unsigned rest = __ballot_sync(0xffffffffu, strange && live && ok && !task.outside); rest; rest &= rest - 1u) {
       const int of = __ffs(rest) - 1;
       const int row = x.row + __shfl_sync(0xffffffffu, index, of), hd = head0 + __shfl_sync(0xffffffffu, head, of);

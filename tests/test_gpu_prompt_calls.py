@@ -220,3 +220,19 @@ def test_more_than_2_to_the_31_elements():
     got = mk.adjust_logits(logits, tokens=ids, repetition=ones, presence=ones, frequency=ones)
     part = mk.adjust_logits(logits[at], tokens=ids[at], repetition=ones[:5], presence=ones[:5], frequency=ones[:5])
     assert torch.equal(got[at], part)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+def test_in_place_where_rows_are_worked_on_again(cache):
+    # values behind a row's own token that are no numbers, so that its first result is none either
+    g = torch.Generator().manual_seed(11)
+    kc, vc = (torch.randn((8, 2, 16, 64), generator=g).to(BF16) for _ in range(2))
+    vc[5:] = float("nan")
+    kc, vc = kc.to(cache).cuda(), vc.to(cache).cuda()
+    q = torch.randn((100, 4, 64), generator=g).to(BF16).cuda()
+    table, starts, lengths = torch.arange(8, dtype=torch.int32, device="cuda").view(1, 8), i32([0, 100]), i32([128])
+    want = mk.paged_prompt_attention(q, kc, vc, table, starts, lengths)
+    assert torch.isfinite(want[:50]).all()
+    got = q.clone()
+    mk.paged_prompt_attention(got, kc, vc, table, starts, lengths, out=got)
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
