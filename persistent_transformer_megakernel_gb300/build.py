@@ -20,7 +20,7 @@ MODULE = os.path.join(HERE, "_mktorch.so")
 SOURCES = ["mk_kernels_d128.cu", "mk_kernels_hidden1024.cu", "mk_kernels_hidden2048.cu", "mk_kernels_d64.cu",
            "mk_host.cu", "mk_embed.cu", "mk_prefill.cu", "mk_gemm.cu", "mk_pfattn.cu",
            "mk_paged.cu", "mk_q4.cu", "mk_q4_bf16.cu",
-           "mk_plan.cu", "mk_prompt.cu", "mk_fp8.cu", "mk_logits.cu"]
+           "mk_plan.cu", "mk_prompt.cu", "mk_prompt_fp8.cu", "mk_fp8.cu", "mk_logits.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 
