@@ -140,9 +140,9 @@ __device__ __forceinline__ int items_of(const PromptParams &p, int i, bool &bad)
 
 // The most blocks of a task: an equal share of all of them, twice that, or no limit, whichever promises the earliest end.  In
 // blocks: a task has kBegin of them to set up and store, a join takes kJoining.  Tasks that run all at once end with the
-// longest; else the SMs' equal shares, and half a task for what is uneven (long ones begin first).  (4 tokens behind 30000: cut 35 us, whole 274; 2000
-// tokens: whole 34, cut to shares 46)
-// (fp32 numbers, in the same order everywhere: 64-bit divisions took each CTA a microsecond)
+// longest; else the SMs' equal shares, and half a task for what is uneven (long ones begin first).  4 tokens behind 30000:
+// cut 35 us, whole 274; 2000 tokens: whole 34, cut to shares 46.  (fp32 numbers, the same everywhere: 64-bit divisions took
+// each CTA a microsecond.)
 __device__ __forceinline__ int share_of(const PromptParams &p, float blocks) {
   return max(kLeastBlocks, static_cast<int>(fminf(blocks / p.sms * 1.0001f, 1e9f)) + 1);   // (no less than the share)
 }

@@ -236,3 +236,45 @@ def test_in_place_where_rows_are_worked_on_again(cache):
     got = q.clone()
     mk.paged_prompt_attention(got, kc, vc, table, starts, lengths, out=got)
     assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("window", [0, 1500])
+def test_few_sequences_and_the_same_among_many(cache, window):
+    # the tasks of few sequences are found otherwise than those of many: empty ones behind them make many of few
+    g = torch.Generator().manual_seed(21)
+    kc, vc = (torch.randn((500, 2, 16, 64), generator=g).to(cache).cuda() for _ in range(2))
+    for new, old in (([300, 40, 1, 0, 200], [1000, 3000, 5, 70, 0]), ([4], [7000]), ([1, 1, 1], [7000, 0, 2500]), ([900], [0]), ([2000, 30], [0, 4000])):
+        lengths = [a + b for a, b in zip(new, old)]
+        rows = sum(new)
+        starts = [sum(new[:i]) for i in range(len(new) + 1)]
+        table = torch.randint(0, 500, (len(new) + 40, 450), generator=g).int().cuda()
+        q = torch.randn((rows, 4, 64), generator=g).to(BF16).cuda()
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        few_lse, many_lse = (torch.full((rows, 4), -7.0, device="cuda") for _ in range(2))
+        few = mk.paged_prompt_attention(q, kc, vc, table, i32(starts), i32(lengths), window=window, sinks=4, lse=few_lse, status=status)
+        many = mk.paged_prompt_attention(q, kc, vc, table, i32(starts + [rows] * 40), i32(lengths + [9] * 40), window=window, sinks=4, lse=many_lse, status=status)
+        mk.check_status(status)
+        # weights and results are rounded to bf16 in both, each by 2^-8 at most, and a result is no larger than the largest value
+        assert ((few.double() - many.double()).abs() <= 4 * 2.0 ** -8 * vc.float().abs().max()).all()
+        # lse: tokens of a row summed in other parts, (64 + n / 32) 2^-23 each way, and 2^-22 of it for the logarithm
+        assert ((few_lse.double() - many_lse.double()).abs() <= 2 * (64 + max(lengths) / 32) * 2.0 ** -23 + 2.0 ** -20 * many_lse.abs()).all()
+
+
+def test_starts_that_decrease_among_long_contexts():
+    g = torch.Generator().manual_seed(22)
+    kc, vc = (torch.randn((400, 2, 16, 64), generator=g).to(BF16).cuda() for _ in range(2))
+    table = torch.randint(0, 400, (5, 400), generator=g).int().cuda()
+    q = torch.randn((400, 4, 64), generator=g).to(BF16).cuda()
+    want = mk.paged_prompt_attention(q, kc, vc, table[:2], i32([0, 150, 300]), i32([5000, 3000]))
+    for starts, lengths in (([0, 150, 300, 100, 80, 80], [5000, 3000, 900, 900, 900]), ([0, 150, 300, 500, 400, 380], [5000, 3000, 900, 900, 900]),
+                            ([0, 150, 300, 300, 300, 300], [5000, 3000, -1, 7000, 2 ** 31 - 1])):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = mk.paged_prompt_attention(q, kc, vc, table, i32(starts), i32(lengths), status=status)
+        # sequences are cut otherwise among others: as above
+        assert ((got[:300].double() - want[:300].double()).abs() <= 4 * 2.0 ** -8 * vc.float().abs().max()).all()
+        if starts[-1] < 300 or starts[3] > 400:
+            with pytest.raises(mk.MKError):
+                mk.check_status(status)
+        else:
+            mk.check_status(status)
