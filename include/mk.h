@@ -331,8 +331,10 @@ int mk_embed_sum_noalloc(const void *books, int32_t n_books, int32_t book_rows, 
 
 /* ---- paged KV cache: several sequences ------------------------------------
  * A decode step of many sequences at once, for callers that hold the layer loop
- * themselves: the three operators below are one layer's attention block
- * (mk_matvec_q4 for the projections, mk_paged_append, mk_paged_attention), and
+ * themselves: the operators below are one layer's attention block
+ * (mk_matvec_q4 or mk_matmul_fp8 for the projections, mk_paged_append,
+ * mk_paged_attention or, for prompts, mk_paged_prompt_attention) and what is
+ * before and behind a step (mk_paged_plan, mk_adjust_logits), and
  * mk_export_kv hands them a context that mk_prefill or mk_decode has built.  The
  * pages cover one sequence per kernel only; these entry points have no
  * counterpart there.
