@@ -113,7 +113,7 @@ PyObject *paged_append(PyObject *const *o) {
   at::Tensor made;
   if (o[A_Q] && !o[A_QOUT]) {
     const at::Tensor &q = THPVariable_Unpack(o[A_Q]);
-    made = at::empty(q.sizes(), q.options());
+    made = fresh(q.sizes(), q.scalar_type(), q);
     a.q_out = made.data_ptr();
     a.out_row = made.stride(0);
     a.out_head = made.stride(1);
@@ -191,7 +191,7 @@ PyObject *paged_attention(PyObject *const *o) {
   at::Tensor made;
   if (!o[T_OUT]) {
     const at::Tensor &q = THPVariable_Unpack(o[T_Q]);
-    made = at::empty(q.sizes(), q.options());
+    made = fresh(q.sizes(), q.scalar_type(), q);
     a.out = made.data_ptr();
     a.out_row = made.stride(0);
     a.out_head = made.stride(1);
@@ -274,7 +274,8 @@ PyObject *matvec_q4(PyObject *const *o) {
   const Launch on(dev, o[M_STREAM]);
   at::Tensor made;
   if (!o[M_OUT]) {
-    made = at::empty({a.m, a.n}, THPVariable_Unpack(o[M_X]).options());
+    const at::Tensor &x = THPVariable_Unpack(o[M_X]);
+    made = fresh({a.m, a.n}, x.scalar_type(), x);
     a.y = made.data_ptr();
     a.y_row = a.n;
   }

@@ -4,6 +4,8 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/Context.h>
+#include <ATen/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDACachingAllocator.h>
@@ -332,6 +334,12 @@ struct Memory {
     return m.held.get();
   }
 };
+
+// A new tensor on the current device, as at::empty makes it, without the way through the dispatcher (half a microsecond less a call).
+inline at::Tensor fresh(c10::IntArrayRef sizes, at::ScalarType type, const at::Tensor &like) {
+  if (at::globalContext().deterministicAlgorithms()) return at::empty(sizes, like.options().dtype(type));   // (which may fill it)
+  return at::Tensor(at::detail::empty_generic(sizes, c10::cuda::CUDACachingAllocator::get(), c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt));
+}
 
 // ---- functions of the module ----------------------------------------------------------
 

@@ -8,13 +8,13 @@ namespace mkt {
 namespace prompts {
 
 // New results of a call, one behind the other in one allocation, each on 16 bytes: an allocation costs the host 1.2 us, what
-// a tensor around a part of it costs is a tenth of that (paged_plan 7.8 -> 5.1 us a call, quantize_fp8 4.7 -> 4.1).
+// a tensor around a part of it costs is a tenth of that (paged_plan 7.8 -> 5.1 us a call, quantize_fp8 4.7 -> 4.1, when allocations took that long).
 class Results {
  public:
   // room for a result, before the allocation
   bool any() const { return bytes_ > 0; }
   void want(int64_t bytes) { bytes_ += (bytes + 15) / 16 * 16; }
-  void allocate(const at::Tensor &like) { memory_ = at::empty({bytes_}, like.options().dtype(at::kByte)); }
+  void allocate(const at::Tensor &like) { memory_ = fresh({bytes_}, at::kByte, like); }
   // the next result, in the order of the wants
   at::Tensor take(c10::IntArrayRef sizes, at::ScalarType type) {
     at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(memory_.storage()), memory_.key_set(), c10::scalarTypeToTypeMeta(type));
@@ -205,7 +205,7 @@ PyObject *paged_prompt_attention(PyObject *const *o) {
   at::Tensor made;
   if (!o[T_OUT]) {
     const at::Tensor &q = THPVariable_Unpack(o[T_Q]);
-    made = at::empty(q.sizes(), q.options());
+    made = fresh(q.sizes(), q.scalar_type(), q);
     a.out = made.data_ptr();
     a.out_row = made.stride(0);
     a.out_head = made.stride(1);
@@ -378,7 +378,7 @@ PyObject *matmul_fp8(PyObject *const *o) {
   const Launch on(dev, o[M_STREAM]);
   at::Tensor made;
   if (!o[M_OUT]) {
-    made = at::empty({a.m, a.n}, THPVariable_Unpack(o[M_X]).options().dtype(a.dtype == MK_F32 ? at::kFloat : at::kBFloat16));
+    made = fresh({a.m, a.n}, a.dtype == MK_F32 ? at::kFloat : at::kBFloat16, THPVariable_Unpack(o[M_X]));
     a.y = made.data_ptr();
     a.y_row = a.n;
   }
@@ -453,7 +453,8 @@ PyObject *adjust_logits(PyObject *const *o) {
   const Launch on(dev, o[L_STREAM]);
   at::Tensor made;
   if (!o[L_OUT]) {
-    made = at::empty({a.n, a.vocab}, THPVariable_Unpack(o[L_X]).options());
+    const at::Tensor &x = THPVariable_Unpack(o[L_X]);
+    made = fresh({a.n, a.vocab}, x.scalar_type(), x);
     a.out = made.data_ptr();
     a.out_row = a.vocab;
   }
