@@ -99,10 +99,11 @@ int prompt_attention(const mk_paged_kv *kv, const mk_prompt_args *a, mk_stream s
   // one tile a CTA where that leaves no SM with more to do (1000 tokens 16.0 us, two 18.9); not where items are cut, as two
   // tiles share their blocks (200 tokens behind 8000: 54 us, two 29)
   if (shape.few && !p.joins) p.item = p.tokens;
-  p.ctas = static_cast<int>(most_items(p.n, p.rows, p.item) * p.vh) + sms;
+  const int items = static_cast<int>(most_items(p.n, p.rows, p.item) * p.vh);
+  p.ctas = items + (p.joins ? sms : 0);
   // No list for few items of few sequences: a CTA that finds its own task takes longer, and a kernel before it more (77 tokens
-  // 8.2 us, with a list 12.6; 2000 tokens 34 and 40; from 3 CTAs an SM on the list is quicker: 8192 tokens 195, without 200).
-  p.how = p.n > 32 ? kListed : !p.joins ? kWhole : p.ctas <= 3 * sms ? kCut : kListed;
+  // 7.8 us, with a list 12.6; 2000 tokens 34 and 40; from two items an SM on the list is quicker: 8192 tokens 195, without 200).
+  p.how = p.n > 32 ? kListed : !p.joins ? kWhole : items <= 2 * sms ? kCut : kListed;
   const int64_t bytes = workspace_bytes(sms, kv->head_dim, shape.ctas);
   if (!ask && (!a->workspace || a->workspace_bytes < bytes)) return MK_ERR_INVALID_ARG;
   if (p.how != kWhole) {

@@ -36,7 +36,7 @@ using namespace mktc;
 // products alone 137 at the rate of a long matrix product, and their pipe is 52 % busy), over an e4m3 cache 204 us, with
 // heads of 64 193; 32768 tokens take 2.5 ms (1760 TFLOP/s), 2000 34 us.  Per 64 scores a row waits for the products, for the exponential's
 // pipe and for tensor memory in turn, and tensor memory (512 columns: 2 x 128 of scores, 2 x 128 of O) has no room for a third
-// place of scores.  Few rows are bound by latency: 77 tokens 8.2 us.
+// place of scores.  Few rows are bound by latency: 77 tokens 7.8 us.
 // ---------------------------------------------------------------------------
 
 constexpr int kSoftWarps = 8, kMmaWarps = 2, kCopyWarps = 4, kWarps = kSoftWarps + kMmaWarps + kCopyWarps, kThreads = 32 * kWarps;
