@@ -278,3 +278,18 @@ def test_starts_that_decrease_among_long_contexts():
                 mk.check_status(status)
         else:
             mk.check_status(status)
+
+
+def test_deterministic_mode_fills_new_results_and_changes_none():
+    w = Work(9)
+    want = [t.clone() for t in w.run()]
+    kc, vc = (torch.randn((4, 1, 16, 64), device="cuda").to(BF16) for _ in range(2))
+    q, table = torch.randn((5, 2, 64), device="cuda").to(BF16), torch.arange(4, dtype=torch.int32, device="cuda").view(1, 4)
+    torch.use_deterministic_algorithms(True)
+    try:
+        got = w.run()
+        out = mk.paged_prompt_attention(q, kc, vc, table, i32([0, 3]), i32([20]))    # two rows of no sequence
+    finally:
+        torch.use_deterministic_algorithms(False)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.isfinite(out[:3]).all() and torch.isnan(out[3:]).all()
