@@ -112,11 +112,11 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_co
 // accumulators in tensor memory (a row of x a lane, a row of w a column); eight warps take it out, multiply it by xs ws --
 // one number for all of a thread's columns -- and add it to fp32 sums in registers while the next block is multiplied into
 // others.  Warp 0 asks for x and w by TMA, warps 1 and 2 multiply, warp 3 brings the scales, warps 4-11 add up.
-// Bound by what surrounds the products (8192 x 12288 x 2048: 177 us, 2330 TFLOP/s): a block's four instructions take 256
+// Bound by what surrounds the products (8192 x 12288 x 2048: 169 us, 2440 TFLOP/s; with four stages 176): a block's four instructions take 256
 // clocks, taking its sums out of tensor memory about as many, and every hand-over between warps some 200 more.  So two
 // blocks are handed over at a time, and two warps multiply in turn, one waiting while the other's instructions run (one
-// warp: 186 us).  Tiles of 256 columns hold fewer accumulators and spill (230 us and more).
-// Pairs of CTAs that ask for shared tiles once (multicast) take 178 us for the same: not kept.
+// warp, with four stages: 186 us).  Tiles of 256 columns hold fewer accumulators and spill (230 us and more).
+// Pairs of CTAs that ask for shared tiles once (multicast) took as long (178 us for 177, with four stages): not kept.
 // splits > 1 (few tiles): K is shared by the CTAs of a cluster, whose sums are added in order through their shared memory.
 // ---------------------------------------------------------------------------
 
@@ -139,7 +139,6 @@ struct MatmulParams {
   int tiles_m, tiles;          // tiles along m, in all
   int splits;                  // CTAs of a cluster that share a tile's K
   int x_rows;                  // rows that a copy of x brings: no more than there are (what else is in a tile is no row's)
-  int tma;                     // rows of y and of the residual are on 16 bytes
   int wide_scales;             // rows of x's scales on 16 bytes
 };
 
@@ -154,7 +153,7 @@ struct Cfg {
   static constexpr int COLS = BN / 2;                                      // of an adding warp
   // results leave (and the residual comes) in boxes of 32 rows and 128 bytes, or what an adding warp has of a row
   static constexpr int ROWB = COLS * sizeof(T) < 128 ? COLS * static_cast<int>(sizeof(T)) : 128, PIECE = ROWB / static_cast<int>(sizeof(T));
-  static constexpr int STAGES = BN >= 256 ? 3 : ROWB == 64 ? 5 : 4;
+  static constexpr int STAGES = BN >= 256 ? 3 : 5;
   static constexpr uint32_t RESULTS = STAGES * STAGE;                      // behind the stages: a box an adding warp
   static constexpr uint32_t SCALES = RESULTS + kAddWarps * 32 * ROWB;      // [group][row][4] of x, [group][2][4] of w
   static constexpr uint32_t CONTROL = SCALES + kGroups * (kRows + 2) * 16;
@@ -220,7 +219,8 @@ struct Out<__nv_bfloat16> {
   }
 };
 
-template <int BN, class T>
+// TMA: rows of y and of the residual are on 16 bytes.  (Both ways in one kernel cost 8192 x 12288 x 2048 six microseconds.)
+template <int BN, class T, bool TMA>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap ty,
                   const __grid_constant__ CUtensorMap tr, const __grid_constant__ MatmulParams p) {
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < C::COLS / 2; ++i) acc[i] = 0ull;
       // the residual comes to where the results will be, once what was there has been stored
-      const bool by_tma = p.tma && p.splits == 1 && !idle;
+      const bool by_tma = TMA && p.splits == 1 && !idle;
       auto ask_residual = [&](int c) {
         if (lane == 0) {
           bulk_wait_read();
@@ -478,23 +478,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-      } else if (!idle) {
-        // rows that are not on 16 bytes: 16 columns of 32 rows at a time through shared memory, then element by element
+      } else if (!TMA && !idle) {
+        // rows that are not on 16 bytes: 32 columns of 32 rows at a time through shared memory, then a row's numbers together,
+        // 16 rows of the residual on their way at once (1101 x 83799 x 880 with a residual 283 us; 16 columns and four rows 865)
+        static_assert(ROWB == 128 && C::COLS % 32 == 0, "32 fp32 numbers a row");
+        auto at = [&](int row, int col) { return reinterpret_cast<float *>(mine) + row * 32 + (col ^ ((row & 7) << 2)); };
+        const int rows = min(32, p.m - (t - lane));
 #pragma unroll
-        for (int c = 0; c < C::COLS; c += 16) {
-          auto at = [&](int row, int col) { return reinterpret_cast<float *>(mine) + row * 16 + (col ^ ((row >> 1 & 3) << 2)); };
+        for (int c = 0; c < C::COLS; c += 32) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(at(lane, i)) = make_float4(sum(c + i), sum(c + i + 1), sum(c + i + 2), sum(c + i + 3));
+          for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4 *>(at(lane, i)) = make_float4(sum(c + i), sum(c + i + 1), sum(c + i + 2), sum(c + i + 3));
           __syncwarp();
-          const int col = j0 + c + (lane & 15);
-          if (col < p.n)
-#pragma unroll 4
-            for (int row = lane >> 4; row < min(32, p.m - (t - lane)); row += 2) {
-              const int64_t r = t - lane + row;
-              float v = *at(row, lane & 15);
-              if (p.residual) v += static_cast<float>(static_cast<const T *>(p.residual)[r * p.residual_row + col]);
-              static_cast<T *>(p.y)[r * p.y_row + col] = static_cast<T>(v);
+          const int col = j0 + c + lane;
+          if (col < p.n) {
+            T *y = static_cast<T *>(p.y) + (t - lane) * p.y_row + col;
+            const T *res = p.residual ? static_cast<const T *>(p.residual) + (t - lane) * p.residual_row + col : nullptr;
+#pragma unroll 1
+            for (int r0 = 0; r0 < rows; r0 += 16) {
+              T r[16];
+              if (res) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                  if (r0 + k < rows) r[k] = res[(r0 + k) * p.residual_row];
+              }
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                if (r0 + k >= rows) break;
+                const float v = *at(r0 + k, lane);
+                y[(r0 + k) * p.y_row] = static_cast<T>(res ? v + static_cast<float>(r[k]) : v);
+              }
             }
+          }
           __syncwarp();
         }
       }
@@ -569,16 +583,16 @@ bool byte_map(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, i
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, class T>
+template <int BN, class T, bool TMA>
 int launch(const mk_matmul_fp8_args *a, MatmulParams &p, int sms, int dev, cudaStream_t s) {
   using C = Cfg<BN, T>;
   static mkw::Ready ready[mkw::kMaxDevices];
-  const auto fn = &matmul_kernel<BN, T>;
+  const auto fn = &matmul_kernel<BN, T, TMA>;
   mkw::Ready &r = ready[dev];
   if (!r.get(reinterpret_cast<const void *>(fn), kThreads, C::SMEM)) return MK_ERR_CUDA;
   p.x_rows = std::min(kRows, (a->m + 7) / 8 * 8);
   CUtensorMap tw, tx, ty = {}, tr = {};
-  if (p.tma && (!result_map<T>(&ty, a->y, a->n, a->m, p.y_map_row, C::PIECE) || (a->residual && !result_map<T>(&tr, a->residual, a->n, a->m, p.residual_map_row, C::PIECE))))
+  if (TMA && (!result_map<T>(&ty, a->y, a->n, a->m, p.y_map_row, C::PIECE) || (a->residual && !result_map<T>(&tr, a->residual, a->n, a->m, p.residual_map_row, C::PIECE))))
     return MK_ERR_CUDA;
   if (!byte_map(&tx, a->x, a->k, a->m, a->x_row, p.x_rows) || !byte_map(&tw, a->w, a->k, a->n, a->w_row, BN)) return MK_ERR_CUDA;
   p.tiles_m = (a->m - 1) / kRows + 1;
@@ -664,8 +678,10 @@ extern "C" int mk_matmul_fp8(const mk_matmul_fp8_args *a, mk_stream stream) {
   const int64_t one = (a->n * static_cast<int64_t>(es) + 15) / 16 * 16 / static_cast<int64_t>(es);
   p.y_map_row = a->m == 1 ? one : a->y_row, p.residual_map_row = a->m == 1 ? one : a->residual_row;
   auto mapped = [&](const void *t, int64_t row) { return aligned16(t) && row * es % 16 == 0 && row >= a->n && row < (int64_t{1} << 36); };
-  p.tma = mapped(a->y, p.y_map_row) && (!a->residual || mapped(a->residual, p.residual_map_row));
+  const bool tma = mapped(a->y, p.y_map_row) && (!a->residual || mapped(a->residual, p.residual_map_row));
   p.wide_scales = aligned16(a->x_scale) && a->x_scale_row % 4 == 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return a->dtype == MK_F32 ? launch<kColumns, float>(a, p, sms, dev, s) : launch<kColumns, __nv_bfloat16>(a, p, sms, dev, s);
+  using B = __nv_bfloat16;
+  if (tma) return a->dtype == MK_F32 ? launch<kColumns, float, true>(a, p, sms, dev, s) : launch<kColumns, B, true>(a, p, sms, dev, s);
+  return a->dtype == MK_F32 ? launch<kColumns, float, false>(a, p, sms, dev, s) : launch<kColumns, B, false>(a, p, sms, dev, s);
 }
