@@ -562,7 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   auto last_of = [&](int tile) { return x.pos + min(x.count, (tile + 1) * p.tokens) - 1; };
   auto sees = [&](int tile, int b) {
     const int from = b * kBlock;
-    return x.count > tile * p.tokens && from <= last_of(tile) && (p.window == 0 || from + kBlock - 1 > first_of(tile) - p.window || from < p.sinks);
+    // (rows before the sequence's first token see nothing, and their positions less a window may pass 32 bits)
+    return x.count > tile * p.tokens && from <= last_of(tile) && (p.window == 0 || from + kBlock - 1 > max(first_of(tile), 0) - p.window || from < p.sinks);
   };
   if (warp == kSoftWarps) tmem_alloc(tslot, LY::TMEM_COLS);
 
@@ -833,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     const int pos = first_of(tile) + token;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t s_at = tmem + lanes + tile * LY::S_COLS, o_at = tmem + lanes + LY::O_COL + tile * D;
-    const int hidden_below = p.window > 0 ? pos - p.window : -1;   // hidden: at <= hidden_below and not a first token
+    const int hidden_below = p.window > 0 ? max(pos, 0) - p.window : -1;   // hidden: at <= hidden_below and not a first token
     float m = -INFINITY, l = 0.f;                          // m: of scores before to_log2
     uint32_t phase = 0;                                    // parity of the blocks that the tile has seen
     bool started = false, ok = true;
