@@ -494,7 +494,8 @@ typedef struct {
  * gives zeros and lse -inf; tokens that a row does not see are never read into
  * its result, whatever they hold.  A row that sees a page id outside the cache, or
  * whose sequence is longer than table_cols * page_size, gives NaN and MK_ERR_BAD_PAGE;
- * a sequence whose starts are outside rows or decrease is skipped (MK_ERR_BAD_PAGE).
+ * a sequence whose starts are outside rows or decrease is skipped (MK_ERR_BAD_PAGE),
+ * and all are where the others then overlap to more than 2^30 tiles.
  * Rows whose results are infinite or NaN take a slow path.  Errors:
  * MK_ERR_INVALID_ARG, MK_ERR_UNSUPPORTED (dtype, head_dim, sizes), MK_ERR_CUDA; in
  * *status also MK_ERR_TIMEOUT if a wait inside the kernel ran out. */

@@ -91,7 +91,7 @@ int prompt_attention(const mk_paged_kv *kv, const mk_prompt_args *a, mk_stream s
   p.sinks = a->window > 0 ? std::min(a->sinks, p.capacity) : 0;
   p.sms = sms;
   p.scale = a->scale;
-  if (shape.ctas > INT32_MAX) return MK_ERR_UNSUPPORTED;
+  if (shape.ctas > INT32_MAX / 2) return MK_ERR_UNSUPPORTED;   // (task numbers and sums of them are 32 bits)
   p.item = 2 * p.tokens;
   // blocks of an item: of all its row's tokens, or of the window, its own rows and the first tokens
   const int64_t span = p.window > 0 ? static_cast<int64_t>(p.window) + p.item + p.sinks + 3 * kBlock : slots + kBlock;

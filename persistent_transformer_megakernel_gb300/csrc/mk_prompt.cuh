@@ -261,7 +261,9 @@ static __global__ void __launch_bounds__(kTaskThreads) task_kernel(const __grid_
       total += s_warps[i];
     }
     if (pass == 0) {
-      if (total > INT32_MAX / 2) {                         // (starts that overlap; the same for all threads)
+      // Starts that overlap can promise more tasks than a number of 32 bits holds; no others pass p.ctas, which is at most half
+      // of that.  (The same for all threads.)
+      if (total > INT32_MAX / 2 / p.vh) {
         if (tid == 0) report(p.status, MK_ERR_BAD_PAGE);
         for (int i = a; i < b; ++i) before[i] = 0;
         at = total = 0;
