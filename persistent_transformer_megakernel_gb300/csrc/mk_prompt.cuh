@@ -1033,6 +1033,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     if (token >= p.tokens || head >= heads || index >= rec.y) continue;
     constexpr int64_t kPart = 2 * kRows * (D + 4);
     const float *part = p.parts + static_cast<int64_t>(slot) * kPart + i * (D + 4);
+    // The parts' sums are finite, what they add up to may not be before it is divided: weights are scaled down by the number
+    // of parts, rounded up to a power of two.
+    const int spare = 32 - __clz(parts - 1);
+    const float shrink = __int_as_float((127 - spare) << 23), grow = __int_as_float((127 + spare) << 23);
     float m = -INFINITY, l = 0.f, o[E] = {};
     for (int j0 = 0; j0 < parts; j0 += 32) {
       const bool mine = j0 + lane < parts;
@@ -1040,7 +1044,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
       float top = fmaxf(m, mj);
 #pragma unroll
       for (int o2 = 16; o2 > 0; o2 >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
-      const float base = top == -INFINITY ? 0.f : top, f = mkw::exp2_fast(m - base), fj = mkw::exp2_fast(mj - base);
+      const float base = top == -INFINITY ? 0.f : top, f = mkw::exp2_fast(m - base), fj = mkw::exp2_fast(mj - base) * shrink;
       m = top;
       l = l * f + lj * fj;                                 // (a lane's own; added up at the end)
 #pragma unroll
@@ -1065,7 +1069,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (rec.x + index) * p.out_row + (head0 + head) * p.out_head + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = pack_weights<false>(o[e] * inv, o[e + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[static_cast<int64_t>(rec.x + index) * p.hq + head0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    if (lane == 0 && p.lse) p.lse[static_cast<int64_t>(rec.x + index) * p.hq + head0 + head] = l == 0.f ? -INFINITY : (m + log2f(l * grow)) * 0.69314718055994531f;
   }
 }
 
