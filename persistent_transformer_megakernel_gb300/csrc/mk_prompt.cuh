@@ -1017,6 +1017,8 @@ __device__ __forceinline__ void load_part(const float *p, float (&x)[2]) {
   const float2 v = *reinterpret_cast<const float2 *>(p);
   x[0] = v.x, x[1] = v.y;
 }
+// (an infinity stays one, however small its weight: fp32's may be 0)
+__device__ __forceinline__ float weighted(float x, float w) { return fabsf(x) < INFINITY ? x * w : x; }
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ PromptParams p) {
   constexpr int E = D / 32;
@@ -1048,7 +1050,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
       m = top;
       l = l * f + lj * fj;                                 // (a lane's own; added up at the end)
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] *= f;
+      for (int e = 0; e < E; ++e) o[e] = weighted(o[e], f);
       const int count = min(32, parts - j0);
 #pragma unroll 1
       for (int j = 0; j < count; j += 8) {                 // eight parts' elements on their way together
@@ -1059,7 +1061,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
         for (int k = 0; k < 8; ++k) {
           const float w = __shfl_sync(0xffffffffu, fj, j + k & 31);   // (0 for a lane without a part)
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[e] += j + k < count ? x[k][e] * w : 0.f;
+          for (int e = 0; e < E; ++e) o[e] += j + k < count ? weighted(x[k][e], w) : 0.f;
         }
       }
     }

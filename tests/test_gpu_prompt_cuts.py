@@ -1,5 +1,7 @@
 """``paged_prompt_attention`` where the work of a sequence is shared by CTAs and joined, against its definition in 64 bits
 element by element: with and without a list of tasks, and values whose sums over the parts pass fp32's largest."""
+import math
+
 import pytest
 import torch
 
@@ -56,5 +58,29 @@ def test_parts_of_large_values(d, among):
     out, lse, status = _run(q, kc, vc, table, st, ln)
     want, wl, err, el = P.prompt_attention(q[:4], kc, vc, table, st[:2], ln[:1], d ** -0.5)
     assert status == 0 and torch.isfinite(want).all()
+    U.assert_within(out[:4], want, U.half_step(BF16, want) + err, "out")
+    U.assert_within(lse[:4], wl, el, "lse")
+
+
+@pytest.mark.parametrize("among", [0, 40])
+@pytest.mark.parametrize("where", [100, 6900])
+def test_an_infinity_whose_part_has_no_weight(among, where):
+    # a visible infinity is the result however small its weight: as in a sequence that is not cut
+    n, d = 7000, 64
+    kc, vc, table, _, _ = _cache([n] + [1] * among, 2, d, 16, BF16, 4)
+    kc = kc * 0.01
+    for at, score in ((3500, 60.0), (where, -150.0)):
+        kc[table[0, at // 16].long(), :, at % 16] = score / d ** 0.5
+    first, last = where // 1024 * 1024, (where // 1024 + 1) * 1024
+    for at in range(max(0, first - 1024), min(n, last + 1024)):  # (and of its neighbours: nothing in the part weighs anything)
+        if at != 3500:
+            kc[table[0, at // 16].long(), :, at % 16] = -150.0 / d ** 0.5
+    vc[table[0, where // 16].long(), :, where % 16, 5] = math.inf
+    vc[table[0, where // 16].long(), 1, where % 16, 7] = -math.inf
+    q = torch.ones((4 + among, 4, d), dtype=BF16)
+    st = torch.tensor([0, 4] + [4 + i for i in range(1, among + 1)], dtype=torch.int32)
+    out, lse, status = _run(q, kc, vc, table, st, torch.tensor([n] + [1] * among, dtype=torch.int32))
+    want, wl, err, el = P.prompt_attention(q[:4], kc, vc, table, st[:2], torch.tensor([n]), d ** -0.5)
+    assert status == 0 and (want[:, :, 5] == math.inf).all() and (want[:, 2:, 7] == -math.inf).all()
     U.assert_within(out[:4], want, U.half_step(BF16, want) + err, "out")
     U.assert_within(lse[:4], wl, el, "lse")
