@@ -89,14 +89,15 @@ def quantize_q4(w: torch.Tensor, group: int = 64, zeros: bool = False):
 def quantize_fp8_weight(w: torch.Tensor):
     """8-bit codes of ``w`` [n][k] (k a multiple of 16), once per weight: ``(codes
     float8_e4m3fn [n][k], scales fp32 [n / 128][k / 128], rounded up)``; a block of
-    128 x 128 has the scale largest / 448."""
+    128 x 128 has the scale largest / 448.  NaN stays NaN and does not count for
+    the scale."""
     w = w.detach()
     n, k = w.shape
     if k % 16 or k == 0:
         raise ValueError("k (%d) must be a multiple of 16" % k)
     nb, kb = -(-n // 128), -(-k // 128)
     x = torch.nn.functional.pad(w.float(), (0, kb * 128 - k, 0, nb * 128 - n)).view(nb, 128, kb, 128)
-    largest = x.abs().amax((1, 3))
+    largest = x.abs().nan_to_num_(nan=0.0, posinf=float("inf")).amax((1, 3))
     scales = largest / torch.full_like(largest, 448.0)
     scales = torch.where(scales > 0, scales, torch.ones_like(scales))
     codes = (x / scales[:, None, :, None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(nb * 128, kb * 128)[:n, :k]
