@@ -7,6 +7,7 @@
 #include <ATen/Context.h>
 #include <ATen/EmptyTensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -93,6 +94,8 @@ inline const at::Tensor &tensor(PyObject *o, const char *name) {
   const at::Tensor &t = THPVariable_Unpack(o);
   if (t.requires_grad() && c10::GradMode::is_enabled())
     throw Bad{std::string(name) + " requires grad, and this operator has no gradient: call it under torch.no_grad()"};
+  if (t._fw_grad(0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode())
+    throw Bad{std::string(name) + " has a tangent (forward-mode differentiation), and this operator has none: unpack_dual it first"};
   return t;
 }
 

@@ -9,7 +9,8 @@ rows) or ``quantize_fp8`` -> ``matmul_fp8`` (many) for the projections;
 cache, a position outside the rotary table) goes to an optional ``status`` word
 that ``check_status`` turns into an ``MKError``.  They have no gradients:
 a tensor that requires them is refused unless gradients are off
-(``torch.no_grad``).
+(``torch.no_grad``), and so is one that carries a tangent of forward-mode
+differentiation.
 
 They are functions of the module ``_mktorch`` (``csrc/mk_torch.cpp``,
 ``csrc/mk_torch_prompts.h``), which checks the tensors of a call against what
