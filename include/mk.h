@@ -496,7 +496,9 @@ typedef struct {
  * whose sequence is longer than table_cols * page_size, gives NaN and MK_ERR_BAD_PAGE;
  * a sequence whose starts are outside rows or decrease is skipped (MK_ERR_BAD_PAGE),
  * and all are where the others then overlap to more than 2^30 tiles.
- * Rows whose results are infinite or NaN take a slow path.  Errors:
+ * Rows whose results are infinite or NaN take a slow path, a position at a time up
+ * to the first score that is NaN (a prompt of 8192 tokens of 16 heads, all of which
+ * see a NaN among the values: 80 ms instead of 0.2).  Errors:
  * MK_ERR_INVALID_ARG, MK_ERR_UNSUPPORTED (dtype, head_dim, sizes), MK_ERR_CUDA; in
  * *status also MK_ERR_TIMEOUT if a wait inside the kernel ran out. */
 int mk_paged_prompt_attention(const mk_paged_kv *kv, const mk_prompt_args *a, mk_stream stream);

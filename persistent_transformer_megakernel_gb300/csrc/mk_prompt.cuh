@@ -461,23 +461,55 @@ __device__ __forceinline__ int64_t slot_of(const PromptParams &p, int seq, int p
   return page * p.page_stride + (pos - col * static_cast<int>(p.page_size.value)) * p.slot_stride;
 }
 
+// N elements of the cache, as they are and as numbers
 template <bool FP8, int N>
-__device__ __forceinline__ void cached(const void *base, int64_t at, float (&x)[N]) {
+struct Raw;
+template <>
+struct Raw<false, 4> {
+  using type = uint2;
+  static __device__ __forceinline__ uint32_t word(const type &w, int i) { return i ? w.y : w.x; }
+};
+template <>
+struct Raw<false, 2> {
+  using type = uint32_t;
+  static __device__ __forceinline__ uint32_t word(type w, int) { return w; }
+};
+template <>
+struct Raw<true, 4> {
+  using type = uint32_t;
+};
+template <>
+struct Raw<true, 2> {
+  using type = uint16_t;
+};
+template <bool FP8, int N>
+__device__ __forceinline__ void numbers_of(const typename Raw<FP8, N>::type &w, float (&x)[N]) {
+  if constexpr (FP8) {
+    uint32_t h[2];
+    mkw::e4m3x4_to_half2(w, h[0], h[1]);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if constexpr (FP8) x[i] = static_cast<float>(static_cast<const __nv_fp8_e4m3 *>(base)[at + i]);
-    else x[i] = __bfloat162float(static_cast<const __nv_bfloat16 *>(base)[at + i]);
+    for (int i = 0; i < N; i += 2) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i / 2]));
+      x[i] = f.x, x[i + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint32_t u = Raw<false, N>::word(w, i / 2);
+      x[i] = __uint_as_float(u << 16), x[i + 1] = __uint_as_float(u & 0xffff0000u);
+    }
   }
 }
 
-// A row by fp32 products, one warp, position by position: for rows whose tensor-core result is not finite.  There a
+// A row by fp32 products, one warp, eight positions at a time: for rows whose tensor-core result is not finite.  There a
 // value outside the row's mask (infinity or NaN times a weight of 0) or a sum of large values can have done it, so that
 // the answer may be finite all the same.  Leaves the row's maximum (log2 units), sum and O (lane's elements) where the sum
-// counts weights times `shrink`.
+// counts weights times `shrink`.  Each row reads keys and values for itself: 8192 tokens that all see a NaN among the values
+// take 82 ms (one position at a time 240); a score that is NaN ends its row.
 template <bool FP8, int D>
-__device__ void row_alone(const PromptParams &p, const Task &task, const Pair &x, int b0, int b1, int row, int head, int pos, int lane, float &m, float &l,
+__device__ void row_alone(const PromptParams &p, const Task &task, const Pair &pair, int b0, int b1, int row, int head, int pos, int lane, float &m, float &l,
                           float (&o)[D / 32], float &shrink) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, ES = FP8 ? 1 : 2;
   float q[E];
   const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) + row * p.q_row + head * p.q_head + lane * E;
 #pragma unroll
@@ -488,34 +520,60 @@ __device__ void row_alone(const PromptParams &p, const Task &task, const Pair &x
   for (int i = 1; i < pos + 1 && i > 0; i <<= 1) shrink *= 0.5f;
   m = -INFINITY;
   l = 0.f;
-  for (int b = b0; b < b1; ++b) {
-    const int first = x.number(b) * kBlock;
-    for (int at = first; at < first + kBlock && at <= pos; ++at) {
-      if (p.window > 0 && at <= pos - p.window && at >= p.sinks) continue;
-      const int64_t slot = slot_of(p, task.seq, at);
-      if (slot < 0) {
-        m = l = NAN;
-        return;
+  constexpr int U = 8;                                     // positions whose keys and values are on their way together
+#pragma unroll 1
+  for (int i = 4 * b0; i < 4 * b1; ++i) {                  // 32 positions, a lane looks up one
+    const int at = pair.number(i >> 2) * kBlock + (i & 3) * 32 + lane;
+    const bool want = at <= pos && (p.window == 0 || at > pos - p.window || at < p.sinks);
+    const int64_t slot = want ? slot_of(p, task.seq, at) : 0;
+    if (__any_sync(0xffffffffu, slot < 0)) {
+      m = l = NAN;
+      return;
+    }
+    const unsigned wanted = __ballot_sync(0xffffffffu, want);
+#pragma unroll 1
+    for (int j = 0; j < 32; j += U) {
+      if (!(wanted >> j & ((1u << U) - 1u))) continue;
+      typename Raw<FP8, E>::type k[U], v[U];
+      float s[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t from = __shfl_sync(0xffffffffu, slot, j + u) + kvh * p.head_stride + lane * E;
+        k[u] = v[u] = {};
+        if (wanted >> (j + u) & 1) {
+          k[u] = *reinterpret_cast<const typename Raw<FP8, E>::type *>(static_cast<const unsigned char *>(p.k) + from * ES);
+          v[u] = *reinterpret_cast<const typename Raw<FP8, E>::type *>(static_cast<const unsigned char *>(p.v) + from * ES);
+        }
       }
-      float k[E], v[E];
-      cached<FP8>(p.k, slot + kvh * p.head_stride + lane * E, k);
-      cached<FP8>(p.v, slot + kvh * p.head_stride + lane * E, v);
-      float s = 0.f;
+      float mx = m;
 #pragma unroll
-      for (int i = 0; i < E; ++i) s += q[i] * k[i];
+      for (int u = 0; u < U; ++u) {
+        s[u] = 0.f;
+        float x[E];
+        numbers_of<FP8, E>(k[u], x);
 #pragma unroll
-      for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-      s *= c;
-      const float mx = fmaxf(m, s), base = mx == -INFINITY ? 0.f : mx;
-      const float f = mkw::exp2_fast(m - base), w = mkw::exp2_fast(s - base) * shrink;
+        for (int e = 0; e < E; ++e) s[u] += q[e] * x[e];
+#pragma unroll
+        for (int o2 = 16; o2 > 0; o2 >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o2);
+        s[u] = wanted >> (j + u) & 1 ? s[u] * c : -INFINITY;
+        mx = fmaxf(mx, s[u]);
+      }
+      const float base = mx == -INFINITY ? 0.f : mx, f = mkw::exp2_fast(m - base);
       m = mx;
-      l = l * f + w;
+      l *= f;
+      // an infinity stays one, however small its weight (fp32's may be 0; a score of -infinity makes it 0 in truth)
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        // an infinity stays one, however small its weight (fp32's may be 0; a score of -infinity makes it 0 in truth)
-        const float old = fabsf(o[i]) < INFINITY ? o[i] * f : o[i];
-        o[i] = old + (fabsf(v[i]) < INFINITY ? w * v[i] : s == -INFINITY ? NAN : v[i]);
+      for (int e = 0; e < E; ++e) o[e] = fabsf(o[e]) < INFINITY ? o[e] * f : o[e];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float w = mkw::exp2_fast(s[u] - base) * shrink;
+        l += w;
+        float x[E];
+        numbers_of<FP8, E>(v[u], x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += fabsf(x[e]) < INFINITY ? w * x[e] : s[u] == -INFINITY ? NAN : x[e];
       }
+      if (l != l) return;                                  // (a score that is no number: so is all of the row, whatever follows)
     }
   }
 }
@@ -980,6 +1038,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       if (!whole) part[D] = m, part[D + 1] = l;
       else if (p.lse) p.lse[static_cast<int64_t>(x.row + index) * p.hq + head0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     }
+    __syncwarp();                                          // (what was put by a row's own lane, the warp puts again)
     for (unsigned rest = __ballot_sync(0xffffffffu, strange && live && ok && !task.outside); rest; rest &= rest - 1u) {
       const int of = __ffs(rest) - 1;
       const int row = x.row + __shfl_sync(0xffffffffu, index, of), hd = head0 + __shfl_sync(0xffffffffu, head, of);
