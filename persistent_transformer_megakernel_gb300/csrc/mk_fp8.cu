@@ -24,8 +24,8 @@ constexpr int kBlock = 128;
 // ---------------------------------------------------------------------------
 // Quantisation of rows: for each 128 of a row scale = largest / 448, code = x / scale rounded to e4m3.
 //
-// Bound by bytes: x read once, a byte an element and 4 a block written.  16 lanes have a block, 8 elements each, or four
-// blocks at a time, all asked for before the first is worked on.  The quotient is fp32's (a bf16 element over its scale is
+// Bound by bytes: x read once, a byte an element and 4 a block written.  16 lanes have a block, 8 elements each, or (bf16)
+// four blocks at a time, all asked for before the first is worked on.  The quotient is fp32's (a bf16 element over its scale is
 // often half way between two codes, so that a last place decides): the product with the reciprocal, corrected by its
 // remainder, which is the correctly rounded quotient if the reciprocal is (P. Markstein, Computation of elementary functions
 // on the IBM RISC System/6000 processor, 1990), away from the ends of the exponents' range.
@@ -644,15 +644,15 @@ extern "C" int mk_quantize_fp8(const mk_quantize_fp8_args *a, mk_stream stream) 
   const int64_t items = static_cast<int64_t>(a->m) * p.blocks.value;
   if (items > INT32_MAX - 65536) return MK_ERR_UNSUPPORTED;
   p.items = static_cast<int>(items);
-  // four blocks at a time where there are enough to fill the SMs several times over (8192 x 2048 in bf16: 11.2 us, one at a
-  // time 16), else one (8 x 1024: 1.5 us, 2.1 with four)
-  const bool many = items >= int64_t{4} * 16 * 16 * sms;
+  // bf16: four blocks at a time where there are enough to fill the SMs several times over (32768 x 2048: 40.5 us, one at a time
+  // 46; 8192 x 2048, which is about as quick either way, 11.0 and 10.5; 1024 x 2048 3.2 and 2.5).  fp32, with twice the bytes
+  // on their way, always one (32768 x 2048: 49.0 us, four at a time 49.1; 8192 x 2048 10.3 and 10.9).
+  const bool many = a->dtype == MK_BF16 && items >= int64_t{4} * 16 * 16 * sms;
   const int each = kQuantThreads / 16 * (many ? 4 : 1);
   const dim3 grid(static_cast<unsigned>((items - 1) / each + 1));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   using B = __nv_bfloat16;
-  if (a->dtype == MK_F32)
-    return many ? mkw::launch_after(&quantize_kernel<float, 4>, grid, kQuantThreads, 0, s, p) : mkw::launch_after(&quantize_kernel<float, 1>, grid, kQuantThreads, 0, s, p);
+  if (a->dtype == MK_F32) return mkw::launch_after(&quantize_kernel<float, 1>, grid, kQuantThreads, 0, s, p);
   return many ? mkw::launch_after(&quantize_kernel<B, 4>, grid, kQuantThreads, 0, s, p) : mkw::launch_after(&quantize_kernel<B, 1>, grid, kQuantThreads, 0, s, p);
 }
 
