@@ -1,6 +1,4 @@
 // Products in 8-bit floating point with block scales (mk_quantize_fp8, mk_matmul_fp8).
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -14,6 +12,7 @@
 #include "mk_mma.cuh"
 #include "mk_paged.h"
 #include "mk_tc.cuh"
+#include "mk_tmap.h"
 
 namespace mkf8 {
 
@@ -108,7 +107,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_co
 // ---------------------------------------------------------------------------
 // y[t][j] = sum_b xs[t][b] ws[j / 128][b] sum_{k in b} x[t][k] w[j][k]  (+ residual)
 //
-// A CTA has 128 rows of x and BN rows of w.  The inner sums of a block of 128 are four tensor instructions into one of the
+// A CTA has 128 rows of x and 128 rows of w.  The inner sums of a block of 128 are four tensor instructions into one of the
 // accumulators in tensor memory (a row of x a lane, a row of w a column); eight warps take it out, multiply it by xs ws --
 // one number for all of a thread's columns -- and add it to fp32 sums in registers while the next block is multiplied into
 // others.  Warp 0 asks for x and w by TMA, warps 1 and 2 multiply, warp 3 brings the scales, warps 4-11 add up.
@@ -143,23 +142,18 @@ struct MatmulParams {
 };
 
 // numbers of a row of sums that a cluster's CTAs leave each other (16 bytes of eight rows are in different banks)
-template <int BN>
-constexpr int kSplitRow = BN + 4;
-
-template <int BN, class T>
-struct Cfg {
-  static constexpr uint32_t STAGE = kXTile + BN * 128;
-  static constexpr int TCOLS = 512, SUMS = TCOLS / (2 * BN);               // pairs of accumulators
-  static constexpr int COLS = BN / 2;                                      // of an adding warp
-  // results leave (and the residual comes) in boxes of 32 rows and 128 bytes, or what an adding warp has of a row
-  static constexpr int ROWB = COLS * sizeof(T) < 128 ? COLS * static_cast<int>(sizeof(T)) : 128, PIECE = ROWB / static_cast<int>(sizeof(T));
-  static constexpr int STAGES = BN >= 256 ? 3 : 5;
-  static constexpr uint32_t RESULTS = STAGES * STAGE;                      // behind the stages: a box an adding warp
-  static constexpr uint32_t SCALES = RESULTS + kAddWarps * 32 * ROWB;      // [group][row][4] of x, [group][2][4] of w
-  static constexpr uint32_t CONTROL = SCALES + kGroups * (kRows + 2) * 16;
-  static constexpr int SMEM = static_cast<int>(1024 + CONTROL + 512);
-  static_assert(SMEM <= 232448 && kRows * kSplitRow<BN> * 4 <= RESULTS, "shared memory");
-};
+constexpr int kSplitRow = kColumns + 4;
+constexpr uint32_t kStage = kXTile + kColumns * 128;
+constexpr int kStages = 5;
+constexpr int kTensorColumns = 512, kSums = kTensorColumns / (2 * kColumns);   // pairs of accumulators
+constexpr int kCols = kColumns / 2;                        // of an adding warp
+constexpr int kBoxRow = 128;                               // results leave (and the residual comes) in boxes of 32 rows and 128 bytes
+constexpr uint32_t kResults = kStages * kStage;            // behind the stages: a box an adding warp
+constexpr uint32_t kScales = kResults + kAddWarps * 32 * kBoxRow;              // [group][row][4] of x, [group][4] of w
+constexpr uint32_t kControl = kScales + kGroups * (kRows + 1) * 16;
+constexpr int kSmem = static_cast<int>(1024 + kControl + 512);
+static_assert(kSmem <= 232448 && kRows * kSplitRow * 4 <= kResults, "shared memory");
+static_assert(kColumns == kBlock, "a tile has one row of w's scales");
 
 __device__ __forceinline__ void fail(int32_t *status) {
   if (status) atomicCAS(status, 0, MK_ERR_TIMEOUT);
@@ -220,31 +214,30 @@ struct Out<__nv_bfloat16> {
 };
 
 // TMA: rows of y and of the residual are on 16 bytes.  (Both ways in one kernel cost 8192 x 12288 x 2048 six microseconds.)
-template <int BN, class T, bool TMA>
+template <class T, bool TMA>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap ty,
                   const __grid_constant__ CUtensorMap tr, const __grid_constant__ MatmulParams p) {
-  using C = Cfg<BN, T>;
-  constexpr int N = Out<T>::N, PIECE = C::PIECE, ROWB = C::ROWB;   // numbers in 16 bytes and in a row of a box, its bytes
-  constexpr uint32_t kId = idesc_f32(kRows, BN);
+  constexpr int N = Out<T>::N, PIECE = kBoxRow / static_cast<int>(sizeof(T));   // numbers in 16 bytes and in a row of a box
+  constexpr uint32_t kId = idesc_f32(kRows, kColumns);
   extern __shared__ unsigned char smraw[];
   mkw::follow_previous_kernel();
   unsigned char *sm = smraw + ((1024u - (smem_addr(smraw) & 1023u)) & 1023u);
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::CONTROL), *empty = full + C::STAGES, *tfull = empty + C::STAGES, *tempty = tfull + C::SUMS,
-           *sfull = tempty + C::SUMS, *sempty = sfull + kGroups, *rfull = sempty + kGroups;
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + kControl), *empty = full + kStages, *tfull = empty + kStages, *tempty = tfull + kSums,
+           *sfull = tempty + kSums, *sempty = sfull + kGroups, *rfull = sempty + kGroups;
   uint32_t *tslot = reinterpret_cast<uint32_t *>(rfull + kAddWarps);
-  float4 *scales = reinterpret_cast<float4 *>(sm + C::SCALES);             // a group: kRows of x, 2 of w
+  float4 *scales = reinterpret_cast<float4 *>(sm + kScales);               // a group: kRows of x, one of w
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::STAGES; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-    for (int i = 0; i < C::SUMS; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], kAddWarps);
+    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+    for (int i = 0; i < kSums; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], kAddWarps);
     for (int i = 0; i < kGroups; ++i) mbar_init(&sfull[i], 1), mbar_init(&sempty[i], kAddWarps);
     for (int i = 0; i < kAddWarps; ++i) mbar_init(&rfull[i], 1);
     fence_mbar_init();
     prefetch_tmap(&tw);
     prefetch_tmap(&tx);
   }
-  if (warp == 1) tmem_alloc(tslot, C::TCOLS);
+  if (warp == 1) tmem_alloc(tslot, kTensorColumns);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -253,25 +246,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int split = static_cast<int>(blockIdx.x) % p.splits, step = static_cast<int>(gridDim.x) / p.splits, first = static_cast<int>(blockIdx.x) / p.splits;
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.kb) * split / p.splits), kb1 = static_cast<int>(static_cast<int64_t>(p.kb) * (split + 1) / p.splits);
   auto row_of = [&](int tile) { return tile % p.tiles_m * kRows; };
-  auto column_of = [&](int tile) { return tile / p.tiles_m * BN; };
+  auto column_of = [&](int tile) { return tile / p.tiles_m * kColumns; };
 
   if (warp < kHelpers) {
     if (warp == 0) {
-      Turn<C::STAGES> at;
+      Turn<kStages> at;
       int it = 0;
       bool ok = true;
       for (int tile = first; tile < p.tiles && ok; tile += step) {
         const int t0 = row_of(tile), j0 = column_of(tile);
         for (int kb = kb0; kb < kb1; ++kb, ++it, at.next()) {
           const int s = at.i;
-          if (it >= C::STAGES && !__all_sync(0xffffffffu, mbar_wait(&empty[s], at.parity ^ 1u, kWaitNs))) {
+          if (it >= kStages && !__all_sync(0xffffffffu, mbar_wait(&empty[s], at.parity ^ 1u, kWaitNs))) {
             if (lane == 0) fail(p.status);
             ok = false;
             break;
           }
-          unsigned char *to = sm + s * C::STAGE;
+          unsigned char *to = sm + s * kStage;
           if (elect_one()) {
-            mbar_expect_tx(&full[s], p.x_rows * 128 + BN * 128);
+            mbar_expect_tx(&full[s], p.x_rows * 128 + kColumns * 128);
             tma_load_2d(to, &tx, kb * kBlock, t0, &full[s]);
             tma_load_2d(to + kXTile, &tw, kb * kBlock, j0, &full[s]);
           }
@@ -279,13 +272,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // no copy may be on its way when the CTA ends
-      for (int i = it - C::STAGES < 0 ? 0 : it - C::STAGES; i < it; ++i) mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1, kWaitNs);
+      for (int i = it - kStages < 0 ? 0 : it - kStages; i < it; ++i) mbar_wait(&full[i % kStages], (i / kStages) & 1, kWaitNs);
     } else if (warp <= kMmaWarps) {
       // descriptors: the low words move with the stage, the high ones are constants
       const uint32_t base = smem_addr(sm);
       const uint32_t lo = static_cast<uint32_t>(desc_sw128(base)), hi = static_cast<uint32_t>(desc_sw128(base) >> 32);
-      Turn<C::STAGES> at;
-      Turn<C::SUMS> sums;
+      Turn<kStages> at;
+      Turn<kSums> sums;
       int pair = 0;
       bool ok = true;
       auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -309,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait(&full[at.i], at.parity)) break;
             tc_fence_after();
             if (elect_one()) {
-              const uint32_t x = lo + at.i * (C::STAGE >> 4), w = x + (kXTile >> 4), d = tmem + (sums.i * 2 + i) * BN;
+              const uint32_t x = lo + at.i * (kStage >> 4), w = x + (kXTile >> 4), d = tmem + (sums.i * 2 + i) * kColumns;
 #pragma unroll
               for (int k = 0; k < 4; ++k) mma_e4m3(d, desc_of(x + 2 * k, hi), desc_of(w + 2 * k, hi), kId, k != 0);
               mma_commit(&empty[at.i]);
@@ -319,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       // every product is finished before tensor memory goes
-      for (int i = pair - C::SUMS < 0 ? 0 : pair - C::SUMS; i < pair && ok; ++i) mbar_wait(&tfull[i % C::SUMS], (i / C::SUMS) & 1, kWaitNs);
+      for (int i = pair - kSums < 0 ? 0 : pair - kSums; i < pair && ok; ++i) mbar_wait(&tfull[i % kSums], (i / kSums) & 1, kWaitNs);
     } else {
       // scales: a lane has four rows of x; copies of two groups are on their way while a third is told of
       constexpr int kAhead = 2;
@@ -339,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t to = smem_addr(scales + at.i * (kRows + 2));
+          const uint32_t to = smem_addr(scales + at.i * (kRows + 1));
           auto copy = [&](int place, const float *row, bool there, bool wide) {
             if (wide && kb + 4 <= p.kb) {
               mkw::cp_async16(to + place * 16, row + (there ? kb : 0), there);
@@ -356,10 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool there = t0 + 32 * i < p.m;
             copy(lane + 32 * i, p.x_scale + (there ? (t0 + 32 * i) * p.x_scale_row : 0), there, p.wide_scales && kb0 % 4 == 0);
           }
-          if (lane < 2) {
-            const bool there = (jb + lane) * kBlock < p.n;
-            copy(kRows + lane, p.w_scale + (there ? static_cast<int64_t>(jb + lane) * p.kb : 0), there, false);
-          }
+          if (lane == 0) copy(kRows, p.w_scale + static_cast<int64_t>(jb) * p.kb, true, false);
           mkw::cp_async_commit();
           mkw::cp_async_wait<kAhead>();
           if (g >= kAhead) tell(g - kAhead + 1);
@@ -370,10 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     const int q = warp & 3, part = (warp - kHelpers) >> 2; // lanes of tensor memory, half of the columns
-    const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + part * C::COLS;
-    Turn<C::SUMS> sums;
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + part * kCols;
+    Turn<kSums> sums;
     Turn<kGroups> groups;
-    unsigned char *mine = sm + C::RESULTS + (warp - kHelpers) * 32 * ROWB;
+    unsigned char *mine = sm + kResults + (warp - kHelpers) * 32 * kBoxRow;
     uint64_t *loaded = rfull + (warp - kHelpers);
     uint32_t load_parity = 0;
     bool ok = true;
@@ -385,25 +375,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       return ok;
     };
     for (int tile = first; tile < p.tiles; tile += step) {
-      const int t = row_of(tile) + 32 * q + lane, j0 = column_of(tile) + part * C::COLS;
+      const int t = row_of(tile) + 32 * q + lane, j0 = column_of(tile) + part * kCols;
       const bool idle = __all_sync(0xffffffffu, t >= p.m || j0 >= p.n);   // a warp without a result only takes part
-      unsigned long long acc[C::COLS / 2];
+      unsigned long long acc[kCols / 2];
 #pragma unroll
-      for (int i = 0; i < C::COLS / 2; ++i) acc[i] = 0ull;
+      for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
       // the residual comes to where the results will be, once what was there has been stored
       const bool by_tma = TMA && p.splits == 1 && !idle;
       auto ask_residual = [&](int c) {
         if (lane == 0) {
           bulk_wait_read();
-          mbar_expect_tx(loaded, 32 * ROWB);
+          mbar_expect_tx(loaded, 32 * kBoxRow);
           tma_load_2d(mine, &tr, j0 + c, t - lane, loaded);
         }
       };
       for (int kbg = kb0; kbg < kb1 && ok; kbg += kGroup, groups.next()) {
         if (by_tma && p.residual && kbg + kGroup >= kb1) ask_residual(0);
-        const float4 *sc = scales + groups.i * (kRows + 2);
+        const float4 *sc = scales + groups.i * (kRows + 1);
         if (!wait(&sfull[groups.i], groups.parity)) break;
-        const float4 fx = sc[32 * q + lane], fw = sc[kRows + part * C::COLS / kBlock];
+        const float4 fx = sc[32 * q + lane], fw = sc[kRows];
         __syncwarp();
         if (lane == 0) mbar_arrive(&sempty[groups.i]);
 #pragma unroll
@@ -413,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait(&tfull[sums.i], sums.parity)) break;
           tc_fence_after();
           if (!idle) {
-            const uint32_t from = at + sums.i * 2 * BN;
+            const uint32_t from = at + sums.i * 2 * kColumns;
             uint32_t v[2][32];
             tmem_ld32(from, v[0]);
 #pragma unroll
@@ -423,11 +413,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               unsigned long long ff;
               asm("mov.b64 %0, {%1, %1};" : "=l"(ff) : "f"(f));
 #pragma unroll
-              for (int c = 0; c < C::COLS; c += 32) {
+              for (int c = 0; c < kCols; c += 32) {
                 uint32_t(&now)[32] = v[c / 32 & 1];
                 tmem_ld_wait(now);
-                if (c + 32 < C::COLS) tmem_ld32(from + i * BN + c + 32, v[(c / 32 + 1) & 1]);
-                else if (i == 0 && two) tmem_ld32(from + BN, v[(c / 32 + 1) & 1]);
+                if (c + 32 < kCols) tmem_ld32(from + i * kColumns + c + 32, v[(c / 32 + 1) & 1]);
+                else if (i == 0 && two) tmem_ld32(from + kColumns, v[(c / 32 + 1) & 1]);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) add_scaled(acc[c / 2 + e], now[2 * e], now[2 * e + 1], ff);
               }
@@ -443,15 +433,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto sum = [&](int i) { return __uint_as_float(static_cast<uint32_t>(i & 1 ? acc[i / 2] >> 32 : acc[i / 2])); };
       if (p.splits > 1) {
         // (one tile a cluster; its stages have been read)
-        float4 *to = reinterpret_cast<float4 *>(reinterpret_cast<float *>(sm) + (32 * q + lane) * kSplitRow<BN> + part * C::COLS);
+        float4 *to = reinterpret_cast<float4 *>(reinterpret_cast<float *>(sm) + (32 * q + lane) * kSplitRow + part * kCols);
         if (!idle) {
 #pragma unroll
-          for (int i = 0; i < C::COLS / 4; ++i) to[i] = make_float4(sum(4 * i), sum(4 * i + 1), sum(4 * i + 2), sum(4 * i + 3));
+          for (int i = 0; i < kCols / 4; ++i) to[i] = make_float4(sum(4 * i), sum(4 * i + 1), sum(4 * i + 2), sum(4 * i + 3));
         }
       } else if (by_tma) {
         // a box of 32 rows at a time: the residual is there, the results go out
 #pragma unroll
-        for (int c = 0; c < C::COLS; c += PIECE) {
+        for (int c = 0; c < kCols; c += PIECE) {
           if (!p.residual) {
             if (lane == 0) bulk_wait_read();
             __syncwarp();
@@ -463,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < PIECE / N; ++i) {
-            uint4 *at = reinterpret_cast<uint4 *>(mine + lane * ROWB + ((i ^ (ROWB == 128 ? lane & 7 : lane >> 1 & 3)) << 4));
+            uint4 *at = reinterpret_cast<uint4 *>(mine + lane * kBoxRow + ((i ^ (lane & 7)) << 4));
             float v[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) v[e] = sum(c + i * N + e);
@@ -481,11 +471,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (!TMA && !idle) {
         // rows that are not on 16 bytes: 32 columns of 32 rows at a time through shared memory, then a row's numbers together,
         // 16 rows of the residual on their way at once (1101 x 83799 x 880 with a residual 283 us; 16 columns and four rows 865)
-        static_assert(ROWB == 128 && C::COLS % 32 == 0, "32 fp32 numbers a row");
         auto at = [&](int row, int col) { return reinterpret_cast<float *>(mine) + row * 32 + (col ^ ((row & 7) << 2)); };
         const int rows = min(32, p.m - (t - lane));
 #pragma unroll
-        for (int c = 0; c < C::COLS; c += 32) {
+        for (int c = 0; c < kCols; c += 32) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4 *>(at(lane, i)) = make_float4(sum(c + i), sum(c + i + 1), sum(c + i + 2), sum(c + i + 3));
           __syncwarp();
@@ -518,12 +507,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.splits > 1) {
     mkw::cluster_arrive();
     mkw::cluster_wait();
-    // BN / splits columns each, four a thread: the CTAs' sums in order
-    const int t0 = first % p.tiles_m * kRows, j0 = first / p.tiles_m * BN, rows = min(kRows, p.m - t0), columns = BN / p.splits, fours = columns / 4;
+    // kColumns / splits columns each, four a thread: the CTAs' sums in order
+    const int t0 = first % p.tiles_m * kRows, j0 = first / p.tiles_m * kColumns, rows = min(kRows, p.m - t0), columns = kColumns / p.splits, fours = columns / 4;
     for (int i = threadIdx.x; i < fours * rows; i += kThreads) {
       const int t = i / fours, c = split * columns + i % fours * 4, col = j0 + c;
       if (col >= p.n) continue;
-      const float *own = reinterpret_cast<const float *>(sm) + t * kSplitRow<BN> + c;
+      const float *own = reinterpret_cast<const float *>(sm) + t * kSplitRow + c;
       float4 part[8];
 #pragma unroll
       for (int r = 0; r < 8; ++r)
@@ -543,39 +532,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, C::TCOLS);
+  if (warp == 1) tmem_dealloc(tmem, kTensorColumns);
 }
 
 // ---- host side ---------------------------------------------------------------------------
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    cudaDriverEntryPointQueryResult q;
-    void *f = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      f = nullptr;
-    }
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  return fn;
-}
-
-// rows of T, `row` apart, in boxes of 32 rows, 64 or 128 bytes of each
+// rows of T, `row` apart, in boxes of 32 rows, 128 bytes of each
 template <class T>
-bool result_map(CUtensorMap *map, const void *base, int64_t columns, int64_t rows, int64_t row, int box_columns) {
-  const auto enc = encoder();
+bool result_map(CUtensorMap *map, const void *base, int64_t columns, int64_t rows, int64_t row) {
+  const auto enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(rows)}, strides[1] = {static_cast<cuuint64_t>(row) * sizeof(T)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_columns), 32}, es[2] = {1, 1};
+  const cuuint32_t box[2] = {kBoxRow / sizeof(T), 32}, es[2] = {1, 1};
   return enc(map, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, box_columns * sizeof(T) == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // rows of `inner` bytes, `row` apart, in boxes of 128 bytes by box_rows
 bool byte_map(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, int64_t row, int box_rows) {
-  const auto enc = encoder();
+  const auto enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)}, strides[1] = {static_cast<cuuint64_t>(row)};
   const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)}, es[2] = {1, 1};
@@ -583,20 +559,19 @@ bool byte_map(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, i
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, class T, bool TMA>
+template <class T, bool TMA>
 int launch(const mk_matmul_fp8_args *a, MatmulParams &p, int sms, int dev, cudaStream_t s) {
-  using C = Cfg<BN, T>;
   static mkw::Ready ready[mkw::kMaxDevices];
-  const auto fn = &matmul_kernel<BN, T, TMA>;
+  const auto fn = &matmul_kernel<T, TMA>;
   mkw::Ready &r = ready[dev];
-  if (!r.get(reinterpret_cast<const void *>(fn), kThreads, C::SMEM)) return MK_ERR_CUDA;
+  if (!r.get(reinterpret_cast<const void *>(fn), kThreads, kSmem)) return MK_ERR_CUDA;
   p.x_rows = std::min(kRows, (a->m + 7) / 8 * 8);
   CUtensorMap tw, tx, ty = {}, tr = {};
-  if (TMA && (!result_map<T>(&ty, a->y, a->n, a->m, p.y_map_row, C::PIECE) || (a->residual && !result_map<T>(&tr, a->residual, a->n, a->m, p.residual_map_row, C::PIECE))))
+  if (TMA && (!result_map<T>(&ty, a->y, a->n, a->m, p.y_map_row) || (a->residual && !result_map<T>(&tr, a->residual, a->n, a->m, p.residual_map_row))))
     return MK_ERR_CUDA;
-  if (!byte_map(&tx, a->x, a->k, a->m, a->x_row, p.x_rows) || !byte_map(&tw, a->w, a->k, a->n, a->w_row, BN)) return MK_ERR_CUDA;
+  if (!byte_map(&tx, a->x, a->k, a->m, a->x_row, p.x_rows) || !byte_map(&tw, a->w, a->k, a->n, a->w_row, kColumns)) return MK_ERR_CUDA;
   p.tiles_m = (a->m - 1) / kRows + 1;
-  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * ((a->n - 1) / BN + 1);
+  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * ((a->n - 1) / kColumns + 1);
   if (tiles > INT32_MAX - 65536) return MK_ERR_UNSUPPORTED;
   p.tiles = static_cast<int>(tiles);
   p.splits = 1;
@@ -611,7 +586,7 @@ int launch(const mk_matmul_fp8_args *a, MatmulParams &p, int sms, int dev, cudaS
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(clusters * p.splits);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = p.splits > 1 ? 2 : 1;
@@ -682,6 +657,6 @@ extern "C" int mk_matmul_fp8(const mk_matmul_fp8_args *a, mk_stream stream) {
   p.wide_scales = aligned16(a->x_scale) && a->x_scale_row % 4 == 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   using B = __nv_bfloat16;
-  if (tma) return a->dtype == MK_F32 ? launch<kColumns, float, true>(a, p, sms, dev, s) : launch<kColumns, B, true>(a, p, sms, dev, s);
-  return a->dtype == MK_F32 ? launch<kColumns, float, false>(a, p, sms, dev, s) : launch<kColumns, B, false>(a, p, sms, dev, s);
+  if (tma) return a->dtype == MK_F32 ? launch<float, true>(a, p, sms, dev, s) : launch<B, true>(a, p, sms, dev, s);
+  return a->dtype == MK_F32 ? launch<float, false>(a, p, sms, dev, s) : launch<B, false>(a, p, sms, dev, s);
 }

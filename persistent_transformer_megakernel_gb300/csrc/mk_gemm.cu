@@ -20,8 +20,6 @@
 // separate accumulators, measured against the oracle).
 // Every wait is bounded (2 s); on expiry the CTA records MK_ERR_TIMEOUT,
 // still waits for the MMAs it issued, frees its tensor memory and returns.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -29,6 +27,7 @@
 #include "../../include/mk.h"
 #include "mk_gemm.h"
 #include "mk_tc.cuh"
+#include "mk_tmap.h"
 
 namespace mkg {
 
@@ -167,23 +166,6 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 // ---------------------------------------------------------------------------
 namespace {
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    cudaDriverEntryPointQueryResult q;
-    void *p = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    else
-      cudaGetLastError();
-  }
-  return fn;
-}
-
 template <int BN, int STAGES>
 int launch(const WMaps &w, const CUtensorMap &x, const GemmCall &c, cudaStream_t s) {
   static bool attr = false;
@@ -206,7 +188,7 @@ int launch(const WMaps &w, const CUtensorMap &x, const GemmCall &c, cudaStream_t
 
 bool make_tmap(CUtensorMap *map, const void *base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                uint32_t box_rows, uint64_t planes, uint64_t plane_bytes) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  const auto enc = mktc::tensor_map_encoder();
   if (!enc || (reinterpret_cast<uintptr_t>(base) & 15u) || (row_bytes & 15u) || inner % 64 || box_rows == 0 ||
       box_rows > 256 || planes < 1 || (planes > 1 && (plane_bytes & 15u)))
     return false;

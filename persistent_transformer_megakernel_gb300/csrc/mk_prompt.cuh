@@ -505,7 +505,7 @@ __device__ __forceinline__ void numbers_of(const typename Raw<FP8, N>::type &w, 
 // value outside the row's mask (infinity or NaN times a weight of 0) or a sum of large values can have done it, so that
 // the answer may be finite all the same.  Leaves the row's maximum (log2 units), sum and O (lane's elements) where the sum
 // counts weights times `shrink`.  Each row reads keys and values for itself: 8192 tokens that all see a NaN among the values
-// take 82 ms (one position at a time 240); a score that is NaN ends its row.
+// take 82 ms (one position at a time 216); a score that is NaN ends its row.
 template <bool FP8, int D>
 __device__ void row_alone(const PromptParams &p, const Task &task, const Pair &pair, int b0, int b1, int row, int head, int pos, int lane, float &m, float &l,
                           float (&o)[D / 32], float &shrink) {
