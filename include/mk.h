@@ -412,6 +412,8 @@ typedef struct {
   int32_t n;                   /* query rows, one per table row: 0 <= n <= table_rows */
   int32_t dtype;               /* of q and out: MK_F32 or MK_BF16 */
   int32_t n_q_heads;           /* a multiple of n_kv_heads; head j reads kv head j / (n_q_heads / n_kv_heads) */
+  int32_t sinks;               /* with a window: the first `sinks` tokens stay visible beside it; else unused.  (Where there
+                                  was padding: a host built without it, which clears the struct, calls as before.) */
   const void *q;               /* device [n][n_q_heads][head_dim] */
   void *out;                   /* device, the same shape; may be q itself (same strides), else no part
                                   of it or the cache */
@@ -425,7 +427,6 @@ typedef struct {
   void *workspace;             /* device, 16-byte aligned; the call's own until the stream has passed it */
   int64_t workspace_bytes;     /* at least mk_paged_attention_workspace */
   int32_t *status;             /* device, or NULL */
-  int32_t sinks;               /* with a window: the first `sinks` tokens stay visible beside it; else unused */
 } mk_attention_args;
 
 /* Attention of one new token per row over the paged cache:

@@ -88,11 +88,11 @@ class mk_append_args(C.Structure):
 
 
 class mk_attention_args(C.Structure):
-    _fields_ = [("n", C.c_int32), ("dtype", C.c_int32), ("n_q_heads", C.c_int32), ("q", C.c_void_p),
-                ("out", C.c_void_p), ("q_row", C.c_int64), ("q_head", C.c_int64), ("out_row", C.c_int64),
+    _fields_ = [("n", C.c_int32), ("dtype", C.c_int32), ("n_q_heads", C.c_int32), ("sinks", C.c_int32),
+                ("q", C.c_void_p), ("out", C.c_void_p), ("q_row", C.c_int64), ("q_head", C.c_int64), ("out_row", C.c_int64),
                 ("out_head", C.c_int64), ("lse", C.c_void_p), ("lengths", C.c_void_p), ("window", C.c_int32),
                 ("scale", C.c_float), ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64),
-                ("status", C.c_void_p), ("sinks", C.c_int32)]
+                ("status", C.c_void_p)]
 
 
 class mk_plan_args(C.Structure):

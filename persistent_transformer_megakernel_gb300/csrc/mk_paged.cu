@@ -1506,7 +1506,7 @@ int attention(const mk_paged_kv *kv, const mk_attention_args *a, mk_stream strea
   int rc = check_cache(kv);
   if (rc != MK_OK) return rc;
   if (!a || a->n < 0 || a->n > kv->table_rows || (a->dtype != MK_F32 && a->dtype != MK_BF16) || a->window < 0 ||
-      a->sinks < 0 || !std::isfinite(a->scale))
+      (a->window > 0 && a->sinks < 0) || !std::isfinite(a->scale))
     return MK_ERR_INVALID_ARG;
   rc = check_heads(a->n_q_heads, kv->n_kv_heads, kv->head_dim);
   if (rc != MK_OK) return rc;
