@@ -656,7 +656,8 @@ typedef struct {
  *   c > 0 times in it behind the prompt: x = x - frequency c - presence
  *   x = x + the biases of the token (in their order), x = -inf if it is not allowed
  * in fp32, rounded once; a token that none of them touches is copied.  A row whose
- * mask allows nothing is -inf throughout.  Errors: MK_ERR_INVALID_ARG,
+ * mask allows nothing is -inf throughout.  A token with several biases takes a look
+ * at all of its row's: tens of thousands of tokens may have one, few several.  Errors: MK_ERR_INVALID_ARG,
  * MK_ERR_UNSUPPORTED (sizes near 2^31), MK_ERR_CUDA. */
 int mk_adjust_logits(const mk_logits_args *a, mk_stream stream);
 
