@@ -491,7 +491,9 @@ typedef struct {
  * Whole prompts (lengths = rows), chunks behind what is cached, drafted tokens.
  * Scores and sums are fp32; the weights multiply the values rounded to bf16,
  * over an MK_E4M3 cache to fp16, and query elements there to 2^-38 of their head's
- * largest.  The same inputs give the same bits.  A row that sees nothing (t < 0)
+ * largest.  (mk_paged_attention holds the weights over an MK_BF16 cache to 16 bits
+ * and more: a token's result here may be off from that by 2^-8 of the sum of its
+ * weighted |values|, beside the rounding of both.)  The same inputs give the same bits.  A row that sees nothing (t < 0)
  * gives zeros and lse -inf; tokens that a row does not see are never read into
  * its result, whatever they hold.  A row that sees a page id outside the cache, or
  * whose sequence is longer than table_cols * page_size, gives NaN and MK_ERR_BAD_PAGE;
@@ -624,8 +626,10 @@ typedef struct {
 } mk_matmul_fp8_args;
 
 /* y[t][j] = sum_b x_scale[t][b] w_scale[j / 128][b] sum_{k in block b} x[t][k] w[j][k]
- * (+ residual): a block's products are summed by the tensor cores, the blocks in
- * fp32, rounded once.  The same inputs give the same bits.  Errors:
+ * (+ residual): a block's products are summed by the tensor cores and multiplied by
+ * the product of the two scales, the blocks are added in fp32, rounded once.  (Blocks whose
+ * scales' product leaves fp32's normal numbers, 2^-126 to 2^128, lose bits or are
+ * infinite or NaN.)  The same inputs give the same bits.  Errors:
  * MK_ERR_INVALID_ARG, MK_ERR_UNSUPPORTED (sizes near 2^31), MK_ERR_CUDA. */
 int mk_matmul_fp8(const mk_matmul_fp8_args *a, mk_stream stream);
 

@@ -111,10 +111,12 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_co
 // accumulators in tensor memory (a row of x a lane, a row of w a column); eight warps take it out, multiply it by xs ws --
 // one number for all of a thread's columns -- and add it to fp32 sums in registers while the next block is multiplied into
 // others.  Warp 0 asks for x and w by TMA, warps 1 and 2 multiply, warp 3 brings the scales, warps 4-11 add up.
-// Bound by what surrounds the products (8192 x 12288 x 2048: 169 us, 2440 TFLOP/s; with four stages 176): a block's four instructions take 256
-// clocks, taking its sums out of tensor memory about as many, and every hand-over between warps some 200 more.  So two
-// blocks are handed over at a time, and two warps multiply in turn, one waiting while the other's instructions run (one
-// warp, with four stages: 186 us).  Tiles of 256 columns hold fewer accumulators and spill (230 us and more).
+// Bound by no part alone (8192 x 12288 x 2048: 169 us, 2440 TFLOP/s, 500 clocks a block; with four stages 176): the tensor
+// pipe is busy for 256 of those, reading its operands from shared memory takes as many (32 KB at 128 bytes a clock), as many
+// bytes arrive there, and sums leave tensor memory and are added beside it.  Timed with parts left out: without the copies
+// 163 us, without the additions 153, without both 129; what is left there are the hand-overs between warps.  So two blocks
+// are handed over at a time, and two warps multiply in turn, one waiting while the other's instructions run (one warp, with
+// four stages: 186 us).  Tiles of 256 columns hold fewer accumulators and spill (230 us and more).
 // Pairs of CTAs that ask for shared tiles once (multicast) took as long (178 us for 177, with four stages): not kept.
 // splits > 1 (few tiles): K is shared by the CTAs of a cluster, whose sums are added in order through their shared memory.
 // ---------------------------------------------------------------------------
@@ -470,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       } else if (!TMA && !idle) {
         // rows that are not on 16 bytes: 32 columns of 32 rows at a time through shared memory, then a row's numbers together,
-        // 16 rows of the residual on their way at once (1101 x 83799 x 880 with a residual 283 us; 16 columns and four rows 865)
+        // 16 rows of the residual on their way at once (1101 x 83799 x 880 with a residual 292 us; 16 columns and four rows 865)
         auto at = [&](int row, int col) { return reinterpret_cast<float *>(mine) + row * 32 + (col ^ ((row & 7) << 2)); };
         const int rows = min(32, p.m - (t - lane));
 #pragma unroll

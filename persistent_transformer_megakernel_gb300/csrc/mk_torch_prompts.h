@@ -506,7 +506,7 @@ A token sees itself and the tokens before it, with a ``window`` the last
 ``window`` of them and the first ``sinks``.  Returns ``out`` like ``q`` (it
 may be ``q``, but not overlap it otherwise); ``lse`` fp32 [rows][heads] receives
 the log of each softmax's sum.  Rows of no sequence, and those of a negative
-length, are left as they were.  fp32 queries: ``paged_attention`` with a table
+length, are left as they were (in a new result: whatever its memory holds).  fp32 queries: ``paged_attention`` with a table
 row for each token.)"),
     method<&quantize_sig, &quantize_fp8>("quantize_fp8", R"(quantize_fp8(x, *, codes=None, scales=None, stream=None)
 --
@@ -531,7 +531,7 @@ for the tokens of each row's history, biases of single tokens and a mask; into
 
 ``tokens`` int32 [n][columns] are the histories, the first ``lengths[i]`` of
 each row (all by default; a negative length marks a padding row, which is left as
-it was) and the first ``prompts[i]`` of those the prompt.  A token of the history
+it was, in a new result whatever its memory holds) and the first ``prompts[i]`` of those the prompt.  A token of the history
 is divided by ``repetition[i]`` if positive and multiplied by it if not; one
 that came c > 0 times behind the prompt loses ``frequency[i]`` * c + ``presence[i]``
 (all fp32 [n]).  ``bias`` fp32 [n][b] is added to the tokens ``bias_ids`` int32
