@@ -239,7 +239,8 @@ extern "C" int mk_adjust_logits(const mk_logits_args *a, mk_stream stream) {
   if (!a->x || !a->out || reinterpret_cast<uintptr_t>(a->x) % es || reinterpret_cast<uintptr_t>(a->out) % es || (a->columns > 0 && !a->tokens) ||
       (a->biases > 0 && (!a->bias_ids || !a->bias)))
     return MK_ERR_INVALID_ARG;
-  if (a->vocab > INT32_MAX - 65536) return MK_ERR_UNSUPPORTED;
+  constexpr int kMostOf = INT32_MAX - 65536;               // (a CTA's steps over them, and its tokens beside them, stay within 32 bits)
+  if (a->vocab > kMostOf || a->columns > kMostOf || a->biases > kMostOf) return MK_ERR_UNSUPPORTED;
   int dev = 0;
   const int sms = mkv::sm_count(&dev);
   if (sms < 0) return MK_ERR_CUDA;
