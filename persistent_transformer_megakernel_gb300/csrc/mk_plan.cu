@@ -27,6 +27,8 @@ namespace mkplan {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxSequences = 16384;
 constexpr int kRowsACta = 4 * kThreads;
+// of a step, which takes no more pages: a step of all threads beyond them stays within 32 bits
+constexpr int kMostRows = INT32_MAX - (1 << 20);
 constexpr int smem_of(int n) { return (3 * n + 2) * 4; }
 
 struct PlanParams {
@@ -163,7 +165,7 @@ extern "C" int mk_paged_plan(const mk_plan_args *a, mk_stream stream) {
   if (!a->used || !a->used_out || !a->starts || (a->n > 0 && (!a->lengths || !a->totals)) || (a->rows > 0 && (!a->seqs || !a->slots)) ||
       (a->free_count > 0 && !a->free) || (a->n > 0 && a->table_cols > 0 && !a->table) || (!a->counts && a->n > 0 && a->rows != a->n))
     return MK_ERR_INVALID_ARG;
-  if (a->n > kMaxSequences || a->rows > INT32_MAX - 65536) return MK_ERR_UNSUPPORTED;
+  if (a->n > kMaxSequences || a->rows > kMostRows) return MK_ERR_UNSUPPORTED;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= mkw::kMaxDevices) {
     cudaGetLastError();
@@ -184,7 +186,7 @@ extern "C" int mk_paged_plan(const mk_plan_args *a, mk_stream stream) {
   // A CTA for every kRowsACta rows, a round of four rows a thread, and no more than run at once (131072 rows 4.5 us; two
   // rounds 5.3, half a round 5.0); in place one for every 4096, as far as a cluster reaches
   p.meet = a->totals == a->lengths || a->used_out == a->used;
-  int ctas = p.meet ? 1 : std::max(1, std::min((a->rows - 1) / kRowsACta + 1, mkv::sm_count(&dev)));
+  int ctas = p.meet ? 1 : std::max(1, std::min({(a->rows - 1) / kRowsACta + 1, mkv::sm_count(&dev), (1 << 20) / kThreads}));
   for (int i = 0; p.meet && i < 4 && r.clusters[i] > 0 && a->rows > 4096 * ctas; ++i) ctas = 2 << i;
   return mkw::launch_after(&plan_kernel, dim3(ctas), kThreads, smem_of(a->n), reinterpret_cast<cudaStream_t>(stream), p, p.meet ? ctas : 1);
 }

@@ -27,3 +27,11 @@ def test_histories_and_biases(far):
     assert logits(columns=far) == UNSUPPORTED
     assert logits(biases=far) == UNSUPPORTED
     assert logits(n=0, columns=far) == 0
+
+
+@pytest.mark.parametrize("rows", [MOST, MOST - 65536, MOST - 131072])
+def test_rows_of_a_plan(rows):
+    # as many pages as rows are taken where a page has one token, in steps of all threads of the device
+    a = B.mk_plan_args(n=2, rows=rows, page_size=1, lengths=16, counts=16, table=16, table_cols=MOST, table_stride=MOST, free=16, free_count=MOST, used=16,
+                       seqs=16, slots=16, starts=16, totals=16, used_out=16)
+    assert mk.load_library().mk_paged_plan(C.byref(a), None) == UNSUPPORTED
