@@ -675,8 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     }
     fence_to_tensor_cores();
   }
-  // (a factor of 0 would make the -infinity of a hidden score NaN; the smallest normal one does what 0 does)
-  to_log2 = fmaxf(to_log2, 1.2e-38f);
+  // (a factor of 0 would make the -infinity of a hidden score NaN; the smallest normal one does what 0 does.  NaN stays NaN.)
+  if (to_log2 < 1.2e-38f) to_log2 = 1.2e-38f;
   uint32_t tmem = 0;
   if (warp < kSoftWarps + kMmaWarps) {                     // (the copies begin meanwhile)
     tc_fence_before();
