@@ -344,7 +344,12 @@ struct Memory {
 // dispatch modes and profilers see it), else as it makes it without the way through the dispatcher (half a microsecond less
 // a call).
 inline at::Tensor fresh(c10::IntArrayRef sizes, at::ScalarType type, const at::Tensor &like) {
-  if (at::globalContext().deterministicAlgorithms() || c10::impl::dispatch_mode_enabled() || at::getStepCallbacksUnlessEmpty(at::RecordScope::FUNCTION)) return at::empty(sizes, like.options().dtype(type));
+  if (at::globalContext().deterministicAlgorithms() || c10::impl::dispatch_mode_enabled() || at::getStepCallbacksUnlessEmpty(at::RecordScope::FUNCTION)) {
+    at::Tensor t = at::empty(sizes, like.options().dtype(type));
+    // (what a mode makes in its place may have no memory)
+    need(t.device() == like.device() && (t.numel() == 0 || (t.has_storage() && t.storage().data())), "a dispatch mode made a result without memory on the tensors' device");
+    return t;
+  }
   return at::Tensor(at::detail::empty_generic(sizes, c10::cuda::CUDACachingAllocator::get(), c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt));
 }
 

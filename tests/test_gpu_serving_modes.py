@@ -62,3 +62,34 @@ def test_the_profiler():
             got = f()
         assert same(got, want)
         assert any(e.name.startswith("aten::empty") for e in p.events()), i
+
+
+class Elsewhere(TorchDispatchMode):
+    """New tensors on another device, or without memory."""
+
+    def __init__(self, device):
+        super().__init__()
+        self.device = device
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        kwargs = dict(kwargs or {})
+        if "empty" in str(func):
+            kwargs["device"] = self.device
+        return func(*args, **kwargs)
+
+
+@pytest.mark.parametrize("device", ["meta", "cpu"])
+def test_results_that_a_mode_puts_elsewhere(device):
+    # (one call of each operator: the inputs are made before the mode)
+    g = torch.Generator().manual_seed(0)
+    kc, vc = (torch.randn((4, 1, 16, 64), generator=g).to(BF16).cuda() for _ in range(2))
+    q, table = torch.randn((5, 2, 64), generator=g).to(BF16).cuda(), torch.arange(4, dtype=torch.int32, device="cuda").view(1, 4)
+    x, mask = torch.randn((5, 256), generator=g).to(BF16).cuda(), torch.full((5, 8), -1, dtype=torch.int32, device="cuda")
+    w = torch.randn((64, 256), generator=g).cuda()
+    q4, w8, c = mk.quantize_q4(w), mk.quantize_fp8_weight(w), mk.quantize_fp8(x)
+    starts, five, one, free, none = i32([0, 5]), i32([20]), i32([1]), i32([0, 1, 2]), i32([0])
+    for f in (lambda: mk.paged_append(q[:1, :1], q[:1, 1:], kc, vc, table, one, q=q[:1]), lambda: mk.paged_attention(q[:1], kc, vc, table, five),
+              lambda: mk.paged_prompt_attention(q, kc, vc, table, starts, five), lambda: mk.matvec_q4(x, *q4), lambda: mk.quantize_fp8(x),
+              lambda: mk.matmul_fp8(*c, *w8), lambda: mk.paged_plan(one, table, free, none, 16), lambda: mk.adjust_logits(x, mask=mask)):
+        with Elsewhere(device), pytest.raises(ValueError, match="without memory"):
+            f()
