@@ -215,7 +215,7 @@ struct Out<__nv_bfloat16> {
   }
 };
 
-// TMA: rows of y and of the residual are on 16 bytes.  (Both ways in one kernel cost 8192 x 12288 x 2048 six microseconds.)
+// TMA: rows of y and of the residual start and end on 16 bytes.  (Both ways in one kernel cost 8192 x 12288 x 2048 six microseconds.)
 template <class T, bool TMA>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap ty,
@@ -652,10 +652,10 @@ extern "C" int mk_matmul_fp8(const mk_matmul_fp8_args *a, mk_stream stream) {
   p.x_scale_row = a->x_scale_row, p.residual_row = a->residual_row, p.y_row = a->y_row;
   p.m = a->m, p.n = a->n, p.kb = (a->k - 1) / kBlock + 1;
   // (an expanded residual has no stride that a tensor map takes; a single row may have any)
-  const int64_t one = (a->n * static_cast<int64_t>(es) + 15) / 16 * 16 / static_cast<int64_t>(es);
-  p.y_map_row = a->m == 1 ? one : a->y_row, p.residual_map_row = a->m == 1 ? one : a->residual_row;
+  p.y_map_row = a->m == 1 ? a->n : a->y_row, p.residual_map_row = a->m == 1 ? a->n : a->residual_row;
   auto mapped = [&](const void *t, int64_t row) { return aligned16(t) && row * es % 16 == 0 && row >= a->n && row < (int64_t{1} << 36); };
-  const bool tma = mapped(a->y, p.y_map_row) && (!a->residual || mapped(a->residual, p.residual_map_row));
+  // A copy to memory writes whole pieces of 16 bytes: a row that ends inside one would lose what is behind it.
+  const bool tma = a->n * es % 16 == 0 && mapped(a->y, p.y_map_row) && (!a->residual || mapped(a->residual, p.residual_map_row));
   p.wide_scales = aligned16(a->x_scale) && a->x_scale_row % 4 == 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   using B = __nv_bfloat16;

@@ -95,7 +95,8 @@ __device__ __forceinline__ void tma_load_2d_hint(void *dst, const void *tmap, in
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(smem_addr(bar)), "l"(policy)
       : "memory");
 }
-// shared memory to the tensor, in groups of stores; both coordinates not negative, what is past the ends is left out
+// shared memory to the tensor, in groups of stores; both coordinates not negative, what is past the ends is left out, but whole
+// pieces of 16 bytes are written: the tensor's rows have to end on 16 bytes (zeros came behind them where they did not)
 __device__ __forceinline__ void tma_store_2d(const void *tmap, const void *src, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(x),
                "r"(y), "r"(smem_addr(src))
