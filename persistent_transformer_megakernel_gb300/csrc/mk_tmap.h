@@ -1,4 +1,4 @@
-// The driver's function that encodes a tensor map, looked up once; nullptr if there is none.
+// CUDA's entry point that encodes a tensor map, looked up once; nullptr if there is none.
 #pragma once
 #include <cuda.h>
 #include <cudaTypedefs.h>
